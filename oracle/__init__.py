@@ -553,3 +553,96 @@ def gat_layer_bwd(rowptr, col, dOut, H, M, Hp, Epre, alpha, W, a_src, a_dst, hea
     dH = gemm(dHp, np.asarray(W).T, bf16)
     return dict(dalpha=dalpha, P=P, dE=dE, dEpre=dEpre, dD=dD, dS=dS, dM=dM, dHp=dHp,
                 da_src=da_src, da_dst=da_dst, dW=dW, dH=dH, packed=packed)
+
+
+# --------------------------------------------------------------------------
+# what stands between and behind the layers of a training step: dropout,
+# layer normalization, the class head's cross entropy (no page describes
+# them; the formulas are written out in each docstring)
+# --------------------------------------------------------------------------
+
+def _fmix32_array(h: np.ndarray) -> np.ndarray:
+    h = h.astype(np.uint32)
+    with np.errstate(over="ignore"):
+        h = h ^ (h >> np.uint32(16))
+        h = h * np.uint32(0x85EBCA6B)
+        h = h ^ (h >> np.uint32(13))
+        h = h * np.uint32(0xC2B2AE35)
+        return h ^ (h >> np.uint32(16))
+
+
+def noise_codes(seed: int, n: int, d: int) -> np.ndarray:
+    """The 23-bit noise codes (u = code * 2^-23) of rows 0..n-1, columns 0..d-1."""
+    key = np.uint32(fmix32((seed ^ (seed >> 32)) & 0xFFFFFFFF))
+    rows = _fmix32_array(np.arange(n, dtype=np.uint32) ^ key)
+    with np.errstate(over="ignore"):
+        cols = np.arange(d, dtype=np.uint32) * np.uint32(0x9E3779B9)
+        return _fmix32_array(rows[:, None] + cols[None, :]) >> np.uint32(9)
+
+
+def kept(seed: int, n: int, d: int, p: float) -> np.ndarray:
+    """[u >= p] as booleans; u has 23 bits, so u >= p is code >= p 2^23."""
+    return noise_codes(seed, n, d).astype(np.float64) >= p * 2.0 ** 23
+
+
+def dropout(X, p: float, seed: int) -> np.ndarray:
+    """x / (1 - p) where kept, else 0."""
+    X = np.asarray(X, np.float64)
+    if p == 0.0:
+        return X.copy()
+    keep = kept(seed, *X.shape, p)
+    return np.where(keep, X / (1.0 - p) if p < 1.0 else 0.0, 0.0)
+
+
+def layer_norm_fwd(X, gamma=None, beta=None, eps: float = 1e-5, relu: bool = False, p: float = 0.0, seed: int = 0):
+    """mean = (1/d) sum x; rstd = 1/sqrt((1/d) sum (x - mean)^2 + eps);
+    z = (x - mean) rstd gamma + beta; Y = drop(relu(z)).  Also [z > 0]."""
+    X = np.asarray(X, np.float64)
+    d = X.shape[1]
+    mean = X.sum(1) / d
+    xc = X - mean[:, None]
+    rstd = 1.0 / np.sqrt((xc * xc).sum(1) / d + eps)
+    z = xc * rstd[:, None] * (1.0 if gamma is None else np.asarray(gamma, np.float64))
+    z = z + (0.0 if beta is None else np.asarray(beta, np.float64))
+    y = np.maximum(z, 0.0) if relu else z
+    return dict(Y=dropout(y, p, seed), mean=mean, rstd=rstd, z=z, on=z > 0)
+
+
+def layer_norm_bwd(dY, X, mean, rstd, gamma=None, on=None, p: float = 0.0, seed: int = 0):
+    """dz = drop'(dY) where `on` (everywhere when None); dgamma = sum_rows
+    dz xhat; dbeta = sum_rows dz; g = dz gamma;
+    dX = rstd (g - mean_j g - xhat mean_j(g xhat))."""
+    X, dz = np.asarray(X, np.float64), dropout(dY, p, seed)
+    if on is not None:
+        dz = np.where(on, dz, 0.0)
+    rstd = np.asarray(rstd, np.float64)[:, None]
+    xhat = (X - np.asarray(mean, np.float64)[:, None]) * rstd
+    g = dz * (1.0 if gamma is None else np.asarray(gamma, np.float64))
+    dX = rstd * (g - g.mean(1, keepdims=True) - xhat * (g * xhat).mean(1, keepdims=True))
+    return dict(dX=dX, dgamma=(dz * xhat).sum(0), dbeta=dz.sum(0), xhat=xhat, dz=dz, g=g)
+
+
+def linear_xent(X, W, labels, weight=None, scale: float = 1.0):
+    """Z = X W^T; for a row with 0 <= label < C: lse = log sum_c exp(z_c),
+    loss = lse - z_label, G = weight scale (softmax(z) - onehot(label));
+    other rows: lse = loss = 0 and G = 0.  dX = G W, dW = G^T X (rows
+    without a label do not enter)."""
+    X, W, labels = np.asarray(X, np.float64), np.asarray(W, np.float64), np.asarray(labels)
+    n, C = X.shape[0], W.shape[0]
+    at = np.nonzero((labels >= 0) & (labels < C))[0]
+    lse, loss = np.zeros(n), np.zeros(n)
+    Z = X[at] @ W.T
+    top = Z.max(1, keepdims=True) if at.size else np.zeros((0, 1))
+    E = np.exp(Z - top)
+    s = E.sum(1)
+    lse[at] = np.log(s) + top[:, 0]
+    loss[at] = lse[at] - Z[np.arange(at.size), labels[at]]
+    G = E / s[:, None]
+    G[np.arange(at.size), labels[at]] -= 1.0
+    G *= scale * (np.ones(at.size) if weight is None else np.asarray(weight, np.float64)[at])[:, None]
+    dX = np.zeros(X.shape)
+    dX[at] = G @ W
+    absdX = np.zeros(X.shape)
+    absdX[at] = np.abs(G) @ np.abs(W)
+    return dict(loss=loss, lse=lse, dX=dX, dW=G.T @ X[at], rows=at, absdX=absdX, absdW=np.abs(G).T @ np.abs(X[at]),
+                absZ=(np.abs(X[at]) @ np.abs(W).T).max(1) if at.size else np.zeros(0))

@@ -24,6 +24,7 @@ _lib = None
 GQ_OK = 0
 COEF_GCN, COEF_SAGE, COEF_ONE = 0, 1, 2
 ACT_NONE, ACT_RELU = 0, 1
+F32, BF16, F16 = 0, 1, 2
 
 
 class GQError(RuntimeError):
@@ -97,6 +98,11 @@ def _SIGNATURES(P, I64, I, U64, F, S):
         ("gq_gemm_bf16_tn_workspace_bytes", [I64, I, I], S),
         ("gq_gemm_bf16_tn", [P, I64, I, I64, P, I, I64, P, I64, I, P, S, P, P], I),
         ("gq_to_bf16", [P, I64, I, I64, P, I64, I, P], I),
+        ("gq_dropout", [P, I, I64, I, I64, ctypes.c_double, U64, P, I64, P], I),
+        ("gq_layer_norm_fwd", [P, I, I64, I, I64, P, P, F, I, ctypes.c_double, U64, P, I64, P, P, P, I64, P], I),
+        ("gq_layer_norm_bwd_workspace_bytes", [I64, I], S),
+        ("gq_layer_norm_bwd", [P, I64, P, I64, I, I64, I, P, P, P, I, ctypes.c_double, U64, P, I64, P, I, I64, P, P,
+                               P, S, P], I),
         ("gq_gcn_layer_workspace_bytes", [GP, I, I, I], S),
         ("gq_edge_softmax_workspace_bytes", [GP, I], S),
         ("gq_sddmm_edge_softmax", [GP, P, P, I, F, P, P, P, S, P], I),
@@ -434,6 +440,125 @@ def to_bf16(src: torch.Tensor, pad_to: int = 8) -> torch.Tensor:
     dst = torch.empty(rows, dcols, dtype=torch.bfloat16, device=src.device)
     _check(lib().gq_to_bf16(_ptr(src), rows, cols, _rows(src), _ptr(dst), dcols, dcols, _stream()), "gq_to_bf16")
     return dst[:, :cols]
+
+
+# --------------------------------------------------------------------------
+# dropout and layer normalization
+# --------------------------------------------------------------------------
+
+DROPOUT_SEED_TAG = 0xD6E8FEB86659FD93  # GQ_DROPOUT_SEED_TAG
+_TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+
+
+def _typed(t, name):
+    """gq_type of a CUDA matrix in one of the three element types."""
+    if not t.is_cuda:
+        raise GQError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _TYPES:
+        raise GQError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return _TYPES[t.dtype]
+
+
+def _like(t, ref, name, dtypes=None):
+    """t is a matrix of ref's shape and device, in one of dtypes (ref's)."""
+    if t.shape != ref.shape or t.device != ref.device or t.dtype not in (dtypes or (ref.dtype,)):
+        raise GQError(f"{name}: expected {tuple(ref.shape)} {dtypes or ref.dtype} on {ref.device}, "
+                      f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+    return t
+
+
+def _vec32(t, count, ref, name):
+    """t (or None) is a contiguous fp32 vector of `count` values on ref's device."""
+    if t is not None and (t.dtype != torch.float32 or t.shape != (count,) or t.device != ref.device
+                          or not t.is_contiguous()):
+        raise GQError(f"{name} must be a contiguous float32 vector of {count} values on {ref.device}")
+    return t
+
+
+def _bits32(t, ref):
+    """t (or None) holds the ReLU bits of ref's rows."""
+    if t is not None:
+        _cuda(t, torch.int32, "relu_bits")
+        if t.dim() != 2 or t.shape[0] != ref.shape[0] or t.shape[1] < (ref.shape[1] + 31) // 32 \
+                or t.device != ref.device:
+            raise GQError("relu_bits must be int32 [n x ceil(d / 32)] on the rows' device")
+    return t
+
+
+def dropout(X: torch.Tensor, p: float, seed: int, out: torch.Tensor | None = None) -> torch.Tensor:
+    """X / (1 - p) where the counter hash of (seed, row, column) keeps the
+    element, 0 elsewhere (gq_dropout); the backward pass is the same call on
+    the gradient.  out may be X."""
+    ty = _typed(X, "X")
+    ldx = _rows(X)
+    if out is None:
+        out = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+    _like(out, X, "out")
+    n, d = X.shape
+    with torch.cuda.device(X.device):
+        _check(lib().gq_dropout(_ptr(X), ty, n, d, ldx, p, seed & 0xFFFFFFFFFFFFFFFF, _ptr(out), _rows(out),
+                                _stream()), "gq_dropout")
+    return out
+
+
+def layer_norm_fwd(X: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
+                   eps: float = 1e-5, act: int = ACT_NONE, p: float = 0.0, seed: int = 0,
+                   out: torch.Tensor | None = None, mean: torch.Tensor | None = None,
+                   rstd: torch.Tensor | None = None, relu_bits: torch.Tensor | None = None):
+    """(Y, mean, rstd): Y = drop(act(layer norm of X's rows)), with the row
+    statistics the backward pass takes; relu_bits (int32 [n x ceil(d / 32)],
+    optional) receives [z > 0], which it takes for act = ACT_RELU."""
+    ty = _typed(X, "X")
+    ldx = _rows(X)
+    n, d = X.shape
+    out = torch.empty(X.shape, dtype=X.dtype, device=X.device) if out is None else _like(out, X, "out")
+    if mean is None:
+        mean = torch.empty(n, dtype=torch.float32, device=X.device)
+    if rstd is None:
+        rstd = torch.empty(n, dtype=torch.float32, device=X.device)
+    _vec32(gamma, d, X, "gamma"), _vec32(beta, d, X, "beta"), _vec32(mean, n, X, "mean"), _vec32(rstd, n, X, "rstd")
+    _bits32(relu_bits, X)
+    with torch.cuda.device(X.device):
+        _check(lib().gq_layer_norm_fwd(_ptr(X), ty, n, d, ldx, _ptr(gamma), _ptr(beta), eps, act, p,
+                                       seed & 0xFFFFFFFFFFFFFFFF, _ptr(out), _rows(out), _ptr(mean), _ptr(rstd),
+                                       _ptr(relu_bits), _rows(relu_bits) if relu_bits is not None else 0, _stream()),
+               "gq_layer_norm_fwd")
+    return out, mean, rstd
+
+
+def layer_norm_bwd(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                   gamma: torch.Tensor | None = None, act: int = ACT_NONE, p: float = 0.0, seed: int = 0,
+                   relu_bits: torch.Tensor | None = None, dX: torch.Tensor | None = None,
+                   dgamma: torch.Tensor | None = None, dbeta: torch.Tensor | None = None,
+                   ws: "Workspace | None" = None):
+    """(dX, dgamma, dbeta) from the forward pass's input, statistics, seed
+    and ReLU bits.  dX may be bf16 for fp32 inputs: the dZ_in of
+    gcn_layer_bwd."""
+    ty = _typed(X, "X")
+    n, d = X.shape
+    ldx = _rows(X)
+    _like(dY, X, "dY")
+    if dX is None:
+        dX = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+    _like(dX, X, "dX", (torch.float32, torch.bfloat16) if X.dtype == torch.float32 else None)
+    if dgamma is None:
+        dgamma = torch.empty(d, dtype=torch.float32, device=X.device)
+    if dbeta is None:
+        dbeta = torch.empty(d, dtype=torch.float32, device=X.device)
+    for t, c, name in ((mean, n, "mean"), (rstd, n, "rstd"), (gamma, d, "gamma"), (dgamma, d, "dgamma"),
+                       (dbeta, d, "dbeta")):
+        _vec32(t, c, X, name)
+    _bits32(relu_bits, X)
+    L = lib()
+    with torch.cuda.device(X.device):
+        wb = int(L.gq_layer_norm_bwd_workspace_bytes(n, d))
+        buf = ws.get(wb) if ws is not None else torch.empty(wb, dtype=torch.uint8, device=X.device)
+        _check(L.gq_layer_norm_bwd(_ptr(dY), _rows(dY), _ptr(X), ldx, ty, n, d, _ptr(mean), _ptr(rstd), _ptr(gamma),
+                                   act, p, seed & 0xFFFFFFFFFFFFFFFF, _ptr(relu_bits),
+                                   _rows(relu_bits) if relu_bits is not None else 0, _ptr(dX), _TYPES[dX.dtype],
+                                   _rows(dX), _ptr(dgamma), _ptr(dbeta), _ptr(buf), buf.numel(), _stream()),
+               "gq_layer_norm_bwd")
+    return dX, dgamma, dbeta
 
 
 # --------------------------------------------------------------------------
