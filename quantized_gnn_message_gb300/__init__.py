@@ -103,6 +103,8 @@ def _SIGNATURES(P, I64, I, U64, F, S):
         ("gq_layer_norm_bwd_workspace_bytes", [I64, I], S),
         ("gq_layer_norm_bwd", [P, I64, P, I64, I, I64, I, P, P, P, I, ctypes.c_double, U64, P, I64, P, I, I64, P, P,
                                P, S, P], I),
+        ("gq_linear_xent_workspace_bytes", [I64, I, I, I], S),
+        ("gq_linear_xent", [P, I64, I, I64, P, I, I64, P, P, F, P, P, P, I64, P, I64, P, S, P, P], I),
         ("gq_gcn_layer_workspace_bytes", [GP, I, I, I], S),
         ("gq_edge_softmax_workspace_bytes", [GP, I], S),
         ("gq_sddmm_edge_softmax", [GP, P, P, I, F, P, P, P, S, P], I),
@@ -559,6 +561,49 @@ def layer_norm_bwd(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rstd: 
                                    _rows(dX), _ptr(dgamma), _ptr(dbeta), _ptr(buf), buf.numel(), _stream()),
                "gq_layer_norm_bwd")
     return dX, dgamma, dbeta
+
+
+# --------------------------------------------------------------------------
+# class head
+# --------------------------------------------------------------------------
+
+def linear_xent(X: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, weight: torch.Tensor | None = None,
+                scale: float = 1.0, grad: bool = True, loss: torch.Tensor | None = None,
+                lse: torch.Tensor | None = None, dX: torch.Tensor | None = None, dW: torch.Tensor | None = None,
+                need_dX: bool = True, need_dW: bool = True, ws: "Workspace | None" = None,
+                dev_err: torch.Tensor | None = None):
+    """(loss, dX, dW) of the class head Z = X W^T with X [n x k] and W
+    [C x k] bf16 and int32 labels (outside [0, C): the row has none): per-row
+    cross entropy, and the gradients of scale * sum(weight * loss), in bf16.
+    grad = False computes the losses only; need_dX / need_dW leave one
+    gradient out (None is returned in its place)."""
+    _cuda(X, torch.bfloat16, "X")
+    _cuda(W, torch.bfloat16, "W")
+    _cuda(labels, torch.int32, "labels")
+    if X.dim() != 2 or W.dim() != 2 or X.shape[1] != W.shape[1] or W.device != X.device:
+        raise GQError("X [n x k] and W [C x k] need the same k and device")
+    n, k = X.shape
+    C = W.shape[0]
+    if labels.shape != (n,) or not labels.is_contiguous() or labels.device != X.device:
+        raise GQError(f"labels must be a contiguous int32 vector of {n} values on {X.device}")
+    dev = X.device
+    new = lambda rows: torch.empty(rows, _round8(k), dtype=torch.bfloat16, device=dev)[:, :k]
+    if loss is None:
+        loss = torch.empty(n, dtype=torch.float32, device=dev)
+    for t, name in ((weight, "weight"), (loss, "loss"), (lse, "lse")):
+        _vec32(t, n, X, name)
+    need_dX, need_dW = grad and need_dX, grad and need_dW
+    dX = (_like(dX, X, "dX") if dX is not None else new(n)) if need_dX else None
+    dW = (_like(dW, W, "dW") if dW is not None else new(C)) if need_dW else None
+    L = lib()
+    with torch.cuda.device(dev):
+        wb = int(L.gq_linear_xent_workspace_bytes(n, k, C, int(need_dX or need_dW)))
+        buf = ws.get(wb) if ws is not None else torch.empty(wb, dtype=torch.uint8, device=dev)
+        _check(L.gq_linear_xent(_ptr(X), n, k, _ld_bf16(X), _ptr(W), C, _ld_bf16(W), _ptr(labels), _ptr(weight), scale,
+                                _ptr(loss), _ptr(lse), _ptr(dX), _ld_bf16(dX) if need_dX else 0, _ptr(dW),
+                                _ld_bf16(dW) if need_dW else 0, _ptr(buf), buf.numel(), _ptr(dev_err), _stream()),
+               "gq_linear_xent")
+    return loss, dX, dW
 
 
 # --------------------------------------------------------------------------

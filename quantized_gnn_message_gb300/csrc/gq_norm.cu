@@ -33,6 +33,7 @@
 
 #include "gq_common.cuh"
 #include "gq_internal.cuh"
+#include "gq_train.h"
 
 namespace gq {
 namespace {

@@ -1,0 +1,1049 @@
+// gq_xent.cu -- softmax cross entropy of a linear class head over many
+// classes, with its gradients, without keeping the logits.
+//
+//   Z = X W^T (n x C);  lse_i = log sum_c exp(Z_ic);  loss_i = lse_i - Z_iy
+//   G = w_i (softmax(Z) - onehot(y));  dX = G W;  dW = G^T X
+//
+// Rows without a label take no part: the labelled rows are numbered in order
+// by a scan, and copied together unless every row is labelled, so neither
+// their number nor what they hold reaches the products.
+//
+// Four products on the tcgen05 tensor cores (bf16 inputs, fp32 sums in
+// TMEM), all tiles of one persistent kernel:
+//   STATS  Z tile -> running maximum and sum of exponentials per row and run
+//          of class tiles, and the label's logit
+//   GRAD   Z tile again -> G of one piece of the classes, in bf16
+//   DX     dX += G W over the piece (fp32 sums between pieces)
+//   DW     dW of the piece's classes = G^T X
+// 8 n k C operations where keeping all of Z (4 n C bytes) would need 6.  One
+// launch holds the DX and DW tiles of a piece and the GRAD tiles of the next
+// (two buffers of G), so that only the last launch has a tail.
+//
+// Tiles are 256 x up to 256 x 64 for a pair of CTAs (cta_group::2): each CTA
+// loads 128 rows of A and half of B's columns, so each operand byte is read
+// from L2 once per pair.  Per CTA:
+//   warp 0      TMA loads into a ring of six 32 KB stages; both CTAs' bytes
+//               arrive on the even CTA's barrier
+//   warp 1      (even CTA) one thread issues tcgen05.mma into one of two
+//               TMEM accumulators of 256 columns; its commits release the
+//               stages of both CTAs
+//   warps 2-9   epilogue: lane = row, warps 2-5 the first half of the
+//               columns, 6-9 the second; the next tile's products run
+//               meanwhile in the other accumulator
+//   warp 10     (even CTA) draws the next unit of work from a counter and
+//               posts it to both CTAs.  Which CTA computes a tile does not
+//               change its value, so results do not depend on the order.
+//
+// G is rounded to bf16, the type that the products dX and dW take: each
+// entry is off by at most half a step (2^-8 of its value, about as much as
+// the rounding of a bf16 result; errors of a sum's entries mostly cancel).
+#include <cuda_bf16.h>
+#include <cudaTypedefs.h>
+
+#include <cstdint>
+#include <cstring>
+
+#include "gq_common.cuh"
+#include "gq_internal.cuh"
+#include "gq_sm100.cuh"
+#include "gq_train.h"
+
+namespace gq {
+namespace {
+
+constexpr int kThreads = 352;    // TMA, MMA, 8 epilogue warps, scheduler
+constexpr int kEpiWarps = 8;
+constexpr int kStages = 6;
+constexpr int kStageA = 128 * 128;                    // 128 rows x 64 bf16 (or 2 x 64 x 64)
+constexpr int kStageBytes = 2 * kStageA;
+constexpr int kStg = 4096;       // epilogue staging per warp
+constexpr int kSlots = 4;        // units of work posted ahead
+constexpr int kConsumers = 19;   // even CTA: TMA, MMA, 8 epilogue; odd CTA: TMA, 8 epilogue
+constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kStg + 512;
+constexpr int kTile = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+enum Mode { STATS, GRAD, DX, DW };
+
+struct Maps {
+  CUtensorMap xk[2], xm[2];  // X: [0] as given, [1] the copied labelled rows; K-major / MN-major boxes
+  CUtensorMap wk, wm;        // W
+  CUtensorMap gk, gm;        // the piece of G read by DX / DW
+  CUtensorMap gst;           // the piece of G written by GRAD
+};
+
+struct Args {
+  const int* nl;         // number of labelled rows (device)
+  int* counter;          // next unit of this launch
+  int64_t n, npad;       // rows of X; rounded up to 256
+  int k, C;
+  int NT, NK, nkt;       // class tile width, k tile width, k tiles
+  int stats_tiles, stats_run, stats_units;  // class tiles, tiles per unit, units per row tile (0: none)
+  int gc0, gtiles;       // GRAD: first class and class tiles of the piece written (0 tiles: none)
+  int pc0, psteps, ptiles;  // DX / DW: first class, 64-class steps, 256-class tiles of the piece read
+  int do_dx, do_dw, dw_first;
+  int dxs, dws;          // splits of their sums
+  int first, last;       // the piece read is the first / last one
+  const int* lab;        // per labelled row
+  const float* wrow;
+  const float2* norm;    // r, weight / sum of 2^(z L - r)
+  float* zlab;
+  const int* idx;        // labelled row -> row of X
+  float2* part;          // [unit * 2 + half][npad]: r, sum
+  float* accX;           // [split][row tile][nkt NK][256]
+  float* accW;           // [split][class tile][nkt NK][256]
+  __nv_bfloat16* dX;
+  int64_t lddx;
+  __nv_bfloat16* dW;
+  int64_t lddw;
+  int* err;
+};
+
+// ------------------------------------------------------------ PTX helpers --
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void expect_cluster(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void st_async(uint32_t addr, int v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.s32 [%0], %1, [%2];" ::"r"(addr), "r"(v),
+               "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_alloc2(uint32_t* dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void umma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      "  .reg .pred p;\n"
+      "  setp.ne.b32 p, %4, 0;\n"
+      "  tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+      "}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// arrives on `bar` of both CTAs once the MMAs issued so far are done
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+        "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+
+// ------------------------------------------------------------------ tiles --
+struct Tile {
+  int mode, rt, ct, kt, split;
+  int s0, steps;  // 64-wide steps of the contraction
+  int N;          // columns of the pair's tile
+};
+
+// Units are numbered long tiles first (DX / DW by length), then STATS or
+// GRAD tiles in groups of 32 row tiles, rows fastest: the rows of a group
+// stay in L2 while the class tiles pass.
+struct Plan {
+  int nl, nrt;
+  int64_t ndx, ndw, units;
+};
+
+__device__ __forceinline__ Plan make_plan(const Args& p) {
+  Plan q;
+  q.nl = *p.nl;
+  q.nrt = (q.nl + kTile - 1) / kTile;
+  q.ndx = p.do_dx ? (int64_t)q.nrt * p.nkt * p.dxs : 0;
+  q.ndw = p.do_dw ? (int64_t)p.ptiles * p.nkt * p.dws : 0;
+  q.units = q.ndx + q.ndw + (int64_t)q.nrt * (p.gtiles + p.stats_units);
+  return q;
+}
+
+// the tiles of unit u: `sub` counts them from 0; false past the last one
+__device__ __forceinline__ bool get_tile(const Args& p, const Plan& q, int64_t u, int sub, Tile& t) {
+  const int64_t nfirst = p.dw_first ? q.ndw : q.ndx;
+  const bool out = u < q.ndx + q.ndw;
+  if (out) {
+    if (sub > 0) return false;
+    const bool dw = (u < nfirst) == (p.dw_first != 0);
+    const int i = (int)(u < nfirst ? u : u - nfirst);
+    t.mode = dw ? DW : DX;
+    t.N = p.NK;
+    t.kt = i % p.nkt;
+    const int splits = dw ? p.dws : p.dxs;
+    t.split = i / p.nkt % splits;
+    t.rt = t.ct = i / p.nkt / splits;
+    const int total = dw ? (q.nl + 63) / 64 : p.psteps;
+    const int per = (total + splits - 1) / splits;
+    t.s0 = min(total, t.split * per);
+    t.steps = min(total, t.s0 + per) - t.s0;
+    return true;
+  }
+  int64_t i = u - q.ndx - q.ndw;
+  const int nc = p.gtiles + p.stats_units;
+  const int64_t per = (int64_t)32 * nc;
+  const int g = (int)(i / per), rem = (int)(i % per);
+  const int rows = min(32, q.nrt - g * 32);
+  t.rt = g * 32 + rem % rows;
+  const int c = rem / rows;
+  t.kt = t.split = t.s0 = 0;
+  t.steps = (p.k + 63) / 64;
+  t.N = p.NT;
+  if (p.stats_units > 0) {
+    t.mode = STATS;
+    t.ct = c * p.stats_run + sub;
+    return sub < p.stats_run && t.ct < p.stats_tiles;
+  }
+  t.mode = GRAD;
+  t.ct = c;
+  return sub == 0;
+}
+
+// One role's view of the posted units.
+struct Feed {
+  uint64_t* full;
+  uint32_t empty0;   // slot 0's release barrier in the even CTA (cluster address)
+  volatile int* unit;
+  int slot = 0;
+  uint32_t phase = 0;
+  // next unit, or -1 at the end (or after a wait that gave up)
+  __device__ __forceinline__ int next(volatile int* abort, int* err, int64_t units) {
+    if (!mbar_wait(&full[slot], phase, abort, err, 21)) return -1;
+    const int u = unit[slot];
+    arrive_cluster(empty0 + slot * 8);
+    if (++slot == kSlots) {
+      slot = 0;
+      phase ^= 1;
+    }
+    return u < units ? u : -1;
+  }
+};
+
+// --------------------------------------------------------------- epilogue --
+// Exponentials are 2^(z L - r) with L = log2(e) in fp32 and an integer r, the
+// running maximum of ceil(z L): the fused multiply-add rounds the small
+// difference only, rescaling a sum by 2^(r - r') is exact, and L's own error
+// (below 2^-26 relative) acts as a change of the logits by that much.
+// This adds 32 more logits to (r, s = sum of 2^(z L - r)); limit: columns of
+// the chunk that are classes.
+__device__ __forceinline__ void online(float (&v)[32], int limit, float& r, float& s) {
+  if (limit < 32) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j >= limit) v[j] = neg_inf();
+  }
+  float c[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c[j] = v[j];
+#pragma unroll
+  for (int j = 4; j < 32; ++j) c[j & 3] = fmaxf(c[j & 3], v[j]);
+  const float rn = fmaxf(r, ceilf(fmaxf(fmaxf(c[0], c[1]), fmaxf(c[2], c[3])) * kLog2e));
+  // every logit so far -inf: exponentials of -inf - 0, which are zeros
+  const float ref = rn == neg_inf() ? 0.0f : rn;
+  float a[4] = {s * ex2(r - ref), 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int j = 0; j < 32; ++j) a[j & 3] += ex2(__fmaf_rn(v[j], kLog2e, -ref));
+  s = (a[0] + a[1]) + (a[2] + a[3]);
+  r = rn;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    xent_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* stg_all = smem + kStages * kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(stg_all + kEpiWarps * kStg);
+  uint64_t* empty = full + kStages;
+  uint64_t* tfull = empty + kStages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* ufull = tempty + 2;
+  uint64_t* uempty = ufull + kSlots;
+  int* unit = reinterpret_cast<int*>(uempty + kSlots);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(unit + kSlots);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t cr = cluster_rank();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 2 * kEpiWarps);
+    }
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&ufull[s], 1);
+      mbar_init(&uempty[s], kConsumers);
+    }
+    *abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc2(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Plan q = make_plan(p);
+  Feed feed;
+  feed.full = ufull;
+  feed.empty0 = mapa(smem_u32(uempty), 0);
+  feed.unit = unit;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const CUtensorMap* xk = &maps.xk[q.nl < p.n];
+      const CUtensorMap* xm = &maps.xm[q.nl < p.n];
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      while (ok) {
+        const int u = feed.next(abort, p.err, q.units);
+        if (u < 0) break;
+        Tile t;
+        for (int sub = 0; ok && get_tile(p, q, u, sub, t); ++sub) {
+          const int hn = t.N / 2;
+          const uint32_t bytes = kStageA + (uint32_t)hn * 128;
+          for (int s = 0; s < t.steps; ++s) {
+            if (!(ok = mbar_wait(&empty[stage], phase ^ 1, abort, p.err, 22))) break;
+            const uint32_t a = smem_u32(smem + stage * kStageBytes), b = a + kStageA;
+            const uint32_t bar = mapa(smem_u32(&full[stage]), 0);
+            if (cr == 0) mbar_expect_tx(&full[stage], 2 * bytes);
+            const int x = (t.s0 + s) * 64;
+            if (t.mode <= GRAD) {
+              const int c0 = (t.mode == STATS ? 0 : p.gc0) + t.ct * p.NT;
+              tma_load_pair(a, xk, x, t.rt * kTile + cr * 128, bar);
+              tma_load_pair(b, &maps.wk, x, c0 + cr * hn, bar);
+            } else {
+              const CUtensorMap* bm = t.mode == DX ? &maps.wm : xm;
+              const int y = t.mode == DX ? p.pc0 + x : x;
+              if (t.mode == DX) {
+                tma_load_pair(a, &maps.gk, x, t.rt * kTile + cr * 128, bar);
+              } else {
+                tma_load_pair(a, &maps.gm, t.ct * kTile + cr * 128, x, bar);
+                tma_load_pair(a + 8192, &maps.gm, t.ct * kTile + cr * 128 + 64, x, bar);
+              }
+              for (int j = 0; j < hn; j += 64) tma_load_pair(b + j * 128, bm, t.kt * p.NK + cr * hn + j, y, bar);
+            }
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && cr == 0) {
+      int stage = 0, i = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      while (ok) {
+        const int u = feed.next(abort, p.err, q.units);
+        if (u < 0) break;
+        Tile t;
+        for (int sub = 0; ok && get_tile(p, q, u, sub, t); ++sub, ++i) {
+          const int a = i & 1;
+          if (!(ok = mbar_wait(&tempty[a], ((i >> 1) & 1) ^ 1, abort, p.err, 23))) break;
+          tc_fence_after();
+          const uint32_t d = tmem + a * 256;
+          const int amn = t.mode == DW, bmn = t.mode >= DX;
+          const uint32_t idesc = idesc_bf16_f32(256, t.N, amn, bmn);
+          // 16 contraction elements further: 32 bytes along a K-major row,
+          // two 8-row swizzle atoms in an MN-major block
+          const uint32_t as = amn ? 2048 : 32, bs = bmn ? 2048 : 32;
+          const uint32_t al = amn ? 8192 : 16, bl = bmn ? 8192 : 16;  // next 64-wide MN-major block
+          for (int s = 0; s < t.steps; ++s) {
+            if (!(ok = mbar_wait(&full[stage], phase, abort, p.err, 24))) break;
+            tc_fence_after();
+            const uint32_t ab = smem_u32(smem + stage * kStageBytes), bb = ab + kStageA;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_pair(d, smem_desc_sw128(ab + as * kk, al, 1024), smem_desc_sw128(bb + bs * kk, bl, 1024), idesc,
+                        (s | kk) != 0);
+            commit_pair(&empty[stage]);
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
+          if (ok) commit_pair(&tfull[a]);
+        }
+      }
+    }
+  } else if (warp < 10) {
+    const int quarter = warp & 3, h = (warp - 2) >> 2;
+    const int rit = cr * 128 + quarter * 32 + lane;  // row of the pair's tile
+    uint8_t* stg = stg_all + (warp - 2) * kStg;
+    const uint32_t tempty0 = mapa(smem_u32(tempty), 0);
+    int i = 0, nbox = 0;
+    bool ok = true;
+    while (ok) {
+      int u = 0;
+      if (lane == 0) u = feed.next(abort, p.err, q.units);
+      u = __shfl_sync(FULL, u, 0);
+      if (u < 0) break;
+      Tile t;
+      float m = neg_inf(), sum = 0.0f, w = 0.0f;
+      float2 nm = make_float2(0.0f, 0.0f);
+      int lab = -1, srow = -1;
+      for (int sub = 0; ok && get_tile(p, q, u, sub, t); ++sub, ++i) {
+        if (sub == 0 && t.mode <= GRAD) {
+          srow = t.rt * kTile + rit;
+          if (srow < q.nl) {
+            lab = p.lab[srow];
+            if (t.mode == GRAD) {
+              w = p.wrow[srow];
+              nm = p.norm[srow];
+            }
+          }
+        }
+        const int a = i & 1;
+        int got = 1;
+        if (lane == 0) got = mbar_wait(&tfull[a], (i >> 1) & 1, abort, p.err, 25);
+        ok = __shfl_sync(FULL, got, 0) != 0;
+        if (!ok) break;
+        tc_fence_after();
+        const int hn = t.N / 2, cb = h * hn;
+        const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + a * 256 + cb;
+        if (t.mode == STATS) {
+          for (int c = 0; c < hn; c += 32) {
+            float v[32];
+            tmem_ld32(taddr + c, v);
+            tmem_ld_wait();
+            const int c0 = t.ct * p.NT + cb + c;  // class of v[0]
+            if (__any_sync(FULL, (unsigned)(lab - c0) < 32u)) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (lab == c0 + j) p.zlab[srow] = v[j];
+            }
+            if (c0 < p.C) online(v, p.C - c0, m, sum);
+          }
+        } else if (t.mode == GRAD) {
+          for (int c = 0; c < hn; c += 32) {
+            float v[32];
+            tmem_ld32(taddr + c, v);
+            tmem_ld_wait();
+            const int cl = t.ct * p.NT + cb + c;  // column of G
+            const int c0 = p.gc0 + cl;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = ex2(__fmaf_rn(v[j], kLog2e, -nm.x)) * nm.y;
+            if (__any_sync(FULL, (unsigned)(lab - c0) < 32u)) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (lab == c0 + j) v[j] -= w;
+            }
+            if (c0 + 32 > p.C) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (c0 + j >= p.C) v[j] = 0.0f;
+            }
+            // row `lane` of a 32 x 32 box of 64-byte rows (64-byte swizzle:
+            // 16-byte piece j at piece j ^ ((lane >> 1) & 3))
+            uint8_t* box = stg + (nbox & 1) * 2048;
+            if (lane == 0) bulk_wait_read<1>();  // the store of two boxes ago has read this buffer
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t o[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
+              if (srow >= q.nl) o[0] = o[1] = o[2] = o[3] = 0;
+              *reinterpret_cast<uint4*>(box + lane * 64 + 16 * (j ^ ((lane >> 1) & 3))) =
+                  make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&maps.gst, box, cl, t.rt * kTile + cr * 128 + quarter * 32);
+              bulk_commit();
+            }
+            ++nbox;
+          }
+        } else {
+          const bool dw = t.mode == DW;
+          // fp32 sums that other pieces or splits add to, else the result
+          const bool sums = dw ? p.dws > 1 : p.dxs > 1 || !p.last;
+          const bool add = !dw && !p.first;
+          float* acc = nullptr;
+          if (sums || add) {
+            const int64_t tile = dw ? (int64_t)t.split * p.ptiles + t.ct : (int64_t)t.split * (p.npad / kTile) + t.rt;
+            acc = (dw ? p.accW : p.accX) + (tile * p.nkt + t.kt) * ((int64_t)p.NK * kTile) + rit;
+          }
+          const int r = (dw ? t.ct : t.rt) * kTile + rit;
+          int64_t orow = -1;  // row of the result this lane's sums belong to
+          if (dw) orow = p.pc0 + r < p.C ? p.pc0 + r : -1;
+          else if (r < q.nl) orow = q.nl < p.n ? p.idx[r] : r;
+          __nv_bfloat16* out = dw ? p.dW : p.dX;
+          const int64_t ldo = dw ? p.lddw : p.lddx;
+          for (int c = 0; c < hn; c += 64) {
+            float v[2][32];
+            if (t.steps > 0) {
+              tmem_ld32(taddr + c, v[0]);
+              tmem_ld32(taddr + c + 32, v[1]);
+              tmem_ld_wait();
+            } else {
+#pragma unroll
+              for (int j = 0; j < 64; ++j) v[j >> 5][j & 31] = 0.0f;
+            }
+            if (add) {
+#pragma unroll
+              for (int j = 0; j < 64; ++j) v[j >> 5][j & 31] += acc[(int64_t)(cb + c + j) * kTile];
+            }
+            if (sums) {
+#pragma unroll
+              for (int j = 0; j < 64; ++j) acc[(int64_t)(cb + c + j) * kTile] = v[j >> 5][j & 31];
+              continue;
+            }
+            const int k0 = t.kt * p.NK + cb + c;
+            if (k0 >= p.k) continue;
+            // through shared memory, so that a store writes whole 128-byte
+            // pieces of four rows: piece j of row `lane` at j ^ (lane & 7)
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              uint32_t o[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int x = 8 * j + 2 * e;
+                o[e] = pack_bf16x2(v[x >> 5][x & 31], v[x >> 5][(x & 31) + 1]);
+              }
+              *reinterpret_cast<uint4*>(stg + lane * 128 + 16 * (j ^ (lane & 7))) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int it = 0; it < 8; ++it) {
+              const int rr = it * 4 + (lane >> 3), j = lane & 7;
+              const uint4 o = *reinterpret_cast<const uint4*>(stg + rr * 128 + 16 * (j ^ (rr & 7)));
+              const int64_t to = __shfl_sync(FULL, orow, rr);
+              if (to < 0) continue;
+              const int col = k0 + 8 * j;
+              __nv_bfloat16* dst = out + to * ldo + col;
+              if (col + 8 <= p.k) {
+                *reinterpret_cast<uint4*>(dst) = o;
+              } else {
+                const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(&o);
+                for (int x = 0; col + x < p.k; ++x) dst[x] = e[x];
+              }
+            }
+            __syncwarp();
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(tempty0 + a * 8);
+        if (t.mode == STATS && (sub + 1 == p.stats_run || t.ct + 1 == p.stats_tiles))
+          p.part[(int64_t)(t.ct / p.stats_run * 2 + h) * p.npad + srow] = make_float2(m, sum);
+      }
+    }
+    if (lane == 0) bulk_wait<0>();  // every TMA store of this warp done
+  } else if (lane == 0 && cr == 0) {
+    int slot = 0;
+    uint32_t phase = 0;
+    while (mbar_wait(&uempty[slot], phase ^ 1, abort, p.err, 26)) {
+      const int64_t next = atomicAdd(p.counter, 1);
+      const int u = next < q.units ? (int)next : 0x7fffffff;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t bar = mapa(smem_u32(&ufull[slot]), r);
+        expect_cluster(bar, 4);
+        st_async(mapa(smem_u32(&unit[slot]), r), u, bar);
+      }
+      if (u == 0x7fffffff) break;
+      if (++slot == kSlots) {
+        slot = 0;
+        phase ^= 1;
+      }
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc2(tmem, 512);
+  }
+  cluster_sync();
+}
+
+// ------------------------------------------------------- rows with a label --
+// The labelled rows in order.  Blocks take consecutive segments: a first
+// kernel counts, the second sums the counts before its segment and numbers.
+constexpr int kScanThreads = 1024;
+
+__device__ __forceinline__ bool labelled(int y, int C) { return (unsigned)y < (unsigned)C; }
+
+__global__ void __launch_bounds__(kScanThreads) xent_count_kernel(const int* __restrict__ labels, int64_t n, int C,
+                                                                 int64_t seg, int* cnt) {
+  __shared__ int s;
+  if (threadIdx.x == 0) s = 0;
+  __syncthreads();
+  const int64_t e = min(n, (blockIdx.x + 1) * seg);
+  int c = 0;
+  for (int64_t r = blockIdx.x * seg + threadIdx.x; r < e; r += kScanThreads) c += labelled(labels[r], C);
+  c = __reduce_add_sync(FULL, c);
+  if ((threadIdx.x & 31) == 0) atomicAdd(&s, c);  // integers: the order does not matter
+  __syncthreads();
+  if (threadIdx.x == 0) cnt[blockIdx.x] = s;
+}
+
+struct ScanOut {
+  int* nl;
+  int* pos;       // row of X -> labelled row, or -1
+  int* idx;
+  int* lab;
+  float* wrow;
+  float* loss;
+  float* lse;
+  int* counters;  // of the tile launches, zeroed here
+  int n_counters;
+};
+
+__global__ void __launch_bounds__(kScanThreads)
+    xent_scan_kernel(const int* __restrict__ labels, const float* __restrict__ weight, float scale, int64_t n, int C,
+                     int64_t seg, const int* __restrict__ cnt, const ScanOut o) {
+  __shared__ int ws[32];
+  __shared__ int base;
+  if (threadIdx.x == 0) base = 0;
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x > 0) {
+    int c = 0;
+    for (int b = threadIdx.x; b < (int)blockIdx.x; b += kScanThreads) c += cnt[b];
+    c = __reduce_add_sync(FULL, c);
+    if (lane == 0) atomicAdd(&base, c);
+    __syncthreads();
+  } else {
+    for (int j = threadIdx.x; j < o.n_counters; j += kScanThreads) o.counters[j] = 0;
+  }
+  const int64_t b0 = blockIdx.x * seg, e = min(n, b0 + seg);
+  int at = base;
+  for (int64_t r0 = b0; r0 < e; r0 += kScanThreads) {
+    const int64_t r = r0 + threadIdx.x;
+    const int y = r < e ? labels[r] : -1;
+    const bool on = labelled(y, C);
+    const unsigned bal = __ballot_sync(FULL, on);
+    if (lane == 0) ws[warp] = __popc(bal);
+    __syncthreads();
+    const int mine = ws[lane];
+    const int before = __reduce_add_sync(FULL, lane < warp ? mine : 0);
+    const int all = __reduce_add_sync(FULL, mine);
+    if (r < e) {
+      const int to = on ? at + before + __popc(bal & ((1u << lane) - 1)) : -1;
+      o.pos[r] = to;
+      if (on) {
+        o.idx[to] = (int)r;
+        o.lab[to] = y;
+        o.wrow[to] = (weight != nullptr ? weight[r] : 1.0f) * scale;
+      } else {
+        if (o.loss != nullptr) o.loss[r] = 0.0f;
+        if (o.lse != nullptr) o.lse[r] = 0.0f;
+      }
+    }
+    at += all;
+    __syncthreads();
+  }
+  if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) *o.nl = at;
+}
+
+// The labelled rows of X together (zeros up to a multiple of 256 rows) and
+// zeros in the other rows of dX; nothing when every row is labelled.
+__global__ void __launch_bounds__(256) xent_rows_kernel(const __nv_bfloat16* __restrict__ X, int64_t n, int k,
+                                                        int64_t ldx, const int* __restrict__ pos,
+                                                        const int* __restrict__ nl, __nv_bfloat16* Xc, int64_t ldc,
+                                                        __nv_bfloat16* dX, int64_t lddx) {
+  const int m = *nl;
+  if (m == n) return;
+  const int lane = threadIdx.x & 31;
+  const int64_t step = (int64_t)gridDim.x * 8;
+  for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < n + kTile; r += step) {
+    const int64_t to = r < n ? pos[r] : (m + (r - n) < (m + kTile - 1) / kTile * (int64_t)kTile ? m + (r - n) : -1);
+    if (to < 0 && (r >= n || dX == nullptr)) continue;
+    const __nv_bfloat16* src = r < n && to >= 0 ? X + r * ldx : nullptr;
+    __nv_bfloat16* dst = to >= 0 ? Xc + to * ldc : dX + r * lddx;
+    for (int c = lane * 8; c < k; c += 256) {
+      if (c + 8 <= k) {
+        *reinterpret_cast<uint4*>(dst + c) =
+            src != nullptr ? __ldg(reinterpret_cast<const uint4*>(src + c)) : make_uint4(0, 0, 0, 0);
+      } else {
+        for (int j = c; j < k; ++j) dst[j] = src != nullptr ? src[j] : __float2bfloat16_rn(0.0f);
+      }
+    }
+  }
+}
+
+// lse and loss of 32 labelled rows per block from the runs' (r, sum) pairs:
+// 32 lanes of runs per row, joined in lane order.  The loss is taken from
+// the label's logit in the form the sum has it, z L - r.
+__global__ void __launch_bounds__(1024)
+    xent_join_kernel(const float2* __restrict__ part, int runs, int64_t npad, const int* __restrict__ nl,
+                     const int* __restrict__ idx, const float* __restrict__ zlab, const float* __restrict__ wrow,
+                     float2* norm, float* loss, float* lse) {
+  __shared__ float sm[32][33], ss[32][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int rows = *nl;
+  for (int64_t r0 = (int64_t)blockIdx.x * 32; r0 < rows; r0 += (int64_t)gridDim.x * 32) {
+    const int64_t row = r0 + lane;
+    float r = neg_inf(), s = 0.0f;
+    for (int u = w; u < runs; u += 32) {
+      const float2 v = part[(int64_t)u * npad + row];
+      const float rn = fmaxf(r, v.x), ref = rn == neg_inf() ? 0.0f : rn;
+      s = s * ex2(r - ref) + v.y * ex2(v.x - ref);
+      r = rn;
+    }
+    sm[w][lane] = r;
+    ss[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && row < rows) {
+      for (int j = 1; j < 32; ++j) r = fmaxf(r, sm[j][lane]);
+      const float ref = r == neg_inf() ? 0.0f : r;
+      s = 0.0f;
+      for (int j = 0; j < 32; ++j) s += ss[j][lane] * ex2(sm[j][lane] - ref);
+      const float l2 = log2f(s);
+      if (norm != nullptr) norm[row] = make_float2(ref, wrow[row] / s);
+      const int to = idx[row];
+      if (loss != nullptr) loss[to] = kLn2 * (l2 - __fmaf_rn(zlab[row], kLog2e, -ref));
+      if (lse != nullptr) lse[to] = __fmaf_rn(ref, kLn2, l2 * kLn2);
+    }
+    __syncthreads();
+  }
+}
+
+// Sums of the splits in order -> bf16 rows.  A block: 256 rows of one tile,
+// 8 columns.
+__global__ void __launch_bounds__(256)
+    xent_sum_kernel(const float* __restrict__ acc, int splits, int64_t split_stride, int64_t tile_stride,
+                    const int* __restrict__ nl, int64_t n, const int* __restrict__ idx, int row0, int C, int k,
+                    __nv_bfloat16* out, int64_t ldo) {
+  const int c0 = blockIdx.y * 8;
+  if (c0 >= k) return;
+  const int64_t r = (int64_t)blockIdx.x * kTile + threadIdx.x;
+  int64_t to;
+  if (idx != nullptr) {
+    if (r >= *nl) return;
+    to = *nl < n ? idx[r] : r;
+  } else {
+    to = row0 + r;
+    if (to >= C) return;
+  }
+  const float* a = acc + blockIdx.x * tile_stride + (int64_t)c0 * kTile + threadIdx.x;
+  float v[8] = {};
+  for (int s = 0; s < splits; ++s)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += a[s * split_stride + j * kTile];
+  __nv_bfloat16* dst = out + to * ldo + c0;
+  if (c0 + 8 <= k) {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c0 + j < k) dst[j] = __float2bfloat16_rn(v[j]);
+  }
+}
+
+// ------------------------------------------------------------------- host --
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+// bf16 [outer][inner] of row pitch ld: boxes of bi x bo, zeros out of bounds
+int tmap(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld, int bi, int bo) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return GQ_ERR_CUDA;
+  const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {(cuuint32_t)bi, (cuuint32_t)bo};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r =
+      fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, bi == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? GQ_OK : GQ_ERR_INVALID_ARG;
+}
+
+int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Bytes of one buffer of G.
+constexpr int64_t kPieceBytes = (int64_t)128 << 20;
+
+struct Sizes {
+  int64_t npad, nrt;
+  int clusters;
+  int NT, ctiles;             // class tile width and tiles
+  int NK, nkt;
+  int run, units;             // STATS
+  int per_piece, pieces;      // class tiles of a piece; pieces
+  int64_t Cp;                 // classes of a piece = pitch of G
+  int dxs, dws;
+  int scan_blocks;
+  int64_t seg;
+};
+
+Sizes make_sizes(int64_t n, int k, int C, bool grad) {
+  Sizes z{};
+  z.npad = up(n, kTile);
+  z.nrt = z.npad / kTile;
+  z.clusters = sm_count() / 2 > 0 ? sm_count() / 2 : 1;
+  z.NT = (int)up(cdiv(C, cdiv(C, kTile)), 64);
+  z.ctiles = (int)cdiv(C, z.NT);
+  z.NK = (int)up(cdiv(k, cdiv(k, kTile)), 128);
+  z.nkt = (int)cdiv(k, z.NK);
+  // runs of class tiles per row tile: long runs leave few pairs to join,
+  // about eight units per CTA pair leave a short tail
+  int64_t run = z.nrt * z.ctiles / (8 * z.clusters);
+  z.run = (int)(run < 1 ? 1 : run > 16 ? 16 : run);
+  z.units = (int)cdiv(z.ctiles, z.run);
+  z.seg = up(cdiv(n, 256), kScanThreads);
+  z.scan_blocks = (int)cdiv(n, z.seg);
+  if (!grad) return z;
+  int64_t t = kPieceBytes / (z.npad * z.NT * 2);
+  t = t < 1 ? 1 : t > z.ctiles ? z.ctiles : t;
+  z.per_piece = (int)cdiv(z.ctiles, cdiv(z.ctiles, t));  // pieces of nearly equal size
+  z.pieces = (int)cdiv(z.ctiles, z.per_piece);
+  z.Cp = (int64_t)z.per_piece * z.NT;
+  // Long sums are split where a launch would otherwise wait for them: no
+  // tile longer than a CTA pair's share of the launch, none below 32 steps
+  // (a split writes and reads 256 x NK fp32 sums, about 16 steps' time).
+  const int64_t sx = z.Cp / 64, sw = z.npad / 64, ptiles = cdiv(z.Cp, kTile);
+  const int64_t total = z.nrt * z.nkt * sx + ptiles * z.nkt * sw + (z.pieces > 1 ? z.nrt * z.per_piece * cdiv(k, 64) : 0);
+  int64_t share = total / z.clusters;
+  if (share < 32) share = 32;
+  z.dxs = (int)cdiv(sx, share);
+  z.dws = (int)cdiv(sw, share);
+  return z;
+}
+
+struct Ws {
+  int* nl;
+  int* counters;
+  int n_counters;
+  int *cnt, *pos, *idx, *lab;
+  float *wrow, *zlab;
+  float2* norm;
+  float2* part;
+  void* Xc;
+  void* G[2];
+  float *accX, *accW;
+};
+
+Carve carve(void* ws, size_t bytes, const Sizes& z, int64_t n, int k, bool grad, Ws& w) {
+  Carve c(ws, bytes);
+  w.n_counters = 2 + (grad ? z.pieces : 0);
+  w.nl = static_cast<int*>(c.take(256));
+  w.counters = static_cast<int*>(c.take((size_t)w.n_counters * 4));
+  w.cnt = static_cast<int*>(c.take((size_t)z.scan_blocks * 4));
+  w.pos = static_cast<int*>(c.take((size_t)n * 4));
+  w.idx = static_cast<int*>(c.take((size_t)z.npad * 4));
+  w.lab = static_cast<int*>(c.take((size_t)z.npad * 4));
+  w.wrow = static_cast<float*>(c.take((size_t)z.npad * 4));
+  w.norm = static_cast<float2*>(c.take((size_t)z.npad * 8));
+  w.zlab = static_cast<float*>(c.take((size_t)z.npad * 4));
+  w.part = static_cast<float2*>(c.take((size_t)z.units * 2 * z.npad * sizeof(float2)));
+  w.Xc = c.take((size_t)z.npad * round8(k) * 2);
+  if (!grad) return c;
+  w.G[0] = c.take((size_t)z.npad * z.Cp * 2);
+  w.G[1] = z.pieces > 1 ? c.take((size_t)z.npad * z.Cp * 2) : w.G[0];
+  const size_t tile = (size_t)z.nkt * z.NK * kTile * 4;
+  if (z.pieces > 1 || z.dxs > 1) w.accX = static_cast<float*>(c.take(z.dxs * z.nrt * tile));
+  if (z.dws > 1) w.accW = static_cast<float*>(c.take(z.dws * cdiv(z.Cp, kTile) * tile));
+  return c;
+}
+
+int check_shape(int64_t n, int k, int C) {
+  if (n < 0 || k < 1 || C < 1) return GQ_ERR_INVALID_ARG;
+  if (n > INT32_MAX - 1024 || C > (1 << 30) || k > 16384) return GQ_ERR_UNSUPPORTED;
+  // units of one launch are numbered in 31 bits
+  if (cdiv(n, kTile) * cdiv(C, 64) > INT32_MAX / 4) return GQ_ERR_UNSUPPORTED;
+  return GQ_OK;
+}
+
+int launch_tiles(const Maps& m, Args& a, const Sizes& z, cudaStream_t s) {
+  GQ_TRY_CUDA(cudaFuncSetAttribute(xent_tiles_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+  xent_tiles_kernel<<<2 * z.clusters, kThreads, kSmem, s>>>(m, a);
+  ++a.counter;
+  return launch_status();
+}
+
+}  // namespace
+}  // namespace gq
+
+using namespace gq;
+
+extern "C" size_t gq_linear_xent_workspace_bytes(int64_t n, int k, int C, int need_grad) {
+  if (check_shape(n, k, C) != GQ_OK || n == 0) return 0;
+  Ws w{};
+  return carve(nullptr, 0, make_sizes(n, k, C, need_grad != 0), n, k, need_grad != 0, w).used;
+}
+
+extern "C" int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, const uint16_t* W, int C, int64_t ldw,
+                              const int32_t* labels, const float* weight, float scale, float* loss, float* lse,
+                              uint16_t* dX, int64_t lddx, uint16_t* dW, int64_t lddw, void* ws, size_t ws_bytes,
+                              int* dev_err, gq_stream stream) {
+  GQ_TRY(check_shape(n, k, C));
+  auto s = (cudaStream_t)stream;
+  if (dW != nullptr && (lddw < k || lddw % 8 || !aligned(dW, 16))) return GQ_ERR_INVALID_ARG;
+  if (n == 0) {  // no rows: dW = 0
+    if (dW != nullptr) GQ_TRY_CUDA(cudaMemset2DAsync(dW, (size_t)lddw * 2, 0, (size_t)k * 2, (size_t)C, s));
+    return GQ_OK;
+  }
+  if (X == nullptr || W == nullptr || labels == nullptr || ldx < k || ldw < k || ldx % 8 || ldw % 8 ||
+      !aligned(X, 16) || !aligned(W, 16) || !aligned(labels, 4) || !aligned(weight, 4) || !aligned(loss, 4) ||
+      !aligned(lse, 4) || !aligned(dev_err, 4))
+    return GQ_ERR_INVALID_ARG;
+  if (dX != nullptr && (lddx < k || lddx % 8 || !aligned(dX, 16))) return GQ_ERR_INVALID_ARG;
+  const bool grad = dX != nullptr || dW != nullptr;
+  const Sizes z = make_sizes(n, k, C, grad);
+  Ws w{};
+  if (ws == nullptr || !aligned(ws, 256) || !carve(ws, ws_bytes, z, n, k, grad, w).ok()) return GQ_ERR_WORKSPACE;
+
+  if (z.scan_blocks > 1) {
+    xent_count_kernel<<<z.scan_blocks, kScanThreads, 0, s>>>(labels, n, C, z.seg, w.cnt);
+    GQ_TRY(launch_status());
+  }
+  const ScanOut so{w.nl, w.pos, w.idx, w.lab, w.wrow, loss, lse, w.counters, w.n_counters};
+  xent_scan_kernel<<<z.scan_blocks, kScanThreads, 0, s>>>(labels, weight, scale, n, C, z.seg, w.cnt, so);
+  GQ_TRY(launch_status());
+  const int64_t ldc = round8(k);
+  const int64_t rb = cdiv(n + kTile, 8), rcap = (int64_t)sm_count() * 8;
+  xent_rows_kernel<<<(int)(rb < rcap ? rb : rcap), 256, 0, s>>>(
+      reinterpret_cast<const __nv_bfloat16*>(X), n, k, ldx, w.pos, w.nl, static_cast<__nv_bfloat16*>(w.Xc), ldc,
+      reinterpret_cast<__nv_bfloat16*>(dX), lddx);
+  GQ_TRY(launch_status());
+
+  Maps m;
+  memset(&m, 0, sizeof(m));
+  GQ_TRY(tmap(&m.xk[0], X, k, n, ldx, 64, 128));
+  GQ_TRY(tmap(&m.xk[1], w.Xc, k, z.npad, ldc, 64, 128));
+  GQ_TRY(tmap(&m.wk, W, k, C, ldw, 64, z.NT / 2));
+  Args a{};
+  a.nl = w.nl;
+  a.counter = w.counters;
+  a.n = n;
+  a.npad = z.npad;
+  a.k = k;
+  a.C = C;
+  a.NT = z.NT;
+  a.NK = z.NK;
+  a.nkt = z.nkt;
+  a.lab = w.lab;
+  a.wrow = w.wrow;
+  a.norm = w.norm;
+  a.zlab = w.zlab;
+  a.idx = w.idx;
+  a.part = w.part;
+  a.err = dev_err;
+  a.stats_tiles = z.ctiles;
+  a.stats_run = z.run;
+  a.stats_units = z.units;
+  GQ_TRY(launch_tiles(m, a, z, s));
+  const int64_t jb = cdiv(n, 32), jcap = (int64_t)sm_count() * 2;
+  xent_join_kernel<<<(int)(jb < jcap ? jb : jcap), 1024, 0, s>>>(w.part, 2 * z.units, z.npad, w.nl, w.idx, w.zlab,
+                                                                 w.wrow, grad ? w.norm : nullptr, loss, lse);
+  GQ_TRY(launch_status());
+  if (!grad) return GQ_OK;
+
+  GQ_TRY(tmap(&m.xm[0], X, k, n, ldx, 64, 64));
+  GQ_TRY(tmap(&m.xm[1], w.Xc, k, z.npad, ldc, 64, 64));
+  GQ_TRY(tmap(&m.wm, W, k, C, ldw, 64, 64));
+  a.stats_units = 0;
+  a.dxs = z.dxs;
+  a.dws = z.dws;
+  a.accX = w.accX;
+  a.accW = w.accW;
+  a.dX = reinterpret_cast<__nv_bfloat16*>(dX);
+  a.lddx = lddx;
+  a.dW = reinterpret_cast<__nv_bfloat16*>(dW);
+  a.lddw = lddw;
+  const int64_t tile = (int64_t)z.nkt * z.NK * kTile;
+  for (int i = 0; i <= z.pieces; ++i) {  // GRAD of piece i beside DX and DW of piece i - 1
+    const int done = i - 1;
+    a.gc0 = i * (int)z.Cp;
+    a.gtiles = i < z.pieces ? (z.ctiles - i * z.per_piece < z.per_piece ? z.ctiles - i * z.per_piece : z.per_piece) : 0;
+    if (i < z.pieces) GQ_TRY(tmap(&m.gst, w.G[i & 1], z.Cp, z.npad, z.Cp, 32, 32));
+    int ptiles = 0;
+    if (i > 0) {
+      const int classes = (done + 1 < z.pieces ? z.per_piece : z.ctiles - done * z.per_piece) * z.NT;
+      ptiles = (int)cdiv(classes, kTile);
+      GQ_TRY(tmap(&m.gk, w.G[done & 1], z.Cp, z.npad, z.Cp, 64, 128));
+      GQ_TRY(tmap(&m.gm, w.G[done & 1], z.Cp, z.npad, z.Cp, 64, 64));
+      a.pc0 = done * (int)z.Cp;
+      a.psteps = classes / 64;
+      a.ptiles = ptiles;
+      a.do_dx = dX != nullptr;
+      a.do_dw = dW != nullptr;
+      a.dw_first = z.npad / 64 / z.dws > a.psteps / z.dxs;
+      a.first = done == 0;
+      a.last = i == z.pieces;
+    }
+    GQ_TRY(launch_tiles(m, a, z, s));
+    if (i > 0 && dW != nullptr && z.dws > 1) {
+      xent_sum_kernel<<<dim3(ptiles, (unsigned)cdiv(k, 8)), 256, 0, s>>>(
+          w.accW, z.dws, ptiles * tile, tile, w.nl, n, nullptr, a.pc0, C, k, a.dW, lddw);
+      GQ_TRY(launch_status());
+    }
+  }
+  if (dX != nullptr && z.dxs > 1) {
+    xent_sum_kernel<<<dim3((unsigned)z.nrt, (unsigned)cdiv(k, 8)), 256, 0, s>>>(
+        w.accX, z.dxs, z.nrt * tile, tile, w.nl, n, w.idx, 0, C, k, a.dX, lddx);
+    GQ_TRY(launch_status());
+  }
+  return GQ_OK;
+}

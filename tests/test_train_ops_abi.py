@@ -73,3 +73,30 @@ def test_layer_norm_bwd_refuses(L, kw):
 def test_layer_norm_bwd_workspace(L):
     assert _bwd(L, ws=None) == WORKSPACE
     assert _bwd(L, wsb=L.gq_layer_norm_bwd_workspace_bytes(10, 16) - 1) == WORKSPACE
+
+
+def _xent(L, X=FAKE, n=10, k=16, ldx=16, W=FAKE, C=30, ldw=16, lab=FAKE, dX=FAKE, lddx=16, dW=FAKE, lddw=16,
+          ws=FAKE, wsb=1 << 40, loss=FAKE):
+    return L.gq_linear_xent(X, n, k, ldx, W, C, ldw, lab, None, 1.0, loss, None, dX, lddx, dW, lddw, ws, wsb, None,
+                            None)
+
+
+@pytest.mark.parametrize("kw", [dict(X=None), dict(W=None), dict(lab=None), dict(n=-1), dict(k=0), dict(C=0),
+                                dict(ldx=8), dict(ldx=17), dict(ldw=8), dict(ldw=20), dict(lddx=8), dict(lddx=18),
+                                dict(lddw=8), dict(lddw=18), dict(X=C.c_void_p(0x1008)), dict(W=C.c_void_p(0x1008)),
+                                dict(dX=C.c_void_p(0x1008)), dict(dW=C.c_void_p(0x1008)), dict(lab=ODD),
+                                dict(loss=ODD)])
+def test_linear_xent_refuses(L, kw):
+    assert _xent(L, **kw) == INVALID
+
+
+def test_linear_xent_limits(L):
+    assert _xent(L, k=16392, ldx=16392, ldw=16392, lddx=16392, lddw=16392) == UNSUPPORTED
+    assert _xent(L, n=1 << 31) == UNSUPPORTED and _xent(L, C=(1 << 30) + 1) == UNSUPPORTED
+    assert _xent(L, n=1 << 30, C=1 << 20) == UNSUPPORTED
+    assert _xent(L, ws=None) == WORKSPACE and _xent(L, ws=C.c_void_p(0x1010)) == WORKSPACE
+    need = L.gq_linear_xent_workspace_bytes(10, 16, 30, 1)
+    assert need > L.gq_linear_xent_workspace_bytes(10, 16, 30, 0) > 0
+    assert _xent(L, wsb=need - 1) == WORKSPACE
+    assert L.gq_linear_xent_workspace_bytes(10, 0, 30, 1) == 0
+    assert _xent(L, n=0, X=None, W=None, lab=None, dX=None, dW=None, ws=None) == 0
