@@ -87,10 +87,11 @@ GQ_API int gq_layer_norm_bwd(const void* dY, int64_t lddy, const void* X, int64_
  *   Z = X W^T                       (n x C, fp32 sums of bf16 products)
  *   for a row with 0 <= labels[r] < C:
  *     lse[r]  = log sum_c exp(Z[r,c]);  loss[r] = lse[r] - Z[r, labels[r]]
- *     G[r,c]  = weight[r] * scale * (exp(Z[r,c] - lse[r]) - [c = labels[r]])
+ *     G[r,c]  = weight[r] * (exp(Z[r,c] - lse[r]) - [c = labels[r]])
  *   for any other row (an unlabelled node, padding): loss = lse = 0, its
  *     row of dX is zero, and what X holds there enters nothing
- *   dX = G W,  dW = G^T X           (G in bf16, fp32 sums, rounded to bf16)
+ *   dX = scale G W,  dW = scale G^T X    (G in bf16, fp32 sums and scaling,
+ *     rounded to bf16)
  * so dX and dW are the gradients of scale * sum_r weight[r] loss[r].
  *   X       n x k bf16 (ldx), W  C x k bf16 (ldw), one class per row
  *   labels  n int32;  weight: n fp32 or NULL (1);  scale: host value
@@ -100,14 +101,15 @@ GQ_API int gq_layer_norm_bwd(const void* dY, int64_t lddy, const void* X, int64_
  *           columns past k are neither read as values nor written
  *   ws      gq_linear_xent_workspace_bytes(n, k, C, need_grad) bytes,
  *           256-byte aligned, need_grad != 0 when dX or dW is given (about
- *           2 n k bytes, and two pieces of G of 128 MB or n x 256 classes;
+ *           2 n k bytes, and two pieces of G of 1 GB, or n x C or n x 256 entries,
+ *           whichever applies;
  *           depends on the current device's SM count).  Calls sharing one
  *           workspace must not overlap.
  *   dev_err nullable device int, as for the GEMMs (codes 21 .. 26)
  * Results are the same from run to run.  dX and dW must not overlap X or W.
  * Errors: GQ_ERR_INVALID_ARG (null X, W or labels, n < 0, k < 1, C < 1, bad
  * leading dimensions or alignment); GQ_ERR_UNSUPPORTED for k > 16384,
- * n > 2^31 - 1025, C > 2^30 or ceil(n / 256) * ceil(C / 64) >= 2^29;
+ * n > 2^28, C > 2^30 or ceil(n / 256) * ceil(C / 64) >= 2^29;
  * GQ_ERR_WORKSPACE.  n == 0 writes dW = 0.
  * ---------------------------------------------------------------------- */
 GQ_API size_t gq_linear_xent_workspace_bytes(int64_t n, int k, int C, int need_grad);

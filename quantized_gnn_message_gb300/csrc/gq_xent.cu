@@ -2,7 +2,7 @@
 // classes, with its gradients, without keeping the logits.
 //
 //   Z = X W^T (n x C);  lse_i = log sum_c exp(Z_ic);  loss_i = lse_i - Z_iy
-//   G = w_i (softmax(Z) - onehot(y));  dX = G W;  dW = G^T X
+//   G = w_i (softmax(Z) - onehot(y));  dX = scale G W;  dW = scale G^T X
 //
 // Rows without a label take no part: the labelled rows are numbered in order
 // by a scan, and copied together unless every row is labelled, so neither
@@ -11,7 +11,7 @@
 // Four products on the tcgen05 tensor cores (bf16 inputs, fp32 sums in
 // TMEM), all tiles of one persistent kernel:
 //   STATS  Z tile -> running maximum and sum of exponentials per row and run
-//          of class tiles, and the label's logit
+//          of class tiles
 //   GRAD   Z tile again -> G of one piece of the classes, in bf16
 //   DX     dX += G W over the piece (fp32 sums between pieces)
 //   DW     dW of the piece's classes = G^T X
@@ -27,16 +27,23 @@
 //   warp 1      (even CTA) one thread issues tcgen05.mma into one of two
 //               TMEM accumulators of 256 columns; its commits release the
 //               stages of both CTAs
-//   warps 2-9   epilogue: lane = row, warps 2-5 the first half of the
-//               columns, 6-9 the second; the next tile's products run
-//               meanwhile in the other accumulator
+//   warps 2-9   epilogue: lane = row, the chunks of 32 columns dealt out to
+//               two warps per 32 rows; the next tile's products run
+//               meanwhile in the other accumulator (16 warps: no faster on
+//               short tiles, and 5% slower on long ones, where power counts)
 //   warp 10     (even CTA) draws the next unit of work from a counter and
 //               posts it to both CTAs.  Which CTA computes a tile does not
 //               change its value, so results do not depend on the order.
 //
+// G is kept in blocks of 64 classes, [class / 64][row][class % 64], so that a
+// box of DX (64 classes x 128 rows) or DW (64 x 64) is one contiguous run of
+// memory; rows of a power-of-two pitch made both a third slower.
+//
 // G is rounded to bf16, the type that the products dX and dW take: each
 // entry is off by at most half a step (2^-8 of its value, about as much as
 // the rounding of a bf16 result; errors of a sum's entries mostly cancel).
+// The common factor `scale` is applied to the fp32 sums instead: within G it
+// would put the same rounding error on every row's largest entry, p - 1.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
@@ -51,14 +58,16 @@
 namespace gq {
 namespace {
 
-constexpr int kThreads = 352;    // TMA, MMA, 8 epilogue warps, scheduler
 constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarps + 3);  // TMA, MMA, epilogue, scheduler
+constexpr int kParts = kEpiWarps / 4;           // warps that share a row's columns
 constexpr int kStages = 6;
 constexpr int kStageA = 128 * 128;                    // 128 rows x 64 bf16 (or 2 x 64 x 64)
 constexpr int kStageBytes = 2 * kStageA;
-constexpr int kStg = 4096;       // epilogue staging per warp
+constexpr int kBox = 2048;       // 32 rows x 32 bf16
+constexpr int kStg = 2 * kBox;   // epilogue staging per warp
 constexpr int kSlots = 4;        // units of work posted ahead
-constexpr int kConsumers = 19;   // even CTA: TMA, MMA, 8 epilogue; odd CTA: TMA, 8 epilogue
+constexpr int kConsumers = 3 + 2 * kEpiWarps;  // even CTA: TMA, MMA, epilogue; odd CTA: TMA, epilogue
 constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kStg + 512;
 constexpr int kTile = 256;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -85,12 +94,10 @@ struct Args {
   int do_dx, do_dw, dw_first;
   int dxs, dws;          // splits of their sums
   int first, last;       // the piece read is the first / last one
-  const int* lab;        // per labelled row
-  const float* wrow;
-  const float2* norm;    // r, weight / sum of 2^(z L - r)
-  float* zlab;
+  float scale;           // of the results: G is formed without it, see below
+  const float4* row;     // r, weight / sum of 2^(z L - r), G of the label, label (as int)
   const int* idx;        // labelled row -> row of X
-  float2* part;          // [unit * 2 + half][npad]: r, sum
+  float2* part;          // [unit * kParts + part][npad]: r, sum
   float* accX;           // [split][row tile][nkt NK][256]
   float* accW;           // [split][class tile][nkt NK][256]
   __nv_bfloat16* dX;
@@ -114,11 +121,16 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
+// Arrival on a barrier of either CTA.  CTA scope: what the arrivals order are
+// reads of this thread (of a posted unit, of an accumulator by tcgen05.ld
+// behind its own fence), not global writes, and a release at cluster scope
+// costs a memory barrier each time (a quarter of the warps' stalls; loss and
+// gradients of 16,384 x 256 x 131,072 classes 4.93 -> 4.67 ms without it).
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void expect_cluster(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void st_async(uint32_t addr, int v, uint32_t bar) {
@@ -172,11 +184,58 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
       : "r"(taddr)
       : "memory");
 }
+// Bounded wait on a barrier phase, the thread suspended in hardware meanwhile
+// (spinning warps cost power that the tensor cores could use).  False after
+// the limit, or once another role of the CTA has given up.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, int where) {
+  const uint32_t b = smem_u32(bar);
+  if (mbar_try_wait_u32(b, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait_u32(b, parity)) {
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *abort = 1;
+      if (err != nullptr) atomicCAS(err, 0, where);
+      return false;
+    }
+  }
+  return true;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Two fp32 operations at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
+        "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Rare branches of the epilogue: kept as branches, not as 32 selects a chunk.
+__device__ __forceinline__ void keep_branch() { asm volatile("" ::: "memory"); }
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 
 // ------------------------------------------------------------------ tiles --
@@ -253,7 +312,7 @@ struct Feed {
   uint32_t phase = 0;
   // next unit, or -1 at the end (or after a wait that gave up)
   __device__ __forceinline__ int next(volatile int* abort, int* err, int64_t units) {
-    if (!mbar_wait(&full[slot], phase, abort, err, 21)) return -1;
+    if (!wait(&full[slot], phase, abort, err, 21)) return -1;
     const int u = unit[slot];
     arrive_cluster(empty0 + slot * 8);
     if (++slot == kSlots) {
@@ -273,6 +332,7 @@ struct Feed {
 // the chunk that are classes.
 __device__ __forceinline__ void online(float (&v)[32], int limit, float& r, float& s) {
   if (limit < 32) {
+    keep_branch();
 #pragma unroll
     for (int j = 0; j < 32; ++j)
       if (j >= limit) v[j] = neg_inf();
@@ -281,14 +341,23 @@ __device__ __forceinline__ void online(float (&v)[32], int limit, float& r, floa
 #pragma unroll
   for (int j = 0; j < 4; ++j) c[j] = v[j];
 #pragma unroll
-  for (int j = 4; j < 32; ++j) c[j & 3] = fmaxf(c[j & 3], v[j]);
-  const float rn = fmaxf(r, ceilf(fmaxf(fmaxf(c[0], c[1]), fmaxf(c[2], c[3])) * kLog2e));
+  for (int j = 4; j < 28; j += 8)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = max3(c[i], v[j + 2 * i], v[j + 2 * i + 1]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = fmaxf(c[i], v[28 + i]);
+  const float rn = fmaxf(r, ceilf(fmaxf(max3(c[0], c[1], c[2]), c[3]) * kLog2e));
   // every logit so far -inf: exponentials of -inf - 0, which are zeros
   const float ref = rn == neg_inf() ? 0.0f : rn;
-  float a[4] = {s * ex2(r - ref), 0.0f, 0.0f, 0.0f};
+  const float2 l2e = make_float2(kLog2e, kLog2e), nref = make_float2(-ref, -ref);
+  float2 a[2] = {make_float2(s * ex2(r - ref), 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-  for (int j = 0; j < 32; ++j) a[j & 3] += ex2(__fmaf_rn(v[j], kLog2e, -ref));
-  s = (a[0] + a[1]) + (a[2] + a[3]);
+  for (int j = 0; j < 32; j += 2) {
+    const float2 x = fma2(make_float2(v[j], v[j + 1]), l2e, nref);
+    a[(j >> 1) & 1] = add2(a[(j >> 1) & 1], make_float2(ex2(x.x), ex2(x.y)));
+  }
+  a[0] = add2(a[0], a[1]);
+  s = a[0].x + a[0].y;
   r = rn;
 }
 
@@ -352,7 +421,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int hn = t.N / 2;
           const uint32_t bytes = kStageA + (uint32_t)hn * 128;
           for (int s = 0; s < t.steps; ++s) {
-            if (!(ok = mbar_wait(&empty[stage], phase ^ 1, abort, p.err, 22))) break;
+            if (!(ok = wait(&empty[stage], phase ^ 1, abort, p.err, 22))) break;
             const uint32_t a = smem_u32(smem + stage * kStageBytes), b = a + kStageA;
             const uint32_t bar = mapa(smem_u32(&full[stage]), 0);
             if (cr == 0) mbar_expect_tx(&full[stage], 2 * bytes);
@@ -365,10 +434,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               const CUtensorMap* bm = t.mode == DX ? &maps.wm : xm;
               const int y = t.mode == DX ? p.pc0 + x : x;
               if (t.mode == DX) {
-                tma_load_pair(a, &maps.gk, x, t.rt * kTile + cr * 128, bar);
+                tma_load_pair(a, &maps.gk, 0, (t.s0 + s) * (int)p.npad + t.rt * kTile + cr * 128, bar);
               } else {
-                tma_load_pair(a, &maps.gm, t.ct * kTile + cr * 128, x, bar);
-                tma_load_pair(a + 8192, &maps.gm, t.ct * kTile + cr * 128 + 64, x, bar);
+                const int gy = (t.ct * 4 + cr * 2) * (int)p.npad + x;
+                tma_load_pair(a, &maps.gm, 0, gy, bar);
+                tma_load_pair(a + 8192, &maps.gm, 0, gy + (int)p.npad, bar);
               }
               for (int j = 0; j < hn; j += 64) tma_load_pair(b + j * 128, bm, t.kt * p.NK + cr * hn + j, y, bar);
             }
@@ -391,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         Tile t;
         for (int sub = 0; ok && get_tile(p, q, u, sub, t); ++sub, ++i) {
           const int a = i & 1;
-          if (!(ok = mbar_wait(&tempty[a], ((i >> 1) & 1) ^ 1, abort, p.err, 23))) break;
+          if (!(ok = wait(&tempty[a], ((i >> 1) & 1) ^ 1, abort, p.err, 23))) break;
           tc_fence_after();
           const uint32_t d = tmem + a * 256;
           const int amn = t.mode == DW, bmn = t.mode >= DX;
@@ -401,7 +471,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t as = amn ? 2048 : 32, bs = bmn ? 2048 : 32;
           const uint32_t al = amn ? 8192 : 16, bl = bmn ? 8192 : 16;  // next 64-wide MN-major block
           for (int s = 0; s < t.steps; ++s) {
-            if (!(ok = mbar_wait(&full[stage], phase, abort, p.err, 24))) break;
+            if (!(ok = wait(&full[stage], phase, abort, p.err, 24))) break;
             tc_fence_after();
             const uint32_t ab = smem_u32(smem + stage * kStageBytes), bb = ab + kStageA;
 #pragma unroll
@@ -418,76 +488,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp < 10) {
-    const int quarter = warp & 3, h = (warp - 2) >> 2;
+  } else if (warp < 2 + kEpiWarps) {
+    const int quarter = warp & 3, part = (warp - 2) >> 2;
     const int rit = cr * 128 + quarter * 32 + lane;  // row of the pair's tile
     uint8_t* stg = stg_all + (warp - 2) * kStg;
     const uint32_t tempty0 = mapa(smem_u32(tempty), 0);
     int i = 0, nbox = 0;
     bool ok = true;
-    while (ok) {
-      int u = 0;
-      if (lane == 0) u = feed.next(abort, p.err, q.units);
-      u = __shfl_sync(FULL, u, 0);
-      if (u < 0) break;
+    // one unit ahead: its rows' values are on their way while the current
+    // unit is worked on
+    int un = 0;
+    float4 rwn;
+    auto fetch = [&]() {
+      if (lane == 0) un = feed.next(abort, p.err, q.units);
+      un = __shfl_sync(FULL, un, 0);
+      rwn = make_float4(0.0f, 0.0f, 0.0f, __int_as_float(-1));
+      if (un < 0) return;
       Tile t;
-      float m = neg_inf(), sum = 0.0f, w = 0.0f;
-      float2 nm = make_float2(0.0f, 0.0f);
-      int lab = -1, srow = -1;
+      get_tile(p, q, un, 0, t);
+      const int row = t.rt * kTile + rit;
+      if (t.mode == GRAD && row < q.nl) rwn = p.row[row];
+    };
+    fetch();
+    while (ok && un >= 0) {
+      const int u = un;
+      const float4 rw = rwn;
+      fetch();
+      Tile t;
+      float m = neg_inf(), sum = 0.0f;
       for (int sub = 0; ok && get_tile(p, q, u, sub, t); ++sub, ++i) {
-        if (sub == 0 && t.mode <= GRAD) {
-          srow = t.rt * kTile + rit;
-          if (srow < q.nl) {
-            lab = p.lab[srow];
-            if (t.mode == GRAD) {
-              w = p.wrow[srow];
-              nm = p.norm[srow];
-            }
-          }
-        }
+        const int srow = t.rt * kTile + rit;
         const int a = i & 1;
         int got = 1;
-        if (lane == 0) got = mbar_wait(&tfull[a], (i >> 1) & 1, abort, p.err, 25);
+        if (lane == 0) got = wait(&tfull[a], (i >> 1) & 1, abort, p.err, 25);
         ok = __shfl_sync(FULL, got, 0) != 0;
         if (!ok) break;
         tc_fence_after();
-        const int hn = t.N / 2, cb = h * hn;
-        const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + a * 256 + cb;
-        if (t.mode == STATS) {
-          for (int c = 0; c < hn; c += 32) {
+        const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + a * 256;
+        auto chunks = [&](auto&& work) {
+          for (int c = part * 32; c < t.N; c += 32 * kParts) {
             float v[32];
             tmem_ld32(taddr + c, v);
             tmem_ld_wait();
-            const int c0 = t.ct * p.NT + cb + c;  // class of v[0]
-            if (__any_sync(FULL, (unsigned)(lab - c0) < 32u)) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (lab == c0 + j) p.zlab[srow] = v[j];
-            }
-            if (c0 < p.C) online(v, p.C - c0, m, sum);
+            work(v, c);
           }
+        };
+        if (t.mode == STATS) {
+          chunks([&](float (&v)[32], int c) {
+            const int c0 = t.ct * p.NT + c;  // class of v[0]
+            if (c0 < p.C) online(v, p.C - c0, m, sum);
+          });
         } else if (t.mode == GRAD) {
-          for (int c = 0; c < hn; c += 32) {
-            float v[32];
-            tmem_ld32(taddr + c, v);
-            tmem_ld_wait();
-            const int cl = t.ct * p.NT + cb + c;  // column of G
+          chunks([&](float (&v)[32], int c) {
+            const int cl = t.ct * p.NT + c;  // column of G
             const int c0 = p.gc0 + cl;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = ex2(__fmaf_rn(v[j], kLog2e, -nm.x)) * nm.y;
-            if (__any_sync(FULL, (unsigned)(lab - c0) < 32u)) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (lab == c0 + j) v[j] -= w;
+            for (int j = 0; j < 32; j += 2) {
+              const float2 x = fma2(make_float2(v[j], v[j + 1]), make_float2(kLog2e, kLog2e), make_float2(-rw.x, -rw.x));
+              const float2 g = mul2(make_float2(ex2(x.x), ex2(x.y)), make_float2(rw.y, rw.y));
+              v[j] = g.x;
+              v[j + 1] = g.y;
             }
-            if (c0 + 32 > p.C) {
+            // G is zero past the last class and the last row, whatever the
+            // products gave there
+            const int zeros = srow >= q.nl ? 0 : p.C - c0;
+            if (zeros < 32) {
+              keep_branch();
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (c0 + j >= p.C) v[j] = 0.0f;
+                if (j >= zeros) v[j] = 0.0f;
             }
             // row `lane` of a 32 x 32 box of 64-byte rows (64-byte swizzle:
             // 16-byte piece j at piece j ^ ((lane >> 1) & 3))
-            uint8_t* box = stg + (nbox & 1) * 2048;
+            uint8_t* box = stg + (nbox & 1) * kBox;
             if (lane == 0) bulk_wait_read<1>();  // the store of two boxes ago has read this buffer
             __syncwarp();
 #pragma unroll
@@ -495,18 +568,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               uint32_t o[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
-              if (srow >= q.nl) o[0] = o[1] = o[2] = o[3] = 0;
               *reinterpret_cast<uint4*>(box + lane * 64 + 16 * (j ^ ((lane >> 1) & 3))) =
                   make_uint4(o[0], o[1], o[2], o[3]);
             }
+            const unsigned yl = (unsigned)(__float_as_int(rw.w) - c0);
+            if (yl < 32u)  // the label's entry, made by xent_join_kernel
+              *reinterpret_cast<__nv_bfloat16*>(box + lane * 64 + 16 * ((yl >> 3) ^ ((lane >> 1) & 3)) +
+                                                2 * (yl & 7)) = __float2bfloat16_rn(rw.z);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_2d(&maps.gst, box, cl, t.rt * kTile + cr * 128 + quarter * 32);
+              tma_store_2d(&maps.gst, box, cl & 63,
+                           (cl >> 6) * (int)p.npad + t.rt * kTile + cr * 128 + quarter * 32);
               bulk_commit();
             }
             ++nbox;
-          }
+          });
         } else {
           const bool dw = t.mode == DW;
           // fp32 sums that other pieces or splits add to, else the result
@@ -523,46 +600,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           else if (r < q.nl) orow = q.nl < p.n ? p.idx[r] : r;
           __nv_bfloat16* out = dw ? p.dW : p.dX;
           const int64_t ldo = dw ? p.lddw : p.lddx;
-          for (int c = 0; c < hn; c += 64) {
-            float v[2][32];
+          for (int c = part * 32; c < t.N; c += 32 * kParts) {
+            float v[32];
             if (t.steps > 0) {
-              tmem_ld32(taddr + c, v[0]);
-              tmem_ld32(taddr + c + 32, v[1]);
+              tmem_ld32(taddr + c, v);
               tmem_ld_wait();
             } else {
 #pragma unroll
-              for (int j = 0; j < 64; ++j) v[j >> 5][j & 31] = 0.0f;
+              for (int j = 0; j < 32; ++j) v[j] = 0.0f;
             }
-            if (add) {
+            if (add) {  // sums so far are unscaled
 #pragma unroll
-              for (int j = 0; j < 64; ++j) v[j >> 5][j & 31] += acc[(int64_t)(cb + c + j) * kTile];
+              for (int j = 0; j < 32; ++j) v[j] += acc[(c + j) * kTile];
             }
             if (sums) {
 #pragma unroll
-              for (int j = 0; j < 64; ++j) acc[(int64_t)(cb + c + j) * kTile] = v[j >> 5][j & 31];
+              for (int j = 0; j < 32; ++j) acc[(c + j) * kTile] = v[j];
               continue;
             }
-            const int k0 = t.kt * p.NK + cb + c;
+            const int k0 = t.kt * p.NK + c;
             if (k0 >= p.k) continue;
-            // through shared memory, so that a store writes whole 128-byte
-            // pieces of four rows: piece j of row `lane` at j ^ (lane & 7)
+            // through shared memory (the layout of a GRAD box), so that a
+            // store writes whole 64-byte pieces of eight rows
             if (lane == 0) bulk_wait_read<0>();
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 4; ++j) {
               uint32_t o[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int x = 8 * j + 2 * e;
-                o[e] = pack_bf16x2(v[x >> 5][x & 31], v[x >> 5][(x & 31) + 1]);
-              }
-              *reinterpret_cast<uint4*>(stg + lane * 128 + 16 * (j ^ (lane & 7))) = make_uint4(o[0], o[1], o[2], o[3]);
+              for (int e = 0; e < 4; ++e)
+                o[e] = pack_bf16x2(v[8 * j + 2 * e] * p.scale, v[8 * j + 2 * e + 1] * p.scale);
+              *reinterpret_cast<uint4*>(stg + lane * 64 + 16 * (j ^ ((lane >> 1) & 3))) =
+                  make_uint4(o[0], o[1], o[2], o[3]);
             }
             __syncwarp();
 #pragma unroll
-            for (int it = 0; it < 8; ++it) {
-              const int rr = it * 4 + (lane >> 3), j = lane & 7;
-              const uint4 o = *reinterpret_cast<const uint4*>(stg + rr * 128 + 16 * (j ^ (rr & 7)));
+            for (int it = 0; it < 4; ++it) {
+              const int rr = it * 8 + (lane >> 2), j = lane & 3;
+              const uint4 o = *reinterpret_cast<const uint4*>(stg + rr * 64 + 16 * (j ^ ((rr >> 1) & 3)));
               const int64_t to = __shfl_sync(FULL, orow, rr);
               if (to < 0) continue;
               const int col = k0 + 8 * j;
@@ -570,8 +645,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (col + 8 <= p.k) {
                 *reinterpret_cast<uint4*>(dst) = o;
               } else {
-                const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(&o);
-                for (int x = 0; col + x < p.k; ++x) dst[x] = e[x];
+                const uint32_t e[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                  if (col + x < p.k) dst[x] = __ushort_as_bfloat16((unsigned short)(e[x >> 1] >> (16 * (x & 1))));
               }
             }
             __syncwarp();
@@ -581,14 +658,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) arrive_cluster(tempty0 + a * 8);
         if (t.mode == STATS && (sub + 1 == p.stats_run || t.ct + 1 == p.stats_tiles))
-          p.part[(int64_t)(t.ct / p.stats_run * 2 + h) * p.npad + srow] = make_float2(m, sum);
+          p.part[(int64_t)(t.ct / p.stats_run * kParts + part) * p.npad + srow] = make_float2(m, sum);
       }
     }
     if (lane == 0) bulk_wait<0>();  // every TMA store of this warp done
   } else if (lane == 0 && cr == 0) {
     int slot = 0;
     uint32_t phase = 0;
-    while (mbar_wait(&uempty[slot], phase ^ 1, abort, p.err, 26)) {
+    while (wait(&uempty[slot], phase ^ 1, abort, p.err, 26)) {
       const int64_t next = atomicAdd(p.counter, 1);
       const int u = next < q.units ? (int)next : 0x7fffffff;
 #pragma unroll
@@ -648,7 +725,7 @@ struct ScanOut {
 };
 
 __global__ void __launch_bounds__(kScanThreads)
-    xent_scan_kernel(const int* __restrict__ labels, const float* __restrict__ weight, float scale, int64_t n, int C,
+    xent_scan_kernel(const int* __restrict__ labels, const float* __restrict__ weight, int64_t n, int C,
                      int64_t seg, const int* __restrict__ cnt, const ScanOut o) {
   __shared__ int ws[32];
   __shared__ int base;
@@ -682,7 +759,7 @@ __global__ void __launch_bounds__(kScanThreads)
       if (on) {
         o.idx[to] = (int)r;
         o.lab[to] = y;
-        o.wrow[to] = (weight != nullptr ? weight[r] : 1.0f) * scale;
+        o.wrow[to] = weight != nullptr ? weight[r] : 1.0f;
       } else {
         if (o.loss != nullptr) o.loss[r] = 0.0f;
         if (o.lse != nullptr) o.lse[r] = 0.0f;
@@ -694,29 +771,58 @@ __global__ void __launch_bounds__(kScanThreads)
   if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) *o.nl = at;
 }
 
-// The labelled rows of X together (zeros up to a multiple of 256 rows) and
-// zeros in the other rows of dX; nothing when every row is labelled.
-__global__ void __launch_bounds__(256) xent_rows_kernel(const __nv_bfloat16* __restrict__ X, int64_t n, int k,
-                                                        int64_t ldx, const int* __restrict__ pos,
-                                                        const int* __restrict__ nl, __nv_bfloat16* Xc, int64_t ldc,
-                                                        __nv_bfloat16* dX, int64_t lddx) {
+// Per row of X, a warp: the label's logit x . w_y; the labelled rows copied
+// together (zeros up to a multiple of 256 rows) and zeros in the other rows
+// of dX, unless every row is labelled.  The label's logit costs one gathered
+// row of W here; picked out of the STATS tiles it cost 16% of their time.
+__global__ void __launch_bounds__(256)
+    xent_rows_kernel(const __nv_bfloat16* __restrict__ X, int64_t n, int k, int64_t ldx,
+                     const __nv_bfloat16* __restrict__ W, int64_t ldw, const int* __restrict__ labels,
+                     const int* __restrict__ pos, const int* __restrict__ nl, float* zlab, __nv_bfloat16* Xc,
+                     int64_t ldc, __nv_bfloat16* dX, int64_t lddx) {
   const int m = *nl;
-  if (m == n) return;
+  const bool all = m == n;
   const int lane = threadIdx.x & 31;
   const int64_t step = (int64_t)gridDim.x * 8;
   for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < n + kTile; r += step) {
-    const int64_t to = r < n ? pos[r] : (m + (r - n) < (m + kTile - 1) / kTile * (int64_t)kTile ? m + (r - n) : -1);
-    if (to < 0 && (r >= n || dX == nullptr)) continue;
-    const __nv_bfloat16* src = r < n && to >= 0 ? X + r * ldx : nullptr;
-    __nv_bfloat16* dst = to >= 0 ? Xc + to * ldc : dX + r * lddx;
+    if (r >= n || pos[r] < 0) {  // zeros
+      const int64_t pad = m + (r - n);
+      __nv_bfloat16* dst = nullptr;
+      if (r >= n) dst = !all && pad < (m + kTile - 1) / kTile * (int64_t)kTile ? Xc + pad * ldc : nullptr;
+      else if (dX != nullptr) dst = dX + r * lddx;
+      if (dst == nullptr) continue;
+      for (int c = lane * 8; c < k; c += 256) {
+        if (c + 8 <= k) *reinterpret_cast<uint4*>(dst + c) = make_uint4(0, 0, 0, 0);
+        else
+          for (int j = c; j < k; ++j) dst[j] = __float2bfloat16_rn(0.0f);
+      }
+      continue;
+    }
+    const int to = pos[r];
+    const __nv_bfloat16* x = X + r * ldx;
+    const __nv_bfloat16* w = W + (int64_t)labels[r] * ldw;
+    __nv_bfloat16* dst = all ? nullptr : Xc + (int64_t)to * ldc;
+    float z = 0.0f;
     for (int c = lane * 8; c < k; c += 256) {
       if (c + 8 <= k) {
-        *reinterpret_cast<uint4*>(dst + c) =
-            src != nullptr ? __ldg(reinterpret_cast<const uint4*>(src + c)) : make_uint4(0, 0, 0, 0);
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + c)), b = __ldg(reinterpret_cast<const uint4*>(w + c));
+        const uint32_t au[4] = {a.x, a.y, a.z, a.w}, bu[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // bf16 is the upper half of an fp32
+          z = __fmaf_rn(__uint_as_float(au[j] << 16), __uint_as_float(bu[j] << 16), z);
+          z = __fmaf_rn(__uint_as_float(au[j] & 0xffff0000u), __uint_as_float(bu[j] & 0xffff0000u), z);
+        }
+        if (dst != nullptr) *reinterpret_cast<uint4*>(dst + c) = a;
       } else {
-        for (int j = c; j < k; ++j) dst[j] = src != nullptr ? src[j] : __float2bfloat16_rn(0.0f);
+        for (int j = c; j < k; ++j) {
+          z = __fmaf_rn(__bfloat162float(x[j]), __bfloat162float(w[j]), z);
+          if (dst != nullptr) dst[j] = x[j];
+        }
       }
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(FULL, z, o);
+    if (lane == 0) zlab[to] = z;
   }
 }
 
@@ -726,7 +832,7 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const __nv_bfloat16* __r
 __global__ void __launch_bounds__(1024)
     xent_join_kernel(const float2* __restrict__ part, int runs, int64_t npad, const int* __restrict__ nl,
                      const int* __restrict__ idx, const float* __restrict__ zlab, const float* __restrict__ wrow,
-                     float2* norm, float* loss, float* lse) {
+                     const int* __restrict__ lab, float4* rowinfo, float* loss, float* lse) {
   __shared__ float sm[32][33], ss[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int rows = *nl;
@@ -748,9 +854,13 @@ __global__ void __launch_bounds__(1024)
       s = 0.0f;
       for (int j = 0; j < 32; ++j) s += ss[j][lane] * ex2(sm[j][lane] - ref);
       const float l2 = log2f(s);
-      if (norm != nullptr) norm[row] = make_float2(ref, wrow[row] / s);
+      const float zl = __fmaf_rn(zlab[row], kLog2e, -ref);
+      if (rowinfo != nullptr) {
+        const float wr = wrow[row], ws = wr / s;
+        rowinfo[row] = make_float4(ref, ws, __fmaf_rn(ex2(zl), ws, -wr), __int_as_float(lab[row]));
+      }
       const int to = idx[row];
-      if (loss != nullptr) loss[to] = kLn2 * (l2 - __fmaf_rn(zlab[row], kLog2e, -ref));
+      if (loss != nullptr) loss[to] = kLn2 * (l2 - zl);
       if (lse != nullptr) lse[to] = __fmaf_rn(ref, kLn2, l2 * kLn2);
     }
     __syncthreads();
@@ -762,7 +872,7 @@ __global__ void __launch_bounds__(1024)
 __global__ void __launch_bounds__(256)
     xent_sum_kernel(const float* __restrict__ acc, int splits, int64_t split_stride, int64_t tile_stride,
                     const int* __restrict__ nl, int64_t n, const int* __restrict__ idx, int row0, int C, int k,
-                    __nv_bfloat16* out, int64_t ldo) {
+                    float scale, __nv_bfloat16* out, int64_t ldo) {
   const int c0 = blockIdx.y * 8;
   if (c0 >= k) return;
   const int64_t r = (int64_t)blockIdx.x * kTile + threadIdx.x;
@@ -779,6 +889,8 @@ __global__ void __launch_bounds__(256)
   for (int s = 0; s < splits; ++s)
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += a[s * split_stride + j * kTile];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] *= scale;
   __nv_bfloat16* dst = out + to * ldo + c0;
   if (c0 + 8 <= k) {
     *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
@@ -822,7 +934,7 @@ int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Bytes of one buffer of G.
-constexpr int64_t kPieceBytes = (int64_t)128 << 20;
+constexpr int64_t kPieceBytes = (int64_t)1024 << 20;
 
 struct Sizes {
   int64_t npad, nrt;
@@ -831,7 +943,7 @@ struct Sizes {
   int NK, nkt;
   int run, units;             // STATS
   int per_piece, pieces;      // class tiles of a piece; pieces
-  int64_t Cp;                 // classes of a piece = pitch of G
+  int64_t Cp;                 // classes of a piece
   int dxs, dws;
   int scan_blocks;
   int64_t seg;
@@ -877,7 +989,7 @@ struct Ws {
   int n_counters;
   int *cnt, *pos, *idx, *lab;
   float *wrow, *zlab;
-  float2* norm;
+  float4* row;
   float2* part;
   void* Xc;
   void* G[2];
@@ -894,9 +1006,9 @@ Carve carve(void* ws, size_t bytes, const Sizes& z, int64_t n, int k, bool grad,
   w.idx = static_cast<int*>(c.take((size_t)z.npad * 4));
   w.lab = static_cast<int*>(c.take((size_t)z.npad * 4));
   w.wrow = static_cast<float*>(c.take((size_t)z.npad * 4));
-  w.norm = static_cast<float2*>(c.take((size_t)z.npad * 8));
+  w.row = static_cast<float4*>(c.take((size_t)z.npad * 16));
   w.zlab = static_cast<float*>(c.take((size_t)z.npad * 4));
-  w.part = static_cast<float2*>(c.take((size_t)z.units * 2 * z.npad * sizeof(float2)));
+  w.part = static_cast<float2*>(c.take((size_t)z.units * kParts * z.npad * sizeof(float2)));
   w.Xc = c.take((size_t)z.npad * round8(k) * 2);
   if (!grad) return c;
   w.G[0] = c.take((size_t)z.npad * z.Cp * 2);
@@ -909,7 +1021,7 @@ Carve carve(void* ws, size_t bytes, const Sizes& z, int64_t n, int k, bool grad,
 
 int check_shape(int64_t n, int k, int C) {
   if (n < 0 || k < 1 || C < 1) return GQ_ERR_INVALID_ARG;
-  if (n > INT32_MAX - 1024 || C > (1 << 30) || k > 16384) return GQ_ERR_UNSUPPORTED;
+  if (n > (1 << 28) || C > (1 << 30) || k > 16384) return GQ_ERR_UNSUPPORTED;
   // units of one launch are numbered in 31 bits
   if (cdiv(n, kTile) * cdiv(C, 64) > INT32_MAX / 4) return GQ_ERR_UNSUPPORTED;
   return GQ_OK;
@@ -959,13 +1071,13 @@ extern "C" int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, 
     GQ_TRY(launch_status());
   }
   const ScanOut so{w.nl, w.pos, w.idx, w.lab, w.wrow, loss, lse, w.counters, w.n_counters};
-  xent_scan_kernel<<<z.scan_blocks, kScanThreads, 0, s>>>(labels, weight, scale, n, C, z.seg, w.cnt, so);
+  xent_scan_kernel<<<z.scan_blocks, kScanThreads, 0, s>>>(labels, weight, n, C, z.seg, w.cnt, so);
   GQ_TRY(launch_status());
   const int64_t ldc = round8(k);
   const int64_t rb = cdiv(n + kTile, 8), rcap = (int64_t)sm_count() * 8;
   xent_rows_kernel<<<(int)(rb < rcap ? rb : rcap), 256, 0, s>>>(
-      reinterpret_cast<const __nv_bfloat16*>(X), n, k, ldx, w.pos, w.nl, static_cast<__nv_bfloat16*>(w.Xc), ldc,
-      reinterpret_cast<__nv_bfloat16*>(dX), lddx);
+      reinterpret_cast<const __nv_bfloat16*>(X), n, k, ldx, reinterpret_cast<const __nv_bfloat16*>(W), ldw, labels, w.pos,
+      w.nl, w.zlab, static_cast<__nv_bfloat16*>(w.Xc), ldc, reinterpret_cast<__nv_bfloat16*>(dX), lddx);
   GQ_TRY(launch_status());
 
   Maps m;
@@ -983,10 +1095,7 @@ extern "C" int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, 
   a.NT = z.NT;
   a.NK = z.NK;
   a.nkt = z.nkt;
-  a.lab = w.lab;
-  a.wrow = w.wrow;
-  a.norm = w.norm;
-  a.zlab = w.zlab;
+  a.row = w.row;
   a.idx = w.idx;
   a.part = w.part;
   a.err = dev_err;
@@ -995,8 +1104,8 @@ extern "C" int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, 
   a.stats_units = z.units;
   GQ_TRY(launch_tiles(m, a, z, s));
   const int64_t jb = cdiv(n, 32), jcap = (int64_t)sm_count() * 2;
-  xent_join_kernel<<<(int)(jb < jcap ? jb : jcap), 1024, 0, s>>>(w.part, 2 * z.units, z.npad, w.nl, w.idx, w.zlab,
-                                                                 w.wrow, grad ? w.norm : nullptr, loss, lse);
+  xent_join_kernel<<<(int)(jb < jcap ? jb : jcap), 1024, 0, s>>>(w.part, kParts * z.units, z.npad, w.nl, w.idx, w.zlab,
+                                                                 w.wrow, w.lab, grad ? w.row : nullptr, loss, lse);
   GQ_TRY(launch_status());
   if (!grad) return GQ_OK;
 
@@ -1004,6 +1113,7 @@ extern "C" int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, 
   GQ_TRY(tmap(&m.xm[1], w.Xc, k, z.npad, ldc, 64, 64));
   GQ_TRY(tmap(&m.wm, W, k, C, ldw, 64, 64));
   a.stats_units = 0;
+  a.scale = scale;
   a.dxs = z.dxs;
   a.dws = z.dws;
   a.accX = w.accX;
@@ -1013,17 +1123,18 @@ extern "C" int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, 
   a.dW = reinterpret_cast<__nv_bfloat16*>(dW);
   a.lddw = lddw;
   const int64_t tile = (int64_t)z.nkt * z.NK * kTile;
+  const int64_t gy = z.Cp / 64 * z.npad;  // 64-class blocks of G, one after the other
   for (int i = 0; i <= z.pieces; ++i) {  // GRAD of piece i beside DX and DW of piece i - 1
     const int done = i - 1;
     a.gc0 = i * (int)z.Cp;
     a.gtiles = i < z.pieces ? (z.ctiles - i * z.per_piece < z.per_piece ? z.ctiles - i * z.per_piece : z.per_piece) : 0;
-    if (i < z.pieces) GQ_TRY(tmap(&m.gst, w.G[i & 1], z.Cp, z.npad, z.Cp, 32, 32));
+    if (i < z.pieces) GQ_TRY(tmap(&m.gst, w.G[i & 1], 64, gy, 64, 32, 32));
     int ptiles = 0;
     if (i > 0) {
       const int classes = (done + 1 < z.pieces ? z.per_piece : z.ctiles - done * z.per_piece) * z.NT;
       ptiles = (int)cdiv(classes, kTile);
-      GQ_TRY(tmap(&m.gk, w.G[done & 1], z.Cp, z.npad, z.Cp, 64, 128));
-      GQ_TRY(tmap(&m.gm, w.G[done & 1], z.Cp, z.npad, z.Cp, 64, 64));
+      GQ_TRY(tmap(&m.gk, w.G[done & 1], 64, gy, 64, 64, 128));
+      GQ_TRY(tmap(&m.gm, w.G[done & 1], 64, gy, 64, 64, 64));
       a.pc0 = done * (int)z.Cp;
       a.psteps = classes / 64;
       a.ptiles = ptiles;
@@ -1036,13 +1147,13 @@ extern "C" int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, 
     GQ_TRY(launch_tiles(m, a, z, s));
     if (i > 0 && dW != nullptr && z.dws > 1) {
       xent_sum_kernel<<<dim3(ptiles, (unsigned)cdiv(k, 8)), 256, 0, s>>>(
-          w.accW, z.dws, ptiles * tile, tile, w.nl, n, nullptr, a.pc0, C, k, a.dW, lddw);
+          w.accW, z.dws, ptiles * tile, tile, w.nl, n, nullptr, a.pc0, C, k, scale, a.dW, lddw);
       GQ_TRY(launch_status());
     }
   }
   if (dX != nullptr && z.dxs > 1) {
     xent_sum_kernel<<<dim3((unsigned)z.nrt, (unsigned)cdiv(k, 8)), 256, 0, s>>>(
-        w.accX, z.dxs, z.nrt * tile, tile, w.nl, n, w.idx, 0, C, k, a.dX, lddx);
+        w.accX, z.dxs, z.nrt * tile, tile, w.nl, n, w.idx, 0, C, k, scale, a.dX, lddx);
     GQ_TRY(launch_status());
   }
   return GQ_OK;
