@@ -22,7 +22,7 @@
 // Tiles are 256 x up to 256 x 64 for a pair of CTAs (cta_group::2): each CTA
 // loads 128 rows of A and half of B's columns, so each operand byte is read
 // from L2 once per pair.  Per CTA:
-//   warp 0      TMA loads into a ring of six 32 KB stages; both CTAs' bytes
+//   warp 0      TMA loads into a ring of five 32 KB stages; both CTAs' bytes
 //               arrive on the even CTA's barrier
 //   warp 1      (even CTA) one thread issues tcgen05.mma into one of two
 //               TMEM accumulators of 256 columns; its commits release the
@@ -61,10 +61,10 @@ namespace {
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarps + 3);  // TMA, MMA, epilogue, scheduler
 constexpr int kParts = kEpiWarps / 4;           // warps that share a row's columns
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kStageA = 128 * 128;                    // 128 rows x 64 bf16 (or 2 x 64 x 64)
 constexpr int kStageBytes = 2 * kStageA;
-constexpr int kBox = 2048;       // 32 rows x 32 bf16
+constexpr int kBox = 4096;       // 32 rows x 64 bf16
 constexpr int kStg = 2 * kBox;   // epilogue staging per warp
 constexpr int kSlots = 4;        // units of work posted ahead
 constexpr int kConsumers = 3 + 2 * kEpiWarps;  // even CTA: TMA, MMA, epilogue; odd CTA: TMA, epilogue
@@ -361,6 +361,11 @@ __device__ __forceinline__ void online(float (&v)[32], int limit, float& r, floa
   r = rn;
 }
 
+// entry j of a lane's 128-byte row of a G box
+__device__ __forceinline__ void put_box(uint8_t* row, int lane, unsigned j, __nv_bfloat16 v) {
+  *reinterpret_cast<__nv_bfloat16*>(row + 16 * ((j >> 3) ^ (lane & 7)) + 2 * (j & 7)) = v;
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     xent_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args p) {
   extern __shared__ uint8_t smem_raw[];
@@ -525,65 +530,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + a * 256;
-        auto chunks = [&](auto&& work) {
+        if (t.mode == STATS) {
           for (int c = part * 32; c < t.N; c += 32 * kParts) {
             float v[32];
             tmem_ld32(taddr + c, v);
             tmem_ld_wait();
-            work(v, c);
-          }
-        };
-        if (t.mode == STATS) {
-          chunks([&](float (&v)[32], int c) {
             const int c0 = t.ct * p.NT + c;  // class of v[0]
             if (c0 < p.C) online(v, p.C - c0, m, sum);
-          });
+          }
         } else if (t.mode == GRAD) {
-          chunks([&](float (&v)[32], int c) {
-            const int cl = t.ct * p.NT + c;  // column of G
-            const int c0 = p.gc0 + cl;
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float2 x = fma2(make_float2(v[j], v[j + 1]), make_float2(kLog2e, kLog2e), make_float2(-rw.x, -rw.x));
-              const float2 g = mul2(make_float2(ex2(x.x), ex2(x.y)), make_float2(rw.y, rw.y));
-              v[j] = g.x;
-              v[j + 1] = g.y;
-            }
-            // G is zero past the last class and the last row, whatever the
-            // products gave there
-            const int zeros = srow >= q.nl ? 0 : p.C - c0;
-            if (zeros < 32) {
-              keep_branch();
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (j >= zeros) v[j] = 0.0f;
-            }
-            // row `lane` of a 32 x 32 box of 64-byte rows (64-byte swizzle:
-            // 16-byte piece j at piece j ^ ((lane >> 1) & 3))
+          for (int b = part * 64; b < t.N; b += 64 * kParts) {
+            // a box of 32 rows x 64 classes, 128 bytes a row (128-byte
+            // swizzle: 16-byte piece j of row `lane` at j ^ (lane & 7))
             uint8_t* box = stg + (nbox & 1) * kBox;
-            if (lane == 0) bulk_wait_read<1>();  // the store of two boxes ago has read this buffer
-            __syncwarp();
+            uint8_t* mine = box + lane * 128;
+            const int cl = t.ct * p.NT + b;  // column of G
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              float v[32];
+              tmem_ld32(taddr + b + 32 * h, v);
+              tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t o[4];
+              for (int j = 0; j < 32; j += 2) {
+                const float2 x =
+                    fma2(make_float2(v[j], v[j + 1]), make_float2(kLog2e, kLog2e), make_float2(-rw.x, -rw.x));
+                const float2 g = mul2(make_float2(ex2(x.x), ex2(x.y)), make_float2(rw.y, rw.y));
+                v[j] = g.x;
+                v[j + 1] = g.y;
+              }
+              if (h == 0) {
+                if (lane == 0) bulk_wait_read<1>();  // the store of two boxes ago has read this buffer
+                __syncwarp();
+              }
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
-              *reinterpret_cast<uint4*>(box + lane * 64 + 16 * (j ^ ((lane >> 1) & 3))) =
-                  make_uint4(o[0], o[1], o[2], o[3]);
+              for (int j = 0; j < 4; ++j) {
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
+                *reinterpret_cast<uint4*>(mine + 16 * ((4 * h + j) ^ (lane & 7))) = make_uint4(o[0], o[1], o[2], o[3]);
+              }
             }
+            // entries that are not the product's: the label's (made by
+            // xent_join_kernel), and zeros past the last class and row,
+            // whatever the products gave there
+            const int c0 = p.gc0 + cl;
             const unsigned yl = (unsigned)(__float_as_int(rw.w) - c0);
-            if (yl < 32u)  // the label's entry, made by xent_join_kernel
-              *reinterpret_cast<__nv_bfloat16*>(box + lane * 64 + 16 * ((yl >> 3) ^ ((lane >> 1) & 3)) +
-                                                2 * (yl & 7)) = __float2bfloat16_rn(rw.z);
+            if (yl < 64u) put_box(mine, lane, yl, __float2bfloat16_rn(rw.z));
+            const int zeros = srow < q.nl ? p.C - c0 : 0;
+#pragma unroll 1
+            for (int j = max(zeros, 0); j < 64; ++j) put_box(mine, lane, j, __float2bfloat16_rn(0.0f));
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_2d(&maps.gst, box, cl & 63,
-                           (cl >> 6) * (int)p.npad + t.rt * kTile + cr * 128 + quarter * 32);
+              tma_store_2d(&maps.gst, box, 0, (cl >> 6) * (int)p.npad + t.rt * kTile + cr * 128 + quarter * 32);
               bulk_commit();
             }
             ++nbox;
-          });
+          }
         } else {
           const bool dw = t.mode == DW;
           // fp32 sums that other pieces or splits add to, else the result
@@ -620,8 +623,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             const int k0 = t.kt * p.NK + c;
             if (k0 >= p.k) continue;
-            // through shared memory (the layout of a GRAD box), so that a
-            // store writes whole 64-byte pieces of eight rows
+            // through shared memory (64-byte rows, 16-byte piece j at
+            // j ^ ((lane >> 1) & 3)), so that a store writes whole 64-byte
+            // pieces of eight rows
             if (lane == 0) bulk_wait_read<0>();
             __syncwarp();
 #pragma unroll
@@ -915,18 +919,18 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// bf16 [outer][inner] of row pitch ld: boxes of bi x bo, zeros out of bounds
-int tmap(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld, int bi, int bo) {
+// bf16 [outer][inner] of row pitch ld: boxes of 64 x bo (128-byte rows), zeros
+// out of bounds
+int tmap(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld, int bo) {
   auto fn = encode_fn();
   if (fn == nullptr) return GQ_ERR_CUDA;
   const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
   const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {(cuuint32_t)bi, (cuuint32_t)bo};
+  const cuuint32_t box[2] = {64, (cuuint32_t)bo};
   const cuuint32_t estr[2] = {1, 1};
   const CUresult r =
       fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, bi == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? GQ_OK : GQ_ERR_INVALID_ARG;
 }
 
@@ -1082,9 +1086,9 @@ extern "C" int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, 
 
   Maps m;
   memset(&m, 0, sizeof(m));
-  GQ_TRY(tmap(&m.xk[0], X, k, n, ldx, 64, 128));
-  GQ_TRY(tmap(&m.xk[1], w.Xc, k, z.npad, ldc, 64, 128));
-  GQ_TRY(tmap(&m.wk, W, k, C, ldw, 64, z.NT / 2));
+  GQ_TRY(tmap(&m.xk[0], X, k, n, ldx, 128));
+  GQ_TRY(tmap(&m.xk[1], w.Xc, k, z.npad, ldc, 128));
+  GQ_TRY(tmap(&m.wk, W, k, C, ldw, z.NT / 2));
   Args a{};
   a.nl = w.nl;
   a.counter = w.counters;
@@ -1109,9 +1113,9 @@ extern "C" int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, 
   GQ_TRY(launch_status());
   if (!grad) return GQ_OK;
 
-  GQ_TRY(tmap(&m.xm[0], X, k, n, ldx, 64, 64));
-  GQ_TRY(tmap(&m.xm[1], w.Xc, k, z.npad, ldc, 64, 64));
-  GQ_TRY(tmap(&m.wm, W, k, C, ldw, 64, 64));
+  GQ_TRY(tmap(&m.xm[0], X, k, n, ldx, 64));
+  GQ_TRY(tmap(&m.xm[1], w.Xc, k, z.npad, ldc, 64));
+  GQ_TRY(tmap(&m.wm, W, k, C, ldw, 64));
   a.stats_units = 0;
   a.scale = scale;
   a.dxs = z.dxs;
@@ -1128,13 +1132,13 @@ extern "C" int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, 
     const int done = i - 1;
     a.gc0 = i * (int)z.Cp;
     a.gtiles = i < z.pieces ? (z.ctiles - i * z.per_piece < z.per_piece ? z.ctiles - i * z.per_piece : z.per_piece) : 0;
-    if (i < z.pieces) GQ_TRY(tmap(&m.gst, w.G[i & 1], 64, gy, 64, 32, 32));
+    if (i < z.pieces) GQ_TRY(tmap(&m.gst, w.G[i & 1], 64, gy, 64, 32));
     int ptiles = 0;
     if (i > 0) {
       const int classes = (done + 1 < z.pieces ? z.per_piece : z.ctiles - done * z.per_piece) * z.NT;
       ptiles = (int)cdiv(classes, kTile);
-      GQ_TRY(tmap(&m.gk, w.G[done & 1], 64, gy, 64, 64, 128));
-      GQ_TRY(tmap(&m.gm, w.G[done & 1], 64, gy, 64, 64, 64));
+      GQ_TRY(tmap(&m.gk, w.G[done & 1], 64, gy, 64, 128));
+      GQ_TRY(tmap(&m.gm, w.G[done & 1], 64, gy, 64, 64));
       a.pc0 = done * (int)z.Cp;
       a.psteps = classes / 64;
       a.ptiles = ptiles;
