@@ -469,6 +469,17 @@ def _like(t, ref, name, dtypes=None):
     return t
 
 
+def _rows_like(X):
+    """A new matrix of X's shape and type; where X's rows start 16-byte
+    aligned, so do the new one's (a view of a wider buffer if need be), and
+    calls on the two take the vector path."""
+    e = X.element_size()
+    n, d = X.shape
+    if d * e % 16 == 0 or X.stride(0) * e % 16 or X.data_ptr() % 16:
+        return torch.empty(n, d, dtype=X.dtype, device=X.device)
+    return torch.empty(n, (d * e + 15) // 16 * 16 // e, dtype=X.dtype, device=X.device)[:, :d]
+
+
 def _vec32(t, count, ref, name):
     """t (or None) is a contiguous fp32 vector of `count` values on ref's device."""
     if t is not None and (t.dtype != torch.float32 or t.shape != (count,) or t.device != ref.device
@@ -493,9 +504,7 @@ def dropout(X: torch.Tensor, p: float, seed: int, out: torch.Tensor | None = Non
     the gradient.  out may be X."""
     ty = _typed(X, "X")
     ldx = _rows(X)
-    if out is None:
-        out = torch.empty(X.shape, dtype=X.dtype, device=X.device)
-    _like(out, X, "out")
+    out = _rows_like(X) if out is None else _like(out, X, "out")
     n, d = X.shape
     with torch.cuda.device(X.device):
         _check(lib().gq_dropout(_ptr(X), ty, n, d, ldx, p, seed & 0xFFFFFFFFFFFFFFFF, _ptr(out), _rows(out),
@@ -513,7 +522,7 @@ def layer_norm_fwd(X: torch.Tensor, gamma: torch.Tensor | None = None, beta: tor
     ty = _typed(X, "X")
     ldx = _rows(X)
     n, d = X.shape
-    out = torch.empty(X.shape, dtype=X.dtype, device=X.device) if out is None else _like(out, X, "out")
+    out = _rows_like(X) if out is None else _like(out, X, "out")
     if mean is None:
         mean = torch.empty(n, dtype=torch.float32, device=X.device)
     if rstd is None:
@@ -541,7 +550,7 @@ def layer_norm_bwd(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rstd: 
     ldx = _rows(X)
     _like(dY, X, "dY")
     if dX is None:
-        dX = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+        dX = _rows_like(X)
     _like(dX, X, "dX", (torch.float32, torch.bfloat16) if X.dtype == torch.float32 else None)
     if dgamma is None:
         dgamma = torch.empty(d, dtype=torch.float32, device=X.device)

@@ -30,9 +30,11 @@
 
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include "gq_common.cuh"
 #include "gq_internal.cuh"
+#include "gq_sm100.cuh"
 #include "gq_train.h"
 
 namespace gq {
@@ -42,6 +44,14 @@ constexpr int kEpt = 16;           // elements of a row per lane or thread
 constexpr int kWarpRowMax = 512;   // rows up to here are one warp's (or less)
 constexpr int kMaxWidth = 16384;   // 1024 threads x 16 elements
 constexpr int kNormThreads = 256;
+
+// 1 / sqrt(v): the hardware estimate and one Newton step (2 ulp), a fifth of
+// the instructions of a rounded root and quotient.
+__device__ __forceinline__ float inv_sqrt(float v) {
+  const float y = rsqrtf(v);
+  const float e = __fmaf_rn(-v * y, y, 1.0f);
+  return v > 0.0f && e == e ? __fmaf_rn(0.5f * e, y, y) : y;  // y itself at 0 and infinity
+}
 
 // ---------------------------------------------------------- vector access --
 __device__ __forceinline__ float to_f(float v) { return v; }
@@ -69,6 +79,73 @@ __device__ __forceinline__ void load_vec(const T* p, int col, int d, float (&o)[
   }
 }
 
+// The same elements as they are stored, to be converted later: a row on its
+// way while another one is worked on.  A vector stays the four words of its
+// load: taking 16-bit elements apart would wait for them.
+template <typename T, int V>
+struct Raw {
+  uint32_t w[V * sizeof(T) == 16 ? 4 : V];
+};
+template <typename T, int V>
+__device__ __forceinline__ void load_raw(const T* p, int col, int d, Raw<T, V>& o) {
+  if constexpr (V * sizeof(T) == 16) {
+    if (col + V <= d) {
+      const uint4 q = *reinterpret_cast<const uint4*>(p + col);
+      o.w[0] = q.x, o.w[1] = q.y, o.w[2] = q.z, o.w[3] = q.w;
+      return;
+    }
+  }
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) o.w[j] = col + j < d ? reinterpret_cast<const uint32_t*>(p)[col + j] : 0u;
+  } else if constexpr (V == 1) {
+    o.w[0] = col < d ? reinterpret_cast<const uint16_t*>(p)[col] : 0u;
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+      const uint32_t lo = col + j < d ? reinterpret_cast<const uint16_t*>(p)[col + j] : 0u;
+      const uint32_t hi = col + j + 1 < d ? reinterpret_cast<const uint16_t*>(p)[col + j + 1] : 0u;
+      o.w[j / 2] = lo | hi << 16;
+    }
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Raw<T, V>& r, float* o) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    if constexpr (sizeof(T) == 4) {
+      o[j] = __uint_as_float(r.w[j]);
+    } else {
+      const uint16_t u = (uint16_t)(V == 1 ? r.w[0] : r.w[j / 2] >> (16 * (j & 1)));
+      T t;
+      memcpy(&t, &u, 2);
+      o[j] = to_f(t);
+    }
+  }
+}
+
+// Asynchronous 16-byte copies into a thread's own slots of shared memory,
+// zeros past the end of the row: rows on their way that need no registers,
+// and no barrier, since each thread reads what it copied itself.
+template <typename T, int V>
+__device__ __forceinline__ void copy_vec(uint4* slot, const T* p, int col, int d) {
+  const int bytes = min(max(d - col, 0) * (int)sizeof(T), 16);
+  const T* src = bytes > 0 ? p + col : p;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(slot)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <typename T, int V>
+__device__ __forceinline__ void read_slot(const uint4* slot, float* o) {
+  const uint4 q = *slot;
+  Raw<T, V> r;
+  r.w[0] = q.x, r.w[1] = q.y, r.w[2] = q.z, r.w[3] = q.w;
+  unpack<T, V>(r, o);
+}
+
 // stores V elements; VEC: p is aligned for one store of the whole vector
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T* p, int col, int d, const float (&o)[V], bool vec) {
@@ -86,21 +163,65 @@ __device__ __forceinline__ void store_vec(T* p, int col, int d, const float (&o)
   }
 }
 
+// V consecutive floats of shared memory (16-byte aligned for V >= 4)
+template <int V>
+__device__ __forceinline__ void load_shared(const float* p, float* o) {
+  if (V >= 4) {
+#pragma unroll
+    for (int j = 0; j < V; j += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(p + j);
+      o[j] = q.x;
+      o[j + 1] = q.y;
+      o[j + 2] = q.z;
+      o[j + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[j] = p[j];
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_shared(float* p, const float* o) {
+  if (V >= 4) {
+#pragma unroll
+    for (int j = 0; j < V; j += 4) *reinterpret_cast<float4*>(p + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) p[j] = o[j];
+  }
+}
+
 template <int V>
 __device__ __forceinline__ void load_param(const float* p, int col, int d, float none, float (&o)[V]) {
 #pragma unroll
   for (int j = 0; j < V; ++j) o[j] = p == nullptr ? none : (col + j < d ? __ldg(p + col + j) : 0.0f);
 }
 
-// Dropout: an element is kept when its 23-bit noise code is >= `drop`.
+// Dropout: an element is kept when its 23-bit noise code, the upper bits of
+// the hash, is at least T = ceil(p 2^23), that is when the whole hash exceeds
+// lim = 512 T - 1 (p = 1: T = 2^23 and nothing exceeds lim).
 struct Drop {
-  uint32_t drop;  // ceil(p 2^23); 0: nothing is dropped and the hash is skipped
+  uint32_t on;    // 0: p = 0, nothing is dropped and the hash is skipped
+  uint32_t lim;
   float scale;    // 1 / (1 - p)
   uint32_t key;   // fmix32(low32(seed) ^ high32(seed))
 };
 
-__device__ __forceinline__ bool kept(uint32_t krow, int col, uint32_t drop) {
-  return (fmix32(krow + (uint32_t)col * 0x9E3779B9u) >> 9) >= drop;
+constexpr uint32_t kColMul = 0x9E3779B9u;
+
+// hash of column col0 + j of the row whose key is krow; base = krow + col0 kColMul
+__device__ __forceinline__ bool kept(uint32_t base, int j, uint32_t lim) {
+  return fmix32(base + (uint32_t)j * kColMul) > lim;
+}
+
+// s / d to the nearest: the product with 1 / d, corrected by its remainder
+// (exact where the quotient is, as for the sum of a constant row).
+struct Div {
+  float d, inv;
+};
+__device__ __forceinline__ float over(float s, const Div& v) {
+  const float q = s * v.inv;
+  return __fmaf_rn(__fmaf_rn(-q, v.d, s), v.inv, q);
 }
 
 // ---------------------------------------------------------------- dropout --
@@ -126,9 +247,11 @@ __global__ void __launch_bounds__(kNormThreads)
     for (int u = 0; u < kDropRows; ++u) {
       const int64_t r = r0 + (int64_t)u * rpb;
       if (r >= n) break;
-      const uint32_t kr = row_key(dr.key, (uint32_t)r);
+      if (dr.on) {
+        const uint32_t base = row_key(dr.key, (uint32_t)r) + (uint32_t)col * kColMul;
 #pragma unroll
-      for (int j = 0; j < V; ++j) v[u][j] = kept(kr, col + j, dr.drop) ? v[u][j] * dr.scale : 0.0f;
+        for (int j = 0; j < V; ++j) v[u][j] = kept(base, j, dr.lim) ? v[u][j] * dr.scale : 0.0f;
+      }
       store_vec<T, V>(Y + r * ldy, col, d, v[u], true);
     }
   }
@@ -160,18 +283,39 @@ __device__ __forceinline__ float2 block_sum2(float a, float b, float* red) {
 }
 
 // OR of the lanes' V bits into 32-column words: word of the lane's columns,
-// complete in every lane of the 32 / V lanes that share it (V = 1: the G
-// lanes of the group).
-template <int V, int G>
+// complete in every lane of the 32 / V lanes that share it.
+template <int V>
 __device__ __forceinline__ uint32_t gather_bits(uint32_t bits, int col) {
-  if (V == 1) {
-    const uint32_t all = __ballot_sync(FULL, bits);
-    return G == 32 ? all : (all >> (threadIdx.x & 31 & ~(G - 1))) & ((1u << (G & 31)) - 1);
-  }
+  if (V == 1) return __ballot_sync(FULL, bits);
   uint32_t w = bits << (col & 31);
 #pragma unroll
   for (int o = 1; o < 32 / V; o <<= 1) w |= __shfl_xor_sync(FULL, w, o);
   return w;
+}
+
+// Centres V values of a row (those past its end become 0) and adds their
+// squares to q; `whole`: all V columns are in the row.
+template <int V>
+__device__ __forceinline__ float centre(float* v, float mean, bool whole, int col, int d, float q) {
+  if constexpr (V > 1) {
+    if (whole) {
+      const float2 nm = make_float2(-mean, -mean);
+      float2 a = make_float2(q, 0.0f);
+#pragma unroll
+      for (int j = 0; j < V; j += 2) {
+        const float2 e = add2(make_float2(v[j], v[j + 1]), nm);
+        a = fma2(e, e, a);
+        v[j] = e.x, v[j + 1] = e.y;
+      }
+      return a.x + a.y;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    v[j] = col + j < d ? v[j] - mean : 0.0f;
+    q = __fmaf_rn(v[j], v[j], q);
+  }
+  return q;
 }
 
 struct NormFwd {
@@ -181,7 +325,7 @@ struct NormFwd {
   const float* gamma;
   const float* beta;
   float eps;
-  float fd;  // (float)d; sums are divided by it, so that a constant row's mean is the constant
+  Div dv;
   int relu;
   Drop dr;
   void* Y;
@@ -192,39 +336,47 @@ struct NormFwd {
   int64_t ldrb;
 };
 
-// The row's outputs from its centred values xc.  Every lane of the warp
+// V outputs of a row from its centred values xc.  Every lane of the warp
 // takes part (the bits are gathered by shuffles); `live` lanes store.
-template <typename T, int V, int NV, int G>
-__device__ __forceinline__ void norm_emit(const NormFwd& p, int64_t r, bool live, float rstd, int c0, int cstep,
-                                          const float (&xc)[NV][V], const float (&ga)[NV][V],
-                                          const float (&be)[NV][V]) {
-  const uint32_t kr = row_key(p.dr.key, (uint32_t)r);
+template <typename T, int V>
+__device__ __forceinline__ void norm_emit(const NormFwd& p, int64_t r, uint32_t kr, bool live, float rstd, int col,
+                                          const float* xc, const float* ga, const float* be) {
+  float y[V];
+  uint32_t pos = 0;
+  if constexpr (V > 1) {
+    const float2 rs = make_float2(rstd, rstd);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int col = c0 + i * cstep;
-    float y[V];
-    uint32_t pos = 0;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      float z = __fmaf_rn(xc[i][j] * rstd, ga[i][j], be[i][j]);
-      if (p.relu) {
-        const bool on = z > 0.0f;
-        pos |= (uint32_t)(on && col + j < p.d) << j;
-        z = on ? z : 0.0f;
-      }
-      if (p.dr.drop != 0) z = kept(kr, col + j, p.dr.drop) ? z * p.dr.scale : 0.0f;
-      y[j] = z;
+    for (int j = 0; j < V; j += 2) {
+      const float2 z = fma2(mul2(make_float2(xc[j], xc[j + 1]), rs), make_float2(ga[j], ga[j + 1]),
+                            make_float2(be[j], be[j + 1]));
+      y[j] = z.x, y[j + 1] = z.y;
     }
-    if (live && col < p.d) store_vec<T, V>(static_cast<T*>(p.Y) + r * p.ldy, col, p.d, y, true);
+  } else {
+    y[0] = __fmaf_rn(xc[0] * rstd, ga[0], be[0]);
+  }
+  if (p.relu) {
     if (p.bits != nullptr) {
-      const uint32_t w = gather_bits<V, G>(pos, col);
-      if (live && (col & 31) == 0 && col < p.d) p.bits[r * p.ldrb + (col >> 5)] = w;
+#pragma unroll
+      for (int j = 0; j < V; ++j) pos |= (uint32_t)(y[j] > 0.0f && col + j < p.d) << j;
     }
+#pragma unroll
+    for (int j = 0; j < V; ++j) y[j] = fmaxf(y[j], 0.0f);
+  }
+  if (p.dr.on) {
+    const uint32_t base = kr + (uint32_t)col * kColMul;
+#pragma unroll
+    for (int j = 0; j < V; ++j) y[j] = kept(base, j, p.dr.lim) ? y[j] * p.dr.scale : 0.0f;
+  }
+  if (live && col < p.d) store_vec<T, V>(static_cast<T*>(p.Y) + r * p.ldy, col, p.d, y, true);
+  if (p.bits != nullptr) {
+    const uint32_t w = gather_bits<V>(pos, col);
+    if (live && (col & 31) == 0 && col < p.d) p.bits[r * p.ldrb + (col >> 5)] = w;
   }
 }
 
-// Rows of d <= 512: a group of G lanes per row.
-template <typename T, int V, int NV, int G>
+// Rows of d <= 512: a group of G lanes per row (V = 1: G = 32, so that a
+// word of bits is one vector).  WHOLE: d = G NV V, no column to leave out.
+template <typename T, int V, int NV, int G, bool WHOLE>
 __global__ void __launch_bounds__(kNormThreads) norm_fwd_warp_kernel(const NormFwd p) {
   constexpr int kGroups = 32 / G;
   const int lane = threadIdx.x & 31, sub = lane / G;
@@ -237,80 +389,114 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_warp_kernel(const NormF
     load_param<V>(p.gamma, c0 + i * G * V, p.d, 1.0f, ga[i]);
     load_param<V>(p.beta, c0 + i * G * V, p.d, 0.0f, be[i]);
   }
+  Raw<T, V> nx[NV];  // the next row is on its way while one is worked on
+  auto fetch = [&](int64_t rw) {
+    const T* x = static_cast<const T*>(p.X) + (rw + sub < p.n ? rw + sub : rw) * p.ldx;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) load_raw<T, V>(x, c0 + i * G * V, p.d, nx[i]);
+  };
+  if (warp * kGroups < p.n) fetch(warp * kGroups);
   for (int64_t rw = warp * kGroups; rw < p.n; rw += step) {
     const int64_t r = rw + sub;
     const bool live = r < p.n;
-    const T* x = static_cast<const T*>(p.X) + (live ? r : rw) * p.ldx;
     float v[NV][V];
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      load_vec<T, V>(x, c0 + i * G * V, p.d, v[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
+      unpack<T, V>(nx[i], v[i]);
 #pragma unroll
       for (int j = 0; j < V; ++j) s += v[i][j];
-    const float mean = group_sum<G>(s) / p.fd;
+    }
+    if (rw + step < p.n) fetch(rw + step);
+    const float mean = over(group_sum<G>(s), p.dv);
     float q = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        v[i][j] = c0 + i * G * V + j < p.d ? v[i][j] - mean : 0.0f;
-        q = __fmaf_rn(v[i][j], v[i][j], q);
-      }
-    const float rstd = 1.0f / sqrtf(group_sum<G>(q) / p.fd + p.eps);
+    for (int i = 0; i < NV; ++i) q = centre<V>(v[i], mean, WHOLE || c0 + i * G * V + V <= p.d, c0 + i * G * V, p.d, q);
+    const float rstd = inv_sqrt(over(group_sum<G>(q), p.dv) + p.eps);
     if (live && lane % G == 0) {
       if (p.mean != nullptr) p.mean[r] = mean;
       if (p.rstd != nullptr) p.rstd[r] = rstd;
     }
-    norm_emit<T, V, NV, G>(p, r, live, rstd, c0, G * V, v, ga, be);
+    const uint32_t kr = row_key(p.dr.key, (uint32_t)r);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) norm_emit<T, V>(p, r, kr, live, rstd, c0 + i * G * V, v[i], ga[i], be[i]);
   }
 }
 
 // Wider rows: a block per row, thread t holding columns (i blockDim + t) V.
+// Each warp forms the mean m_w of its n_w columns and their squared distances
+// q_w from it; one barrier later every thread joins the warps' triples:
+//   mean = sum n_w m_w / d,  d var = sum q_w + sum n_w (m_w - mean)^2
+// (both sums of non-negative terms), so a row costs one barrier.  The next
+// row is loaded before the barrier; gamma and beta stay in shared memory.
 template <typename T, int V>
-__global__ void __launch_bounds__(1024) norm_fwd_block_kernel(const NormFwd p) {
+__global__ void __launch_bounds__(1024, 1) norm_fwd_block_kernel(const NormFwd p) {
   constexpr int NV = kEpt / V;
-  __shared__ float red[2][64];
-  const int c0 = (int)threadIdx.x * V, cs = (int)blockDim.x * V;
+  extern __shared__ float par[];  // gamma | beta, each blockDim * kEpt
+  __shared__ float red[2][96];
+  const int c0 = (int)threadIdx.x * V, cs = (int)blockDim.x * V, W = (int)blockDim.x * kEpt;
+  const int w = threadIdx.x >> 5, nw = blockDim.x >> 5, lane = threadIdx.x & 31;
+  for (int c = threadIdx.x; c < W; c += blockDim.x) {
+    par[c] = c < p.d ? (p.gamma != nullptr ? p.gamma[c] : 1.0f) : 0.0f;
+    par[W + c] = c < p.d && p.beta != nullptr ? p.beta[c] : 0.0f;
+  }
+  float cols = 0.0f;  // columns of this warp
+#pragma unroll
+  for (int i = 0; i < NV; ++i) cols += (float)min(max(p.d - (c0 + i * cs), 0), V);
+  cols = group_sum<32>(cols);
   int flip = 0;
-  for (int64_t r = blockIdx.x; r < p.n; r += gridDim.x) {
-    const T* x = static_cast<const T*>(p.X) + r * p.ldx;
+  int64_t r = blockIdx.x;
+  Raw<T, V> nx[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) load_raw<T, V>(static_cast<const T*>(p.X) + r * p.ldx, c0 + i * cs, p.d, nx[i]);
+  __syncthreads();
+  for (; r < p.n; r += gridDim.x) {
     float v[NV][V];
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) load_vec<T, V>(x, c0 + i * cs, p.d, v[i]);
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      unpack<T, V>(nx[i], v[i]);
 #pragma unroll
       for (int j = 0; j < V; ++j) s += v[i][j];
-    const float mean = block_sum2(s, 0.0f, red[flip]).x / p.fd;
-    flip ^= 1;
+    }
+    if (r + gridDim.x < p.n) {
+      const T* x = static_cast<const T*>(p.X) + (r + gridDim.x) * p.ldx;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) load_raw<T, V>(x, c0 + i * cs, p.d, nx[i]);
+    }
+    const float mw = cols > 0.0f ? group_sum<32>(s) / cols : 0.0f;
     float q = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        v[i][j] = c0 + i * cs + j < p.d ? v[i][j] - mean : 0.0f;
-        q = __fmaf_rn(v[i][j], v[i][j], q);
-      }
-    const float rstd = 1.0f / sqrtf(block_sum2(q, 0.0f, red[flip]).x / p.fd + p.eps);
+    for (int i = 0; i < NV; ++i) q = centre<V>(v[i], mw, (i + 1) * cs <= p.d, c0 + i * cs, p.d, q);
+    q = group_sum<32>(q);
+    float* rd = red[flip];
     flip ^= 1;
+    if (lane == 0) {
+      rd[w] = cols;
+      rd[32 + w] = mw;
+      rd[64 + w] = q;
+    }
+    __syncthreads();
+    const float n1 = lane < nw ? rd[lane] : 0.0f, m1 = lane < nw ? rd[32 + lane] : 0.0f;
+    const float mean = over(group_sum<32>(n1 * m1), p.dv);
+    const float e1 = m1 - mean;
+    const float var = over(group_sum<32>(__fmaf_rn(n1 * e1, e1, lane < nw ? rd[64 + lane] : 0.0f)), p.dv);
+    const float rstd = inv_sqrt(var + p.eps);
     if (threadIdx.x == 0) {
       if (p.mean != nullptr) p.mean[r] = mean;
       if (p.rstd != nullptr) p.rstd[r] = rstd;
     }
+    const float off = mw - mean;  // from the warp's mean to the row's
+    const uint32_t kr = row_key(p.dr.key, (uint32_t)r);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {  // one vector at a time: gamma and beta come from L1
-      float ga[1][V], be[1][V];
-      load_param<V>(p.gamma, c0 + i * cs, p.d, 1.0f, ga[0]);
-      load_param<V>(p.beta, c0 + i * cs, p.d, 0.0f, be[0]);
-      float one[1][V];
+    for (int i = 0; i < NV; ++i) {
+      if (i * cs >= p.d) break;
+      float ga[V], be[V];
+      load_shared<V>(par + c0 + i * cs, ga);
+      load_shared<V>(par + W + c0 + i * cs, be);
 #pragma unroll
-      for (int j = 0; j < V; ++j) one[0][j] = v[i][j];
-      norm_emit<T, V, 1, 32>(p, r, true, rstd, c0 + i * cs, 0, one, ga, be);
+      for (int j = 0; j < V; ++j) v[i][j] += off;
+      norm_emit<T, V>(p, r, kr, true, rstd, c0 + i * cs, v[i], ga, be);
     }
   }
 }
@@ -321,7 +507,7 @@ struct NormBwd {
   const void* X;
   int64_t n, lddy, ldx;
   int d;
-  float fd;
+  Div dv;
   const float* mean;
   const float* rstd;
   const float* gamma;
@@ -335,86 +521,79 @@ struct NormBwd {
   float* partial;   // [block][2][d]: dgamma | dbeta
 };
 
-// dz of V columns: the dropout of the forward pass, then its ReLU gate.
+// the ReLU bits of the columns from col on (bit 0: col)
+__device__ __forceinline__ uint32_t gate_bits(const NormBwd& p, int64_t r, int col) {
+  return p.relu && col < p.d ? __ldg(p.bits + r * p.ldrb + (col >> 5)) >> (col & 31) : 0u;
+}
+
+// dz of V columns: the dropout of the forward pass and its ReLU gate w.
+// Where dY was past the row it is 0 and stays 0.
 template <int V>
-__device__ __forceinline__ void gate_dz(const NormBwd& p, int64_t r, uint32_t kr, int col, float (&dz)[V]) {
-  if (p.dr.drop != 0) {
+__device__ __forceinline__ void gate_dz(const NormBwd& p, uint32_t w, uint32_t kr, int col, float* dz) {
+  const uint32_t base = kr + (uint32_t)col * kColMul;
+  if (p.relu) {
+    if (p.dr.on) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) dz[j] = kept(kr, col + j, p.dr.drop) ? dz[j] * p.dr.scale : 0.0f;
-  }
-  if (p.relu && col < p.d) {
-    const uint32_t w = __ldg(p.bits + r * p.ldrb + (col >> 5)) >> (col & 31);
+      for (int j = 0; j < V; ++j) dz[j] = (w >> j & 1u) && kept(base, j, p.dr.lim) ? dz[j] * p.dr.scale : 0.0f;
+    } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (((w >> j) & 1u) == 0) dz[j] = 0.0f;
+      for (int j = 0; j < V; ++j) dz[j] = (w >> j & 1u) ? dz[j] : 0.0f;
+    }
+  } else if (p.dr.on) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) dz[j] = kept(base, j, p.dr.lim) ? dz[j] * p.dr.scale : 0.0f;
   }
 }
 
-template <typename T, typename TO, int V, int NV, int G>
-__global__ void __launch_bounds__(kNormThreads) norm_bwd_warp_kernel(const NormBwd p) {
-  constexpr int kGroups = 32 / G;
+// The backward arithmetic of E (even) elements of a row, two at a time:
+// xh = (x - mean) rstd over x; g = dz gamma over dz; column sums; s1, s2 the
+// row's sums of g and g xh.  Elements past the row have dz = 0 and add
+// nothing.
+template <int E>
+__device__ __forceinline__ void bwd_terms(float* x, float* dz, const float* ga, float* sg, float* sb, float mean,
+                                          float rstd, float& s1, float& s2) {
+  const float2 nm = make_float2(-mean, -mean), rs = make_float2(rstd, rstd);
+  float2 a = make_float2(0.0f, 0.0f), b = a;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    const float2 xh = mul2(add2(make_float2(x[e], x[e + 1]), nm), rs);
+    const float2 z = make_float2(dz[e], dz[e + 1]);
+    const float2 ng = fma2(z, xh, make_float2(sg[e], sg[e + 1])), nb = add2(make_float2(sb[e], sb[e + 1]), z);
+    const float2 g = mul2(z, make_float2(ga[e], ga[e + 1]));
+    a = add2(a, g);
+    b = fma2(g, xh, b);
+    sg[e] = ng.x, sg[e + 1] = ng.y, sb[e] = nb.x, sb[e + 1] = nb.y;
+    x[e] = xh.x, x[e + 1] = xh.y, dz[e] = g.x, dz[e + 1] = g.y;
+  }
+  s1 += a.x + a.y;
+  s2 += b.x + b.y;
+}
+
+// rstd (g - m1 - xh m2) of E elements, over g
+template <int E>
+__device__ __forceinline__ void bwd_out(float* g, const float* xh, float m1, float m2, float rstd) {
+  const float2 n1 = make_float2(-m1, -m1), n2 = make_float2(-m2, -m2), rs = make_float2(rstd, rstd);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    const float2 o =
+        mul2(fma2(make_float2(xh[e], xh[e + 1]), n2, add2(make_float2(g[e], g[e + 1]), n1)), rs);
+    g[e] = o.x, g[e + 1] = o.y;
+  }
+}
+
+// The block's column sums from its lanes' (acc: [warp][2][G NV V] floats).
+template <int V, int NV, int G>
+__device__ __forceinline__ void warp_sums(const NormBwd& p, float* acc, const float* sg, const float* sb) {
   constexpr int kWarps = kNormThreads / 32;
-  extern __shared__ float acc[];  // [warp][2][G * NV * V]
   const int lane = threadIdx.x & 31, sub = lane / G, w = threadIdx.x >> 5;
   const int c0 = (lane % G) * V;
-  const int64_t warp = (int64_t)blockIdx.x * kWarps + w;
-  const int64_t step = (int64_t)gridDim.x * kWarps * kGroups;
-  float ga[NV][V], sg[NV][V], sb[NV][V];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    load_param<V>(p.gamma, c0 + i * G * V, p.d, 1.0f, ga[i]);
-#pragma unroll
-    for (int j = 0; j < V; ++j) sg[i][j] = sb[i][j] = 0.0f;
-  }
-  for (int64_t rw = warp * kGroups; rw < p.n; rw += step) {
-    const int64_t r = rw + sub;
-    const bool live = r < p.n;
-    const int64_t rr = live ? r : rw;
-    const T* x = static_cast<const T*>(p.X) + rr * p.ldx;
-    const T* dy = static_cast<const T*>(p.dY) + rr * p.lddy;
-    float xv[NV][V], dz[NV][V];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      load_vec<T, V>(x, c0 + i * G * V, p.d, xv[i]);
-      load_vec<T, V>(dy, c0 + i * G * V, p.d, dz[i]);
-    }
-    const float mean = __ldg(p.mean + rr), rstd = __ldg(p.rstd + rr);
-    const uint32_t kr = row_key(p.dr.key, (uint32_t)rr);
-    float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      gate_dz<V>(p, rr, kr, c0 + i * G * V, dz[i]);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const bool in = live && c0 + i * G * V + j < p.d;
-        const float xh = in ? (xv[i][j] - mean) * rstd : 0.0f;
-        const float z = in ? dz[i][j] : 0.0f;
-        sg[i][j] = __fmaf_rn(z, xh, sg[i][j]);
-        sb[i][j] += z;
-        const float g = z * ga[i][j];
-        s1 += g;
-        s2 = __fmaf_rn(g, xh, s2);
-        xv[i][j] = xh;
-        dz[i][j] = g;
-      }
-    }
-    const float m1 = group_sum<G>(s1) / p.fd, m2 = group_sum<G>(s2) / p.fd;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int col = c0 + i * G * V;
-      float o[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) o[j] = rstd * (dz[i][j] - m1 - xv[i][j] * m2);
-      if (live && col < p.d) store_vec<TO, V>(static_cast<TO*>(p.dX) + r * p.lddx, col, p.d, o, p.vec_out);
-    }
-  }
   if (p.partial == nullptr) return;
   constexpr int W = G * NV * V;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      float a = sg[i][j], b = sb[i][j];
+      float a = sg[i * V + j], b = sb[i * V + j];
 #pragma unroll
       for (int o = G; o < 32; o <<= 1) {  // groups of the warp
         a += __shfl_xor_sync(FULL, a, o);
@@ -435,62 +614,241 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_warp_kernel(const NormB
   }
 }
 
-// Wide rows: the block's column sums live in shared memory, each column
-// touched by its one owner thread only.
-template <typename T, typename TO, int V>
-__global__ void __launch_bounds__(1024) norm_bwd_block_kernel(const NormBwd p) {
-  constexpr int NV = kEpt / V;
-  extern __shared__ float acc[];  // [2][blockDim * kEpt]
+// Rows of d <= 512 that start 16-byte aligned: S - 1 rows of each warp on
+// their way through shared memory.
+template <typename T, typename TO, int V, int NV, int G, int S>
+__global__ void __launch_bounds__(kNormThreads) norm_bwd_ring_kernel(const NormBwd p) {
+  constexpr int kGroups = 32 / G;
+  constexpr int kWarps = kNormThreads / 32;
+  constexpr int E = NV * V;
+  extern __shared__ uint4 ring[];  // [warp][S][2 NV][lane]; afterwards the block's sums
+  const int lane = threadIdx.x & 31, sub = lane / G, w = threadIdx.x >> 5;
+  const int c0 = (lane % G) * V;
+  const int64_t step = (int64_t)gridDim.x * kWarps * kGroups;
+  uint4* mine = ring + (size_t)w * S * 2 * NV * 32 + lane;
+  float ga[E], sg[E], sb[E];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float q[V];
+    load_param<V>(p.gamma, c0 + i * G * V, p.d, 1.0f, q);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      ga[i * V + j] = q[j];
+      sg[i * V + j] = sb[i * V + j] = 0.0f;
+    }
+  }
+  auto issue = [&](int64_t rw, int slot) {
+    if (rw < p.n) {
+      const int64_t r = rw + sub < p.n ? rw + sub : rw;
+      const int dd = rw + sub < p.n ? p.d : 0;
+      uint4* to = mine + slot * 2 * NV * 32;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        copy_vec<T, V>(to + i * 32, static_cast<const T*>(p.X) + r * p.ldx, c0 + i * G * V, p.d);
+        copy_vec<T, V>(to + (NV + i) * 32, static_cast<const T*>(p.dY) + r * p.lddy, c0 + i * G * V, dd);
+      }
+    }
+    copy_commit();
+  };
+  int64_t rw = ((int64_t)blockIdx.x * kWarps + w) * kGroups;
+  float nm = 0.0f, nr = 0.0f;
+  uint32_t nb[NV] = {};
+  auto fetch = [&](int64_t rn) {  // a row's statistics and ReLU bits
+    if (rn >= p.n) return;
+    const int64_t r = rn + sub < p.n ? rn + sub : rn;
+    nm = __ldg(p.mean + r);
+    nr = __ldg(p.rstd + r);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) nb[i] = gate_bits(p, r, c0 + i * G * V);
+  };
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) issue(rw + s * step, s);
+  fetch(rw);
+  int slot = 0;
+  for (; rw < p.n; rw += step) {
+    const int64_t r = rw + sub;
+    const bool live = r < p.n;
+    const float mean = nm, rstd = nr;
+    float xv[E], dz[E];
+    uint32_t wb[NV];
+    copy_wait<S - 2>();
+    const uint4* from = mine + slot * 2 * NV * 32;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      wb[i] = nb[i];
+      read_slot<T, V>(from + i * 32, xv + i * V);
+      read_slot<T, V>(from + (NV + i) * 32, dz + i * V);
+    }
+    issue(rw + (S - 1) * step, slot == 0 ? S - 1 : slot - 1);
+    fetch(rw + step);
+    if (++slot == S) slot = 0;
+    const uint32_t kr = row_key(p.dr.key, (uint32_t)(live ? r : rw));
+#pragma unroll
+    for (int i = 0; i < NV; ++i) gate_dz<V>(p, wb[i], kr, c0 + i * G * V, dz + i * V);
+    float s1 = 0.0f, s2 = 0.0f;
+    bwd_terms<E>(xv, dz, ga, sg, sb, mean, rstd, s1, s2);
+    const float m1 = over(group_sum<G>(s1), p.dv), m2 = over(group_sum<G>(s2), p.dv);
+    bwd_out<E>(dz, xv, m1, m2, rstd);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = c0 + i * G * V;
+      if (live && col < p.d)
+        store_vec<TO, V>(static_cast<TO*>(p.dX) + r * p.lddx, col, p.d,
+                         *reinterpret_cast<const float(*)[V]>(dz + i * V), p.vec_out);
+    }
+  }
+  copy_wait<0>();
+  __syncthreads();
+  warp_sums<V, NV, G>(p, reinterpret_cast<float*>(ring), sg, sb);
+}
+
+template <typename T, typename TO, int V, int NV, int G>
+__global__ void __launch_bounds__(kNormThreads) norm_bwd_warp_kernel(const NormBwd p) {
+  constexpr int kGroups = 32 / G;
+  constexpr int kWarps = kNormThreads / 32;
+  constexpr int E = NV * V;
+  extern __shared__ float acc[];  // [warp][2][G * NV * V]
+  const int lane = threadIdx.x & 31, sub = lane / G, w = threadIdx.x >> 5;
+  const int c0 = (lane % G) * V;
+  const int64_t warp = (int64_t)blockIdx.x * kWarps + w;
+  const int64_t step = (int64_t)gridDim.x * kWarps * kGroups;
+  float ga[E], sg[E], sb[E];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float q[V];
+    load_param<V>(p.gamma, c0 + i * G * V, p.d, 1.0f, q);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      ga[i * V + j] = q[j];
+      sg[i * V + j] = sb[i * V + j] = 0.0f;
+    }
+  }
+  // the next row is on its way while one is worked on
+  Raw<T, V> nx[NV], ny[NV];
+  float nm = 0.0f, nr = 0.0f;
+  uint32_t nb[NV];
+  auto fetch = [&](int64_t rw) {
+    const int64_t r = rw + sub;
+    const int64_t rr = r < p.n ? r : rw;
+    const T* x = static_cast<const T*>(p.X) + rr * p.ldx;
+    const T* dy = static_cast<const T*>(p.dY) + rr * p.lddy;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      load_raw<T, V>(x, c0 + i * G * V, p.d, nx[i]);
+      load_raw<T, V>(dy, c0 + i * G * V, r < p.n ? p.d : 0, ny[i]);
+      nb[i] = gate_bits(p, rr, c0 + i * G * V);
+    }
+    nm = __ldg(p.mean + rr);
+    nr = __ldg(p.rstd + rr);
+  };
+  if (warp * kGroups < p.n) fetch(warp * kGroups);
+  for (int64_t rw = warp * kGroups; rw < p.n; rw += step) {
+    const int64_t r = rw + sub;
+    const bool live = r < p.n;
+    const int64_t rr = live ? r : rw;
+    const float mean = nm, rstd = nr;
+    float xv[E], dz[E];
+    uint32_t wb[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      wb[i] = nb[i];
+      unpack<T, V>(nx[i], xv + i * V);
+      unpack<T, V>(ny[i], dz + i * V);
+    }
+    if (rw + step < p.n) fetch(rw + step);
+    const uint32_t kr = row_key(p.dr.key, (uint32_t)rr);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) gate_dz<V>(p, wb[i], kr, c0 + i * G * V, dz + i * V);
+    float s1 = 0.0f, s2 = 0.0f;
+    bwd_terms<E>(xv, dz, ga, sg, sb, mean, rstd, s1, s2);
+    const float m1 = over(group_sum<G>(s1), p.dv), m2 = over(group_sum<G>(s2), p.dv);
+    bwd_out<E>(dz, xv, m1, m2, rstd);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = c0 + i * G * V;
+      if (live && col < p.d)
+        store_vec<TO, V>(static_cast<TO*>(p.dX) + r * p.lddx, col, p.d,
+                         *reinterpret_cast<const float(*)[V]>(dz + i * V), p.vec_out);
+    }
+  }
+  warp_sums<V, NV, G>(p, acc, sg, sb);
+}
+
+// Wide rows: gamma and the block's column sums live in shared memory, each
+// column touched by its one owner thread only; the next row is loaded before
+// the current one's barrier.
+template <typename T, typename TO, int V, int EPT>
+__global__ void __launch_bounds__(1024, 1) norm_bwd_block_kernel(const NormBwd p) {
+  constexpr int NV = EPT / V;
+  extern __shared__ float acc[];  // dgamma | dbeta | gamma, each blockDim * EPT
   __shared__ float red[2][64];
   const int c0 = (int)threadIdx.x * V, cs = (int)blockDim.x * V;
-  const int W = (int)blockDim.x * kEpt;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < V; ++j) acc[c0 + i * cs + j] = acc[W + c0 + i * cs + j] = 0.0f;
+  const int W = (int)blockDim.x * EPT;
+  for (int c = threadIdx.x; c < W; c += blockDim.x) {
+    acc[c] = acc[W + c] = 0.0f;
+    acc[2 * W + c] = c < p.d ? (p.gamma != nullptr ? p.gamma[c] : 1.0f) : 0.0f;
+  }
   int flip = 0;
-  for (int64_t r = blockIdx.x; r < p.n; r += gridDim.x) {
-    const T* x = static_cast<const T*>(p.X) + r * p.ldx;
-    const T* dy = static_cast<const T*>(p.dY) + r * p.lddy;
-    float xv[NV][V], dz[NV][V];
+  int64_t r = blockIdx.x;
+  Raw<T, V> nx[NV], ny[NV];
+  float nm, nr;
+  uint32_t nb[NV];
+  auto fetch = [&](int64_t row) {
+    const T* x = static_cast<const T*>(p.X) + row * p.ldx;
+    const T* dy = static_cast<const T*>(p.dY) + row * p.lddy;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      load_vec<T, V>(x, c0 + i * cs, p.d, xv[i]);
-      load_vec<T, V>(dy, c0 + i * cs, p.d, dz[i]);
+      load_raw<T, V>(x, c0 + i * cs, p.d, nx[i]);
+      load_raw<T, V>(dy, c0 + i * cs, p.d, ny[i]);
+      nb[i] = gate_bits(p, row, c0 + i * cs);
     }
-    const float mean = __ldg(p.mean + r), rstd = __ldg(p.rstd + r);
+    nm = __ldg(p.mean + row);
+    nr = __ldg(p.rstd + row);
+  };
+  fetch(r);
+  __syncthreads();
+  for (; r < p.n; r += gridDim.x) {
+    const float mean = nm, rstd = nr;
     const uint32_t kr = row_key(p.dr.key, (uint32_t)r);
-    float s1 = 0.0f, s2 = 0.0f;
+    float xh[EPT], g[EPT];
+    uint32_t wb[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = c0 + i * cs;
-      gate_dz<V>(p, r, kr, col, dz[i]);
-      float ga[V];
-      load_param<V>(p.gamma, col, p.d, 1.0f, ga);
+      wb[i] = nb[i];
+      unpack<T, V>(nx[i], xh + i * V);
+      unpack<T, V>(ny[i], g + i * V);
+    }
+    if (r + gridDim.x < p.n) fetch(r + gridDim.x);
+    float s1 = 0.0f, s2 = 0.0f;
+    constexpr int S = V > 1 ? V : 2;  // elements at a time
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const bool in = col + j < p.d;
-        const float xh = in ? (xv[i][j] - mean) * rstd : 0.0f;
-        const float z = in ? dz[i][j] : 0.0f;
-        acc[col + j] = __fmaf_rn(z, xh, acc[col + j]);
-        acc[W + col + j] += z;
-        const float g = z * ga[j];
-        s1 += g;
-        s2 = __fmaf_rn(g, xh, s2);
-        xv[i][j] = xh;
-        dz[i][j] = g;
+    for (int e = 0; e < EPT; e += S) {
+      float sg[S], sb[S], ga[S];
+#pragma unroll
+      for (int k = 0; k < S; k += V) {
+        const int col = c0 + (e + k) / V * cs;
+        gate_dz<V>(p, wb[(e + k) / V], kr, col, g + e + k);
+        load_shared<V>(acc + col, sg + k);
+        load_shared<V>(acc + W + col, sb + k);
+        load_shared<V>(acc + 2 * W + col, ga + k);
+      }
+      bwd_terms<S>(xh + e, g + e, ga, sg, sb, mean, rstd, s1, s2);
+#pragma unroll
+      for (int k = 0; k < S; k += V) {
+        const int col = c0 + (e + k) / V * cs;
+        store_shared<V>(acc + col, sg + k);
+        store_shared<V>(acc + W + col, sb + k);
       }
     }
     const float2 s = block_sum2(s1, s2, red[flip]);
     flip ^= 1;
-    const float m1 = s.x / p.fd, m2 = s.y / p.fd;
+    bwd_out<EPT>(g, xh, over(s.x, p.dv), over(s.y, p.dv), rstd);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = c0 + i * cs;
-      float o[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) o[j] = rstd * (dz[i][j] - m1 - xv[i][j] * m2);
-      if (col < p.d) store_vec<TO, V>(static_cast<TO*>(p.dX) + r * p.lddx, col, p.d, o, p.vec_out);
+      if (col < p.d)
+        store_vec<TO, V>(static_cast<TO*>(p.dX) + r * p.lddx, col, p.d,
+                         *reinterpret_cast<const float(*)[V]>(g + i * V), p.vec_out);
     }
   }
   if (p.partial == nullptr) return;
@@ -502,6 +860,97 @@ __global__ void __launch_bounds__(1024) norm_bwd_block_kernel(const NormBwd p) {
       if (col >= p.d) continue;
       p.partial[(int64_t)blockIdx.x * 2 * p.d + col] = acc[col];
       p.partial[(int64_t)blockIdx.x * 2 * p.d + p.d + col] = acc[W + col];
+    }
+}
+
+// Wide rows up to 8,192 columns that start 16-byte aligned: the column sums
+// and the row at work in registers (112 to 128 a thread), S - 1 rows on their
+// way through shared memory, gamma there too.
+template <typename T, typename TO, int V, int S, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) norm_bwd_wide_kernel(const NormBwd p) {
+  constexpr int NV = kEpt / V;
+  extern __shared__ uint4 ring[];  // [S][2 NV][thread], then gamma [blockDim * kEpt]
+  __shared__ float red[2][64];
+  const int T0 = (int)blockDim.x;
+  float* gam = reinterpret_cast<float*>(ring + (size_t)S * 2 * NV * T0);
+  uint4* mine = ring + threadIdx.x;
+  const int c0 = (int)threadIdx.x * V, cs = T0 * V;
+  for (int c = threadIdx.x; c < T0 * kEpt; c += T0)
+    gam[c] = c < p.d ? (p.gamma != nullptr ? p.gamma[c] : 1.0f) : 0.0f;
+  float sg[kEpt], sb[kEpt];
+#pragma unroll
+  for (int e = 0; e < kEpt; ++e) sg[e] = sb[e] = 0.0f;
+  auto issue = [&](int64_t r, int slot) {
+    if (r < p.n) {
+      uint4* to = mine + slot * 2 * NV * T0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        copy_vec<T, V>(to + i * T0, static_cast<const T*>(p.X) + r * p.ldx, c0 + i * cs, p.d);
+        copy_vec<T, V>(to + (NV + i) * T0, static_cast<const T*>(p.dY) + r * p.lddy, c0 + i * cs, p.d);
+      }
+    }
+    copy_commit();
+  };
+  int64_t r = blockIdx.x;
+  float nm = 0.0f, nr = 0.0f;
+  uint32_t nb[NV] = {};
+  auto fetch = [&](int64_t rn) {
+    if (rn >= p.n) return;
+    nm = __ldg(p.mean + rn);
+    nr = __ldg(p.rstd + rn);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) nb[i] = gate_bits(p, rn, c0 + i * cs);
+  };
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) issue(r + (int64_t)s * gridDim.x, s);
+  fetch(r);
+  __syncthreads();
+  int slot = 0, flip = 0;
+  for (; r < p.n; r += gridDim.x) {
+    const float mean = nm, rstd = nr;
+    float xv[kEpt], dz[kEpt];
+    uint32_t wb[NV];
+    copy_wait<S - 2>();
+    const uint4* from = mine + slot * 2 * NV * T0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      wb[i] = nb[i];
+      read_slot<T, V>(from + i * T0, xv + i * V);
+      read_slot<T, V>(from + (NV + i) * T0, dz + i * V);
+    }
+    issue(r + (int64_t)(S - 1) * gridDim.x, slot == 0 ? S - 1 : slot - 1);
+    fetch(r + gridDim.x);
+    if (++slot == S) slot = 0;
+    const uint32_t kr = row_key(p.dr.key, (uint32_t)r);
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float ga[V];
+      gate_dz<V>(p, wb[i], kr, c0 + i * cs, dz + i * V);
+      load_shared<V>(gam + c0 + i * cs, ga);
+      bwd_terms<V>(xv + i * V, dz + i * V, ga, sg + i * V, sb + i * V, mean, rstd, s1, s2);
+    }
+    const float2 s = block_sum2(s1, s2, red[flip]);
+    flip ^= 1;
+    bwd_out<kEpt>(dz, xv, over(s.x, p.dv), over(s.y, p.dv), rstd);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = c0 + i * cs;
+      if (col < p.d)
+        store_vec<TO, V>(static_cast<TO*>(p.dX) + r * p.lddx, col, p.d,
+                         *reinterpret_cast<const float(*)[V]>(dz + i * V), p.vec_out);
+    }
+  }
+  copy_wait<0>();
+  if (p.partial == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int col = c0 + i * cs + j;
+      if (col >= p.d) continue;
+      p.partial[(int64_t)blockIdx.x * 2 * p.d + col] = sg[i * V + j];
+      p.partial[(int64_t)blockIdx.x * 2 * p.d + p.d + col] = sb[i * V + j];
     }
 }
 
@@ -531,12 +980,31 @@ bool rows16(const void* p, int64_t ld, int type) { return aligned(p, 16) && ld *
 
 int make_drop(double p, uint64_t seed, Drop* d) {
   if (!(p >= 0.0 && p <= 1.0)) return GQ_ERR_INVALID_ARG;
-  d->drop = (uint32_t)std::ceil(p * 8388608.0);  // p = 1: above every 23-bit code
+  const uint32_t t = (uint32_t)std::ceil(p * 8388608.0);
+  d->on = t > 0;
+  d->lim = t * 512u - 1u;  // p = 1: 2^32 - 1
   d->scale = p < 1.0 ? (float)(1.0 / (1.0 - p)) : 0.0f;
   d->key = seed_key_host(seed);
   return GQ_OK;
 }
 
+// Resident blocks of a wide-row kernel per SM: about 1024 threads (64
+// registers a thread), within 200 KB of shared memory.
+int block_rows_per_sm(int threads, size_t smem) {
+  int per = 1024 / threads;
+  while (per > 1 && per * smem > 200 * 1024) --per;
+  return per < 1 ? 1 : per;
+}
+
+// Elements per thread of a wide row's backward pass: 8 keep the two rows in
+// flight within 64 registers; beyond 1024 threads, 16.
+int bwd_ept(int d) { return d <= 8192 ? 8 : 16; }
+
+// Threads and resident blocks per SM of norm_bwd_wide_kernel.
+int wide_threads(int d) { return ((d + kEpt - 1) / kEpt + 31) / 32 * 32; }
+int wide_per_sm(int threads) { return threads <= 288 ? 576 / threads : 1; }
+
+// Upper bound of the backward's blocks, one partial row of sums each.
 int bwd_blocks(int64_t n, int d) {
   // enough blocks to fill the SMs (4 x 256 threads, or about 1024 threads of
   // wide rows, each), and no more partial rows than that
@@ -545,8 +1013,9 @@ int bwd_blocks(int64_t n, int d) {
     const int64_t want = (n + 7) / 8;
     return (int)(want < 4 * sms ? (want < 1 ? 1 : want) : 4 * sms);
   }
-  const int threads = ((d + kEpt - 1) / kEpt + 31) / 32 * 32;
-  const int per = threads >= 512 ? (threads > 512 ? 1 : 2) : 1024 / threads;
+  const int ept = bwd_ept(d), threads = ((d + ept - 1) / ept + 31) / 32 * 32;
+  int per = block_rows_per_sm(threads, (size_t)3 * threads * ept * sizeof(float));
+  if (per < wide_per_sm(wide_threads(d))) per = wide_per_sm(wide_threads(d));
   const int64_t cap = (int64_t)per * sms;
   return (int)(n < cap ? (n < 1 ? 1 : n) : cap);
 }
@@ -576,57 +1045,112 @@ int fwd_warp(const NormFwd& p, cudaStream_t s) {
   constexpr int rows = kNormThreads / G;
   const int64_t want = (p.n + rows - 1) / rows;
   const int cap = 8 * sm_count();
-  norm_fwd_warp_kernel<T, V, NV, G><<<(int)(want < cap ? want : cap), kNormThreads, 0, s>>>(p);
+  const int grid = (int)(want < cap ? want : cap);
+  if (V > 1 && p.d == G * NV * V)
+    norm_fwd_warp_kernel<T, V, NV, G, true><<<grid, kNormThreads, 0, s>>>(p);
+  else
+    norm_fwd_warp_kernel<T, V, NV, G, false><<<grid, kNormThreads, 0, s>>>(p);
   return launch_status();
 }
 
 template <typename T, int V>
 int fwd_any(const NormFwd& p, cudaStream_t s) {
-  if (p.d <= 8 * V) return fwd_warp<T, V, 1, 8>(p, s);
-  if (p.d <= 16 * V) return fwd_warp<T, V, 1, 16>(p, s);
-  if (p.d <= 32 * V) return fwd_warp<T, V, 1, 32>(p, s);
-  if (p.d <= 64 * V) return fwd_warp<T, V, 2, 32>(p, s);
-  if constexpr (V <= 4) {
-    if (p.d <= 128 * V) return fwd_warp<T, V, 4, 32>(p, s);
-  }
   if constexpr (V == 1) {
-    if (p.d <= 512) return fwd_warp<T, V, 16, 32>(p, s);
+    if (p.d <= 64) return fwd_warp<T, 1, 2, 32>(p, s);
+    if (p.d <= 128) return fwd_warp<T, 1, 4, 32>(p, s);
+    if (p.d <= 256) return fwd_warp<T, 1, 8, 32>(p, s);
+    if (p.d <= 384) return fwd_warp<T, 1, 12, 32>(p, s);
+    if (p.d <= 512) return fwd_warp<T, 1, 16, 32>(p, s);
+  } else {
+    if (p.d <= 8 * V) return fwd_warp<T, V, 1, 8>(p, s);
+    if (p.d <= 16 * V) return fwd_warp<T, V, 1, 16>(p, s);
+    if (p.d <= 32 * V) return fwd_warp<T, V, 1, 32>(p, s);
+    if (p.d <= 64 * V) return fwd_warp<T, V, 2, 32>(p, s);
+    if constexpr (V == 4)
+      if (p.d <= 128 * V) return fwd_warp<T, V, 4, 32>(p, s);
   }
   const int threads = ((p.d + kEpt - 1) / kEpt + 31) / 32 * 32;
-  const int64_t cap = (int64_t)sm_count() * (2048 / threads);
-  norm_fwd_block_kernel<T, V><<<(int)(p.n < cap ? p.n : cap), threads, 0, s>>>(p);
+  const size_t smem = (size_t)2 * threads * kEpt * sizeof(float);
+  const int64_t cap = (int64_t)sm_count() * block_rows_per_sm(threads, smem);
+  const int grid = (int)(p.n < cap ? p.n : cap);
+  GQ_TRY_CUDA(cudaFuncSetAttribute(norm_fwd_block_kernel<T, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   2 * kMaxWidth * (int)sizeof(float)));
+  norm_fwd_block_kernel<T, V><<<grid, threads, smem, s>>>(p);
   return launch_status();
 }
 
 template <typename T, typename TO, int V, int NV, int G>
-int bwd_warp(const NormBwd& p, int blocks, cudaStream_t s) {
-  const size_t smem = (size_t)(kNormThreads / 32) * 2 * G * NV * V * sizeof(float);
-  norm_bwd_warp_kernel<T, TO, V, NV, G><<<blocks, kNormThreads, smem, s>>>(p);
+int bwd_warp(const NormBwd& p, int& blocks, cudaStream_t s) {
+  constexpr int kWarps = kNormThreads / 32;
+  // resident blocks per SM, by the registers the lane's elements take
+  constexpr int E = NV * V;
+  constexpr int kPer = V > 1 ? (E <= 4 ? 4 : E <= 8 ? 3 : 2) : (E <= 2 ? 4 : E <= 4 ? 3 : E <= 12 ? 2 : 1);
+  if (blocks > kPer * sm_count()) blocks = kPer * sm_count();
+  const size_t sums = (size_t)kWarps * 2 * G * NV * V * sizeof(float);
+  if constexpr (V > 1) {
+    constexpr int S = NV > 2 ? 3 : 4;
+    const size_t ring = (size_t)kWarps * S * 2 * NV * 32 * 16;
+    const size_t smem = ring > sums ? ring : sums;
+    GQ_TRY_CUDA(cudaFuncSetAttribute(norm_bwd_ring_kernel<T, TO, V, NV, G, S>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    norm_bwd_ring_kernel<T, TO, V, NV, G, S><<<blocks, kNormThreads, smem, s>>>(p);
+  } else {
+    norm_bwd_warp_kernel<T, TO, V, NV, G><<<blocks, kNormThreads, sums, s>>>(p);
+  }
   return launch_status();
 }
 
+template <typename T, typename TO, int V, int MAXT, int MINB>
+int bwd_wide(const NormBwd& p, int blocks, int threads, cudaStream_t s) {
+  constexpr int S = 3;
+  constexpr int kBytes = S * 2 * (kEpt / V) * 16 + kEpt * (int)sizeof(float);  // per thread
+  auto kernel = norm_bwd_wide_kernel<T, TO, V, S, MAXT, MINB>;
+  GQ_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAXT * kBytes));
+  kernel<<<blocks, threads, threads * kBytes, s>>>(p);
+  return launch_status();
+}
+
+// `blocks`: at most this many, on return the number launched
 template <typename T, typename TO, int V>
-int bwd_any(const NormBwd& p, int blocks, cudaStream_t s) {
-  if (p.d <= 8 * V) return bwd_warp<T, TO, V, 1, 8>(p, blocks, s);
-  if (p.d <= 16 * V) return bwd_warp<T, TO, V, 1, 16>(p, blocks, s);
-  if (p.d <= 32 * V) return bwd_warp<T, TO, V, 1, 32>(p, blocks, s);
-  if (p.d <= 64 * V) return bwd_warp<T, TO, V, 2, 32>(p, blocks, s);
-  if constexpr (V <= 4) {
-    if (p.d <= 128 * V) return bwd_warp<T, TO, V, 4, 32>(p, blocks, s);
-  }
+int bwd_any(const NormBwd& p, int& blocks, cudaStream_t s) {
   if constexpr (V == 1) {
-    if (p.d <= 512) return bwd_warp<T, TO, V, 16, 32>(p, blocks, s);
+    if (p.d <= 64) return bwd_warp<T, TO, 1, 2, 32>(p, blocks, s);
+    if (p.d <= 128) return bwd_warp<T, TO, 1, 4, 32>(p, blocks, s);
+    if (p.d <= 256) return bwd_warp<T, TO, 1, 8, 32>(p, blocks, s);
+    if (p.d <= 384) return bwd_warp<T, TO, 1, 12, 32>(p, blocks, s);
+    if (p.d <= 512) return bwd_warp<T, TO, 1, 16, 32>(p, blocks, s);
+  } else {
+    if (p.d <= 8 * V) return bwd_warp<T, TO, V, 1, 8>(p, blocks, s);
+    if (p.d <= 16 * V) return bwd_warp<T, TO, V, 1, 16>(p, blocks, s);
+    if (p.d <= 32 * V) return bwd_warp<T, TO, V, 1, 32>(p, blocks, s);
+    if (p.d <= 64 * V) return bwd_warp<T, TO, V, 2, 32>(p, blocks, s);
+    if constexpr (V == 4)
+      if (p.d <= 128 * V) return bwd_warp<T, TO, V, 4, 32>(p, blocks, s);
   }
-  const int threads = ((p.d + kEpt - 1) / kEpt + 31) / 32 * 32;
-  const size_t smem = (size_t)2 * threads * kEpt * sizeof(float);
-  GQ_TRY_CUDA(cudaFuncSetAttribute(norm_bwd_block_kernel<T, TO, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   2 * kMaxWidth * (int)sizeof(float)));
-  norm_bwd_block_kernel<T, TO, V><<<blocks, threads, smem, s>>>(p);
+  if constexpr (V > 1) {
+    if (p.d <= 512 * kEpt) {
+      const int threads = wide_threads(p.d), cap = wide_per_sm(threads) * sm_count();
+      if (blocks > cap) blocks = cap;
+      return threads <= 288 ? bwd_wide<T, TO, V, 288, 2>(p, blocks, threads, s)
+                            : bwd_wide<T, TO, V, 512, 1>(p, blocks, threads, s);
+    }
+  }
+  const int ept = bwd_ept(p.d), threads = ((p.d + ept - 1) / ept + 31) / 32 * 32;
+  const size_t smem = (size_t)3 * threads * ept * sizeof(float);
+  if (ept == 8) {
+    GQ_TRY_CUDA(cudaFuncSetAttribute(norm_bwd_block_kernel<T, TO, V, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     3 * 8192 * (int)sizeof(float)));
+    norm_bwd_block_kernel<T, TO, V, 8><<<blocks, threads, smem, s>>>(p);
+  } else {
+    GQ_TRY_CUDA(cudaFuncSetAttribute(norm_bwd_block_kernel<T, TO, V, 16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     3 * kMaxWidth * (int)sizeof(float)));
+    norm_bwd_block_kernel<T, TO, V, 16><<<blocks, threads, smem, s>>>(p);
+  }
   return launch_status();
 }
 
 template <typename T, typename TO>
-int bwd_typed(const NormBwd& p, int blocks, bool vec, cudaStream_t s) {
+int bwd_typed(const NormBwd& p, int& blocks, bool vec, cudaStream_t s) {
   return vec ? bwd_any<T, TO, 16 / sizeof(T)>(p, blocks, s) : bwd_any<T, TO, 1>(p, blocks, s);
 }
 
@@ -673,7 +1197,7 @@ extern "C" int gq_layer_norm_fwd(const void* X, int type, int64_t n, int d, int6
   a.gamma = gamma;
   a.beta = beta;
   a.eps = eps;
-  a.fd = (float)d;
+  a.dv = {(float)d, 1.0f / (float)d};
   a.relu = act == GQ_ACT_RELU;
   a.Y = Y;
   a.ldy = ldy;
@@ -728,7 +1252,7 @@ extern "C" int gq_layer_norm_bwd(const void* dY, int64_t lddy, const void* X, in
   a.lddy = lddy;
   a.ldx = ldx;
   a.d = d;
-  a.fd = (float)d;
+  a.dv = {(float)d, 1.0f / (float)d};
   a.mean = mean;
   a.rstd = rstd;
   a.gamma = gamma;
@@ -742,7 +1266,7 @@ extern "C" int gq_layer_norm_bwd(const void* dY, int64_t lddy, const void* X, in
   // bytes of one stored vector: 16 in the inputs' type, 8 for fp32 -> bf16
   const int ob = type_bytes(dx_type) * 16 / esz;
   a.vec_out = aligned(dX, ob) && lddx * type_bytes(dx_type) % ob == 0;
-  const int blocks = bwd_blocks(n, d);
+  int blocks = bwd_blocks(n, d);
   if (type == GQ_F32 && dx_type == GQ_BF16)
     GQ_TRY((bwd_typed<float, __nv_bfloat16>(a, blocks, vec, s)));
   else if (type == GQ_F32)

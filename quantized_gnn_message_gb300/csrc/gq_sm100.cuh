@@ -1,6 +1,7 @@
 // gq_sm100.cuh -- inline-PTX wrappers for the Blackwell (sm_100 family)
 // asynchronous machinery used by the GEMM kernels: mbarriers, TMA tensor
-// loads, tcgen05 tensor-memory allocation, MMA, commit and loads.
+// loads, tcgen05 tensor-memory allocation, MMA, commit and loads; packed
+// fp32 arithmetic.
 //
 // Every wait is bounded: mbar_wait gives up after ~`kWaitCycles` SM cycles,
 // raises a block-wide abort flag and reports failure, so a kernel that
@@ -181,6 +182,31 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// ---- packed fp32 ------------------------------------------------------------
+// Two fp32 operations at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
+        "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
 
 // ---- descriptors -----------------------------------------------------------
 // Shared-memory matrix descriptor (tcgen05): start address, leading and
