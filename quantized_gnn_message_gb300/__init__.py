@@ -9,6 +9,7 @@ data_ptr(), and every call runs on torch.cuda.current_stream().
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -461,6 +462,14 @@ def _typed(t, name):
     return _TYPES[t.dtype]
 
 
+def _on(device):
+    """The device's guard: nothing to do where it is the current one."""
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+_HERE = contextlib.nullcontext()
+
+
 def _like(t, ref, name, dtypes=None):
     """t is a matrix of ref's shape and device, in one of dtypes (ref's)."""
     if t.shape != ref.shape or t.device != ref.device or t.dtype not in (dtypes or (ref.dtype,)):
@@ -488,6 +497,10 @@ def _vec32(t, count, ref, name):
     return t
 
 
+def _new32(count, ref):
+    return torch.empty(count, dtype=torch.float32, device=ref.device)
+
+
 def _bits32(t, ref):
     """t (or None) holds the ReLU bits of ref's rows."""
     if t is not None:
@@ -506,7 +519,7 @@ def dropout(X: torch.Tensor, p: float, seed: int, out: torch.Tensor | None = Non
     ldx = _rows(X)
     out = _rows_like(X) if out is None else _like(out, X, "out")
     n, d = X.shape
-    with torch.cuda.device(X.device):
+    with _on(X.device):
         _check(lib().gq_dropout(_ptr(X), ty, n, d, ldx, p, seed & 0xFFFFFFFFFFFFFFFF, _ptr(out), _rows(out),
                                 _stream()), "gq_dropout")
     return out
@@ -523,13 +536,12 @@ def layer_norm_fwd(X: torch.Tensor, gamma: torch.Tensor | None = None, beta: tor
     ldx = _rows(X)
     n, d = X.shape
     out = _rows_like(X) if out is None else _like(out, X, "out")
-    if mean is None:
-        mean = torch.empty(n, dtype=torch.float32, device=X.device)
-    if rstd is None:
-        rstd = torch.empty(n, dtype=torch.float32, device=X.device)
-    _vec32(gamma, d, X, "gamma"), _vec32(beta, d, X, "beta"), _vec32(mean, n, X, "mean"), _vec32(rstd, n, X, "rstd")
+    mean = _new32(n, X) if mean is None else _vec32(mean, n, X, "mean")
+    rstd = _new32(n, X) if rstd is None else _vec32(rstd, n, X, "rstd")
+    _vec32(gamma, d, X, "gamma")
+    _vec32(beta, d, X, "beta")
     _bits32(relu_bits, X)
-    with torch.cuda.device(X.device):
+    with _on(X.device):
         _check(lib().gq_layer_norm_fwd(_ptr(X), ty, n, d, ldx, _ptr(gamma), _ptr(beta), eps, act, p,
                                        seed & 0xFFFFFFFFFFFFFFFF, _ptr(out), _rows(out), _ptr(mean), _ptr(rstd),
                                        _ptr(relu_bits), _rows(relu_bits) if relu_bits is not None else 0, _stream()),
@@ -551,17 +563,16 @@ def layer_norm_bwd(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rstd: 
     _like(dY, X, "dY")
     if dX is None:
         dX = _rows_like(X)
-    _like(dX, X, "dX", (torch.float32, torch.bfloat16) if X.dtype == torch.float32 else None)
-    if dgamma is None:
-        dgamma = torch.empty(d, dtype=torch.float32, device=X.device)
-    if dbeta is None:
-        dbeta = torch.empty(d, dtype=torch.float32, device=X.device)
-    for t, c, name in ((mean, n, "mean"), (rstd, n, "rstd"), (gamma, d, "gamma"), (dgamma, d, "dgamma"),
-                       (dbeta, d, "dbeta")):
-        _vec32(t, c, X, name)
+    else:
+        _like(dX, X, "dX", (torch.float32, torch.bfloat16) if X.dtype == torch.float32 else None)
+    dgamma = _new32(d, X) if dgamma is None else _vec32(dgamma, d, X, "dgamma")
+    dbeta = _new32(d, X) if dbeta is None else _vec32(dbeta, d, X, "dbeta")
+    _vec32(mean, n, X, "mean")
+    _vec32(rstd, n, X, "rstd")
+    _vec32(gamma, d, X, "gamma")
     _bits32(relu_bits, X)
     L = lib()
-    with torch.cuda.device(X.device):
+    with _on(X.device):
         wb = int(L.gq_layer_norm_bwd_workspace_bytes(n, d))
         buf = ws.get(wb) if ws is not None else torch.empty(wb, dtype=torch.uint8, device=X.device)
         _check(L.gq_layer_norm_bwd(_ptr(dY), _rows(dY), _ptr(X), ldx, ty, n, d, _ptr(mean), _ptr(rstd), _ptr(gamma),
@@ -575,6 +586,12 @@ def layer_norm_bwd(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rstd: 
 # --------------------------------------------------------------------------
 # class head
 # --------------------------------------------------------------------------
+
+def _rows8(rows, k, dev):
+    """A new bf16 matrix with a leading dimension that is a multiple of 8."""
+    t = torch.empty(rows, _round8(k), dtype=torch.bfloat16, device=dev)
+    return t if k % 8 == 0 else t[:, :k]
+
 
 def linear_xent(X: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, weight: torch.Tensor | None = None,
                 scale: float = 1.0, grad: bool = True, loss: torch.Tensor | None = None,
@@ -596,16 +613,14 @@ def linear_xent(X: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, weight: 
     if labels.shape != (n,) or not labels.is_contiguous() or labels.device != X.device:
         raise GQError(f"labels must be a contiguous int32 vector of {n} values on {X.device}")
     dev = X.device
-    new = lambda rows: torch.empty(rows, _round8(k), dtype=torch.bfloat16, device=dev)[:, :k]
-    if loss is None:
-        loss = torch.empty(n, dtype=torch.float32, device=dev)
-    for t, name in ((weight, "weight"), (loss, "loss"), (lse, "lse")):
-        _vec32(t, n, X, name)
+    loss = _new32(n, X) if loss is None else _vec32(loss, n, X, "loss")
+    _vec32(weight, n, X, "weight")
+    _vec32(lse, n, X, "lse")
     need_dX, need_dW = grad and need_dX, grad and need_dW
-    dX = (_like(dX, X, "dX") if dX is not None else new(n)) if need_dX else None
-    dW = (_like(dW, W, "dW") if dW is not None else new(C)) if need_dW else None
+    dX = (_like(dX, X, "dX") if dX is not None else _rows8(n, k, dev)) if need_dX else None
+    dW = (_like(dW, W, "dW") if dW is not None else _rows8(C, k, dev)) if need_dW else None
     L = lib()
-    with torch.cuda.device(dev):
+    with _on(dev):
         wb = int(L.gq_linear_xent_workspace_bytes(n, k, C, int(need_dX or need_dW)))
         buf = ws.get(wb) if ws is not None else torch.empty(wb, dtype=torch.uint8, device=dev)
         _check(L.gq_linear_xent(_ptr(X), n, k, _ld_bf16(X), _ptr(W), C, _ld_bf16(W), _ptr(labels), _ptr(weight), scale,

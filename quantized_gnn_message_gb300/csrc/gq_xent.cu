@@ -13,6 +13,8 @@
 //   STATS  Z tile -> running maximum and sum of exponentials per row and run
 //          of class tiles
 //   GRAD   Z tile again -> G of one piece of the classes, in bf16
+//   WHOLE  STATS and GRAD of a tile that holds every class (C <= 256): the
+//          logits are read twice from TMEM, and nothing is recomputed
 //   DX     dX += G W over the piece (fp32 sums between pieces)
 //   DW     dW of the piece's classes = G^T X
 // 8 n k C operations where keeping all of Z (4 n C bytes) would need 6.  One
@@ -61,6 +63,7 @@ namespace {
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarps + 3);  // TMA, MMA, epilogue, scheduler
 constexpr int kParts = kEpiWarps / 4;           // warps that share a row's columns
+static_assert(kParts == 2, "a WHOLE tile's rows are exchanged between two warps");
 constexpr int kStages = 5;
 constexpr int kStageA = 128 * 128;                    // 128 rows x 64 bf16 (or 2 x 64 x 64)
 constexpr int kStageBytes = 2 * kStageA;
@@ -73,7 +76,7 @@ constexpr int kTile = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-enum Mode { STATS, GRAD, DX, DW };
+enum Mode { STATS, GRAD, WHOLE, DX, DW };
 
 struct Maps {
   CUtensorMap xk[2], xm[2];  // X: [0] as given, [1] the copied labelled rows; K-major / MN-major boxes
@@ -95,6 +98,12 @@ struct Args {
   int dxs, dws;          // splits of their sums
   int first, last;       // the piece read is the first / last one
   float scale;           // of the results: G is formed without it, see below
+  int full;              // the tiles of gtiles are WHOLE (1: losses only, 2: G too)
+  const float* zlab;     // per labelled row, for WHOLE: logit and weight, label, row of X
+  const float* wrow;
+  const int* lab;
+  float* loss;           // per row of X, nullable
+  float* lse;
   const float4* row;     // r, weight / sum of 2^(z L - r), G of the label, label (as int)
   const int* idx;        // labelled row -> row of X
   float2* part;          // [unit * kParts + part][npad]: r, sum
@@ -275,7 +284,7 @@ __device__ __forceinline__ bool get_tile(const Args& p, const Plan& q, int64_t u
     t.ct = c * p.stats_run + sub;
     return sub < p.stats_run && t.ct < p.stats_tiles;
   }
-  t.mode = GRAD;
+  t.mode = p.full ? WHOLE : GRAD;
   t.ct = c;
   return sub == 0;
 }
@@ -338,11 +347,37 @@ __device__ __forceinline__ void online(float (&v)[32], int limit, float& r, floa
   r = rn;
 }
 
+// A row's values from its (r, sum) pairs, joined in order: the loss is taken
+// from the label's logit zlab in the form the sum has it, z L - r.
+struct RowNorm {
+  float ref, ws, glab, loss, lse;  // r; weight / sum; G of the label
+};
+__device__ __forceinline__ RowNorm norm_of(float ref, float s, float zlab, float weight) {
+  RowNorm f;
+  const float l2 = log2f(s), zl = __fmaf_rn(zlab, kLog2e, -ref);
+  f.ref = ref;
+  f.ws = weight / s;
+  f.glab = __fmaf_rn(ex2(zl), f.ws, -weight);
+  f.loss = kLn2 * (l2 - zl);
+  f.lse = __fmaf_rn(ref, kLn2, l2 * kLn2);
+  return f;
+}
+__device__ __forceinline__ RowNorm finish_row(float r, float2 lo, float2 hi, float zlab, float weight) {
+  const float ref = r == neg_inf() ? 0.0f : r;
+  return norm_of(ref, lo.y * ex2(lo.x - ref) + hi.y * ex2(hi.x - ref), zlab, weight);
+}
+
 // entry j of a lane's 128-byte row of a G box
 __device__ __forceinline__ void put_box(uint8_t* row, int lane, unsigned j, __nv_bfloat16 v) {
   *reinterpret_cast<__nv_bfloat16*>(row + 16 * ((j >> 3) ^ (lane & 7)) + 2 * (j & 7)) = v;
 }
 
+// Instantiated for the kinds of tiles a launch can hold, since the code of
+// the others would cost instruction fetches (STATS of 16,384 x 256 x 131,072:
+// 0.83 ms with all in one kernel).
+enum Kind { LOSSES, PIECE, ONE_TILE };  // STATS | GRAD, DX, DW | WHOLE
+
+template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     xent_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args p) {
   extern __shared__ uint8_t smem_raw[];
@@ -354,7 +389,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* tempty = tfull + 2;
   uint64_t* ufull = tempty + 2;
   uint64_t* uempty = ufull + kSlots;
-  int* unit = reinterpret_cast<int*>(uempty + kSlots);
+  uint64_t* pair = uempty + kSlots;  // of the two warps that share 32 rows
+  int* unit = reinterpret_cast<int*>(pair + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(unit + kSlots);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -373,6 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&ufull[s], 1);
       mbar_init(&uempty[s], kConsumers);
     }
+    for (int j = 0; j < 4; ++j) mbar_init(&pair[j], kParts);
     *abort = 0;
     fence_barrier_init();
   }
@@ -408,7 +445,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t bar = mapa(smem_u32(&full[stage]), 0);
             if (cr == 0) mbar_expect_tx(&full[stage], 2 * bytes);
             const int x = (t.s0 + s) * 64;
-            if (t.mode <= GRAD) {
+            if (KIND != PIECE || t.mode <= WHOLE) {
               const int c0 = (t.mode == STATS ? 0 : p.gc0) + t.ct * p.NT;
               tma_load_pair(a, xk, x, t.rt * kTile + cr * 128, bar);
               tma_load_pair(b, &maps.wk, x, c0 + cr * hn, bar);
@@ -446,7 +483,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!(ok = wait(&tempty[a], ((i >> 1) & 1) ^ 1, abort, p.err, 23))) break;
           tc_fence_after();
           const uint32_t d = tmem + a * 256;
-          const int amn = t.mode == DW, bmn = t.mode >= DX;
+          const int amn = KIND == PIECE && t.mode == DW, bmn = KIND == PIECE && t.mode >= DX;
           const uint32_t idesc = idesc_bf16_f32(256, t.N, amn, bmn);
           // 16 contraction elements further: 32 bytes along a K-major row,
           // two 8-row swizzle atoms in an MN-major block
@@ -483,18 +520,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     float4 rwn;
     auto fetch = [&]() {
       if (lane == 0) un = feed.next(abort, p.err, q.units);
-      un = __shfl_sync(FULL, un, 0);
+      un = __shfl_sync(gq::FULL, un, 0);
       rwn = make_float4(0.0f, 0.0f, 0.0f, __int_as_float(-1));
       if (un < 0) return;
       Tile t;
       get_tile(p, q, un, 0, t);
       const int row = t.rt * kTile + rit;
-      if (t.mode == GRAD && row < q.nl) rwn = p.row[row];
+      if (row < q.nl) {
+        if (KIND == PIECE && t.mode == GRAD) rwn = p.row[row];
+        if (KIND == ONE_TILE)
+          rwn = make_float4(p.zlab[row], p.wrow[row], __int_as_float(p.idx[row]), __int_as_float(p.lab[row]));
+      }
     };
     fetch();
     while (ok && un >= 0) {
       const int u = un;
-      const float4 rw = rwn;
+      float4 rw = rwn;
       fetch();
       Tile t;
       float m = neg_inf(), sum = 0.0f;
@@ -503,11 +544,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int a = i & 1;
         int got = 1;
         if (lane == 0) got = wait(&tfull[a], (i >> 1) & 1, abort, p.err, 25);
-        ok = __shfl_sync(FULL, got, 0) != 0;
+        ok = __shfl_sync(gq::FULL, got, 0) != 0;
         if (!ok) break;
         tc_fence_after();
         const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + a * 256;
-        if (t.mode == STATS) {
+        if (KIND != PIECE) {
           for (int c = part * 32; c < t.N; c += 32 * kParts) {
             float v[32];
             tmem_ld32(taddr + c, v);
@@ -515,7 +556,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int c0 = t.ct * p.NT + c;  // class of v[0]
             if (c0 < p.C) online(v, p.C - c0, m, sum);
           }
-        } else if (t.mode == GRAD) {
+        }
+        if (KIND == ONE_TILE) {
+          // the two warps of these rows exchange their halves: posted, read,
+          // and read by both before the staging is used again
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+          reinterpret_cast<float2*>(stg)[lane] = make_float2(m, sum);
+          __syncwarp();
+          int met = 1;
+          if (lane == 0) {
+            mbar_arrive(&pair[quarter]);
+            met = wait(&pair[quarter], 0, abort, p.err, 27);
+          }
+          ok = __shfl_sync(gq::FULL, met, 0) != 0;
+          if (!ok) break;
+          const float2 o = reinterpret_cast<const float2*>(stg_all + ((warp - 2) ^ 4) * kStg)[lane];
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&pair[quarter]);
+            met = wait(&pair[quarter], 1, abort, p.err, 28);
+          }
+          ok = __shfl_sync(gq::FULL, met, 0) != 0;
+          if (!ok) break;
+          const float2 lo = part == 0 ? make_float2(m, sum) : o, hi = part == 0 ? o : make_float2(m, sum);
+          const RowNorm f = finish_row(fmaxf(lo.x, hi.x), lo, hi, rw.x, rw.y);
+          if (part == 0 && srow < q.nl) {
+            const int to = __float_as_int(rw.z);
+            if (p.loss != nullptr) p.loss[to] = f.loss;
+            if (p.lse != nullptr) p.lse[to] = f.lse;
+          }
+          rw = make_float4(f.ref, f.ws, f.glab, rw.w);
+          if (srow >= q.nl) rw = make_float4(0.0f, 0.0f, 0.0f, rw.w);
+          m = neg_inf();
+          sum = 0.0f;
+        }
+        if ((KIND == PIECE && t.mode == GRAD) || (KIND == ONE_TILE && p.full == 2)) {
           for (int b = part * 64; b < t.N; b += 64 * kParts) {
             // a box of 32 rows x 64 classes, 128 bytes a row (128-byte
             // swizzle: 16-byte piece j of row `lane` at j ^ (lane & 7))
@@ -564,7 +640,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             ++nbox;
           }
-        } else {
+        }
+        if (KIND == PIECE && t.mode >= DX) {
           const bool dw = t.mode == DW;
           // fp32 sums that other pieces or splits add to, else the result
           const bool sums = dw ? p.dws > 1 : p.dxs > 1 || !p.last;
@@ -619,7 +696,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int it = 0; it < 4; ++it) {
               const int rr = it * 8 + (lane >> 2), j = lane & 3;
               const uint4 o = *reinterpret_cast<const uint4*>(stg + rr * 64 + 16 * (j ^ ((rr >> 1) & 3)));
-              const int64_t to = __shfl_sync(FULL, orow, rr);
+              const int64_t to = __shfl_sync(gq::FULL, orow, rr);
               if (to < 0) continue;
               const int col = k0 + 8 * j;
               __nv_bfloat16* dst = out + to * ldo + col;
@@ -638,7 +715,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_cluster(tempty0 + a * 8);
-        if (t.mode == STATS && (sub + 1 == p.stats_run || t.ct + 1 == p.stats_tiles))
+        if (KIND == LOSSES && (sub + 1 == p.stats_run || t.ct + 1 == p.stats_tiles))
           p.part[(int64_t)(t.ct / p.stats_run * kParts + part) * p.npad + srow] = make_float2(m, sum);
       }
     }
@@ -687,7 +764,7 @@ __global__ void __launch_bounds__(kScanThreads) xent_count_kernel(const int* __r
   const int64_t e = min(n, (blockIdx.x + 1) * seg);
   int c = 0;
   for (int64_t r = blockIdx.x * seg + threadIdx.x; r < e; r += kScanThreads) c += labelled(labels[r], C);
-  c = __reduce_add_sync(FULL, c);
+  c = __reduce_add_sync(gq::FULL, c);
   if ((threadIdx.x & 31) == 0) atomicAdd(&s, c);  // integers: the order does not matter
   __syncthreads();
   if (threadIdx.x == 0) cnt[blockIdx.x] = s;
@@ -716,7 +793,7 @@ __global__ void __launch_bounds__(kScanThreads)
   if (blockIdx.x > 0) {
     int c = 0;
     for (int b = threadIdx.x; b < (int)blockIdx.x; b += kScanThreads) c += cnt[b];
-    c = __reduce_add_sync(FULL, c);
+    c = __reduce_add_sync(gq::FULL, c);
     if (lane == 0) atomicAdd(&base, c);
     __syncthreads();
   } else {
@@ -728,12 +805,12 @@ __global__ void __launch_bounds__(kScanThreads)
     const int64_t r = r0 + threadIdx.x;
     const int y = r < e ? labels[r] : -1;
     const bool on = labelled(y, C);
-    const unsigned bal = __ballot_sync(FULL, on);
+    const unsigned bal = __ballot_sync(gq::FULL, on);
     if (lane == 0) ws[warp] = __popc(bal);
     __syncthreads();
     const int mine = ws[lane];
-    const int before = __reduce_add_sync(FULL, lane < warp ? mine : 0);
-    const int all = __reduce_add_sync(FULL, mine);
+    const int before = __reduce_add_sync(gq::FULL, lane < warp ? mine : 0);
+    const int all = __reduce_add_sync(gq::FULL, mine);
     if (r < e) {
       const int to = on ? at + before + __popc(bal & ((1u << lane) - 1)) : -1;
       o.pos[r] = to;
@@ -752,7 +829,7 @@ __global__ void __launch_bounds__(kScanThreads)
   if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) *o.nl = at;
 }
 
-// Per row of X, a warp: the label's logit x . w_y; the labelled rows copied
+// Per row of X: the label's logit x . w_y; the labelled rows copied
 // together (zeros up to a multiple of 256 rows) and zeros in the other rows
 // of dX, unless every row is labelled.  The label's logit costs one gathered
 // row of W here; picked out of the STATS tiles it cost 16% of their time.
@@ -760,56 +837,62 @@ __global__ void __launch_bounds__(256)
     xent_rows_kernel(const __nv_bfloat16* __restrict__ X, int64_t n, int k, int64_t ldx,
                      const __nv_bfloat16* __restrict__ W, int64_t ldw, const int* __restrict__ labels,
                      const int* __restrict__ pos, const int* __restrict__ nl, float* zlab, __nv_bfloat16* Xc,
-                     int64_t ldc, __nv_bfloat16* dX, int64_t lddx) {
+                     int64_t ldc, __nv_bfloat16* dX, int64_t lddx, int per_warp) {
   const int m = *nl;
   const bool all = m == n;
   const int lane = threadIdx.x & 31;
-  const int64_t step = (int64_t)gridDim.x * 8;
-  for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < n + kTile; r += step) {
-    if (r >= n || pos[r] < 0) {  // zeros
-      const int64_t pad = m + (r - n);
-      __nv_bfloat16* dst = nullptr;
-      if (r >= n) dst = !all && pad < (m + kTile - 1) / kTile * (int64_t)kTile ? Xc + pad * ldc : nullptr;
-      else if (dX != nullptr) dst = dX + r * lddx;
+  const int64_t pad_end = all ? n : n + ((m + kTile - 1) / kTile * (int64_t)kTile - m);  // rows of zeros behind Xc
+  const int64_t step = (int64_t)gridDim.x * 8 * per_warp;
+  for (int64_t r0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * per_warp; r0 < pad_end; r0 += step) {
+    // per_warp rows (at most 32) of a warp, their places read at once
+    const int64_t mine = r0 + lane;
+    const int at = lane < per_warp && mine < n ? pos[mine] : -1;
+    const unsigned on = __ballot_sync(gq::FULL, at >= 0);
+    for (int i = 0; i < per_warp && r0 + i < pad_end; ++i) {  // zeros
+      const int64_t r = r0 + i;
+      if (on >> i & 1) continue;
+      __nv_bfloat16* dst = r >= n ? Xc + (m + (r - n)) * ldc : dX != nullptr ? dX + r * lddx : nullptr;
       if (dst == nullptr) continue;
       for (int c = lane * 8; c < k; c += 256) {
         if (c + 8 <= k) *reinterpret_cast<uint4*>(dst + c) = make_uint4(0, 0, 0, 0);
         else
           for (int j = c; j < k; ++j) dst[j] = __float2bfloat16_rn(0.0f);
       }
-      continue;
     }
-    const int to = pos[r];
-    const __nv_bfloat16* x = X + r * ldx;
-    const __nv_bfloat16* w = W + (int64_t)labels[r] * ldw;
-    __nv_bfloat16* dst = all ? nullptr : Xc + (int64_t)to * ldc;
-    float z = 0.0f;
-    for (int c = lane * 8; c < k; c += 256) {
-      if (c + 8 <= k) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + c)), b = __ldg(reinterpret_cast<const uint4*>(w + c));
-        const uint32_t au[4] = {a.x, a.y, a.z, a.w}, bu[4] = {b.x, b.y, b.z, b.w};
+    for (unsigned left = on; left != 0; left &= left - 1) {
+      const int i = __ffs(left) - 1;
+      const int64_t r = r0 + i;
+      const int to = __shfl_sync(gq::FULL, at, i);
+      const __nv_bfloat16* x = X + r * ldx;
+      const __nv_bfloat16* w = W + (int64_t)labels[r] * ldw;
+      __nv_bfloat16* dst = all ? nullptr : Xc + (int64_t)to * ldc;
+      float z = 0.0f;
+      for (int c = lane * 8; c < k; c += 256) {
+        if (c + 8 <= k) {
+          const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + c)), b = __ldg(reinterpret_cast<const uint4*>(w + c));
+          const uint32_t au[4] = {a.x, a.y, a.z, a.w}, bu[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {  // bf16 is the upper half of an fp32
-          z = __fmaf_rn(__uint_as_float(au[j] << 16), __uint_as_float(bu[j] << 16), z);
-          z = __fmaf_rn(__uint_as_float(au[j] & 0xffff0000u), __uint_as_float(bu[j] & 0xffff0000u), z);
-        }
-        if (dst != nullptr) *reinterpret_cast<uint4*>(dst + c) = a;
-      } else {
-        for (int j = c; j < k; ++j) {
-          z = __fmaf_rn(__bfloat162float(x[j]), __bfloat162float(w[j]), z);
-          if (dst != nullptr) dst[j] = x[j];
+          for (int j = 0; j < 4; ++j) {  // bf16 is the upper half of an fp32
+            z = __fmaf_rn(__uint_as_float(au[j] << 16), __uint_as_float(bu[j] << 16), z);
+            z = __fmaf_rn(__uint_as_float(au[j] & 0xffff0000u), __uint_as_float(bu[j] & 0xffff0000u), z);
+          }
+          if (dst != nullptr) *reinterpret_cast<uint4*>(dst + c) = a;
+        } else {
+          for (int j = c; j < k; ++j) {
+            z = __fmaf_rn(__bfloat162float(x[j]), __bfloat162float(w[j]), z);
+            if (dst != nullptr) dst[j] = x[j];
+          }
         }
       }
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(FULL, z, o);
-    if (lane == 0) zlab[to] = z;
+      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(gq::FULL, z, o);
+      if (lane == 0) zlab[to] = z;
+    }
   }
 }
 
 // lse and loss of 32 labelled rows per block from the runs' (r, sum) pairs:
-// 32 lanes of runs per row, joined in lane order.  The loss is taken from
-// the label's logit in the form the sum has it, z L - r.
+// 32 lanes of runs per row, joined in lane order.
 __global__ void __launch_bounds__(1024)
     xent_join_kernel(const float2* __restrict__ part, int runs, int64_t npad, const int* __restrict__ nl,
                      const int* __restrict__ idx, const float* __restrict__ zlab, const float* __restrict__ wrow,
@@ -834,28 +917,25 @@ __global__ void __launch_bounds__(1024)
       const float ref = r == neg_inf() ? 0.0f : r;
       s = 0.0f;
       for (int j = 0; j < 32; ++j) s += ss[j][lane] * ex2(sm[j][lane] - ref);
-      const float l2 = log2f(s);
-      const float zl = __fmaf_rn(zlab[row], kLog2e, -ref);
-      if (rowinfo != nullptr) {
-        const float wr = wrow[row], ws = wr / s;
-        rowinfo[row] = make_float4(ref, ws, __fmaf_rn(ex2(zl), ws, -wr), __int_as_float(lab[row]));
-      }
+      const RowNorm f = norm_of(ref, s, zlab[row], wrow[row]);
+      if (rowinfo != nullptr) rowinfo[row] = make_float4(f.ref, f.ws, f.glab, __int_as_float(lab[row]));
       const int to = idx[row];
-      if (loss != nullptr) loss[to] = kLn2 * (l2 - zl);
-      if (lse != nullptr) lse[to] = __fmaf_rn(ref, kLn2, l2 * kLn2);
+      if (loss != nullptr) loss[to] = f.loss;
+      if (lse != nullptr) lse[to] = f.lse;
     }
     __syncthreads();
   }
 }
 
 // Sums of the splits in order -> bf16 rows.  A block: 256 rows of one tile,
-// 8 columns.
+// COLS columns: 8, a whole 16-byte store per row, or 2 where so few blocks
+// would leave SMs idle.
+template <int COLS>
 __global__ void __launch_bounds__(256)
     xent_sum_kernel(const float* __restrict__ acc, int splits, int64_t split_stride, int64_t tile_stride,
                     const int* __restrict__ nl, int64_t n, const int* __restrict__ idx, int row0, int C, int k,
                     float scale, __nv_bfloat16* out, int64_t ldo) {
-  const int c0 = blockIdx.y * 8;
-  if (c0 >= k) return;
+  const int c0 = blockIdx.y * COLS;
   const int64_t r = (int64_t)blockIdx.x * kTile + threadIdx.x;
   int64_t to;
   if (idx != nullptr) {
@@ -866,19 +946,21 @@ __global__ void __launch_bounds__(256)
     if (to >= C) return;
   }
   const float* a = acc + blockIdx.x * tile_stride + (int64_t)c0 * kTile + threadIdx.x;
-  float v[8] = {};
+  float v[COLS] = {};
+#pragma unroll 8
   for (int s = 0; s < splits; ++s)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += a[s * split_stride + j * kTile];
+    for (int j = 0; j < COLS; ++j) v[j] += a[s * split_stride + j * kTile];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] *= scale;
+  for (int j = 0; j < COLS; ++j) v[j] *= scale;
   __nv_bfloat16* dst = out + to * ldo + c0;
-  if (c0 + 8 <= k) {
+  if (COLS == 8 && c0 + 8 <= k) {
     *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                                                pack_bf16x2(v[4 % COLS], v[5 % COLS]),
+                                                pack_bf16x2(v[6 % COLS], v[7 % COLS]));
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < COLS; ++j)
       if (c0 + j < k) dst[j] = __float2bfloat16_rn(v[j]);
   }
 }
@@ -1008,11 +1090,30 @@ int check_shape(int64_t n, int k, int C) {
   return GQ_OK;
 }
 
-int launch_tiles(const Maps& m, Args& a, const Sizes& z, cudaStream_t s) {
-  GQ_TRY_CUDA(cudaFuncSetAttribute(xent_tiles_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
-  xent_tiles_kernel<<<2 * z.clusters, kThreads, kSmem, s>>>(m, a);
-  ++a.counter;
+int launch_sum(int64_t tiles, const float* acc, int splits, int64_t split_stride, int64_t tile_stride, const int* nl,
+               int64_t n, const int* idx, int row0, int C, int k, float scale, __nv_bfloat16* out, int64_t ldo,
+               cudaStream_t s) {
+  if (tiles * cdiv(k, 8) < 2 * sm_count())
+    xent_sum_kernel<2><<<dim3((unsigned)tiles, (unsigned)cdiv(k, 2)), 256, 0, s>>>(
+        acc, splits, split_stride, tile_stride, nl, n, idx, row0, C, k, scale, out, ldo);
+  else
+    xent_sum_kernel<8><<<dim3((unsigned)tiles, (unsigned)cdiv(k, 8)), 256, 0, s>>>(
+        acc, splits, split_stride, tile_stride, nl, n, idx, row0, C, k, scale, out, ldo);
   return launch_status();
+}
+
+template <int KIND>
+int launch_kind(const Maps& m, const Args& a, const Sizes& z, cudaStream_t s) {
+  GQ_TRY_CUDA(cudaFuncSetAttribute(xent_tiles_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+  xent_tiles_kernel<KIND><<<2 * z.clusters, kThreads, kSmem, s>>>(m, a);
+  return launch_status();
+}
+
+int launch_tiles(const Maps& m, Args& a, const Sizes& z, cudaStream_t s) {
+  GQ_TRY(a.full ? launch_kind<ONE_TILE>(m, a, z, s)
+                : a.stats_units > 0 ? launch_kind<LOSSES>(m, a, z, s) : launch_kind<PIECE>(m, a, z, s));
+  ++a.counter;
+  return GQ_OK;
 }
 
 }  // namespace
@@ -1055,10 +1156,12 @@ extern "C" int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, 
   xent_scan_kernel<<<z.scan_blocks, kScanThreads, 0, s>>>(labels, weight, n, C, z.seg, w.cnt, so);
   GQ_TRY(launch_status());
   const int64_t ldc = round8(k);
-  const int64_t rb = cdiv(n + kTile, 8), rcap = (int64_t)sm_count() * 8;
-  xent_rows_kernel<<<(int)(rb < rcap ? rb : rcap), 256, 0, s>>>(
+  const int64_t warps = (int64_t)sm_count() * 64, share = cdiv(n + kTile, warps);
+  const int per_warp = share > 32 ? 32 : (int)share;
+  const int64_t rb = cdiv(n + kTile, 8 * per_warp);
+  xent_rows_kernel<<<(int)(rb < warps / 8 ? rb : warps / 8), 256, 0, s>>>(
       reinterpret_cast<const __nv_bfloat16*>(X), n, k, ldx, reinterpret_cast<const __nv_bfloat16*>(W), ldw, labels, w.pos,
-      w.nl, w.zlab, static_cast<__nv_bfloat16*>(w.Xc), ldc, reinterpret_cast<__nv_bfloat16*>(dX), lddx);
+      w.nl, w.zlab, static_cast<__nv_bfloat16*>(w.Xc), ldc, reinterpret_cast<__nv_bfloat16*>(dX), lddx, per_warp);
   GQ_TRY(launch_status());
 
   Maps m;
@@ -1080,20 +1183,32 @@ extern "C" int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, 
   a.idx = w.idx;
   a.part = w.part;
   a.err = dev_err;
-  a.stats_tiles = z.ctiles;
-  a.stats_run = z.run;
-  a.stats_units = z.units;
-  GQ_TRY(launch_tiles(m, a, z, s));
-  const int64_t jb = cdiv(n, 32), jcap = (int64_t)sm_count() * 2;
-  xent_join_kernel<<<(int)(jb < jcap ? jb : jcap), 1024, 0, s>>>(w.part, kParts * z.units, z.npad, w.nl, w.idx, w.zlab,
-                                                                 w.wrow, w.lab, grad ? w.row : nullptr, loss, lse);
-  GQ_TRY(launch_status());
-  if (!grad) return GQ_OK;
+  a.zlab = w.zlab;
+  a.wrow = w.wrow;
+  a.lab = w.lab;
+  a.loss = loss;
+  a.lse = lse;
+  const bool whole = z.ctiles == 1;
+  if (whole) {
+    a.full = grad ? 2 : 1;
+    a.gtiles = 1;
+    if (!grad) return launch_tiles(m, a, z, s);
+  } else {
+    a.stats_tiles = z.ctiles;
+    a.stats_run = z.run;
+    a.stats_units = z.units;
+    GQ_TRY(launch_tiles(m, a, z, s));
+    const int64_t jb = cdiv(n, 32), jcap = (int64_t)sm_count() * 2;
+    xent_join_kernel<<<(int)(jb < jcap ? jb : jcap), 1024, 0, s>>>(w.part, kParts * z.units, z.npad, w.nl, w.idx, w.zlab,
+                                                                   w.wrow, w.lab, grad ? w.row : nullptr, loss, lse);
+    GQ_TRY(launch_status());
+    if (!grad) return GQ_OK;
+    a.stats_units = 0;
+  }
 
   GQ_TRY(tmap(&m.xm[0], X, k, n, ldx, 64));
   GQ_TRY(tmap(&m.xm[1], w.Xc, k, z.npad, ldc, 64));
   GQ_TRY(tmap(&m.wm, W, k, C, ldw, 64));
-  a.stats_units = 0;
   a.scale = scale;
   a.dxs = z.dxs;
   a.dws = z.dws;
@@ -1125,17 +1240,12 @@ extern "C" int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, 
       a.first = done == 0;
       a.last = i == z.pieces;
     }
+    if (i > 0) a.full = 0;
     GQ_TRY(launch_tiles(m, a, z, s));
-    if (i > 0 && dW != nullptr && z.dws > 1) {
-      xent_sum_kernel<<<dim3(ptiles, (unsigned)cdiv(k, 8)), 256, 0, s>>>(
-          w.accW, z.dws, ptiles * tile, tile, w.nl, n, nullptr, a.pc0, C, k, scale, a.dW, lddw);
-      GQ_TRY(launch_status());
-    }
+    if (i > 0 && dW != nullptr && z.dws > 1)
+      GQ_TRY(launch_sum(ptiles, w.accW, z.dws, ptiles * tile, tile, w.nl, n, nullptr, a.pc0, C, k, scale, a.dW, lddw, s));
   }
-  if (dX != nullptr && z.dxs > 1) {
-    xent_sum_kernel<<<dim3((unsigned)z.nrt, (unsigned)cdiv(k, 8)), 256, 0, s>>>(
-        w.accX, z.dxs, z.nrt * tile, tile, w.nl, n, w.idx, 0, C, k, scale, a.dX, lddx);
-    GQ_TRY(launch_status());
-  }
+  if (dX != nullptr && z.dxs > 1)
+    GQ_TRY(launch_sum(z.nrt, w.accX, z.dxs, z.nrt * tile, tile, w.nl, n, w.idx, 0, C, k, scale, a.dX, lddx, s));
   return GQ_OK;
 }
