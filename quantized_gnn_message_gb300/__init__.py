@@ -143,7 +143,8 @@ def _check(status: int, what: str):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the raw handle: building a torch.cuda.Stream takes longer than a launch
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _ptr(t):
@@ -434,13 +435,17 @@ def gemm_tn(X: torch.Tensor, Y: torch.Tensor, out: torch.Tensor | None = None, a
     return out
 
 
-def to_bf16(src: torch.Tensor, pad_to: int = 8) -> torch.Tensor:
+def to_bf16(src: torch.Tensor, pad_to: int = 8, out: torch.Tensor | None = None) -> torch.Tensor:
     """bf16 copy of a 2-D fp32 tensor, columns zero-padded to a multiple of
-    `pad_to` (returned as a view of the unpadded width)."""
+    `pad_to` (returned as a view of the unpadded width); out: the padded
+    buffer to write, if given."""
     _cuda(src, torch.float32, "src")
     rows, cols = src.shape
     dcols = (cols + pad_to - 1) // pad_to * pad_to
-    dst = torch.empty(rows, dcols, dtype=torch.bfloat16, device=src.device)
+    dst = out if out is not None else torch.empty(rows, dcols, dtype=torch.bfloat16, device=src.device)
+    _cuda(dst, torch.bfloat16, "out")
+    if dst.shape != (rows, dcols) or not dst.is_contiguous():
+        raise GQError(f"out must be contiguous and {rows} x {dcols}")
     _check(lib().gq_to_bf16(_ptr(src), rows, cols, _rows(src), _ptr(dst), dcols, dcols, _stream()), "gq_to_bf16")
     return dst[:, :cols]
 
@@ -484,9 +489,8 @@ def _rows_like(X):
     calls on the two take the vector path."""
     e = X.element_size()
     n, d = X.shape
-    if d * e % 16 == 0 or X.stride(0) * e % 16 or X.data_ptr() % 16:
-        return torch.empty(n, d, dtype=X.dtype, device=X.device)
-    return torch.empty(n, (d * e + 15) // 16 * 16 // e, dtype=X.dtype, device=X.device)[:, :d]
+    pitch = d if d * e % 16 == 0 or X.stride(0) * e % 16 or X.data_ptr() % 16 else (d * e + 15) // 16 * 16 // e
+    return torch.empty_strided((n, d), (pitch, 1), dtype=X.dtype, device=X.device)
 
 
 def _vec32(t, count, ref, name):
@@ -589,8 +593,7 @@ def layer_norm_bwd(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rstd: 
 
 def _rows8(rows, k, dev):
     """A new bf16 matrix with a leading dimension that is a multiple of 8."""
-    t = torch.empty(rows, _round8(k), dtype=torch.bfloat16, device=dev)
-    return t if k % 8 == 0 else t[:, :k]
+    return torch.empty_strided((rows, k), (_round8(k), 1), dtype=torch.bfloat16, device=dev)
 
 
 def linear_xent(X: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, weight: torch.Tensor | None = None,
