@@ -221,7 +221,7 @@ struct Div {
 };
 __device__ __forceinline__ float over(float s, const Div& v) {
   const float q = s * v.inv;
-  return __fmaf_rn(__fmaf_rn(-q, v.d, s), v.inv, q);
+  return fabsf(q) < INFINITY ? __fmaf_rn(__fmaf_rn(-q, v.d, s), v.inv, q) : q;
 }
 
 // ---------------------------------------------------------------- dropout --
@@ -958,6 +958,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_wide_kernel(const NormBwd
 // lanes whose sums are added in lane order.
 __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* __restrict__ partial, int blocks, int d,
                                                            float* dgamma, float* dbeta) {
+  grid_wait();
   __shared__ float s[32][33];
   const int c = (int)blockIdx.x * 32 + (int)(threadIdx.x & 31), lane = threadIdx.x >> 5;
   float a = 0.0f;
@@ -1006,12 +1007,12 @@ int wide_per_sm(int threads) { return threads <= 288 ? 576 / threads : 1; }
 
 // Upper bound of the backward's blocks, one partial row of sums each.
 int bwd_blocks(int64_t n, int d) {
-  // enough blocks to fill the SMs (4 x 256 threads, or about 1024 threads of
+  // enough blocks to fill the SMs (8 x 256 threads, or about 1024 threads of
   // wide rows, each), and no more partial rows than that
   const int sms = sm_count();
   if (d <= kWarpRowMax) {
     const int64_t want = (n + 7) / 8;
-    return (int)(want < 4 * sms ? (want < 1 ? 1 : want) : 4 * sms);
+    return (int)(want < 8 * sms ? (want < 1 ? 1 : want) : 8 * sms);
   }
   const int ept = bwd_ept(d), threads = ((d + ept - 1) / ept + 31) / 32 * 32;
   int per = block_rows_per_sm(threads, (size_t)3 * threads * ept * sizeof(float));
@@ -1040,16 +1041,23 @@ int launch_dropout(const void* X, int64_t n, int d, int64_t ldx, const Drop& dr,
   return launch_status();
 }
 
+// Blocks of a persistent kernel: as many as are resident at once (one wave;
+// 2.7 waves of 8 blocks per SM cost the 131,072 x 256 forward pass a tenth).
+template <typename K>
+int wave(K kernel, size_t smem, int64_t want) {
+  int per = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kNormThreads, smem) != cudaSuccess || per < 1) per = 1;
+  const int64_t cap = (int64_t)per * sm_count();
+  return (int)(want < cap ? want : cap);
+}
+
 template <typename T, int V, int NV, int G>
 int fwd_warp(const NormFwd& p, cudaStream_t s) {
   constexpr int rows = kNormThreads / G;
   const int64_t want = (p.n + rows - 1) / rows;
-  const int cap = 8 * sm_count();
-  const int grid = (int)(want < cap ? want : cap);
-  if (V > 1 && p.d == G * NV * V)
-    norm_fwd_warp_kernel<T, V, NV, G, true><<<grid, kNormThreads, 0, s>>>(p);
-  else
-    norm_fwd_warp_kernel<T, V, NV, G, false><<<grid, kNormThreads, 0, s>>>(p);
+  auto kernel = V > 1 && p.d == G * NV * V ? norm_fwd_warp_kernel<T, V, NV, G, (V > 1)>
+                                           : norm_fwd_warp_kernel<T, V, NV, G, false>;
+  kernel<<<wave(kernel, 0, want), kNormThreads, 0, s>>>(p);
   return launch_status();
 }
 
@@ -1082,20 +1090,19 @@ int fwd_any(const NormFwd& p, cudaStream_t s) {
 template <typename T, typename TO, int V, int NV, int G>
 int bwd_warp(const NormBwd& p, int& blocks, cudaStream_t s) {
   constexpr int kWarps = kNormThreads / 32;
-  // resident blocks per SM, by the registers the lane's elements take
-  constexpr int E = NV * V;
-  constexpr int kPer = V > 1 ? (E <= 4 ? 4 : E <= 8 ? 3 : 2) : (E <= 2 ? 4 : E <= 4 ? 3 : E <= 12 ? 2 : 1);
-  if (blocks > kPer * sm_count()) blocks = kPer * sm_count();
   const size_t sums = (size_t)kWarps * 2 * G * NV * V * sizeof(float);
   if constexpr (V > 1) {
     constexpr int S = NV > 2 ? 3 : 4;
     const size_t ring = (size_t)kWarps * S * 2 * NV * 32 * 16;
     const size_t smem = ring > sums ? ring : sums;
-    GQ_TRY_CUDA(cudaFuncSetAttribute(norm_bwd_ring_kernel<T, TO, V, NV, G, S>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-    norm_bwd_ring_kernel<T, TO, V, NV, G, S><<<blocks, kNormThreads, smem, s>>>(p);
+    auto kernel = norm_bwd_ring_kernel<T, TO, V, NV, G, S>;
+    GQ_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    blocks = wave(kernel, smem, blocks);
+    kernel<<<blocks, kNormThreads, smem, s>>>(p);
   } else {
-    norm_bwd_warp_kernel<T, TO, V, NV, G><<<blocks, kNormThreads, sums, s>>>(p);
+    auto kernel = norm_bwd_warp_kernel<T, TO, V, NV, G>;
+    blocks = wave(kernel, sums, blocks);
+    kernel<<<blocks, kNormThreads, sums, s>>>(p);
   }
   return launch_status();
 }
@@ -1276,6 +1283,6 @@ extern "C" int gq_layer_norm_bwd(const void* dY, int64_t lddy, const void* X, in
   else
     GQ_TRY((bwd_typed<__half, __half>(a, blocks, vec, s)));
   if (!sums) return GQ_OK;
-  norm_reduce_kernel<<<(2 * d + 31) / 32, 1024, 0, s>>>(a.partial, blocks, d, dgamma, dbeta);
-  return launch_status();
+  return launch_after(norm_reduce_kernel, dim3((2 * d + 31) / 32), dim3(1024), 0, s, (const float*)a.partial, blocks, d,
+                      dgamma, dbeta);
 }

@@ -12,6 +12,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "gq.h"
+
 namespace gq {
 
 constexpr long long kWaitCycles = 4000000000LL;  // ~2 s at 2 GHz
@@ -182,6 +184,29 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// ---- programmatic launches ---------------------------------------------------
+// A kernel launched by launch_after may be set up while the kernel before it
+// on the stream still runs; grid_wait returns once that one has completed and
+// its writes are visible.  Every such kernel calls grid_wait before it touches
+// global memory, so the one before has, by its own completion, waited for
+// everything earlier.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+int launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = block;
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...) == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
+}
 
 // ---- packed fp32 ------------------------------------------------------------
 // Two fp32 operations at once.

@@ -419,6 +419,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_wait();
   const Plan q = make_plan(p);
   Feed feed;
   feed.full = ufull;
@@ -785,6 +786,7 @@ struct ScanOut {
 __global__ void __launch_bounds__(kScanThreads)
     xent_scan_kernel(const int* __restrict__ labels, const float* __restrict__ weight, int64_t n, int C,
                      int64_t seg, const int* __restrict__ cnt, const ScanOut o) {
+  grid_wait();
   __shared__ int ws[32];
   __shared__ int base;
   if (threadIdx.x == 0) base = 0;
@@ -838,6 +840,7 @@ __global__ void __launch_bounds__(256)
                      const __nv_bfloat16* __restrict__ W, int64_t ldw, const int* __restrict__ labels,
                      const int* __restrict__ pos, const int* __restrict__ nl, float* zlab, __nv_bfloat16* Xc,
                      int64_t ldc, __nv_bfloat16* dX, int64_t lddx, int per_warp) {
+  grid_wait();
   const int m = *nl;
   const bool all = m == n;
   const int lane = threadIdx.x & 31;
@@ -898,6 +901,7 @@ __global__ void __launch_bounds__(1024)
                      const int* __restrict__ idx, const float* __restrict__ zlab, const float* __restrict__ wrow,
                      const int* __restrict__ lab, float4* rowinfo, float* loss, float* lse) {
   __shared__ float sm[32][33], ss[32][33];
+  grid_wait();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int rows = *nl;
   for (int64_t r0 = (int64_t)blockIdx.x * 32; r0 < rows; r0 += (int64_t)gridDim.x * 32) {
@@ -935,6 +939,7 @@ __global__ void __launch_bounds__(256)
     xent_sum_kernel(const float* __restrict__ acc, int splits, int64_t split_stride, int64_t tile_stride,
                     const int* __restrict__ nl, int64_t n, const int* __restrict__ idx, int row0, int C, int k,
                     float scale, __nv_bfloat16* out, int64_t ldo) {
+  grid_wait();
   const int c0 = blockIdx.y * COLS;
   const int64_t r = (int64_t)blockIdx.x * kTile + threadIdx.x;
   int64_t to;
@@ -1094,19 +1099,16 @@ int launch_sum(int64_t tiles, const float* acc, int splits, int64_t split_stride
                int64_t n, const int* idx, int row0, int C, int k, float scale, __nv_bfloat16* out, int64_t ldo,
                cudaStream_t s) {
   if (tiles * cdiv(k, 8) < 2 * sm_count())
-    xent_sum_kernel<2><<<dim3((unsigned)tiles, (unsigned)cdiv(k, 2)), 256, 0, s>>>(
-        acc, splits, split_stride, tile_stride, nl, n, idx, row0, C, k, scale, out, ldo);
-  else
-    xent_sum_kernel<8><<<dim3((unsigned)tiles, (unsigned)cdiv(k, 8)), 256, 0, s>>>(
-        acc, splits, split_stride, tile_stride, nl, n, idx, row0, C, k, scale, out, ldo);
-  return launch_status();
+    return launch_after(xent_sum_kernel<2>, dim3((unsigned)tiles, (unsigned)cdiv(k, 2)), dim3(256), 0, s, acc, splits,
+                        split_stride, tile_stride, nl, n, idx, row0, C, k, scale, out, ldo);
+  return launch_after(xent_sum_kernel<8>, dim3((unsigned)tiles, (unsigned)cdiv(k, 8)), dim3(256), 0, s, acc, splits,
+                      split_stride, tile_stride, nl, n, idx, row0, C, k, scale, out, ldo);
 }
 
 template <int KIND>
 int launch_kind(const Maps& m, const Args& a, const Sizes& z, cudaStream_t s) {
   GQ_TRY_CUDA(cudaFuncSetAttribute(xent_tiles_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
-  xent_tiles_kernel<KIND><<<2 * z.clusters, kThreads, kSmem, s>>>(m, a);
-  return launch_status();
+  return launch_after(xent_tiles_kernel<KIND>, dim3(2 * z.clusters), dim3(kThreads), kSmem, s, m, a);
 }
 
 int launch_tiles(const Maps& m, Args& a, const Sizes& z, cudaStream_t s) {
@@ -1153,16 +1155,20 @@ extern "C" int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, 
     GQ_TRY(launch_status());
   }
   const ScanOut so{w.nl, w.pos, w.idx, w.lab, w.wrow, loss, lse, w.counters, w.n_counters};
-  xent_scan_kernel<<<z.scan_blocks, kScanThreads, 0, s>>>(labels, weight, n, C, z.seg, w.cnt, so);
+  if (z.scan_blocks > 1)
+    GQ_TRY(launch_after(xent_scan_kernel, dim3(z.scan_blocks), dim3(kScanThreads), 0, s, labels, weight, n, C, z.seg,
+                        w.cnt, so));
+  else
+    xent_scan_kernel<<<1, kScanThreads, 0, s>>>(labels, weight, n, C, z.seg, w.cnt, so);
   GQ_TRY(launch_status());
   const int64_t ldc = round8(k);
   const int64_t warps = (int64_t)sm_count() * 64, share = cdiv(n + kTile, warps);
   const int per_warp = share > 32 ? 32 : (int)share;
   const int64_t rb = cdiv(n + kTile, 8 * per_warp);
-  xent_rows_kernel<<<(int)(rb < warps / 8 ? rb : warps / 8), 256, 0, s>>>(
-      reinterpret_cast<const __nv_bfloat16*>(X), n, k, ldx, reinterpret_cast<const __nv_bfloat16*>(W), ldw, labels, w.pos,
-      w.nl, w.zlab, static_cast<__nv_bfloat16*>(w.Xc), ldc, reinterpret_cast<__nv_bfloat16*>(dX), lddx, per_warp);
-  GQ_TRY(launch_status());
+  GQ_TRY(launch_after(xent_rows_kernel, dim3((unsigned)(rb < warps / 8 ? rb : warps / 8)), dim3(256), 0, s,
+                      reinterpret_cast<const __nv_bfloat16*>(X), n, k, ldx, reinterpret_cast<const __nv_bfloat16*>(W),
+                      ldw, labels, w.pos, w.nl, w.zlab, static_cast<__nv_bfloat16*>(w.Xc), ldc,
+                      reinterpret_cast<__nv_bfloat16*>(dX), lddx, per_warp));
 
   Maps m;
   memset(&m, 0, sizeof(m));
@@ -1199,9 +1205,9 @@ extern "C" int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, 
     a.stats_units = z.units;
     GQ_TRY(launch_tiles(m, a, z, s));
     const int64_t jb = cdiv(n, 32), jcap = (int64_t)sm_count() * 2;
-    xent_join_kernel<<<(int)(jb < jcap ? jb : jcap), 1024, 0, s>>>(w.part, kParts * z.units, z.npad, w.nl, w.idx, w.zlab,
-                                                                   w.wrow, w.lab, grad ? w.row : nullptr, loss, lse);
-    GQ_TRY(launch_status());
+    GQ_TRY(launch_after(xent_join_kernel, dim3((unsigned)(jb < jcap ? jb : jcap)), dim3(1024), 0, s, w.part,
+                        kParts * z.units, z.npad, w.nl, w.idx, w.zlab, w.wrow, w.lab, grad ? w.row : nullptr, loss,
+                        lse));
     if (!grad) return GQ_OK;
     a.stats_units = 0;
   }

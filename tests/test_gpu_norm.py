@@ -271,3 +271,13 @@ def test_refusals_of_the_binding():
                  lambda: q.layer_norm_bwd(x, x, m, m, dX=x.half())):
         with pytest.raises(q.GQError):
             call()
+
+
+def test_overflowing_variance_is_not_nan():
+    # squares beyond fp32: the variance is infinite, 1 / sqrt of it 0
+    q = gq()
+    for d in (64, 100, 1000):
+        x = synth.normal_matrix(3, d, seed=1, device="cuda") * 1e25
+        beta = torch.ones(d, device="cuda")
+        y, mean, rstd = q.layer_norm_fwd(x, None, beta)
+        assert (rstd == 0).all() and (y == 1).all() and torch.isfinite(mean).all()
