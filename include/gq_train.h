@@ -105,7 +105,7 @@ GQ_API int gq_layer_norm_bwd(const void* dY, int64_t lddy, const void* X, int64_
  *           whichever applies;
  *           depends on the current device's SM count).  Calls sharing one
  *           workspace must not overlap.
- *   dev_err nullable device int, as for the GEMMs (codes 21 .. 28)
+ *   dev_err nullable device int, as for the GEMMs (codes 21 .. 26)
  * Results are the same from run to run.  dX and dW must not overlap X or W.
  * Errors: GQ_ERR_INVALID_ARG (null X, W or labels, n < 0, k < 1, C < 1, bad
  * leading dimensions or alignment); GQ_ERR_UNSUPPORTED for k > 16384,

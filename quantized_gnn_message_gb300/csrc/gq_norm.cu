@@ -42,6 +42,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "gq_common.cuh"
 #include "gq_internal.cuh"
@@ -126,6 +127,9 @@ __device__ __forceinline__ void unpack(const Raw<T, V>& r, float* o) {
   for (int j = 0; j < V; ++j) {
     if constexpr (sizeof(T) == 4) {
       o[j] = __uint_as_float(r.w[j]);
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {  // the upper half of an fp32
+      const uint32_t w = V == 1 ? r.w[0] : r.w[j / 2];
+      o[j] = __uint_as_float(V > 1 && (j & 1) ? w & 0xffff0000u : w << 16);
     } else {
       const uint16_t u = (uint16_t)(V == 1 ? r.w[0] : r.w[j / 2] >> (16 * (j & 1)));
       T t;
@@ -305,6 +309,18 @@ __device__ __forceinline__ uint32_t gather_bits(uint32_t bits, int col) {
   return w;
 }
 
+// s plus V values
+template <int V>
+__device__ __forceinline__ float sum_of(const float* v, float s) {
+  if constexpr (V > 1) {
+    float2 a = make_float2(s, 0.0f);
+#pragma unroll
+    for (int j = 0; j < V; j += 2) a = add2(a, make_float2(v[j], v[j + 1]));
+    return a.x + a.y;
+  }
+  return s + v[0];
+}
+
 // Centres V values of a row (those past its end become 0) and adds their
 // squares to q; `whole`: all V columns are in the row.
 template <int V>
@@ -348,23 +364,24 @@ struct NormFwd {
   int64_t ldrb;
 };
 
-// V outputs of a row from its centred values xc.  Every lane of the warp
+// V outputs of a row from its centred values xc + off, with shift = off rstd.
+// Every lane of the warp
 // takes part (the bits are gathered by shuffles); `live` lanes store.
 template <typename T, int V>
-__device__ __forceinline__ void norm_emit(const NormFwd& p, int64_t r, uint32_t kr, bool live, float rstd, int col,
-                                          const float* xc, const float* ga, const float* be) {
+__device__ __forceinline__ void norm_emit(const NormFwd& p, int64_t r, uint32_t kr, bool live, float rstd, float shift,
+                                          int col, const float* xc, const float* ga, const float* be) {
   float y[V];
   uint32_t pos = 0;
   if constexpr (V > 1) {
-    const float2 rs = make_float2(rstd, rstd);
+    const float2 rs = make_float2(rstd, rstd), sh = make_float2(shift, shift);
 #pragma unroll
     for (int j = 0; j < V; j += 2) {
-      const float2 z = fma2(mul2(make_float2(xc[j], xc[j + 1]), rs), make_float2(ga[j], ga[j + 1]),
+      const float2 z = fma2(fma2(make_float2(xc[j], xc[j + 1]), rs, sh), make_float2(ga[j], ga[j + 1]),
                             make_float2(be[j], be[j + 1]));
       y[j] = z.x, y[j + 1] = z.y;
     }
   } else {
-    y[0] = __fmaf_rn(xc[0] * rstd, ga[0], be[0]);
+    y[0] = __fmaf_rn(__fmaf_rn(xc[0], rstd, shift), ga[0], be[0]);
   }
   if (p.relu) {
     if (p.bits != nullptr) {
@@ -416,8 +433,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_warp_kernel(const NormF
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       unpack<T, V>(nx[i], v[i]);
-#pragma unroll
-      for (int j = 0; j < V; ++j) s += v[i][j];
+      s = sum_of<V>(v[i], s);
     }
     if (rw + step < p.n) fetch(rw + step);
     const float mean = over(group_sum<G>(s), p.dv);
@@ -431,7 +447,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_warp_kernel(const NormF
     }
     const uint32_t kr = row_key(p.dr.key, (uint32_t)r);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) norm_emit<T, V>(p, r, kr, live, rstd, c0 + i * G * V, v[i], ga[i], be[i]);
+    for (int i = 0; i < NV; ++i) norm_emit<T, V>(p, r, kr, live, rstd, 0.0f, c0 + i * G * V, v[i], ga[i], be[i]);
   }
 }
 
@@ -468,8 +484,7 @@ __global__ void __launch_bounds__(1024, 1) norm_fwd_block_kernel(const NormFwd p
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       unpack<T, V>(nx[i], v[i]);
-#pragma unroll
-      for (int j = 0; j < V; ++j) s += v[i][j];
+      s = sum_of<V>(v[i], s);
     }
     if (r + gridDim.x < p.n) {
       const T* x = static_cast<const T*>(p.X) + (r + gridDim.x) * p.ldx;
@@ -498,7 +513,7 @@ __global__ void __launch_bounds__(1024, 1) norm_fwd_block_kernel(const NormFwd p
       if (p.mean != nullptr) p.mean[r] = mean;
       if (p.rstd != nullptr) p.rstd[r] = rstd;
     }
-    const float off = mw - mean;  // from the warp's mean to the row's
+    const float shift = (mw - mean) * rstd;  // from the warp's mean to the row's
     const uint32_t kr = row_key(p.dr.key, (uint32_t)r);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -506,9 +521,7 @@ __global__ void __launch_bounds__(1024, 1) norm_fwd_block_kernel(const NormFwd p
       float ga[V], be[V];
       load_shared<V>(par + c0 + i * cs, ga);
       load_shared<V>(par + W + c0 + i * cs, be);
-#pragma unroll
-      for (int j = 0; j < V; ++j) v[i][j] += off;
-      norm_emit<T, V>(p, r, kr, true, rstd, c0 + i * cs, v[i], ga, be);
+      norm_emit<T, V>(p, r, kr, true, rstd, shift, c0 + i * cs, v[i], ga, be);
     }
   }
 }

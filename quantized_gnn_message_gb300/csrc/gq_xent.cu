@@ -69,7 +69,7 @@ namespace {
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarps + 3);  // TMA, MMA, epilogue, scheduler
 constexpr int kParts = kEpiWarps / 4;           // warps that share a row's columns
-static_assert(kParts == 2, "a WHOLE tile's rows are exchanged between two warps");
+static_assert(kParts == 2, "WHOLE tiles go by turns to the two warps of 32 rows");
 constexpr int kStages = 5;
 constexpr int kStageA = 128 * 128;                    // 128 rows x 64 bf16 (or 2 x 64 x 64)
 constexpr int kStageBytes = 2 * kStageA;
@@ -89,6 +89,7 @@ struct Maps {
   CUtensorMap wk, wm;        // W
   CUtensorMap gk, gm;        // the piece of G read by DX / DW
   CUtensorMap gst;           // the piece of G written by GRAD
+  CUtensorMap ox, ow;        // dX, dW
 };
 
 struct Args {
@@ -105,8 +106,7 @@ struct Args {
   int first, last;       // the piece read is the first / last one
   float scale;           // of the results: G is formed without it, see below
   int full;              // the tiles of gtiles are WHOLE (1: losses only, 2: G too)
-  const float* zlab;     // per labelled row, for WHOLE: logit and weight, label, row of X
-  const float* wrow;
+  const float* wrow;     // per labelled row, for WHOLE: weight, label
   const int* lab;
   float* loss;           // per row of X, nullable
   float* lse;
@@ -225,6 +225,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+// z = v where y == j, as a select (the compiler would index the 32 values
+// through local memory).
+__device__ __forceinline__ void pick(float& z, float v, int y, int j) {
+  asm("{\n  .reg .pred p;\n  setp.eq.s32 p, %2, %3;\n  selp.f32 %0, %1, %0, p;\n}" : "+f"(z) : "f"(v), "r"(y), "r"(j));
 }
 // Rare branches of the epilogue: kept as branches, not as 32 selects a chunk.
 __device__ __forceinline__ void keep_branch() { asm volatile("" ::: "memory"); }
@@ -353,8 +358,8 @@ __device__ __forceinline__ void online(float (&v)[32], int limit, float& r, floa
   r = rn;
 }
 
-// A row's values from its (r, sum) pairs, joined in order: the loss is taken
-// from the label's logit zlab in the form the sum has it, z L - r.
+// A row's values from its r and sum: the loss is taken from the label's logit
+// zlab in the form the sum has it, z L - r.
 struct RowNorm {
   float ref, ws, glab, loss, lse;  // r; weight / sum; G of the label
 };
@@ -368,11 +373,6 @@ __device__ __forceinline__ RowNorm norm_of(float ref, float s, float zlab, float
   f.lse = __fmaf_rn(ref, kLn2, l2 * kLn2);
   return f;
 }
-__device__ __forceinline__ RowNorm finish_row(float r, float2 lo, float2 hi, float zlab, float weight) {
-  const float ref = r == neg_inf() ? 0.0f : r;
-  return norm_of(ref, lo.y * ex2(lo.x - ref) + hi.y * ex2(hi.x - ref), zlab, weight);
-}
-
 // entry j of a lane's 128-byte row of a G box
 __device__ __forceinline__ void put_box(uint8_t* row, int lane, unsigned j, __nv_bfloat16 v) {
   *reinterpret_cast<__nv_bfloat16*>(row + 16 * ((j >> 3) ^ (lane & 7)) + 2 * (j & 7)) = v;
@@ -395,8 +395,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* tempty = tfull + 2;
   uint64_t* ufull = tempty + 2;
   uint64_t* uempty = ufull + kSlots;
-  uint64_t* pair = uempty + kSlots;  // of the two warps that share 32 rows
-  int* unit = reinterpret_cast<int*>(pair + 4);
+  int* unit = reinterpret_cast<int*>(uempty + kSlots);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(unit + kSlots);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -409,13 +408,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 2 * kEpiWarps);
+      mbar_init(&tempty[a], KIND == ONE_TILE ? kEpiWarps : 2 * kEpiWarps);
     }
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&ufull[s], 1);
       mbar_init(&uempty[s], kConsumers);
     }
-    for (int j = 0; j < 4; ++j) mbar_init(&pair[j], kParts);
     *abort = 0;
     fence_barrier_init();
   }
@@ -536,7 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (row < q.nl) {
         if (KIND == PIECE && t.mode == GRAD) rwn = p.row[row];
         if (KIND == ONE_TILE)
-          rwn = make_float4(p.zlab[row], p.wrow[row], __int_as_float(p.idx[row]), __int_as_float(p.lab[row]));
+          rwn = make_float4(0.0f, p.wrow[row], __int_as_float(p.idx[row]), __int_as_float(p.lab[row]));
       }
     };
     fetch();
@@ -549,6 +547,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int sub = 0; ok && get_tile(p, q, u, sub, t); ++sub, ++i) {
         const int srow = t.rt * kTile + rit;
         const int a = i & 1;
+        // a WHOLE tile belongs to one of the two warps of its rows, which
+        // take tiles by turns: a lane holds all of its row's classes
+        if (KIND == ONE_TILE && a != part) continue;
         int got = 1;
         if (lane == 0) got = wait(&tfull[a], (i >> 1) & 1, abort, p.err, 25);
         ok = __shfl_sync(gq::FULL, got, 0) != 0;
@@ -556,50 +557,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + a * 256;
         if (KIND != PIECE) {
-          for (int c = part * 32; c < t.N; c += 32 * kParts) {
+          float zl = 0.0f;
+          const int lab = __float_as_int(rw.w);
+          for (int c = KIND == ONE_TILE ? 0 : part * 32; c < t.N; c += KIND == ONE_TILE ? 32 : 32 * kParts) {
             float v[32];
             tmem_ld32(taddr + c, v);
             tmem_ld_wait();
+            if (KIND == ONE_TILE) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) pick(zl, v[j], lab - c, j);
+            }
             const int c0 = t.ct * p.NT + c;  // class of v[0]
             if (c0 < p.C) online(v, p.C - c0, m, sum);
           }
-        }
-        if (KIND == ONE_TILE) {
-          // the two warps of these rows exchange their halves: posted, read,
-          // and read by both before the staging is used again
-          if (lane == 0) bulk_wait_read<0>();
-          __syncwarp();
-          reinterpret_cast<float2*>(stg)[lane] = make_float2(m, sum);
-          __syncwarp();
-          int met = 1;
-          if (lane == 0) {
-            mbar_arrive(&pair[quarter]);
-            met = wait(&pair[quarter], 0, abort, p.err, 27);
+          if (KIND == ONE_TILE) {
+            const RowNorm f = norm_of(m == neg_inf() ? 0.0f : m, sum, zl, rw.y);
+            if (srow < q.nl) {
+              const int to = __float_as_int(rw.z);
+              if (p.loss != nullptr) p.loss[to] = f.loss;
+              if (p.lse != nullptr) p.lse[to] = f.lse;
+              rw = make_float4(f.ref, f.ws, f.glab, rw.w);
+            }
           }
-          ok = __shfl_sync(gq::FULL, met, 0) != 0;
-          if (!ok) break;
-          const float2 o = reinterpret_cast<const float2*>(stg_all + ((warp - 2) ^ 4) * kStg)[lane];
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&pair[quarter]);
-            met = wait(&pair[quarter], 1, abort, p.err, 28);
-          }
-          ok = __shfl_sync(gq::FULL, met, 0) != 0;
-          if (!ok) break;
-          const float2 lo = part == 0 ? make_float2(m, sum) : o, hi = part == 0 ? o : make_float2(m, sum);
-          const RowNorm f = finish_row(fmaxf(lo.x, hi.x), lo, hi, rw.x, rw.y);
-          if (part == 0 && srow < q.nl) {
-            const int to = __float_as_int(rw.z);
-            if (p.loss != nullptr) p.loss[to] = f.loss;
-            if (p.lse != nullptr) p.lse[to] = f.lse;
-          }
-          rw = make_float4(f.ref, f.ws, f.glab, rw.w);
-          if (srow >= q.nl) rw = make_float4(0.0f, 0.0f, 0.0f, rw.w);
-          m = neg_inf();
-          sum = 0.0f;
         }
         if ((KIND == PIECE && t.mode == GRAD) || (KIND == ONE_TILE && p.full == 2)) {
-          for (int b = part * 64; b < t.N; b += 64 * kParts) {
+          for (int b = KIND == ONE_TILE ? 0 : part * 64; b < t.N; b += KIND == ONE_TILE ? 64 : 64 * kParts) {
             // a box of 32 rows x 64 classes, 128 bytes a row (128-byte
             // swizzle: 16-byte piece j of row `lane` at j ^ (lane & 7))
             uint8_t* box = stg + (nbox & 1) * kBox;
@@ -658,14 +640,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int64_t tile = dw ? (int64_t)t.split * p.ptiles + t.ct : (int64_t)t.split * (p.npad / kTile) + t.rt;
             acc = (dw ? p.accW : p.accX) + (tile * p.nkt + t.kt) * ((int64_t)p.NK * kTile) + rit;
           }
+          // rows of the result that follow one another are stored by TMA in
+          // boxes of 64 columns; rows scattered among unlabelled ones, and
+          // rows whose last 16 bytes are not all theirs (a bulk store would
+          // write them), by plain stores.  Either way row `lane` of the
+          // staging is 128 bytes, 16-byte piece j at j ^ (lane & 7)
+          const bool apart = (!dw && q.nl < p.n) || (p.k & 7) != 0;
           const int r = (dw ? t.ct : t.rt) * kTile + rit;
-          int64_t orow = -1;  // row of the result this lane's sums belong to
-          if (dw) orow = p.pc0 + r < p.C ? p.pc0 + r : -1;
-          else if (r < q.nl) orow = q.nl < p.n ? p.idx[r] : r;
-          __nv_bfloat16* out = dw ? p.dW : p.dX;
-          const int64_t ldo = dw ? p.lddw : p.lddx;
-          for (int c = part * 32; c < t.N; c += 32 * kParts) {
-            float v[32];
+          int64_t orow = -1;  // row of the result that this lane's sums belong to
+          if (apart) {
+            if (dw) orow = p.pc0 + r < p.C ? p.pc0 + r : -1;
+            else if (r < q.nl) orow = q.nl < p.n ? p.idx[r] : r;
+          }
+          auto load = [&](int c, float (&v)[32]) {
             if (t.steps > 0) {
               tmem_ld32(taddr + c, v);
               tmem_ld_wait();
@@ -677,36 +664,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[j] += acc[(c + j) * kTile];
             }
-            if (sums) {
+          };
+          for (int b = part * 64; b < t.N; b += 64 * kParts) {
+            const int k0 = t.kt * p.NK + b;
+            if (!sums && k0 >= p.k) break;
+            uint8_t* box = stg + (nbox & 1) * kBox;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              float v[32];
+              load(b + 32 * h, v);
+              if (sums) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) acc[(c + j) * kTile] = v[j];
+                for (int j = 0; j < 32; ++j) acc[(b + 32 * h + j) * kTile] = v[j];
+                continue;
+              }
+              if (h == 0) {
+                if (lane == 0) bulk_wait_read<1>();
+                __syncwarp();
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  o[e] = pack_bf16x2(v[8 * j + 2 * e] * p.scale, v[8 * j + 2 * e + 1] * p.scale);
+                *reinterpret_cast<uint4*>(box + lane * 128 + 16 * ((4 * h + j) ^ (lane & 7))) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
+              }
+            }
+            if (sums) continue;
+            ++nbox;
+            if (!apart) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                const int y = (dw ? p.pc0 + t.ct * kTile : t.rt * kTile) + cr * 128 + quarter * 32;
+                if (y < (dw ? p.C : q.nl)) tma_store_2d(dw ? &maps.ow : &maps.ox, box, k0, y);
+                bulk_commit();
+              }
               continue;
             }
-            const int k0 = t.kt * p.NK + c;
-            if (k0 >= p.k) continue;
-            // through shared memory (64-byte rows, 16-byte piece j at
-            // j ^ ((lane >> 1) & 3)), so that a store writes whole 64-byte
-            // pieces of eight rows
-            if (lane == 0) bulk_wait_read<0>();
+            if (lane == 0) bulk_commit();  // an empty group: this box has no bulk store to wait for
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t o[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                o[e] = pack_bf16x2(v[8 * j + 2 * e] * p.scale, v[8 * j + 2 * e + 1] * p.scale);
-              *reinterpret_cast<uint4*>(stg + lane * 64 + 16 * (j ^ ((lane >> 1) & 3))) =
-                  make_uint4(o[0], o[1], o[2], o[3]);
-            }
-            __syncwarp();
-#pragma unroll
-            for (int it = 0; it < 4; ++it) {
-              const int rr = it * 8 + (lane >> 2), j = lane & 3;
-              const uint4 o = *reinterpret_cast<const uint4*>(stg + rr * 64 + 16 * (j ^ ((rr >> 1) & 3)));
+            for (int it = 0; it < 8; ++it) {
+              const int rr = it * 4 + (lane >> 3), j = lane & 7;
+              const uint4 o = *reinterpret_cast<const uint4*>(box + rr * 128 + 16 * (j ^ (rr & 7)));
               const int64_t to = __shfl_sync(gq::FULL, orow, rr);
               if (to < 0) continue;
               const int col = k0 + 8 * j;
-              __nv_bfloat16* dst = out + to * ldo + col;
+              __nv_bfloat16* dst = (dw ? p.dW + to * p.lddw : p.dX + to * p.lddx) + col;
               if (col + 8 <= p.k) {
                 *reinterpret_cast<uint4*>(dst) = o;
               } else {
@@ -840,15 +847,17 @@ __global__ void __launch_bounds__(kScanThreads)
 // Per row of X: the label's logit x . w_y; the labelled rows copied
 // together (zeros up to a multiple of 256 rows) and zeros in the other rows
 // of dX, unless every row is labelled.  The label's logit costs one gathered
-// row of W here; picked out of the STATS tiles it cost 16% of their time.
+// row of W here; picked out of the STATS tiles it cost 16% of their time
+// (dots = 0: a WHOLE tile's lanes hold it).
 __global__ void __launch_bounds__(256)
     xent_rows_kernel(const __nv_bfloat16* __restrict__ X, int64_t n, int k, int64_t ldx,
                      const __nv_bfloat16* __restrict__ W, int64_t ldw, const int* __restrict__ labels,
                      const int* __restrict__ pos, const int* __restrict__ nl, float* zlab, __nv_bfloat16* Xc,
-                     int64_t ldc, __nv_bfloat16* dX, int64_t lddx, int per_warp) {
+                     int64_t ldc, __nv_bfloat16* dX, int64_t lddx, int per_warp, int dots) {
   grid_wait();
   const int m = *nl;
   const bool all = m == n;
+  if (all && !dots) return;
   const int lane = threadIdx.x & 31;
   const int64_t pad_end = all ? n : n + ((m + kTile - 1) / kTile * (int64_t)kTile - m);  // rows of zeros behind Xc
   const int64_t step = (int64_t)gridDim.x * 8 * per_warp;
@@ -873,26 +882,29 @@ __global__ void __launch_bounds__(256)
       const int64_t r = r0 + i;
       const int to = __shfl_sync(gq::FULL, at, i);
       const __nv_bfloat16* x = X + r * ldx;
-      const __nv_bfloat16* w = W + (int64_t)labels[r] * ldw;
+      const __nv_bfloat16* w = dots ? W + (int64_t)labels[r] * ldw : nullptr;
       __nv_bfloat16* dst = all ? nullptr : Xc + (int64_t)to * ldc;
       float z = 0.0f;
       for (int c = lane * 8; c < k; c += 256) {
         if (c + 8 <= k) {
-          const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + c)), b = __ldg(reinterpret_cast<const uint4*>(w + c));
+          const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + c));
+          if (dst != nullptr) *reinterpret_cast<uint4*>(dst + c) = a;
+          if (!dots) continue;
+          const uint4 b = __ldg(reinterpret_cast<const uint4*>(w + c));
           const uint32_t au[4] = {a.x, a.y, a.z, a.w}, bu[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {  // bf16 is the upper half of an fp32
             z = __fmaf_rn(__uint_as_float(au[j] << 16), __uint_as_float(bu[j] << 16), z);
             z = __fmaf_rn(__uint_as_float(au[j] & 0xffff0000u), __uint_as_float(bu[j] & 0xffff0000u), z);
           }
-          if (dst != nullptr) *reinterpret_cast<uint4*>(dst + c) = a;
         } else {
           for (int j = c; j < k; ++j) {
-            z = __fmaf_rn(__bfloat162float(x[j]), __bfloat162float(w[j]), z);
+            if (dots) z = __fmaf_rn(__bfloat162float(x[j]), __bfloat162float(w[j]), z);
             if (dst != nullptr) dst[j] = x[j];
           }
         }
       }
+      if (!dots) continue;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(gq::FULL, z, o);
       if (lane == 0) zlab[to] = z;
@@ -1176,7 +1188,7 @@ extern "C" int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, 
   GQ_TRY(launch_after(xent_rows_kernel, dim3((unsigned)(rb < warps / 8 ? rb : warps / 8)), dim3(256), 0, s,
                       reinterpret_cast<const __nv_bfloat16*>(X), n, k, ldx, reinterpret_cast<const __nv_bfloat16*>(W),
                       ldw, labels, w.pos, w.nl, w.zlab, static_cast<__nv_bfloat16*>(w.Xc), ldc,
-                      reinterpret_cast<__nv_bfloat16*>(dX), lddx, per_warp));
+                      reinterpret_cast<__nv_bfloat16*>(dX), lddx, per_warp, z.ctiles > 1 ? 1 : 0));
 
   Maps m;
   memset(&m, 0, sizeof(m));
@@ -1197,7 +1209,6 @@ extern "C" int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, 
   a.idx = w.idx;
   a.part = w.part;
   a.err = dev_err;
-  a.zlab = w.zlab;
   a.wrow = w.wrow;
   a.lab = w.lab;
   a.loss = loss;
@@ -1232,6 +1243,8 @@ extern "C" int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, 
   a.lddx = lddx;
   a.dW = reinterpret_cast<__nv_bfloat16*>(dW);
   a.lddw = lddw;
+  if (dX != nullptr) GQ_TRY(tmap(&m.ox, dX, k, n, lddx, 32));
+  if (dW != nullptr) GQ_TRY(tmap(&m.ow, dW, k, C, lddw, 32));
   const int64_t tile = (int64_t)z.nkt * z.NK * kTile;
   const int64_t gy = z.Cp / 64 * z.npad;  // 64-class blocks of G, one after the other
   for (int i = 0; i <= z.pieces; ++i) {  // GRAD of piece i beside DX and DW of piece i - 1

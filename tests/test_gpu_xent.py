@@ -119,6 +119,14 @@ def test_long_sums_are_split(orc):
     _check(q, orc, _bf(40, 64, 3), _bf(60_000, 64, 4, 0.4), _labels(40, 60_000, 1.0, 2))
 
 
+def test_few_classes_many_rows(orc):
+    # tiles that hold every class, by turns to two warps; every row labelled,
+    # so that gradients leave in whole boxes
+    q = gq()
+    _check(q, orc, _bf(40_003, 72, 5), _bf(200, 72, 6, 0.4), _labels(40_003, 200, 1.0, 3), None, 1e-3)
+    _check(q, orc, _bf(20_481, 64, 7), _bf(3, 64, 8, 0.4), _labels(20_481, 3, 0.9, 4))
+
+
 def test_no_labelled_row():
     q = gq()
     X, W = _bf(300, 64, 1), _bf(500, 64, 2)
