@@ -29,9 +29,9 @@
 // at an odd pitch, 249 us aligned).
 //
 // Measured (GB300, copy rate 6.8 TB/s): dropout of 2,449,029 x 256 fp32 0.71 ms
-// (7.0 TB/s); backward of the same with ReLU and dropout 1.31 ms (5.8 TB/s);
+// (7.1 TB/s); backward of the same with ReLU and dropout 1.30 ms (5.9 TB/s);
 // forward of 131,072 x 256 fp32 with ReLU 47 us (5.7 TB/s); 30,001 x 4,099
-// bf16 with dropout, forward and backward, 437 us (2.8 TB/s).
+// bf16 with dropout, forward and backward, 430 us (2.9 TB/s).
 //
 // Dropout draws u(seed, row, column) from the library's counter hash (see
 // gq_quantize_pack) and keeps an element when u >= p, so the backward pass

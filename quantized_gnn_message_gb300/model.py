@@ -107,8 +107,11 @@ class GCNStack:
             self.dZ[self.L - 1] = torch.empty(n, r8(d), dtype=torch.bfloat16, device=device)
             self.ws_head = Workspace(device)
         L = lib()
-        self.ws.get(max(int(L.gq_gcn_layer_workspace_bytes(g.ref, widths[l], widths[l + 1], 2))
-                        for l in range(self.L)))
+        self.ws.get(max([int(L.gq_gcn_layer_workspace_bytes(g.ref, widths[l], widths[l + 1], 2))
+                         for l in range(self.L)] +
+                        [int(L.gq_layer_norm_bwd_workspace_bytes(n, widths[l + 1])) for l in hidden if norm]))
+        if classes:
+            self.ws_head.get(int(L.gq_linear_xent_workspace_bytes(n, widths[self.L], classes, 1)))
 
     def act(self, l: int) -> int:
         return ACT_RELU if l < self.L - 1 and not self.norm else ACT_NONE

@@ -281,3 +281,81 @@ def test_overflowing_variance_is_not_nan():
         beta = torch.ones(d, device="cuda")
         y, mean, rstd = q.layer_norm_fwd(x, None, beta)
         assert (rstd == 0).all() and (y == 1).all() and torch.isfinite(mean).all()
+
+
+@pytest.mark.parametrize("d", [17, 64, 300, 700, 2000])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_rows_that_start_anywhere(d, dtype):
+    """Column slices, whose rows start off the 16-byte grid, give bit for bit
+    what aligned copies give (sums run over the same lanes' columns in another
+    order: only what is elementwise is compared exactly, the rest by norm)."""
+    q = gq()
+    t = TYPES[dtype]
+    buf, _ = _mat(45, d + 9, 0, t, seed=d, off=0.5)
+    dbuf, _ = _mat(45, d + 9, 0, t, seed=d + 1)
+    x, dy = buf[:, 3:3 + d], dbuf[:, 5:5 + d]
+    assert torch.equal(q.dropout(x, 0.3, 5), q.dropout(x.contiguous(), 0.3, 5))
+    a = q.layer_norm_fwd(x, p=0.3, seed=5)
+    b = q.layer_norm_fwd(x.contiguous(), p=0.3, seed=5)
+    ga = q.layer_norm_bwd(dy, x, a[1], a[2], p=0.3, seed=5)
+    gb = q.layer_norm_bwd(dy.contiguous(), x.contiguous(), a[1], a[2], p=0.3, seed=5)
+    # one rounding of the type, and 40 of fp32 (the row sums' orders differ)
+    tol = torch.finfo(t).eps + 40 * U
+    for u, v in zip(a + ga, b + gb):
+        u, v = u.double(), v.double()
+        assert torch.linalg.norm(u - v) <= tol * torch.linalg.norm(v)
+
+
+@pytest.mark.parametrize("d", [40, 600, 9000])
+def test_everything_dropped_and_one_row(d):
+    q = gq()
+    x = synth.normal_matrix(1, d, seed=1, device="cuda")
+    dy = synth.normal_matrix(1, d, seed=2, device="cuda")
+    y, mean, rstd = q.layer_norm_fwd(x, beta=torch.ones(d, device="cuda"), p=1.0, seed=3)
+    assert not y.any() and abs(mean.item() - x.double().mean().item()) < 1e-6
+    dx, dg, db = q.layer_norm_bwd(dy, x, mean, rstd, p=1.0, seed=3)
+    assert not dx.any() and not dg.any() and not db.any()
+    # one row: dgamma and dbeta are the row's own terms
+    dx, dg, db = q.layer_norm_bwd(dy, x, mean, rstd)
+    assert torch.equal(db, dy[0])
+    xh = ((x.double() - mean.double()) * rstd.double())[0]
+    assert (dg.double() - dy[0].double() * xh).abs().max() <= 4 * U * (dy[0].double() * xh).abs().max()
+
+
+@pytest.mark.parametrize("d", [64, 100, 2000, 10000])
+def test_without_weight_gradients(d):
+    """gq_layer_norm_bwd with NULL dgamma and dbeta needs no workspace."""
+    q = gq()
+    x = synth.normal_matrix(70, d, seed=1, device="cuda")
+    dy = synth.normal_matrix(70, d, seed=2, device="cuda")
+    _, mean, rstd = q.layer_norm_fwd(x)
+    ref, dg, db = q.layer_norm_bwd(dy, x, mean, rstd)
+    dx = torch.empty_like(x)
+    p = q._ptr
+    q._check(q.lib().gq_layer_norm_bwd(p(dy), d, p(x), d, q.F32, 70, d, p(mean), p(rstd), None, q.ACT_NONE, 0.0, 0,
+                                       None, 0, p(dx), q.F32, d, None, None, None, 0, q._stream()), "bwd")
+    assert torch.equal(dx, ref)
+    # one of the two
+    only = torch.empty(d, device="cuda")
+    ws = torch.empty(int(q.lib().gq_layer_norm_bwd_workspace_bytes(70, d)), dtype=torch.uint8, device="cuda")
+    q._check(q.lib().gq_layer_norm_bwd(p(dy), d, p(x), d, q.F32, 70, d, p(mean), p(rstd), None, q.ACT_NONE, 0.0, 0,
+                                       None, 0, p(dx), q.F32, d, None, p(only), p(ws), ws.numel(), q._stream()), "bwd")
+    assert torch.equal(only, db)
+
+
+def test_two_streams_at_once():
+    q = gq()
+    x = synth.normal_matrix(20000, 256, seed=1, device="cuda")
+    dy = synth.normal_matrix(20000, 256, seed=2, device="cuda")
+    y, mean, rstd = q.layer_norm_fwd(x, p=0.2, seed=1)
+    ref = q.layer_norm_bwd(dy, x, mean, rstd, p=0.2, seed=1)
+    torch.cuda.synchronize()
+    outs = []
+    for st in (torch.cuda.Stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(st):
+            for _ in range(3):
+                a = q.layer_norm_fwd(x, p=0.2, seed=1)
+                outs.append((a[0], *q.layer_norm_bwd(dy, x, a[1], a[2], p=0.2, seed=1)))
+    torch.cuda.synchronize()
+    for o in outs:
+        assert all(torch.equal(a, b) for a, b in zip(o, (y, *ref)))

@@ -256,3 +256,25 @@ def test_refusals_of_the_binding():
                  lambda: q.linear_xent(X.t(), W, lab), lambda: q.linear_xent(X, W.cpu(), lab)):
         with pytest.raises(q.GQError):
             call()
+
+
+def test_rows_and_classes_off_the_grid_are_refused():
+    q = gq()
+    buf = torch.zeros(20, 32, dtype=torch.bfloat16, device="cuda")
+    lab = torch.zeros(20, dtype=torch.int32, device="cuda")
+    for X, W in ((buf[:, 1:17], buf[:, :16]), (buf[:, :16], buf[:, 4:20])):
+        with pytest.raises(q.GQError):
+            q.linear_xent(X, W, lab)
+
+
+def test_weights_and_the_same_class_everywhere(orc):
+    # one class takes every label; weights of both signs and zero
+    q = gq()
+    X, W = _bf(700, 48, 1), _bf(600, 48, 2, 0.3)
+    w = torch.linspace(-1.0, 1.0, 700, device="cuda")
+    w[100:200] = 0.0
+    _check(q, orc, X, W, torch.full((700,), 599, dtype=torch.int32, device="cuda"), w.abs(), 0.125)
+    a = q.linear_xent(X, W, torch.full((700,), 599, dtype=torch.int32, device="cuda"), w, 1.0)
+    b = q.linear_xent(X, W, torch.full((700,), 599, dtype=torch.int32, device="cuda"), -w, -1.0)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and torch.equal(a[2], b[2])
+    assert not a[1][100:200].any()
