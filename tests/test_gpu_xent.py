@@ -278,3 +278,32 @@ def test_weights_and_the_same_class_everywhere(orc):
     b = q.linear_xent(X, W, torch.full((700,), 599, dtype=torch.int32, device="cuda"), -w, -1.0)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and torch.equal(a[2], b[2])
     assert not a[1][100:200].any()
+
+
+@pytest.mark.parametrize("n,k,C,frac", [(5, 16384, 70, 1.0), (2, 64, 200_000, 1.0), (70_000, 8, 3000, 0.3),
+                                        (1, 256, 131_072, 1.0)])
+def test_long_axes(orc, n, k, C, frac):
+    q = gq()
+    _check(q, orc, _bf(n, k, 1), _bf(C, k, 2, 2.0 / np.sqrt(k)), _labels(n, C, frac, 3), None, 1.0 / n)
+
+
+def test_offsets_past_32_bits():
+    """X and dX of more than 2^32 elements: the last rows' losses and gradients
+    are those of a call on them alone (a row's depend on the row and W only)."""
+    q = gq()
+    n, k, C, last = (1 << 24) + 300, 264, 70, 333
+    X = torch.zeros(n, k, dtype=torch.bfloat16, device="cuda")
+    X[-last:] = _bf(last, k, 1)
+    W = _bf(C, k, 2, 0.2)
+    lab = torch.zeros(n, dtype=torch.int32, device="cuda")
+    lab[-last:] = torch.arange(last, dtype=torch.int32, device="cuda") % C
+    few = q.linear_xent(X[-last:], W, lab[-last:].contiguous())
+    loss, dX, _ = q.linear_xent(X, W, lab)  # every row labelled
+    assert torch.equal(loss[-last:], few[0]) and torch.equal(dX[-last:], few[1])
+    del dX
+    lab[:-last] = -1                        # none but the last
+    loss, dX, dW = q.linear_xent(X, W, lab)
+    assert torch.equal(loss[-last:], few[0]) and torch.equal(dX[-last:], few[1]) and not dX[:-last].any()
+    assert torch.linalg.norm((dW - few[2]).double()) <= 2.0 ** -7 * torch.linalg.norm(few[2].double())
+    del X, dX
+    torch.cuda.empty_cache()
