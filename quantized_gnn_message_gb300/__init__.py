@@ -484,12 +484,14 @@ def _like(t, ref, name, dtypes=None):
 
 
 def _rows_like(X):
-    """A new matrix of X's shape and type; where X's rows start 16-byte
-    aligned, so do the new one's (a view of a wider buffer if need be), and
+    """A new matrix of X's shape and type; where X's rows start 16-byte (or
+    4-byte) aligned, so do the new one's, at a wider pitch if need be, and
     calls on the two take the vector path."""
     e = X.element_size()
     n, d = X.shape
-    pitch = d if d * e % 16 == 0 or X.stride(0) * e % 16 or X.data_ptr() % 16 else (d * e + 15) // 16 * 16 // e
+    at = X.stride(0) * e | X.data_ptr()
+    a = (16 if at % 16 == 0 else 4 if at % 4 == 0 else e) // e
+    pitch = (d + a - 1) // a * a
     return torch.empty_strided((n, d), (pitch, 1), dtype=X.dtype, device=X.device)
 
 

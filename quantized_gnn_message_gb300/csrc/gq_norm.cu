@@ -24,9 +24,8 @@
 // kernel, so results do not depend on scheduling.
 //
 // Rows that start 16-byte aligned take the vector path; others are read and
-// written element by element, neighbouring lanes on neighbouring columns,
-// which costs about 1.8 times as long (30,001 x 4,096 bf16 backward: 458 us
-// at an odd pitch, 249 us aligned).
+// written element by element (16-bit ones of wide rows in pairs where rows
+// start 4-byte aligned), neighbouring lanes on neighbouring columns.
 //
 // Measured (GB300, copy rate 6.8 TB/s): dropout of 2,449,029 x 256 fp32 0.71 ms
 // (7.1 TB/s); backward of the same with ReLU and dropout 1.30 ms (5.9 TB/s);
@@ -96,7 +95,7 @@ __device__ __forceinline__ void load_vec(const T* p, int col, int d, float (&o)[
 // load: taking 16-bit elements apart would wait for them.
 template <typename T, int V>
 struct Raw {
-  uint32_t w[V * sizeof(T) == 16 ? 4 : V];
+  uint32_t w[V * sizeof(T) >= 4 ? V * sizeof(T) / 4 : 1];
 };
 template <typename T, int V>
 __device__ __forceinline__ void load_raw(const T* p, int col, int d, Raw<T, V>& o) {
@@ -104,6 +103,12 @@ __device__ __forceinline__ void load_raw(const T* p, int col, int d, Raw<T, V>& 
     if (col + V <= d) {
       const uint4 q = *reinterpret_cast<const uint4*>(p + col);
       o.w[0] = q.x, o.w[1] = q.y, o.w[2] = q.z, o.w[3] = q.w;
+      return;
+    }
+  }
+  if constexpr (V == 2 && sizeof(T) == 2) {
+    if (col + 2 <= d) {
+      o.w[0] = *reinterpret_cast<const uint32_t*>(p + col);
       return;
     }
   }
@@ -251,16 +256,17 @@ __global__ void __launch_bounds__(kNormThreads)
     dropout_kernel(const T* X, int64_t n, int d, int64_t ldx, const Drop dr, T* Y, int64_t ldy, int tpr, int rpb) {
   const int local = (int)threadIdx.x / tpr;
   if (local >= rpb) return;
-  const int64_t r0 = (int64_t)blockIdx.x * rpb * kDropRows + local;
+  constexpr int U = kDropRows;
+  const int64_t r0 = (int64_t)blockIdx.x * rpb * U + local;
   for (int col = ((int)threadIdx.x - local * tpr) * V; col < d; col += tpr * V) {
-    float v[kDropRows][V];
+    float v[U][V];
 #pragma unroll
-    for (int u = 0; u < kDropRows; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int64_t r = r0 + (int64_t)u * rpb;
       if (r < n) load_vec<T, V>(X + r * ldx, col, d, v[u]);
     }
 #pragma unroll
-    for (int u = 0; u < kDropRows; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int64_t r = r0 + (int64_t)u * rpb;
       if (r >= n) break;
       if (dr.on) {
@@ -269,6 +275,35 @@ __global__ void __launch_bounds__(kNormThreads)
         for (int j = 0; j < V; ++j) v[u][j] = kept(base, j, dr.lim) ? v[u][j] * dr.scale : 0.0f;
       }
       store_vec<T, V>(Y + r * ldy, col, d, v[u], true);
+    }
+  }
+}
+
+// Rows that start anywhere, d >= 32: a warp per row, eight elements of a lane
+// on their way at once.  2,449,029 x 251 bf16 0.50 ms, fp32 0.73 ms; the kernel
+// above hashes a row's key again for each element there, 1.26 ms in bf16.
+template <typename T>
+__global__ void __launch_bounds__(kNormThreads)
+    dropout_rows_kernel(const T* X, int64_t n, int d, int64_t ldx, const Drop dr, T* Y, int64_t ldy) {
+  constexpr int U = 8;
+  const int lane = threadIdx.x & 31;
+  const int64_t step = (int64_t)gridDim.x * (kNormThreads / 32);
+  for (int64_t r = (int64_t)blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5); r < n; r += step) {
+    const T* x = X + r * ldx;
+    T* y = Y + r * ldy;
+    const uint32_t kr = row_key(dr.key, (uint32_t)r);
+    for (int c = lane; c < d; c += 32 * U) {
+      float v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = c + 32 * u < d ? to_f(x[c + 32 * u]) : 0.0f;
+      if (dr.on) {
+        const uint32_t base = kr + (uint32_t)c * kColMul;
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = kept(base, 32 * u, dr.lim) ? v[u] * dr.scale : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (c + 32 * u < d) from_f(v[u], y + c + 32 * u);
     }
   }
 }
@@ -1005,8 +1040,14 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* __restri
 // ------------------------------------------------------------------- host --
 int type_bytes(int type) { return type == GQ_F32 ? 4 : (type == GQ_BF16 || type == GQ_F16) ? 2 : 0; }
 
-// Whether rows of this matrix can be read and written 16 bytes at a time.
-bool rows16(const void* p, int64_t ld, int type) { return aligned(p, 16) && ld * type_bytes(type) % 16 == 0; }
+// Elements at a time for rows of two matrices: 16 bytes, or two 16-bit ones,
+// where the rows of both start so aligned; else one.
+int vec_of(const void* p, int64_t ldp, const void* q, int64_t ldq, int type) {
+  const int e = type_bytes(type);
+  for (int v = 16 / e; v > 1; v = e == 2 && v > 2 ? 2 : 1)
+    if (aligned(p, v * e) && aligned(q, v * e) && ldp % v == 0 && ldq % v == 0) return v;
+  return 1;
+}
 
 int make_drop(double p, uint64_t seed, Drop* d) {
   if (!(p >= 0.0 && p <= 1.0)) return GQ_ERR_INVALID_ARG;
@@ -1051,9 +1092,15 @@ int bwd_blocks(int64_t n, int d) {
 }
 
 template <typename T>
-int launch_dropout(const void* X, int64_t n, int d, int64_t ldx, const Drop& dr, void* Y, int64_t ldy, bool vec,
+int launch_dropout(const void* X, int64_t n, int d, int64_t ldx, const Drop& dr, void* Y, int64_t ldy,
                    cudaStream_t s) {
-  const int V = vec ? 16 / (int)sizeof(T) : 1;
+  const int V = vec_of(X, ldx, Y, ldy, sizeof(T) == 4 ? GQ_F32 : GQ_BF16) * (int)sizeof(T) == 16 ? 16 / (int)sizeof(T) : 1;
+  if (V == 1 && d >= 32) {
+    const int64_t want = (n + kNormThreads / 32 - 1) / (kNormThreads / 32), cap = (int64_t)sm_count() * 64;
+    dropout_rows_kernel<T><<<(unsigned)(want < cap ? want : cap), kNormThreads, 0, s>>>(
+        static_cast<const T*>(X), n, d, ldx, dr, static_cast<T*>(Y), ldy);
+    return launch_status();
+  }
   const int vpr = (d + V - 1) / V;
   const int passes = (vpr + kNormThreads - 1) / kNormThreads;
   const int tpr = (vpr + passes - 1) / passes;
@@ -1061,12 +1108,9 @@ int launch_dropout(const void* X, int64_t n, int d, int64_t ldx, const Drop& dr,
   const int64_t blocks = (n + (int64_t)rpb * kDropRows - 1) / ((int64_t)rpb * kDropRows);
   if (blocks > 0x7fffffff) return GQ_ERR_UNSUPPORTED;
   const int threads = (tpr * rpb + 31) / 32 * 32;
-  if (vec)
-    dropout_kernel<T, 16 / sizeof(T)><<<(unsigned)blocks, threads, 0, s>>>(static_cast<const T*>(X), n, d, ldx, dr,
-                                                                          static_cast<T*>(Y), ldy, tpr, rpb);
-  else
-    dropout_kernel<T, 1><<<(unsigned)blocks, threads, 0, s>>>(static_cast<const T*>(X), n, d, ldx, dr,
-                                                             static_cast<T*>(Y), ldy, tpr, rpb);
+  auto kernel = V > 1 ? dropout_kernel<T, 16 / sizeof(T)> : dropout_kernel<T, 1>;
+  kernel<<<(unsigned)blocks, threads, 0, s>>>(static_cast<const T*>(X), n, d, ldx, dr, static_cast<T*>(Y), ldy, tpr,
+                                              rpb);
   return launch_status();
 }
 
@@ -1084,7 +1128,7 @@ template <typename T, int V, int NV, int G>
 int fwd_warp(const NormFwd& p, cudaStream_t s) {
   constexpr int rows = kNormThreads / G;
   const int64_t want = (p.n + rows - 1) / rows;
-  auto kernel = V > 1 && p.d == G * NV * V ? norm_fwd_warp_kernel<T, V, NV, G, (V > 1)>
+  auto kernel = V > 2 && p.d == G * NV * V ? norm_fwd_warp_kernel<T, V, NV, G, (V > 2)>
                                            : norm_fwd_warp_kernel<T, V, NV, G, false>;
   kernel<<<wave(kernel, 0, want), kNormThreads, 0, s>>>(p);
   return launch_status();
@@ -1092,7 +1136,8 @@ int fwd_warp(const NormFwd& p, cudaStream_t s) {
 
 template <typename T, int V>
 int fwd_any(const NormFwd& p, cudaStream_t s) {
-  if constexpr (V == 1) {
+  if constexpr (V == 2) {  // wide rows only, see fwd_typed
+  } else if constexpr (V == 1) {
     if (p.d <= 64) return fwd_warp<T, 1, 2, 32>(p, s);
     if (p.d <= 128) return fwd_warp<T, 1, 4, 32>(p, s);
     if (p.d <= 256) return fwd_warp<T, 1, 8, 32>(p, s);
@@ -1120,7 +1165,7 @@ template <typename T, typename TO, int V, int NV, int G>
 int bwd_warp(const NormBwd& p, int& blocks, cudaStream_t s) {
   constexpr int kWarps = kNormThreads / 32;
   const size_t sums = (size_t)kWarps * 2 * G * NV * V * sizeof(float);
-  if constexpr (V > 1) {
+  if constexpr (V > 2) {
     constexpr int S = NV > 2 ? 3 : 4;
     const size_t ring = (size_t)kWarps * S * 2 * NV * 32 * 16;
     const size_t smem = ring > sums ? ring : sums;
@@ -1149,7 +1194,8 @@ int bwd_wide(const NormBwd& p, int blocks, int threads, cudaStream_t s) {
 // `blocks`: at most this many, on return the number launched
 template <typename T, typename TO, int V>
 int bwd_any(const NormBwd& p, int& blocks, cudaStream_t s) {
-  if constexpr (V == 1) {
+  if constexpr (V == 2) {
+  } else if constexpr (V == 1) {
     if (p.d <= 64) return bwd_warp<T, TO, 1, 2, 32>(p, blocks, s);
     if (p.d <= 128) return bwd_warp<T, TO, 1, 4, 32>(p, blocks, s);
     if (p.d <= 256) return bwd_warp<T, TO, 1, 8, 32>(p, blocks, s);
@@ -1163,7 +1209,7 @@ int bwd_any(const NormBwd& p, int& blocks, cudaStream_t s) {
     if constexpr (V == 4)
       if (p.d <= 128 * V) return bwd_warp<T, TO, V, 4, 32>(p, blocks, s);
   }
-  if constexpr (V > 1) {
+  if constexpr (V > 2) {
     if (p.d <= 512 * kEpt) {
       const int threads = wide_threads(p.d), cap = wide_per_sm(threads) * sm_count();
       if (blocks > cap) blocks = cap;
@@ -1186,8 +1232,23 @@ int bwd_any(const NormBwd& p, int& blocks, cudaStream_t s) {
 }
 
 template <typename T, typename TO>
-int bwd_typed(const NormBwd& p, int& blocks, bool vec, cudaStream_t s) {
-  return vec ? bwd_any<T, TO, 16 / sizeof(T)>(p, blocks, s) : bwd_any<T, TO, 1>(p, blocks, s);
+int bwd_typed(const NormBwd& p, int& blocks, int vec, cudaStream_t s) {
+  if (vec > 2) return bwd_any<T, TO, 16 / sizeof(T)>(p, blocks, s);
+  if constexpr (sizeof(T) == 2)
+    if (vec == 2 && p.d > kWarpRowMax) return bwd_any<T, TO, 2>(p, blocks, s);
+  return bwd_any<T, TO, 1>(p, blocks, s);
+}
+
+// Pairs of 16-bit elements only for rows of a block (120,000 x 1,000 bf16 at a
+// pitch of 1,006: forward 290 -> 218 us, backward 495 -> 374 us); a lane of a
+// warp's row would hold more columns than one by one (300,000 x 334: forward
+// 190 -> 273 us, backward 240 -> 963 us).
+template <typename T>
+int fwd_typed(const NormFwd& p, int vec, cudaStream_t s) {
+  if (vec > 2) return fwd_any<T, 16 / sizeof(T)>(p, s);
+  if constexpr (sizeof(T) == 2)
+    if (vec == 2 && p.d > kWarpRowMax) return fwd_any<T, 2>(p, s);
+  return fwd_any<T, 1>(p, s);
 }
 
 }  // namespace
@@ -1204,11 +1265,10 @@ extern "C" int gq_dropout(const void* X, int type, int64_t n, int d, int64_t ldx
   if (n == 0) return GQ_OK;
   if (X == nullptr || Y == nullptr || !aligned(X, type_bytes(type)) || !aligned(Y, type_bytes(type)))
     return GQ_ERR_INVALID_ARG;
-  const bool vec = rows16(X, ldx, type) && rows16(Y, ldy, type);
   auto s = (cudaStream_t)stream;
-  if (type == GQ_F32) return launch_dropout<float>(X, n, d, ldx, dr, Y, ldy, vec, s);
-  if (type == GQ_BF16) return launch_dropout<__nv_bfloat16>(X, n, d, ldx, dr, Y, ldy, vec, s);
-  return launch_dropout<__half>(X, n, d, ldx, dr, Y, ldy, vec, s);
+  if (type == GQ_F32) return launch_dropout<float>(X, n, d, ldx, dr, Y, ldy, s);
+  if (type == GQ_BF16) return launch_dropout<__nv_bfloat16>(X, n, d, ldx, dr, Y, ldy, s);
+  return launch_dropout<__half>(X, n, d, ldx, dr, Y, ldy, s);
 }
 
 extern "C" int gq_layer_norm_fwd(const void* X, int type, int64_t n, int d, int64_t ldx, const float* gamma,
@@ -1241,11 +1301,11 @@ extern "C" int gq_layer_norm_fwd(const void* X, int type, int64_t n, int d, int6
   a.rstd = rstd;
   a.bits = relu_bits;
   a.ldrb = ldrb;
-  const bool vec = rows16(X, ldx, type) && rows16(Y, ldy, type);
+  const int vec = vec_of(X, ldx, Y, ldy, type);
   auto s = (cudaStream_t)stream;
-  if (type == GQ_F32) return vec ? fwd_any<float, 4>(a, s) : fwd_any<float, 1>(a, s);
-  if (type == GQ_BF16) return vec ? fwd_any<__nv_bfloat16, 8>(a, s) : fwd_any<__nv_bfloat16, 1>(a, s);
-  return vec ? fwd_any<__half, 8>(a, s) : fwd_any<__half, 1>(a, s);
+  if (type == GQ_F32) return fwd_typed<float>(a, vec, s);
+  if (type == GQ_BF16) return fwd_typed<__nv_bfloat16>(a, vec, s);
+  return fwd_typed<__half>(a, vec, s);
 }
 
 extern "C" size_t gq_layer_norm_bwd_workspace_bytes(int64_t n, int d) {
@@ -1298,10 +1358,9 @@ extern "C" int gq_layer_norm_bwd(const void* dY, int64_t lddy, const void* X, in
   a.dX = dX;
   a.lddx = lddx;
   a.partial = sums ? static_cast<float*>(ws) : nullptr;
-  const bool vec = rows16(X, ldx, type) && rows16(dY, lddy, type);
-  // bytes of one stored vector: 16 in the inputs' type, 8 for fp32 -> bf16
-  const int ob = type_bytes(dx_type) * 16 / esz;
-  a.vec_out = aligned(dX, ob) && lddx * type_bytes(dx_type) % ob == 0;
+  const int vec = vec_of(X, ldx, dY, lddy, type);
+  // a stored vector: as many elements, of dX's type
+  a.vec_out = aligned(dX, vec * type_bytes(dx_type)) && lddx % vec == 0;
   int blocks = bwd_blocks(n, d);
   if (type == GQ_F32 && dx_type == GQ_BF16)
     GQ_TRY((bwd_typed<float, __nv_bfloat16>(a, blocks, vec, s)));
