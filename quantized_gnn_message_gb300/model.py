@@ -99,6 +99,7 @@ class GCNStack:
                 self.dZ[l] = torch.empty(n, r8(widths[l + 1]), dtype=torch.bfloat16, device=device)
         self._drop = [None] * (self.L - 1)
         self._training = False
+        self._graded = False  # the last layer's dZ is the head's gradient on the latest forward pass
         if classes:
             d = widths[self.L]
             self.Hb = torch.empty(n, r8(d), dtype=torch.bfloat16, device=device)
@@ -128,6 +129,7 @@ class GCNStack:
         overwrites what a backward pass needs, so that one follows a training
         pass only."""
         self._training = training
+        self._graded = False
         h = X
         for l in range(self.L):
             ev = None if events is None else events[l]
@@ -155,9 +157,12 @@ class GCNStack:
     def backward(self, dY: torch.Tensor | None, Ws, bits: int, seeds, need_input_grad: bool = False, events=None,
                  norms=None):
         """Weight gradients from dY, or, with dY None, from the dZ that
-        loss_and_grad left for the last layer."""
+        loss_and_grad left for the last layer (refused where it has not run
+        since the latest forward pass)."""
         if dY is None and not self.classes:
             raise GQError("backward needs dY: the stack has no class head")
+        if dY is None and not self._graded:
+            raise GQError("backward without dY follows loss_and_grad on the latest forward pass")
         if self.p > 0.0 and not self._training:
             raise GQError("backward follows a training forward pass")
         g = dY
@@ -205,7 +210,9 @@ class GCNStack:
         """Per-node cross entropy; leaves the gradients of scale *
         sum(weight * loss) in dWc and, for backward(None, ...), in the last
         layer's dZ.  scale: 1 / (number of labelled nodes) for their mean."""
-        return self._head(Wc, labels, scale, weight, True)
+        loss = self._head(Wc, labels, scale, weight, True)
+        self._graded = True
+        return loss
 
     def launches(self, bits: int, need_input_grad: bool = False) -> int:
         """Kernels of one forward and backward pass, the class head's not
