@@ -85,7 +85,7 @@ class GCNStack:
         # what stands between the hidden layers: the next layer's input, the
         # row statistics, the ReLU bits, the bf16 dZ that normalization's
         # backward pass hands the layer, and the dropout seeds of the last
-        # training forward pass
+        # forward pass
         hidden = range(self.L - 1)
         e32 = lambda *shape: torch.empty(*shape, dtype=torch.float32, device=device)
         self.N = [e32(n, widths[l + 1]) if norm or p > 0.0 else None for l in hidden]
@@ -126,8 +126,8 @@ class GCNStack:
 
     def forward(self, X: torch.Tensor, Ws, bits: int, seeds, events=None, norms=None, training: bool = True):
         """The last layer's output.  training = False leaves dropout out; it
-        overwrites what a backward pass needs, so that one follows a training
-        pass only."""
+        overwrites what a backward pass needs, so that with p > 0 one follows
+        a training pass only."""
         self._training = training
         self._graded = False
         h = X
@@ -142,9 +142,7 @@ class GCNStack:
                 continue
             p = self.p if training else 0.0
             # the layer's quantizer draws its noise from the same seed
-            seed = seeds[l] ^ DROPOUT_SEED_TAG
-            if training:
-                self._drop[l] = seed
+            seed = self._drop[l] = seeds[l] ^ DROPOUT_SEED_TAG
             if self.norm:
                 gamma, beta = self._norm_of(norms, l)
                 layer_norm_fwd(h, gamma, beta, act=ACT_RELU, p=p, seed=seed, out=self.N[l], mean=self.mean[l],

@@ -57,3 +57,18 @@ def test_backward_from_the_head_follows_loss_and_grad(stack):
     with pytest.raises(err):
         m.backward(None, WS, 32, [3, 4])       # the gradient is the last step's
     m.backward(torch.zeros(5, 8), WS, 32, [3, 4])  # a gradient of the caller's own
+
+
+def test_normalized_stack_without_dropout_goes_backward_from_an_evaluation_pass(stack):
+    # with p = 0 the evaluation pass is the training pass
+    err, make = stack
+    m = make(norm=True)
+    m.forward(X, WS, 32, [1, 2], training=False)
+    m.backward(torch.zeros(5, 8), WS, 32, [3, 4])
+    (call,) = [c for c in m.calls if c[0] == "layer_norm_bwd"]
+    (fwd,) = [c for c in m.calls if c[0] == "layer_norm_fwd"]
+    assert call[2]["p"] == fwd[2]["p"] == 0.0 and call[2]["seed"] == fwd[2]["seed"]
+    m = make(norm=True, p=0.5)
+    m.forward(X, WS, 32, [1, 2], training=False)
+    with pytest.raises(err):
+        m.backward(torch.zeros(5, 8), WS, 32, [3, 4])
