@@ -98,8 +98,9 @@ class GCNStack:
                 self.Rb[l] = torch.empty(n, (widths[l + 1] + 31) // 32, dtype=torch.int32, device=device)
                 self.dZ[l] = torch.empty(n, r8(widths[l + 1]), dtype=torch.bfloat16, device=device)
         self._drop = [None] * (self.L - 1)
-        self._training = False
-        self._graded = False  # the last layer's dZ is the head's gradient on the latest forward pass
+        # of the latest forward pass: it dropped, it had normalization weights,
+        # the last layer's dZ is the head's gradient on it
+        self._training = self._weighted = self._graded = False
         if classes:
             d = widths[self.L]
             self.Hb = torch.empty(n, r8(d), dtype=torch.bfloat16, device=device)
@@ -130,6 +131,7 @@ class GCNStack:
         a training pass only."""
         self._training = training
         self._graded = False
+        self._weighted = norms is not None
         h = X
         for l in range(self.L):
             ev = None if events is None else events[l]
@@ -163,6 +165,8 @@ class GCNStack:
             raise GQError("backward without dY follows loss_and_grad on the latest forward pass")
         if self.p > 0.0 and not self._training:
             raise GQError("backward follows a training forward pass")
+        if self.norm and self._weighted != (norms is not None):
+            raise GQError("norms: backward takes the normalization weights of the forward pass, if it had any")
         g = dY
         for l in reversed(range(self.L)):
             need = need_input_grad or l > 0

@@ -72,3 +72,16 @@ def test_normalized_stack_without_dropout_goes_backward_from_an_evaluation_pass(
     m.forward(X, WS, 32, [1, 2], training=False)
     with pytest.raises(err):
         m.backward(torch.zeros(5, 8), WS, 32, [3, 4])
+
+
+def test_backward_takes_the_weights_that_forward_took(stack):
+    err, make = stack
+    pair = [(torch.ones(8), torch.zeros(8))]
+    m = make(norm=True)
+    for given, missing in ((pair, None), (None, pair)):
+        m.forward(X, WS, 32, [1, 2], norms=given)
+        with pytest.raises(err):
+            m.backward(torch.zeros(5, 8), WS, 32, [3, 4], norms=missing)
+        m.backward(torch.zeros(5, 8), WS, 32, [3, 4], norms=given)
+    gammas = [c[1][4] for c in m.calls if c[0] == "layer_norm_bwd"]
+    assert len(gammas) == 2 and gammas[0] is pair[0][0] and gammas[1] is None
