@@ -34,7 +34,8 @@ typedef enum { GQ_F32 = 0, GQ_BF16 = 1, GQ_F16 = 2 } gq_type;
  *   p      in [0, 1]; 1 drops everything
  *   Y      may be X (ldy == ldx)
  * Errors: GQ_ERR_INVALID_ARG (bad type, p, n < 0, n >= 2^32, d < 1, short
- * leading dimension, null or misaligned pointers); n == 0 is a no-op.
+ * leading dimension, null or misaligned pointers); GQ_ERR_UNSUPPORTED for
+ * d > 2^31 - 4096; n == 0 is a no-op.
  * ---------------------------------------------------------------------- */
 #define GQ_DROPOUT_SEED_TAG 0xD6E8FEB86659FD93ULL
 GQ_API int gq_dropout(const void* X, int type, int64_t n, int d, int64_t ldx, double p, uint64_t seed, void* Y,

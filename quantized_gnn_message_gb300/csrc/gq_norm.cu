@@ -55,6 +55,9 @@ constexpr int kEpt = 16;           // elements of a row per lane or thread
 constexpr int kWarpRowMax = 512;   // rows up to here are one warp's (or less)
 constexpr int kMaxWidth = 16384;   // 1024 threads x 16 elements
 constexpr int kNormThreads = 256;
+// dropout's columns are counted in 31 bits; a thread's next ones are up to
+// 256 threads x 8 elements further
+constexpr int kMaxDropWidth = 0x7fffffff - 4095;
 
 // 1 / sqrt(v): the hardware estimate and one Newton step (2 ulp), a fifth of
 // the instructions of a rounded root and quotient.
@@ -1262,6 +1265,7 @@ extern "C" int gq_dropout(const void* X, int type, int64_t n, int d, int64_t ldx
   if (type_bytes(type) == 0 || n < 0 || n > (int64_t)UINT32_MAX || d < 1 || ldx < d || ldy < d)
     return GQ_ERR_INVALID_ARG;
   GQ_TRY(make_drop(p, seed, &dr));
+  if (d > kMaxDropWidth) return GQ_ERR_UNSUPPORTED;
   if (n == 0) return GQ_OK;
   if (X == nullptr || Y == nullptr || !aligned(X, type_bytes(type)) || !aligned(Y, type_bytes(type)))
     return GQ_ERR_INVALID_ARG;
