@@ -138,11 +138,13 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-// Arrival on a barrier of either CTA.  CTA scope: what the arrivals order are
-// reads of this thread (of a posted unit, of an accumulator by tcgen05.ld
-// behind its own fence), not global writes, and a release at cluster scope
-// costs a memory barrier each time (a quarter of the warps' stalls; loss and
-// gradients of 16,384 x 256 x 131,072 classes 4.93 -> 4.67 ms without it).
+// Arrival on a barrier of either CTA.  CTA scope: what the arrivals follow are
+// reads of this warp, not global writes, and a release at cluster scope costs
+// a memory barrier each time (a quarter of the warps' stalls; loss and
+// gradients of 16,384 x 256 x 131,072 classes 4.93 -> 4.67 ms without it).  At
+// this scope the arrival orders nothing that the other CTA sees, so what has
+// been read must be in registers before it: a posted unit by a branch on its
+// value (Feed::next), an accumulator by tcgen05.wait::ld.
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -313,12 +315,18 @@ struct Feed {
   __device__ __forceinline__ int next(volatile int* abort, int* err, int64_t units) {
     if (!wait(&full[slot], phase, abort, err, 21)) return -1;
     const int u = unit[slot];
+    // Behind the last unit nothing is posted, and its slot is not given back.
+    // The branch on u is also what keeps the arrival behind the read: the
+    // arrival alone would not wait for it, and with shared memory's queue full
+    // of an epilogue's global accesses the next unit could overtake the read
+    // (the odd CTA's, whose slots another SM fills).
+    if (u >= units) return -1;
     arrive_cluster(empty0 + slot * 8);
     if (++slot == kSlots) {
       slot = 0;
       phase ^= 1;
     }
-    return u < units ? u : -1;
+    return u;
   }
 };
 
