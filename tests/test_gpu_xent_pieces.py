@@ -1,6 +1,6 @@
 """gq_linear_xent where G takes several pieces of 1 GB (sums carried from piece
-to piece, two buffers of G, a shorter last piece, split sums), against the
-formulas in 64 bits.
+to piece, two buffers of G, a shorter last piece, split sums) and over the
+longest contraction, against the formulas in 64 bits.
 
 Bounds, h = 2^-8 half a step of bf16, relative:
   a sum of m products on the tensor cores takes m / 16 additions, each off by
@@ -137,6 +137,12 @@ def test_several_pieces(n, k, C, frac):
     weight = torch.rand(n, device="cuda") + 0.5 if frac < 1 else None
     _check(q, _bf(n, k, 1), _bf(C, k, 2, 2 / k ** 0.5), _labels(n, C, frac, 3), weight, 1.0)
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("n,k,C", [(5, 16384, 70), (300, 16384, 300), (300, 8192, 47)])
+def test_longest_contraction(n, k, C):
+    q = gq()
+    _check(q, _bf(n, k, 1), _bf(C, k, 2, 2 / k ** 0.5), _labels(n, C, 0.9, 3))
 
 
 @pytest.mark.parametrize("n,k,C", [(1_500_000, 8, 520), (1_200_000, 24, 600)])
