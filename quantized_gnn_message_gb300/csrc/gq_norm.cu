@@ -608,14 +608,22 @@ __device__ __forceinline__ void gate_dz(const NormBwd& p, uint32_t w, uint32_t k
   }
 }
 
+// The factor of x - mean in xhat: rstd, or 0 for a constant row whose
+// mean rstd is beyond fp32 (a row that varies at all has mean rstd below
+// 2^24 sqrt(d)).  Its x are the mean, xhat 0; but past the row's end x = 0, and
+// an infinite xhat there would make the sums' 0 xhat NaN.
+__device__ __forceinline__ float xhat_scale(float mean, float rstd) {
+  return rstd < INFINITY && !(fabsf(mean * rstd) < INFINITY) ? 0.0f : rstd;
+}
+
 // The backward arithmetic of E (even) elements of a row, two at a time:
-// xh = (x - mean) rstd over x; g = dz gamma over dz; column sums; s1, s2 the
+// xh = (x - mean) xs over x; g = dz gamma over dz; column sums; s1, s2 the
 // row's sums of g and g xh.  Elements past the row have dz = 0 and add
 // nothing.
 template <int E>
 __device__ __forceinline__ void bwd_terms(float* x, float* dz, const float* ga, float* sg, float* sb, float mean,
-                                          float rstd, float& s1, float& s2) {
-  const float2 nm = make_float2(-mean, -mean), rs = make_float2(rstd, rstd);
+                                          float xs, float& s1, float& s2) {
+  const float2 nm = make_float2(-mean, -mean), rs = make_float2(xs, xs);
   float2 a = make_float2(0.0f, 0.0f), b = a;
 #pragma unroll
   for (int e = 0; e < E; e += 2) {
@@ -751,7 +759,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_ring_kernel(const NormB
 #pragma unroll
     for (int i = 0; i < NV; ++i) gate_dz<V>(p, wb[i], kr, c0 + i * G * V, dz + i * V);
     float s1 = 0.0f, s2 = 0.0f;
-    bwd_terms<E>(xv, dz, ga, sg, sb, mean, rstd, s1, s2);
+    bwd_terms<E>(xv, dz, ga, sg, sb, mean, xhat_scale(mean, rstd), s1, s2);
     const float m1 = over(group_sum<G>(s1), p.dv), m2 = over(group_sum<G>(s2), p.dv);
     bwd_out<E>(dz, xv, m1, m2, rstd);
 #pragma unroll
@@ -825,7 +833,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_warp_kernel(const NormB
 #pragma unroll
     for (int i = 0; i < NV; ++i) gate_dz<V>(p, wb[i], kr, c0 + i * G * V, dz + i * V);
     float s1 = 0.0f, s2 = 0.0f;
-    bwd_terms<E>(xv, dz, ga, sg, sb, mean, rstd, s1, s2);
+    bwd_terms<E>(xv, dz, ga, sg, sb, mean, xhat_scale(mean, rstd), s1, s2);
     const float m1 = over(group_sum<G>(s1), p.dv), m2 = over(group_sum<G>(s2), p.dv);
     bwd_out<E>(dz, xv, m1, m2, rstd);
 #pragma unroll
@@ -873,7 +881,7 @@ __global__ void __launch_bounds__(1024, 1) norm_bwd_block_kernel(const NormBwd p
   fetch(r);
   __syncthreads();
   for (; r < p.n; r += gridDim.x) {
-    const float mean = nm, rstd = nr;
+    const float mean = nm, rstd = nr, xs = xhat_scale(mean, rstd);
     const uint32_t kr = row_key(p.dr.key, (uint32_t)r);
     float xh[EPT], g[EPT];
     uint32_t wb[NV];
@@ -897,7 +905,7 @@ __global__ void __launch_bounds__(1024, 1) norm_bwd_block_kernel(const NormBwd p
         load_shared<V>(acc + W + col, sb + k);
         load_shared<V>(acc + 2 * W + col, ga + k);
       }
-      bwd_terms<S>(xh + e, g + e, ga, sg, sb, mean, rstd, s1, s2);
+      bwd_terms<S>(xh + e, g + e, ga, sg, sb, mean, xs, s1, s2);
 #pragma unroll
       for (int k = 0; k < S; k += V) {
         const int col = c0 + (e + k) / V * cs;
@@ -974,7 +982,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_wide_kernel(const NormBwd
   __syncthreads();
   int slot = 0, flip = 0;
   for (; r < p.n; r += gridDim.x) {
-    const float mean = nm, rstd = nr;
+    const float mean = nm, rstd = nr, xs = xhat_scale(mean, rstd);
     float xv[kEpt], dz[kEpt];
     uint32_t wb[NV];
     copy_wait<S - 2>();
@@ -995,7 +1003,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_wide_kernel(const NormBwd
       float ga[V];
       gate_dz<V>(p, wb[i], kr, c0 + i * cs, dz + i * V);
       load_shared<V>(gam + c0 + i * cs, ga);
-      bwd_terms<V>(xv + i * V, dz + i * V, ga, sg + i * V, sb + i * V, mean, rstd, s1, s2);
+      bwd_terms<V>(xv + i * V, dz + i * V, ga, sg + i * V, sb + i * V, mean, xs, s1, s2);
     }
     const float2 s = block_sum2(s1, s2, red[flip]);
     flip ^= 1;

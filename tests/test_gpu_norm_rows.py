@@ -96,3 +96,28 @@ def test_many_rows_of_a_block(orc, n, d, dtype, pitch):
 @pytest.mark.parametrize("pad", [0, 1])
 def test_many_rows_of_a_group(orc, n, d, dtype, pad):
     _both_ways(gq(), orc, n, d, pad, TYPES[dtype], d > 64, 0.25, d, 1000)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [5, 21, 47, 133, 301, 515, 2_051, 9_001])
+def test_constant_rows_of_huge_values(d, dtype):
+    """A constant row has xhat = 0: dx = rstd (g - mean g), dgamma = 0.  The
+    lanes past its end must add nothing either, although (0 - mean) rstd is
+    beyond fp32 there: mean 2^113 and rstd = 1 / sqrt(1e-10) = 1e5.  (Sums of
+    d times a power of two are exact, and the longest is within fp32.)"""
+    q = gq()
+    t, n, eps = TYPES[dtype], 70, 1e-10
+    ld = (d + 7) // 8 * 8 + 8
+    buf = torch.full((n, ld), 2.0 ** 113, dtype=t, device="cuda")
+    dbuf = synth.normal_matrix(n, ld, seed=d, device="cuda").to(t)
+    for first in (0, 1):  # whole vectors, single elements
+        x, dy = buf[:, first:first + d], dbuf[:, first:first + d]
+        y, mean, rstd = q.layer_norm_fwd(x, eps=eps)
+        assert not y.any() and torch.equal(mean, x[:, 0].float())
+        dx, dgamma, dbeta = q.layer_norm_bwd(dy, x, mean, rstd)
+        assert torch.isfinite(dx).all() and not dgamma.any()
+        g = dy.double()
+        ref = rstd.double()[:, None] * (g - g.mean(1, keepdim=True))
+        tol = rstd.double()[:, None] * U * (6 * g.abs() + 34 * g.abs().mean(1, keepdim=True))
+        assert ((dx.double() - ref).abs() <= tol + torch.finfo(t).eps / 2 * ref.abs() * (1 + 1e-3)).all()
+        assert ((dbeta.double() - g.sum(0)).abs() <= (n + 100) * U * g.abs().sum(0)).all()
