@@ -1082,9 +1082,13 @@ int block_rows_per_sm(int threads, size_t smem) {
 // flight within 64 registers; beyond 1024 threads, 16.
 int bwd_ept(int d) { return d <= 8192 ? 8 : 16; }
 
-// Threads and resident blocks per SM of norm_bwd_wide_kernel.
+// Threads of norm_bwd_wide_kernel, and the most that it is built for two
+// blocks per SM with: it needs 112 registers a thread, of which an SM has
+// 65,536 (2 x 112 x 288 = 64,512).  Resident blocks as far as registers go;
+// fp32 rows are fewer, by shared memory.
 int wide_threads(int d) { return ((d + kEpt - 1) / kEpt + 31) / 32 * 32; }
-int wide_per_sm(int threads) { return threads <= 288 ? 576 / threads : 1; }
+constexpr int kPairThreads = 288;
+int wide_per_sm(int threads) { return threads <= kPairThreads ? 2 * kPairThreads / threads : 1; }
 
 // Upper bound of the backward's blocks, one partial row of sums each.
 int bwd_blocks(int64_t n, int d) {
@@ -1126,11 +1130,12 @@ int launch_dropout(const void* X, int64_t n, int d, int64_t ldx, const Drop& dr,
 }
 
 // Blocks of a persistent kernel: as many as are resident at once (one wave;
-// 2.7 waves of 8 blocks per SM cost the 131,072 x 256 forward pass a tenth).
+// 2.7 waves of 8 blocks per SM cost the 131,072 x 256 forward pass a tenth), at
+// most `want`.
 template <typename K>
-int wave(K kernel, size_t smem, int64_t want) {
+int wave(K kernel, int threads, size_t smem, int64_t want) {
   int per = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kNormThreads, smem) != cudaSuccess || per < 1) per = 1;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem) != cudaSuccess || per < 1) per = 1;
   const int64_t cap = (int64_t)per * sm_count();
   return (int)(want < cap ? want : cap);
 }
@@ -1141,7 +1146,7 @@ int fwd_warp(const NormFwd& p, cudaStream_t s) {
   const int64_t want = (p.n + rows - 1) / rows;
   auto kernel = V > 2 && p.d == G * NV * V ? norm_fwd_warp_kernel<T, V, NV, G, (V > 2)>
                                            : norm_fwd_warp_kernel<T, V, NV, G, false>;
-  kernel<<<wave(kernel, 0, want), kNormThreads, 0, s>>>(p);
+  kernel<<<wave(kernel, kNormThreads, 0, want), kNormThreads, 0, s>>>(p);
   return launch_status();
 }
 
@@ -1182,23 +1187,36 @@ int bwd_warp(const NormBwd& p, int& blocks, cudaStream_t s) {
     const size_t smem = ring > sums ? ring : sums;
     auto kernel = norm_bwd_ring_kernel<T, TO, V, NV, G, S>;
     GQ_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-    blocks = wave(kernel, smem, blocks);
+    blocks = wave(kernel, kNormThreads, smem, blocks);
     kernel<<<blocks, kNormThreads, smem, s>>>(p);
   } else {
     auto kernel = norm_bwd_warp_kernel<T, TO, V, NV, G>;
-    blocks = wave(kernel, sums, blocks);
+    blocks = wave(kernel, kNormThreads, sums, blocks);
     kernel<<<blocks, kNormThreads, sums, s>>>(p);
   }
   return launch_status();
 }
 
 template <typename T, typename TO, int V, int MAXT, int MINB>
-int bwd_wide(const NormBwd& p, int blocks, int threads, cudaStream_t s) {
+int bwd_wide(const NormBwd& p, int& blocks, int threads, cudaStream_t s) {
   constexpr int S = 3;
   constexpr int kBytes = S * 2 * (kEpt / V) * 16 + kEpt * (int)sizeof(float);  // per thread
   auto kernel = norm_bwd_wide_kernel<T, TO, V, S, MAXT, MINB>;
   GQ_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAXT * kBytes));
+  blocks = wave(kernel, threads, threads * kBytes, blocks);
   kernel<<<blocks, threads, threads * kBytes, s>>>(p);
+  return launch_status();
+}
+
+template <typename T, typename TO, int V, int EPT>
+int bwd_block(const NormBwd& p, int& blocks, cudaStream_t s) {
+  const int threads = ((p.d + EPT - 1) / EPT + 31) / 32 * 32;
+  const size_t smem = (size_t)3 * threads * EPT * sizeof(float);
+  auto kernel = norm_bwd_block_kernel<T, TO, V, EPT>;
+  GQ_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   3 * 1024 * EPT * (int)sizeof(float)));
+  blocks = wave(kernel, threads, smem, blocks);
+  kernel<<<blocks, threads, smem, s>>>(p);
   return launch_status();
 }
 
@@ -1220,26 +1238,14 @@ int bwd_any(const NormBwd& p, int& blocks, cudaStream_t s) {
     if constexpr (V == 4)
       if (p.d <= 128 * V) return bwd_warp<T, TO, V, 4, 32>(p, blocks, s);
   }
+  if (p.d > 8192) return bwd_block<T, TO, V, 16>(p, blocks, s);
   if constexpr (V > 2) {
-    if (p.d <= 512 * kEpt) {
-      const int threads = wide_threads(p.d), cap = wide_per_sm(threads) * sm_count();
-      if (blocks > cap) blocks = cap;
-      return threads <= 288 ? bwd_wide<T, TO, V, 288, 2>(p, blocks, threads, s)
-                            : bwd_wide<T, TO, V, 512, 1>(p, blocks, threads, s);
-    }
-  }
-  const int ept = bwd_ept(p.d), threads = ((p.d + ept - 1) / ept + 31) / 32 * 32;
-  const size_t smem = (size_t)3 * threads * ept * sizeof(float);
-  if (ept == 8) {
-    GQ_TRY_CUDA(cudaFuncSetAttribute(norm_bwd_block_kernel<T, TO, V, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     3 * 8192 * (int)sizeof(float)));
-    norm_bwd_block_kernel<T, TO, V, 8><<<blocks, threads, smem, s>>>(p);
+    const int threads = wide_threads(p.d);
+    return threads <= kPairThreads ? bwd_wide<T, TO, V, kPairThreads, 2>(p, blocks, threads, s)
+                                   : bwd_wide<T, TO, V, 512, 1>(p, blocks, threads, s);
   } else {
-    GQ_TRY_CUDA(cudaFuncSetAttribute(norm_bwd_block_kernel<T, TO, V, 16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     3 * kMaxWidth * (int)sizeof(float)));
-    norm_bwd_block_kernel<T, TO, V, 16><<<blocks, threads, smem, s>>>(p);
+    return bwd_block<T, TO, V, 8>(p, blocks, s);
   }
-  return launch_status();
 }
 
 template <typename T, typename TO>
