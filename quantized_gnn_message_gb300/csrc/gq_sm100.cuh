@@ -205,7 +205,9 @@ int launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaS
   c.stream = s;
   c.attrs = &at;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...) == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
+  if (cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...) == cudaSuccess) return GQ_OK;
+  (void)cudaGetLastError();  // reported here; the next call's check must not find it again
+  return GQ_ERR_CUDA;
 }
 
 // ---- packed fp32 ------------------------------------------------------------
