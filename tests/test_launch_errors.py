@@ -1,16 +1,28 @@
 """launch_after (gq_sm100.cuh) reports a launch that the runtime refuses and
 takes the error from it, so that the next call of the library, or of anything
-else in the process, does not report it again.  The launch is refused on any
-machine: by its block size, or for want of a device."""
+else in the process, does not report it again.  Host code with a fake of the
+runtime's launch and error calls."""
 import subprocess
 
 SOURCE = r"""
-#include "gq_sm100.cuh"
+#include <cuda.h>
+#include <cuda_runtime.h>
 #include <cstdio>
-__global__ void kernel(int) {}
+static cudaError_t refuse = cudaErrorInvalidConfiguration, last = cudaSuccess;
+template <typename... A>
+static cudaError_t fake_launch(A&&...) { return refuse == cudaSuccess ? refuse : last = refuse; }
+static cudaError_t fake_last() { const cudaError_t e = last; last = cudaSuccess; return e; }
+#define cudaLaunchKernelEx fake_launch
+#define cudaGetLastError fake_last
+#include "gq_sm100.cuh"
+static void kernel(int) {}
 int main() {
-  const int status = gq::launch_after(kernel, dim3(1), dim3(2048), 0, nullptr, 1);
-  std::printf("%d %d", status, (int)cudaPeekAtLastError());
+  int status = gq::launch_after(kernel, dim3(1), dim3(2048), 0, nullptr, 1);
+  std::printf("%d %d ", status, (int)last);
+  refuse = cudaSuccess;
+  last = cudaErrorInvalidValue;  // of an earlier call: not this one's to take
+  status = gq::launch_after(kernel, dim3(1), dim3(32), 0, nullptr, 1);
+  std::printf("%d %d", status, (int)last);
   return 0;
 }
 """
@@ -23,5 +35,5 @@ def test_a_refused_launch_leaves_no_error_behind(tmp_path):
     subprocess.run([build._nvcc(), *build.ARCH, "-std=c++17", "-I" + build.INCLUDE, "-I" + build.CSRC, str(src), "-o",
                     str(exe)], check=True, capture_output=True)
     out = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout
-    status, left = map(int, out.split())
-    assert status == 4 and left == 0  # GQ_ERR_CUDA, cudaSuccess
+    # GQ_ERR_CUDA and nothing left behind; GQ_OK and cudaErrorInvalidValue
+    assert out.split() == ["4", "0", "0", "1"]
