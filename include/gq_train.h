@@ -101,11 +101,15 @@ GQ_API int gq_layer_norm_bwd(const void* dY, int64_t lddy, const void* X, int64_
  *   bf16 matrices: 16-byte aligned, leading dimension a multiple of 8;
  *           columns past k are neither read as values nor written
  *   ws      gq_linear_xent_workspace_bytes(n, k, C, need_grad) bytes,
- *           256-byte aligned, need_grad != 0 when dX or dW is given: about
- *           2 n k bytes, with gradients two pieces of G (2 n c bytes each, c
- *           classes a piece: at most 1 GB, but no fewer than C or 256
- *           classes) and, where sums are split or carried from piece to
- *           piece, 4 n k bytes more.  It depends on the current device's SM
+ *           256-byte aligned, need_grad != 0 when dX or dW is given.  With n
+ *           and k rounded up to multiples of 256 and 8: 2 n k + 16 n bytes;
+ *           for t = ceil(C / 256) > 1 another 4 n + 16 n ceil(t / run), where
+ *           run = n t / (1024 SMs), at least 1 and at most 16; with gradients
+ *           two pieces of G (2 n c bytes each, c classes a piece: at most
+ *           1 GB, but no fewer than C or 256 classes; one if it holds every
+ *           class), 16 n for t > 1 and, where sums are split or carried from
+ *           piece to piece, 4 n k bytes for each split of dX's, 4 c k of dW's
+ *           (k a multiple of 128).  It depends on the current device's SM
  *           count.  Calls sharing one workspace must not overlap.
  *   dev_err nullable device int, as for the GEMMs (codes 21 .. 26)
  * Results are the same from run to run.  dX and dW must not overlap X or W.

@@ -1104,10 +1104,12 @@ Carve carve(void* ws, size_t bytes, const Sizes& z, int64_t n, int k, bool grad,
   w.idx = static_cast<int*>(c.take((size_t)z.npad * 4));
   w.lab = static_cast<int*>(c.take((size_t)z.npad * 4));
   w.wrow = static_cast<float*>(c.take((size_t)z.npad * 4));
-  w.row = static_cast<float4*>(c.take((size_t)z.npad * 16));
-  w.zlab = static_cast<float*>(c.take((size_t)z.npad * 4));
-  w.part = static_cast<float2*>(c.take((size_t)z.units * kParts * z.npad * sizeof(float2)));
   w.Xc = c.take((size_t)z.npad * round8(k) * 2);
+  if (z.ctiles > 1) {  // WHOLE tiles keep these to themselves
+    w.zlab = static_cast<float*>(c.take((size_t)z.npad * 4));
+    w.part = static_cast<float2*>(c.take((size_t)z.units * kParts * z.npad * sizeof(float2)));
+    if (grad) w.row = static_cast<float4*>(c.take((size_t)z.npad * 16));
+  }
   if (!grad) return c;
   w.G[0] = c.take((size_t)z.npad * z.Cp * 2);
   w.G[1] = z.pieces > 1 ? c.take((size_t)z.npad * z.Cp * 2) : w.G[0];
