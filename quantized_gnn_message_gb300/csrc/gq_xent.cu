@@ -112,7 +112,8 @@ struct Args {
   const int* lab;
   float* loss;           // per row of X, nullable
   float* lse;
-  const float4* row;     // r, weight / sum of 2^(z L - r), G of the label, label (as int)
+  const float4* row;     // r, weight / sum of 2^(z L - r), weight, label (as int)
+  float* zlab;           // per labelled row, by STATS: the label's logit
   const int* idx;        // labelled row -> row of X
   float2* part;          // [unit * kParts + part][npad]: r, sum
   float* accX;           // [split][row tile][nkt NK][256]
@@ -543,6 +544,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int row = t.rt * kTile + rit;
       if (row < q.nl) {
         if (KIND == PIECE && t.mode == GRAD) rwn = p.row[row];
+        if (KIND == LOSSES) rwn.w = __int_as_float(p.lab[row]);
         if (KIND == ONE_TILE)
           rwn = make_float4(0.0f, p.wrow[row], __int_as_float(p.idx[row]), __int_as_float(p.lab[row]));
       }
@@ -569,15 +571,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (KIND != PIECE) {
           float zl = 0.0f;
           const int lab = __float_as_int(rw.w);
+          // most tiles hold the label of none of a warp's rows
+          const bool hit = KIND == ONE_TILE || __any_sync(gq::FULL, (unsigned)(lab - t.ct * p.NT) < (unsigned)t.N);
           for (int c = KIND == ONE_TILE ? 0 : part * 32; c < t.N; c += KIND == ONE_TILE ? 32 : 32 * kParts) {
             float v[32];
             tmem_ld32(taddr + c, v);
             tmem_ld_wait();
-            if (KIND == ONE_TILE) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) pick(zl, v[j], lab - c, j);
-            }
             const int c0 = t.ct * p.NT + c;  // class of v[0]
+            if (KIND == ONE_TILE || (hit && __any_sync(gq::FULL, (unsigned)(lab - c0) < 32u))) {
+              if (KIND != ONE_TILE) keep_branch();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) pick(zl, v[j], lab - c0, j);
+              if (KIND == LOSSES && (unsigned)(lab - c0) < 32u) p.zlab[srow] = zl;
+            }
             if (c0 < p.C) online(v, p.C - c0, m, sum);
           }
           if (KIND == ONE_TILE) {
@@ -591,12 +597,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         if ((KIND == PIECE && t.mode == GRAD) || (KIND == ONE_TILE && p.full == 2)) {
+          const bool hit =
+              KIND == PIECE &&
+              __any_sync(gq::FULL, (unsigned)(__float_as_int(rw.w) - p.gc0 - t.ct * p.NT) < (unsigned)t.N);
           for (int b = KIND == ONE_TILE ? 0 : part * 64; b < t.N; b += KIND == ONE_TILE ? 64 : 64 * kParts) {
             // a box of 32 rows x 64 classes, 128 bytes a row (128-byte
             // swizzle: 16-byte piece j of row `lane` at j ^ (lane & 7))
             uint8_t* box = stg + (nbox & 1) * kBox;
             uint8_t* mine = box + lane * 128;
             const int cl = t.ct * p.NT + b;  // column of G
+            const int c0 = p.gc0 + cl;
+            const unsigned yl = (unsigned)(__float_as_int(rw.w) - c0);
+            float gl = rw.z;  // the label's entry, if it is here
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
               float v[32];
@@ -610,6 +622,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 v[j] = g.x;
                 v[j + 1] = g.y;
               }
+              if (hit && __any_sync(gq::FULL, yl - 32 * h < 32u)) {
+                keep_branch();
+                float pw = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) pick(pw, v[j], (int)yl - 32 * h, j);
+                if (yl - 32 * h < 32u) gl = pw - rw.z;
+              }
               if (h == 0) {
                 if (lane == 0) bulk_wait_read<1>();  // the store of two boxes ago has read this buffer
                 __syncwarp();
@@ -622,12 +641,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint4*>(mine + 16 * ((4 * h + j) ^ (lane & 7))) = make_uint4(o[0], o[1], o[2], o[3]);
               }
             }
-            // entries that are not the product's: the label's (made by
-            // xent_join_kernel), and zeros past the last class and row,
-            // whatever the products gave there
-            const int c0 = p.gc0 + cl;
-            const unsigned yl = (unsigned)(__float_as_int(rw.w) - c0);
-            if (yl < 64u) put_box(mine, lane, yl, __float2bfloat16_rn(rw.z));
+            // entries that are not the product's: the label's, p - 1 in fp32,
+            // and zeros past the last class and row, whatever the products
+            // gave there
+            if (yl < 64u) put_box(mine, lane, yl, __float2bfloat16_rn(gl));
             const int zeros = srow < q.nl ? p.C - c0 : 0;
 #pragma unroll 1
             for (int j = max(zeros, 0); j < 64; ++j) put_box(mine, lane, j, __float2bfloat16_rn(0.0f));
@@ -854,22 +871,17 @@ __global__ void __launch_bounds__(kScanThreads)
   if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) *o.nl = at;
 }
 
-// Per row of X: the label's logit x . w_y; the labelled rows copied
-// together (zeros up to a multiple of 256 rows) and zeros in the other rows
-// of dX, unless every row is labelled.  The label's logit costs one gathered
-// row of W here; picked out of the STATS tiles it cost 16% of their time
-// (dots = 0: a WHOLE tile's lanes hold it).
+// Unless every row is labelled: the labelled rows of X copied together (zeros
+// up to a multiple of 256 rows) and zeros in the other rows of dX.
 __global__ void __launch_bounds__(256)
-    xent_rows_kernel(const __nv_bfloat16* __restrict__ X, int64_t n, int k, int64_t ldx,
-                     const __nv_bfloat16* __restrict__ W, int64_t ldw, const int* __restrict__ labels,
-                     const int* __restrict__ pos, const int* __restrict__ nl, float* zlab, __nv_bfloat16* Xc,
-                     int64_t ldc, __nv_bfloat16* dX, int64_t lddx, int per_warp, int dots) {
+    xent_rows_kernel(const __nv_bfloat16* __restrict__ X, int64_t n, int k, int64_t ldx, const int* __restrict__ pos,
+                     const int* __restrict__ nl, __nv_bfloat16* Xc, int64_t ldc, __nv_bfloat16* dX, int64_t lddx,
+                     int per_warp) {
   grid_wait();
   const int m = *nl;
-  const bool all = m == n;
-  if (all && !dots) return;
+  if (m == n) return;
   const int lane = threadIdx.x & 31;
-  const int64_t pad_end = all ? n : n + ((m + kTile - 1) / kTile * (int64_t)kTile - m);  // rows of zeros behind Xc
+  const int64_t pad_end = n + ((m + kTile - 1) / kTile * (int64_t)kTile - m);  // rows of zeros behind Xc
   const int64_t step = (int64_t)gridDim.x * 8 * per_warp;
   for (int64_t r0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * per_warp; r0 < pad_end; r0 += step) {
     // per_warp rows (at most 32) of a warp, their places read at once
@@ -889,35 +901,13 @@ __global__ void __launch_bounds__(256)
     }
     for (unsigned left = on; left != 0; left &= left - 1) {
       const int i = __ffs(left) - 1;
-      const int64_t r = r0 + i;
-      const int to = __shfl_sync(gq::FULL, at, i);
-      const __nv_bfloat16* x = X + r * ldx;
-      const __nv_bfloat16* w = dots ? W + (int64_t)labels[r] * ldw : nullptr;
-      __nv_bfloat16* dst = all ? nullptr : Xc + (int64_t)to * ldc;
-      float z = 0.0f;
+      const __nv_bfloat16* x = X + (r0 + i) * ldx;
+      __nv_bfloat16* dst = Xc + (int64_t)__shfl_sync(gq::FULL, at, i) * ldc;
       for (int c = lane * 8; c < k; c += 256) {
-        if (c + 8 <= k) {
-          const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + c));
-          if (dst != nullptr) *reinterpret_cast<uint4*>(dst + c) = a;
-          if (!dots) continue;
-          const uint4 b = __ldg(reinterpret_cast<const uint4*>(w + c));
-          const uint32_t au[4] = {a.x, a.y, a.z, a.w}, bu[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {  // bf16 is the upper half of an fp32
-            z = __fmaf_rn(__uint_as_float(au[j] << 16), __uint_as_float(bu[j] << 16), z);
-            z = __fmaf_rn(__uint_as_float(au[j] & 0xffff0000u), __uint_as_float(bu[j] & 0xffff0000u), z);
-          }
-        } else {
-          for (int j = c; j < k; ++j) {
-            if (dots) z = __fmaf_rn(__bfloat162float(x[j]), __bfloat162float(w[j]), z);
-            if (dst != nullptr) dst[j] = x[j];
-          }
-        }
+        if (c + 8 <= k) *reinterpret_cast<uint4*>(dst + c) = __ldg(reinterpret_cast<const uint4*>(x + c));
+        else
+          for (int j = c; j < k; ++j) dst[j] = x[j];
       }
-      if (!dots) continue;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(gq::FULL, z, o);
-      if (lane == 0) zlab[to] = z;
     }
   }
 }
@@ -950,7 +940,7 @@ __global__ void __launch_bounds__(1024)
       s = 0.0f;
       for (int j = 0; j < 32; ++j) s += ss[j][lane] * ex2(sm[j][lane] - ref);
       const RowNorm f = norm_of(ref, s, zlab[row], wrow[row]);
-      if (rowinfo != nullptr) rowinfo[row] = make_float4(f.ref, f.ws, f.glab, __int_as_float(lab[row]));
+      if (rowinfo != nullptr) rowinfo[row] = make_float4(f.ref, f.ws, wrow[row], __int_as_float(lab[row]));
       const int to = idx[row];
       if (loss != nullptr) loss[to] = f.loss;
       if (lse != nullptr) lse[to] = f.lse;
@@ -1198,9 +1188,8 @@ extern "C" int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, 
   const int per_warp = share > 32 ? 32 : (int)share;
   const int64_t rb = cdiv(n + kTile, 8 * per_warp);
   GQ_TRY(launch_after(xent_rows_kernel, dim3((unsigned)(rb < warps / 8 ? rb : warps / 8)), dim3(256), 0, s,
-                      reinterpret_cast<const __nv_bfloat16*>(X), n, k, ldx, reinterpret_cast<const __nv_bfloat16*>(W),
-                      ldw, labels, w.pos, w.nl, w.zlab, static_cast<__nv_bfloat16*>(w.Xc), ldc,
-                      reinterpret_cast<__nv_bfloat16*>(dX), lddx, per_warp, z.ctiles > 1 ? 1 : 0));
+                      reinterpret_cast<const __nv_bfloat16*>(X), n, k, ldx, w.pos, w.nl,
+                      static_cast<__nv_bfloat16*>(w.Xc), ldc, reinterpret_cast<__nv_bfloat16*>(dX), lddx, per_warp));
 
   Maps m;
   memset(&m, 0, sizeof(m));
@@ -1218,6 +1207,7 @@ extern "C" int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, 
   a.NK = z.NK;
   a.nkt = z.nkt;
   a.row = w.row;
+  a.zlab = w.zlab;
   a.idx = w.idx;
   a.part = w.part;
   a.err = dev_err;
