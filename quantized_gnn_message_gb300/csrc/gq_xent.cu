@@ -336,7 +336,19 @@ struct Feed {
 // running maximum of ceil(z L): the fused multiply-add rounds the small
 // difference only, rescaling a sum by 2^(r - r') is exact, and L's own error
 // (below 2^-26 relative) acts as a change of the logits by that much.
-// This adds 32 more logits to (r, s = sum of 2^(z L - r)); limit: columns of
+// Where z L is beyond 2^30, its neighbours are 64 and more away and r would be
+// off by up to half of that (an exponent of 128 is infinite).  There distinct
+// logits are further apart than any exponential holds, and 4^(z - max z) does
+// as well: 2^(z M - r) with M = 2 and r = 2 max z, both exact.  r stays
+// increasing in max z, and tells by its size which of the two it is.
+constexpr float kFar = 1073741824.0f;
+__device__ __forceinline__ float ref_of(float top) {
+  const float r = top * kLog2e;
+  return fabsf(r) < kFar ? ceilf(r) : 2.0f * top;
+}
+__device__ __forceinline__ float scale_of(float r) { return fabsf(r) < kFar ? kLog2e : 2.0f; }
+
+// This adds 32 more logits to (r, s = sum of 2^(z M - r)); limit: columns of
 // the chunk that are classes.
 __device__ __forceinline__ void online(float (&v)[32], int limit, float& r, float& s) {
   if (limit < 32) {
@@ -354,14 +366,15 @@ __device__ __forceinline__ void online(float (&v)[32], int limit, float& r, floa
     for (int i = 0; i < 4; ++i) c[i] = max3(c[i], v[j + 2 * i], v[j + 2 * i + 1]);
 #pragma unroll
   for (int i = 0; i < 4; ++i) c[i] = fmaxf(c[i], v[28 + i]);
-  const float rn = fmaxf(r, ceilf(fmaxf(max3(c[0], c[1], c[2]), c[3]) * kLog2e));
+  const float rn = fmaxf(r, ref_of(fmaxf(max3(c[0], c[1], c[2]), c[3])));
   // every logit so far -inf: exponentials of -inf - 0, which are zeros
   const float ref = rn == neg_inf() ? 0.0f : rn;
-  const float2 l2e = make_float2(kLog2e, kLog2e), nref = make_float2(-ref, -ref);
+  const float sc = scale_of(ref);
+  const float2 m2 = make_float2(sc, sc), nref = make_float2(-ref, -ref);
   float2 a[2] = {make_float2(s * ex2(r - ref), 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
   for (int j = 0; j < 32; j += 2) {
-    const float2 x = fma2(make_float2(v[j], v[j + 1]), l2e, nref);
+    const float2 x = fma2(make_float2(v[j], v[j + 1]), m2, nref);
     a[(j >> 1) & 1] = add2(a[(j >> 1) & 1], make_float2(ex2(x.x), ex2(x.y)));
   }
   a[0] = add2(a[0], a[1]);
@@ -370,18 +383,19 @@ __device__ __forceinline__ void online(float (&v)[32], int limit, float& r, floa
 }
 
 // A row's values from its r and sum: the loss is taken from the label's logit
-// zlab in the form the sum has it, z L - r.
+// zlab in the form the sum has it, z M - r.
 struct RowNorm {
   float ref, ws, glab, loss, lse;  // r; weight / sum; G of the label
 };
 __device__ __forceinline__ RowNorm norm_of(float ref, float s, float zlab, float weight) {
   RowNorm f;
-  const float l2 = log2f(s), zl = __fmaf_rn(zlab, kLog2e, -ref);
+  const float sc = scale_of(ref), l2 = log2f(s), zl = __fmaf_rn(zlab, sc, -ref);
+  const bool far = sc == 2.0f;
   f.ref = ref;
   f.ws = weight / s;
   f.glab = __fmaf_rn(ex2(zl), f.ws, -weight);
-  f.loss = kLn2 * (l2 - zl);
-  f.lse = __fmaf_rn(ref, kLn2, l2 * kLn2);
+  f.loss = far ? __fmaf_rn(-0.5f, zl, l2 * kLn2) : kLn2 * (l2 - zl);
+  f.lse = __fmaf_rn(ref, far ? 0.5f : kLn2, l2 * kLn2);
   return f;
 }
 // entry j of a lane's 128-byte row of a G box
@@ -597,6 +611,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         if ((KIND == PIECE && t.mode == GRAD) || (KIND == ONE_TILE && p.full == 2)) {
+          const float sc = scale_of(rw.x);
           const bool hit =
               KIND == PIECE &&
               __any_sync(gq::FULL, (unsigned)(__float_as_int(rw.w) - p.gc0 - t.ct * p.NT) < (unsigned)t.N);
@@ -617,7 +632,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int j = 0; j < 32; j += 2) {
                 const float2 x =
-                    fma2(make_float2(v[j], v[j + 1]), make_float2(kLog2e, kLog2e), make_float2(-rw.x, -rw.x));
+                    fma2(make_float2(v[j], v[j + 1]), make_float2(sc, sc), make_float2(-rw.x, -rw.x));
                 const float2 g = mul2(make_float2(ex2(x.x), ex2(x.y)), make_float2(rw.y, rw.y));
                 v[j] = g.x;
                 v[j + 1] = g.y;

@@ -42,3 +42,36 @@ def test_certain_rows(n, k, C, spread):
     assert (dW.double().abs() <= E * 1.01 * X.double().abs().sum(0)).all()
     # the losses alone are the same
     assert torch.equal(q.linear_xent(X, W, lab, grad=False)[0], loss)
+
+
+# a single feature: every logit is exact.  log2(e) z is beyond 2^31 from 2e9
+# on, where a step of it is 256
+@pytest.mark.parametrize("size", [1e8, 1.2e9, 2e9, 3e10, 1e20, 1e38])
+@pytest.mark.parametrize("C", [5, 256, 300, 5000])
+def test_huge_logits(C, size):
+    """Logits are apart by more than any exponential holds: the top class has
+    probability 1, the loss is the difference to it."""
+    q = gq()
+    X = torch.zeros(6, 8, dtype=torch.bfloat16, device="cuda")
+    X[:, 0] = 1.0
+    W = torch.zeros(C, 8, dtype=torch.bfloat16, device="cuda")
+    top, low, mid = C - 1, 0, C // 2
+    W[:, 0] = -1e6
+    W[top, 0], W[low, 0], W[mid, 0] = size, -size / 2, size / 2
+    lab = torch.tensor([top, low, mid, -1, 1, top], dtype=torch.int32, device="cuda")
+    lse = torch.empty(6, device="cuda")
+    loss, dX, dW = q.linear_xent(X, W, lab, lse=lse)
+    w = W[:, 0].double()
+    ref = torch.where(lab >= 0, w[top] - w[lab.long()], 0.0)
+    # the scaled logits, their difference, ln 2 and the product: one rounding each
+    assert ((loss.double() - ref).abs() <= 8 * 2.0 ** -24 * size + E).all() and (loss[[0, 5]].abs() <= E).all()
+    assert ((lse.double() - torch.where(lab >= 0, w[top], 0.0)).abs() <= 8 * 2.0 ** -24 * size).all()
+    # G = onehot(top) - onehot(label); half a step of bf16
+    ref = torch.where(lab >= 0, w[top] - w[lab.long()], 0.0)
+    assert ((dX[:, 0].double() - ref).abs() <= 2.0 ** -8 * ref.abs() * 1.01 + E * size).all() and not dX[:, 1:].any()
+    G = torch.zeros(6, C, dtype=torch.float64, device="cuda")
+    on = torch.nonzero(lab >= 0)[:, 0]
+    G[on, top] = 1.0
+    G[on, lab[on].long()] -= 1.0
+    ref = G.T @ X.double()
+    assert ((dW.double() - ref).abs() <= 2.0 ** -8 * ref.abs() * 1.01 + 6 * E).all()
