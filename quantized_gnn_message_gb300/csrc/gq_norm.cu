@@ -1031,7 +1031,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_wide_kernel(const NormBwd
 
 // out[c] = sum over the blocks' partial rows, 32 columns per block, 32 row
 // lanes whose sums are added in lane order.
-__global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* __restrict__ partial, int blocks, int d,
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* partial, int blocks, int d,
                                                            float* dgamma, float* dbeta) {
   grid_wait();
   __shared__ float s[32][33];

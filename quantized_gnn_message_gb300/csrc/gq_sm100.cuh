@@ -190,7 +190,9 @@ __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.
 // on the stream still runs; grid_wait returns once that one has completed and
 // its writes are visible.  Every such kernel calls grid_wait before it touches
 // global memory, so the one before has, by its own completion, waited for
-// everything earlier.
+// everything earlier.  Its pointers are not __restrict__, and what earlier
+// kernels of the call wrote is not read by __ldg: both let a load move up past
+// the wait.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <typename... P, typename... A>

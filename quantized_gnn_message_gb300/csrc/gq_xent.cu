@@ -839,8 +839,8 @@ struct ScanOut {
 };
 
 __global__ void __launch_bounds__(kScanThreads)
-    xent_scan_kernel(const int* __restrict__ labels, const float* __restrict__ weight, int64_t n, int C,
-                     int64_t seg, const int* __restrict__ cnt, const ScanOut o) {
+    xent_scan_kernel(const int* labels, const float* weight, int64_t n, int C, int64_t seg, const int* cnt,
+                     const ScanOut o) {
   grid_wait();
   __shared__ int ws[32];
   __shared__ int base;
@@ -889,9 +889,8 @@ __global__ void __launch_bounds__(kScanThreads)
 // Unless every row is labelled: the labelled rows of X copied together (zeros
 // up to a multiple of 256 rows) and zeros in the other rows of dX.
 __global__ void __launch_bounds__(256)
-    xent_rows_kernel(const __nv_bfloat16* __restrict__ X, int64_t n, int k, int64_t ldx, const int* __restrict__ pos,
-                     const int* __restrict__ nl, __nv_bfloat16* Xc, int64_t ldc, __nv_bfloat16* dX, int64_t lddx,
-                     int per_warp) {
+    xent_rows_kernel(const __nv_bfloat16* X, int64_t n, int k, int64_t ldx, const int* pos, const int* nl,
+                     __nv_bfloat16* Xc, int64_t ldc, __nv_bfloat16* dX, int64_t lddx, int per_warp) {
   grid_wait();
   const int m = *nl;
   if (m == n) return;
@@ -930,9 +929,8 @@ __global__ void __launch_bounds__(256)
 // lse and loss of 32 labelled rows per block from the runs' (r, sum) pairs:
 // 32 lanes of runs per row, joined in lane order.
 __global__ void __launch_bounds__(1024)
-    xent_join_kernel(const float2* __restrict__ part, int runs, int64_t npad, const int* __restrict__ nl,
-                     const int* __restrict__ idx, const float* __restrict__ zlab, const float* __restrict__ wrow,
-                     const int* __restrict__ lab, float4* rowinfo, float* loss, float* lse) {
+    xent_join_kernel(const float2* part, int runs, int64_t npad, const int* nl, const int* idx, const float* zlab,
+                     const float* wrow, const int* lab, float4* rowinfo, float* loss, float* lse) {
   __shared__ float sm[32][33], ss[32][33];
   grid_wait();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -969,9 +967,8 @@ __global__ void __launch_bounds__(1024)
 // would leave SMs idle.
 template <int COLS>
 __global__ void __launch_bounds__(256)
-    xent_sum_kernel(const float* __restrict__ acc, int splits, int64_t split_stride, int64_t tile_stride,
-                    const int* __restrict__ nl, int64_t n, const int* __restrict__ idx, int row0, int C, int k,
-                    float scale, __nv_bfloat16* out, int64_t ldo) {
+    xent_sum_kernel(const float* acc, int splits, int64_t split_stride, int64_t tile_stride, const int* nl, int64_t n,
+                    const int* idx, int row0, int C, int k, float scale, __nv_bfloat16* out, int64_t ldo) {
   grid_wait();
   const int c0 = blockIdx.y * COLS;
   const int64_t r = (int64_t)blockIdx.x * kTile + threadIdx.x;

@@ -37,3 +37,23 @@ def test_a_refused_launch_leaves_no_error_behind(tmp_path):
     out = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout
     # GQ_ERR_CUDA and nothing left behind; GQ_OK and cudaErrorInvalidValue
     assert out.split() == ["4", "0", "0", "1"]
+
+
+def test_kernels_that_wait_for_the_one_before_promise_nothing_about_their_inputs():
+    """A `const T* __restrict__` parameter says that its data do not change
+    while the kernel runs, so its loads may be moved up past grid_wait(),
+    behind which alone the kernel before has written them."""
+    import glob
+    import re
+    from quantized_gnn_message_gb300 import build
+    seen = 0
+    for path in glob.glob(build.CSRC + "/*.cu"):
+        with open(path, encoding="utf-8") as f:
+            text = build._code_only(f.read())
+        for kernel in re.split(r"\b__global__\b", text)[1:]:
+            head, _, rest = kernel.partition("{")
+            body = re.split(r"\n}", rest)[0]
+            if "grid_wait()" in body:
+                seen += 1
+                assert "__restrict__" not in head, f"{path}: {head.split('(')[0].split()[-1]}"
+    assert seen >= 6
