@@ -111,7 +111,9 @@ GQ_API int gq_layer_norm_bwd(const void* dY, int64_t lddy, const void* X, int64_
  *           piece to piece, 4 n k bytes for each split of dX's, 4 c k of dW's
  *           (k a multiple of 128).  It depends on the current device's SM
  *           count.  Calls sharing one workspace must not overlap.
- *   dev_err nullable device int, as for the GEMMs (codes 21 .. 26)
+ *   dev_err nullable device int, as for the GEMMs (codes 21 .. 26).  Without it
+ *           a bounded wait that gave up, and left results half made, is not
+ *           reported
  * Results are the same from run to run.  dX and dW must not overlap X or W.
  * Errors: GQ_ERR_INVALID_ARG (null X, W or labels, n < 0, k < 1, C < 1, bad
  * leading dimensions or alignment); GQ_ERR_UNSUPPORTED for k > 16384,

@@ -81,6 +81,7 @@ constexpr int kSlots = 4;        // units of work posted ahead
 constexpr int kConsumers = 3 + 2 * kEpiWarps;  // even CTA: TMA, MMA, epilogue; odd CTA: TMA, epilogue
 constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kStg + 512;
 constexpr int kTile = 256;
+constexpr long long kDrainCycles = 1 << 21;  // 1 ms
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -797,6 +798,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   __syncwarp();
   __syncthreads();
+  // after a wait that gave up: loads, products and posts under way (they take
+  // microseconds) land before the pair's shared and tensor memory is given up
+  if (*abort) {
+    const long long t0 = clock64();
+    while (clock64() - t0 < kDrainCycles) {
+    }
+  }
   cluster_sync();
   if (warp == 1) {
     tc_fence_after();
