@@ -26,7 +26,8 @@ typedef enum { GQ_F32 = 0, GQ_BF16 = 1, GQ_F16 = 2 } gq_type;
  * to the type.  Dropped elements are +0 whatever X holds there (NaN and
  * infinity included).  The backward pass is the same call on dY with the
  * same p and seed.  Attention values are dropped the same way, as an
- * E x heads matrix.  Bit-for-bit reproducible; independent of the leading
+ * E x heads matrix (by a caller of the edge operators; gq_gat_layer_fwd and
+ * _bwd drop none).  Bit-for-bit reproducible; independent of the leading
  * dimensions.  A call whose seed also drives a quantizer on the same rows
  * passes seed ^ GQ_DROPOUT_SEED_TAG, so that the two draw different noise.
  *   type   gq_type of X and Y (n x d, ldx, ldy >= d, any alignment of the
@@ -53,7 +54,9 @@ GQ_API int gq_dropout(const void* X, int type, int64_t n, int d, int64_t ldx, do
  *   (n fp32 each) and relu_bits (as in gq_gcn_layer_fwd: bit c % 32 of word
  *   relu_bits[r * ldrb + c / 32] = [z > 0], act = RELU only) are nullable;
  *   the backward pass needs them.  gamma, beta: d fp32; NULL: 1 and 0.
- *   Y may be X (ldy == ldx).
+ *   Y may be X (ldy == ldx).  RELU keeps z where z > 0 and gives 0 elsewhere,
+ *   for a NaN too (its bit is clear), as the layers' own ReLU does; without
+ *   it a NaN in X fills its row of Y.
  * gq_layer_norm_bwd:
  *   dz = drop'(dY), with dz[r,c] = 0 where act = RELU and the bit is clear
  *   dgamma[j] = sum_r dz[r,j] xhat[r,j];  dbeta[j] = sum_r dz[r,j]
@@ -88,6 +91,8 @@ GQ_API int gq_layer_norm_bwd(const void* dY, int64_t lddy, const void* X, int64_
  *   Z = X W^T                       (n x C, fp32 sums of bf16 products)
  *   for a row with 0 <= labels[r] < C:
  *     lse[r]  = log sum_c exp(Z[r,c]);  loss[r] = lse[r] - Z[r, labels[r]]
+ *       (one Z: a certain row's loss is 0 to within 2^-20, whatever the size of
+ *       its logits, up to 1e38)
  *     G[r,c]  = weight[r] * (exp(Z[r,c] - lse[r]) - [c = labels[r]])
  *   for any other row (an unlabelled node, padding): loss = lse = 0, its
  *     row of dX is zero, and what X holds there enters nothing

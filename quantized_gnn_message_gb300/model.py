@@ -204,14 +204,16 @@ class GCNStack:
 
     def loss(self, Wc: torch.Tensor, labels: torch.Tensor) -> torch.Tensor:
         """Per-node cross entropy of the head on the latest forward pass's
-        output (0 for nodes without a label)."""
+        output (0 for nodes without a label): the stack's own buffer, which
+        the next call of loss or loss_and_grad overwrites."""
         return self._head(Wc, labels, 1.0, None, False)
 
     def loss_and_grad(self, Wc: torch.Tensor, labels: torch.Tensor, scale: float,
                       weight: torch.Tensor | None = None) -> torch.Tensor:
         """Per-node cross entropy; leaves the gradients of scale *
         sum(weight * loss) in dWc and, for backward(None, ...), in the last
-        layer's dZ.  scale: 1 / (number of labelled nodes) for their mean."""
+        layer's dZ.  scale: 1 / (number of labelled nodes) for their mean.
+        Returns the buffer that loss returns."""
         loss = self._head(Wc, labels, scale, weight, True)
         self._graded = True
         return loss

@@ -121,3 +121,25 @@ def test_constant_rows_of_huge_values(d, dtype):
         tol = rstd.double()[:, None] * U * (6 * g.abs() + 34 * g.abs().mean(1, keepdim=True))
         assert ((dx.double() - ref).abs() <= tol + torch.finfo(t).eps / 2 * ref.abs() * (1 + 1e-3)).all()
         assert ((dbeta.double() - g.sum(0)).abs() <= (n + 100) * U * g.abs().sum(0)).all()
+
+
+@pytest.mark.parametrize("d", [40, 300, 1000])
+def test_relu_gives_zero_for_nan(d):
+    q = gq()
+    x = synth.normal_matrix(5, d, seed=1, device="cuda")
+    x[2, d // 2] = float("nan")
+    bits = torch.full((5, (d + 31) // 32), -1, dtype=torch.int32, device="cuda")
+    y = q.layer_norm_fwd(x, act=q.ACT_RELU, relu_bits=bits)[0]
+    assert torch.isfinite(y).all() and not y[2].any() and not bits[2].any() and y[1].any()
+    assert torch.isnan(q.layer_norm_fwd(x)[0][2]).all()
+
+
+@pytest.mark.parametrize("d", [64, 300, 2000])
+def test_forward_without_statistics(d):
+    """gq_layer_norm_fwd with NULL mean and rstd."""
+    q = gq()
+    x = synth.normal_matrix(50, d, seed=1, device="cuda")
+    ref, y, p = q.layer_norm_fwd(x)[0], torch.empty_like(x), q._ptr
+    q._check(q.lib().gq_layer_norm_fwd(p(x), q.F32, 50, d, d, None, None, 1e-5, q.ACT_NONE, 0.0, 0, p(y), d, None,
+                                       None, None, 0, q._stream()), "fwd")
+    assert torch.equal(y, ref)

@@ -127,9 +127,10 @@ def _check(q, X, W, lab, weight=None, scale=1.0):
 
 # classes per piece: 192 of 520 (its last 256-class tile of dW reaches into the
 # next piece), 256 of 600, 92, 92 and 90 tiles of 256, 10 tiles of 256 with the
-# sums of dW split, 4,493 tiles with the sums of dX split
+# sums of dW split, 4,493 tiles with the sums of dX split, three column tiles
+# of the gradients
 @pytest.mark.parametrize("n,k,C", [(1_500_000, 8, 520), (1_200_000, 24, 600), (20_000, 72, 70_001),
-                                   (200_000, 16, 30_000), (250, 16, 2_300_000)])
+                                   (200_000, 16, 30_000), (250, 16, 2_300_000), (20_000, 520, 30_000)])
 @pytest.mark.parametrize("frac", [1.0, 0.5])
 def test_several_pieces(n, k, C, frac):
     assert 2 * n * C > 1 << 30, "G fits one piece"
@@ -165,4 +166,15 @@ def test_short_tiles_of_several_pieces_are_the_same_every_time(n, k, C):
             assert all(torch.isfinite(t).all() for t in first)
         assert all(torch.equal(a, b) for a, b in zip(first, (loss, dX, dW)))
     del ws, dX
+    torch.cuda.empty_cache()
+
+
+def test_one_gradient_of_several_pieces():
+    q = gq()
+    n, k, C = 1_200_000, 24, 600
+    X, W, lab = _bf(n, k, 1), _bf(C, k, 2, 2 / k ** 0.5), _labels(n, C, 0.7, 3)
+    loss, dX, dW = q.linear_xent(X, W, lab)
+    a, b = q.linear_xent(X, W, lab, need_dW=False), q.linear_xent(X, W, lab, need_dX=False)
+    assert torch.equal(a[0], loss) and torch.equal(a[1], dX) and a[2] is None
+    assert torch.equal(b[0], loss) and torch.equal(b[2], dW) and b[1] is None
     torch.cuda.empty_cache()
