@@ -28,9 +28,12 @@
 // start 4-byte aligned), neighbouring lanes on neighbouring columns.
 //
 // Measured (GB300, copy rate 6.8 TB/s): dropout of 2,449,029 x 256 fp32 0.71 ms
-// (7.1 TB/s); backward of the same with ReLU and dropout 1.30 ms (5.9 TB/s);
+// (7.1 TB/s); backward of the same with ReLU and dropout 1.31 ms (5.8 TB/s);
 // forward of 131,072 x 256 fp32 with ReLU 47 us (5.7 TB/s); 30,001 x 4,099
-// bf16 with dropout, forward and backward, 430 us (2.9 TB/s).
+// bf16 with dropout, forward and backward, 430 us (2.9 TB/s).  Rows of more
+// than 8,192 columns keep a backward pass's column sums in shared memory and
+// spill registers: 10,000 x 16,384 fp32 610 us (3.2 TB/s), bf16 440 us, off the
+// 16-byte grid 1.1 ms.
 //
 // Dropout draws u(seed, row, column) from the library's counter hash (see
 // gq_quantize_pack) and keeps an element when u >= p, so the backward pass
@@ -937,10 +940,10 @@ __global__ void __launch_bounds__(1024, 1) norm_bwd_block_kernel(const NormBwd p
 }
 
 // Wide rows up to 8,192 columns that start 16-byte aligned: the column sums
-// and the row at work in registers (112 to 128 a thread), S - 1 rows on their
-// way through shared memory, gamma there too.  30,001 x 4,099 bf16: 249 us;
-// with the sums in shared memory (norm_bwd_block_kernel) 390 us, its shared
-// memory pipe the bound.
+// and the row at work in registers (96 to 128 a thread), S - 1 rows on their
+// way through shared memory, gamma there too.  30,001 x 4,099 bf16: 230 us, with
+// dropout 260; with the sums in shared memory (norm_bwd_block_kernel) 390 us,
+// its shared memory pipe the bound.
 template <typename T, typename TO, int V, int S, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_wide_kernel(const NormBwd p) {
   constexpr int NV = kEpt / V;
@@ -1082,13 +1085,18 @@ int block_rows_per_sm(int threads, size_t smem) {
 // flight within 64 registers; beyond 1024 threads, 16.
 int bwd_ept(int d) { return d <= 8192 ? 8 : 16; }
 
-// Threads of norm_bwd_wide_kernel, and the most that it is built for two
-// blocks per SM with: it needs 112 registers a thread, of which an SM has
-// 65,536 (2 x 112 x 288 = 64,512).  Resident blocks as far as registers go;
-// fp32 rows are fewer, by shared memory.
+// norm_bwd_wide_kernel is built for three sizes of blocks.  Two blocks of up to
+// 256 threads share an SM at the 128 registers that a thread can use (96 of
+// them, to fit more threads: 120,000 x 1,024 bf16 163 -> 198 us, fp32 249 -> 281,
+// 30,000 x 4,096 bf16 164 -> 220).  Above that one block has the SM, but for
+// 16-bit rows of up to 288 threads with dropout, whose hash needs the warps
+// more than the registers: two blocks, at 96 (with dropout 4,099 bf16 columns
+// 285 -> 263 us, 4,608 248 -> 232, from 4,864 on no difference; without it 229
+// -> 233 and 200 -> 204).
+constexpr int kPairThreads = 256, kPairThreadsDrop = 288;
 int wide_threads(int d) { return ((d + kEpt - 1) / kEpt + 31) / 32 * 32; }
-constexpr int kPairThreads = 288;
-int wide_per_sm(int threads) { return threads <= kPairThreads ? 2 * kPairThreads / threads : 1; }
+// At most so many of its blocks are resident per SM, as far as registers go.
+int wide_per_sm(int threads) { return threads <= kPairThreadsDrop ? 2 * kPairThreadsDrop / threads : 1; }
 
 // Upper bound of the backward's blocks, one partial row of sums each.
 int bwd_blocks(int64_t n, int d) {
@@ -1241,8 +1249,10 @@ int bwd_any(const NormBwd& p, int& blocks, cudaStream_t s) {
   if (p.d > 8192) return bwd_block<T, TO, V, 16>(p, blocks, s);
   if constexpr (V > 2) {
     const int threads = wide_threads(p.d);
-    return threads <= kPairThreads ? bwd_wide<T, TO, V, kPairThreads, 2>(p, blocks, threads, s)
-                                   : bwd_wide<T, TO, V, 512, 1>(p, blocks, threads, s);
+    if (threads <= kPairThreads) return bwd_wide<T, TO, V, kPairThreads, 2>(p, blocks, threads, s);
+    if constexpr (sizeof(T) == 2)
+      if (threads <= kPairThreadsDrop && p.dr.on) return bwd_wide<T, TO, V, kPairThreadsDrop, 2>(p, blocks, threads, s);
+    return bwd_wide<T, TO, V, 512, 1>(p, blocks, threads, s);
   } else {
     return bwd_block<T, TO, V, 8>(p, blocks, s);
   }
@@ -1256,8 +1266,9 @@ int bwd_typed(const NormBwd& p, int& blocks, int vec, cudaStream_t s) {
   return bwd_any<T, TO, 1>(p, blocks, s);
 }
 
-// Pairs of 16-bit elements only for rows of a block (120,000 x 1,000 bf16 at a
-// pitch of 1,006: forward 290 -> 218 us, backward 495 -> 374 us); a lane of a
+// Pairs of 16-bit elements only for rows of a block (120,000 x 1,000 bf16, one by
+// one at a pitch of 1,001 and in pairs at 1,006: forward 254 and 191 us, backward
+// 457 and 276 us); a lane of a
 // warp's row would hold more columns than one by one (300,000 x 334: forward
 // 190 -> 273 us, backward 240 -> 963 us).
 template <typename T>
