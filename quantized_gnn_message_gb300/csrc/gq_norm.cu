@@ -1268,9 +1268,8 @@ int bwd_typed(const NormBwd& p, int& blocks, int vec, cudaStream_t s) {
 
 // Pairs of 16-bit elements only for rows of a block (120,000 x 1,000 bf16, one by
 // one at a pitch of 1,001 and in pairs at 1,006: forward 254 and 191 us, backward
-// 457 and 276 us); a lane of a
-// warp's row would hold more columns than one by one (300,000 x 334: forward
-// 190 -> 273 us, backward 240 -> 963 us).
+// 457 and 276 us); a lane of a warp's row would hold more columns than one by
+// one (300,000 x 334: forward 190 -> 273 us, backward 240 -> 963 us).
 template <typename T>
 int fwd_typed(const NormFwd& p, int vec, cudaStream_t s) {
   if (vec > 2) return fwd_any<T, 16 / sizeof(T)>(p, s);

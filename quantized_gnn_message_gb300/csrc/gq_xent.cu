@@ -11,7 +11,7 @@
 // Products on the tcgen05 tensor cores (bf16 inputs, fp32 sums in TMEM), all
 // tiles of one persistent kernel:
 //   STATS  Z tile -> running maximum and sum of exponentials per row and run
-//          of class tiles
+//          of class tiles, and the label's logit of the rows that have it there
 //   GRAD   Z tile again -> G of one piece of the classes, in bf16
 //   WHOLE  STATS and GRAD of a tile that holds every class (C <= 256): the
 //          logits are read twice from TMEM, and nothing is recomputed
@@ -46,8 +46,13 @@
 // 1,024 x 131,072 with gradients: 11.0 ms, 1.60 PFLOP/s of the 8 n k C, of
 // 1.69 that a plain bf16 product sustains); the epilogues and G's way through
 // DRAM (written once, read twice: 12.9 GB) where it is small (k = 256: 3.7 ms,
-// 1.20 PFLOP/s).  Few classes (2,449,029 x 256 x 47, every row labelled): 0.90
-// ms for 3.2 GB read and 1.6 GB written, 5.3 TB/s.
+// 1.19 PFLOP/s).  Few classes (2,449,029 x 256 x 47, every row labelled): 0.89 to
+// 0.96 ms for 3.2 GB read and 1.6 GB written, 5.0 to 5.4 TB/s.
+//
+// The label's logit comes out of the same tiles as the sum of exponentials: a dot
+// product of its own is cheaper by 1 to 2% of STATS, but sums in another order
+// (and the tensor cores truncate), and the difference stood as loss and as
+// gradient in rows that are certain of their label.
 //
 // G is rounded to bf16, the type that the products dX and dW take: each
 // entry is off by at most half a step (2^-8 of its value, about as much as
@@ -406,7 +411,8 @@ __device__ __forceinline__ void put_box(uint8_t* row, int lane, unsigned j, __nv
 
 // Instantiated for the kinds of tiles a launch can hold, since the code of
 // the others would cost instruction fetches (STATS of 16,384 x 256 x 131,072:
-// 0.83 ms with all in one kernel, 0.78 ms alone).
+// 0.83 ms with all in one kernel, 0.78 ms alone, before the label's logit and
+// the far references came in: 0.80).
 enum Kind { LOSSES, PIECE, ONE_TILE };  // STATS | GRAD, DX, DW | WHOLE
 
 template <int KIND>

@@ -219,8 +219,8 @@ class GCNStack:
         return loss
 
     def launches(self, bits: int, need_input_grad: bool = False) -> int:
-        """Kernels of one forward and backward pass, the class head's not
-        counted."""
+        """Kernels of one forward and backward pass (from the class head's
+        gradient where there is a head), the head's own not counted."""
         n = sum(launches_fwd(bits) + launches_bwd(bits, need_input_grad or l > 0, self.dZ[l] is not None)
                 for l in range(self.L))
         # normalization: one forward, the pass and its column sums backward; dropout alone: one each
