@@ -275,7 +275,7 @@ def _quantize(x):
     whole numbers in [-127, 127] of them that are nearest, decided in 64 bits: of
     millions of quotients many lie next to a half."""
     x = x.float()
-    scale = x.abs().amax(1) / 127.0
+    scale = (x.abs().amax(1).double() / 127.0).float()
     wide = scale.double()[:, None]
     return torch.round(torch.where(wide > 0, x / wide, torch.zeros_like(wide))).float(), scale
 
@@ -455,7 +455,7 @@ def _rounded64(x, u, mantissa, top):
 
 
 def _quantize64(x):
-    scale = (x.abs().amax(1).float() / 127).double()  # what the operator stores, codes are multiples of it
+    scale = (x.abs().amax(1).double() / 127).float().double()  # what the operator stores, codes are multiples of it
     return torch.round(x.double() / scale.clamp(min=1e-300)[:, None]), scale
 
 
