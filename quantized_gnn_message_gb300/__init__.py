@@ -24,7 +24,7 @@ _lib = None
 
 GQ_OK = 0
 COEF_GCN, COEF_SAGE, COEF_ONE = 0, 1, 2
-ACT_NONE, ACT_RELU = 0, 1
+ACT_NONE, ACT_RELU, ACT_SILU = 0, 1, 2  # SiLU: group normalization only
 F32, BF16, F16 = 0, 1, 2
 
 
@@ -51,6 +51,19 @@ class Graph_t(ctypes.Structure):
         ("max_deg", ctypes.c_int32), ("tr_max_deg", ctypes.c_int32),
         ("status", ctypes.c_void_p),
     ]
+
+
+class AdamwTensor_t(ctypes.Structure):
+    """Mirror of the C struct gq_adamw_tensor."""
+    _fields_ = [(name, ctypes.c_void_p) for name in ("p", "g", "m", "v", "m_exp", "v_exp")] + \
+               [(name, ctypes.c_int64) for name in ("n", "cols", "ldp", "ldg", "block0")]
+
+
+class AdamwArgs_t(ctypes.Structure):
+    """Mirror of the C struct gq_adamw_args."""
+    _fields_ = [(name, ctypes.c_double) for name in ("lr", "beta1", "beta2", "eps", "weight_decay")] + \
+               [("step", ctypes.c_int64), ("seed", ctypes.c_uint64), ("grad_scale", ctypes.c_void_p),
+                ("dev", ctypes.c_void_p), ("advance", ctypes.c_int32)]
 
 
 def library_path() -> str:
@@ -106,6 +119,20 @@ def _SIGNATURES(P, I64, I, U64, F, S):
                                P, S, P], I),
         ("gq_linear_xent_workspace_bytes", [I64, I, I, I], S),
         ("gq_linear_xent", [P, I64, I, I64, P, I, I64, P, P, F, P, P, P, I64, P, I64, P, S, P, P], I),
+        ("gq_quantize_i8_workspace_bytes", [I64, I, I], S),
+        ("gq_quantize_i8", [P, I, I64, I, I64, I, P, I64, P, P, S, P], I),
+        ("gq_gemm_i8_workspace_bytes", [I64, I64, I64], S),
+        ("gq_gemm_i8", [P, I64, I64, P, P, I64, I64, P, I64, P, I, P, I, I64, P, S, P, P], I),
+        ("gq_linear_i8_workspace_bytes", [I64, I, I], S),
+        ("gq_linear_i8", [P, I, I64, I, I64, P, I, I64, P, P, I, P, I, I64, P, S, P, P], I),
+        ("gq_linear_i8_bwd_workspace_bytes", [I64, I, I, I, I], S),
+        ("gq_linear_i8_bwd", [P, I64, P, I64, I, I64, I, I, P, I, I64, P, I, I64, P, I, I64, P, P, S, P, P], I),
+        ("gq_group_norm_workspace_bytes", [I64, I, I, I, I64, I64, I], S),
+        ("gq_group_norm_fwd", [P, I, I64, I, I64, I, P, I64, I64, P, P, F, I, P, I64, P, P, P, S, P], I),
+        ("gq_group_norm_bwd", [P, I64, P, I64, I, I64, I, I, P, I64, I64, P, P, P, P, I, P, I64, P, P, P, S, P], I),
+        ("gq_adamw_dev_bytes", [], S),
+        ("gq_adamw_step", [ctypes.POINTER(AdamwTensor_t), I, I, I, I, ctypes.POINTER(AdamwArgs_t), P], I),
+        ("gq_adam_moment", [P, P, I64, I, P, I, P], I),
         ("gq_gcn_layer_workspace_bytes", [GP, I, I, I], S),
         ("gq_edge_softmax_workspace_bytes", [GP, I], S),
         ("gq_sddmm_edge_softmax", [GP, P, P, I, F, P, P, P, S, P], I),
@@ -590,6 +617,88 @@ def layer_norm_bwd(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rstd: 
 
 
 # --------------------------------------------------------------------------
+# group normalization
+# --------------------------------------------------------------------------
+
+def _segments(ptr, X):
+    """The number of segments that ptr (int64 offsets, or None: all rows are one) gives."""
+    if ptr is None:
+        return 1
+    _cuda(ptr, torch.int64, "ptr")
+    if ptr.dim() != 1 or ptr.numel() < 1 or not ptr.is_contiguous() or ptr.device != X.device:
+        raise GQError(f"ptr must be a contiguous int64 vector of row offsets on {X.device}")
+    return ptr.numel() - 1
+
+
+def _stats(t, s, groups, X, name):
+    if t is None:
+        return torch.empty(s, groups, dtype=torch.float32, device=X.device)
+    if t.dtype != torch.float32 or tuple(t.shape) != (s, groups) or t.device != X.device or not t.is_contiguous():
+        raise GQError(f"{name} must be contiguous float32 {s} x {groups} on {X.device}")
+    return t
+
+
+def group_norm_fwd(X: torch.Tensor, groups: int, ptr: torch.Tensor | None = None, gamma: torch.Tensor | None = None,
+                   beta: torch.Tensor | None = None, eps: float = 1e-5, act: int = ACT_NONE, max_rows: int = 0,
+                   out: torch.Tensor | None = None, mean: torch.Tensor | None = None,
+                   rstd: torch.Tensor | None = None, ws: "Workspace | None" = None):
+    """(Y, mean, rstd): act(group norm) of each segment of X's rows (the
+    graphs of a batch: segment j holds rows ptr[j] .. ptr[j+1] - 1), over the rows
+    and the channels of a group; the statistics [segments x groups] are what the
+    backward pass takes.  max_rows: the longest segment's rows if known (a hint).
+    out may be X.  Rows outside every segment: not written."""
+    ty = _typed(X, "X")
+    n, d = X.shape
+    s = _segments(ptr, X)
+    if out is None:
+        out = _rows_like(X)
+    else:
+        _like(out, X, "out")
+    _vec32(gamma, d, X, "gamma")
+    _vec32(beta, d, X, "beta")
+    mean, rstd = _stats(mean, s, groups, X, "mean"), _stats(rstd, s, groups, X, "rstd")
+    L = lib()
+    with _on(X.device):
+        wb = int(L.gq_group_norm_workspace_bytes(max(n, 1), d, groups, ty, s, max_rows, 0))
+        buf = None if wb == 0 else ws.get(wb) if ws is not None else torch.empty(wb, dtype=torch.uint8, device=X.device)
+        _check(L.gq_group_norm_fwd(_ptr(X), ty, n, d, _ld_any(X, d), groups, _ptr(ptr), s, max_rows, _ptr(gamma),
+                                   _ptr(beta), eps, act, _ptr(out), _ld_any(out, d), _ptr(mean), _ptr(rstd), _ptr(buf),
+                                   wb, _stream()), "gq_group_norm_fwd")
+    return out, mean, rstd
+
+
+def group_norm_bwd(dY: torch.Tensor, X: torch.Tensor, groups: int, mean: torch.Tensor, rstd: torch.Tensor,
+                   ptr: torch.Tensor | None = None, gamma: torch.Tensor | None = None,
+                   beta: torch.Tensor | None = None, act: int = ACT_NONE, max_rows: int = 0,
+                   dX: torch.Tensor | None = None, dgamma: torch.Tensor | None = None,
+                   dbeta: torch.Tensor | None = None, ws: "Workspace | None" = None):
+    """(dX, dgamma, dbeta) from the forward pass's input, weights and
+    statistics.  dX may be dY or X."""
+    ty = _typed(X, "X")
+    n, d = X.shape
+    s = _segments(ptr, X)
+    _like(dY, X, "dY")
+    dX = _rows_like(X) if dX is None else _like(dX, X, "dX")
+    _vec32(gamma, d, X, "gamma")
+    _vec32(beta, d, X, "beta")
+    if mean is None or rstd is None:
+        raise GQError("the backward pass takes the forward pass's mean and rstd")
+    _stats(mean, s, groups, X, "mean")
+    _stats(rstd, s, groups, X, "rstd")
+    dgamma = _new32(d, X) if dgamma is None else _vec32(dgamma, d, X, "dgamma")
+    dbeta = _new32(d, X) if dbeta is None else _vec32(dbeta, d, X, "dbeta")
+    L = lib()
+    with _on(X.device):
+        wb = int(L.gq_group_norm_workspace_bytes(max(n, 1), d, groups, ty, s, max_rows, 1))
+        buf = None if wb == 0 else ws.get(wb) if ws is not None else torch.empty(wb, dtype=torch.uint8, device=X.device)
+        _check(L.gq_group_norm_bwd(_ptr(dY), _ld_any(dY, d), _ptr(X), _ld_any(X, d), ty, n, d, groups, _ptr(ptr), s,
+                                   max_rows, _ptr(mean), _ptr(rstd), _ptr(gamma), _ptr(beta), act, _ptr(dX),
+                                   _ld_any(dX, d), _ptr(dgamma), _ptr(dbeta), _ptr(buf), wb, _stream()),
+               "gq_group_norm_bwd")
+    return dX, dgamma, dbeta
+
+
+# --------------------------------------------------------------------------
 # class head
 # --------------------------------------------------------------------------
 
@@ -633,6 +742,353 @@ def linear_xent(X: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, weight: 
                                 _ld_bf16(dW) if need_dW else 0, _ptr(buf), buf.numel(), _ptr(dev_err), _stream()),
                "gq_linear_xent")
     return loss, dX, dW
+
+
+# --------------------------------------------------------------------------
+# products of 8-bit integers
+# --------------------------------------------------------------------------
+
+def _codes(rows, cols, dev):
+    """A new int8 matrix with a leading dimension that is a multiple of 16."""
+    pitch = (cols + 15) // 16 * 16
+    return torch.empty(rows, pitch, dtype=torch.int8, device=dev)[:, :cols]
+
+
+def _ld_i8(t, name):
+    """Leading dimension of an int8 matrix whose rows can be read to a multiple of 16 bytes."""
+    _cuda(t, torch.int8, name)
+    ld = _rows(t)
+    rows, cols = t.shape
+    if rows > 1 and ld % 16 or t.data_ptr() % 16:
+        raise GQError(f"{name}: int8 rows must start 16-byte aligned, at a pitch that is a multiple of 16")
+    pitch = (cols + 15) // 16 * 16
+    if rows == 1:
+        ld = max(pitch, ld // 16 * 16)
+    end = t.storage_offset() + (rows - 1) * ld + pitch
+    if rows > 0 and end > t.untyped_storage().nbytes():
+        raise GQError(f"{name}: the last row must be readable to a multiple of 16 bytes")
+    return max(ld, pitch)
+
+
+def _scales(t, count, ref, name):
+    if t is None:
+        raise GQError(f"{name} is missing")
+    return _vec32(t, count, ref, name)
+
+
+def _out(out, shape, dtype, dev, name):
+    """`out`, or a new matrix of that shape and type whose rows start 16-byte aligned."""
+    if out is None:
+        a = 16 // torch.empty((), dtype=dtype).element_size()
+        return torch.empty_strided(shape, ((shape[1] + a - 1) // a * a, 1), dtype=dtype, device=dev)
+    _typed(out, name)
+    if tuple(out.shape) != tuple(shape) or out.device != dev:
+        raise GQError(f"{name}: expected {tuple(shape)} on {dev}, got {tuple(out.shape)} on {out.device}")
+    return out
+
+
+def _ld_any(t, cols):
+    """Leading dimension; of a single row any will do."""
+    ld = _rows(t)
+    return max(ld, cols) if t.shape[0] <= 1 else ld
+
+
+def quantize_i8(X: torch.Tensor, transpose: bool = False, out: torch.Tensor | None = None,
+                scale: torch.Tensor | None = None, ws: "Workspace | None" = None):
+    """(codes, scale) of X's rows, or, with transpose, of its columns (the
+    codes of column i are then row i): 8-bit integers and the fp32 value that
+    one stands for (gq_quantize_i8)."""
+    ty = _typed(X, "X")
+    n, d = X.shape
+    ldx = _ld_any(X, d)
+    rows, cols = (d, n) if transpose else (n, d)
+    if out is None:
+        out = _codes(rows, cols, X.device)
+    elif tuple(out.shape) != (rows, cols) or out.device != X.device:
+        raise GQError(f"out must be int8 {rows} x {cols} on {X.device}")
+    scale = _new32(rows, X) if scale is None else _vec32(scale, rows, X, "scale")
+    if n == 0:
+        return out, scale.zero_() if transpose else scale
+    L = lib()
+    with _on(X.device):
+        wb = int(L.gq_quantize_i8_workspace_bytes(n, d, int(transpose)))
+        buf = None if wb == 0 else ws.get(wb) if ws is not None else torch.empty(wb, dtype=torch.uint8, device=X.device)
+        _check(L.gq_quantize_i8(_ptr(X), ty, n, d, ldx, int(transpose), _ptr(out), _ld_i8(out, "out"), _ptr(scale),
+                                _ptr(buf), wb, _stream()), "gq_quantize_i8")
+    return out, scale
+
+
+def gemm_i8(A: torch.Tensor, scale_a: torch.Tensor, B: torch.Tensor, scale_b: torch.Tensor,
+            bias: torch.Tensor | None = None, act: int = ACT_NONE, dtype: torch.dtype = torch.float32,
+            out: torch.Tensor | None = None, ws: "Workspace | None" = None, dev_err: torch.Tensor | None = None):
+    """act(scale_a A B^T scale_b + bias) of int8 matrices A [m x k] and B
+    [n x k], one scale for each row of both (gq_gemm_i8): m x n of `dtype`, or
+    of out's type."""
+    m, k = A.shape
+    n = B.shape[0]
+    if B.dim() != 2 or B.shape[1] != k or B.device != A.device:
+        raise GQError("A [m x k] and B [n x k] need the same k and device")
+    lda, ldb = _ld_i8(A, "A"), _ld_i8(B, "B")
+    _scales(scale_a, m, A, "scale_a")
+    _scales(scale_b, n, A, "scale_b")
+    _vec32(bias, n, A, "bias")
+    if out is None and dtype not in _TYPES:
+        raise GQError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+    out = _out(out, (m, n), dtype, A.device, "out")
+    L = lib()
+    with _on(A.device):
+        wb = int(L.gq_gemm_i8_workspace_bytes(m, n, k))
+        buf = None if wb == 0 else ws.get(wb) if ws is not None else torch.empty(wb, dtype=torch.uint8, device=A.device)
+        _check(L.gq_gemm_i8(_ptr(A), m, lda, _ptr(scale_a), _ptr(B), n, ldb, _ptr(scale_b), k, _ptr(bias), act,
+                            _ptr(out), _TYPES[out.dtype], _ld_any(out, n), _ptr(buf), wb, _ptr(dev_err), _stream()),
+               "gq_gemm_i8")
+    return out
+
+
+def linear_i8(X: torch.Tensor, W: torch.Tensor, scale_w: torch.Tensor, bias: torch.Tensor | None = None,
+              act: int = ACT_NONE, out: torch.Tensor | None = None, ws: "Workspace | None" = None,
+              dev_err: torch.Tensor | None = None):
+    """act(X W^T + bias) with X's rows quantized to 8 bits in the call and the
+    weights as quantize_i8 left them, out x k codes and a scale for each output
+    channel (gq_linear_i8).  The result has X's type, or out's."""
+    ty = _typed(X, "X")
+    n, k = X.shape
+    if W.dim() != 2 or W.shape[1] != k or W.device != X.device:
+        raise GQError("X [n x k] and W [out x k] need the same k and device")
+    m = W.shape[0]
+    ldw = _ld_i8(W, "W")
+    _scales(scale_w, m, X, "scale_w")
+    _vec32(bias, m, X, "bias")
+    out = _out(out, (n, m), X.dtype, X.device, "out")
+    L = lib()
+    with _on(X.device):
+        wb = int(L.gq_linear_i8_workspace_bytes(n, k, m))
+        buf = ws.get(wb) if ws is not None else torch.empty(wb, dtype=torch.uint8, device=X.device)
+        _check(L.gq_linear_i8(_ptr(X), ty, n, k, _ld_any(X, k), _ptr(W), m, ldw, _ptr(scale_w), _ptr(bias), act,
+                              _ptr(out), _TYPES[out.dtype], _ld_any(out, m), _ptr(buf), buf.numel(), _ptr(dev_err),
+                              _stream()), "gq_linear_i8")
+    return out
+
+
+def linear_i8_bwd(dY: torch.Tensor, X: torch.Tensor, W: torch.Tensor, need_dX: bool = True, need_dW: bool = True,
+                  dX: torch.Tensor | None = None, dW: torch.Tensor | None = None, dbias: torch.Tensor | None = None,
+                  ws: "Workspace | None" = None, dev_err: torch.Tensor | None = None):
+    """(dX, dW, dbias) of the linear layer, its products on operands
+    quantized in the call (gq_linear_i8_bwd): X [n x k] and W [out x k] are the
+    layer's full-precision ones, dY [n x out] the gradient of X W^T + bias.
+    dX has X's type, dW W's.  need_dX / need_dW leave one out (None in its
+    place; without dW there is no dbias)."""
+    ty = _typed(X, "X")
+    tw = _typed(W, "W")
+    n, k = X.shape
+    m = W.shape[0]
+    if W.dim() != 2 or W.shape[1] != k or W.device != X.device:
+        raise GQError("X [n x k] and W [out x k] need the same k and device")
+    if tuple(dY.shape) != (n, m) or dY.dtype != X.dtype or dY.device != X.device:
+        raise GQError(f"dY must be {X.dtype} {n} x {m} on {X.device}")
+    dX = _out(dX, (n, k), X.dtype, X.device, "dX") if need_dX else None
+    dW = _out(dW, (m, k), W.dtype, X.device, "dW") if need_dW else None
+    dbias = (_new32(m, X) if dbias is None else _vec32(dbias, m, X, "dbias")) if need_dW else None
+    L = lib()
+    with _on(X.device):
+        wb = int(L.gq_linear_i8_bwd_workspace_bytes(n, k, m, int(need_dX), int(need_dW)))
+        buf = ws.get(wb) if ws is not None else torch.empty(wb, dtype=torch.uint8, device=X.device)
+        _check(L.gq_linear_i8_bwd(_ptr(dY), _ld_any(dY, m), _ptr(X), _ld_any(X, k), ty, n, k, m, _ptr(W), tw,
+                                  _ld_any(W, k), _ptr(dX), _TYPES[dX.dtype] if need_dX else 0,
+                                  _ld_any(dX, k) if need_dX else 0, _ptr(dW), _TYPES[dW.dtype] if need_dW else 0,
+                                  _ld_any(dW, k) if need_dW else 0, _ptr(dbias), _ptr(buf), buf.numel(),
+                                  _ptr(dev_err), _stream()), "gq_linear_i8_bwd")
+    return dX, dW, dbias
+
+
+# --------------------------------------------------------------------------
+# optimizer
+# --------------------------------------------------------------------------
+
+ADAM_BLOCK = 256  # values of an 8-bit moment that share an exponent
+
+
+def adam_moment(codes: torch.Tensor, exponents: torch.Tensor, second: bool, dtype: torch.dtype = torch.float32,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values of an 8-bit first or second moment (gq_adam_moment)."""
+    _cuda(codes, torch.uint8, "codes")
+    _cuda(exponents, torch.uint8, "exponents")
+    n = codes.numel()
+    if not codes.is_contiguous() or not exponents.is_contiguous() or exponents.device != codes.device \
+            or exponents.numel() != (n + ADAM_BLOCK - 1) // ADAM_BLOCK:
+        raise GQError(f"codes and their exponents, one of each {ADAM_BLOCK}, must be contiguous on one device")
+    if out is None:
+        if dtype not in _TYPES:
+            raise GQError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+        out = torch.empty(codes.shape, dtype=dtype, device=codes.device)
+    elif out.shape != codes.shape or out.device != codes.device or not out.is_contiguous():
+        raise GQError("out must be contiguous, of the codes' shape and device")
+    with _on(codes.device):
+        _check(lib().gq_adam_moment(_ptr(codes), _ptr(exponents), n, int(second), _ptr(out), _typed(out, "out"),
+                                    _stream()), "gq_adam_moment")
+    return out
+
+
+class AdamW:
+    """AdamW over a list of parameters, every step one launch for all of them
+    (gq_adamw_step).  Parameters: CUDA tensors of float32, bfloat16 or float16,
+    contiguous or 2-D with unit column stride; those of one type share a launch.
+    state_bits: 32, or 8 for block-wise 8-bit moments with stochastic rounding
+    drawn from seed and the step's number.
+
+    grads: the gradients' buffers where they stay the same from step to step;
+    otherwise step takes them.  state: moments to go on with, the optimizer's own
+    from then on: (m, v) lists of contiguous float32 tensors, or (m, v, m_exp,
+    v_exp) lists of uint8 ones; step: the number of steps they have seen.
+    capturable: the step number and lr live on the device, so that a step that a
+    graph replays counts, and set_lr reaches it."""
+
+    def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
+                 state_bits: int = 32, seed: int = 0, state=None, step: int = 0, grads=None, capturable: bool = False):
+        params = list(params)
+        if state_bits not in (8, 32):
+            raise GQError(f"state_bits must be 8 or 32, got {state_bits}")
+        if not params:
+            raise GQError("AdamW needs parameters")
+        dev = params[0].device
+        for i, t in enumerate(params):
+            _typed(t, f"parameter {i}")
+            if t.device != dev:
+                raise GQError("the parameters must be on one device")
+            self._pitch(t, f"parameter {i}")
+        spans = sorted((t.data_ptr(), t.data_ptr() + self._span(t)) for t in params if t.numel())
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise GQError("no parameter may appear twice or overlap another")
+        self.params, self.state_bits, self.device = params, state_bits, dev
+        self.steps = int(step)
+        blocks = [(t.numel() + ADAM_BLOCK - 1) // ADAM_BLOCK for t in params]
+        if state is None:
+            if state_bits == 32:
+                state = [[torch.zeros(t.numel(), dtype=torch.float32, device=dev) for t in params] for _ in range(2)]
+            else:
+                state = [[torch.zeros(t.numel(), dtype=torch.uint8, device=dev) for t in params] for _ in range(2)] + \
+                        [[torch.zeros(b, dtype=torch.uint8, device=dev) for b in blocks] for _ in range(2)]
+        kind = torch.float32 if state_bits == 32 else torch.uint8
+        if len(state) != (2 if state_bits == 32 else 4):
+            raise GQError("state: (m, v), or (m, v, m_exp, v_exp) for 8-bit moments")
+        for j, part in enumerate(state):
+            for i, t in enumerate(part):
+                want = params[i].numel() if j < 2 else blocks[i]
+                if len(part) != len(params) or t.dtype != kind or t.numel() != want or not t.is_contiguous() \
+                        or t.device != dev:
+                    raise GQError(f"state: contiguous {kind} tensors of each parameter's "
+                                  f"{'values' if j < 2 else 'blocks'} on {dev}")
+        self.m, self.v = state[0], state[1]
+        self.m_exp, self.v_exp = (state[2], state[3]) if state_bits == 8 else (None, None)
+        self._args = AdamwArgs_t(lr, betas[0], betas[1], eps, weight_decay, 0, seed & 0xFFFFFFFFFFFFFFFF, None, None, 0)
+        self._dev = None
+        if capturable:
+            rec = torch.zeros((int(lib().gq_adamw_dev_bytes()) + 7) // 8, dtype=torch.int64, device=dev)
+            rec[0] = self.steps
+            rec[1:2].view(torch.float64)[0] = lr
+            self._dev = rec
+            self._args.dev = rec.data_ptr()
+        # one C array for each parameter type, in the order of the parameters
+        self._groups = {}
+        at = 0
+        for i, t in enumerate(params):
+            cols, ld = self._pitch(t, "")
+            rec = AdamwTensor_t(t.data_ptr(), None, self.m[i].data_ptr(), self.v[i].data_ptr(),
+                                self.m_exp[i].data_ptr() if state_bits == 8 else None,
+                                self.v_exp[i].data_ptr() if state_bits == 8 else None, t.numel(), cols, ld, cols, at)
+            self._groups.setdefault(t.dtype, []).append((i, rec))
+            at += blocks[i]
+        if at > 1 << 32:
+            raise GQError("too many blocks of moments for their noise")
+        self._bound = None
+        if grads is not None:
+            self._bound = self._calls(grads)
+
+    @staticmethod
+    def _pitch(t, name):
+        """(cols, ld) of rows at a pitch, (0, 0) of a dense tensor."""
+        if t.is_contiguous():
+            return 0, 0
+        if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1]:
+            return t.shape[1], t.stride(0)
+        raise GQError(f"{name} must be contiguous, or 2-D with unit column stride")
+
+    @staticmethod
+    def _span(t):
+        return ((t.numel() if t.is_contiguous() else (t.shape[0] - 1) * t.stride(0) + t.shape[1]) * t.element_size())
+
+    def _calls(self, grads):
+        """[(C array, count, parameter type, gradient type)], and the tensors they point to."""
+        grads = list(grads)
+        if len(grads) != len(self.params):
+            raise GQError(f"{len(self.params)} parameters, but {len(grads)} gradients")
+        calls = []
+        for dtype, group in self._groups.items():
+            parts = {}
+            for i, rec in group:
+                g, p = grads[i], self.params[i]
+                if g is None:
+                    continue
+                gt = _typed(g, f"gradient {i}")
+                if g.shape != p.shape or g.device != self.device:
+                    raise GQError(f"gradient {i}: expected {tuple(p.shape)} on {self.device}, got {tuple(g.shape)} on "
+                                  f"{g.device}")
+                cols, ld = self._pitch(g, f"gradient {i}")
+                r = AdamwTensor_t()
+                ctypes.pointer(r)[0] = rec
+                r.g = g.data_ptr()
+                if cols or rec.cols:
+                    cols = cols or rec.cols
+                    r.cols, r.ldp, r.ldg = cols, rec.ldp or cols, ld or cols
+                parts.setdefault(gt, []).append(r)
+            for gt, recs in parts.items():
+                calls.append(((AdamwTensor_t * len(recs))(*recs), len(recs), _TYPES[dtype], gt))
+        return calls, grads
+
+    @property
+    def lr(self) -> float:
+        return self._args.lr
+
+    def set_lr(self, lr: float):
+        """The learning rate from the next step on (with capturable, of replayed steps too)."""
+        self._args.lr = lr
+        if self._dev is not None:
+            self._dev[1:2].view(torch.float64).fill_(lr)
+
+    def step(self, grads=None, grad_scale: torch.Tensor | None = None):
+        """One step.  grads: one for each parameter (None: that one is left as it
+        is); without them those given at the start.  grad_scale: device float32
+        value that the gradients are multiplied by; where it is not finite the step
+        changes nothing (without capturable it still counts)."""
+        if grads is None and self._bound is None:
+            raise GQError("step needs gradients: none were given at the start")
+        calls, held = self._bound if grads is None else self._calls(grads)
+        a = self._args
+        a.grad_scale = None
+        if grad_scale is not None:
+            if grad_scale.numel() != 1 or grad_scale.dtype != torch.float32 or grad_scale.device != self.device:
+                raise GQError(f"grad_scale must be one float32 value on {self.device}")
+            a.grad_scale = grad_scale.data_ptr()
+        self.steps += 1
+        a.step = self.steps
+        L = lib()
+        with _on(self.device):
+            s = _stream()
+            a.advance = 1
+            for arr, count, pt, gt in calls:
+                _check(L.gq_adamw_step(arr, count, pt, gt, self.state_bits, ctypes.byref(a), s), "gq_adamw_step")
+                a.advance = 0
+
+    def device_steps(self) -> torch.Tensor | None:
+        """With capturable: the step number that the device holds (int64 view)."""
+        return None if self._dev is None else self._dev[:1]
+
+    def moments(self, dtype: torch.dtype = torch.float32):
+        """(m, v): the moments' values, each in its parameter's shape."""
+        if self.state_bits == 32:
+            return tuple([t.to(dtype).view(p.shape) for t, p in zip(part, self.params)] for part in (self.m, self.v))
+        return tuple([adam_moment(t, e, second, dtype).view(p.shape) for t, e, p in zip(part, exps, self.params)]
+                     for second, part, exps in ((False, self.m, self.m_exp), (True, self.v, self.v_exp)))
 
 
 # --------------------------------------------------------------------------

@@ -1,0 +1,907 @@
+// gq_gnorm.cu -- group normalization of segments of rows (the graphs of a batch,
+// channels last) with the activation behind it, forward and backward.
+//
+//   over the rows r of segment s and the channels c of group g (N cells):
+//     mean = sum x / N,  rstd = 1 / sqrt(sum (x - mean)^2 / N + eps)
+//     z = (x - mean) rstd gamma + beta,  y = act(z)
+//   dz = dy act'(z),  h = dz gamma
+//     dx = rstd (h - mean(h) - xhat mean(h xhat)),  dgamma = sum dz xhat,  dbeta = sum dz
+//
+// Everything is bound by memory.  Two forms:
+//
+//   short segments  one block a segment reads its rows, makes the statistics and
+//                   reads the rows again, from L1 or L2: DRAM sees x once.  The
+//                   backward blocks take several segments and keep their
+//                   sums of dgamma and dbeta.
+//   long segments   three launches: statistics of pieces (a chunk of rows cut at
+//                   segment borders), their combination, and the rows again.  A piece's
+//                   number is chunk + segment: neither falls along the rows and
+//                   one of them grows from piece to piece, so the numbers are
+//                   distinct and every kernel finds them without a table.
+//
+// A thread owns 16 bytes of channels and walks rows, so groups of any width are
+// met only when channels' sums are put together.  Variances are sums of squares
+// around the first value that a thread meets, then around the mean of the parts:
+// no difference of large squares.  All sums run in fp32 in a fixed order.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cmath>
+
+#include "gq_common.cuh"
+#include "gq_internal.cuh"
+#include "gq_sm100.cuh"
+#include "gq_train.h"
+
+namespace gq {
+namespace {
+
+constexpr int kMaxThreads = 512;
+
+struct Args {
+  const void* X;
+  const void* dY;
+  void* Y;               // or dX
+  int64_t n, ldx, lddy, ldy;
+  int d, groups, cg;
+  const int64_t* ptr;    // s + 1 offsets, or null: one segment of n rows
+  int64_t s;
+  const float* gamma;
+  const float* beta;
+  float eps;
+  float* mean;
+  float* rstd;
+  int vpr, tx, ry;       // vectors of a row, of a slab's row; rows at a time
+  // long segments
+  int64_t rows_per, chunks;
+  float2* part;          // [chunks + s][d]
+  float2* hsum;          // backward: [s][groups] means of h and h xhat
+  float2* tot;           // backward: [chunks or blocks][d] sums of dz xhat and dz
+  int64_t parts;
+  float* dgamma;
+  float* dbeta;
+};
+
+// Rows of a segment, kept inside [0, n] whatever ptr holds.
+__device__ __forceinline__ void segment(const Args& p, int64_t j, int64_t& r0, int64_t& r1) {
+  if (p.ptr == nullptr) {
+    r0 = 0;
+    r1 = p.n;
+    return;
+  }
+  r0 = min(max(p.ptr[j], (int64_t)0), p.n);
+  r1 = min(max(p.ptr[j + 1], r0), p.n);
+}
+// The first segment that ends behind row r.
+__device__ __forceinline__ int64_t first_segment(const Args& p, int64_t r) {
+  if (p.ptr == nullptr) return 0;
+  int64_t lo = 0, hi = p.s;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (p.ptr[mid + 1] > r)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
+
+// ------------------------------------------------------------------- types --
+template <typename T, int V>
+__device__ __forceinline__ void load(const void* base, int64_t i, float (&x)[V]) {
+  if (V == 1) {
+    x[0] = (float)static_cast<const T*>(base)[i];
+  } else {
+    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const T*>(base) + i);
+    const T* e = reinterpret_cast<const T*>(&w);
+#pragma unroll
+    for (int k = 0; k < V; ++k) x[k] = (float)e[k];
+  }
+}
+__device__ __forceinline__ void put(float& o, float x) { o = x; }
+__device__ __forceinline__ void put(__nv_bfloat16& o, float x) { o = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void put(__half& o, float x) { o = __float2half_rn(x); }
+template <typename T, int V>
+__device__ __forceinline__ void store(void* base, int64_t i, const float (&x)[V]) {
+  if (V == 1) {
+    put(static_cast<T*>(base)[i], x[0]);
+  } else {
+    uint4 w;
+    T* e = reinterpret_cast<T*>(&w);
+#pragma unroll
+    for (int k = 0; k < V; ++k) put(e[k], x[k]);
+    *reinterpret_cast<uint4*>(static_cast<T*>(base) + i) = w;
+  }
+}
+
+// 1 / (1 + e^-z); 0 and 1 where e^-z leaves fp32's range
+__device__ __forceinline__ float sigmoid(float z) { return __frcp_rn(1.0f + __expf(-z)); }
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+  return ACT == GQ_ACT_RELU ? (z > 0.0f ? z : 0.0f) : ACT == GQ_ACT_SILU ? z * sigmoid(z) : z;
+}
+template <int ACT>
+__device__ __forceinline__ float derivative(float z) {
+  if (ACT == GQ_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+  if (ACT == GQ_ACT_SILU) {
+    const float g = sigmoid(z);
+    return g * fmaf(z, 1.0f - g, 1.0f);
+  }
+  return 1.0f;
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) x += __shfl_xor_sync(FULL, x, k);
+  return x;
+}
+
+// ---------------------------------------------------------- sums of a piece --
+// Rows [r0, r1) of one thread's channels: mean and sum of squares around it.
+template <typename T, int V>
+__device__ __forceinline__ void spread(const Args& p, int64_t r0, int64_t r1, int ry, int c, float (&mean)[V],
+                                       float (&m2)[V], int& rows) {
+  float k[V], s[V], q[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) k[e] = s[e] = q[e] = 0.0f;
+  int64_t r = r0 + ry;
+  rows = r < r1 ? (int)((r1 - r + p.ry - 1) / p.ry) : 0;
+  if (rows > 0) load<T, V>(p.X, r * p.ldx + c, k);
+#pragma unroll 4
+  for (int i = 0; i < rows; ++i, r += p.ry) {
+    float x[V];
+    load<T, V>(p.X, r * p.ldx + c, x);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float y = x[e] - k[e];
+      s[e] += y;
+      q[e] = fmaf(y, y, q[e]);
+    }
+  }
+  const float inv = rows > 0 ? 1.0f / (float)rows : 0.0f;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const float m = s[e] * inv;
+    mean[e] = k[e] + m;
+    m2[e] = fmaxf(fmaf(-s[e], m, q[e]), 0.0f);
+  }
+}
+
+// What the backward pass needs of a thread's channels.
+template <int V>
+struct Chan {
+  float mu[V], rs[V], ga[V], be[V];
+};
+template <int V>
+__device__ __forceinline__ void channels(const Args& p, int64_t j, int c, Chan<V>& h) {
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const int64_t g = j * p.groups + (c + e) / p.cg;
+    h.mu[e] = p.mean[g];
+    h.rs[e] = p.rstd[g];
+    h.ga[e] = p.gamma != nullptr ? p.gamma[c + e] : 1.0f;
+    h.be[e] = p.beta != nullptr ? p.beta[c + e] : 0.0f;
+  }
+}
+
+// sums of dz xhat and of dz
+template <typename T, int V, int ACT>
+__device__ __forceinline__ void slopes(const Args& p, int64_t r0, int64_t r1, int ry, int c, const Chan<V>& h,
+                                       float (&a)[V], float (&b)[V]) {
+#pragma unroll
+  for (int e = 0; e < V; ++e) a[e] = b[e] = 0.0f;
+#pragma unroll 4
+  for (int64_t r = r0 + ry; r < r1; r += p.ry) {
+    float x[V], y[V];
+    load<T, V>(p.X, r * p.ldx + c, x);
+    load<T, V>(p.dY, r * p.lddy + c, y);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float xh = (x[e] - h.mu[e]) * h.rs[e];
+      const float dz = ACT == GQ_ACT_NONE ? y[e] : y[e] * derivative<ACT>(fmaf(xh, h.ga[e], h.be[e]));
+      a[e] = fmaf(dz, xh, a[e]);
+      b[e] += dz;
+    }
+  }
+}
+
+// Several rows are read before the first is written: the output may be an input,
+// so the compiler cannot move a read ahead of a write by itself.
+constexpr int kAhead = 4, kAheadBwd = 2;
+
+template <typename T, int V, int ACT>
+__device__ __forceinline__ void apply(const Args& p, int64_t r0, int64_t r1, int ry, int c, const float (&mu)[V],
+                                      const float (&sc)[V], const float (&be)[V]) {
+  for (int64_t r = r0 + ry; r < r1; r += kAhead * p.ry) {
+    float x[kAhead][V];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (r + u * p.ry < r1) load<T, V>(p.X, (r + u * p.ry) * p.ldx + c, x[u]);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (r + u * p.ry < r1) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) x[u][e] = activate<ACT>(fmaf(x[u][e] - mu[e], sc[e], be[e]));
+        store<T, V>(p.Y, (r + u * p.ry) * p.ldy + c, x[u]);
+      }
+    }
+  }
+}
+
+template <typename T, int V, int ACT>
+__device__ __forceinline__ void apply_bwd(const Args& p, int64_t r0, int64_t r1, int ry, int c, const Chan<V>& h,
+                                          const float (&h1)[V], const float (&h2)[V]) {
+  for (int64_t r = r0 + ry; r < r1; r += kAheadBwd * p.ry) {
+    float x[kAheadBwd][V], y[kAheadBwd][V];
+#pragma unroll
+    for (int u = 0; u < kAheadBwd; ++u)
+      if (r + u * p.ry < r1) {
+        load<T, V>(p.X, (r + u * p.ry) * p.ldx + c, x[u]);
+        load<T, V>(p.dY, (r + u * p.ry) * p.lddy + c, y[u]);
+      }
+#pragma unroll
+    for (int u = 0; u < kAheadBwd; ++u) {
+      if (r + u * p.ry < r1) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float xh = (x[u][e] - h.mu[e]) * h.rs[e];
+          const float dz = ACT == GQ_ACT_NONE ? y[u][e] : y[u][e] * derivative<ACT>(fmaf(xh, h.ga[e], h.be[e]));
+          x[u][e] = h.rs[e] * (fmaf(dz, h.ga[e], -h1[e]) - xh * h2[e]);
+        }
+        store<T, V>(p.Y, (r + u * p.ry) * p.ldy + c, x[u]);
+      }
+    }
+  }
+}
+
+// Rows of thread `ry` among `rows`.
+__device__ __forceinline__ int rows_of(int64_t rows, int ry, int step) {
+  return ry < rows ? (int)((rows - ry + step - 1) / step) : 0;
+}
+
+// Channel `k` of the slab from its threads' means and squares in red.
+template <int V>
+__device__ __forceinline__ float2 merge(const float2* red, const Args& p, int k, int64_t rows) {
+  const int tv = k / V, e = k - tv * V;
+  float s = 0.0f;
+  for (int y = 0; y < p.ry; ++y) s = fmaf((float)rows_of(rows, y, p.ry), red[(y * p.tx + tv) * V + e].x, s);
+  const float mean = s / (float)rows;
+  float q = 0.0f;
+  for (int y = 0; y < p.ry; ++y) {
+    const float2 w = red[(y * p.tx + tv) * V + e];
+    const float dev = w.x - mean;
+    q += fmaf((float)rows_of(rows, y, p.ry) * dev, dev, w.y);
+  }
+  return make_float2(mean, q);
+}
+
+template <int V>
+__device__ __forceinline__ float2 add_up(const float2* red, const Args& p, int k) {
+  const int tv = k / V, e = k - tv * V;
+  float2 s = make_float2(0.0f, 0.0f);
+  for (int y = 0; y < p.ry; ++y) {
+    const float2 w = red[(y * p.tx + tv) * V + e];
+    s.x += w.x;
+    s.y += w.y;
+  }
+  return s;
+}
+
+// ---------------------------------------------------------- short segments --
+// Shared memory: [d] channel values, [threads x V] of the threads'; the backward
+// kernel's [d] sums over its segments behind them.
+template <typename T, int V, int ACT>
+__global__ void __launch_bounds__(kMaxThreads) short_fwd_kernel(const Args p) {
+  extern __shared__ float2 sm[];
+  float2* ch = sm;
+  float2* red = sm + p.d;
+  grid_wait();
+  const int t = threadIdx.x, tx = t % p.tx, ry = t / p.tx;
+  const int warp = t >> 5, lane = t & 31, warps = blockDim.x >> 5;
+  for (int64_t j = blockIdx.x; j < p.s; j += gridDim.x) {
+    int64_t r0, r1;
+    segment(p, j, r0, r1);
+    const int64_t rows = r1 - r0;
+    if (rows == 0) {
+      for (int g = t; g < p.groups; g += blockDim.x) {
+        p.mean[j * p.groups + g] = 0.0f;
+        p.rstd[j * p.groups + g] = __frcp_rn(__fsqrt_rn(p.eps));
+      }
+      continue;
+    }
+    for (int v0 = 0; v0 < p.vpr; v0 += p.tx) {
+      const int c = (v0 + tx) * V;
+      if (ry < p.ry && v0 + tx < p.vpr) {
+        float mean[V], m2[V];
+        int mine;
+        spread<T, V>(p, r0, r1, ry, c, mean, m2, mine);
+#pragma unroll
+        for (int e = 0; e < V; ++e) red[(ry * p.tx + tx) * V + e] = make_float2(mean[e], m2[e]);
+      }
+      __syncthreads();
+      for (int k = t; k < min(p.tx, p.vpr - v0) * V; k += blockDim.x) ch[v0 * V + k] = merge<V>(red, p, k, rows);
+      __syncthreads();
+    }
+    for (int g = warp; g < p.groups; g += warps) {
+      float s = 0.0f;
+      for (int k = lane; k < p.cg; k += 32) s += ch[g * p.cg + k].x;
+      const float mean = warp_sum(s) / (float)p.cg;
+      float q = 0.0f;
+      for (int k = lane; k < p.cg; k += 32) {
+        const float2 w = ch[g * p.cg + k];
+        q += fmaf((float)rows * (w.x - mean), w.x - mean, w.y);
+      }
+      const float var = warp_sum(q) / ((float)rows * (float)p.cg);
+      const float rstd = __frcp_rn(__fsqrt_rn(var + p.eps));
+      for (int k = lane; k < p.cg; k += 32) ch[g * p.cg + k] = make_float2(mean, rstd);
+      if (lane == 0) {
+        p.mean[j * p.groups + g] = mean;
+        p.rstd[j * p.groups + g] = rstd;
+      }
+    }
+    __syncthreads();
+    for (int v0 = 0; v0 < p.vpr; v0 += p.tx) {
+      const int c = (v0 + tx) * V;
+      if (ry < p.ry && v0 + tx < p.vpr) {
+        float mu[V], sc[V], be[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float2 w = ch[c + e];
+          mu[e] = w.x;
+          sc[e] = w.y * (p.gamma != nullptr ? p.gamma[c + e] : 1.0f);
+          be[e] = p.beta != nullptr ? p.beta[c + e] : 0.0f;
+        }
+        apply<T, V, ACT>(p, r0, r1, ry, c, mu, sc, be);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <typename T, int V, int ACT>
+__global__ void __launch_bounds__(kMaxThreads) short_bwd_kernel(const Args p) {
+  extern __shared__ float2 sm[];
+  float2* ch = sm;
+  float2* tot = sm + p.d;
+  float2* red = tot + p.d;
+  grid_wait();
+  const int t = threadIdx.x, tx = t % p.tx, ry = t / p.tx;
+  const int warp = t >> 5, lane = t & 31, warps = blockDim.x >> 5;
+  for (int k = t; k < p.d; k += blockDim.x) tot[k] = make_float2(0.0f, 0.0f);
+  __syncthreads();
+  for (int64_t j = blockIdx.x; j < p.s; j += gridDim.x) {
+    int64_t r0, r1;
+    segment(p, j, r0, r1);
+    const int64_t rows = r1 - r0;
+    if (rows == 0) continue;
+    for (int v0 = 0; v0 < p.vpr; v0 += p.tx) {
+      const int c = (v0 + tx) * V;
+      if (ry < p.ry && v0 + tx < p.vpr) {
+        Chan<V> h;
+        float a[V], b[V];
+        channels<V>(p, j, c, h);
+        slopes<T, V, ACT>(p, r0, r1, ry, c, h, a, b);
+#pragma unroll
+        for (int e = 0; e < V; ++e) red[(ry * p.tx + tx) * V + e] = make_float2(a[e], b[e]);
+      }
+      __syncthreads();
+      for (int k = t; k < min(p.tx, p.vpr - v0) * V; k += blockDim.x) {
+        const float2 w = add_up<V>(red, p, k);
+        ch[v0 * V + k] = w;
+        tot[v0 * V + k].x += w.x;
+        tot[v0 * V + k].y += w.y;
+      }
+      __syncthreads();
+    }
+    for (int g = warp; g < p.groups; g += warps) {
+      float s1 = 0.0f, s2 = 0.0f;
+      for (int k = lane; k < p.cg; k += 32) {
+        const float2 w = ch[g * p.cg + k];
+        const float ga = p.gamma != nullptr ? p.gamma[g * p.cg + k] : 1.0f;
+        s1 = fmaf(ga, w.y, s1);
+        s2 = fmaf(ga, w.x, s2);
+      }
+      const float inv = 1.0f / ((float)rows * (float)p.cg);
+      s1 = warp_sum(s1) * inv;
+      s2 = warp_sum(s2) * inv;
+      for (int k = lane; k < p.cg; k += 32) ch[g * p.cg + k] = make_float2(s1, s2);
+    }
+    __syncthreads();
+    for (int v0 = 0; v0 < p.vpr; v0 += p.tx) {
+      const int c = (v0 + tx) * V;
+      if (ry < p.ry && v0 + tx < p.vpr) {
+        Chan<V> h;
+        float h1[V], h2[V];
+        channels<V>(p, j, c, h);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float2 w = ch[c + e];
+          h1[e] = w.x;
+          h2[e] = w.y;
+        }
+        apply_bwd<T, V, ACT>(p, r0, r1, ry, c, h, h1, h2);
+      }
+    }
+    __syncthreads();
+  }
+  for (int k = t; k < p.d; k += blockDim.x) p.tot[(int64_t)blockIdx.x * p.d + k] = tot[k];
+}
+
+// ----------------------------------------------------------- long segments --
+// block: chunk blockIdx.x of rows, slab blockIdx.y of channels
+template <typename T, int V>
+__global__ void __launch_bounds__(kMaxThreads) stats_kernel(const Args p) {
+  extern __shared__ float2 red[];
+  grid_wait();
+  const int t = threadIdx.x, tx = t % p.tx, ry = t / p.tx;
+  const int v0 = blockIdx.y * p.tx, c = (v0 + tx) * V;
+  const bool live = ry < p.ry && v0 + tx < p.vpr;
+  const int64_t chunk = blockIdx.x, a = chunk * p.rows_per, b = min(p.n, a + p.rows_per);
+  for (int64_t j = first_segment(p, a); j < p.s; ++j) {
+    int64_t r0, r1;
+    segment(p, j, r0, r1);
+    if (r0 >= b) break;
+    r0 = max(r0, a);
+    r1 = min(r1, b);
+    if (r1 <= r0) continue;
+    if (live) {
+      float mean[V], m2[V];
+      int mine;
+      spread<T, V>(p, r0, r1, ry, c, mean, m2, mine);
+#pragma unroll
+      for (int e = 0; e < V; ++e) red[(ry * p.tx + tx) * V + e] = make_float2(mean[e], m2[e]);
+    }
+    __syncthreads();
+    for (int k = t; k < min(p.tx, p.vpr - v0) * V; k += blockDim.x)
+      p.part[(chunk + j) * p.d + v0 * V + k] = merge<V>(red, p, k, r1 - r0);
+    __syncthreads();
+  }
+}
+
+// A block (BLOCK) or a warp a segment and group: its pieces' channels together.
+constexpr int kCombine = 512;
+template <bool BLOCK>
+__device__ __forceinline__ float unit_sum(float x, float* sh) {
+  x = warp_sum(x);
+  if (!BLOCK) return x;
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
+  __syncthreads();
+  float s = 0.0f;
+  for (int w = 0; w < kCombine / 32; ++w) s += sh[w];
+  return s;
+}
+template <bool BWD, bool BLOCK>
+__global__ void __launch_bounds__(kCombine) combine_kernel(const Args p) {
+  __shared__ float sh[kCombine / 32];
+  grid_wait();
+  constexpr int per = BLOCK ? 1 : kCombine / 32, step = BLOCK ? kCombine : 32;
+  const int64_t unit = (int64_t)blockIdx.x * per + (BLOCK ? 0 : threadIdx.x >> 5);
+  const int lane = BLOCK ? threadIdx.x : threadIdx.x & 31;
+  if (unit >= p.s * p.groups) return;
+  const int64_t j = unit / p.groups;
+  const int g = (int)(unit - j * p.groups);
+  int64_t r0, r1;
+  segment(p, j, r0, r1);
+  const int64_t rows = r1 - r0;
+  if (rows == 0) {
+    if (!BWD && lane == 0) {
+      p.mean[unit] = 0.0f;
+      p.rstd[unit] = __frcp_rn(__fsqrt_rn(p.eps));
+    }
+    return;
+  }
+  const int64_t c0 = r0 / p.rows_per, c1 = (r1 - 1) / p.rows_per;
+  const int64_t cells = (c1 - c0 + 1) * p.cg;
+  auto count = [&](int64_t k) {  // rows of the segment's piece in its k-th chunk
+    return (float)(min(r1, (c0 + k + 1) * p.rows_per) - max(r0, (c0 + k) * p.rows_per));
+  };
+  float s1 = 0.0f, s2 = 0.0f;
+  for (int64_t i = lane; i < cells; i += step) {
+    const int64_t k = i / p.cg;
+    const int c = g * p.cg + (int)(i - k * p.cg);
+    const float2 w = p.part[(c0 + k + j) * p.d + c];
+    if (BWD) {
+      const float ga = p.gamma != nullptr ? p.gamma[c] : 1.0f;
+      s1 = fmaf(ga, w.y, s1);
+      s2 = fmaf(ga, w.x, s2);
+    } else {
+      s1 = fmaf(count(k), w.x, s1);
+    }
+  }
+  const float inv = 1.0f / ((float)rows * (float)p.cg);
+  s1 = unit_sum<BLOCK>(s1, sh) * inv;
+  if constexpr (BWD) {
+    s2 = unit_sum<BLOCK>(s2, sh) * inv;
+    if (lane == 0) p.hsum[unit] = make_float2(s1, s2);
+  } else {
+    for (int64_t i = lane; i < cells; i += step) {
+      const int64_t k = i / p.cg;
+      const float2 w = p.part[(c0 + k + j) * p.d + g * p.cg + (int)(i - k * p.cg)];
+      const float dev = w.x - s1;
+      s2 += fmaf(count(k) * dev, dev, w.y);
+    }
+    s2 = unit_sum<BLOCK>(s2, sh) * inv;
+    if (lane == 0) {
+      p.mean[unit] = s1;
+      p.rstd[unit] = __frcp_rn(__fsqrt_rn(s2 + p.eps));
+    }
+  }
+}
+
+template <typename T, int V, int ACT>
+__global__ void __launch_bounds__(kMaxThreads) apply_kernel(const Args p) {
+  grid_wait();
+  const int t = threadIdx.x, tx = t % p.tx, ry = t / p.tx;
+  const int v0 = blockIdx.y * p.tx, c = (v0 + tx) * V;
+  if (ry >= p.ry || v0 + tx >= p.vpr) return;
+  const int64_t a = (int64_t)blockIdx.x * p.rows_per, b = min(p.n, a + p.rows_per);
+  for (int64_t j = first_segment(p, a); j < p.s; ++j) {
+    int64_t r0, r1;
+    segment(p, j, r0, r1);
+    if (r0 >= b) break;
+    r0 = max(r0, a);
+    r1 = min(r1, b);
+    if (r1 <= r0) continue;
+    float mu[V], sc[V], be[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const int64_t g = j * p.groups + (c + e) / p.cg;
+      mu[e] = p.mean[g];
+      sc[e] = p.rstd[g] * (p.gamma != nullptr ? p.gamma[c + e] : 1.0f);
+      be[e] = p.beta != nullptr ? p.beta[c + e] : 0.0f;
+    }
+    apply<T, V, ACT>(p, r0, r1, ry, c, mu, sc, be);
+  }
+}
+
+template <typename T, int V, int ACT>
+__global__ void __launch_bounds__(kMaxThreads) slopes_kernel(const Args p) {
+  extern __shared__ float2 red[];
+  grid_wait();
+  const int t = threadIdx.x, tx = t % p.tx, ry = t / p.tx;
+  const int v0 = blockIdx.y * p.tx, c = (v0 + tx) * V;
+  const bool live = ry < p.ry && v0 + tx < p.vpr;
+  const int64_t chunk = blockIdx.x, a = chunk * p.rows_per, b = min(p.n, a + p.rows_per);
+  float ta[V], tb[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) ta[e] = tb[e] = 0.0f;
+  for (int64_t j = first_segment(p, a); j < p.s; ++j) {
+    int64_t r0, r1;
+    segment(p, j, r0, r1);
+    if (r0 >= b) break;
+    r0 = max(r0, a);
+    r1 = min(r1, b);
+    if (r1 <= r0) continue;
+    if (live) {
+      Chan<V> h;
+      float sa[V], sb[V];
+      channels<V>(p, j, c, h);
+      slopes<T, V, ACT>(p, r0, r1, ry, c, h, sa, sb);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        ta[e] += sa[e];
+        tb[e] += sb[e];
+        red[(ry * p.tx + tx) * V + e] = make_float2(sa[e], sb[e]);
+      }
+    }
+    __syncthreads();
+    for (int k = t; k < min(p.tx, p.vpr - v0) * V; k += blockDim.x)
+      p.part[(chunk + j) * p.d + v0 * V + k] = add_up<V>(red, p, k);
+    __syncthreads();
+  }
+  if (live) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) red[(ry * p.tx + tx) * V + e] = make_float2(ta[e], tb[e]);
+  }
+  __syncthreads();
+  for (int k = t; k < min(p.tx, p.vpr - v0) * V; k += blockDim.x)
+    p.tot[chunk * p.d + v0 * V + k] = add_up<V>(red, p, k);
+}
+
+template <typename T, int V, int ACT>
+__global__ void __launch_bounds__(kMaxThreads) apply_bwd_kernel(const Args p) {
+  grid_wait();
+  const int t = threadIdx.x, tx = t % p.tx, ry = t / p.tx;
+  const int v0 = blockIdx.y * p.tx, c = (v0 + tx) * V;
+  if (ry >= p.ry || v0 + tx >= p.vpr) return;
+  const int64_t a = (int64_t)blockIdx.x * p.rows_per, b = min(p.n, a + p.rows_per);
+  for (int64_t j = first_segment(p, a); j < p.s; ++j) {
+    int64_t r0, r1;
+    segment(p, j, r0, r1);
+    if (r0 >= b) break;
+    r0 = max(r0, a);
+    r1 = min(r1, b);
+    if (r1 <= r0) continue;
+    Chan<V> h;
+    float h1[V], h2[V];
+    channels<V>(p, j, c, h);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float2 w = p.hsum[j * p.groups + (c + e) / p.cg];
+      h1[e] = w.x;
+      h2[e] = w.y;
+    }
+    apply_bwd<T, V, ACT>(p, r0, r1, ry, c, h, h1, h2);
+  }
+}
+
+// dgamma, dbeta from the parts' sums: 32 channels x 32 parts at a time
+__global__ void __launch_bounds__(1024) columns_kernel(const Args p) {
+  __shared__ float2 sh[32][33];
+  grid_wait();
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + x;
+  float2 s = make_float2(0.0f, 0.0f);
+  if (c < p.d)
+    for (int64_t k = y; k < p.parts; k += 32) {
+      const float2 w = p.tot[k * p.d + c];
+      s.x += w.x;
+      s.y += w.y;
+    }
+  sh[y][x] = s;
+  __syncthreads();
+  if (y == 0 && c < p.d) {
+    for (int k = 1; k < 32; ++k) {
+      s.x += sh[k][x].x;
+      s.y += sh[k][x].y;
+    }
+    if (p.dgamma != nullptr) p.dgamma[c] = s.x;
+    if (p.dbeta != nullptr) p.dbeta[c] = s.y;
+  }
+}
+
+// -------------------------------------------------------------------- host --
+bool valid_type(int type) { return type == GQ_F32 || type == GQ_BF16 || type == GQ_F16; }
+int type_bytes(int type) { return type == GQ_F32 ? 4 : 2; }
+
+struct Plan {
+  bool brief;            // one block a segment
+  int threads, tx, ry, vpr, slabs;
+  int64_t rows_per, chunks, blocks;
+};
+
+// A segment of up to kShortBytes stays in a block's share of L2 between its two
+// readings, and one block reads it in the time of the two launches saved.
+constexpr int64_t kShortBytes = 512 << 10;
+constexpr int kShortMaxD = 8192;
+
+Plan make_plan(int64_t n, int d, int64_t s, int64_t max_rows, int bytes, int v, bool bwd) {
+  Plan z{};
+  z.vpr = d / v;
+  const int64_t longest = max_rows > 0 && max_rows < n ? max_rows : s <= 1 || max_rows > 0 ? n : 4 * (n / s + 1);
+  z.brief = longest * d * bytes <= kShortBytes && d <= kShortMaxD;
+  // threads: at least four rows for each where a segment has them
+  z.threads = kMaxThreads;
+  if (z.brief) {
+    const int64_t mean = n / (s > 0 ? s : 1) + 1;
+    while (z.threads > 64 && (int64_t)z.vpr * mean < 4 * (int64_t)z.threads) z.threads /= 2;
+  } else {
+    z.threads = 256;
+  }
+  z.tx = z.vpr < z.threads ? z.vpr : z.threads;
+  z.ry = z.threads / z.tx;
+  z.slabs = (z.vpr + z.tx - 1) / z.tx;
+  const int64_t sms = sm_count();
+  if (z.brief) {
+    // the backward blocks' sums are written and read once a block
+    const int64_t most = bwd ? sms * (2048 / z.threads) : 0x7fffffff;
+    z.blocks = s < most ? s : most;
+    z.chunks = 0;
+    return z;
+  }
+  // 16 chunks an SM, of at least 4 rows a thread
+  int64_t chunks = 16 * sms / z.slabs;
+  const int64_t rows = 4 * (int64_t)z.ry;
+  if (chunks > (n + rows - 1) / rows) chunks = (n + rows - 1) / rows;
+  if (chunks < 1) chunks = 1;
+  z.rows_per = (n + chunks - 1) / chunks;
+  z.chunks = (n + z.rows_per - 1) / z.rows_per;
+  z.blocks = z.chunks;
+  return z;
+}
+
+int vec_of(int type) { return type == GQ_F32 ? 4 : 8; }
+
+// The workspace does not depend on the matrices' alignment: the larger of both vector widths'.
+size_t workspace(int64_t n, int d, int groups, int type, int64_t s, int64_t max_rows, bool bwd) {
+  size_t most = 0;
+  for (int v : {1, vec_of(type)}) {
+    if (d % v) continue;
+    const Plan z = make_plan(n, d, s, max_rows, type_bytes(type), v, bwd);
+    size_t b = 0;
+    if (z.brief)
+      b = bwd ? (size_t)z.blocks * d * 8 : 0;
+    else
+      b = ((size_t)(z.chunks + s) * d * 8 + 255) / 256 * 256 +
+          (bwd ? ((size_t)s * groups * 8 + 255) / 256 * 256 + (size_t)z.chunks * d * 8 : 0);
+    if (b > most) most = b;
+  }
+  return most;
+}
+
+// A block for each segment and group where that has more than 1,024 values to
+// put together on average, else a warp.
+template <bool BWD>
+int combine(const Args& a, cudaStream_t s) {
+  const int64_t units = a.s * a.groups;
+  if ((a.chunks + a.s) * a.cg > 1024 * a.s) {
+    if (units > 0x7fffffff) return GQ_ERR_UNSUPPORTED;
+    return launch_after(combine_kernel<BWD, true>, dim3((unsigned)units), dim3(kCombine), 0, s, a);
+  }
+  return launch_after(combine_kernel<BWD, false>, dim3((unsigned)((units + kCombine / 32 - 1) / (kCombine / 32))),
+                      dim3(kCombine), 0, s, a);
+}
+
+template <typename T, int V, int ACT>
+int run_fwd(const Args& a, const Plan& z, cudaStream_t s) {
+  const size_t red = (size_t)z.threads * V * 8;
+  if (z.brief) {
+    const size_t sm = red + (size_t)a.d * 8;
+    GQ_TRY_CUDA(cudaFuncSetAttribute(short_fwd_kernel<T, V, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+    return launch_after(short_fwd_kernel<T, V, ACT>, dim3((unsigned)z.blocks), dim3(z.threads), sm, s, a);
+  }
+  const dim3 g((unsigned)z.chunks, z.slabs);
+  GQ_TRY(launch_after(stats_kernel<T, V>, g, dim3(z.threads), red, s, a));
+  GQ_TRY(combine<false>(a, s));
+  return launch_after(apply_kernel<T, V, ACT>, g, dim3(z.threads), 0, s, a);
+}
+
+template <typename T, int V, int ACT>
+int run_bwd(const Args& a, const Plan& z, cudaStream_t s) {
+  const size_t red = (size_t)z.threads * V * 8;
+  if (z.brief) {
+    const size_t sm = red + (size_t)a.d * 16;
+    GQ_TRY_CUDA(cudaFuncSetAttribute(short_bwd_kernel<T, V, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+    GQ_TRY(launch_after(short_bwd_kernel<T, V, ACT>, dim3((unsigned)z.blocks), dim3(z.threads), sm, s, a));
+  } else {
+    const dim3 g((unsigned)z.chunks, z.slabs);
+    GQ_TRY(launch_after(slopes_kernel<T, V, ACT>, g, dim3(z.threads), red, s, a));
+    GQ_TRY(combine<true>(a, s));
+    GQ_TRY(launch_after(apply_bwd_kernel<T, V, ACT>, g, dim3(z.threads), 0, s, a));
+  }
+  if (a.dgamma == nullptr && a.dbeta == nullptr) return GQ_OK;
+  return launch_after(columns_kernel, dim3((a.d + 31) / 32), dim3(1024), 0, s, a);
+}
+
+template <typename T, int V>
+int run_act(bool bwd, int act, const Args& a, const Plan& z, cudaStream_t s) {
+  switch (act) {
+    case GQ_ACT_NONE: return bwd ? run_bwd<T, V, GQ_ACT_NONE>(a, z, s) : run_fwd<T, V, GQ_ACT_NONE>(a, z, s);
+    case GQ_ACT_RELU: return bwd ? run_bwd<T, V, GQ_ACT_RELU>(a, z, s) : run_fwd<T, V, GQ_ACT_RELU>(a, z, s);
+    default: return bwd ? run_bwd<T, V, GQ_ACT_SILU>(a, z, s) : run_fwd<T, V, GQ_ACT_SILU>(a, z, s);
+  }
+}
+
+int run(bool bwd, int type, int act, int v, const Args& a, const Plan& z, cudaStream_t s) {
+  switch (type) {
+    case GQ_F32: return v == 1 ? run_act<float, 1>(bwd, act, a, z, s) : run_act<float, 4>(bwd, act, a, z, s);
+    case GQ_BF16:
+      return v == 1 ? run_act<__nv_bfloat16, 1>(bwd, act, a, z, s) : run_act<__nv_bfloat16, 8>(bwd, act, a, z, s);
+    default: return v == 1 ? run_act<__half, 1>(bwd, act, a, z, s) : run_act<__half, 8>(bwd, act, a, z, s);
+  }
+}
+
+bool rows16(const void* p, int64_t ld, int type) { return aligned(p, 16) && ld * type_bytes(type) % 16 == 0; }
+
+int check(int type, int64_t n, int d, int groups, int64_t s, int64_t max_rows, int act, const int64_t* ptr) {
+  if (!valid_type(type) || n < 0 || d < 1 || groups < 1 || d % groups || s < 0 || max_rows < 0 ||
+      (act != GQ_ACT_NONE && act != GQ_ACT_RELU && act != GQ_ACT_SILU) || !aligned(ptr, 8) || (ptr == nullptr && s != 1))
+    return GQ_ERR_INVALID_ARG;
+  if (d > 16384 || n > (int64_t)1 << 31 || s > (int64_t)1 << 30 || s * groups > 0x7fffffff) return GQ_ERR_UNSUPPORTED;
+  return GQ_OK;
+}
+
+}  // namespace
+}  // namespace gq
+
+extern "C" size_t gq_group_norm_workspace_bytes(int64_t n, int d, int groups, int type, int64_t segments,
+                                                int64_t max_rows, int backward) {
+  using namespace gq;
+  if (!valid_type(type) || n < 1 || d < 1 || d > 16384 || groups < 1 || d % groups || segments < 1 || max_rows < 0) return 0;
+  return workspace(n, d, groups, type, segments, max_rows, backward != 0);
+}
+
+extern "C" int gq_group_norm_fwd(const void* X, int type, int64_t n, int d, int64_t ldx, int groups, const int64_t* ptr,
+                                 int64_t segments, int64_t max_rows, const float* gamma, const float* beta, float eps,
+                                 int act, void* Y, int64_t ldy, float* mean, float* rstd, void* ws, size_t ws_bytes,
+                                 gq_stream stream) {
+  using namespace gq;
+  GQ_TRY(check(type, n, d, groups, segments, max_rows, act, ptr));
+  if (ldx < d || ldy < d || !(eps >= 0.0f) || std::isinf(eps)) return GQ_ERR_INVALID_ARG;
+  if (segments == 0) return GQ_OK;
+  const int e = type_bytes(type);
+  if (mean == nullptr || rstd == nullptr || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(gamma, 4) ||
+      !aligned(beta, 4) || (n > 0 && (X == nullptr || Y == nullptr)) || !aligned(X, e) || !aligned(Y, e))
+    return GQ_ERR_INVALID_ARG;
+  const int64_t rows = n > 0 ? n : 1;  // without rows: the statistics of empty segments
+  const int v = d % vec_of(type) == 0 && rows16(X, ldx, type) && rows16(Y, ldy, type) ? vec_of(type) : 1;
+  const Plan z = make_plan(rows, d, segments, max_rows, e, v, false);
+  const size_t need = workspace(rows, d, groups, type, segments, max_rows, false);
+  if (need > 0 && (ws == nullptr || !aligned(ws, 256) || ws_bytes < need)) return GQ_ERR_WORKSPACE;
+  Args a{};
+  a.X = X;
+  a.Y = Y;
+  a.n = n;
+  a.ldx = ldx;
+  a.ldy = ldy;
+  a.d = d;
+  a.groups = groups;
+  a.cg = d / groups;
+  a.ptr = ptr;
+  a.s = segments;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.eps = eps;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.vpr = z.vpr;
+  a.tx = z.tx;
+  a.ry = z.ry;
+  a.rows_per = z.rows_per;
+  a.chunks = z.chunks;
+  a.part = static_cast<float2*>(ws);
+  return run(false, type, act, v, a, z, (cudaStream_t)stream);
+}
+
+extern "C" int gq_group_norm_bwd(const void* dY, int64_t lddy, const void* X, int64_t ldx, int type, int64_t n, int d,
+                                 int groups, const int64_t* ptr, int64_t segments, int64_t max_rows, const float* mean,
+                                 const float* rstd, const float* gamma, const float* beta, int act, void* dX,
+                                 int64_t lddx, float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
+                                 gq_stream stream) {
+  using namespace gq;
+  GQ_TRY(check(type, n, d, groups, segments, max_rows, act, ptr));
+  if (ldx < d || lddy < d || lddx < d || !aligned(dgamma, 4) || !aligned(dbeta, 4)) return GQ_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (segments == 0 || n == 0) {
+    if (dgamma != nullptr) GQ_TRY_CUDA(cudaMemsetAsync(dgamma, 0, (size_t)d * 4, s));
+    if (dbeta != nullptr) GQ_TRY_CUDA(cudaMemsetAsync(dbeta, 0, (size_t)d * 4, s));
+    return GQ_OK;
+  }
+  const int e = type_bytes(type);
+  if (mean == nullptr || rstd == nullptr || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(gamma, 4) ||
+      !aligned(beta, 4) || X == nullptr || dY == nullptr || dX == nullptr || !aligned(X, e) || !aligned(dY, e) ||
+      !aligned(dX, e))
+    return GQ_ERR_INVALID_ARG;
+  const int v = d % vec_of(type) == 0 && rows16(X, ldx, type) && rows16(dY, lddy, type) && rows16(dX, lddx, type)
+                    ? vec_of(type) : 1;
+  const Plan z = make_plan(n, d, segments, max_rows, e, v, true);
+  const size_t need = workspace(n, d, groups, type, segments, max_rows, true);
+  if (ws == nullptr || !aligned(ws, 256) || ws_bytes < need) return GQ_ERR_WORKSPACE;
+  Args a{};
+  a.X = X;
+  a.dY = dY;
+  a.Y = dX;
+  a.n = n;
+  a.ldx = ldx;
+  a.lddy = lddy;
+  a.ldy = lddx;
+  a.d = d;
+  a.groups = groups;
+  a.cg = d / groups;
+  a.ptr = ptr;
+  a.s = segments;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.vpr = z.vpr;
+  a.tx = z.tx;
+  a.ry = z.ry;
+  a.rows_per = z.rows_per;
+  a.chunks = z.chunks;
+  a.dgamma = dgamma;
+  a.dbeta = dbeta;
+  a.parts = z.blocks;
+  if (z.brief) {
+    a.tot = static_cast<float2*>(ws);
+  } else {
+    char* w = static_cast<char*>(ws);
+    a.part = reinterpret_cast<float2*>(w);
+    w += ((size_t)(z.chunks + segments) * d * 8 + 255) / 256 * 256;
+    a.hsum = reinterpret_cast<float2*>(w);
+    w += ((size_t)segments * groups * 8 + 255) / 256 * 256;
+    a.tot = reinterpret_cast<float2*>(w);
+  }
+  return run(true, type, act, v, a, z, s);
+}

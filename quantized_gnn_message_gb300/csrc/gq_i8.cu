@@ -1,0 +1,1159 @@
+// gq_i8.cu -- products of 8-bit integers with a scale for each row of both
+// operands, and the quantizers that make them.
+//
+//   s[i] = max_k |x[i,k]| / 127,   q[i,k] = round(x[i,k] / s[i])
+//   C[i,j] = act(sa[i] sb[j] sum_k a[i,k] b[j,k] + bias[j])
+//
+// (Tango Sec. 3.2 quantizes both operands of the update's products.)  The sum of
+// products is exact.  This GPU's 8-bit integer tensor rate is about a 25th of
+// its bf16 rate, so the integers are multiplied on the fp16 path: every
+// 8-bit integer is an fp16 number, a product of two needs 15 bits and a sum of
+// 1,024 of them 24, so an fp32 accumulator holds it exactly; accumulators are
+// drained into 32-bit integers every 1,024 products, and partial sums of a split
+// contraction are added as 64-bit integers.
+//
+// Tile product: a pair of CTAs (cta_group::2) takes 256 rows of one operand, S,
+// and up to 256 of the other, F.  Per step of 64 products each CTA
+//   warp 0      copies its 128 rows of S and its half of F's as bytes (TMA, a
+//               ring of kRing8 stages),
+//   warps 4-11  turn bytes into fp16 (below) in the swizzled layout that the
+//               tensor cores read (a ring of kRing16 stages),
+//   warp 1      issues tcgen05.mma (even CTA) or tells the even CTA that its
+//               stage is ready (odd CTA),
+//   warps 12-19 epilogue: TMEM -> registers -> scales, bias, activation ->
+//               shared memory -> rows of C, while the next tile's products run.
+// Four bytes become four fp16 in five instructions: x ^ 0x80 is x + 128; put
+// under the byte 0x64 it is the fp16 number 1024 + 128 + x, and one packed
+// subtraction of 1152 leaves x.
+// Bytes cross DRAM and L2, fp16 only shared memory; its ports are what
+// bounds long contractions: per step of 512 tensor cycles a CTA moves 16 KB in,
+// 16 KB to registers, 32 KB back and 32 KB to the tensor cores at 128 bytes a
+// cycle, 768 cycles.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cudaTypedefs.h>
+
+#include <climits>
+#include <cmath>
+
+#include "gq_common.cuh"
+#include "gq_internal.cuh"
+#include "gq_sm100.cuh"
+#include "gq_train.h"
+
+namespace gq {
+namespace {
+
+// ------------------------------------------------------------- PTX helpers --
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// an accumulator has been read (tcgen05.wait::ld before it): CTA scope will do
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// shared memory of this CTA has been written, for the other CTA's MMA
+__device__ __forceinline__ void arrive_release_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_alloc2(uint32_t* dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void umma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      "  .reg .pred p;\n"
+      "  setp.ne.b32 p, %4, 0;\n"
+      "  tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+      "}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// arrives on `bar` of both CTAs once the MMAs issued so far are done
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n"
+      "  .reg .pred p;\n"
+      "  mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+      "  selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "n"(kSuspendNs)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait on a barrier phase, the thread suspended in hardware meanwhile;
+// CLUSTER: on what the other CTA released.  False after the limit, or once
+// another role of the CTA has given up.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, int where) {
+  const uint32_t b = smem_u32(bar);
+  auto done = [&]() { return CLUSTER ? try_wait_cluster(b, parity) : mbar_try_wait_u32(b, parity); };
+  if (done()) return true;
+  const long long t0 = clock64();
+  while (!done()) {
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *abort = 1;
+      if (err != nullptr) atomicCAS(err, 0, where);
+      return false;
+    }
+  }
+  return true;
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// ------------------------------------------------------------------- types --
+template <typename T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
+
+// Stores one value of the output type chosen at run time.
+__device__ __forceinline__ void store_as(void* base, int64_t i, float x, int type) {
+  if (type == GQ_F32)
+    static_cast<float*>(base)[i] = x;
+  else if (type == GQ_BF16)
+    static_cast<__nv_bfloat16*>(base)[i] = __float2bfloat16_rn(x);
+  else
+    static_cast<__half*>(base)[i] = __float2half_rn(x);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int type) {
+  if (type == GQ_BF16) return pack_bf16x2(lo, hi);
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// ReLU as the other operators have it: 0 for a NaN
+__device__ __forceinline__ float activate(float y, int relu) { return relu ? fmaxf(y, 0.0f) : y; }
+
+// ------------------------------------------------------------- quantization --
+// A row's scale is its largest magnitude / 127; a row that holds a NaN or an
+// infinity has that scale not finite and codes 0, so that its products are NaN
+// as the row's own would be.  Below kTiny a row counts as zero: the
+// quotients' arithmetic needs a normal scale.
+constexpr float kTiny = 7.888609052210118e-31f;  // 2^-100
+
+struct Scale {
+  float s, inv, half;
+};
+__device__ __forceinline__ Scale make_scale(uint32_t bits) {
+  const float top = __uint_as_float(bits);
+  Scale r;
+  if (!(top < INFINITY)) {  // infinite or NaN
+    r.s = __int_as_float(0x7fc00000);
+    r.inv = r.half = 0.0f;
+    return r;
+  }
+  r.s = top < kTiny ? 0.0f : __fdiv_rn(top, 127.0f);
+  r.inv = top < kTiny ? 0.0f : __fdiv_rn(1.0f, r.s);
+  r.half = 0.5f * r.s;
+  return r;
+}
+// round(x / s), ties to even, exactly: q within one of it from the reciprocal,
+// then by the remainder x - q s, which a fused multiply-add gives exactly
+// (it is a multiple of half a step of s and no larger than s).
+__device__ __forceinline__ int quantize(float x, const Scale& c) {
+  const float q = rintf(x * c.inv);
+  const float r = fmaf(-q, c.s, x);
+  int k = (int)q;
+  if (fabsf(r) >= c.half && c.inv > 0.0f) {  // rare
+    if (fabsf(r) > c.half || (k & 1)) k += r > 0.0f ? 1 : -1;
+  }
+  return c.inv > 0.0f ? k : 0;
+}
+__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
+  return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 | (uint32_t)(d & 255) << 24;
+}
+__device__ __forceinline__ uint32_t mag(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// 4 consecutive values of a row
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float4 load4<__half>(const __half* p) {
+  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// Rows: LANES threads a row (a warp up to 4,096 columns, else the block), the
+// row read twice, the second time from L1.
+constexpr int kQThreads = 256;
+template <typename T, bool VEC, int LANES>
+__global__ void __launch_bounds__(kQThreads)
+    quant_rows_kernel(const T* __restrict__ X, int64_t n, int d, int64_t ldx, int8_t* __restrict__ Q, int64_t ldq,
+                      float* __restrict__ S) {
+  __shared__ uint32_t smax[kQThreads / 32];
+  const int lane = threadIdx.x % LANES;
+  const int64_t r = (int64_t)blockIdx.x * (kQThreads / LANES) + threadIdx.x / LANES;
+  const bool live = r < n;
+  const T* x = X + (live ? r : 0) * ldx;
+  uint32_t top = 0;
+  if (live) {
+    if (VEC) {
+      const int d4 = d & ~3;
+      for (int c = lane * 4; c < d4; c += LANES * 4) {
+        const float4 v = load4<T>(x + c);
+        top = max(max(top, mag(v.x)), max(mag(v.y), max(mag(v.z), mag(v.w))));
+      }
+      if (d4 + lane < d) top = max(top, mag((float)x[d4 + lane]));
+    } else {
+      for (int c = lane; c < d; c += LANES) top = max(top, mag((float)x[c]));
+    }
+  }
+  top = __reduce_max_sync(FULL, top);
+  if (LANES > 32) {
+    if ((threadIdx.x & 31) == 0) smax[threadIdx.x >> 5] = top;
+    __syncthreads();
+    top = smax[0];
+    for (int w = 1; w < LANES / 32; ++w) top = max(top, smax[w]);
+  }
+  if (!live) return;
+  const Scale c = make_scale(top);
+  if (lane == 0) S[r] = c.s;
+  int8_t* q = Q + r * ldq;
+  if (VEC) {
+    const int d4 = d & ~3;
+    for (int k = lane * 4; k < d4; k += LANES * 4) {
+      const float4 v = load4<T>(x + k);
+      *reinterpret_cast<uint32_t*>(q + k) = pack4(quantize(v.x, c), quantize(v.y, c), quantize(v.z, c), quantize(v.w, c));
+    }
+    if (d4 + lane < d) q[d4 + lane] = (int8_t)quantize((float)x[d4 + lane], c);
+  } else {
+    for (int k = lane; k < d; k += LANES) q[k] = (int8_t)quantize((float)x[k], c);
+  }
+}
+
+// Columns, first pass: the largest magnitude of each column (the order of
+// integer maxima does not matter) and, where asked for, sums of the block's rows.
+// A block takes kColW columns and rows_per rows, a thread one column of every
+// kColRows-th row.
+constexpr int kColW = 64, kColRows = kQThreads / kColW;
+template <typename T>
+__global__ void __launch_bounds__(kQThreads)
+    col_max_kernel(const T* __restrict__ X, int64_t n, int d, int64_t ldx, int64_t rows_per, uint32_t* __restrict__ top,
+                   float* __restrict__ sums) {
+  __shared__ uint32_t st[kColRows][kColW];
+  __shared__ float ss[kColRows][kColW];
+  const int cx = threadIdx.x % kColW, ry = threadIdx.x / kColW;
+  const int c = blockIdx.x * kColW + cx;
+  const int64_t r0 = (int64_t)blockIdx.y * rows_per, r1 = min(n, r0 + rows_per);
+  uint32_t m = 0;
+  float s = 0.0f;
+  if (c < d) {
+#pragma unroll 8
+    for (int64_t r = r0 + ry; r < r1; r += kColRows) {
+      const float v = (float)X[r * ldx + c];
+      m = max(m, mag(v));
+      s += v;
+    }
+  }
+  st[ry][cx] = m;
+  ss[ry][cx] = s;
+  __syncthreads();
+  if (ry == 0 && c < d) {
+#pragma unroll
+    for (int k = 1; k < kColRows; ++k) {
+      m = max(m, st[k][cx]);
+      s += ss[k][cx];
+    }
+    if (m > 0) atomicMax(top + c, m);
+    if (sums != nullptr) sums[(int64_t)blockIdx.y * d + c] = s;
+  }
+}
+
+__global__ void col_sum_kernel(const float* __restrict__ sums, int parts, int d, float* __restrict__ out) {
+  const int c = blockIdx.x * blockDim.x + threadIdx.x;
+  if (c >= d) return;
+  float s = 0.0f;
+  for (int p = 0; p < parts; ++p) s += sums[(int64_t)p * d + c];
+  out[c] = s;
+}
+
+// Second pass: a block turns 128 rows x 64 columns into 64 rows of 128 bytes.
+constexpr int kTrRows = 128, kTrCols = 64, kTrPitch = kTrRows + 4;
+template <typename T>
+__global__ void __launch_bounds__(kQThreads)
+    quant_cols_kernel(const T* __restrict__ X, int64_t n, int d, int64_t ldx, const uint32_t* __restrict__ top,
+                      int8_t* __restrict__ Q, int64_t ldq, float* __restrict__ S) {
+  __shared__ __align__(16) int8_t tile[kTrCols][kTrPitch];
+  const int c0 = blockIdx.y * kTrCols;
+  const int64_t r0 = (int64_t)blockIdx.x * kTrRows;
+  const int cx = threadIdx.x % kTrCols;
+  const int c = c0 + cx;
+  if (c < d) {
+    const Scale sc = make_scale(top[c]);
+    if (blockIdx.x == 0 && threadIdx.x < kTrCols) S[c] = sc.s;
+    for (int rr = threadIdx.x / kTrCols * 4; rr < kTrRows; rr += kQThreads / kTrCols * 4) {
+      int v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = r0 + rr + j < n ? quantize((float)X[(r0 + rr + j) * ldx + c], sc) : 0;
+      *reinterpret_cast<uint32_t*>(&tile[cx][rr]) = pack4(v[0], v[1], v[2], v[3]);
+    }
+  }
+  __syncthreads();
+  // rows of Q start 16-byte aligned; bytes past n of the last 16 are written as 0
+  for (int i = threadIdx.x; i < kTrCols * (kTrRows / 4); i += kQThreads) {
+    const int row = i / (kTrRows / 4), at = i % (kTrRows / 4) * 4;
+    if (c0 + row < d && r0 + at < n)
+      *reinterpret_cast<uint32_t*>(Q + (int64_t)(c0 + row) * ldq + r0 + at) =
+          *reinterpret_cast<const uint32_t*>(&tile[row][at]);
+  }
+}
+
+// ------------------------------------------------------------- tile product --
+constexpr int kThreads = 640;
+constexpr int kConvWarps = 8, kEpiWarps = 8;
+constexpr int kTile = 256;                 // rows of S a pair, at most as many of F
+constexpr int kStep = 64;                  // products of a step
+constexpr int kDrain = 16;                 // steps after which an accumulator is drained: 1,024 products
+constexpr int kRing8 = 5, kRing16 = 3;
+constexpr int kBytes8 = 2 * 128 * kStep;   // S | F bytes of a stage
+constexpr int kBytes16 = 2 * kBytes8;
+constexpr int kStgPitch = 36;              // floats: 32 columns and a shift of 4 banks a row
+constexpr int kStg = 32 * kStgPitch * 4;
+constexpr int kSmem = 1024 + kRing16 * kBytes16 + kRing8 * kBytes8 + kEpiWarps * kStg + 512;
+constexpr long long kDrainCycles = 4000000;
+constexpr int64_t kMaxSplitSteps = 1024;   // 65,536 products: a 32-bit sum holds twice that
+
+struct TileArgs {
+  int64_t M, N;                            // rows of S and F
+  int steps, NT, half;                     // F rows of a tile; the epilogue's first column half
+  int64_t tm, tn, units;
+  int splits, split_steps;
+  void* C;
+  int64_t ldc;
+  int type, relu, swap, vec;               // swap: C[f][s] instead of C[s][f]
+  const float* sS;
+  const float* sF;
+  const float* bias;                       // of F's rows; with swap of S's
+  int* part;                               // split sums [split][M][ldp]
+  int64_t ldp;
+  int* err;
+};
+
+struct Unit {
+  int64_t mt, nt;
+  int split, s0, s1;
+};
+
+// Groups of 8 tiles of S share F's tiles: their rows stay in L2 while F streams.
+__device__ __forceinline__ Unit get_unit(const TileArgs& p, int64_t u) {
+  Unit r;
+  const int64_t tiles = p.tm * p.tn;
+  r.split = (int)(u / tiles);
+  const int64_t t = u - r.split * tiles;
+  const int64_t g = t / (8 * p.tn), in = t - g * 8 * p.tn;
+  const int64_t gm = min((int64_t)8, p.tm - g * 8);
+  r.nt = in / gm;
+  r.mt = g * 8 + in - r.nt * gm;
+  r.s0 = r.split * p.split_steps;
+  r.s1 = min(p.steps, r.s0 + p.split_steps);
+  return r;
+}
+
+// 16 bytes -> 16 fp16 in two 16-byte pieces
+__device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  w ^= 0x80808080u;
+  const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+  const __half2 k = __half2half2(__ushort_as_half(0x6480));  // 1152
+  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), k);
+  const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), k);
+  lo = *reinterpret_cast<const uint32_t*>(&x);
+  hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+// chunk i of 16 bytes of a [rows][64] byte tile into a [rows][64] fp16 tile, 128-byte swizzle
+__device__ __forceinline__ void widen_chunk(const uint8_t* src, uint8_t* dst, int i) {
+  const uint4 w = *reinterpret_cast<const uint4*>(src + i * 16);
+  uint4 a, b;
+  widen(w.x, a.x, a.y);
+  widen(w.y, a.z, a.w);
+  widen(w.z, b.x, b.y);
+  widen(w.w, b.z, b.w);
+  const int row = i >> 2, piece = (i & 3) * 2, x = row & 7;
+  *reinterpret_cast<uint4*>(dst + row * 128 + ((piece ^ x) << 4)) = a;
+  *reinterpret_cast<uint4*>(dst + row * 128 + (((piece + 1) ^ x) << 4)) = b;
+}
+
+// 32 rows x 32 columns of sums, lane = row, columns c0.. of the tile at (row0, col0)
+__device__ __forceinline__ void put(const TileArgs& p, const Unit& u, int64_t row0, int64_t col0, const int (&v)[32],
+                                    float* stg, int lane) {
+  const int64_t row = row0 + lane;
+  if (p.part != nullptr) {
+    int* s = reinterpret_cast<int*>(stg);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      *reinterpret_cast<int4*>(s + lane * kStgPitch + 4 * j) = make_int4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    __syncwarp();
+    const int64_t col = col0 + (lane & 7) * 4;
+    int* out = p.part + (int64_t)u.split * p.M * p.ldp;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int rr = 4 * k + (lane >> 3);
+      if (row0 + rr < p.M && col < p.ldp)
+        *reinterpret_cast<int4*>(out + (row0 + rr) * p.ldp + col) =
+            *reinterpret_cast<const int4*>(s + rr * kStgPitch + (lane & 7) * 4);
+    }
+    __syncwarp();
+    return;
+  }
+  if (p.swap) {  // a lane's row is a column of C: lanes write side by side
+    if (row >= p.M) return;
+    const float sr = p.sS[row], b = p.bias != nullptr ? p.bias[row] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (col0 + j < p.N) {
+        const float y = fmaf(__fmul_rn((float)v[j], p.sF[col0 + j]), sr, b);
+        store_as(p.C, (col0 + j) * p.ldc + row, activate(y, p.relu), p.type);
+      }
+    return;
+  }
+  const float sr = row < p.M ? p.sS[row] : 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<float4*>(stg + lane * kStgPitch + 4 * j) =
+        make_float4((float)v[4 * j] * sr, (float)v[4 * j + 1] * sr, (float)v[4 * j + 2] * sr, (float)v[4 * j + 3] * sr);
+  __syncwarp();
+  if (p.vec && col0 + 32 <= p.N) {
+    if (p.type == GQ_F32) {
+      const int c = (lane & 7) * 4;
+      float sf[4], b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sf[j] = p.sF[col0 + c + j];
+        b[j] = p.bias != nullptr ? p.bias[col0 + c + j] : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int rr = 4 * k + (lane >> 3);
+        const float4 x = *reinterpret_cast<const float4*>(stg + rr * kStgPitch + c);
+        if (row0 + rr < p.M)
+          st_f4(static_cast<float*>(p.C) + (row0 + rr) * p.ldc + col0 + c, activate(fmaf(x.x, sf[0], b[0]), p.relu),
+                activate(fmaf(x.y, sf[1], b[1]), p.relu), activate(fmaf(x.z, sf[2], b[2]), p.relu),
+                activate(fmaf(x.w, sf[3], b[3]), p.relu));
+      }
+    } else {
+      const int c = (lane & 3) * 8;
+      float sf[8], b[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        sf[j] = p.sF[col0 + c + j];
+        b[j] = p.bias != nullptr ? p.bias[col0 + c + j] : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int rr = 8 * k + (lane >> 2);
+        const float4 x = *reinterpret_cast<const float4*>(stg + rr * kStgPitch + c);
+        const float4 z = *reinterpret_cast<const float4*>(stg + rr * kStgPitch + c + 4);
+        float y[8] = {x.x, x.y, x.z, x.w, z.x, z.y, z.z, z.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = activate(fmaf(y[j], sf[j], b[j]), p.relu);
+        if (row0 + rr < p.M)
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.C) + (row0 + rr) * p.ldc + col0 + c) =
+              make_uint4(pack2(y[0], y[1], p.type), pack2(y[2], y[3], p.type), pack2(y[4], y[5], p.type),
+                         pack2(y[6], y[7], p.type));
+      }
+    }
+  } else if (col0 + lane < p.N) {
+    const float sf = p.sF[col0 + lane], b = p.bias != nullptr ? p.bias[col0 + lane] : 0.0f;
+    for (int rr = 0; rr < 32 && row0 + rr < p.M; ++rr)
+      store_as(p.C, (row0 + rr) * p.ldc + col0 + lane, activate(fmaf(stg[rr * kStgPitch + lane], sf, b), p.relu), p.type);
+  }
+  __syncwarp();
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    i8_tiles_kernel(const __grid_constant__ CUtensorMap mS, const __grid_constant__ CUtensorMap mF, const TileArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* s16 = smem;
+  uint8_t* s8 = s16 + kRing16 * kBytes16;
+  float* stg_all = reinterpret_cast<float*>(s8 + kRing8 * kBytes8);
+  uint64_t* full8 = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(stg_all) + kEpiWarps * kStg);
+  uint64_t* empty8 = full8 + kRing8;
+  uint64_t* conv = empty8 + kRing8;      // this CTA's fp16 stage is made
+  uint64_t* peer = conv + kRing16;       // the odd CTA's is (in the even CTA)
+  uint64_t* empty16 = peer + kRing16;
+  uint64_t* tfull = empty16 + kRing16;
+  uint64_t* tempty = tfull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t cr = cluster_rank();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kRing8; ++s) {
+      mbar_init(&full8[s], 1);
+      mbar_init(&empty8[s], kConvWarps);
+    }
+    for (int s = 0; s < kRing16; ++s) {
+      mbar_init(&conv[s], kConvWarps);
+      mbar_init(&peer[s], 1);
+      mbar_init(&empty16[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 2 * kEpiWarps);
+    }
+    *abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc2(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_wait();
+  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int hn = p.NT / 2;
+
+  // 3 warpgroups at 40 registers and 2 at 176: 60,416 in all, of the
+  // 61,440 (96 a thread) that the block is launched with
+  if (warp < 4) {
+    regs_down<40>();
+    if (warp == 0 && lane == 0) {
+      prefetch_tmap(&mS);
+      prefetch_tmap(&mF);
+      int st = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int64_t i = pair; ok && i < p.units; i += pairs) {
+        const Unit u = get_unit(p, i);
+        const int ys = (int)(u.mt * kTile + cr * 128), yf = (int)(u.nt * p.NT + cr * hn);
+        for (int s = u.s0; s < u.s1; ++s) {
+          if (!(ok = wait(&empty8[st], ph ^ 1, abort, p.err, 31))) break;
+          mbar_expect_tx(&full8[st], (uint32_t)((128 + hn) * kStep));
+          uint8_t* dst = s8 + st * kBytes8;
+          tma_load_2d(dst, &mS, s * kStep, ys, &full8[st]);
+          tma_load_2d(dst + 128 * kStep, &mF, s * kStep, yf, &full8[st]);
+          if (++st == kRing8) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+    } else if (warp == 1 && lane == 0 && cr == 0) {
+      // fp16 operands, fp32 sums: the formats are 0
+      const uint32_t idesc = (1u << 4) | ((uint32_t)(p.NT >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+      int st = 0, gen = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int64_t i = pair; ok && i < p.units; i += pairs) {
+        const Unit u = get_unit(p, i);
+        for (int g = u.s0; ok && g < u.s1; g += kDrain, ++gen) {
+          const int a = gen & 1;
+          if (!(ok = wait(&tempty[a], ((gen >> 1) & 1) ^ 1, abort, p.err, 32))) break;
+          tc_fence_after();
+          const uint32_t d = tmem + a * 256;
+          const int e = min(u.s1, g + kDrain);
+          for (int s = g; s < e; ++s) {
+            if (!(ok = wait(&conv[st], ph, abort, p.err, 33))) break;
+            if (!(ok = wait<true>(&peer[st], ph, abort, p.err, 34))) break;
+            tc_fence_after();
+            const uint32_t ab = smem_u32(s16 + st * kBytes16), bb = ab + 128 * 128;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_pair(d, smem_desc_sw128(ab + 32 * kk, 16, 1024), smem_desc_sw128(bb + 32 * kk, 16, 1024), idesc,
+                        s > g || kk > 0);
+            commit_pair(&empty16[st]);
+            if (++st == kRing16) {
+              st = 0;
+              ph ^= 1;
+            }
+          }
+          if (ok) commit_pair(&tfull[a]);
+        }
+      }
+    } else if (warp == 1 && lane == 0) {
+      int st = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int64_t i = pair; ok && i < p.units; i += pairs) {
+        const Unit u = get_unit(p, i);
+        for (int s = u.s0; s < u.s1; ++s) {
+          if (!(ok = wait(&conv[st], ph, abort, p.err, 35))) break;
+          arrive_release_cluster(mapa(smem_u32(&peer[st]), 0));
+          if (++st == kRing16) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+    }
+  } else if (warp < 4 + kConvWarps) {
+    regs_down<40>();
+    const int t = threadIdx.x - 128;
+    int st8 = 0, st = 0;
+    uint32_t ph8 = 0, ph = 0;
+    bool ok = true;
+    for (int64_t i = pair; ok && i < p.units; i += pairs) {
+      const Unit u = get_unit(p, i);
+      for (int s = u.s0; s < u.s1; ++s) {
+        ok = wait(&full8[st8], ph8, abort, p.err, 36) && wait(&empty16[st], ph ^ 1, abort, p.err, 37);
+        if (!(ok = __all_sync(FULL, ok))) break;
+        const uint8_t* src = s8 + st8 * kBytes8;
+        uint8_t* dst = s16 + st * kBytes16;
+        widen_chunk(src, dst, t);
+        widen_chunk(src, dst, t + 256);
+        for (int k = t; k < hn * 4; k += 256) widen_chunk(src + 128 * kStep, dst + 128 * 128, k);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&empty8[st8]);
+          mbar_arrive(&conv[st]);
+        }
+        if (++st8 == kRing8) {
+          st8 = 0;
+          ph8 ^= 1;
+        }
+        if (++st == kRing16) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    }
+  } else {
+    regs_up<176>();
+    const int quarter = warp & 3, part = (warp - 12) >> 2;
+    float* stg = stg_all + (warp - 12) * (kStg / 4);
+    const uint32_t tempty0 = mapa(smem_u32(tempty), 0);
+    const int cb = part ? p.half : 0, ce = part ? p.NT : p.half;
+    int gen = 0;
+    bool ok = true;
+    for (int64_t i = pair; ok && i < p.units; i += pairs) {
+      const Unit u = get_unit(p, i);
+      const int64_t row0 = u.mt * kTile + cr * 128 + quarter * 32, col0 = u.nt * p.NT;
+      const int gens = (u.s1 - u.s0 + kDrain - 1) / kDrain;
+      int acc[4][32];
+      for (int g = 0; g < gens; ++g, ++gen) {
+        const int a = gen & 1;
+        ok = wait(&tfull[a], (gen >> 1) & 1, abort, p.err, 38);
+        ok = __all_sync(FULL, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + a * 256 + cb;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (cb + 32 * c < ce) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t r[16];
+              tmem_ld16(taddr + 32 * c + 16 * h, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const int x = __float2int_rn(__uint_as_float(r[j]));
+                acc[c][16 * h + j] = g == 0 ? x : acc[c][16 * h + j] + x;
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(tempty0 + a * 8);
+      }
+      if (!ok) break;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (cb + 32 * c < ce) put(p, u, row0, col0 + cb + 32 * c, acc[c], stg, lane);
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  // after a wait that gave up: copies and products under way (they take
+  // microseconds) land before the pair's shared and tensor memory is given up
+  if (*abort) {
+    const long long t0 = clock64();
+    while (clock64() - t0 < kDrainCycles) {
+    }
+  }
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc2(tmem, 512);
+  }
+  cluster_sync();
+}
+
+// C from the splits' sums, added as 64-bit integers.
+__global__ void __launch_bounds__(256) join_kernel(const TileArgs p) {
+  grid_wait();
+  const int64_t total = p.M * p.ldp;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / p.ldp, c = i - r * p.ldp;
+    if (c >= p.N) continue;
+    int64_t s = 0;
+    for (int k = 0; k < p.splits; ++k) s += p.part[k * total + i];
+    const float v = (float)s;
+    if (p.swap)
+      store_as(p.C, c * p.ldc + r,
+               activate(fmaf(__fmul_rn(v, p.sF[c]), p.sS[r], p.bias != nullptr ? p.bias[r] : 0.0f), p.relu), p.type);
+    else
+      store_as(p.C, r * p.ldc + c,
+               activate(fmaf(__fmul_rn(v, p.sS[r]), p.sF[c], p.bias != nullptr ? p.bias[c] : 0.0f), p.relu), p.type);
+  }
+}
+
+// ---------------------------------------------------------------- few rows --
+// Up to kFew rows of A: a warp takes rows of B, its lanes 16 bytes each of a
+// row, products by dp4a; A's rows are read through L1 again and again.  Bound
+// by reading B.
+constexpr int kFew = 8;
+template <int M, int ROWS>
+__global__ void __launch_bounds__(256)
+    few_rows_kernel(const int8_t* A, int64_t lda, const float* sA, const int8_t* B, int64_t N, int64_t ldb,
+                    const float* sB, int K, const float* bias, void* C, int64_t ldc, int type, int relu) {
+  grid_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t j0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * ROWS;
+  if (j0 >= N) return;
+  int acc[M][ROWS];
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) acc[m][r] = 0;
+  for (int k = lane * 16; k < K; k += 512) {
+    uint4 b[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+      b[r] = *reinterpret_cast<const uint4*>(B + (j0 + r < N ? j0 + r : N - 1) * ldb + k);
+    const int left = K - k;  // bytes past K may hold anything: A's are taken as 0 there
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      uint4 a = *reinterpret_cast<const uint4*>(A + m * lda + k);
+      if (left < 16) {
+        uint32_t* w = &a.x;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[q] = left >= 4 * q + 4 ? w[q] : left <= 4 * q ? 0u : w[q] & ((1u << 8 * (left - 4 * q)) - 1);
+      }
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        acc[m][r] = __dp4a((int)a.x, (int)b[r].x, acc[m][r]);
+        acc[m][r] = __dp4a((int)a.y, (int)b[r].y, acc[m][r]);
+        acc[m][r] = __dp4a((int)a.z, (int)b[r].z, acc[m][r]);
+        acc[m][r] = __dp4a((int)a.w, (int)b[r].w, acc[m][r]);
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const int s = __reduce_add_sync(FULL, acc[m][r]);
+      const int64_t j = j0 + r;
+      if (lane == (m * ROWS + r) % 32 && j < N)
+        store_as(C, m * ldc + j,
+                 activate(fmaf(__fmul_rn((float)s, sA[m]), sB[j], bias != nullptr ? bias[j] : 0.0f), relu), type);
+    }
+}
+
+// -------------------------------------------------------------------- host --
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// bytes [rows][cols] with row pitch ld; boxes of 64 columns, zeros outside
+int make_tmap8(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return GQ_ERR_CUDA;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld};
+  const cuuint32_t box[2] = {kStep, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? GQ_OK : GQ_ERR_INVALID_ARG;
+}
+
+bool valid_type(int type) { return type == GQ_F32 || type == GQ_BF16 || type == GQ_F16; }
+int type_bytes(int type) { return type == GQ_F32 ? 4 : 2; }
+constexpr int64_t kMaxRows = (int64_t)1 << 30;  // tensor maps and coordinates
+
+struct Plan {
+  int swap, NT, steps, splits, split_steps;
+  int64_t M, N, tm, tn, ldp;
+  size_t ws;
+};
+
+// The operand with more rows is S.  F's tiles are as equal as multiples of 32
+// allow.  The contraction is split where the tiles alone leave more than half
+// of the pairs without work (each split at least one drained accumulator's 1,024
+// products, 256 where that still leaves pairs idle), and beyond 65,536 products.
+Plan make_plan(int64_t m, int64_t n, int64_t k) {
+  Plan z{};
+  z.swap = n > m;
+  z.M = z.swap ? n : m;
+  z.N = z.swap ? m : n;
+  z.tm = (z.M + kTile - 1) / kTile;
+  z.tn = (z.N + kTile - 1) / kTile;
+  const int64_t per = (z.N + z.tn - 1) / z.tn;
+  z.NT = (int)((per + 31) / 32 * 32);
+  z.tn = (z.N + z.NT - 1) / z.NT;
+  z.steps = (int)((k + kStep - 1) / kStep);
+  const int64_t pairs = sm_count() / 2 > 0 ? sm_count() / 2 : 1;
+  int64_t want = pairs / (z.tm * z.tn);
+  if (want < 1) want = 1;
+  int64_t most = (z.steps + 3) / 4;
+  if (want > most) want = most;
+  const int64_t least = (z.steps + kMaxSplitSteps - 1) / kMaxSplitSteps;
+  if (want < least) want = least;
+  int64_t per_split = (z.steps + want - 1) / want;
+  if (per_split > kDrain) per_split = (per_split + kDrain - 1) / kDrain * kDrain;
+  z.split_steps = (int)per_split;
+  z.splits = (int)((z.steps + per_split - 1) / per_split);
+  z.ldp = (z.N + 3) / 4 * 4;
+  z.ws = z.splits > 1 ? (size_t)z.splits * z.M * z.ldp * 4 : 0;
+  return z;
+}
+
+bool valid_shape(int64_t m, int64_t n, int64_t k) {
+  return m >= 0 && n >= 1 && k >= 1 && m <= kMaxRows && n <= kMaxRows && k <= kMaxRows;
+}
+
+bool few(int64_t m, int64_t k) { return m <= kFew && k <= 65536; }  // a 32-bit sum holds twice that
+
+size_t gemm_ws(int64_t m, int64_t n, int64_t k) {
+  if (few(m, k)) return 0;
+  return make_plan(m, n, k).ws;
+}
+
+template <int M>
+int few_rows(const int8_t* A, int64_t lda, const float* sA, const int8_t* B, int64_t N, int64_t ldb, const float* sB,
+             int K, const float* bias, void* C, int64_t ldc, int type, int relu, cudaStream_t s) {
+  constexpr int ROWS = M <= 2 ? 4 : 2;
+  const int64_t blocks = (N + 8 * ROWS - 1) / (8 * ROWS);
+  return launch_after(few_rows_kernel<M, ROWS>, dim3((unsigned)blocks), dim3(256), 0, s, A, lda, sA, B, N, ldb, sB, K,
+                      bias, C, ldc, type, relu);
+}
+
+int gemm(const int8_t* A, int64_t m, int64_t lda, const float* sA, const int8_t* B, int64_t n, int64_t ldb,
+         const float* sB, int64_t k, const float* bias, int relu, void* C, int type, int64_t ldc, void* ws,
+         size_t ws_bytes, int* err, cudaStream_t s) {
+  if (few(m, k)) {
+#define GQ_FEW(I) \
+  case I: return few_rows<I>(A, lda, sA, B, n, ldb, sB, (int)k, bias, C, ldc, type, relu, s);
+    switch (m) {
+      GQ_FEW(1) GQ_FEW(2) GQ_FEW(3) GQ_FEW(4) GQ_FEW(5) GQ_FEW(6) GQ_FEW(7) GQ_FEW(8)
+    }
+#undef GQ_FEW
+  }
+  const Plan z = make_plan(m, n, k);
+  if (z.ws > 0 && (ws == nullptr || ws_bytes < z.ws || !aligned(ws, 16))) return GQ_ERR_WORKSPACE;
+  TileArgs a{};
+  a.M = z.M;
+  a.N = z.N;
+  a.steps = z.steps;
+  a.NT = z.NT;
+  a.half = (z.NT / 2 + 31) / 32 * 32;
+  a.tm = z.tm;
+  a.tn = z.tn;
+  a.splits = z.splits;
+  a.split_steps = z.split_steps;
+  a.units = z.tm * z.tn * z.splits;
+  a.C = C;
+  a.ldc = ldc;
+  a.type = type;
+  a.relu = relu;
+  a.swap = z.swap;
+  a.vec = aligned(C, 16) && ldc * type_bytes(type) % 16 == 0;
+  a.sS = z.swap ? sB : sA;
+  a.sF = z.swap ? sA : sB;
+  a.bias = bias;
+  a.part = z.splits > 1 ? static_cast<int*>(ws) : nullptr;
+  a.ldp = z.ldp;
+  a.err = err;
+  CUtensorMap mS, mF;
+  GQ_TRY(make_tmap8(&mS, z.swap ? B : A, k, z.M, z.swap ? ldb : lda, 128));
+  GQ_TRY(make_tmap8(&mF, z.swap ? A : B, k, z.N, z.swap ? lda : ldb, z.NT / 2));
+  GQ_TRY_CUDA(cudaFuncSetAttribute(i8_tiles_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+  const int64_t pairs = sm_count() / 2 > 0 ? sm_count() / 2 : 1;
+  const int64_t use = a.units < pairs ? a.units : pairs;
+  GQ_TRY(launch_after(i8_tiles_kernel, dim3((unsigned)(2 * use)), dim3(kThreads), kSmem, s, mS, mF, a));
+  if (a.part == nullptr) return GQ_OK;
+  int64_t blocks = (z.M * z.ldp + 255) / 256;
+  if (blocks > 65536) blocks = 65536;
+  return launch_after(join_kernel, dim3((unsigned)blocks), dim3(256), 0, s, a);
+}
+
+template <typename T>
+int quant_rows(const T* X, int64_t n, int d, int64_t ldx, int8_t* Q, int64_t ldq, float* S, cudaStream_t s) {
+  const bool vec = aligned(X, 4 * sizeof(T)) && ldx % 4 == 0;
+  const int per = d <= 4096 ? kQThreads / 32 : 1;
+  const int64_t blocks = (n + per - 1) / per;
+  if (blocks > 0x7fffffff) return GQ_ERR_UNSUPPORTED;
+  const dim3 g((unsigned)blocks);
+  if (d <= 4096) {
+    if (vec)
+      quant_rows_kernel<T, true, 32><<<g, kQThreads, 0, s>>>(X, n, d, ldx, Q, ldq, S);
+    else
+      quant_rows_kernel<T, false, 32><<<g, kQThreads, 0, s>>>(X, n, d, ldx, Q, ldq, S);
+  } else {
+    if (vec)
+      quant_rows_kernel<T, true, kQThreads><<<g, kQThreads, 0, s>>>(X, n, d, ldx, Q, ldq, S);
+    else
+      quant_rows_kernel<T, false, kQThreads><<<g, kQThreads, 0, s>>>(X, n, d, ldx, Q, ldq, S);
+  }
+  return launch_status();
+}
+
+// Row pieces of the columns' first pass: four blocks an SM, at least 64 rows each.
+int64_t col_parts(int64_t n, int d) {
+  const int64_t gx = (d + kColW - 1) / kColW;
+  int64_t parts = (4 * (int64_t)sm_count() + gx - 1) / gx;
+  const int64_t most = (n + 63) / 64;
+  if (parts > most) parts = most;
+  if (parts > 65535) parts = 65535;
+  return parts < 1 ? 1 : parts;
+}
+size_t cols_ws(int64_t n, int d, int sums) {
+  return ((size_t)d * 4 + 255) / 256 * 256 + (sums ? (size_t)col_parts(n, d) * d * 4 : 0);
+}
+
+template <typename T>
+int quant_cols(const T* X, int64_t n, int d, int64_t ldx, int8_t* Q, int64_t ldq, float* S, float* colsum, void* ws,
+               cudaStream_t s) {
+  uint32_t* top = static_cast<uint32_t*>(ws);
+  float* sums = colsum != nullptr ? reinterpret_cast<float*>(static_cast<char*>(ws) + ((size_t)d * 4 + 255) / 256 * 256)
+                                  : nullptr;
+  const int64_t parts = col_parts(n, d), rows_per = (n + parts - 1) / parts;
+  GQ_TRY_CUDA(cudaMemsetAsync(top, 0, (size_t)d * 4, s));
+  col_max_kernel<T><<<dim3((d + kColW - 1) / kColW, (unsigned)parts), kQThreads, 0, s>>>(X, n, d, ldx, rows_per, top, sums);
+  GQ_TRY(launch_status());
+  if (sums != nullptr) {
+    col_sum_kernel<<<(d + 255) / 256, 256, 0, s>>>(sums, (int)parts, d, colsum);
+    GQ_TRY(launch_status());
+  }
+  quant_cols_kernel<T><<<dim3((unsigned)((n + kTrRows - 1) / kTrRows), (d + kTrCols - 1) / kTrCols), kQThreads, 0, s>>>(
+      X, n, d, ldx, top, Q, ldq, S);
+  return launch_status();
+}
+
+int quant(const void* X, int type, int64_t n, int d, int64_t ldx, int transpose, int8_t* Q, int64_t ldq, float* S,
+          float* colsum, void* ws, cudaStream_t s) {
+  switch (type) {
+    case GQ_F32:
+      return transpose ? quant_cols(static_cast<const float*>(X), n, d, ldx, Q, ldq, S, colsum, ws, s)
+                       : quant_rows(static_cast<const float*>(X), n, d, ldx, Q, ldq, S, s);
+    case GQ_BF16:
+      return transpose ? quant_cols(static_cast<const __nv_bfloat16*>(X), n, d, ldx, Q, ldq, S, colsum, ws, s)
+                       : quant_rows(static_cast<const __nv_bfloat16*>(X), n, d, ldx, Q, ldq, S, s);
+    default:
+      return transpose ? quant_cols(static_cast<const __half*>(X), n, d, ldx, Q, ldq, S, colsum, ws, s)
+                       : quant_rows(static_cast<const __half*>(X), n, d, ldx, Q, ldq, S, s);
+  }
+}
+
+constexpr int kMaxCols = 65535 * kTrCols / 2;  // quantizer's grid in y
+int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+}  // namespace gq
+
+extern "C" size_t gq_quantize_i8_workspace_bytes(int64_t n, int d, int transpose) {
+  if (n < 0 || d < 1 || d > gq::kMaxCols || !transpose) return 0;
+  return gq::cols_ws(n, d, 0);
+}
+
+extern "C" int gq_quantize_i8(const void* X, int type, int64_t n, int d, int64_t ldx, int transpose, int8_t* Q,
+                              int64_t ldq, float* scale, void* ws, size_t ws_bytes, gq_stream stream) {
+  using namespace gq;
+  if (!valid_type(type) || n < 0 || d < 1 || ldx < d || ldq < (transpose ? n : d) || ldq % 16) return GQ_ERR_INVALID_ARG;
+  if (n > kMaxRows || d > kMaxCols) return GQ_ERR_UNSUPPORTED;
+  if (n == 0) return GQ_OK;
+  if (X == nullptr || Q == nullptr || scale == nullptr || !aligned(X, type_bytes(type)) || !aligned(Q, 16) ||
+      !aligned(scale, 4))
+    return GQ_ERR_INVALID_ARG;
+  if (transpose && (ws == nullptr || !aligned(ws, 16) || ws_bytes < cols_ws(n, d, 0))) return GQ_ERR_WORKSPACE;
+  return quant(X, type, n, d, ldx, transpose, Q, ldq, scale, nullptr, ws, (cudaStream_t)stream);
+}
+
+extern "C" size_t gq_gemm_i8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  if (!gq::valid_shape(m, n, k) || m == 0) return 0;
+  return gq::gemm_ws(m, n, k);
+}
+
+extern "C" int gq_gemm_i8(const int8_t* A, int64_t m, int64_t lda, const float* scale_a, const int8_t* B, int64_t n,
+                          int64_t ldb, const float* scale_b, int64_t k, const float* bias, int act, void* C, int type,
+                          int64_t ldc, void* ws, size_t ws_bytes, int* dev_err, gq_stream stream) {
+  using namespace gq;
+  if (m < 0 || n < 1 || k < 1 || !valid_type(type) || (act != GQ_ACT_NONE && act != GQ_ACT_RELU) || lda < k ||
+      ldb < k || lda % 16 || ldb % 16 || ldc < n)
+    return GQ_ERR_INVALID_ARG;
+  if (!valid_shape(m, n, k)) return GQ_ERR_UNSUPPORTED;
+  if (m == 0) return GQ_OK;
+  if (A == nullptr || B == nullptr || C == nullptr || scale_a == nullptr || scale_b == nullptr || !aligned(A, 16) ||
+      !aligned(B, 16) || !aligned(C, type_bytes(type)) || !aligned(scale_a, 4) || !aligned(scale_b, 4) ||
+      !aligned(bias, 4) || !aligned(dev_err, 4))
+    return GQ_ERR_INVALID_ARG;
+  return gemm(A, m, lda, scale_a, B, n, ldb, scale_b, k, bias, act == GQ_ACT_RELU, C, type, ldc, ws, ws_bytes, dev_err,
+              (cudaStream_t)stream);
+}
+
+extern "C" size_t gq_linear_i8_workspace_bytes(int64_t n, int k, int out) {
+  using namespace gq;
+  if (!valid_shape(n, out, k) || n == 0) return 0;
+  return round256((size_t)n * round16(k)) + round256((size_t)n * 4) + gemm_ws(n, out, k);
+}
+
+extern "C" int gq_linear_i8(const void* X, int type, int64_t n, int k, int64_t ldx, const int8_t* W, int out,
+                            int64_t ldw, const float* scale_w, const float* bias, int act, void* Y, int y_type,
+                            int64_t ldy, void* ws, size_t ws_bytes, int* dev_err, gq_stream stream) {
+  using namespace gq;
+  if (!valid_type(type) || !valid_type(y_type) || n < 0 || k < 1 || out < 1 || ldx < k || ldw < k || ldw % 16 ||
+      ldy < out || (act != GQ_ACT_NONE && act != GQ_ACT_RELU))
+    return GQ_ERR_INVALID_ARG;
+  if (!valid_shape(n, out, k) || k > kMaxCols) return GQ_ERR_UNSUPPORTED;
+  if (n == 0) return GQ_OK;
+  if (X == nullptr || W == nullptr || Y == nullptr || scale_w == nullptr || !aligned(X, type_bytes(type)) ||
+      !aligned(W, 16) || !aligned(Y, type_bytes(y_type)) || !aligned(scale_w, 4) || !aligned(bias, 4) ||
+      !aligned(dev_err, 4))
+    return GQ_ERR_INVALID_ARG;
+  if (ws == nullptr || !aligned(ws, 256) || ws_bytes < gq_linear_i8_workspace_bytes(n, k, out)) return GQ_ERR_WORKSPACE;
+  Carve w(ws, ws_bytes);
+  const int64_t ldq = round16(k);
+  int8_t* q = static_cast<int8_t*>(w.take((size_t)n * ldq));
+  float* sc = static_cast<float*>(w.take((size_t)n * 4));
+  const size_t gw = gemm_ws(n, out, k);
+  void* g = gw > 0 ? w.take(gw) : nullptr;
+  cudaStream_t s = (cudaStream_t)stream;
+  GQ_TRY(quant(X, type, n, k, ldx, 0, q, ldq, sc, nullptr, nullptr, s));
+  return gemm(q, n, ldq, sc, W, out, ldw, scale_w, k, bias, act == GQ_ACT_RELU, Y, y_type, ldy, g, gw, dev_err, s);
+}
+
+namespace gq {
+namespace {
+size_t bwd_ws(int64_t n, int k, int out, bool need_dx, bool need_dw) {
+  size_t dx = 0, dw = 0;
+  if (need_dx) {  // codes of dY's rows and W's columns
+    dx = round256((size_t)n * round16(out)) + round256((size_t)n * 4) + round256((size_t)k * round16(out)) +
+         round256((size_t)k * 4) + round256(cols_ws(out, k, 0)) + round256(gemm_ws(n, k, out));
+  }
+  if (need_dw) {  // codes of dY's and X's columns
+    dw = round256((size_t)out * round16(n)) + round256((size_t)out * 4) + round256((size_t)k * round16(n)) +
+         round256((size_t)k * 4) + round256(cols_ws(n, out, 1)) + round256(cols_ws(n, k, 0)) +
+         round256(gemm_ws(out, k, n));
+  }
+  return dx > dw ? dx : dw;
+}
+}  // namespace
+}  // namespace gq
+
+extern "C" size_t gq_linear_i8_bwd_workspace_bytes(int64_t n, int k, int out, int need_dx, int need_dw) {
+  using namespace gq;
+  if (!valid_shape(n, out, k) || n == 0 || k > kMaxCols || out > kMaxCols) return 0;
+  return bwd_ws(n, k, out, need_dx != 0, need_dw != 0);
+}
+
+extern "C" int gq_linear_i8_bwd(const void* dY, int64_t lddy, const void* X, int64_t ldx, int type, int64_t n, int k,
+                                int out, const void* W, int w_type, int64_t ldw, void* dX, int dx_type, int64_t lddx,
+                                void* dW, int dw_type, int64_t lddw, float* dbias, void* ws, size_t ws_bytes,
+                                int* dev_err, gq_stream stream) {
+  using namespace gq;
+  if (!valid_type(type) || n < 0 || k < 1 || out < 1 || lddy < out) return GQ_ERR_INVALID_ARG;
+  if (dbias != nullptr && dW == nullptr) return GQ_ERR_INVALID_ARG;
+  if (dX != nullptr && (W == nullptr || !valid_type(w_type) || !valid_type(dx_type) || ldw < k || lddx < k ||
+                        !aligned(W, type_bytes(w_type)) || !aligned(dX, type_bytes(dx_type))))
+    return GQ_ERR_INVALID_ARG;
+  if (dW != nullptr && (!valid_type(dw_type) || ldx < k || lddw < k || !aligned(dW, type_bytes(dw_type))))
+    return GQ_ERR_INVALID_ARG;
+  if (!aligned(dbias, 4) || !aligned(dev_err, 4)) return GQ_ERR_INVALID_ARG;
+  if (!valid_shape(n, out, k) || k > kMaxCols || out > kMaxCols) return GQ_ERR_UNSUPPORTED;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (n == 0) {
+    if (dW != nullptr)
+      GQ_TRY_CUDA(cudaMemset2DAsync(dW, (size_t)lddw * type_bytes(dw_type), 0, (size_t)k * type_bytes(dw_type),
+                                    (size_t)out, s));
+    if (dbias != nullptr) GQ_TRY_CUDA(cudaMemsetAsync(dbias, 0, (size_t)out * 4, s));
+    return GQ_OK;
+  }
+  if (dY == nullptr || !aligned(dY, type_bytes(type)) ||
+      (dW != nullptr && (X == nullptr || !aligned(X, type_bytes(type)))))
+    return GQ_ERR_INVALID_ARG;
+  if (dX == nullptr && dW == nullptr) return GQ_OK;
+  if (ws == nullptr || !aligned(ws, 256) || ws_bytes < bwd_ws(n, k, out, dX != nullptr, dW != nullptr))
+    return GQ_ERR_WORKSPACE;
+  if (dX != nullptr) {
+    Carve w(ws, ws_bytes);
+    const int64_t ld = round16(out);
+    int8_t* qy = static_cast<int8_t*>(w.take((size_t)n * ld));
+    float* sy = static_cast<float*>(w.take((size_t)n * 4));
+    int8_t* qw = static_cast<int8_t*>(w.take((size_t)k * ld));
+    float* sw = static_cast<float*>(w.take((size_t)k * 4));
+    void* cw = w.take(cols_ws(out, k, 0));
+    const size_t gw = gemm_ws(n, k, out);
+    void* g = gw > 0 ? w.take(gw) : nullptr;
+    GQ_TRY(quant(dY, type, n, out, lddy, 0, qy, ld, sy, nullptr, nullptr, s));
+    GQ_TRY(quant(W, w_type, out, k, ldw, 1, qw, ld, sw, nullptr, cw, s));
+    GQ_TRY(gemm(qy, n, ld, sy, qw, k, ld, sw, out, nullptr, 0, dX, dx_type, lddx, g, gw, dev_err, s));
+  }
+  if (dW != nullptr) {
+    Carve w(ws, ws_bytes);
+    const int64_t ld = round16(n);
+    int8_t* qy = static_cast<int8_t*>(w.take((size_t)out * ld));
+    float* sy = static_cast<float*>(w.take((size_t)out * 4));
+    int8_t* qx = static_cast<int8_t*>(w.take((size_t)k * ld));
+    float* sx = static_cast<float*>(w.take((size_t)k * 4));
+    void* cy = w.take(cols_ws(n, out, 1));
+    void* cx = w.take(cols_ws(n, k, 0));
+    const size_t gw = gemm_ws(out, k, n);
+    void* g = gw > 0 ? w.take(gw) : nullptr;
+    GQ_TRY(quant(dY, type, n, out, lddy, 1, qy, ld, sy, dbias, cy, s));
+    GQ_TRY(quant(X, type, n, k, ldx, 1, qx, ld, sx, nullptr, cx, s));
+    GQ_TRY(gemm(qy, out, ld, sy, qx, k, ld, sx, n, nullptr, 0, dW, dw_type, lddw, g, gw, dev_err, s));
+  }
+  return GQ_OK;
+}
