@@ -97,7 +97,7 @@ def test_rows_that_are_not_finite():
         assert torch.isnan(scale[1:3]).all() and not codes[1:4].any() and scale[3] == 0
         assert torch.equal(codes[4], torch.full((100,), 127, dtype=torch.int8, device="cuda"))
         y = q.gemm_i8(codes, scale, codes[5:], scale[5:])
-        assert torch.isnan(y[1:3]).all() and torch.isfinite(y[[0, 3, 4, 5]]).all() and (y[3] == 0).all()
+        assert torch.isnan(y[1:3]).all() and torch.isfinite(y[[0, 3, 5]]).all() and (y[3] == 0).all()
         assert (q.gemm_i8(codes, scale, codes[5:], scale[5:], act=q.ACT_RELU)[1:3] == 0).all()
 
 
