@@ -458,22 +458,25 @@ __global__ void __launch_bounds__(kMaxThreads) stats_kernel(const Args p) {
   }
 }
 
-// A block (BLOCK) or a warp a segment and group: its pieces' channels together.
+// A block (BLOCK) or a warp a segment and group: its pieces' channels together,
+// in 64 bits: a mean over millions of cells can be thousands of times smaller
+// than they are (2,449,029 x 16 of them: off by 2e-6 of itself in fp32, 5e-8 so).
 constexpr int kCombine = 512;
 template <bool BLOCK>
-__device__ __forceinline__ float unit_sum(float x, float* sh) {
-  x = warp_sum(x);
+__device__ __forceinline__ double unit_sum(double x, double* sh) {
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) x += __shfl_xor_sync(FULL, x, k);
   if (!BLOCK) return x;
   __syncthreads();
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
   __syncthreads();
-  float s = 0.0f;
+  double s = 0.0;
   for (int w = 0; w < kCombine / 32; ++w) s += sh[w];
   return s;
 }
 template <bool BWD, bool BLOCK>
 __global__ void __launch_bounds__(kCombine) combine_kernel(const Args p) {
-  __shared__ float sh[kCombine / 32];
+  __shared__ double sh[kCombine / 32];
   grid_wait();
   constexpr int per = BLOCK ? 1 : kCombine / 32, step = BLOCK ? kCombine : 32;
   const int64_t unit = (int64_t)blockIdx.x * per + (BLOCK ? 0 : threadIdx.x >> 5);
@@ -496,35 +499,36 @@ __global__ void __launch_bounds__(kCombine) combine_kernel(const Args p) {
   auto count = [&](int64_t k) {  // rows of the segment's piece in its k-th chunk
     return (float)(min(r1, (c0 + k + 1) * p.rows_per) - max(r0, (c0 + k) * p.rows_per));
   };
-  float s1 = 0.0f, s2 = 0.0f;
+  double s1 = 0.0, s2 = 0.0;
   for (int64_t i = lane; i < cells; i += step) {
     const int64_t k = i / p.cg;
     const int c = g * p.cg + (int)(i - k * p.cg);
     const float2 w = p.part[(c0 + k + j) * p.d + c];
     if (BWD) {
       const float ga = p.gamma != nullptr ? p.gamma[c] : 1.0f;
-      s1 = fmaf(ga, w.y, s1);
-      s2 = fmaf(ga, w.x, s2);
+      s1 += (double)ga * w.y;
+      s2 += (double)ga * w.x;
     } else {
-      s1 = fmaf(count(k), w.x, s1);
+      s1 += (double)count(k) * w.x;
     }
   }
-  const float inv = 1.0f / ((float)rows * (float)p.cg);
+  const double inv = 1.0 / ((double)rows * p.cg);
   s1 = unit_sum<BLOCK>(s1, sh) * inv;
   if constexpr (BWD) {
     s2 = unit_sum<BLOCK>(s2, sh) * inv;
-    if (lane == 0) p.hsum[unit] = make_float2(s1, s2);
+    if (lane == 0) p.hsum[unit] = make_float2((float)s1, (float)s2);
   } else {
+    const float mean = (float)s1;
     for (int64_t i = lane; i < cells; i += step) {
       const int64_t k = i / p.cg;
       const float2 w = p.part[(c0 + k + j) * p.d + g * p.cg + (int)(i - k * p.cg)];
-      const float dev = w.x - s1;
-      s2 += fmaf(count(k) * dev, dev, w.y);
+      const float dev = w.x - mean;
+      s2 += (double)fmaf(count(k) * dev, dev, w.y);
     }
     s2 = unit_sum<BLOCK>(s2, sh) * inv;
     if (lane == 0) {
-      p.mean[unit] = s1;
-      p.rstd[unit] = __frcp_rn(__fsqrt_rn(s2 + p.eps));
+      p.mean[unit] = mean;
+      p.rstd[unit] = __frcp_rn(__fsqrt_rn((float)s2 + p.eps));
     }
   }
 }

@@ -8,17 +8,21 @@ calls; no arithmetic happens here.  Layer l uses ReLU except the last
 Between the hidden layers a stack may normalize and drop features, and it
 may end in a class head (gq_train.h; the pages describe neither):
 
-    hidden layer l:  H = A W;  input of layer l + 1 = drop(relu(layer norm(H)))
+    hidden layer l:  H = A W;  input of layer l + 1 = drop(relu(norm(H))), norm
+                     over a node's row (layer) or over each graph of a batch and
+                     groups of channels (group)
                      (without norm: drop(relu(H)))
     class head:      loss = mean cross entropy of softmax(H_last Wc^T) over
-                     the labelled nodes
+                     the labelled nodes; scores = H_last Wc^T of 8-bit integers
+    optimizer:       AdamW on the stack's gradient buffers
 """
 from __future__ import annotations
 
 import torch
 
-from . import (ACT_NONE, ACT_RELU, COEF_GCN, DROPOUT_SEED_TAG, GQError, Graph, Workspace, dropout, gcn_layer_bwd,
-               gcn_layer_fwd, layer_norm_bwd, layer_norm_fwd, lib, linear_xent, to_bf16)
+from . import (ACT_NONE, ACT_RELU, COEF_GCN, DROPOUT_SEED_TAG, F32, AdamW, GQError, Graph, Workspace, dropout,
+               gcn_layer_bwd, gcn_layer_fwd, group_norm_bwd, group_norm_fwd, layer_norm_bwd, layer_norm_fwd, lib,
+               linear_i8, linear_xent, to_bf16)
 
 # stages traced per call (see gq_gcn_layer_fwd / gq_gcn_layer_bwd)
 FWD_STAGES = ("quantize", "aggregate", "update_gemm")
@@ -41,19 +45,33 @@ def launches_bwd(bits: int, need_dinput: bool, dz_given: bool = False) -> int:
 
 
 class GCNStack:
-    """norm: layer normalization behind every hidden layer (its weights are
-    the `norms` of forward and backward, a (gamma, beta) pair per hidden
-    layer; gradients in dgamma, dbeta).  p: dropout rate of the hidden
+    """norm: True or "layer" for layer normalization, "group" for group
+    normalization behind every hidden layer (its weights are the `norms` of
+    forward and backward, a (gamma, beta) pair per hidden layer; gradients in
+    dgamma, dbeta).  "group" takes groups, and, where the graph is a batch of
+    graphs, ptr, the int64 offsets of their nodes, and max_rows, the largest one's
+    number of nodes.  p: dropout rate of the hidden
     layers' outputs (training passes only).  classes: width of the class
     head behind the last layer (loss_and_grad, loss; gradient in dWc).  With
     norm or p the hand-off of dZ between layers is theirs, and fuse_dz does
     not apply."""
 
     def __init__(self, g: Graph, widths, mask: torch.Tensor | None, coef: int = COEF_GCN,
-                 device="cuda", keep_dA: bool = False, fuse_dz: bool = True, norm: bool = False, p: float = 0.0,
-                 classes: int = 0):
+                 device="cuda", keep_dA: bool = False, fuse_dz: bool = True, norm: bool | str = False, p: float = 0.0,
+                 classes: int = 0, groups: int = 1, ptr: torch.Tensor | None = None, max_rows: int = 0):
         if not 0.0 <= p <= 1.0 or classes < 0:
             raise GQError("p must lie in [0, 1] and classes must not be negative")
+        if norm not in (True, False, "layer", "group"):
+            raise GQError(f'norm must be "layer", "group", True (layer) or False, got {norm!r}')
+        self.grouped = grouped = norm == "group"
+        if not grouped and (groups != 1 or ptr is not None or max_rows):
+            raise GQError('groups, ptr and max_rows go with norm="group"')
+        if grouped and any(w % groups for w in widths[1:-1]):
+            raise GQError(f"every hidden width must be a multiple of the {groups} groups")
+        if grouped and ptr is not None and (ptr.dtype != torch.int64 or ptr.dim() != 1 or ptr.numel() < 1):
+            raise GQError("ptr must be an int64 vector of node offsets")
+        norm = bool(norm)
+        self.groups, self.ptr, self.max_rows = groups, ptr, max_rows
         self.norm, self.p, self.classes = norm, float(p), classes
         self.g = g
         self.widths = tuple(widths)
@@ -89,11 +107,12 @@ class GCNStack:
         hidden = range(self.L - 1)
         e32 = lambda *shape: torch.empty(*shape, dtype=torch.float32, device=device)
         self.N = [e32(n, widths[l + 1]) if norm or p > 0.0 else None for l in hidden]
-        self.mean = [e32(n) if norm else None for l in hidden]
-        self.rstd = [e32(n) if norm else None for l in hidden]
+        stats = (n,) if not grouped else (1 if ptr is None else ptr.numel() - 1, groups)
+        self.mean = [e32(*stats) if norm else None for l in hidden]
+        self.rstd = [e32(*stats) if norm else None for l in hidden]
         self.dgamma = [e32(widths[l + 1]) if norm else None for l in hidden]
         self.dbeta = [e32(widths[l + 1]) if norm else None for l in hidden]
-        if norm:
+        if norm and not grouped:  # group normalization makes its ReLU's derivative again, and its gradient in place
             for l in hidden:
                 self.Rb[l] = torch.empty(n, (widths[l + 1] + 31) // 32, dtype=torch.int32, device=device)
                 self.dZ[l] = torch.empty(n, r8(widths[l + 1]), dtype=torch.bfloat16, device=device)
@@ -111,9 +130,16 @@ class GCNStack:
         L = lib()
         self.ws.get(max([int(L.gq_gcn_layer_workspace_bytes(g.ref, widths[l], widths[l + 1], 2))
                          for l in range(self.L)] +
-                        [int(L.gq_layer_norm_bwd_workspace_bytes(n, widths[l + 1])) for l in hidden if norm]))
+                        [int(L.gq_layer_norm_bwd_workspace_bytes(n, widths[l + 1])) for l in hidden
+                         if norm and not grouped] +
+                        [self._group_ws(l, b) for l in hidden for b in (0, 1) if grouped]))
         if classes:
             self.ws_head.get(int(L.gq_linear_xent_workspace_bytes(n, widths[self.L], classes, 1)))
+
+    def _group_ws(self, l, backward):
+        """Workspace of hidden layer l's group normalization."""
+        return int(lib().gq_group_norm_workspace_bytes(self.g.n, self.widths[l + 1], self.groups, F32,
+                                                       self.mean[l].shape[0], self.max_rows, backward))
 
     def act(self, l: int) -> int:
         return ACT_RELU if l < self.L - 1 and not self.norm else ACT_NONE
@@ -145,7 +171,13 @@ class GCNStack:
             p = self.p if training else 0.0
             # the layer's quantizer draws its noise from the same seed
             seed = self._drop[l] = seeds[l] ^ DROPOUT_SEED_TAG
-            if self.norm:
+            if self.grouped:
+                gamma, beta = self._norm_of(norms, l)
+                h, _, _ = group_norm_fwd(h, self.groups, self.ptr, gamma, beta, act=ACT_RELU, max_rows=self.max_rows,
+                                         out=self.N[l], mean=self.mean[l], rstd=self.rstd[l], ws=self.ws)
+                if p > 0.0:
+                    dropout(h, p, seed, out=h)
+            elif self.norm:
                 gamma, beta = self._norm_of(norms, l)
                 layer_norm_fwd(h, gamma, beta, act=ACT_RELU, p=p, seed=seed, out=self.N[l], mean=self.mean[l],
                                rstd=self.rstd[l], relu_bits=self.Rb[l])
@@ -183,7 +215,14 @@ class GCNStack:
             g = self.dH[l]
             if l == 0:
                 continue
-            if self.norm:
+            if self.grouped:
+                gamma, beta = self._norm_of(norms, l - 1)
+                if self.p > 0.0:
+                    dropout(g, self.p, self._drop[l - 1], out=g)
+                group_norm_bwd(g, self.H[l - 1], self.groups, self.mean[l - 1], self.rstd[l - 1], self.ptr, gamma, beta,
+                               act=ACT_RELU, max_rows=self.max_rows, dX=g, dgamma=self.dgamma[l - 1],
+                               dbeta=self.dbeta[l - 1], ws=self.ws)
+            elif self.norm:
                 gamma, _ = self._norm_of(norms, l - 1)
                 layer_norm_bwd(g, self.H[l - 1], self.mean[l - 1], self.rstd[l - 1], gamma, act=ACT_RELU, p=self.p,
                                seed=self._drop[l - 1], relu_bits=self.Rb[l - 1],
@@ -218,10 +257,42 @@ class GCNStack:
         self._graded = True
         return loss
 
+    def scores(self, Wc: torch.Tensor, scale: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+        """Scores of every node over classes on the latest forward pass's
+        output: H_last Wc^T with both quantized to 8 bits, Wc and scale as
+        quantize_i8 left them (any number of classes; no head is needed)."""
+        if getattr(self, "ws_scores", None) is None:
+            self.ws_scores = Workspace(self.H[0].device)
+        return linear_i8(self.H[self.L - 1], Wc, scale, out=out, ws=self.ws_scores, dev_err=self.err)
+
+    def optimizer(self, Ws, norms=None, Wc: torch.Tensor | None = None, **kw) -> AdamW:
+        """An AdamW over the weights, the normalization weights (where forward
+        is given them) and the class head's, whose gradients are the buffers that
+        backward and loss_and_grad write: after them, step() updates all in place.
+        kw: AdamW's arguments (lr, betas, eps, weight_decay, state_bits, ...)."""
+        params, grads = list(Ws), list(self.dW)
+        if len(params) != self.L:
+            raise GQError(f"Ws: one weight matrix for each of the {self.L} layers")
+        if norms is not None:
+            if not self.norm or len(norms) != self.L - 1:
+                raise GQError(f"norms: one (gamma, beta) pair for each of the {self.L - 1} hidden layers of a stack with norm")
+            for l, pair in enumerate(norms):
+                params += pair
+                grads += [self.dgamma[l], self.dbeta[l]]
+        if Wc is not None:
+            if not self.classes or Wc.shape != self.dWc.shape:
+                raise GQError("Wc: the weights of the stack's class head")
+            params.append(Wc)
+            grads.append(self.dWc)
+        return AdamW(params, grads=grads, **kw)
+
     def launches(self, bits: int, need_input_grad: bool = False) -> int:
         """Kernels of one forward and backward pass (from the class head's
         gradient where there is a head), the head's own not counted."""
         n = sum(launches_fwd(bits) + launches_bwd(bits, need_input_grad or l > 0, self.dZ[l] is not None)
                 for l in range(self.L))
+        if self.grouped:  # one pass each way, or three, and the column sums; dropout one each
+            return n + sum((3 if self._group_ws(l, 0) else 1) + (4 if self._group_ws(l, 0) else 2) +
+                           (2 if self.p > 0.0 else 0) for l in range(self.L - 1))
         # normalization: one forward, the pass and its column sums backward; dropout alone: one each
         return n + (self.L - 1) * (3 if self.norm else 2 if self.p > 0.0 else 0)
