@@ -151,9 +151,9 @@ GQ_API int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, cons
  *   for nothing); C m x n of `type` (gq_type), any alignment; bias n fp32 or NULL.
  *   The sum over k is exact; (float)sum times one scale, times the other plus
  *   bias, is rounded at each step and once more to the type.  act = RELU gives 0 for
- *   a NaN.  ws: gq_gemm_i8_workspace_bytes(m, n, k), 16-byte aligned (the
- *   sums of a split contraction; often 0; depends on the device's SM count).
- *   dev_err as for the GEMMs (codes 31 .. 38).
+ *   a NaN.  ws: gq_gemm_i8_workspace_bytes(m, n, k), 256-byte aligned (operands
+ *   as fp16, the sums of a split contraction; 0 for few rows; depends on the
+ *   device's SM count).  dev_err as for the GEMMs (codes 31 .. 38).
  * gq_linear_i8: Y = act(X W^T + bias) with X's rows (n x k) quantized in the call
  *   and W (out x k) as gq_quantize_i8 left it.
  * gq_linear_i8_bwd, W (out x k) and X in full precision, each product of

@@ -165,46 +165,85 @@ struct Code {
   static constexpr int top = SECOND ? 8 : 7;
   static constexpr float far = 1.329227995784916e36f;   // 2^120: fp32's exponent bias less the codes'
   static constexpr float near = 7.52316384526264e-37f;  // 2^-120
-
-  static __device__ __forceinline__ float decode(uint32_t c, float scale) {
-    const uint32_t bits = SECOND ? c << shift : ((c & 127u) << shift | (c & 128u) << 24);
-    return __fmul_rn(__fmul_rn(__uint_as_float(bits), far), scale);
-  }
   // scale of decode, its reciprocal for encode
   static __device__ __forceinline__ float down(int e) { return pow2f(e - top); }
   static __device__ __forceinline__ float up(int e) { return pow2f(254 - (e - top)); }
-
-  static __device__ __forceinline__ uint32_t encode(float x, float scale, uint32_t noise) {
-    const uint32_t add = SECOND ? noise & 0x7FFFFu : noise >> 12;
-    const float y = __fmul_rn(__fmul_rn(fabsf(x), scale), near);
-    uint32_t c = (__float_as_uint(y) + add) >> shift;
-    if (SECOND) return x > 0.0f ? min(max(c, 1u), 255u) : x == 0.0f ? 0u : 255u;
-    return min(c, 126u) | (__float_as_uint(x) >> 24 & 128u);
+  // a code, byte K of w, as the bits of its value times 2^-120
+  template <int K>
+  static __device__ __forceinline__ uint32_t bits(uint32_t w) {
+    if (SECOND) return K < 3 ? ((w >> (8 * K)) & 255u) << shift : w >> 24 << shift;
+    const int at_top = (int)__byte_perm(w, 0, 0x0444 | K << 12);  // bit 31 is the sign
+    return (uint32_t)(at_top >> 4) & 0x87F00000u;
   }
 };
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// codes w (4 values) -> values
+template <bool SECOND>
+__device__ __forceinline__ void decode4(uint32_t w, float scale, float2& lo, float2& hi) {
+  using F = Code<SECOND>;
+  const float2 far = both(F::far), s = both(scale);
+  lo = make_float2(__uint_as_float(F::template bits<0>(w)), __uint_as_float(F::template bits<1>(w)));
+  hi = make_float2(__uint_as_float(F::template bits<2>(w)), __uint_as_float(F::template bits<3>(w)));
+  lo = mul2(mul2(lo, far), s);
+  hi = mul2(mul2(hi, far), s);
+}
+// values -> codes, byte k from noise word h[k].  Codes end at 126 (E4M3's 127 is
+// its NaN) and 255; a second moment that is not 0 gets at least 1.
+template <bool SECOND>
+__device__ __forceinline__ uint32_t encode4(float2 lo, float2 hi, float scale, const uint32_t (&h)[4]) {
+  using F = Code<SECOND>;
+  const float2 near = both(F::near), s = both(scale);
+  const float2 a = mul2(mul2(lo, s), near), b = mul2(mul2(hi, s), near);
+  const uint32_t x[4] = {__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y)};
+  const uint32_t v[4] = {__float_as_uint(lo.x), __float_as_uint(lo.y), __float_as_uint(hi.x), __float_as_uint(hi.y)};
+  uint32_t c[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (SECOND)
+      c[k] = min(max((x[k] + (h[k] & 0x7FFFFu)) >> F::shift, min(v[k], 1u)), 255u);
+    else
+      c[k] = min(((x[k] & 0x7FFFFFFFu) + (h[k] >> 12)) >> F::shift, 126u);
+  }
+  const uint32_t w = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+  if (SECOND) return w;
+  const uint32_t sign = __byte_perm(__byte_perm(v[0], v[1], 0x0073), __byte_perm(v[2], v[3], 0x0073), 0x5410);
+  return w | (sign & 0x80808080u);
+}
 
 __device__ __forceinline__ int block_exp(uint32_t largest_bits) {
   return min(max((int)(__reduce_max_sync(FULL, largest_bits) >> 23), kMinExp), kMaxExp);
 }
+__device__ __forceinline__ float sqrt_fast(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
-// The moments' update is products and a sum, each rounded: the codes can be
-// reproduced from elementary operations.  The quotient is MUFU's (2 steps off at
-// most): it is lr times smaller than p.
-__device__ __forceinline__ void update(float& p, float g, float& m, float& v, const Coef& c) {
-  m = __fadd_rn(__fmul_rn(m, c.b1), __fmul_rn(g, c.o1));
-  v = __fadd_rn(__fmul_rn(v, c.b2), __fmul_rn(__fmul_rn(g, g), c.o2));
-  p = fmaf(p, c.keep, -__fdividef(c.lr1 * m, fmaf(sqrtf(v), c.rs2, c.eps)));
+// Two values.  The moments' update is products and a sum, each rounded: the codes
+// can be reproduced from elementary operations.  The root and the reciprocal are
+// the special function unit's (a step off each): their quotient is lr times smaller than p.
+__device__ __forceinline__ void update(float2& p, float2 g, float2& m, float2& v, const Coef& c) {
+  m = add2(mul2(m, both(c.b1)), mul2(g, both(c.o1)));
+  v = add2(mul2(v, both(c.b2)), mul2(mul2(g, g), both(c.o2)));
+  const float2 den = fma2(make_float2(sqrt_fast(v.x), sqrt_fast(v.y)), both(c.rs2), both(c.eps));
+  const float2 step = mul2(mul2(m, both(-c.lr1)), make_float2(rcp_fast(den.x), rcp_fast(den.y)));
+  p = fma2(p, both(c.keep), step);
 }
 
 // One warp, one block of 256 values: lane l holds values 8 l .. 8 l + 7.
 template <typename TP, typename TG, bool SMALL>
 __device__ __forceinline__ void block_step(const Tensor& t, int64_t b, int lane, const Coef& c, float gs) {
   const int64_t i0 = b * kBlockValues + lane * 8;
-  float p[8], g[8], m[8], v[8];
+  alignas(16) float p[8], g[8], m[8], v[8];
   const bool whole = t.vec && (b + 1) * kBlockValues <= t.n;
   const int live = i0 >= t.n ? 0 : (int)min((int64_t)8, t.n - i0);
   uint2 mc = make_uint2(0, 0), vc = make_uint2(0, 0);
-  int em = 0, ev = 0;
   if (whole) {
     const Raw<TP> rp = load8<TP>(t.p, i0);
     const Raw<TG> rg = load8<TG>(t.g, i0);
@@ -239,18 +278,20 @@ __device__ __forceinline__ void block_step(const Tensor& t, int64_t b, int lane,
     mc = make_uint2(w[0], w[1]);
     vc = make_uint2(w[2], w[3]);
   }
+  float2* p2 = reinterpret_cast<float2*>(p);
+  float2* g2 = reinterpret_cast<float2*>(g);
+  float2* m2 = reinterpret_cast<float2*>(m);
+  float2* v2 = reinterpret_cast<float2*>(v);
   if (SMALL) {
-    em = min(max((int)t.me[b], kMinExp), kMaxExp);
-    ev = min(max((int)t.ve[b], kMinExp), kMaxExp);
-    const float dm = Code<false>::down(em), dv = Code<true>::down(ev);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      m[j] = Code<false>::decode(((j < 4 ? mc.x : mc.y) >> (8 * (j & 3))) & 255u, dm);
-      v[j] = Code<true>::decode(((j < 4 ? vc.x : vc.y) >> (8 * (j & 3))) & 255u, dv);
-    }
+    const float dm = Code<false>::down(min(max((int)t.me[b], kMinExp), kMaxExp));
+    const float dv = Code<true>::down(min(max((int)t.ve[b], kMinExp), kMaxExp));
+    decode4<false>(mc.x, dm, m2[0], m2[1]);
+    decode4<false>(mc.y, dm, m2[2], m2[3]);
+    decode4<true>(vc.x, dv, v2[0], v2[1]);
+    decode4<true>(vc.y, dv, v2[2], v2[3]);
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) update(p[j], g[j] * gs, m[j], v[j], c);
+  for (int j = 0; j < 4; ++j) update(p2[j], mul2(g2[j], both(gs)), m2[j], v2[j], c);
   if (SMALL) {
     uint32_t bm = 0, bv = 0;
 #pragma unroll
@@ -258,24 +299,14 @@ __device__ __forceinline__ void block_step(const Tensor& t, int64_t b, int lane,
       bm = max(bm, __float_as_uint(m[j]) & 0x7FFFFFFFu);
       bv = max(bv, __float_as_uint(v[j]) & 0x7FFFFFFFu);
     }
-    em = block_exp(bm);
-    ev = block_exp(bv);
+    const int em = block_exp(bm), ev = block_exp(bv);
     const float um = Code<false>::up(em), uv = Code<true>::up(ev);
-    const uint32_t kr = row_key(c.key, t.block0 + (uint32_t)b);
-    mc = vc = make_uint2(0, 0);
+    const uint32_t kr = row_key(c.key, t.block0 + (uint32_t)b) + (uint32_t)lane * (8u * 0x9E3779B9u);
+    uint32_t h[2][4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t h = fmix32(kr + (uint32_t)(lane * 8 + j) * 0x9E3779B9u);
-      const uint32_t a = Code<false>::encode(m[j], um, h) << (8 * (j & 3));
-      const uint32_t d = Code<true>::encode(v[j], uv, h) << (8 * (j & 3));
-      if (j < 4) {
-        mc.x |= a;
-        vc.x |= d;
-      } else {
-        mc.y |= a;
-        vc.y |= d;
-      }
-    }
+    for (int j = 0; j < 8; ++j) h[j >> 2][j & 3] = fmix32(kr + (uint32_t)j * 0x9E3779B9u);
+    mc = make_uint2(encode4<false>(m2[0], m2[1], um, h[0]), encode4<false>(m2[2], m2[3], um, h[1]));
+    vc = make_uint2(encode4<true>(v2[0], v2[1], uv, h[0]), encode4<true>(v2[2], v2[3], uv, h[1]));
     if (lane == 0) {
       t.me[b] = (uint8_t)em;
       t.ve[b] = (uint8_t)ev;
@@ -347,14 +378,17 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t i0 = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 8;
   if (i0 >= n) return;
   const float s = Code<SECOND>::down(min(max((int)exps[i0 / kBlockValues], kMinExp), kMaxExp));
+  float2 x[4];
   if (vec && i0 + 8 <= n) {
     const uint2 c = *reinterpret_cast<const uint2*>(codes + i0);
-    float x[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = Code<SECOND>::decode(((j < 4 ? c.x : c.y) >> (8 * (j & 3))) & 255u, s);
-    store8<T>(out, i0, x);
+    decode4<SECOND>(c.x, s, x[0], x[1]);
+    decode4<SECOND>(c.y, s, x[2], x[3]);
+    store8<T>(out, i0, reinterpret_cast<const float(&)[8]>(x));
   } else {
-    for (int64_t i = i0; i < n && i < i0 + 8; ++i) out[i] = from_f<T>(Code<SECOND>::decode(codes[i], s));
+    for (int64_t i = i0; i < n && i < i0 + 8; ++i) {
+      decode4<SECOND>(codes[i], s, x[0], x[1]);
+      out[i] = from_f<T>(x[0].x);
+    }
   }
 }
 

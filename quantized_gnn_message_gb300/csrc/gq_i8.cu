@@ -74,6 +74,14 @@ __device__ __forceinline__ void tmem_alloc2(uint32_t* dst, uint32_t cols) {
 __device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t cols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
 }
+// a box into this CTA's shared memory, its bytes counted on a barrier of the even CTA
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
 __device__ __forceinline__ void umma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n"
@@ -198,6 +206,14 @@ __device__ __forceinline__ int quantize(float x, const Scale& c) {
 __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
   return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 | (uint32_t)(d & 255) << 24;
 }
+// four codes, as bytes or as fp16
+__device__ __forceinline__ void put4(int8_t* q, int a, int b, int c, int d) {
+  *reinterpret_cast<uint32_t*>(q) = pack4(a, b, c, d);
+}
+__device__ __forceinline__ void put4(__half* q, int a, int b, int c, int d) {
+  const __half2 x = __floats2half2_rn((float)a, (float)b), y = __floats2half2_rn((float)c, (float)d);
+  *reinterpret_cast<uint2*>(q) = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+}
 __device__ __forceinline__ uint32_t mag(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
 // 4 consecutive values of a row
@@ -222,9 +238,9 @@ __device__ __forceinline__ float4 load4<__half>(const __half* p) {
 // Rows: LANES threads a row (a warp up to 4,096 columns, else the block), the
 // row read twice, the second time from L1.
 constexpr int kQThreads = 256;
-template <typename T, bool VEC, int LANES>
+template <typename T, typename O, bool VEC, int LANES>
 __global__ void __launch_bounds__(kQThreads)
-    quant_rows_kernel(const T* __restrict__ X, int64_t n, int d, int64_t ldx, int8_t* __restrict__ Q, int64_t ldq,
+    quant_rows_kernel(const T* __restrict__ X, int64_t n, int d, int64_t ldx, O* __restrict__ Q, int64_t ldq,
                       float* __restrict__ S) {
   __shared__ uint32_t smax[kQThreads / 32];
   const int lane = threadIdx.x % LANES;
@@ -254,16 +270,16 @@ __global__ void __launch_bounds__(kQThreads)
   if (!live) return;
   const Scale c = make_scale(top);
   if (lane == 0) S[r] = c.s;
-  int8_t* q = Q + r * ldq;
+  O* q = Q + r * ldq;
   if (VEC) {
     const int d4 = d & ~3;
     for (int k = lane * 4; k < d4; k += LANES * 4) {
       const float4 v = load4<T>(x + k);
-      *reinterpret_cast<uint32_t*>(q + k) = pack4(quantize(v.x, c), quantize(v.y, c), quantize(v.z, c), quantize(v.w, c));
+      put4(q + k, quantize(v.x, c), quantize(v.y, c), quantize(v.z, c), quantize(v.w, c));
     }
-    if (d4 + lane < d) q[d4 + lane] = (int8_t)quantize((float)x[d4 + lane], c);
+    if (d4 + lane < d) q[d4 + lane] = (O)quantize((float)x[d4 + lane], c);
   } else {
-    for (int k = lane; k < d; k += LANES) q[k] = (int8_t)quantize((float)x[k], c);
+    for (int k = lane; k < d; k += LANES) q[k] = (O)quantize((float)x[k], c);
   }
 }
 
@@ -315,10 +331,10 @@ __global__ void col_sum_kernel(const float* __restrict__ sums, int parts, int d,
 
 // Second pass: a block turns 128 rows x 64 columns into 64 rows of 128 bytes.
 constexpr int kTrRows = 128, kTrCols = 64, kTrPitch = kTrRows + 4;
-template <typename T>
+template <typename T, typename O>
 __global__ void __launch_bounds__(kQThreads)
     quant_cols_kernel(const T* __restrict__ X, int64_t n, int d, int64_t ldx, const uint32_t* __restrict__ top,
-                      int8_t* __restrict__ Q, int64_t ldq, float* __restrict__ S) {
+                      O* __restrict__ Q, int64_t ldq, float* __restrict__ S) {
   __shared__ __align__(16) int8_t tile[kTrCols][kTrPitch];
   const int c0 = blockIdx.y * kTrCols;
   const int64_t r0 = (int64_t)blockIdx.x * kTrRows;
@@ -338,26 +354,36 @@ __global__ void __launch_bounds__(kQThreads)
   // rows of Q start 16-byte aligned; bytes past n of the last 16 are written as 0
   for (int i = threadIdx.x; i < kTrCols * (kTrRows / 4); i += kQThreads) {
     const int row = i / (kTrRows / 4), at = i % (kTrRows / 4) * 4;
-    if (c0 + row < d && r0 + at < n)
-      *reinterpret_cast<uint32_t*>(Q + (int64_t)(c0 + row) * ldq + r0 + at) =
-          *reinterpret_cast<const uint32_t*>(&tile[row][at]);
+    if (c0 + row < d && r0 + at < n) {
+      const int w = *reinterpret_cast<const int*>(&tile[row][at]);
+      put4(Q + (int64_t)(c0 + row) * ldq + r0 + at, w << 24 >> 24, w << 16 >> 24, w << 8 >> 24, w >> 24);
+    }
   }
 }
 
 // ------------------------------------------------------------- tile product --
-constexpr int kThreads = 640;
-constexpr int kConvWarps = 8, kEpiWarps = 8;
+constexpr int kConvWarps = 8, kTeams = 2, kTeamWarps = kConvWarps / kTeams, kEpiWarps = 8;
 constexpr int kTile = 256;                 // rows of S a pair, at most as many of F
 constexpr int kStep = 64;                  // products of a step
 constexpr int kDrain = 16;                 // steps after which an accumulator is drained: 1,024 products
-constexpr int kRing8 = 5, kRing16 = 3;
-constexpr int kBytes8 = 2 * 128 * kStep;   // S | F bytes of a stage
-constexpr int kBytes16 = 2 * kBytes8;
+constexpr int kSBytes = 128 * kStep * 2;   // a CTA's half of S in a stage, F's at most as much
+constexpr int kStage = 2 * kSBytes;
+constexpr int kBytes8 = 128 * kStep;       // S as bytes
 constexpr int kStgPitch = 36;              // floats: 32 columns and a shift of 4 banks a row
 constexpr int kStg = 32 * kStgPitch * 4;
-constexpr int kSmem = 1024 + kRing16 * kBytes16 + kRing8 * kBytes8 + kEpiWarps * kStg + 512;
 constexpr long long kDrainCycles = 4000000;
 constexpr int64_t kMaxSplitSteps = 1024;   // 65,536 products: a 32-bit sum holds twice that
+
+// CONV: S arrives as bytes and is widened in the kernel.
+template <bool CONV>
+struct Shape {
+  static constexpr int threads = CONV ? 640 : 384;
+  static constexpr int epi0 = threads / 32 - kEpiWarps;  // first epilogue warp
+  static constexpr int ring = CONV ? 4 : 5;
+  static constexpr int ring8 = CONV ? 6 : 0;
+  static constexpr int smem = 1024 + ring * kStage + ring8 * kBytes8 + kEpiWarps * kStg + 512;
+};
+static_assert(Shape<true>::ring % kTeams == 0 && Shape<true>::ring8 % kTeams == 0, "a team meets every other stage");
 
 struct TileArgs {
   int64_t M, N;                            // rows of S and F
@@ -406,8 +432,7 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
   hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 // chunk i of 16 bytes of a [rows][64] byte tile into a [rows][64] fp16 tile, 128-byte swizzle
-__device__ __forceinline__ void widen_chunk(const uint8_t* src, uint8_t* dst, int i) {
-  const uint4 w = *reinterpret_cast<const uint4*>(src + i * 16);
+__device__ __forceinline__ void widen_chunk(uint4 w, uint8_t* dst, int i) {
   uint4 a, b;
   widen(w.x, a.x, a.y);
   widen(w.y, a.z, a.w);
@@ -505,34 +530,39 @@ __device__ __forceinline__ void put(const TileArgs& p, const Unit& u, int64_t ro
   __syncwarp();
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <bool CONV>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<CONV>::threads, 1)
     i8_tiles_kernel(const __grid_constant__ CUtensorMap mS, const __grid_constant__ CUtensorMap mF, const TileArgs p) {
+  using Z = Shape<CONV>;
+  constexpr int R = Z::ring, R8 = CONV ? Z::ring8 : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* s16 = smem;
-  uint8_t* s8 = s16 + kRing16 * kBytes16;
-  float* stg_all = reinterpret_cast<float*>(s8 + kRing8 * kBytes8);
-  uint64_t* full8 = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(stg_all) + kEpiWarps * kStg);
-  uint64_t* empty8 = full8 + kRing8;
-  uint64_t* conv = empty8 + kRing8;      // this CTA's fp16 stage is made
-  uint64_t* peer = conv + kRing16;       // the odd CTA's is (in the even CTA)
-  uint64_t* empty16 = peer + kRing16;
-  uint64_t* tfull = empty16 + kRing16;
+  uint8_t* s8 = s16 + R * kStage;
+  float* stg_all = reinterpret_cast<float*>(s8 + Z::ring8 * kBytes8);
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(stg_all) + kEpiWarps * kStg);
+  uint64_t* empty = full + R;
+  uint64_t* tfull = empty + R;
   uint64_t* tempty = tfull + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  uint64_t* conv = tempty + 2;           // this CTA's S of a stage is widened
+  uint64_t* peer = conv + R;             // the odd CTA's is (in the even CTA)
+  uint64_t* full8 = peer + R;
+  uint64_t* empty8 = full8 + R8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(empty8 + R8);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t cr = cluster_rank();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kRing8; ++s) {
-      mbar_init(&full8[s], 1);
-      mbar_init(&empty8[s], kConvWarps);
-    }
-    for (int s = 0; s < kRing16; ++s) {
-      mbar_init(&conv[s], kConvWarps);
+    for (int s = 0; s < R; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&conv[s], kTeamWarps);
       mbar_init(&peer[s], 1);
-      mbar_init(&empty16[s], 1);
+    }
+    for (int s = 0; s < R8; ++s) {
+      mbar_init(&full8[s], 1);
+      mbar_init(&empty8[s], kTeamWarps);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
@@ -551,13 +581,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int hn = p.NT / 2;
 
-  // 3 warpgroups at 40 registers and 2 at 176: 60,416 in all, of the
-  // 61,440 (96 a thread) that the block is launched with
+  // With CONV 3 warpgroups at 48 registers and 2 at 168: the 61,440 (96 a
+  // thread) that the block is launched with.
   if (warp < 4) {
-    regs_down<40>();
-    if (warp == 0 && lane == 0) {
-      prefetch_tmap(&mS);
+    if constexpr (CONV) regs_down<48>();
+    if (warp == 0 && lane == 0) {  // fp16 operands: F, and S where it is not widened here
       prefetch_tmap(&mF);
+      if (!CONV) prefetch_tmap(&mS);
+      const uint32_t bytes = (uint32_t)hn * 128 + (CONV ? 0 : kSBytes);
       int st = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -565,12 +596,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const Unit u = get_unit(p, i);
         const int ys = (int)(u.mt * kTile + cr * 128), yf = (int)(u.nt * p.NT + cr * hn);
         for (int s = u.s0; s < u.s1; ++s) {
-          if (!(ok = wait(&empty8[st], ph ^ 1, abort, p.err, 31))) break;
-          mbar_expect_tx(&full8[st], (uint32_t)((128 + hn) * kStep));
-          uint8_t* dst = s8 + st * kBytes8;
-          tma_load_2d(dst, &mS, s * kStep, ys, &full8[st]);
-          tma_load_2d(dst + 128 * kStep, &mF, s * kStep, yf, &full8[st]);
-          if (++st == kRing8) {
+          if (!(ok = wait(&empty[st], ph ^ 1, abort, p.err, 31))) break;
+          const uint32_t dst = smem_u32(s16 + st * kStage), bar = mapa(smem_u32(&full[st]), 0);
+          if (cr == 0) mbar_expect_tx(&full[st], 2 * bytes);
+          if (!CONV) tma_load_pair(dst, &mS, s * kStep, ys, bar);
+          tma_load_pair(dst + kSBytes, &mF, s * kStep, yf, bar);
+          if (++st == R) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+    } else if (CONV && warp == 2 && lane == 0) {  // S as bytes
+      prefetch_tmap(&mS);
+      int st = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int64_t i = pair; ok && i < p.units; i += pairs) {
+        const Unit u = get_unit(p, i);
+        const int ys = (int)(u.mt * kTile + cr * 128);
+        for (int s = u.s0; s < u.s1; ++s) {
+          if (!(ok = wait(&empty8[st], ph ^ 1, abort, p.err, 36))) break;
+          mbar_expect_tx(&full8[st], kBytes8);
+          tma_load_2d(s8 + st * kBytes8, &mS, s * kStep, ys, &full8[st]);
+          if (++st == R8) {
             st = 0;
             ph ^= 1;
           }
@@ -591,16 +640,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t d = tmem + a * 256;
           const int e = min(u.s1, g + kDrain);
           for (int s = g; s < e; ++s) {
-            if (!(ok = wait(&conv[st], ph, abort, p.err, 33))) break;
-            if (!(ok = wait<true>(&peer[st], ph, abort, p.err, 34))) break;
+            if (!(ok = wait(&full[st], ph, abort, p.err, 33))) break;
+            if (CONV && !(ok = wait(&conv[st], ph, abort, p.err, 34) && wait<true>(&peer[st], ph, abort, p.err, 34))) break;
             tc_fence_after();
-            const uint32_t ab = smem_u32(s16 + st * kBytes16), bb = ab + 128 * 128;
+            const uint32_t ab = smem_u32(s16 + st * kStage), bb = ab + kSBytes;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               umma_pair(d, smem_desc_sw128(ab + 32 * kk, 16, 1024), smem_desc_sw128(bb + 32 * kk, 16, 1024), idesc,
                         s > g || kk > 0);
-            commit_pair(&empty16[st]);
-            if (++st == kRing16) {
+            commit_pair(&empty[st]);
+            if (++st == R) {
               st = 0;
               ph ^= 1;
             }
@@ -608,7 +657,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (ok) commit_pair(&tfull[a]);
         }
       }
-    } else if (warp == 1 && lane == 0) {
+    } else if (CONV && warp == 1 && lane == 0) {
       int st = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -617,49 +666,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int s = u.s0; s < u.s1; ++s) {
           if (!(ok = wait(&conv[st], ph, abort, p.err, 35))) break;
           arrive_release_cluster(mapa(smem_u32(&peer[st]), 0));
-          if (++st == kRing16) {
+          if (++st == R) {
             st = 0;
             ph ^= 1;
           }
         }
       }
     }
-  } else if (warp < 4 + kConvWarps) {
-    regs_down<40>();
-    const int t = threadIdx.x - 128;
-    int st8 = 0, st = 0;
-    uint32_t ph8 = 0, ph = 0;
+  } else if (CONV && warp < Z::epi0) {
+    // a team of four warps widens every other step: the waits, reads and writes
+    // of one step lie under those of the next
+    if constexpr (CONV) regs_down<48>();
+    const int t = (threadIdx.x - 128) % (32 * kTeamWarps), team = (warp - 4) / kTeamWarps;
+    int st = team, st8 = team;
+    uint32_t ph = 0, ph8 = 0;
+    int turn = 0;
     bool ok = true;
     for (int64_t i = pair; ok && i < p.units; i += pairs) {
       const Unit u = get_unit(p, i);
       for (int s = u.s0; s < u.s1; ++s) {
-        ok = wait(&full8[st8], ph8, abort, p.err, 36) && wait(&empty16[st], ph ^ 1, abort, p.err, 37);
+        const bool mine = turn == team;
+        turn = turn + 1 == kTeams ? 0 : turn + 1;
+        if (!mine) continue;
+        ok = wait(&full8[st8], ph8, abort, p.err, 37);
         if (!(ok = __all_sync(FULL, ok))) break;
         const uint8_t* src = s8 + st8 * kBytes8;
-        uint8_t* dst = s16 + st * kBytes16;
-        widen_chunk(src, dst, t);
-        widen_chunk(src, dst, t + 256);
-        for (int k = t; k < hn * 4; k += 256) widen_chunk(src + 128 * kStep, dst + 128 * 128, k);
+        uint4 w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = *reinterpret_cast<const uint4*>(src + (t + 128 * k) * 16);
+        ok = wait(&empty[st], ph ^ 1, abort, p.err, 37);
+        if (!(ok = __all_sync(FULL, ok))) break;
+        uint8_t* dst = s16 + st * kStage;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) widen_chunk(w[k], dst, t + 128 * k);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&empty8[st8]);
           mbar_arrive(&conv[st]);
         }
-        if (++st8 == kRing8) {
-          st8 = 0;
+        if ((st8 += kTeams) >= R8) {
+          st8 = team;
           ph8 ^= 1;
         }
-        if (++st == kRing16) {
-          st = 0;
+        if ((st += kTeams) >= R) {
+          st = team;
           ph ^= 1;
         }
       }
     }
   } else {
-    regs_up<176>();
-    const int quarter = warp & 3, part = (warp - 12) >> 2;
-    float* stg = stg_all + (warp - 12) * (kStg / 4);
+    if constexpr (CONV) regs_up<168>();
+    const int quarter = warp & 3, part = (warp - Z::epi0) >> 2;
+    float* stg = stg_all + (warp - Z::epi0) * (kStg / 4);
     const uint32_t tempty0 = mapa(smem_u32(tempty), 0);
     const int cb = part ? p.half : 0, ce = part ? p.NT : p.half;
     int gen = 0;
@@ -717,6 +776,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tmem_dealloc2(tmem, 512);
   }
   cluster_sync();
+}
+
+// Bytes as fp16, 16 at a time (a row's bytes up to the next multiple of 16 are read and widened too).
+__global__ void __launch_bounds__(256)
+    widen_kernel(const int8_t* A, int64_t rows, int per_row, int64_t lda, __half* out, int64_t ldo) {
+  grid_wait();
+  const int64_t total = rows * per_row;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / per_row, c = (i - r * per_row) * 16;
+    const uint4 w = *reinterpret_cast<const uint4*>(A + r * lda + c);
+    uint4 a, b;
+    widen(w.x, a.x, a.y);
+    widen(w.y, a.z, a.w);
+    widen(w.z, b.x, b.y);
+    widen(w.w, b.z, b.w);
+    uint4* o = reinterpret_cast<uint4*>(out + r * ldo + c);
+    o[0] = a;
+    o[1] = b;
+  }
 }
 
 // C from the splits' sums, added as 64-bit integers.
@@ -804,16 +882,17 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// bytes [rows][cols] with row pitch ld; boxes of 64 columns, zeros outside
-int make_tmap8(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
+// bytes or fp16 [rows][cols] with row pitch ld (elements); boxes of 64 columns, zeros outside
+int make_tmap(CUtensorMap* m, const void* base, bool wide, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
   auto fn = encode_fn();
   if (fn == nullptr) return GQ_ERR_CUDA;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)ld};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * (wide ? 2 : 1)};
   const cuuint32_t box[2] = {kStep, (cuuint32_t)box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const CUresult r = fn(m, wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                        const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? GQ_OK : GQ_ERR_INVALID_ARG;
 }
@@ -823,20 +902,26 @@ int type_bytes(int type) { return type == GQ_F32 ? 4 : 2; }
 constexpr int64_t kMaxRows = (int64_t)1 << 30;  // tensor maps and coordinates
 
 struct Plan {
-  int swap, NT, steps, splits, split_steps;
+  int swap, conv, NT, steps, splits, split_steps;
   int64_t M, N, tm, tn, ldp;
-  size_t ws;
+  size_t sums;           // bytes of the splits' sums
 };
 
-// The operand with more rows is S.  F's tiles are as equal as multiples of 32
-// allow.  The contraction is split where the tiles alone leave more than half
-// of the pairs without work (each split at least one drained accumulator's 1,024
-// products, 256 where that still leaves pairs idle), and beyond 65,536 products.
+constexpr int64_t kConvColumns = 2048;
+
+// S is A, unless A has fewer rows than a tile and than B: then B's rows fill
+// the tiles, and C is written transposed.  F's tiles are as equal as multiples
+// of 32 allow.  S is widened in the kernel where it meets few rows of F: one
+// pass over DRAM as bytes instead of bytes, fp16 out and fp16 in; otherwise
+// before it, and the tile loop has TMA feed the tensor cores alone.
+// The contraction is split where the tiles alone leave more than half of the
+// pairs without work, and beyond 65,536 products.
 Plan make_plan(int64_t m, int64_t n, int64_t k) {
   Plan z{};
-  z.swap = n > m;
+  z.swap = m < kTile && n > m;
   z.M = z.swap ? n : m;
   z.N = z.swap ? m : n;
+  z.conv = z.N < kConvColumns;
   z.tm = (z.M + kTile - 1) / kTile;
   z.tn = (z.N + kTile - 1) / kTile;
   const int64_t per = (z.N + z.tn - 1) / z.tn;
@@ -846,7 +931,7 @@ Plan make_plan(int64_t m, int64_t n, int64_t k) {
   const int64_t pairs = sm_count() / 2 > 0 ? sm_count() / 2 : 1;
   int64_t want = pairs / (z.tm * z.tn);
   if (want < 1) want = 1;
-  int64_t most = (z.steps + 3) / 4;
+  const int64_t most = (z.steps + 3) / 4;
   if (want > most) want = most;
   const int64_t least = (z.steps + kMaxSplitSteps - 1) / kMaxSplitSteps;
   if (want < least) want = least;
@@ -855,7 +940,7 @@ Plan make_plan(int64_t m, int64_t n, int64_t k) {
   z.split_steps = (int)per_split;
   z.splits = (int)((z.steps + per_split - 1) / per_split);
   z.ldp = (z.N + 3) / 4 * 4;
-  z.ws = z.splits > 1 ? (size_t)z.splits * z.M * z.ldp * 4 : 0;
+  z.sums = z.splits > 1 ? (size_t)z.splits * z.M * z.ldp * 4 : 0;
   return z;
 }
 
@@ -865,10 +950,18 @@ bool valid_shape(int64_t m, int64_t n, int64_t k) {
 
 bool few(int64_t m, int64_t k) { return m <= kFew && k <= 65536; }  // a 32-bit sum holds twice that
 
-size_t gemm_ws(int64_t m, int64_t n, int64_t k) {
-  if (few(m, k)) return 0;
-  return make_plan(m, n, k).ws;
-}
+int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+// One operand of a product: codes as bytes or fp16, rows of a multiple of 16.
+struct Operand {
+  const void* q;
+  int64_t ld;
+  const float* scale;
+};
+// Whether the tile kernel takes A (or B) as fp16.
+bool wants_wide(const Plan& z, bool is_a) { return !z.conv || is_a == (z.swap != 0); }
+size_t code_bytes(int64_t rows, int64_t k, bool wide) { return round256((size_t)rows * round16(k) * (wide ? 2 : 1)); }
 
 template <int M>
 int few_rows(const int8_t* A, int64_t lda, const float* sA, const int8_t* B, int64_t N, int64_t ldb, const float* sB,
@@ -879,19 +972,39 @@ int few_rows(const int8_t* A, int64_t lda, const float* sA, const int8_t* B, int
                       bias, C, ldc, type, relu);
 }
 
-int gemm(const int8_t* A, int64_t m, int64_t lda, const float* sA, const int8_t* B, int64_t n, int64_t ldb,
-         const float* sB, int64_t k, const float* bias, int relu, void* C, int type, int64_t ldc, void* ws,
-         size_t ws_bytes, int* err, cudaStream_t s) {
-  if (few(m, k)) {
+int few_gemm(const Operand& A, int64_t m, const Operand& B, int64_t n, int64_t k, const float* bias, int relu, void* C,
+             int type, int64_t ldc, cudaStream_t s) {
+  const int8_t* a = static_cast<const int8_t*>(A.q);
+  const int8_t* b = static_cast<const int8_t*>(B.q);
 #define GQ_FEW(I) \
-  case I: return few_rows<I>(A, lda, sA, B, n, ldb, sB, (int)k, bias, C, ldc, type, relu, s);
-    switch (m) {
-      GQ_FEW(1) GQ_FEW(2) GQ_FEW(3) GQ_FEW(4) GQ_FEW(5) GQ_FEW(6) GQ_FEW(7) GQ_FEW(8)
-    }
-#undef GQ_FEW
+  case I: return few_rows<I>(a, A.ld, A.scale, b, n, B.ld, B.scale, (int)k, bias, C, ldc, type, relu, s);
+  switch (m) {
+    GQ_FEW(1) GQ_FEW(2) GQ_FEW(3) GQ_FEW(4) GQ_FEW(5) GQ_FEW(6) GQ_FEW(7) GQ_FEW(8)
   }
-  const Plan z = make_plan(m, n, k);
-  if (z.ws > 0 && (ws == nullptr || ws_bytes < z.ws || !aligned(ws, 16))) return GQ_ERR_WORKSPACE;
+#undef GQ_FEW
+  return GQ_ERR_UNSUPPORTED;
+}
+
+int widen(const int8_t* q, int64_t rows, int64_t k, int64_t ld, void* out, cudaStream_t s) {
+  const int64_t per_row = round16(k) / 16;
+  int64_t blocks = (rows * per_row + 255) / 256;
+  if (blocks > 16 * (int64_t)sm_count()) blocks = 16 * (int64_t)sm_count();
+  return launch_after(widen_kernel, dim3((unsigned)blocks), dim3(256), 0, s, q, rows, (int)per_row, ld,
+                      static_cast<__half*>(out), round16(k));
+}
+
+template <bool CONV>
+int launch_tiles(const CUtensorMap& mS, const CUtensorMap& mF, const TileArgs& a, cudaStream_t s) {
+  GQ_TRY_CUDA(cudaFuncSetAttribute(i8_tiles_kernel<CONV>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<CONV>::smem));
+  const int64_t pairs = sm_count() / 2 > 0 ? sm_count() / 2 : 1;
+  const int64_t use = a.units < pairs ? a.units : pairs;
+  return launch_after(i8_tiles_kernel<CONV>, dim3((unsigned)(2 * use)), dim3(Shape<CONV>::threads), Shape<CONV>::smem, s,
+                      mS, mF, a);
+}
+
+// The product of operands as wants_wide has them.
+int tile_gemm(const Plan& z, const Operand& A, const Operand& B, int64_t k, const float* bias, int relu, void* C, int type,
+              int64_t ldc, void* sums, int* err, cudaStream_t s) {
   TileArgs a{};
   a.M = z.M;
   a.N = z.N;
@@ -909,27 +1022,34 @@ int gemm(const int8_t* A, int64_t m, int64_t lda, const float* sA, const int8_t*
   a.relu = relu;
   a.swap = z.swap;
   a.vec = aligned(C, 16) && ldc * type_bytes(type) % 16 == 0;
-  a.sS = z.swap ? sB : sA;
-  a.sF = z.swap ? sA : sB;
+  const Operand& S = z.swap ? B : A;
+  const Operand& F = z.swap ? A : B;
+  a.sS = S.scale;
+  a.sF = F.scale;
   a.bias = bias;
-  a.part = z.splits > 1 ? static_cast<int*>(ws) : nullptr;
+  a.part = z.splits > 1 ? static_cast<int*>(sums) : nullptr;
   a.ldp = z.ldp;
   a.err = err;
   CUtensorMap mS, mF;
-  GQ_TRY(make_tmap8(&mS, z.swap ? B : A, k, z.M, z.swap ? ldb : lda, 128));
-  GQ_TRY(make_tmap8(&mF, z.swap ? A : B, k, z.N, z.swap ? lda : ldb, z.NT / 2));
-  GQ_TRY_CUDA(cudaFuncSetAttribute(i8_tiles_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
-  const int64_t pairs = sm_count() / 2 > 0 ? sm_count() / 2 : 1;
-  const int64_t use = a.units < pairs ? a.units : pairs;
-  GQ_TRY(launch_after(i8_tiles_kernel, dim3((unsigned)(2 * use)), dim3(kThreads), kSmem, s, mS, mF, a));
+  GQ_TRY(make_tmap(&mS, S.q, !z.conv, k, z.M, S.ld, 128));
+  GQ_TRY(make_tmap(&mF, F.q, true, k, z.N, F.ld, z.NT / 2));
+  GQ_TRY(z.conv ? launch_tiles<true>(mS, mF, a, s) : launch_tiles<false>(mS, mF, a, s));
   if (a.part == nullptr) return GQ_OK;
   int64_t blocks = (z.M * z.ldp + 255) / 256;
   if (blocks > 65536) blocks = 65536;
   return launch_after(join_kernel, dim3((unsigned)blocks), dim3(256), 0, s, a);
 }
 
-template <typename T>
-int quant_rows(const T* X, int64_t n, int d, int64_t ldx, int8_t* Q, int64_t ldq, float* S, cudaStream_t s) {
+// Workspace of a product whose operands are given as bytes (a, b) or made in it.
+size_t gemm_ws(int64_t m, int64_t n, int64_t k, bool a_bytes, bool b_bytes) {
+  if (few(m, k)) return 0;
+  const Plan z = make_plan(m, n, k);
+  return round256(z.sums) + (a_bytes && wants_wide(z, true) ? code_bytes(m, k, true) : 0) +
+         (b_bytes && wants_wide(z, false) ? code_bytes(n, k, true) : 0);
+}
+
+template <typename T, typename O>
+int quant_rows(const T* X, int64_t n, int d, int64_t ldx, O* Q, int64_t ldq, float* S, cudaStream_t s) {
   const bool vec = aligned(X, 4 * sizeof(T)) && ldx % 4 == 0;
   const int per = d <= 4096 ? kQThreads / 32 : 1;
   const int64_t blocks = (n + per - 1) / per;
@@ -937,14 +1057,14 @@ int quant_rows(const T* X, int64_t n, int d, int64_t ldx, int8_t* Q, int64_t ldq
   const dim3 g((unsigned)blocks);
   if (d <= 4096) {
     if (vec)
-      quant_rows_kernel<T, true, 32><<<g, kQThreads, 0, s>>>(X, n, d, ldx, Q, ldq, S);
+      quant_rows_kernel<T, O, true, 32><<<g, kQThreads, 0, s>>>(X, n, d, ldx, Q, ldq, S);
     else
-      quant_rows_kernel<T, false, 32><<<g, kQThreads, 0, s>>>(X, n, d, ldx, Q, ldq, S);
+      quant_rows_kernel<T, O, false, 32><<<g, kQThreads, 0, s>>>(X, n, d, ldx, Q, ldq, S);
   } else {
     if (vec)
-      quant_rows_kernel<T, true, kQThreads><<<g, kQThreads, 0, s>>>(X, n, d, ldx, Q, ldq, S);
+      quant_rows_kernel<T, O, true, kQThreads><<<g, kQThreads, 0, s>>>(X, n, d, ldx, Q, ldq, S);
     else
-      quant_rows_kernel<T, false, kQThreads><<<g, kQThreads, 0, s>>>(X, n, d, ldx, Q, ldq, S);
+      quant_rows_kernel<T, O, false, kQThreads><<<g, kQThreads, 0, s>>>(X, n, d, ldx, Q, ldq, S);
   }
   return launch_status();
 }
@@ -962,8 +1082,8 @@ size_t cols_ws(int64_t n, int d, int sums) {
   return ((size_t)d * 4 + 255) / 256 * 256 + (sums ? (size_t)col_parts(n, d) * d * 4 : 0);
 }
 
-template <typename T>
-int quant_cols(const T* X, int64_t n, int d, int64_t ldx, int8_t* Q, int64_t ldq, float* S, float* colsum, void* ws,
+template <typename T, typename O>
+int quant_cols(const T* X, int64_t n, int d, int64_t ldx, O* Q, int64_t ldq, float* S, float* colsum, void* ws,
                cudaStream_t s) {
   uint32_t* top = static_cast<uint32_t*>(ws);
   float* sums = colsum != nullptr ? reinterpret_cast<float*>(static_cast<char*>(ws) + ((size_t)d * 4 + 255) / 256 * 256)
@@ -976,30 +1096,35 @@ int quant_cols(const T* X, int64_t n, int d, int64_t ldx, int8_t* Q, int64_t ldq
     col_sum_kernel<<<(d + 255) / 256, 256, 0, s>>>(sums, (int)parts, d, colsum);
     GQ_TRY(launch_status());
   }
-  quant_cols_kernel<T><<<dim3((unsigned)((n + kTrRows - 1) / kTrRows), (d + kTrCols - 1) / kTrCols), kQThreads, 0, s>>>(
+  quant_cols_kernel<T, O><<<dim3((unsigned)((n + kTrRows - 1) / kTrRows), (d + kTrCols - 1) / kTrCols), kQThreads, 0, s>>>(
       X, n, d, ldx, top, Q, ldq, S);
   return launch_status();
 }
 
-int quant(const void* X, int type, int64_t n, int d, int64_t ldx, int transpose, int8_t* Q, int64_t ldq, float* S,
+template <typename T, typename O>
+int quant_to(const void* X, int64_t n, int d, int64_t ldx, int transpose, void* Q, int64_t ldq, float* S, float* colsum,
+             void* ws, cudaStream_t s) {
+  const T* x = static_cast<const T*>(X);
+  O* q = static_cast<O*>(Q);
+  return transpose ? quant_cols(x, n, d, ldx, q, ldq, S, colsum, ws, s) : quant_rows(x, n, d, ldx, q, ldq, S, s);
+}
+
+int quant(const void* X, int type, int64_t n, int d, int64_t ldx, int transpose, bool wide, void* Q, int64_t ldq, float* S,
           float* colsum, void* ws, cudaStream_t s) {
   switch (type) {
     case GQ_F32:
-      return transpose ? quant_cols(static_cast<const float*>(X), n, d, ldx, Q, ldq, S, colsum, ws, s)
-                       : quant_rows(static_cast<const float*>(X), n, d, ldx, Q, ldq, S, s);
+      return wide ? quant_to<float, __half>(X, n, d, ldx, transpose, Q, ldq, S, colsum, ws, s)
+                  : quant_to<float, int8_t>(X, n, d, ldx, transpose, Q, ldq, S, colsum, ws, s);
     case GQ_BF16:
-      return transpose ? quant_cols(static_cast<const __nv_bfloat16*>(X), n, d, ldx, Q, ldq, S, colsum, ws, s)
-                       : quant_rows(static_cast<const __nv_bfloat16*>(X), n, d, ldx, Q, ldq, S, s);
+      return wide ? quant_to<__nv_bfloat16, __half>(X, n, d, ldx, transpose, Q, ldq, S, colsum, ws, s)
+                  : quant_to<__nv_bfloat16, int8_t>(X, n, d, ldx, transpose, Q, ldq, S, colsum, ws, s);
     default:
-      return transpose ? quant_cols(static_cast<const __half*>(X), n, d, ldx, Q, ldq, S, colsum, ws, s)
-                       : quant_rows(static_cast<const __half*>(X), n, d, ldx, Q, ldq, S, s);
+      return wide ? quant_to<__half, __half>(X, n, d, ldx, transpose, Q, ldq, S, colsum, ws, s)
+                  : quant_to<__half, int8_t>(X, n, d, ldx, transpose, Q, ldq, S, colsum, ws, s);
   }
 }
 
 constexpr int kMaxCols = 65535 * kTrCols / 2;  // quantizer's grid in y
-int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
-size_t round256(size_t x) { return (x + 255) / 256 * 256; }
-
 }  // namespace
 }  // namespace gq
 
@@ -1018,12 +1143,12 @@ extern "C" int gq_quantize_i8(const void* X, int type, int64_t n, int d, int64_t
       !aligned(scale, 4))
     return GQ_ERR_INVALID_ARG;
   if (transpose && (ws == nullptr || !aligned(ws, 16) || ws_bytes < cols_ws(n, d, 0))) return GQ_ERR_WORKSPACE;
-  return quant(X, type, n, d, ldx, transpose, Q, ldq, scale, nullptr, ws, (cudaStream_t)stream);
+  return quant(X, type, n, d, ldx, transpose, false, Q, ldq, scale, nullptr, ws, (cudaStream_t)stream);
 }
 
 extern "C" size_t gq_gemm_i8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   if (!gq::valid_shape(m, n, k) || m == 0) return 0;
-  return gq::gemm_ws(m, n, k);
+  return gq::gemm_ws(m, n, k, true, true);
 }
 
 extern "C" int gq_gemm_i8(const int8_t* A, int64_t m, int64_t lda, const float* scale_a, const int8_t* B, int64_t n,
@@ -1039,14 +1164,31 @@ extern "C" int gq_gemm_i8(const int8_t* A, int64_t m, int64_t lda, const float* 
       !aligned(B, 16) || !aligned(C, type_bytes(type)) || !aligned(scale_a, 4) || !aligned(scale_b, 4) ||
       !aligned(bias, 4) || !aligned(dev_err, 4))
     return GQ_ERR_INVALID_ARG;
-  return gemm(A, m, lda, scale_a, B, n, ldb, scale_b, k, bias, act == GQ_ACT_RELU, C, type, ldc, ws, ws_bytes, dev_err,
-              (cudaStream_t)stream);
+  cudaStream_t s = (cudaStream_t)stream;
+  Operand a{A, lda, scale_a}, b{B, ldb, scale_b};
+  if (few(m, k)) return few_gemm(a, m, b, n, k, bias, act == GQ_ACT_RELU, C, type, ldc, s);
+  const Plan z = make_plan(m, n, k);
+  const size_t need = gemm_ws(m, n, k, true, true);
+  if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned(ws, 256))) return GQ_ERR_WORKSPACE;
+  Carve w(ws, ws_bytes);
+  if (wants_wide(z, true)) {
+    void* q = w.take(code_bytes(m, k, true));
+    GQ_TRY(widen(A, m, k, lda, q, s));
+    a = Operand{q, round16(k), scale_a};
+  }
+  if (wants_wide(z, false)) {
+    void* q = w.take(code_bytes(n, k, true));
+    GQ_TRY(widen(B, n, k, ldb, q, s));
+    b = Operand{q, round16(k), scale_b};
+  }
+  return tile_gemm(z, a, b, k, bias, act == GQ_ACT_RELU, C, type, ldc, z.sums > 0 ? w.take(z.sums) : nullptr, dev_err, s);
 }
 
 extern "C" size_t gq_linear_i8_workspace_bytes(int64_t n, int k, int out) {
   using namespace gq;
   if (!valid_shape(n, out, k) || n == 0) return 0;
-  return round256((size_t)n * round16(k)) + round256((size_t)n * 4) + gemm_ws(n, out, k);
+  const bool wide = !few(n, k) && wants_wide(make_plan(n, out, k), true);
+  return code_bytes(n, k, wide) + round256((size_t)n * 4) + gemm_ws(n, out, k, false, true);
 }
 
 extern "C" int gq_linear_i8(const void* X, int type, int64_t n, int k, int64_t ldx, const int8_t* W, int out,
@@ -1063,30 +1205,70 @@ extern "C" int gq_linear_i8(const void* X, int type, int64_t n, int k, int64_t l
       !aligned(dev_err, 4))
     return GQ_ERR_INVALID_ARG;
   if (ws == nullptr || !aligned(ws, 256) || ws_bytes < gq_linear_i8_workspace_bytes(n, k, out)) return GQ_ERR_WORKSPACE;
-  Carve w(ws, ws_bytes);
-  const int64_t ldq = round16(k);
-  int8_t* q = static_cast<int8_t*>(w.take((size_t)n * ldq));
-  float* sc = static_cast<float*>(w.take((size_t)n * 4));
-  const size_t gw = gemm_ws(n, out, k);
-  void* g = gw > 0 ? w.take(gw) : nullptr;
   cudaStream_t s = (cudaStream_t)stream;
-  GQ_TRY(quant(X, type, n, k, ldx, 0, q, ldq, sc, nullptr, nullptr, s));
-  return gemm(q, n, ldq, sc, W, out, ldw, scale_w, k, bias, act == GQ_ACT_RELU, Y, y_type, ldy, g, gw, dev_err, s);
+  const int relu = act == GQ_ACT_RELU;
+  const int64_t ld = round16(k);
+  Carve w(ws, ws_bytes);
+  float* sc = static_cast<float*>(w.take((size_t)n * 4));
+  if (few(n, k)) {
+    void* q = w.take(code_bytes(n, k, false));
+    GQ_TRY(quant(X, type, n, k, ldx, 0, false, q, ld, sc, nullptr, nullptr, s));
+    return few_gemm(Operand{q, ld, sc}, n, Operand{W, ldw, scale_w}, out, k, bias, relu, Y, y_type, ldy, s);
+  }
+  const Plan z = make_plan(n, out, k);
+  const bool wide = wants_wide(z, true);
+  void* q = w.take(code_bytes(n, k, wide));
+  GQ_TRY(quant(X, type, n, k, ldx, 0, wide, q, ld, sc, nullptr, nullptr, s));
+  Operand b{W, ldw, scale_w};
+  if (wants_wide(z, false)) {
+    void* qw = w.take(code_bytes(out, k, true));
+    GQ_TRY(widen(W, out, k, ldw, qw, s));
+    b = Operand{qw, ld, scale_w};
+  }
+  return tile_gemm(z, Operand{q, ld, sc}, b, k, bias, relu, Y, y_type, ldy, z.sums > 0 ? w.take(z.sums) : nullptr, dev_err,
+                   s);
 }
 
 namespace gq {
 namespace {
+// a product of rows (or columns) of two matrices that are quantized for it
+struct Side {
+  const void* X;
+  int type;
+  int64_t n;
+  int d;
+  int64_t ldx;
+  int transpose;
+};
+size_t product_ws(int64_t m, int64_t n, int64_t k, bool ta, bool tb, bool sums) {
+  const bool tiny = few(m, k);
+  const Plan z = make_plan(m, n, k);
+  return code_bytes(m, k, !tiny && wants_wide(z, true)) + code_bytes(n, k, !tiny && wants_wide(z, false)) +
+         round256((size_t)m * 4) + round256((size_t)n * 4) + (ta ? round256(cols_ws(k, (int)m, sums)) : 0) +
+         (tb ? round256(cols_ws(k, (int)n, 0)) : 0) + (tiny ? 0 : round256(z.sums));
+}
+int product(const Side& a, const Side& b, int64_t m, int64_t n, int64_t k, float* colsum, void* C, int type, int64_t ldc,
+            void* ws, size_t ws_bytes, int* err, cudaStream_t s) {
+  const bool tiny = few(m, k);
+  const Plan z = make_plan(m, n, k);
+  const bool wa = !tiny && wants_wide(z, true), wb = !tiny && wants_wide(z, false);
+  const int64_t ld = round16(k);
+  Carve w(ws, ws_bytes);
+  void* qa = w.take(code_bytes(m, k, wa));
+  void* qb = w.take(code_bytes(n, k, wb));
+  float* sa = static_cast<float*>(w.take((size_t)m * 4));
+  float* sb = static_cast<float*>(w.take((size_t)n * 4));
+  void* ca = a.transpose ? w.take(cols_ws(a.n, a.d, colsum != nullptr)) : nullptr;
+  void* cb = b.transpose ? w.take(cols_ws(b.n, b.d, 0)) : nullptr;
+  GQ_TRY(quant(a.X, a.type, a.n, a.d, a.ldx, a.transpose, wa, qa, ld, sa, colsum, ca, s));
+  GQ_TRY(quant(b.X, b.type, b.n, b.d, b.ldx, b.transpose, wb, qb, ld, sb, nullptr, cb, s));
+  const Operand A{qa, ld, sa}, B{qb, ld, sb};
+  if (tiny) return few_gemm(A, m, B, n, k, nullptr, 0, C, type, ldc, s);
+  return tile_gemm(z, A, B, k, nullptr, 0, C, type, ldc, z.sums > 0 ? w.take(z.sums) : nullptr, err, s);
+}
 size_t bwd_ws(int64_t n, int k, int out, bool need_dx, bool need_dw) {
-  size_t dx = 0, dw = 0;
-  if (need_dx) {  // codes of dY's rows and W's columns
-    dx = round256((size_t)n * round16(out)) + round256((size_t)n * 4) + round256((size_t)k * round16(out)) +
-         round256((size_t)k * 4) + round256(cols_ws(out, k, 0)) + round256(gemm_ws(n, k, out));
-  }
-  if (need_dw) {  // codes of dY's and X's columns
-    dw = round256((size_t)out * round16(n)) + round256((size_t)out * 4) + round256((size_t)k * round16(n)) +
-         round256((size_t)k * 4) + round256(cols_ws(n, out, 1)) + round256(cols_ws(n, k, 0)) +
-         round256(gemm_ws(out, k, n));
-  }
+  const size_t dx = need_dx ? product_ws(n, k, out, false, true, false) : 0;
+  const size_t dw = need_dw ? product_ws(out, k, n, true, true, true) : 0;
   return dx > dw ? dx : dw;
 }
 }  // namespace
@@ -1126,34 +1308,11 @@ extern "C" int gq_linear_i8_bwd(const void* dY, int64_t lddy, const void* X, int
   if (dX == nullptr && dW == nullptr) return GQ_OK;
   if (ws == nullptr || !aligned(ws, 256) || ws_bytes < bwd_ws(n, k, out, dX != nullptr, dW != nullptr))
     return GQ_ERR_WORKSPACE;
-  if (dX != nullptr) {
-    Carve w(ws, ws_bytes);
-    const int64_t ld = round16(out);
-    int8_t* qy = static_cast<int8_t*>(w.take((size_t)n * ld));
-    float* sy = static_cast<float*>(w.take((size_t)n * 4));
-    int8_t* qw = static_cast<int8_t*>(w.take((size_t)k * ld));
-    float* sw = static_cast<float*>(w.take((size_t)k * 4));
-    void* cw = w.take(cols_ws(out, k, 0));
-    const size_t gw = gemm_ws(n, k, out);
-    void* g = gw > 0 ? w.take(gw) : nullptr;
-    GQ_TRY(quant(dY, type, n, out, lddy, 0, qy, ld, sy, nullptr, nullptr, s));
-    GQ_TRY(quant(W, w_type, out, k, ldw, 1, qw, ld, sw, nullptr, cw, s));
-    GQ_TRY(gemm(qy, n, ld, sy, qw, k, ld, sw, out, nullptr, 0, dX, dx_type, lddx, g, gw, dev_err, s));
-  }
-  if (dW != nullptr) {
-    Carve w(ws, ws_bytes);
-    const int64_t ld = round16(n);
-    int8_t* qy = static_cast<int8_t*>(w.take((size_t)out * ld));
-    float* sy = static_cast<float*>(w.take((size_t)out * 4));
-    int8_t* qx = static_cast<int8_t*>(w.take((size_t)k * ld));
-    float* sx = static_cast<float*>(w.take((size_t)k * 4));
-    void* cy = w.take(cols_ws(n, out, 1));
-    void* cx = w.take(cols_ws(n, k, 0));
-    const size_t gw = gemm_ws(out, k, n);
-    void* g = gw > 0 ? w.take(gw) : nullptr;
-    GQ_TRY(quant(dY, type, n, out, lddy, 1, qy, ld, sy, dbias, cy, s));
-    GQ_TRY(quant(X, type, n, k, ldx, 1, qx, ld, sx, nullptr, cx, s));
-    GQ_TRY(gemm(qy, out, ld, sy, qx, k, ld, sx, n, nullptr, 0, dW, dw_type, lddw, g, gw, dev_err, s));
-  }
+  if (dX != nullptr)  // dY by rows, W by columns
+    GQ_TRY(product(Side{dY, type, n, out, lddy, 0}, Side{W, w_type, out, k, ldw, 1}, n, k, out, nullptr, dX, dx_type, lddx,
+                   ws, ws_bytes, dev_err, s));
+  if (dW != nullptr)  // both by columns
+    GQ_TRY(product(Side{dY, type, n, out, lddy, 1}, Side{X, type, n, k, ldx, 1}, out, k, n, dbias, dW, dw_type, lddw, ws,
+                   ws_bytes, dev_err, s));
   return GQ_OK;
 }
