@@ -208,8 +208,8 @@ GQ_API int gq_linear_i8_bwd(const void* dY, int64_t lddy, const void* X, int64_t
  *   or 0 if the caller does not know; it chooses between kernels, a wrong value
  *   costs time only.  gamma, beta: d fp32; NULL: 1 and 0.  Y may be X, dX may be
  *   dY or X (same leading dimension).  Matrices: n x d of `type`, any alignment of
- *   the type; 16-byte aligned rows of a multiple of 16 bytes take the vector
- *   path.  Sums run in fp32 in a fixed order; results are rounded once.
+ *   the type; rows of a multiple of 4 values that start aligned for 4 take the
+ *   vector path.  Sums run in fp32 in a fixed order; results are rounded once.
  *   ws: gq_group_norm_workspace_bytes(n, d, groups, type, segments, max_rows,
  *   backward), 256-byte aligned; it depends on the device's SM count.
  * Errors: GQ_ERR_INVALID_ARG (bad type, act, sizes, eps; d not a multiple of

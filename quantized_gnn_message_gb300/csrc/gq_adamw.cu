@@ -33,10 +33,9 @@
 namespace gq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBlockValues = 256;                   // values that share an exponent: a warp's, 8 a lane
-constexpr int kTileBlocks = 16;                     // blocks of a thread block's tile
 constexpr int kMinExp = 16, kMaxExp = 254;          // so that every scale below is a normal fp32 number
 
 // What a step multiplies by; made on the host, or by begin_kernel from the
@@ -122,17 +121,24 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return
 template <>
 __device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
 
-// 8 consecutive values, 16-byte aligned
+// A lane's eight values of a block: 4 l .. 4 l + 3 and 128 further, so that a
+// warp's loads and stores are contiguous whatever the type.
+__device__ __forceinline__ int place(int lane, int j) { return 4 * lane + (j & 3) + (j & 4) * 32; }
 template <typename T>
 struct Raw {
   uint4 w[sizeof(T) / 2];
 };
 template <typename T>
-__device__ __forceinline__ Raw<T> load8(const void* base, int64_t i) {
+__device__ __forceinline__ Raw<T> load8(const void* base, int64_t block, int lane) {
   Raw<T> r;
-  const uint4* a = reinterpret_cast<const uint4*>(static_cast<const T*>(base) + i);
-#pragma unroll
-  for (int k = 0; k < (int)(sizeof(T) / 2); ++k) r.w[k] = a[k];
+  const T* a = static_cast<const T*>(base) + block * 256 + 4 * lane;
+  if constexpr (sizeof(T) == 4) {
+    r.w[0] = *reinterpret_cast<const uint4*>(a);
+    r.w[1] = *reinterpret_cast<const uint4*>(a + 128);
+  } else {
+    const uint2 x = *reinterpret_cast<const uint2*>(a), y = *reinterpret_cast<const uint2*>(a + 128);
+    r.w[0] = make_uint4(x.x, x.y, y.x, y.y);
+  }
   return r;
 }
 template <typename T>
@@ -142,14 +148,28 @@ __device__ __forceinline__ void unpack8(const Raw<T>& r, float (&x)[8]) {
   for (int j = 0; j < 8; ++j) x[j] = to_f(e[j]);
 }
 template <typename T>
-__device__ __forceinline__ void store8(void* base, int64_t i, const float (&x)[8]) {
+__device__ __forceinline__ void store8(void* base, int64_t block, int lane, const float (&x)[8]) {
   Raw<T> r;
   T* e = reinterpret_cast<T*>(&r);
 #pragma unroll
   for (int j = 0; j < 8; ++j) e[j] = from_f<T>(x[j]);
-  uint4* a = reinterpret_cast<uint4*>(static_cast<T*>(base) + i);
-#pragma unroll
-  for (int k = 0; k < (int)(sizeof(T) / 2); ++k) a[k] = r.w[k];
+  T* a = static_cast<T*>(base) + block * 256 + 4 * lane;
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<uint4*>(a) = r.w[0];
+    *reinterpret_cast<uint4*>(a + 128) = r.w[1];
+  } else {
+    *reinterpret_cast<uint2*>(a) = make_uint2(r.w[0].x, r.w[0].y);
+    *reinterpret_cast<uint2*>(a + 128) = make_uint2(r.w[0].z, r.w[0].w);
+  }
+}
+__device__ __forceinline__ uint2 load8c(const void* base, int64_t block, int lane) {
+  const uint32_t* a = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(base) + block * 256) + lane;
+  return make_uint2(a[0], a[32]);
+}
+__device__ __forceinline__ void store8c(void* base, int64_t block, int lane, uint2 w) {
+  uint32_t* a = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(base) + block * 256) + lane;
+  a[0] = w.x;
+  a[32] = w.y;
 }
 
 // ------------------------------------------------------------ 8-bit floats --
@@ -236,55 +256,27 @@ __device__ __forceinline__ void update(float2& p, float2 g, float2& m, float2& v
   p = fma2(p, both(c.keep), step);
 }
 
-// One warp, one block of 256 values: lane l holds values 8 l .. 8 l + 7.
+// What a lane holds of a block, as loaded.
 template <typename TP, typename TG, bool SMALL>
-__device__ __forceinline__ void block_step(const Tensor& t, int64_t b, int lane, const Coef& c, float gs) {
-  const int64_t i0 = b * kBlockValues + lane * 8;
-  alignas(16) float p[8], g[8], m[8], v[8];
-  const bool whole = t.vec && (b + 1) * kBlockValues <= t.n;
-  const int live = i0 >= t.n ? 0 : (int)min((int64_t)8, t.n - i0);
-  uint2 mc = make_uint2(0, 0), vc = make_uint2(0, 0);
-  if (whole) {
-    const Raw<TP> rp = load8<TP>(t.p, i0);
-    const Raw<TG> rg = load8<TG>(t.g, i0);
-    if (SMALL) {
-      mc = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + i0);
-      vc = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + i0);
-    } else {
-      unpack8<float>(load8<float>(t.m, i0), m);
-      unpack8<float>(load8<float>(t.v, i0), v);
-    }
-    unpack8<TP>(rp, p);
-    unpack8<TG>(rg, g);
-  } else {
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      p[j] = g[j] = m[j] = v[j] = 0.0f;
-      if (j < live) {
-        const int64_t i = i0 + j;
-        const int64_t r = t.cols == t.n ? 0 : i / t.cols, col = i - r * t.cols;
-        p[j] = to_f(static_cast<const TP*>(t.p)[r * t.ldp + col]);
-        g[j] = to_f(static_cast<const TG*>(t.g)[r * t.ldg + col]);
-        if (SMALL) {
-          w[j >> 2] |= (uint32_t) static_cast<const uint8_t*>(t.m)[i] << (8 * (j & 3));
-          w[2 + (j >> 2)] |= (uint32_t) static_cast<const uint8_t*>(t.v)[i] << (8 * (j & 3));
-        } else {
-          m[j] = static_cast<const float*>(t.m)[i];
-          v[j] = static_cast<const float*>(t.v)[i];
-        }
-      }
-    }
-    mc = make_uint2(w[0], w[1]);
-    vc = make_uint2(w[2], w[3]);
-  }
+struct Held {
+  Raw<TP> p;
+  Raw<TG> g;
+  Raw<float> m, v;       // 32-bit moments
+  uint2 mc, vc;          // 8-bit ones
+  int em, ev;
+};
+
+// The arithmetic of a lane's eight values; mc, vc, em, ev are replaced by the new ones.
+template <bool SMALL>
+__device__ __forceinline__ void step8(float (&p)[8], float (&g)[8], float (&m)[8], float (&v)[8], uint2& mc, uint2& vc,
+                                      int& em, int& ev, uint32_t block, int lane, const Coef& c, float gs) {
   float2* p2 = reinterpret_cast<float2*>(p);
   float2* g2 = reinterpret_cast<float2*>(g);
   float2* m2 = reinterpret_cast<float2*>(m);
   float2* v2 = reinterpret_cast<float2*>(v);
   if (SMALL) {
-    const float dm = Code<false>::down(min(max((int)t.me[b], kMinExp), kMaxExp));
-    const float dv = Code<true>::down(min(max((int)t.ve[b], kMinExp), kMaxExp));
+    const float dm = Code<false>::down(min(max(em, kMinExp), kMaxExp));
+    const float dv = Code<true>::down(min(max(ev, kMinExp), kMaxExp));
     decode4<false>(mc.x, dm, m2[0], m2[1]);
     decode4<false>(mc.y, dm, m2[2], m2[3]);
     decode4<true>(vc.x, dv, v2[0], v2[1]);
@@ -299,49 +291,111 @@ __device__ __forceinline__ void block_step(const Tensor& t, int64_t b, int lane,
       bm = max(bm, __float_as_uint(m[j]) & 0x7FFFFFFFu);
       bv = max(bv, __float_as_uint(v[j]) & 0x7FFFFFFFu);
     }
-    const int em = block_exp(bm), ev = block_exp(bv);
+    em = block_exp(bm);
+    ev = block_exp(bv);
     const float um = Code<false>::up(em), uv = Code<true>::up(ev);
-    const uint32_t kr = row_key(c.key, t.block0 + (uint32_t)b) + (uint32_t)lane * (8u * 0x9E3779B9u);
+    const uint32_t kr = row_key(c.key, block) + (uint32_t)lane * (4u * 0x9E3779B9u);
     uint32_t h[2][4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) h[j >> 2][j & 3] = fmix32(kr + (uint32_t)j * 0x9E3779B9u);
+    for (int j = 0; j < 8; ++j) h[j >> 2][j & 3] = fmix32(kr + (uint32_t)place(0, j) * 0x9E3779B9u);
     mc = make_uint2(encode4<false>(m2[0], m2[1], um, h[0]), encode4<false>(m2[2], m2[3], um, h[1]));
     vc = make_uint2(encode4<true>(v2[0], v2[1], uv, h[0]), encode4<true>(v2[2], v2[3], uv, h[1]));
-    if (lane == 0) {
-      t.me[b] = (uint8_t)em;
-      t.ve[b] = (uint8_t)ev;
-    }
   }
-  if (whole) {
-    store8<TP>(t.p, i0, p);
-    if (SMALL) {
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + i0) = mc;
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + i0) = vc;
-    } else {
-      store8<float>(t.m, i0, m);
-      store8<float>(t.v, i0, v);
+}
+
+template <typename TP, typename TG, bool SMALL>
+__device__ __forceinline__ void take(const Tensor& t, int64_t b, int lane, Held<TP, TG, SMALL>& w) {
+  w.p = load8<TP>(t.p, b, lane);
+  w.g = load8<TG>(t.g, b, lane);
+  if constexpr (SMALL) {
+    w.mc = load8c(t.m, b, lane);
+    w.vc = load8c(t.v, b, lane);
+    w.em = t.me[b];
+    w.ev = t.ve[b];
+  } else {
+    w.m = load8<float>(t.m, b, lane);
+    w.v = load8<float>(t.v, b, lane);
+  }
+}
+
+template <typename TP, typename TG, bool SMALL>
+__device__ __forceinline__ void work(const Tensor& t, int64_t b, int lane, Held<TP, TG, SMALL>& w, const Coef& c, float gs) {
+  alignas(16) float p[8], g[8], m[8], v[8];
+  unpack8<TP>(w.p, p);
+  unpack8<TG>(w.g, g);
+  if constexpr (!SMALL) {
+    unpack8<float>(w.m, m);
+    unpack8<float>(w.v, v);
+  }
+  step8<SMALL>(p, g, m, v, w.mc, w.vc, w.em, w.ev, t.block0 + (uint32_t)b, lane, c, gs);
+  store8<TP>(t.p, b, lane, p);
+  if constexpr (SMALL) {
+    store8c(t.m, b, lane, w.mc);
+    store8c(t.v, b, lane, w.vc);
+    if (lane == 0) {
+      t.me[b] = (uint8_t)w.em;
+      t.ve[b] = (uint8_t)w.ev;
     }
   } else {
+    store8<float>(t.m, b, lane, m);
+    store8<float>(t.v, b, lane, v);
+  }
+}
+
+// A block that is not whole, not aligned or not dense, value by value.
+template <typename TP, typename TG, bool SMALL>
+__device__ __forceinline__ void ragged(const Tensor& t, int64_t b, int lane, const Coef& c, float gs) {
+  const int64_t i0 = b * kBlockValues;
+  alignas(16) float p[8], g[8], m[8], v[8];
+  uint32_t w[4] = {0, 0, 0, 0};
+  const bool dense = t.cols == t.n;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j < live) {
-        const int64_t i = i0 + j;
-        const int64_t r = t.cols == t.n ? 0 : i / t.cols, col = i - r * t.cols;
-        static_cast<TP*>(t.p)[r * t.ldp + col] = from_f<TP>(p[j]);
-        if (SMALL) {
-          static_cast<uint8_t*>(t.m)[i] = (uint8_t)((j < 4 ? mc.x : mc.y) >> (8 * (j & 3)));
-          static_cast<uint8_t*>(t.v)[i] = (uint8_t)((j < 4 ? vc.x : vc.y) >> (8 * (j & 3)));
-        } else {
-          static_cast<float*>(t.m)[i] = m[j];
-          static_cast<float*>(t.v)[i] = v[j];
-        }
+  for (int j = 0; j < 8; ++j) {
+    p[j] = g[j] = m[j] = v[j] = 0.0f;
+    const int64_t i = i0 + place(lane, j);
+    if (i < t.n) {
+      const int64_t r = dense ? 0 : i / t.cols, col = i - r * t.cols;
+      p[j] = to_f(static_cast<const TP*>(t.p)[r * t.ldp + col]);
+      g[j] = to_f(static_cast<const TG*>(t.g)[r * t.ldg + col]);
+      if (SMALL) {
+        w[j >> 2] |= (uint32_t) static_cast<const uint8_t*>(t.m)[i] << (8 * (j & 3));
+        w[2 + (j >> 2)] |= (uint32_t) static_cast<const uint8_t*>(t.v)[i] << (8 * (j & 3));
+      } else {
+        m[j] = static_cast<const float*>(t.m)[i];
+        v[j] = static_cast<const float*>(t.v)[i];
+      }
+    }
+  }
+  uint2 mc = make_uint2(w[0], w[1]), vc = make_uint2(w[2], w[3]);
+  int em = SMALL ? t.me[b] : 0, ev = SMALL ? t.ve[b] : 0;
+  step8<SMALL>(p, g, m, v, mc, vc, em, ev, t.block0 + (uint32_t)b, lane, c, gs);
+  if (SMALL && lane == 0) {
+    t.me[b] = (uint8_t)em;
+    t.ve[b] = (uint8_t)ev;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int64_t i = i0 + place(lane, j);
+    if (i < t.n) {
+      const int64_t r = dense ? 0 : i / t.cols, col = i - r * t.cols;
+      static_cast<TP*>(t.p)[r * t.ldp + col] = from_f<TP>(p[j]);
+      if (SMALL) {
+        static_cast<uint8_t*>(t.m)[i] = (uint8_t)((j < 4 ? mc.x : mc.y) >> (8 * (j & 3)));
+        static_cast<uint8_t*>(t.v)[i] = (uint8_t)((j < 4 ? vc.x : vc.y) >> (8 * (j & 3)));
+      } else {
+        static_cast<float*>(t.m)[i] = m[j];
+        static_cast<float*>(t.v)[i] = v[j];
       }
     }
   }
 }
 
+// A block a warp, and as many warps as 48 registers a thread allow: what hides the
+// reads is other warps.  145 M fp32 values with 8-bit moments: 395 us, 6.2 TB/s
+// with 40 warps an SM; 415 us with 32, 440 with 48 (spills), 655 with 24 that
+// each read their next block while they work on one.
 template <typename TP, typename TG, bool SMALL, int CAP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 10)
     adamw_kernel(const __grid_constant__ Batch<CAP> batch, const Coef host, const DevRecord* rec, const float* gscale) {
   grid_wait();
   float gs = 1.0f;
@@ -361,12 +415,13 @@ __global__ void __launch_bounds__(kThreads)
   }
   const Tensor& t = batch.t[lo];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t first = (tile - t.tile0) * kTileBlocks;
-  const int64_t blocks = (t.n + kBlockValues - 1) / kBlockValues;
-#pragma unroll 2
-  for (int k = 0; k < kTileBlocks; k += kWarps) {
-    const int64_t b = first + k + warp;
-    if (b < blocks) block_step<TP, TG, SMALL>(t, b, lane, c, gs);
+  const int64_t b = (tile - t.tile0) * kWarps + warp;
+  if (t.vec && (b + 1) * kBlockValues <= t.n) {
+    Held<TP, TG, SMALL> w;
+    take(t, b, lane, w);
+    work(t, b, lane, w, c, gs);
+  } else if (b * kBlockValues < t.n) {
+    ragged<TP, TG, SMALL>(t, b, lane, c, gs);
   }
 }
 
@@ -375,19 +430,22 @@ template <typename T, bool SECOND>
 __global__ void __launch_bounds__(kThreads)
     moment_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ exps, int64_t n, T* __restrict__ out,
                   int vec) {
-  const int64_t i0 = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 8;
-  if (i0 >= n) return;
-  const float s = Code<SECOND>::down(min(max((int)exps[i0 / kBlockValues], kMinExp), kMaxExp));
-  float2 x[4];
-  if (vec && i0 + 8 <= n) {
-    const uint2 c = *reinterpret_cast<const uint2*>(codes + i0);
-    decode4<SECOND>(c.x, s, x[0], x[1]);
-    decode4<SECOND>(c.y, s, x[2], x[3]);
-    store8<T>(out, i0, reinterpret_cast<const float(&)[8]>(x));
-  } else {
-    for (int64_t i = i0; i < n && i < i0 + 8; ++i) {
-      decode4<SECOND>(codes[i], s, x[0], x[1]);
-      out[i] = from_f<T>(x[0].x);
+  const int lane = threadIdx.x & 31;
+  const int64_t blocks = (n + kBlockValues - 1) / kBlockValues;
+  for (int64_t b = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); b < blocks; b += (int64_t)gridDim.x * kWarps) {
+    const float s = Code<SECOND>::down(min(max((int)exps[b], kMinExp), kMaxExp));
+    alignas(16) float x[8];
+    float2* x2 = reinterpret_cast<float2*>(x);
+    if (vec && (b + 1) * kBlockValues <= n) {
+      const uint2 c = load8c(codes, b, lane);
+      decode4<SECOND>(c.x, s, x2[0], x2[1]);
+      decode4<SECOND>(c.y, s, x2[2], x2[3]);
+      store8<T>(out, b, lane, x);
+    } else {
+      for (int j = lane; j < kBlockValues && b * kBlockValues + j < n; j += 32) {
+        decode4<SECOND>(codes[b * kBlockValues + j], s, x2[0], x2[1]);
+        out[b * kBlockValues + j] = from_f<T>(x[0]);
+      }
     }
   }
 }
@@ -440,7 +498,7 @@ int run(const gq_adamw_tensor* ts, int count, int pt, int gt, int bits, const Co
   for (int i = 0; i < count; ++i) {
     const gq_adamw_tensor& t = ts[i];
     if (t.n > 0) {
-      const int64_t per = (int64_t)kTileBlocks * kBlockValues, add = (t.n + per - 1) / per;
+      const int64_t per = (int64_t)kWarps * kBlockValues, add = (t.n + per - 1) / per;
       if (tiles + add > 0x7fffffff && b.count > 0) {
         GQ_TRY(launch_p<CAP>(pt, gt, bits, b, tiles, c, rec, gs, s));
         b.count = 0;
@@ -499,8 +557,8 @@ int check(const gq_adamw_tensor* ts, int count, int pt, int gt, int bits, const 
 
 template <typename T>
 int moment(const uint8_t* codes, const uint8_t* exps, int64_t n, int second, T* out, cudaStream_t s) {
-  const int64_t blocks = (n + 8 * kThreads - 1) / (8 * kThreads);
-  if (blocks > 0x7fffffff) return GQ_ERR_UNSUPPORTED;
+  const int64_t tiles = (n + kWarps * kBlockValues - 1) / (kWarps * kBlockValues), most = 16 * (int64_t)sm_count();
+  const int64_t blocks = tiles < most ? tiles : most;
   const int vec = aligned(codes, 8) && aligned(out, 16);
   if (second)
     moment_kernel<T, true><<<(unsigned)blocks, kThreads, 0, s>>>(codes, exps, n, out, vec);

@@ -9,18 +9,18 @@
 //
 // Everything is bound by memory.  Two forms:
 //
-//   short segments  one block a segment reads its rows, makes the statistics and
-//                   reads the rows again, from L1 or L2: DRAM sees x once.  The
-//                   backward blocks take several segments and keep their
-//                   sums of dgamma and dbeta.
+//   short segments  one block (or, for the smallest, one warp) a segment reads its
+//                   rows, makes the statistics and reads the rows again, from L1
+//                   or L2: DRAM sees x once.  The backward pass's take several
+//                   segments and keep their sums of dgamma and dbeta.
 //   long segments   three launches: statistics of pieces (a chunk of rows cut at
 //                   segment borders), their combination, and the rows again.  A piece's
 //                   number is chunk + segment: neither falls along the rows and
 //                   one of them grows from piece to piece, so the numbers are
 //                   distinct and every kernel finds them without a table.
 //
-// A thread owns 16 bytes of channels and walks rows, so groups of any width are
-// met only when channels' sums are put together.  Variances are sums of squares
+// A thread owns four channels (one where rows are not aligned for that) and walks
+// rows, so groups of any width are met only when channels' sums are put together.  Variances are sums of squares
 // around the first value that a thread meets, then around the mean of the parts:
 // no difference of large squares.  All sums run in fp32 in a fixed order.
 #include <cuda_bf16.h>
@@ -36,7 +36,7 @@
 namespace gq {
 namespace {
 
-constexpr int kMaxThreads = 512;
+constexpr int kThreads = 256;
 
 struct Args {
   const void* X;
@@ -52,10 +52,11 @@ struct Args {
   float* mean;
   float* rstd;
   int vpr, tx, ry;       // vectors of a row, of a slab's row; rows at a time
+  int lpg;               // lanes that put a group's channels together: a power of two
   // long segments
   int64_t rows_per, chunks;
   float2* part;          // [chunks + s][d]
-  float2* hsum;          // backward: [s][groups] means of h and h xhat
+  float2* hsum;          // backward: [s][groups] means of h and h xhat, negated
   float2* tot;           // backward: [chunks or blocks][d] sums of dz xhat and dz
   int64_t parts;
   float* dgamma;
@@ -87,47 +88,150 @@ __device__ __forceinline__ int64_t first_segment(const Args& p, int64_t r) {
 }
 
 // ------------------------------------------------------------------- types --
-template <typename T, int V>
-__device__ __forceinline__ void load(const void* base, int64_t i, float (&x)[V]) {
-  if (V == 1) {
-    x[0] = (float)static_cast<const T*>(base)[i];
+// V = 4 or 1 values, two at a time where there are four
+template <int V>
+struct Pk {
+  alignas(4 * V) float e[V];
+};
+template <int V>
+__device__ __forceinline__ float2& two(Pk<V>& a, int k) { return reinterpret_cast<float2*>(a.e)[k]; }
+template <int V>
+__device__ __forceinline__ const float2& two(const Pk<V>& a, int k) { return reinterpret_cast<const float2*>(a.e)[k]; }
+template <int V>
+__device__ __forceinline__ Pk<V> add(const Pk<V>& a, const Pk<V>& b) {
+  Pk<V> r;
+  if constexpr (V == 1) {
+    r.e[0] = a.e[0] + b.e[0];
   } else {
-    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const T*>(base) + i);
-    const T* e = reinterpret_cast<const T*>(&w);
 #pragma unroll
-    for (int k = 0; k < V; ++k) x[k] = (float)e[k];
+    for (int k = 0; k < V / 2; ++k) two(r, k) = add2(two(a, k), two(b, k));
   }
+  return r;
+}
+template <int V>
+__device__ __forceinline__ Pk<V> mul(const Pk<V>& a, const Pk<V>& b) {
+  Pk<V> r;
+  if constexpr (V == 1) {
+    r.e[0] = a.e[0] * b.e[0];
+  } else {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) two(r, k) = mul2(two(a, k), two(b, k));
+  }
+  return r;
+}
+template <int V>
+__device__ __forceinline__ Pk<V> fma(const Pk<V>& a, const Pk<V>& b, const Pk<V>& c) {
+  Pk<V> r;
+  if constexpr (V == 1) {
+    r.e[0] = fmaf(a.e[0], b.e[0], c.e[0]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) two(r, k) = fma2(two(a, k), two(b, k), two(c, k));
+  }
+  return r;
+}
+template <int V>
+__device__ __forceinline__ Pk<V> all(float x) {
+  Pk<V> r;
+#pragma unroll
+  for (int k = 0; k < V; ++k) r.e[k] = x;
+  return r;
+}
+template <int V>
+__device__ __forceinline__ Pk<V> neg(const Pk<V>& a) {
+  Pk<V> r;
+#pragma unroll
+  for (int k = 0; k < V; ++k) r.e[k] = -a.e[k];
+  return r;
+}
+
+// raw values of a row, as loaded
+template <typename T, int V>
+struct Raw {
+  alignas(sizeof(T) * V) T e[V];
+};
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load(const void* base, int64_t i) {
+  Raw<T, V> r;
+  const T* a = static_cast<const T*>(base) + i;
+  if constexpr (V == 1)
+    r.e[0] = *a;
+  else if constexpr (sizeof(T) == 4)
+    *reinterpret_cast<uint4*>(r.e) = *reinterpret_cast<const uint4*>(a);
+  else
+    *reinterpret_cast<uint2*>(r.e) = *reinterpret_cast<const uint2*>(a);
+  return r;
+}
+template <typename T, int V>
+__device__ __forceinline__ Pk<V> value(const Raw<T, V>& r) {
+  Pk<V> x;
+#pragma unroll
+  for (int k = 0; k < V; ++k) x.e[k] = (float)r.e[k];
+  return x;
 }
 __device__ __forceinline__ void put(float& o, float x) { o = x; }
 __device__ __forceinline__ void put(__nv_bfloat16& o, float x) { o = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void put(__half& o, float x) { o = __float2half_rn(x); }
 template <typename T, int V>
-__device__ __forceinline__ void store(void* base, int64_t i, const float (&x)[V]) {
-  if (V == 1) {
-    put(static_cast<T*>(base)[i], x[0]);
-  } else {
-    uint4 w;
-    T* e = reinterpret_cast<T*>(&w);
+__device__ __forceinline__ void store(void* base, int64_t i, const Pk<V>& x) {
+  Raw<T, V> r;
 #pragma unroll
-    for (int k = 0; k < V; ++k) put(e[k], x[k]);
-    *reinterpret_cast<uint4*>(static_cast<T*>(base) + i) = w;
-  }
+  for (int k = 0; k < V; ++k) put(r.e[k], x.e[k]);
+  T* a = static_cast<T*>(base) + i;
+  if constexpr (V == 1)
+    *a = r.e[0];
+  else if constexpr (sizeof(T) == 4)
+    *reinterpret_cast<uint4*>(a) = *reinterpret_cast<const uint4*>(r.e);
+  else
+    *reinterpret_cast<uint2*>(a) = *reinterpret_cast<const uint2*>(r.e);
 }
 
-// 1 / (1 + e^-z); 0 and 1 where e^-z leaves fp32's range
-__device__ __forceinline__ float sigmoid(float z) { return __frcp_rn(1.0f + __expf(-z)); }
-template <int ACT>
-__device__ __forceinline__ float activate(float z) {
-  return ACT == GQ_ACT_RELU ? (z > 0.0f ? z : 0.0f) : ACT == GQ_ACT_SILU ? z * sigmoid(z) : z;
+// 1 / (1 + e^-z) by the special function unit's 2^x and 1 / x (each within two
+// steps): off by u (8 + 2 |z|) of itself at most.  0 and 1 where e^-z leaves
+// fp32's range.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
-template <int ACT>
-__device__ __forceinline__ float derivative(float z) {
-  if (ACT == GQ_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
-  if (ACT == GQ_ACT_SILU) {
-    const float g = sigmoid(z);
-    return g * fmaf(z, 1.0f - g, 1.0f);
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <int V>
+__device__ __forceinline__ Pk<V> sigmoid(const Pk<V>& z) {
+  Pk<V> t = mul(z, all<V>(-1.4426950408889634f));
+#pragma unroll
+  for (int k = 0; k < V; ++k) t.e[k] = ex2(t.e[k]);
+  t = add(t, all<V>(1.0f));
+#pragma unroll
+  for (int k = 0; k < V; ++k) t.e[k] = rcp(t.e[k]);
+  return t;
+}
+template <int ACT, int V>
+__device__ __forceinline__ Pk<V> activate(const Pk<V>& z) {
+  if constexpr (ACT == GQ_ACT_SILU) return mul(z, sigmoid(z));
+  Pk<V> y = z;
+  if constexpr (ACT == GQ_ACT_RELU) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) y.e[k] = z.e[k] > 0.0f ? z.e[k] : 0.0f;
   }
-  return 1.0f;
+  return y;
+}
+// dy act'(z)
+template <int ACT, int V>
+__device__ __forceinline__ Pk<V> slope(const Pk<V>& dy, const Pk<V>& z) {
+  if constexpr (ACT == GQ_ACT_SILU) {
+    const Pk<V> g = sigmoid(z);
+    return mul(mul(dy, g), fma(z, fma(g, all<V>(-1.0f), all<V>(1.0f)), all<V>(1.0f)));
+  }
+  Pk<V> d = dy;
+  if constexpr (ACT == GQ_ACT_RELU) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) d.e[k] = z.e[k] > 0.0f ? dy.e[k] : 0.0f;
+  }
+  return d;
 }
 
 __device__ __forceinline__ float warp_sum(float x) {
@@ -135,122 +239,159 @@ __device__ __forceinline__ float warp_sum(float x) {
   for (int k = 16; k > 0; k >>= 1) x += __shfl_xor_sync(FULL, x, k);
   return x;
 }
+// over groups of `lanes` lanes
+__device__ __forceinline__ float lane_sum(float x, int lanes) {
+  for (int k = lanes >> 1; k > 0; k >>= 1) x += __shfl_xor_sync(FULL, x, k);
+  return x;
+}
 
 // ---------------------------------------------------------- sums of a piece --
+// Several rows are read before the first is used (and, where the output may be
+// an input, before the first is written: the compiler cannot move a read ahead
+// of a write by itself).
+template <int V>
+struct Ahead {
+  static constexpr int sums = 8, sums_bwd = 4, fwd = V == 1 ? 8 : 4, bwd = V == 1 ? 8 : 4;
+};
+
 // Rows [r0, r1) of one thread's channels: mean and sum of squares around it.
 template <typename T, int V>
-__device__ __forceinline__ void spread(const Args& p, int64_t r0, int64_t r1, int ry, int c, float (&mean)[V],
-                                       float (&m2)[V], int& rows) {
-  float k[V], s[V], q[V];
+__device__ __forceinline__ void spread(const Args& p, int64_t r0, int64_t r1, int ry, int c, Pk<V>& mean, Pk<V>& m2) {
+  constexpr int U = Ahead<V>::sums;
+  Pk<V> k = all<V>(0.0f), s = k, q = k;
+  const int64_t first = r0 + ry;
+  const int rows = first < r1 ? (int)((r1 - first + p.ry - 1) / p.ry) : 0;
+  if (rows > 0) k = neg(value(load<T, V>(p.X, first * p.ldx + c)));
+  const T* x = static_cast<const T*>(p.X) + first * p.ldx + c;
+  const int64_t step = (int64_t)p.ry * p.ldx;
+  int i = 0;
+  for (; i + U <= rows; i += U) {
+    Raw<T, V> w[U];
 #pragma unroll
-  for (int e = 0; e < V; ++e) k[e] = s[e] = q[e] = 0.0f;
-  int64_t r = r0 + ry;
-  rows = r < r1 ? (int)((r1 - r + p.ry - 1) / p.ry) : 0;
-  if (rows > 0) load<T, V>(p.X, r * p.ldx + c, k);
-#pragma unroll 4
-  for (int i = 0; i < rows; ++i, r += p.ry) {
-    float x[V];
-    load<T, V>(p.X, r * p.ldx + c, x);
+    for (int u = 0; u < U; ++u) w[u] = load<T, V>(x, u * step);
+    x += U * step;
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float y = x[e] - k[e];
-      s[e] += y;
-      q[e] = fmaf(y, y, q[e]);
+    for (int u = 0; u < U; ++u) {
+      const Pk<V> y = add(value(w[u]), k);
+      s = add(s, y);
+      q = fma(y, y, q);
     }
+  }
+  for (; i < rows; ++i, x += step) {
+    const Pk<V> y = add(value(load<T, V>(x, 0)), k);
+    s = add(s, y);
+    q = fma(y, y, q);
   }
   const float inv = rows > 0 ? 1.0f / (float)rows : 0.0f;
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    const float m = s[e] * inv;
-    mean[e] = k[e] + m;
-    m2[e] = fmaxf(fmaf(-s[e], m, q[e]), 0.0f);
+    const float m = s.e[e] * inv;
+    mean.e[e] = m - k.e[e];
+    m2.e[e] = fmaxf(fmaf(-s.e[e], m, q.e[e]), 0.0f);
+    if (!(q.e[e] == q.e[e])) m2.e[e] = q.e[e];  // fmaxf would drop a NaN
   }
 }
 
-// What the backward pass needs of a thread's channels.
+// What the backward pass needs of a thread's channels (mean negated).
 template <int V>
 struct Chan {
-  float mu[V], rs[V], ga[V], be[V];
+  Pk<V> mu, rs, ga, be;
 };
 template <int V>
 __device__ __forceinline__ void channels(const Args& p, int64_t j, int c, Chan<V>& h) {
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     const int64_t g = j * p.groups + (c + e) / p.cg;
-    h.mu[e] = p.mean[g];
-    h.rs[e] = p.rstd[g];
-    h.ga[e] = p.gamma != nullptr ? p.gamma[c + e] : 1.0f;
-    h.be[e] = p.beta != nullptr ? p.beta[c + e] : 0.0f;
+    h.mu.e[e] = -p.mean[g];
+    h.rs.e[e] = p.rstd[g];
+    h.ga.e[e] = p.gamma != nullptr ? p.gamma[c + e] : 1.0f;
+    h.be.e[e] = p.beta != nullptr ? p.beta[c + e] : 0.0f;
   }
 }
 
 // sums of dz xhat and of dz
 template <typename T, int V, int ACT>
-__device__ __forceinline__ void slopes(const Args& p, int64_t r0, int64_t r1, int ry, int c, const Chan<V>& h,
-                                       float (&a)[V], float (&b)[V]) {
+__device__ __forceinline__ void slopes(const Args& p, int64_t r0, int64_t r1, int ry, int c, const Chan<V>& h, Pk<V>& a,
+                                       Pk<V>& b) {
+  constexpr int U = Ahead<V>::sums_bwd;
+  a = b = all<V>(0.0f);
+  const int64_t first = r0 + ry;
+  const int rows = first < r1 ? (int)((r1 - first + p.ry - 1) / p.ry) : 0;
+  const T* x = static_cast<const T*>(p.X) + first * p.ldx + c;
+  const T* y = static_cast<const T*>(p.dY) + first * p.lddy + c;
+  const int64_t sx = (int64_t)p.ry * p.ldx, sy = (int64_t)p.ry * p.lddy;
+  auto use = [&](const Raw<T, V>& wx, const Raw<T, V>& wy) {
+    const Pk<V> xh = mul(add(value(wx), h.mu), h.rs);
+    const Pk<V> dz = ACT == GQ_ACT_NONE ? value(wy) : slope<ACT>(value(wy), fma(xh, h.ga, h.be));
+    a = fma(dz, xh, a);
+    b = add(b, dz);
+  };
+  int i = 0;
+  for (; i + U <= rows; i += U) {
+    Raw<T, V> wx[U], wy[U];
 #pragma unroll
-  for (int e = 0; e < V; ++e) a[e] = b[e] = 0.0f;
-#pragma unroll 4
-  for (int64_t r = r0 + ry; r < r1; r += p.ry) {
-    float x[V], y[V];
-    load<T, V>(p.X, r * p.ldx + c, x);
-    load<T, V>(p.dY, r * p.lddy + c, y);
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float xh = (x[e] - h.mu[e]) * h.rs[e];
-      const float dz = ACT == GQ_ACT_NONE ? y[e] : y[e] * derivative<ACT>(fmaf(xh, h.ga[e], h.be[e]));
-      a[e] = fmaf(dz, xh, a[e]);
-      b[e] += dz;
+    for (int u = 0; u < U; ++u) {
+      wx[u] = load<T, V>(x, u * sx);
+      wy[u] = load<T, V>(y, u * sy);
     }
+    x += U * sx;
+    y += U * sy;
+#pragma unroll
+    for (int u = 0; u < U; ++u) use(wx[u], wy[u]);
   }
+  for (; i < rows; ++i, x += sx, y += sy) use(load<T, V>(x, 0), load<T, V>(y, 0));
 }
 
-// Several rows are read before the first is written: the output may be an input,
-// so the compiler cannot move a read ahead of a write by itself.
-constexpr int kAhead = 4, kAheadBwd = 2;
-
 template <typename T, int V, int ACT>
-__device__ __forceinline__ void apply(const Args& p, int64_t r0, int64_t r1, int ry, int c, const float (&mu)[V],
-                                      const float (&sc)[V], const float (&be)[V]) {
-  for (int64_t r = r0 + ry; r < r1; r += kAhead * p.ry) {
-    float x[kAhead][V];
+__device__ __forceinline__ void apply(const Args& p, int64_t r0, int64_t r1, int ry, int c, const Pk<V>& mu, const Pk<V>& sc,
+                                      const Pk<V>& be) {
+  constexpr int U = Ahead<V>::fwd;
+  const int64_t first = r0 + ry;
+  const int rows = first < r1 ? (int)((r1 - first + p.ry - 1) / p.ry) : 0;
+  const T* x = static_cast<const T*>(p.X) + first * p.ldx + c;
+  T* o = static_cast<T*>(p.Y) + first * p.ldy + c;
+  const int64_t sx = (int64_t)p.ry * p.ldx, so = (int64_t)p.ry * p.ldy;
+  for (int i = 0; i < rows; i += U) {
+    Raw<T, V> w[U];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (r + u * p.ry < r1) load<T, V>(p.X, (r + u * p.ry) * p.ldx + c, x[u]);
+    for (int u = 0; u < U; ++u)
+      if (i + u < rows) w[u] = load<T, V>(x, u * sx);
+    x += U * sx;
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (r + u * p.ry < r1) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) x[u][e] = activate<ACT>(fmaf(x[u][e] - mu[e], sc[e], be[e]));
-        store<T, V>(p.Y, (r + u * p.ry) * p.ldy + c, x[u]);
-      }
-    }
+    for (int u = 0; u < U; ++u)
+      if (i + u < rows) store<T, V>(o, u * so, activate<ACT>(fma(add(value(w[u]), mu), sc, be)));
+    o += U * so;
   }
 }
 
 template <typename T, int V, int ACT>
 __device__ __forceinline__ void apply_bwd(const Args& p, int64_t r0, int64_t r1, int ry, int c, const Chan<V>& h,
-                                          const float (&h1)[V], const float (&h2)[V]) {
-  for (int64_t r = r0 + ry; r < r1; r += kAheadBwd * p.ry) {
-    float x[kAheadBwd][V], y[kAheadBwd][V];
+                                          const Pk<V>& h1, const Pk<V>& h2) {  // the means of h and h xhat, negated
+  constexpr int U = Ahead<V>::bwd;
+  const int64_t first = r0 + ry;
+  const int rows = first < r1 ? (int)((r1 - first + p.ry - 1) / p.ry) : 0;
+  const T* x = static_cast<const T*>(p.X) + first * p.ldx + c;
+  const T* y = static_cast<const T*>(p.dY) + first * p.lddy + c;
+  T* o = static_cast<T*>(p.Y) + first * p.ldy + c;
+  const int64_t sx = (int64_t)p.ry * p.ldx, sy = (int64_t)p.ry * p.lddy, so = (int64_t)p.ry * p.ldy;
+  for (int i = 0; i < rows; i += U) {
+    Raw<T, V> wx[U], wy[U];
 #pragma unroll
-    for (int u = 0; u < kAheadBwd; ++u)
-      if (r + u * p.ry < r1) {
-        load<T, V>(p.X, (r + u * p.ry) * p.ldx + c, x[u]);
-        load<T, V>(p.dY, (r + u * p.ry) * p.lddy + c, y[u]);
+    for (int u = 0; u < U; ++u)
+      if (i + u < rows) {
+        wx[u] = load<T, V>(x, u * sx);
+        wy[u] = load<T, V>(y, u * sy);
       }
+    x += U * sx;
+    y += U * sy;
 #pragma unroll
-    for (int u = 0; u < kAheadBwd; ++u) {
-      if (r + u * p.ry < r1) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float xh = (x[u][e] - h.mu[e]) * h.rs[e];
-          const float dz = ACT == GQ_ACT_NONE ? y[u][e] : y[u][e] * derivative<ACT>(fmaf(xh, h.ga[e], h.be[e]));
-          x[u][e] = h.rs[e] * (fmaf(dz, h.ga[e], -h1[e]) - xh * h2[e]);
-        }
-        store<T, V>(p.Y, (r + u * p.ry) * p.ldy + c, x[u]);
+    for (int u = 0; u < U; ++u)
+      if (i + u < rows) {
+        const Pk<V> xh = mul(add(value(wx[u]), h.mu), h.rs);
+        const Pk<V> dz = ACT == GQ_ACT_NONE ? value(wy[u]) : slope<ACT>(value(wy[u]), fma(xh, h.ga, h.be));
+        store<T, V>(o, u * so, mul(h.rs, fma(xh, h2, fma(dz, h.ga, h1))));
       }
-    }
+    o += U * so;
   }
 }
 
@@ -288,22 +429,33 @@ __device__ __forceinline__ float2 add_up(const float2* red, const Args& p, int k
 }
 
 // ---------------------------------------------------------- short segments --
-// Shared memory: [d] channel values, [threads x V] of the threads'; the backward
-// kernel's [d] sums over its segments behind them.
-template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kMaxThreads) short_fwd_kernel(const Args p) {
+// GROUP threads, a warp or the whole block, take a segment.  Shared memory of each
+// of them: [d] channel values, the backward kernel's [d] sums over its segments,
+// [GROUP x V] of the threads'.
+template <int GROUP>
+__device__ __forceinline__ void group_sync() {
+  if constexpr (GROUP == 32)
+    __syncwarp();
+  else
+    __syncthreads();
+}
+
+template <typename T, int V, int ACT, int GROUP>
+__global__ void __launch_bounds__(kThreads, 4) short_fwd_kernel(const Args p) {
   extern __shared__ float2 sm[];
-  float2* ch = sm;
-  float2* red = sm + p.d;
+  constexpr int per_block = kThreads / GROUP, warps = GROUP / 32;
+  const int t = threadIdx.x % GROUP, unit = threadIdx.x / GROUP;
+  float2* ch = sm + unit * (p.d + GROUP * V);
+  float2* red = ch + p.d;
   grid_wait();
-  const int t = threadIdx.x, tx = t % p.tx, ry = t / p.tx;
-  const int warp = t >> 5, lane = t & 31, warps = blockDim.x >> 5;
-  for (int64_t j = blockIdx.x; j < p.s; j += gridDim.x) {
+  const int tx = t % p.tx, ry = t / p.tx;
+  const int warp = t >> 5, lane = t & 31;
+  for (int64_t j = (int64_t)blockIdx.x * per_block + unit; j < p.s; j += (int64_t)gridDim.x * per_block) {
     int64_t r0, r1;
     segment(p, j, r0, r1);
     const int64_t rows = r1 - r0;
     if (rows == 0) {
-      for (int g = t; g < p.groups; g += blockDim.x) {
+      for (int g = t; g < p.groups; g += GROUP) {
         p.mean[j * p.groups + g] = 0.0f;
         p.rstd[j * p.groups + g] = __frcp_rn(__fsqrt_rn(p.eps));
       }
@@ -312,64 +464,67 @@ __global__ void __launch_bounds__(kMaxThreads) short_fwd_kernel(const Args p) {
     for (int v0 = 0; v0 < p.vpr; v0 += p.tx) {
       const int c = (v0 + tx) * V;
       if (ry < p.ry && v0 + tx < p.vpr) {
-        float mean[V], m2[V];
-        int mine;
-        spread<T, V>(p, r0, r1, ry, c, mean, m2, mine);
+        Pk<V> mean, m2;
+        spread<T, V>(p, r0, r1, ry, c, mean, m2);
 #pragma unroll
-        for (int e = 0; e < V; ++e) red[(ry * p.tx + tx) * V + e] = make_float2(mean[e], m2[e]);
+        for (int e = 0; e < V; ++e) red[(ry * p.tx + tx) * V + e] = make_float2(mean.e[e], m2.e[e]);
       }
-      __syncthreads();
-      for (int k = t; k < min(p.tx, p.vpr - v0) * V; k += blockDim.x) ch[v0 * V + k] = merge<V>(red, p, k, rows);
-      __syncthreads();
+      group_sync<GROUP>();
+      for (int k = t; k < min(p.tx, p.vpr - v0) * V; k += GROUP) ch[v0 * V + k] = merge<V>(red, p, k, rows);
+      group_sync<GROUP>();
     }
-    for (int g = warp; g < p.groups; g += warps) {
-      float s = 0.0f;
-      for (int k = lane; k < p.cg; k += 32) s += ch[g * p.cg + k].x;
-      const float mean = warp_sum(s) / (float)p.cg;
-      float q = 0.0f;
-      for (int k = lane; k < p.cg; k += 32) {
-        const float2 w = ch[g * p.cg + k];
-        q += fmaf((float)rows * (w.x - mean), w.x - mean, w.y);
+    const int at_once = 32 / p.lpg, sub = lane % p.lpg;
+    for (int g0 = warp * at_once; g0 < p.groups; g0 += warps * at_once) {
+      const int g = g0 + lane / p.lpg, end = g < p.groups ? p.cg : 0;
+      float2* w = ch + (g < p.groups ? g * p.cg : 0);
+      float s = 0.0f, q = 0.0f;
+      for (int k = sub; k < end; k += p.lpg) s += w[k].x;
+      const float mean = lane_sum(s, p.lpg) / (float)p.cg;
+      for (int k = sub; k < end; k += p.lpg) {
+        const float dev = w[k].x - mean;
+        q += fmaf((float)rows * dev, dev, w[k].y);
       }
-      const float var = warp_sum(q) / ((float)rows * (float)p.cg);
+      const float var = lane_sum(q, p.lpg) / ((float)rows * (float)p.cg);
       const float rstd = __frcp_rn(__fsqrt_rn(var + p.eps));
-      for (int k = lane; k < p.cg; k += 32) ch[g * p.cg + k] = make_float2(mean, rstd);
-      if (lane == 0) {
+      for (int k = sub; k < end; k += p.lpg) w[k] = make_float2(mean, rstd);
+      if (sub == 0 && g < p.groups) {
         p.mean[j * p.groups + g] = mean;
         p.rstd[j * p.groups + g] = rstd;
       }
     }
-    __syncthreads();
+    group_sync<GROUP>();
     for (int v0 = 0; v0 < p.vpr; v0 += p.tx) {
       const int c = (v0 + tx) * V;
       if (ry < p.ry && v0 + tx < p.vpr) {
-        float mu[V], sc[V], be[V];
+        Pk<V> mu, sc, be;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           const float2 w = ch[c + e];
-          mu[e] = w.x;
-          sc[e] = w.y * (p.gamma != nullptr ? p.gamma[c + e] : 1.0f);
-          be[e] = p.beta != nullptr ? p.beta[c + e] : 0.0f;
+          mu.e[e] = -w.x;
+          sc.e[e] = w.y * (p.gamma != nullptr ? p.gamma[c + e] : 1.0f);
+          be.e[e] = p.beta != nullptr ? p.beta[c + e] : 0.0f;
         }
         apply<T, V, ACT>(p, r0, r1, ry, c, mu, sc, be);
       }
     }
-    __syncthreads();
+    group_sync<GROUP>();
   }
 }
 
-template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kMaxThreads) short_bwd_kernel(const Args p) {
+template <typename T, int V, int ACT, int GROUP>
+__global__ void __launch_bounds__(kThreads, 3) short_bwd_kernel(const Args p) {
   extern __shared__ float2 sm[];
-  float2* ch = sm;
-  float2* tot = sm + p.d;
+  constexpr int per_block = kThreads / GROUP, warps = GROUP / 32;
+  const int t = threadIdx.x % GROUP, unit = threadIdx.x / GROUP;
+  float2* ch = sm + unit * (2 * p.d + GROUP * V);
+  float2* tot = ch + p.d;
   float2* red = tot + p.d;
   grid_wait();
-  const int t = threadIdx.x, tx = t % p.tx, ry = t / p.tx;
-  const int warp = t >> 5, lane = t & 31, warps = blockDim.x >> 5;
-  for (int k = t; k < p.d; k += blockDim.x) tot[k] = make_float2(0.0f, 0.0f);
-  __syncthreads();
-  for (int64_t j = blockIdx.x; j < p.s; j += gridDim.x) {
+  const int tx = t % p.tx, ry = t / p.tx;
+  const int warp = t >> 5, lane = t & 31;
+  for (int k = t; k < p.d; k += GROUP) tot[k] = make_float2(0.0f, 0.0f);
+  group_sync<GROUP>();
+  for (int64_t j = (int64_t)blockIdx.x * per_block + unit; j < p.s; j += (int64_t)gridDim.x * per_block) {
     int64_t r0, r1;
     segment(p, j, r0, r1);
     const int64_t rows = r1 - r0;
@@ -378,59 +533,61 @@ __global__ void __launch_bounds__(kMaxThreads) short_bwd_kernel(const Args p) {
       const int c = (v0 + tx) * V;
       if (ry < p.ry && v0 + tx < p.vpr) {
         Chan<V> h;
-        float a[V], b[V];
+        Pk<V> a, b;
         channels<V>(p, j, c, h);
         slopes<T, V, ACT>(p, r0, r1, ry, c, h, a, b);
 #pragma unroll
-        for (int e = 0; e < V; ++e) red[(ry * p.tx + tx) * V + e] = make_float2(a[e], b[e]);
+        for (int e = 0; e < V; ++e) red[(ry * p.tx + tx) * V + e] = make_float2(a.e[e], b.e[e]);
       }
-      __syncthreads();
-      for (int k = t; k < min(p.tx, p.vpr - v0) * V; k += blockDim.x) {
+      group_sync<GROUP>();
+      for (int k = t; k < min(p.tx, p.vpr - v0) * V; k += GROUP) {
         const float2 w = add_up<V>(red, p, k);
         ch[v0 * V + k] = w;
         tot[v0 * V + k].x += w.x;
         tot[v0 * V + k].y += w.y;
       }
-      __syncthreads();
+      group_sync<GROUP>();
     }
-    for (int g = warp; g < p.groups; g += warps) {
+    const int at_once = 32 / p.lpg, sub = lane % p.lpg;
+    for (int g0 = warp * at_once; g0 < p.groups; g0 += warps * at_once) {
+      const int g = g0 + lane / p.lpg, end = g < p.groups ? p.cg : 0, c0 = g < p.groups ? g * p.cg : 0;
+      float2* w = ch + c0;
       float s1 = 0.0f, s2 = 0.0f;
-      for (int k = lane; k < p.cg; k += 32) {
-        const float2 w = ch[g * p.cg + k];
-        const float ga = p.gamma != nullptr ? p.gamma[g * p.cg + k] : 1.0f;
-        s1 = fmaf(ga, w.y, s1);
-        s2 = fmaf(ga, w.x, s2);
+      for (int k = sub; k < end; k += p.lpg) {
+        const float ga = p.gamma != nullptr ? p.gamma[c0 + k] : 1.0f;
+        s1 = fmaf(ga, w[k].y, s1);
+        s2 = fmaf(ga, w[k].x, s2);
       }
-      const float inv = 1.0f / ((float)rows * (float)p.cg);
-      s1 = warp_sum(s1) * inv;
-      s2 = warp_sum(s2) * inv;
-      for (int k = lane; k < p.cg; k += 32) ch[g * p.cg + k] = make_float2(s1, s2);
+      const float inv = -1.0f / ((float)rows * (float)p.cg);
+      s1 = lane_sum(s1, p.lpg) * inv;
+      s2 = lane_sum(s2, p.lpg) * inv;
+      for (int k = sub; k < end; k += p.lpg) w[k] = make_float2(s1, s2);
     }
-    __syncthreads();
+    group_sync<GROUP>();
     for (int v0 = 0; v0 < p.vpr; v0 += p.tx) {
       const int c = (v0 + tx) * V;
       if (ry < p.ry && v0 + tx < p.vpr) {
         Chan<V> h;
-        float h1[V], h2[V];
+        Pk<V> h1, h2;
         channels<V>(p, j, c, h);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           const float2 w = ch[c + e];
-          h1[e] = w.x;
-          h2[e] = w.y;
+          h1.e[e] = w.x;
+          h2.e[e] = w.y;
         }
         apply_bwd<T, V, ACT>(p, r0, r1, ry, c, h, h1, h2);
       }
     }
-    __syncthreads();
+    group_sync<GROUP>();
   }
-  for (int k = t; k < p.d; k += blockDim.x) p.tot[(int64_t)blockIdx.x * p.d + k] = tot[k];
+  for (int k = t; k < p.d; k += GROUP) p.tot[((int64_t)blockIdx.x * per_block + unit) * p.d + k] = tot[k];
 }
 
 // ----------------------------------------------------------- long segments --
 // block: chunk blockIdx.x of rows, slab blockIdx.y of channels
 template <typename T, int V>
-__global__ void __launch_bounds__(kMaxThreads) stats_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, 4) stats_kernel(const Args p) {
   extern __shared__ float2 red[];
   grid_wait();
   const int t = threadIdx.x, tx = t % p.tx, ry = t / p.tx;
@@ -445,11 +602,10 @@ __global__ void __launch_bounds__(kMaxThreads) stats_kernel(const Args p) {
     r1 = min(r1, b);
     if (r1 <= r0) continue;
     if (live) {
-      float mean[V], m2[V];
-      int mine;
-      spread<T, V>(p, r0, r1, ry, c, mean, m2, mine);
+      Pk<V> mean, m2;
+      spread<T, V>(p, r0, r1, ry, c, mean, m2);
 #pragma unroll
-      for (int e = 0; e < V; ++e) red[(ry * p.tx + tx) * V + e] = make_float2(mean[e], m2[e]);
+      for (int e = 0; e < V; ++e) red[(ry * p.tx + tx) * V + e] = make_float2(mean.e[e], m2.e[e]);
     }
     __syncthreads();
     for (int k = t; k < min(p.tx, p.vpr - v0) * V; k += blockDim.x)
@@ -516,7 +672,7 @@ __global__ void __launch_bounds__(kCombine) combine_kernel(const Args p) {
   s1 = unit_sum<BLOCK>(s1, sh) * inv;
   if constexpr (BWD) {
     s2 = unit_sum<BLOCK>(s2, sh) * inv;
-    if (lane == 0) p.hsum[unit] = make_float2((float)s1, (float)s2);
+    if (lane == 0) p.hsum[unit] = make_float2(-(float)s1, -(float)s2);
   } else {
     const float mean = (float)s1;
     for (int64_t i = lane; i < cells; i += step) {
@@ -534,7 +690,7 @@ __global__ void __launch_bounds__(kCombine) combine_kernel(const Args p) {
 }
 
 template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kMaxThreads) apply_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, 4) apply_kernel(const Args p) {
   grid_wait();
   const int t = threadIdx.x, tx = t % p.tx, ry = t / p.tx;
   const int v0 = blockIdx.y * p.tx, c = (v0 + tx) * V;
@@ -547,29 +703,27 @@ __global__ void __launch_bounds__(kMaxThreads) apply_kernel(const Args p) {
     r0 = max(r0, a);
     r1 = min(r1, b);
     if (r1 <= r0) continue;
-    float mu[V], sc[V], be[V];
+    Pk<V> mu, sc, be;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       const int64_t g = j * p.groups + (c + e) / p.cg;
-      mu[e] = p.mean[g];
-      sc[e] = p.rstd[g] * (p.gamma != nullptr ? p.gamma[c + e] : 1.0f);
-      be[e] = p.beta != nullptr ? p.beta[c + e] : 0.0f;
+      mu.e[e] = -p.mean[g];
+      sc.e[e] = p.rstd[g] * (p.gamma != nullptr ? p.gamma[c + e] : 1.0f);
+      be.e[e] = p.beta != nullptr ? p.beta[c + e] : 0.0f;
     }
     apply<T, V, ACT>(p, r0, r1, ry, c, mu, sc, be);
   }
 }
 
 template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kMaxThreads) slopes_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, 3) slopes_kernel(const Args p) {
   extern __shared__ float2 red[];
   grid_wait();
   const int t = threadIdx.x, tx = t % p.tx, ry = t / p.tx;
   const int v0 = blockIdx.y * p.tx, c = (v0 + tx) * V;
   const bool live = ry < p.ry && v0 + tx < p.vpr;
   const int64_t chunk = blockIdx.x, a = chunk * p.rows_per, b = min(p.n, a + p.rows_per);
-  float ta[V], tb[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) ta[e] = tb[e] = 0.0f;
+  Pk<V> ta = all<V>(0.0f), tb = ta;
   for (int64_t j = first_segment(p, a); j < p.s; ++j) {
     int64_t r0, r1;
     segment(p, j, r0, r1);
@@ -579,15 +733,13 @@ __global__ void __launch_bounds__(kMaxThreads) slopes_kernel(const Args p) {
     if (r1 <= r0) continue;
     if (live) {
       Chan<V> h;
-      float sa[V], sb[V];
+      Pk<V> sa, sb;
       channels<V>(p, j, c, h);
       slopes<T, V, ACT>(p, r0, r1, ry, c, h, sa, sb);
+      ta = add(ta, sa);
+      tb = add(tb, sb);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        ta[e] += sa[e];
-        tb[e] += sb[e];
-        red[(ry * p.tx + tx) * V + e] = make_float2(sa[e], sb[e]);
-      }
+      for (int e = 0; e < V; ++e) red[(ry * p.tx + tx) * V + e] = make_float2(sa.e[e], sb.e[e]);
     }
     __syncthreads();
     for (int k = t; k < min(p.tx, p.vpr - v0) * V; k += blockDim.x)
@@ -596,7 +748,7 @@ __global__ void __launch_bounds__(kMaxThreads) slopes_kernel(const Args p) {
   }
   if (live) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) red[(ry * p.tx + tx) * V + e] = make_float2(ta[e], tb[e]);
+    for (int e = 0; e < V; ++e) red[(ry * p.tx + tx) * V + e] = make_float2(ta.e[e], tb.e[e]);
   }
   __syncthreads();
   for (int k = t; k < min(p.tx, p.vpr - v0) * V; k += blockDim.x)
@@ -604,7 +756,7 @@ __global__ void __launch_bounds__(kMaxThreads) slopes_kernel(const Args p) {
 }
 
 template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kMaxThreads) apply_bwd_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, 3) apply_bwd_kernel(const Args p) {
   grid_wait();
   const int t = threadIdx.x, tx = t % p.tx, ry = t / p.tx;
   const int v0 = blockIdx.y * p.tx, c = (v0 + tx) * V;
@@ -618,13 +770,13 @@ __global__ void __launch_bounds__(kMaxThreads) apply_bwd_kernel(const Args p) {
     r1 = min(r1, b);
     if (r1 <= r0) continue;
     Chan<V> h;
-    float h1[V], h2[V];
+    Pk<V> h1, h2;
     channels<V>(p, j, c, h);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       const float2 w = p.hsum[j * p.groups + (c + e) / p.cg];
-      h1[e] = w.x;
-      h2[e] = w.y;
+      h1.e[e] = w.x;
+      h2.e[e] = w.y;
     }
     apply_bwd<T, V, ACT>(p, r0, r1, ry, c, h, h1, h2);
   }
@@ -660,38 +812,35 @@ bool valid_type(int type) { return type == GQ_F32 || type == GQ_BF16 || type == 
 int type_bytes(int type) { return type == GQ_F32 ? 4 : 2; }
 
 struct Plan {
-  bool brief;            // one block a segment
-  int threads, tx, ry, vpr, slabs;
-  int64_t rows_per, chunks, blocks;
+  bool brief;            // a block or a warp a segment
+  int group;             // threads of a segment
+  int tx, ry, vpr, slabs;
+  int64_t rows_per, chunks, blocks, parts;
 };
 
 // A segment of up to kShortBytes stays in a block's share of L2 between its two
-// readings, and one block reads it in the time of the two launches saved.
+// readings, and one block reads it in the time of the two launches saved.  A
+// warp takes it where it has at most kWarpVectors for each lane.
 constexpr int64_t kShortBytes = 512 << 10;
-constexpr int kShortMaxD = 8192;
+constexpr int kShortMaxD = 8192, kWarpMaxD = 512, kWarpVectors = 16;
 
 Plan make_plan(int64_t n, int d, int64_t s, int64_t max_rows, int bytes, int v, bool bwd) {
   Plan z{};
   z.vpr = d / v;
   const int64_t longest = max_rows > 0 && max_rows < n ? max_rows : s <= 1 || max_rows > 0 ? n : 4 * (n / s + 1);
   z.brief = longest * d * bytes <= kShortBytes && d <= kShortMaxD;
-  // threads: at least four rows for each where a segment has them
-  z.threads = kMaxThreads;
-  if (z.brief) {
-    const int64_t mean = n / (s > 0 ? s : 1) + 1;
-    while (z.threads > 64 && (int64_t)z.vpr * mean < 4 * (int64_t)z.threads) z.threads /= 2;
-  } else {
-    z.threads = 256;
-  }
-  z.tx = z.vpr < z.threads ? z.vpr : z.threads;
-  z.ry = z.threads / z.tx;
+  const int64_t mean = n / (s > 0 ? s : 1) + 1;
+  z.group = z.brief && d <= kWarpMaxD && mean * z.vpr <= 32 * kWarpVectors && s > 4 * (int64_t)sm_count() ? 32 : kThreads;
+  z.tx = z.vpr < z.group ? z.vpr : z.group;
+  z.ry = z.group / z.tx;
   z.slabs = (z.vpr + z.tx - 1) / z.tx;
   const int64_t sms = sm_count();
   if (z.brief) {
+    const int64_t per_block = kThreads / z.group;
     // the backward blocks' sums are written and read once a block
-    const int64_t most = bwd ? sms * (2048 / z.threads) : 0x7fffffff;
-    z.blocks = s < most ? s : most;
-    z.chunks = 0;
+    const int64_t most = bwd ? 3 * sms : 0x7fffffff, want = (s + per_block - 1) / per_block;
+    z.blocks = want < most ? want : most;
+    z.parts = z.blocks * per_block;
     return z;
   }
   // 16 chunks an SM, of at least 4 rows a thread
@@ -701,21 +850,21 @@ Plan make_plan(int64_t n, int d, int64_t s, int64_t max_rows, int bytes, int v, 
   if (chunks < 1) chunks = 1;
   z.rows_per = (n + chunks - 1) / chunks;
   z.chunks = (n + z.rows_per - 1) / z.rows_per;
-  z.blocks = z.chunks;
+  z.parts = z.chunks;
   return z;
 }
 
-int vec_of(int type) { return type == GQ_F32 ? 4 : 8; }
+constexpr int kVec = 4;
 
 // The workspace does not depend on the matrices' alignment: the larger of both vector widths'.
 size_t workspace(int64_t n, int d, int groups, int type, int64_t s, int64_t max_rows, bool bwd) {
   size_t most = 0;
-  for (int v : {1, vec_of(type)}) {
+  for (int v : {1, kVec}) {
     if (d % v) continue;
     const Plan z = make_plan(n, d, s, max_rows, type_bytes(type), v, bwd);
     size_t b = 0;
     if (z.brief)
-      b = bwd ? (size_t)z.blocks * d * 8 : 0;
+      b = bwd ? (size_t)z.parts * d * 8 : 0;
     else
       b = ((size_t)(z.chunks + s) * d * 8 + 255) / 256 * 256 +
           (bwd ? ((size_t)s * groups * 8 + 255) / 256 * 256 + (size_t)z.chunks * d * 8 : 0);
@@ -737,32 +886,32 @@ int combine(const Args& a, cudaStream_t s) {
                       dim3(kCombine), 0, s, a);
 }
 
+template <typename T, int V, int ACT, int GROUP>
+int run_short(bool bwd, const Args& a, const Plan& z, cudaStream_t s) {
+  const size_t sm = (size_t)(kThreads / GROUP) * ((bwd ? 2 : 1) * a.d + GROUP * V) * 8;
+  auto* kernel = bwd ? short_bwd_kernel<T, V, ACT, GROUP> : short_fwd_kernel<T, V, ACT, GROUP>;
+  GQ_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+  return launch_after(kernel, dim3((unsigned)z.blocks), dim3(kThreads), sm, s, a);
+}
+
 template <typename T, int V, int ACT>
 int run_fwd(const Args& a, const Plan& z, cudaStream_t s) {
-  const size_t red = (size_t)z.threads * V * 8;
-  if (z.brief) {
-    const size_t sm = red + (size_t)a.d * 8;
-    GQ_TRY_CUDA(cudaFuncSetAttribute(short_fwd_kernel<T, V, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
-    return launch_after(short_fwd_kernel<T, V, ACT>, dim3((unsigned)z.blocks), dim3(z.threads), sm, s, a);
-  }
+  if (z.brief) return z.group == 32 ? run_short<T, V, ACT, 32>(false, a, z, s) : run_short<T, V, ACT, kThreads>(false, a, z, s);
   const dim3 g((unsigned)z.chunks, z.slabs);
-  GQ_TRY(launch_after(stats_kernel<T, V>, g, dim3(z.threads), red, s, a));
+  GQ_TRY(launch_after(stats_kernel<T, V>, g, dim3(kThreads), kThreads * V * 8, s, a));
   GQ_TRY(combine<false>(a, s));
-  return launch_after(apply_kernel<T, V, ACT>, g, dim3(z.threads), 0, s, a);
+  return launch_after(apply_kernel<T, V, ACT>, g, dim3(kThreads), 0, s, a);
 }
 
 template <typename T, int V, int ACT>
 int run_bwd(const Args& a, const Plan& z, cudaStream_t s) {
-  const size_t red = (size_t)z.threads * V * 8;
   if (z.brief) {
-    const size_t sm = red + (size_t)a.d * 16;
-    GQ_TRY_CUDA(cudaFuncSetAttribute(short_bwd_kernel<T, V, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
-    GQ_TRY(launch_after(short_bwd_kernel<T, V, ACT>, dim3((unsigned)z.blocks), dim3(z.threads), sm, s, a));
+    GQ_TRY((z.group == 32 ? run_short<T, V, ACT, 32>(true, a, z, s) : run_short<T, V, ACT, kThreads>(true, a, z, s)));
   } else {
     const dim3 g((unsigned)z.chunks, z.slabs);
-    GQ_TRY(launch_after(slopes_kernel<T, V, ACT>, g, dim3(z.threads), red, s, a));
+    GQ_TRY(launch_after(slopes_kernel<T, V, ACT>, g, dim3(kThreads), kThreads * V * 8, s, a));
     GQ_TRY(combine<true>(a, s));
-    GQ_TRY(launch_after(apply_bwd_kernel<T, V, ACT>, g, dim3(z.threads), 0, s, a));
+    GQ_TRY(launch_after(apply_bwd_kernel<T, V, ACT>, g, dim3(kThreads), 0, s, a));
   }
   if (a.dgamma == nullptr && a.dbeta == nullptr) return GQ_OK;
   return launch_after(columns_kernel, dim3((a.d + 31) / 32), dim3(1024), 0, s, a);
@@ -779,14 +928,22 @@ int run_act(bool bwd, int act, const Args& a, const Plan& z, cudaStream_t s) {
 
 int run(bool bwd, int type, int act, int v, const Args& a, const Plan& z, cudaStream_t s) {
   switch (type) {
-    case GQ_F32: return v == 1 ? run_act<float, 1>(bwd, act, a, z, s) : run_act<float, 4>(bwd, act, a, z, s);
+    case GQ_F32: return v == 1 ? run_act<float, 1>(bwd, act, a, z, s) : run_act<float, kVec>(bwd, act, a, z, s);
     case GQ_BF16:
-      return v == 1 ? run_act<__nv_bfloat16, 1>(bwd, act, a, z, s) : run_act<__nv_bfloat16, 8>(bwd, act, a, z, s);
-    default: return v == 1 ? run_act<__half, 1>(bwd, act, a, z, s) : run_act<__half, 8>(bwd, act, a, z, s);
+      return v == 1 ? run_act<__nv_bfloat16, 1>(bwd, act, a, z, s) : run_act<__nv_bfloat16, kVec>(bwd, act, a, z, s);
+    default: return v == 1 ? run_act<__half, 1>(bwd, act, a, z, s) : run_act<__half, kVec>(bwd, act, a, z, s);
   }
 }
 
-bool rows16(const void* p, int64_t ld, int type) { return aligned(p, 16) && ld * type_bytes(type) % 16 == 0; }
+// rows that start aligned for four values
+bool rows4(const void* p, int64_t ld, int type) { return aligned(p, 4 * type_bytes(type)) && ld % kVec == 0; }
+
+// The largest power of two of lanes that each have a channel of a group.
+int lanes_of(int cg) {
+  int l = 1;
+  while (l < 32 && 2 * l <= cg) l *= 2;
+  return l;
+}
 
 int check(int type, int64_t n, int d, int groups, int64_t s, int64_t max_rows, int act, const int64_t* ptr) {
   if (!valid_type(type) || n < 0 || d < 1 || groups < 1 || d % groups || s < 0 || max_rows < 0 ||
@@ -819,7 +976,7 @@ extern "C" int gq_group_norm_fwd(const void* X, int type, int64_t n, int d, int6
       !aligned(beta, 4) || (n > 0 && (X == nullptr || Y == nullptr)) || !aligned(X, e) || !aligned(Y, e))
     return GQ_ERR_INVALID_ARG;
   const int64_t rows = n > 0 ? n : 1;  // without rows: the statistics of empty segments
-  const int v = d % vec_of(type) == 0 && rows16(X, ldx, type) && rows16(Y, ldy, type) ? vec_of(type) : 1;
+  const int v = d % kVec == 0 && rows4(X, ldx, type) && rows4(Y, ldy, type) ? kVec : 1;
   const Plan z = make_plan(rows, d, segments, max_rows, e, v, false);
   const size_t need = workspace(rows, d, groups, type, segments, max_rows, false);
   if (need > 0 && (ws == nullptr || !aligned(ws, 256) || ws_bytes < need)) return GQ_ERR_WORKSPACE;
@@ -842,6 +999,7 @@ extern "C" int gq_group_norm_fwd(const void* X, int type, int64_t n, int d, int6
   a.vpr = z.vpr;
   a.tx = z.tx;
   a.ry = z.ry;
+  a.lpg = lanes_of(a.cg);
   a.rows_per = z.rows_per;
   a.chunks = z.chunks;
   a.part = static_cast<float2*>(ws);
@@ -867,8 +1025,7 @@ extern "C" int gq_group_norm_bwd(const void* dY, int64_t lddy, const void* X, in
       !aligned(beta, 4) || X == nullptr || dY == nullptr || dX == nullptr || !aligned(X, e) || !aligned(dY, e) ||
       !aligned(dX, e))
     return GQ_ERR_INVALID_ARG;
-  const int v = d % vec_of(type) == 0 && rows16(X, ldx, type) && rows16(dY, lddy, type) && rows16(dX, lddx, type)
-                    ? vec_of(type) : 1;
+  const int v = d % kVec == 0 && rows4(X, ldx, type) && rows4(dY, lddy, type) && rows4(dX, lddx, type) ? kVec : 1;
   const Plan z = make_plan(n, d, segments, max_rows, e, v, true);
   const size_t need = workspace(n, d, groups, type, segments, max_rows, true);
   if (ws == nullptr || !aligned(ws, 256) || ws_bytes < need) return GQ_ERR_WORKSPACE;
@@ -892,11 +1049,12 @@ extern "C" int gq_group_norm_bwd(const void* dY, int64_t lddy, const void* X, in
   a.vpr = z.vpr;
   a.tx = z.tx;
   a.ry = z.ry;
+  a.lpg = lanes_of(a.cg);
   a.rows_per = z.rows_per;
   a.chunks = z.chunks;
   a.dgamma = dgamma;
   a.dbeta = dbeta;
-  a.parts = z.blocks;
+  a.parts = z.parts;
   if (z.brief) {
     a.tot = static_cast<float2*>(ws);
   } else {

@@ -113,6 +113,19 @@ __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) 
       : "memory");
   return ok != 0;
 }
+// 32 lanes x 32 consecutive columns of TMEM
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&u)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+        "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(taddr)
+      : "memory");
+}
 // Bounded wait on a barrier phase, the thread suspended in hardware meanwhile;
 // CLUSTER: on what the other CTA released.  False after the limit, or once
 // another role of the CTA has given up.
@@ -371,6 +384,7 @@ constexpr int kStage = 2 * kSBytes;
 constexpr int kBytes8 = 128 * kStep;       // S as bytes
 constexpr int kStgPitch = 36;              // floats: 32 columns and a shift of 4 banks a row
 constexpr int kStg = 32 * kStgPitch * 4;
+constexpr int kColVec = 2 * 128 * 4;        // an epilogue warp's columns: scales | biases
 constexpr long long kDrainCycles = 4000000;
 constexpr int64_t kMaxSplitSteps = 1024;   // 65,536 products: a 32-bit sum holds twice that
 
@@ -381,7 +395,7 @@ struct Shape {
   static constexpr int epi0 = threads / 32 - kEpiWarps;  // first epilogue warp
   static constexpr int ring = CONV ? 4 : 5;
   static constexpr int ring8 = CONV ? 6 : 0;
-  static constexpr int smem = 1024 + ring * kStage + ring8 * kBytes8 + kEpiWarps * kStg + 512;
+  static constexpr int smem = 1024 + ring * kStage + ring8 * kBytes8 + kEpiWarps * (kStg + kColVec) + 512;
 };
 static_assert(Shape<true>::ring % kTeams == 0 && Shape<true>::ring8 % kTeams == 0, "a team meets every other stage");
 
@@ -443,89 +457,82 @@ __device__ __forceinline__ void widen_chunk(uint4 w, uint8_t* dst, int i) {
   *reinterpret_cast<uint4*>(dst + row * 128 + (((piece + 1) ^ x) << 4)) = b;
 }
 
-// 32 rows x 32 columns of sums, lane = row, columns c0.. of the tile at (row0, col0)
-__device__ __forceinline__ void put(const TileArgs& p, const Unit& u, int64_t row0, int64_t col0, const int (&v)[32],
-                                    float* stg, int lane) {
-  const int64_t row = row0 + lane;
-  if (p.part != nullptr) {
-    int* s = reinterpret_cast<int*>(stg);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      *reinterpret_cast<int4*>(s + lane * kStgPitch + 4 * j) = make_int4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    __syncwarp();
-    const int64_t col = col0 + (lane & 7) * 4;
-    int* out = p.part + (int64_t)u.split * p.M * p.ldp;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int rr = 4 * k + (lane >> 3);
-      if (row0 + rr < p.M && col < p.ldp)
-        *reinterpret_cast<int4*>(out + (row0 + rr) * p.ldp + col) =
-            *reinterpret_cast<const int4*>(s + rr * kStgPitch + (lane & 7) * 4);
-    }
-    __syncwarp();
-    return;
-  }
+// 32 rows x 32 columns of sums, lane = row, the tile's columns col0..  cv: the
+// columns' scales, and 128 floats on their biases.
+__device__ __forceinline__ void put(const TileArgs& p, int64_t row0, int64_t col0, const float (&v)[32], float sr, float br,
+                                    const float* cv, float* stg, int lane) {
   if (p.swap) {  // a lane's row is a column of C: lanes write side by side
+    const int64_t row = row0 + lane;
     if (row >= p.M) return;
-    const float sr = p.sS[row], b = p.bias != nullptr ? p.bias[row] : 0.0f;
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-      if (col0 + j < p.N) {
-        const float y = fmaf(__fmul_rn((float)v[j], p.sF[col0 + j]), sr, b);
-        store_as(p.C, (col0 + j) * p.ldc + row, activate(y, p.relu), p.type);
-      }
+      if (col0 + j < p.N)
+        store_as(p.C, (col0 + j) * p.ldc + row, activate(fmaf(__fmul_rn(v[j], cv[j]), sr, br), p.relu), p.type);
     return;
   }
-  const float sr = row < p.M ? p.sS[row] : 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     *reinterpret_cast<float4*>(stg + lane * kStgPitch + 4 * j) =
-        make_float4((float)v[4 * j] * sr, (float)v[4 * j + 1] * sr, (float)v[4 * j + 2] * sr, (float)v[4 * j + 3] * sr);
+        make_float4(v[4 * j] * sr, v[4 * j + 1] * sr, v[4 * j + 2] * sr, v[4 * j + 3] * sr);
   __syncwarp();
+  const int rows = (int)min((int64_t)32, p.M - row0);
   if (p.vec && col0 + 32 <= p.N) {
     if (p.type == GQ_F32) {
       const int c = (lane & 7) * 4;
-      float sf[4], b[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        sf[j] = p.sF[col0 + c + j];
-        b[j] = p.bias != nullptr ? p.bias[col0 + c + j] : 0.0f;
-      }
+      const float4 sf = *reinterpret_cast<const float4*>(cv + c), b = *reinterpret_cast<const float4*>(cv + 128 + c);
+      float* out = static_cast<float*>(p.C) + (row0 + (lane >> 3)) * p.ldc + col0 + c;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int rr = 4 * k + (lane >> 3);
         const float4 x = *reinterpret_cast<const float4*>(stg + rr * kStgPitch + c);
-        if (row0 + rr < p.M)
-          st_f4(static_cast<float*>(p.C) + (row0 + rr) * p.ldc + col0 + c, activate(fmaf(x.x, sf[0], b[0]), p.relu),
-                activate(fmaf(x.y, sf[1], b[1]), p.relu), activate(fmaf(x.z, sf[2], b[2]), p.relu),
-                activate(fmaf(x.w, sf[3], b[3]), p.relu));
+        if (rr < rows)
+          st_f4(out, activate(fmaf(x.x, sf.x, b.x), p.relu), activate(fmaf(x.y, sf.y, b.y), p.relu),
+                activate(fmaf(x.z, sf.z, b.z), p.relu), activate(fmaf(x.w, sf.w, b.w), p.relu));
+        out += 4 * p.ldc;
       }
     } else {
       const int c = (lane & 3) * 8;
-      float sf[8], b[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        sf[j] = p.sF[col0 + c + j];
-        b[j] = p.bias != nullptr ? p.bias[col0 + c + j] : 0.0f;
-      }
+      const float4 s0 = *reinterpret_cast<const float4*>(cv + c), s1 = *reinterpret_cast<const float4*>(cv + c + 4);
+      const float4 b0 = *reinterpret_cast<const float4*>(cv + 128 + c);
+      const float4 b1 = *reinterpret_cast<const float4*>(cv + 132 + c);
+      uint16_t* out = static_cast<uint16_t*>(p.C) + (row0 + (lane >> 2)) * p.ldc + col0 + c;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int rr = 8 * k + (lane >> 2);
         const float4 x = *reinterpret_cast<const float4*>(stg + rr * kStgPitch + c);
         const float4 z = *reinterpret_cast<const float4*>(stg + rr * kStgPitch + c + 4);
-        float y[8] = {x.x, x.y, x.z, x.w, z.x, z.y, z.z, z.w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = activate(fmaf(y[j], sf[j], b[j]), p.relu);
-        if (row0 + rr < p.M)
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.C) + (row0 + rr) * p.ldc + col0 + c) =
-              make_uint4(pack2(y[0], y[1], p.type), pack2(y[2], y[3], p.type), pack2(y[4], y[5], p.type),
-                         pack2(y[6], y[7], p.type));
+        const uint32_t w0 = pack2(activate(fmaf(x.x, s0.x, b0.x), p.relu), activate(fmaf(x.y, s0.y, b0.y), p.relu), p.type);
+        const uint32_t w1 = pack2(activate(fmaf(x.z, s0.z, b0.z), p.relu), activate(fmaf(x.w, s0.w, b0.w), p.relu), p.type);
+        const uint32_t w2 = pack2(activate(fmaf(z.x, s1.x, b1.x), p.relu), activate(fmaf(z.y, s1.y, b1.y), p.relu), p.type);
+        const uint32_t w3 = pack2(activate(fmaf(z.z, s1.z, b1.z), p.relu), activate(fmaf(z.w, s1.w, b1.w), p.relu), p.type);
+        if (rr < rows) *reinterpret_cast<uint4*>(out) = make_uint4(w0, w1, w2, w3);
+        out += 8 * p.ldc;
       }
     }
   } else if (col0 + lane < p.N) {
-    const float sf = p.sF[col0 + lane], b = p.bias != nullptr ? p.bias[col0 + lane] : 0.0f;
-    for (int rr = 0; rr < 32 && row0 + rr < p.M; ++rr)
+    const float sf = cv[lane], b = cv[128 + lane];
+    for (int rr = 0; rr < rows; ++rr)
       store_as(p.C, (row0 + rr) * p.ldc + col0 + lane, activate(fmaf(stg[rr * kStgPitch + lane], sf, b), p.relu), p.type);
+  }
+  __syncwarp();
+}
+
+// the same of a split's sums, unscaled
+__device__ __forceinline__ void put_part(const TileArgs& p, const Unit& u, int64_t row0, int64_t col0, const int (&v)[32],
+                                         float* stg, int lane) {
+  int* s = reinterpret_cast<int*>(stg);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<int4*>(s + lane * kStgPitch + 4 * j) = make_int4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+  __syncwarp();
+  const int64_t col = col0 + (lane & 7) * 4;
+  int* out = p.part + ((int64_t)u.split * p.M + row0 + (lane >> 3)) * p.ldp + col;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int rr = 4 * k + (lane >> 3);
+    if (row0 + rr < p.M && col < p.ldp)
+      *reinterpret_cast<int4*>(out) = *reinterpret_cast<const int4*>(s + rr * kStgPitch + (lane & 7) * 4);
+    out += 4 * p.ldp;
   }
   __syncwarp();
 }
@@ -540,7 +547,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<CONV>::threads
   uint8_t* s16 = smem;
   uint8_t* s8 = s16 + R * kStage;
   float* stg_all = reinterpret_cast<float*>(s8 + Z::ring8 * kBytes8);
-  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(stg_all) + kEpiWarps * kStg);
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(stg_all) + kEpiWarps * (kStg + kColVec));
   uint64_t* empty = full + R;
   uint64_t* tfull = empty + R;
   uint64_t* tempty = tfull + 2;
@@ -718,15 +725,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<CONV>::threads
   } else {
     if constexpr (CONV) regs_up<168>();
     const int quarter = warp & 3, part = (warp - Z::epi0) >> 2;
-    float* stg = stg_all + (warp - Z::epi0) * (kStg / 4);
+    float* stg = stg_all + (warp - Z::epi0) * ((kStg + kColVec) / 4);
+    float* cv = stg + kStg / 4;
     const uint32_t tempty0 = mapa(smem_u32(tempty), 0);
     const int cb = part ? p.half : 0, ce = part ? p.NT : p.half;
     int gen = 0;
     bool ok = true;
     for (int64_t i = pair; ok && i < p.units; i += pairs) {
       const Unit u = get_unit(p, i);
-      const int64_t row0 = u.mt * kTile + cr * 128 + quarter * 32, col0 = u.nt * p.NT;
+      const int64_t row0 = u.mt * kTile + cr * 128 + quarter * 32, col0 = u.nt * p.NT + cb;
       const int gens = (u.s1 - u.s0 + kDrain - 1) / kDrain;
+      const int64_t row = row0 + lane;
+      float sr = 0.0f, br = 0.0f;
+      if (p.part == nullptr) {  // while the products run
+        if (row < p.M) {
+          sr = p.sS[row];
+          if (p.swap && p.bias != nullptr) br = p.bias[row];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int64_t c = col0 + 32 * k + lane;
+          cv[32 * k + lane] = c < p.N ? p.sF[c] : 0.0f;
+          cv[128 + 32 * k + lane] = c < p.N && p.bias != nullptr && !p.swap ? p.bias[c] : 0.0f;
+        }
+        __syncwarp();
+      }
+      if (gens == 1 && p.part == nullptr) {
+        // the accumulator is the sum
+        const int a = gen & 1;
+        ok = wait(&tfull[a], (gen >> 1) & 1, abort, p.err, 38);
+        ok = __all_sync(FULL, ok);
+        if (!ok) break;
+        ++gen;
+        tc_fence_after();
+        const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + a * 256 + cb;
+#pragma unroll 1
+        for (int c = 0; c < ce - cb; c += 32) {
+          float v[32];
+          tmem_ld32(taddr + c, reinterpret_cast<uint32_t(&)[32]>(v));
+          tmem_ld_wait();
+          if (c + 32 >= ce - cb) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(tempty0 + a * 8);
+          }
+          put(p, row0, col0 + c, v, sr, br, cv + c, stg, lane);
+        }
+        continue;
+      }
       int acc[4][32];
       for (int g = 0; g < gens; ++g, ++gen) {
         const int a = gen & 1;
@@ -757,8 +803,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<CONV>::threads
       }
       if (!ok) break;
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (cb + 32 * c < ce) put(p, u, row0, col0 + cb + 32 * c, acc[c], stg, lane);
+      for (int c = 0; c < 4; ++c) {
+        if (cb + 32 * c >= ce) continue;
+        if (p.part != nullptr) {
+          put_part(p, u, row0, col0 + 32 * c, acc[c], stg, lane);
+        } else {
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = (float)acc[c][j];
+          put(p, row0, col0 + 32 * c, v, sr, br, cv + 32 * c, stg, lane);
+        }
+      }
     }
   }
   __syncwarp();
