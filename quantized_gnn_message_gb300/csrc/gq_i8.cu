@@ -458,10 +458,11 @@ __device__ __forceinline__ void widen_chunk(uint4 w, uint8_t* dst, int i) {
 }
 
 // 32 rows x 32 columns of sums, lane = row, the tile's columns col0..  cv: the
-// columns' scales, and 128 floats on their biases.
+// columns' scales, and 128 floats on their biases.  SWAP: C may be transposed.
+template <bool SWAP>
 __device__ __forceinline__ void put(const TileArgs& p, int64_t row0, int64_t col0, const float (&v)[32], float sr, float br,
                                     const float* cv, float* stg, int lane) {
-  if (p.swap) {  // a lane's row is a column of C: lanes write side by side
+  if (SWAP && p.swap) {  // a lane's row is a column of C: lanes write side by side
     const int64_t row = row0 + lane;
     if (row >= p.M) return;
 #pragma unroll
@@ -537,7 +538,8 @@ __device__ __forceinline__ void put_part(const TileArgs& p, const Unit& u, int64
   __syncwarp();
 }
 
-template <bool CONV>
+// MULTI: a unit's sum takes several accumulators, or is a part of a split one's.
+template <bool CONV, bool MULTI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<CONV>::threads, 1)
     i8_tiles_kernel(const __grid_constant__ CUtensorMap mS, const __grid_constant__ CUtensorMap mF, const TileArgs p) {
   using Z = Shape<CONV>;
@@ -738,6 +740,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<CONV>::threads
       const int64_t row = row0 + lane;
       float sr = 0.0f, br = 0.0f;
       if (p.part == nullptr) {  // while the products run
+        __syncwarp();           // every lane is done with the last tile's
         if (row < p.M) {
           sr = p.sS[row];
           if (p.swap && p.bias != nullptr) br = p.bias[row];
@@ -750,7 +753,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<CONV>::threads
         }
         __syncwarp();
       }
-      if (gens == 1 && p.part == nullptr) {
+      if constexpr (!MULTI) {
         // the accumulator is the sum
         const int a = gen & 1;
         ok = wait(&tfull[a], (gen >> 1) & 1, abort, p.err, 38);
@@ -761,57 +764,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<CONV>::threads
         const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + a * 256 + cb;
 #pragma unroll 1
         for (int c = 0; c < ce - cb; c += 32) {
-          float v[32];
-          tmem_ld32(taddr + c, reinterpret_cast<uint32_t(&)[32]>(v));
+          uint32_t r[32];
+          tmem_ld32(taddr + c, r);
           tmem_ld_wait();
           if (c + 32 >= ce - cb) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_cluster(tempty0 + a * 8);
           }
-          put(p, row0, col0 + c, v, sr, br, cv + c, stg, lane);
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+          put<CONV>(p, row0, col0 + c, v, sr, br, cv + c, stg, lane);
         }
-        continue;
-      }
-      int acc[4][32];
-      for (int g = 0; g < gens; ++g, ++gen) {
-        const int a = gen & 1;
-        ok = wait(&tfull[a], (gen >> 1) & 1, abort, p.err, 38);
-        ok = __all_sync(FULL, ok);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + a * 256 + cb;
+      } else {
+        int acc[4][32];
+        for (int g = 0; g < gens; ++g, ++gen) {
+          const int a = gen & 1;
+          ok = wait(&tfull[a], (gen >> 1) & 1, abort, p.err, 38);
+          ok = __all_sync(FULL, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + a * 256 + cb;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (cb + 32 * c < ce) {
+          for (int c = 0; c < 4; ++c) {
+            if (cb + 32 * c < ce) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t r[16];
-              tmem_ld16(taddr + 32 * c + 16 * h, r);
-              tmem_ld_wait();
+              for (int h = 0; h < 2; ++h) {
+                uint32_t r[16];
+                tmem_ld16(taddr + 32 * c + 16 * h, r);
+                tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int x = __float2int_rn(__uint_as_float(r[j]));
-                acc[c][16 * h + j] = g == 0 ? x : acc[c][16 * h + j] + x;
+                for (int j = 0; j < 16; ++j) {
+                  const int x = __float2int_rn(__uint_as_float(r[j]));
+                  acc[c][16 * h + j] = g == 0 ? x : acc[c][16 * h + j] + x;
+                }
               }
             }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(tempty0 + a * 8);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_cluster(tempty0 + a * 8);
-      }
-      if (!ok) break;
+        if (!ok) break;
+// one copy of what follows for all four: the instruction cache holds it
+#pragma unroll 1
+        for (int c = 0; c < ce - cb; c += 32) {
+          int x[32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (cb + 32 * c >= ce) continue;
-        if (p.part != nullptr) {
-          put_part(p, u, row0, col0 + 32 * c, acc[c], stg, lane);
-        } else {
-          float v[32];
+          for (int j = 0; j < 32; ++j) x[j] = c == 0 ? acc[0][j] : c == 32 ? acc[1][j] : c == 64 ? acc[2][j] : acc[3][j];
+          if (p.part != nullptr) {
+            put_part(p, u, row0, col0 + c, x, stg, lane);
+          } else {
+            float v[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = (float)acc[c][j];
-          put(p, row0, col0 + 32 * c, v, sr, br, cv + 32 * c, stg, lane);
+            for (int j = 0; j < 32; ++j) v[j] = (float)x[j];
+            put<CONV>(p, row0, col0 + c, v, sr, br, cv + c, stg, lane);
+          }
         }
       }
     }
@@ -1048,12 +1057,13 @@ int widen(const int8_t* q, int64_t rows, int64_t k, int64_t ld, void* out, cudaS
                       static_cast<__half*>(out), round16(k));
 }
 
-template <bool CONV>
+template <bool CONV, bool MULTI>
 int launch_tiles(const CUtensorMap& mS, const CUtensorMap& mF, const TileArgs& a, cudaStream_t s) {
-  GQ_TRY_CUDA(cudaFuncSetAttribute(i8_tiles_kernel<CONV>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<CONV>::smem));
+  GQ_TRY_CUDA(cudaFuncSetAttribute(i8_tiles_kernel<CONV, MULTI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   Shape<CONV>::smem));
   const int64_t pairs = sm_count() / 2 > 0 ? sm_count() / 2 : 1;
   const int64_t use = a.units < pairs ? a.units : pairs;
-  return launch_after(i8_tiles_kernel<CONV>, dim3((unsigned)(2 * use)), dim3(Shape<CONV>::threads), Shape<CONV>::smem, s,
+  return launch_after(i8_tiles_kernel<CONV, MULTI>, dim3((unsigned)(2 * use)), dim3(Shape<CONV>::threads), Shape<CONV>::smem, s,
                       mS, mF, a);
 }
 
@@ -1088,7 +1098,11 @@ int tile_gemm(const Plan& z, const Operand& A, const Operand& B, int64_t k, cons
   CUtensorMap mS, mF;
   GQ_TRY(make_tmap(&mS, S.q, !z.conv, k, z.M, S.ld, 128));
   GQ_TRY(make_tmap(&mF, F.q, true, k, z.N, F.ld, z.NT / 2));
-  GQ_TRY(z.conv ? launch_tiles<true>(mS, mF, a, s) : launch_tiles<false>(mS, mF, a, s));
+  const bool multi = z.splits > 1 || z.steps > kDrain;
+  if (z.conv)
+    GQ_TRY((multi ? launch_tiles<true, true>(mS, mF, a, s) : launch_tiles<true, false>(mS, mF, a, s)));
+  else
+    GQ_TRY((multi ? launch_tiles<false, true>(mS, mF, a, s) : launch_tiles<false, false>(mS, mF, a, s)));
   if (a.part == nullptr) return GQ_OK;
   int64_t blocks = (z.M * z.ldp + 255) / 256;
   if (blocks > 65536) blocks = 65536;
