@@ -18,8 +18,7 @@
 //               ring of kRing8 stages),
 //   warps 4-11  turn bytes into fp16 (below) in the swizzled layout that the
 //               tensor cores read (a ring of kRing16 stages),
-//   warp 1      issues tcgen05.mma (even CTA) or tells the even CTA that its
-//               stage is ready (odd CTA),
+//   warp 1      issues tcgen05.mma (even CTA),
 //   warps 12-19 epilogue: TMEM -> registers -> scales, bias, activation ->
 //               shared memory -> rows of C, while the next tile's products run.
 // Four bytes become four fp16 in five instructions: x ^ 0x80 is x + 128; put
@@ -58,13 +57,14 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-// an accumulator has been read (tcgen05.wait::ld before it): CTA scope will do
+// Arrival on a barrier of either CTA, released at CTA scope, which costs no
+// memory barrier.  That will do for an accumulator that has been read
+// (tcgen05.wait::ld before it), and for shared memory that was written for the
+// tensor cores: it is this CTA's own, read by this SM, written and fenced towards
+// the asynchronous proxy before the arrival; what crosses is the barrier alone.
+// (With a release at cluster scope a step took 1,380 cycles instead of 630.)
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// shared memory of this CTA has been written, for the other CTA's MMA
-__device__ __forceinline__ void arrive_release_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void tmem_alloc2(uint32_t* dst, uint32_t cols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols)
@@ -100,19 +100,6 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
       "h"((uint16_t)3)
       : "memory");
 }
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n"
-      "  .reg .pred p;\n"
-      "  mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
-      "  selp.u32 %0, 1, 0, p;\n"
-      "}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "n"(kSuspendNs)
-      : "memory");
-  return ok != 0;
-}
 // 32 lanes x 32 consecutive columns of TMEM
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&u)[32]) {
   asm volatile(
@@ -126,16 +113,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&u)[32]) {
       : "r"(taddr)
       : "memory");
 }
-// Bounded wait on a barrier phase, the thread suspended in hardware meanwhile;
-// CLUSTER: on what the other CTA released.  False after the limit, or once
-// another role of the CTA has given up.
-template <bool CLUSTER = false>
+// Bounded wait on a barrier phase, the thread suspended in hardware meanwhile.
+// False after the limit, or once another role of the CTA has given up.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, int where) {
   const uint32_t b = smem_u32(bar);
-  auto done = [&]() { return CLUSTER ? try_wait_cluster(b, parity) : mbar_try_wait_u32(b, parity); };
-  if (done()) return true;
+  if (mbar_try_wait_u32(b, parity)) return true;
   const long long t0 = clock64();
-  while (!done()) {
+  while (!mbar_try_wait_u32(b, parity)) {
     if (*abort) return false;
     if (clock64() - t0 > kWaitCycles) {
       *abort = 1;
@@ -553,9 +537,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<CONV>::threads
   uint64_t* empty = full + R;
   uint64_t* tfull = empty + R;
   uint64_t* tempty = tfull + 2;
-  uint64_t* conv = tempty + 2;           // this CTA's S of a stage is widened
-  uint64_t* peer = conv + R;             // the odd CTA's is (in the even CTA)
-  uint64_t* full8 = peer + R;
+  uint64_t* full8 = tempty + 2;
   uint64_t* empty8 = full8 + R8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(empty8 + R8);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -564,10 +546,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<CONV>::threads
   const uint32_t cr = cluster_rank();
   if (threadIdx.x == 0) {
     for (int s = 0; s < R; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], CONV ? 1 + 2 * kTeamWarps : 1);  // TMA's bytes, and both CTAs' widening warps
       mbar_init(&empty[s], 1);
-      mbar_init(&conv[s], kTeamWarps);
-      mbar_init(&peer[s], 1);
     }
     for (int s = 0; s < R8; ++s) {
       mbar_init(&full8[s], 1);
@@ -650,7 +630,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<CONV>::threads
           const int e = min(u.s1, g + kDrain);
           for (int s = g; s < e; ++s) {
             if (!(ok = wait(&full[st], ph, abort, p.err, 33))) break;
-            if (CONV && !(ok = wait(&conv[st], ph, abort, p.err, 34) && wait<true>(&peer[st], ph, abort, p.err, 34))) break;
             tc_fence_after();
             const uint32_t ab = smem_u32(s16 + st * kStage), bb = ab + kSBytes;
 #pragma unroll
@@ -666,21 +645,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<CONV>::threads
           if (ok) commit_pair(&tfull[a]);
         }
       }
-    } else if (CONV && warp == 1 && lane == 0) {
-      int st = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (int64_t i = pair; ok && i < p.units; i += pairs) {
-        const Unit u = get_unit(p, i);
-        for (int s = u.s0; s < u.s1; ++s) {
-          if (!(ok = wait(&conv[st], ph, abort, p.err, 35))) break;
-          arrive_release_cluster(mapa(smem_u32(&peer[st]), 0));
-          if (++st == R) {
-            st = 0;
-            ph ^= 1;
-          }
-        }
-      }
     }
   } else if (CONV && warp < Z::epi0) {
     // a team of four warps widens every other step: the waits, reads and writes
@@ -689,6 +653,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<CONV>::threads
     const int t = (threadIdx.x - 128) % (32 * kTeamWarps), team = (warp - 4) / kTeamWarps;
     int st = team, st8 = team;
     uint32_t ph = 0, ph8 = 0;
+    const uint32_t full0 = mapa(smem_u32(full), 0);
     int turn = 0;
     bool ok = true;
     for (int64_t i = pair; ok && i < p.units; i += pairs) {
@@ -712,7 +677,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<CONV>::threads
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&empty8[st8]);
-          mbar_arrive(&conv[st]);
+          arrive_cluster(full0 + st * 8);
         }
         if ((st8 += kTeams) >= R8) {
           st8 = team;
