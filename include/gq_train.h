@@ -142,8 +142,8 @@ GQ_API int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, cons
  *   integer, ties to even, decided exactly;  |Q| <= 127
  *   A row whose largest magnitude is below 2^-100 has scale and codes 0.  One
  *   that holds a NaN or an infinity has scale NaN and codes 0.
- *   Q is 16-byte aligned, ldq a multiple of 16 and at least the row's length; up
- *   to 3 bytes behind a row's last code may be written.  ws (transpose only):
+ *   Q is 16-byte aligned, ldq a multiple of 16 and at least the row's length;
+ *   bytes behind a row's last code, up to the next multiple of 4, may be written.  ws (transpose only):
  *   gq_quantize_i8_workspace_bytes bytes, 16-byte aligned.
  * gq_gemm_i8: C = act(diag(scale_a) A B^T diag(scale_b) + bias)
  *   A m x k, B n x k, any int8 values (16-byte aligned, lda and ldb multiples

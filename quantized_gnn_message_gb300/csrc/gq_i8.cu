@@ -173,7 +173,7 @@ __device__ __forceinline__ float activate(float y, int relu) { return relu ? fma
 constexpr float kTiny = 7.888609052210118e-31f;  // 2^-100
 
 struct Scale {
-  float s, inv, half;
+  float s, inv, half;    // inv = 0: the codes are 0
 };
 __device__ __forceinline__ Scale make_scale(uint32_t bits) {
   const float top = __uint_as_float(bits);
@@ -190,70 +190,123 @@ __device__ __forceinline__ Scale make_scale(uint32_t bits) {
 }
 // round(x / s), ties to even, exactly: q within one of it from the reciprocal,
 // then by the remainder x - q s, which a fused multiply-add gives exactly
-// (it is a multiple of half a step of s and no larger than s).
-__device__ __forceinline__ int quantize(float x, const Scale& c) {
-  const float q = rintf(x * c.inv);
+// (it is a multiple of half a step of s and no larger than s).  q is the last bits
+// of 1.5 2^23 + x / s, whose low byte is the code: conversions and roundings go
+// through the special function unit at an eighth of the speed.
+constexpr float kMagic = 12582912.0f;
+__device__ __forceinline__ uint32_t quantize(float x, const Scale& c) {
+  const float t = fmaf(x, c.inv, kMagic);
+  const float q = t - kMagic;
   const float r = fmaf(-q, c.s, x);
-  int k = (int)q;
-  if (fabsf(r) >= c.half && c.inv > 0.0f) {  // rare
-    if (fabsf(r) > c.half || (k & 1)) k += r > 0.0f ? 1 : -1;
+  uint32_t k = __float_as_uint(t);
+  if (fabsf(r) >= c.half) {  // rare
+    if (c.inv > 0.0f && (fabsf(r) > c.half || (k & 1))) k += r > 0.0f ? 1 : -1;
   }
-  return c.inv > 0.0f ? k : 0;
+  return k;
 }
-__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
-  return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 | (uint32_t)(d & 255) << 24;
+// four codes of them, as bytes or as fp16
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, const Scale& s) {
+  const uint32_t w = __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+  return s.inv > 0.0f ? w : 0u;
 }
-// four codes, as bytes or as fp16
-__device__ __forceinline__ void put4(int8_t* q, int a, int b, int c, int d) {
-  *reinterpret_cast<uint32_t*>(q) = pack4(a, b, c, d);
+// 4 bytes -> 4 fp16
+__device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  w ^= 0x80808080u;
+  const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+  const __half2 k = __half2half2(__ushort_as_half(0x6480));  // 1152
+  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), k);
+  const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), k);
+  lo = *reinterpret_cast<const uint32_t*>(&x);
+  hi = *reinterpret_cast<const uint32_t*>(&y);
 }
-__device__ __forceinline__ void put4(__half* q, int a, int b, int c, int d) {
-  const __half2 x = __floats2half2_rn((float)a, (float)b), y = __floats2half2_rn((float)c, (float)d);
-  *reinterpret_cast<uint2*>(q) = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+__device__ __forceinline__ void put4(int8_t* q, uint32_t w) { *reinterpret_cast<uint32_t*>(q) = w; }
+__device__ __forceinline__ void put4(__half* q, uint32_t w) {
+  uint2 h;
+  widen(w, h.x, h.y);
+  *reinterpret_cast<uint2*>(q) = h;
 }
+__device__ __forceinline__ void put1(int8_t* q, uint32_t w) { *q = (int8_t)w; }
+__device__ __forceinline__ void put1(__half* q, uint32_t w) { *q = __int2half_rn((int)(int8_t)w); }
 __device__ __forceinline__ uint32_t mag(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
 // 4 consecutive values of a row
 template <typename T>
 __device__ __forceinline__ float4 load4(const T* p);
 template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ float4 load4<float>(const float* p) { return *reinterpret_cast<const float4*>(p); }
 template <>
 __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
   return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
                      __uint_as_float(w.y & 0xffff0000u));
 }
 template <>
 __device__ __forceinline__ float4 load4<__half>(const __half* p) {
-  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
   const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
   const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
   return make_float4(a.x, a.y, b.x, b.y);
 }
 
-// Rows: LANES threads a row (a warp up to 4,096 columns, else the block), the
-// row read twice, the second time from L1.
 constexpr int kQThreads = 256;
+
+// Rows of up to 128 NV columns that start aligned for four: a warp a row, which it
+// holds in registers.
+template <typename T, typename O, int NV>
+__global__ void __launch_bounds__(kQThreads)
+    quant_short_rows_kernel(const T* X, int64_t n, int d, int64_t ldx, O* Q, int64_t ldq, float* S) {
+  grid_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t r = (int64_t)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
+  if (r >= n) return;
+  const T* x = X + r * ldx;
+  float4 v[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = i * 128 + lane * 4;
+    if (c + 4 <= d)
+      v[i] = load4<T>(x + c);
+    else
+      v[i] = make_float4(c < d ? (float)x[c] : 0.0f, c + 1 < d ? (float)x[c + 1] : 0.0f, c + 2 < d ? (float)x[c + 2] : 0.0f,
+                         0.0f);
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) top = max(max(top, mag(v[i].x)), max(mag(v[i].y), max(mag(v[i].z), mag(v[i].w))));
+  const Scale c = make_scale(__reduce_max_sync(FULL, top));
+  if (lane == 0) S[r] = c.s;
+  O* q = Q + r * ldq;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int at = i * 128 + lane * 4;  // ldq is a multiple of 16: the last four may reach behind d
+    if (at < d)
+      put4(q + at, pack4(quantize(v[i].x, c), quantize(v[i].y, c), quantize(v[i].z, c), quantize(v[i].w, c), c));
+  }
+}
+
+// Other rows: LANES threads a row (a warp up to 4,096 columns, else the block),
+// the row read twice, the second time from L1 or L2.
 template <typename T, typename O, bool VEC, int LANES>
 __global__ void __launch_bounds__(kQThreads)
-    quant_rows_kernel(const T* __restrict__ X, int64_t n, int d, int64_t ldx, O* __restrict__ Q, int64_t ldq,
-                      float* __restrict__ S) {
+    quant_rows_kernel(const T* X, int64_t n, int d, int64_t ldx, O* Q, int64_t ldq, float* S) {
   __shared__ uint32_t smax[kQThreads / 32];
+  grid_wait();
   const int lane = threadIdx.x % LANES;
   const int64_t r = (int64_t)blockIdx.x * (kQThreads / LANES) + threadIdx.x / LANES;
   const bool live = r < n;
   const T* x = X + (live ? r : 0) * ldx;
+  const int d4 = d & ~3;
   uint32_t top = 0;
   if (live) {
     if (VEC) {
-      const int d4 = d & ~3;
+#pragma unroll 4
       for (int c = lane * 4; c < d4; c += LANES * 4) {
         const float4 v = load4<T>(x + c);
         top = max(max(top, mag(v.x)), max(mag(v.y), max(mag(v.z), mag(v.w))));
       }
       if (d4 + lane < d) top = max(top, mag((float)x[d4 + lane]));
     } else {
+#pragma unroll 8
       for (int c = lane; c < d; c += LANES) top = max(top, mag((float)x[c]));
     }
   }
@@ -269,92 +322,141 @@ __global__ void __launch_bounds__(kQThreads)
   if (lane == 0) S[r] = c.s;
   O* q = Q + r * ldq;
   if (VEC) {
-    const int d4 = d & ~3;
+#pragma unroll 4
     for (int k = lane * 4; k < d4; k += LANES * 4) {
       const float4 v = load4<T>(x + k);
-      put4(q + k, quantize(v.x, c), quantize(v.y, c), quantize(v.z, c), quantize(v.w, c));
+      put4(q + k, pack4(quantize(v.x, c), quantize(v.y, c), quantize(v.z, c), quantize(v.w, c), c));
     }
-    if (d4 + lane < d) q[d4 + lane] = (O)quantize((float)x[d4 + lane], c);
+    if (d4 + lane < d) put1(q + d4 + lane, pack4(quantize((float)x[d4 + lane], c), 0, 0, 0, c));
   } else {
-    for (int k = lane; k < d; k += LANES) q[k] = (O)quantize((float)x[k], c);
+#pragma unroll 8
+    for (int k = lane; k < d; k += LANES) put1(q + k, pack4(quantize((float)x[k], c), 0, 0, 0, c));
   }
 }
 
-// Columns, first pass: the largest magnitude of each column (the order of
-// integer maxima does not matter) and, where asked for, sums of the block's rows.
-// A block takes kColW columns and rows_per rows, a thread one column of every
-// kColRows-th row.
-constexpr int kColW = 64, kColRows = kQThreads / kColW;
-template <typename T>
+// Columns.  First the largest magnitude of each column's pieces and, where asked
+// for, their sums: a block takes kColW columns (a thread four of them) and one
+// piece of the rows.
+constexpr int kColW = 64, kColRows = kQThreads / (kColW / 4), kMaxParts = 128;
+template <typename T, bool VEC>
+__device__ __forceinline__ float4 load_cols(const T* x, int left) {  // `left` columns are there
+  if (VEC && left >= 4) return load4<T>(x);
+  return make_float4(left > 0 ? (float)x[0] : 0.0f, left > 1 ? (float)x[1] : 0.0f, left > 2 ? (float)x[2] : 0.0f,
+                     left > 3 ? (float)x[3] : 0.0f);
+}
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(kQThreads)
-    col_max_kernel(const T* __restrict__ X, int64_t n, int d, int64_t ldx, int64_t rows_per, uint32_t* __restrict__ top,
-                   float* __restrict__ sums) {
+    col_max_kernel(const T* X, int64_t n, int d, int64_t ldx, int64_t rows_per, uint32_t* top, float* sums) {
   __shared__ uint32_t st[kColRows][kColW];
   __shared__ float ss[kColRows][kColW];
-  const int cx = threadIdx.x % kColW, ry = threadIdx.x / kColW;
-  const int c = blockIdx.x * kColW + cx;
-  const int64_t r0 = (int64_t)blockIdx.y * rows_per, r1 = min(n, r0 + rows_per);
-  uint32_t m = 0;
-  float s = 0.0f;
-  if (c < d) {
-#pragma unroll 8
-    for (int64_t r = r0 + ry; r < r1; r += kColRows) {
-      const float v = (float)X[r * ldx + c];
-      m = max(m, mag(v));
-      s += v;
-    }
-  }
-  st[ry][cx] = m;
-  ss[ry][cx] = s;
-  __syncthreads();
-  if (ry == 0 && c < d) {
+  grid_wait();
+  const int cv = threadIdx.x % (kColW / 4), ry = threadIdx.x / (kColW / 4);
+  const int c = blockIdx.x * kColW + 4 * cv;
+  const int64_t r1 = min(n, (blockIdx.y + 1) * rows_per);
+  uint32_t m[4] = {0, 0, 0, 0};
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  constexpr int U = 8;
+  for (int64_t r = blockIdx.y * rows_per + ry; r < r1; r += U * kColRows) {
+    float4 v[U];
 #pragma unroll
-    for (int k = 1; k < kColRows; ++k) {
-      m = max(m, st[k][cx]);
-      s += ss[k][cx];
+    for (int u = 0; u < U; ++u)
+      v[u] = load_cols<T, VEC>(X + (r + u * kColRows) * ldx + c, r + u * kColRows < r1 ? d - c : 0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      m[0] = max(m[0], mag(v[u].x));
+      m[1] = max(m[1], mag(v[u].y));
+      m[2] = max(m[2], mag(v[u].z));
+      m[3] = max(m[3], mag(v[u].w));
+      s[0] += v[u].x;
+      s[1] += v[u].y;
+      s[2] += v[u].z;
+      s[3] += v[u].w;
     }
-    if (m > 0) atomicMax(top + c, m);
-    if (sums != nullptr) sums[(int64_t)blockIdx.y * d + c] = s;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    st[ry][4 * cv + k] = m[k];
+    ss[ry][4 * cv + k] = s[k];
+  }
+  __syncthreads();
+  const int x = threadIdx.x, col = blockIdx.x * kColW + x;
+  if (x < kColW && col < d) {
+    uint32_t a = 0;
+    float b = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kColRows; ++k) {
+      a = max(a, st[k][x]);
+      b += ss[k][x];
+    }
+    top[(int64_t)blockIdx.y * d + col] = a;
+    if (sums != nullptr) sums[(int64_t)blockIdx.y * d + col] = b;
   }
 }
 
-__global__ void col_sum_kernel(const float* __restrict__ sums, int parts, int d, float* __restrict__ out) {
-  const int c = blockIdx.x * blockDim.x + threadIdx.x;
-  if (c >= d) return;
-  float s = 0.0f;
-  for (int p = 0; p < parts; ++p) s += sums[(int64_t)p * d + c];
-  out[c] = s;
-}
-
-// Second pass: a block turns 128 rows x 64 columns into 64 rows of 128 bytes.
-constexpr int kTrRows = 128, kTrCols = 64, kTrPitch = kTrRows + 4;
-template <typename T, typename O>
+// Then the pieces' largest and the sums together, by every block for its 64
+// columns, and tiles of 128 rows turned into 64 rows of 128 codes.
+constexpr int kTrRows = 128, kTrPitch = kTrRows / 4 + 1;  // words
+template <typename T, typename O, bool VEC>
 __global__ void __launch_bounds__(kQThreads)
-    quant_cols_kernel(const T* __restrict__ X, int64_t n, int d, int64_t ldx, const uint32_t* __restrict__ top,
-                      O* __restrict__ Q, int64_t ldq, float* __restrict__ S) {
-  __shared__ __align__(16) int8_t tile[kTrCols][kTrPitch];
-  const int c0 = blockIdx.y * kTrCols;
-  const int64_t r0 = (int64_t)blockIdx.x * kTrRows;
-  const int cx = threadIdx.x % kTrCols;
-  const int c = c0 + cx;
-  if (c < d) {
-    const Scale sc = make_scale(top[c]);
-    if (blockIdx.x == 0 && threadIdx.x < kTrCols) S[c] = sc.s;
-    for (int rr = threadIdx.x / kTrCols * 4; rr < kTrRows; rr += kQThreads / kTrCols * 4) {
-      int v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = r0 + rr + j < n ? quantize((float)X[(r0 + rr + j) * ldx + c], sc) : 0;
-      *reinterpret_cast<uint32_t*>(&tile[cx][rr]) = pack4(v[0], v[1], v[2], v[3]);
+    quant_cols_kernel(const T* X, int64_t n, int d, int64_t ldx, const uint32_t* top, const float* sums, int parts, O* Q,
+                      int64_t ldq, float* S, float* colsum) {
+  __shared__ uint32_t tile[kColW][kTrPitch];
+  __shared__ uint32_t smax[4][kColW];
+  __shared__ float ssum[4][kColW];
+  __shared__ Scale sc[kColW];
+  grid_wait();
+  const int t = threadIdx.x, c0 = blockIdx.y * kColW;
+  {
+    const int x = t % kColW, y = t / kColW;
+    uint32_t m = 0;
+    float s = 0.0f;
+    if (c0 + x < d)
+#pragma unroll 8
+      for (int p = y; p < parts; p += 4) {
+        m = max(m, top[(int64_t)p * d + c0 + x]);
+        if (sums != nullptr && blockIdx.x == 0) s += sums[(int64_t)p * d + c0 + x];
+      }
+    smax[y][x] = m;
+    ssum[y][x] = s;
+    __syncthreads();
+    if (t < kColW) {
+      sc[t] = make_scale(max(max(smax[0][t], smax[1][t]), max(smax[2][t], smax[3][t])));
+      if (blockIdx.x == 0 && c0 + t < d) {
+        S[c0 + t] = sc[t].s;
+        if (sums != nullptr) colsum[c0 + t] = (ssum[0][t] + ssum[1][t]) + (ssum[2][t] + ssum[3][t]);
+      }
     }
+    __syncthreads();
   }
-  __syncthreads();
-  // rows of Q start 16-byte aligned; bytes past n of the last 16 are written as 0
-  for (int i = threadIdx.x; i < kTrCols * (kTrRows / 4); i += kQThreads) {
-    const int row = i / (kTrRows / 4), at = i % (kTrRows / 4) * 4;
-    if (c0 + row < d && r0 + at < n) {
-      const int w = *reinterpret_cast<const int*>(&tile[row][at]);
-      put4(Q + (int64_t)(c0 + row) * ldq + r0 + at, w << 24 >> 24, w << 16 >> 24, w << 8 >> 24, w >> 24);
+  const int cv = t % 16, rg = t / 16;  // four columns, four rows
+  const int left = d - c0 - 4 * cv;
+  const int64_t tiles = (n + kTrRows - 1) / kTrRows;
+  for (int64_t k = blockIdx.x; k < tiles; k += gridDim.x) {
+    const int64_t r0 = k * kTrRows;
+    float4 v[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t r = r0 + (rg + 16 * h) * 4 + j;
+        v[h][j] = load_cols<T, VEC>(X + r * ldx + c0 + 4 * cv, r < n ? left : 0);
+      }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t* o = &tile[4 * cv][rg + 16 * h];
+      const Scale a = sc[4 * cv], b = sc[4 * cv + 1], c = sc[4 * cv + 2], e = sc[4 * cv + 3];
+      o[0] = pack4(quantize(v[h][0].x, a), quantize(v[h][1].x, a), quantize(v[h][2].x, a), quantize(v[h][3].x, a), a);
+      o[kTrPitch] = pack4(quantize(v[h][0].y, b), quantize(v[h][1].y, b), quantize(v[h][2].y, b), quantize(v[h][3].y, b), b);
+      o[2 * kTrPitch] = pack4(quantize(v[h][0].z, c), quantize(v[h][1].z, c), quantize(v[h][2].z, c), quantize(v[h][3].z, c), c);
+      o[3 * kTrPitch] = pack4(quantize(v[h][0].w, e), quantize(v[h][1].w, e), quantize(v[h][2].w, e), quantize(v[h][3].w, e), e);
     }
+    __syncthreads();
+    // rows of Q are a multiple of 16 codes: those past n are written as 0
+    for (int i = t; i < kColW * (kTrRows / 4); i += kQThreads) {
+      const int row = i / (kTrRows / 4), w = i % (kTrRows / 4);
+      if (c0 + row < d && r0 + 4 * w < n) put4(Q + (int64_t)(c0 + row) * ldq + r0 + 4 * w, tile[row][w]);
+    }
+    __syncthreads();
   }
 }
 
@@ -419,16 +521,6 @@ __device__ __forceinline__ Unit get_unit(const TileArgs& p, int64_t u) {
   return r;
 }
 
-// 16 bytes -> 16 fp16 in two 16-byte pieces
-__device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  w ^= 0x80808080u;
-  const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
-  const __half2 k = __half2half2(__ushort_as_half(0x6480));  // 1152
-  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), k);
-  const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), k);
-  lo = *reinterpret_cast<const uint32_t*>(&x);
-  hi = *reinterpret_cast<const uint32_t*>(&y);
-}
 // chunk i of 16 bytes of a [rows][64] byte tile into a [rows][64] fp16 tile, 128-byte swizzle
 __device__ __forceinline__ void widen_chunk(uint4 w, uint8_t* dst, int i) {
   uint4 a, b;
@@ -1088,51 +1180,41 @@ int quant_rows(const T* X, int64_t n, int d, int64_t ldx, O* Q, int64_t ldq, flo
   const int per = d <= 4096 ? kQThreads / 32 : 1;
   const int64_t blocks = (n + per - 1) / per;
   if (blocks > 0x7fffffff) return GQ_ERR_UNSUPPORTED;
-  const dim3 g((unsigned)blocks);
-  if (d <= 4096) {
-    if (vec)
-      quant_rows_kernel<T, O, true, 32><<<g, kQThreads, 0, s>>>(X, n, d, ldx, Q, ldq, S);
-    else
-      quant_rows_kernel<T, O, false, 32><<<g, kQThreads, 0, s>>>(X, n, d, ldx, Q, ldq, S);
-  } else {
-    if (vec)
-      quant_rows_kernel<T, O, true, kQThreads><<<g, kQThreads, 0, s>>>(X, n, d, ldx, Q, ldq, S);
-    else
-      quant_rows_kernel<T, O, false, kQThreads><<<g, kQThreads, 0, s>>>(X, n, d, ldx, Q, ldq, S);
-  }
-  return launch_status();
+  auto go = [&](void (*kernel)(const T*, int64_t, int, int64_t, O*, int64_t, float*)) {
+    return launch_after(kernel, dim3((unsigned)blocks), dim3(kQThreads), 0, s, X, n, d, ldx, Q, ldq, S);
+  };
+  if (vec && d <= 1024)
+    return go(d <= 128 ? quant_short_rows_kernel<T, O, 1> : d <= 256 ? quant_short_rows_kernel<T, O, 2>
+              : d <= 512 ? quant_short_rows_kernel<T, O, 4> : quant_short_rows_kernel<T, O, 8>);
+  if (d <= 4096) return go(vec ? quant_rows_kernel<T, O, true, 32> : quant_rows_kernel<T, O, false, 32>);
+  return go(vec ? quant_rows_kernel<T, O, true, kQThreads> : quant_rows_kernel<T, O, false, kQThreads>);
 }
 
-// Row pieces of the columns' first pass: four blocks an SM, at least 64 rows each.
+// Pieces of the columns' first pass: four blocks an SM, at least 64 rows each, and
+// no more than every block of the second pass can put together.
 int64_t col_parts(int64_t n, int d) {
   const int64_t gx = (d + kColW - 1) / kColW;
   int64_t parts = (4 * (int64_t)sm_count() + gx - 1) / gx;
   const int64_t most = (n + 63) / 64;
   if (parts > most) parts = most;
-  if (parts > 65535) parts = 65535;
+  if (parts > kMaxParts) parts = kMaxParts;
   return parts < 1 ? 1 : parts;
 }
-size_t cols_ws(int64_t n, int d, int sums) {
-  return ((size_t)d * 4 + 255) / 256 * 256 + (sums ? (size_t)col_parts(n, d) * d * 4 : 0);
-}
+size_t cols_ws(int64_t n, int d, int sums) { return (size_t)col_parts(n, d) * d * 4 * (sums ? 2 : 1); }
 
-template <typename T, typename O>
+template <typename T, typename O, bool VEC>
 int quant_cols(const T* X, int64_t n, int d, int64_t ldx, O* Q, int64_t ldq, float* S, float* colsum, void* ws,
                cudaStream_t s) {
-  uint32_t* top = static_cast<uint32_t*>(ws);
-  float* sums = colsum != nullptr ? reinterpret_cast<float*>(static_cast<char*>(ws) + ((size_t)d * 4 + 255) / 256 * 256)
-                                  : nullptr;
   const int64_t parts = col_parts(n, d), rows_per = (n + parts - 1) / parts;
-  GQ_TRY_CUDA(cudaMemsetAsync(top, 0, (size_t)d * 4, s));
-  col_max_kernel<T><<<dim3((d + kColW - 1) / kColW, (unsigned)parts), kQThreads, 0, s>>>(X, n, d, ldx, rows_per, top, sums);
-  GQ_TRY(launch_status());
-  if (sums != nullptr) {
-    col_sum_kernel<<<(d + 255) / 256, 256, 0, s>>>(sums, (int)parts, d, colsum);
-    GQ_TRY(launch_status());
-  }
-  quant_cols_kernel<T, O><<<dim3((unsigned)((n + kTrRows - 1) / kTrRows), (d + kTrCols - 1) / kTrCols), kQThreads, 0, s>>>(
-      X, n, d, ldx, top, Q, ldq, S);
-  return launch_status();
+  uint32_t* top = static_cast<uint32_t*>(ws);
+  float* sums = colsum != nullptr ? reinterpret_cast<float*>(top + parts * d) : nullptr;
+  const unsigned gx = (unsigned)((d + kColW - 1) / kColW);
+  GQ_TRY(launch_after(col_max_kernel<T, VEC>, dim3(gx, (unsigned)parts), dim3(kQThreads), 0, s, X, n, d, ldx, rows_per, top,
+                      sums));
+  int64_t tiles = (n + kTrRows - 1) / kTrRows, most = (8 * (int64_t)sm_count() + gx - 1) / gx;
+  if (most < 1) most = 1;
+  return launch_after(quant_cols_kernel<T, O, VEC>, dim3((unsigned)(tiles < most ? tiles : most), gx), dim3(kQThreads), 0, s,
+                      X, n, d, ldx, top, sums, (int)parts, Q, ldq, S, colsum);
 }
 
 template <typename T, typename O>
@@ -1140,7 +1222,9 @@ int quant_to(const void* X, int64_t n, int d, int64_t ldx, int transpose, void* 
              void* ws, cudaStream_t s) {
   const T* x = static_cast<const T*>(X);
   O* q = static_cast<O*>(Q);
-  return transpose ? quant_cols(x, n, d, ldx, q, ldq, S, colsum, ws, s) : quant_rows(x, n, d, ldx, q, ldq, S, s);
+  if (!transpose) return quant_rows(x, n, d, ldx, q, ldq, S, s);
+  if (aligned(x, 4 * sizeof(T)) && ldx % 4 == 0) return quant_cols<T, O, true>(x, n, d, ldx, q, ldq, S, colsum, ws, s);
+  return quant_cols<T, O, false>(x, n, d, ldx, q, ldq, S, colsum, ws, s);
 }
 
 int quant(const void* X, int type, int64_t n, int d, int64_t ldx, int transpose, bool wide, void* Q, int64_t ldq, float* S,
@@ -1158,7 +1242,7 @@ int quant(const void* X, int type, int64_t n, int d, int64_t ldx, int transpose,
   }
 }
 
-constexpr int kMaxCols = 65535 * kTrCols / 2;  // quantizer's grid in y
+constexpr int kMaxCols = 65535 * kColW / 2;  // quantizer's grid in y
 }  // namespace
 }  // namespace gq
 
