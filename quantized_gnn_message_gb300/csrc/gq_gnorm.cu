@@ -27,6 +27,7 @@
 #include <cuda_fp16.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "gq_common.cuh"
 #include "gq_internal.cuh"
@@ -165,8 +166,21 @@ __device__ __forceinline__ Raw<T, V> load(const void* base, int64_t i) {
 template <typename T, int V>
 __device__ __forceinline__ Pk<V> value(const Raw<T, V>& r) {
   Pk<V> x;
+  if constexpr (V == 1 || sizeof(T) == 4) {
 #pragma unroll
-  for (int k = 0; k < V; ++k) x.e[k] = (float)r.e[k];
+    for (int k = 0; k < V; ++k) x.e[k] = (float)r.e[k];
+  } else {
+    const uint2 w = *reinterpret_cast<const uint2*>(r.e);
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {  // its bits are fp32's upper half
+      x.e[0] = __uint_as_float(w.x << 16);
+      x.e[1] = __uint_as_float(w.x & 0xffff0000u);
+      x.e[2] = __uint_as_float(w.y << 16);
+      x.e[3] = __uint_as_float(w.y & 0xffff0000u);
+    } else {
+      two(x, 0) = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+      two(x, 1) = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+    }
+  }
   return x;
 }
 __device__ __forceinline__ void put(float& o, float x) { o = x; }
@@ -174,16 +188,27 @@ __device__ __forceinline__ void put(__nv_bfloat16& o, float x) { o = __float2bfl
 __device__ __forceinline__ void put(__half& o, float x) { o = __float2half_rn(x); }
 template <typename T, int V>
 __device__ __forceinline__ void store(void* base, int64_t i, const Pk<V>& x) {
-  Raw<T, V> r;
-#pragma unroll
-  for (int k = 0; k < V; ++k) put(r.e[k], x.e[k]);
   T* a = static_cast<T*>(base) + i;
-  if constexpr (V == 1)
-    *a = r.e[0];
-  else if constexpr (sizeof(T) == 4)
-    *reinterpret_cast<uint4*>(a) = *reinterpret_cast<const uint4*>(r.e);
-  else
-    *reinterpret_cast<uint2*>(a) = *reinterpret_cast<const uint2*>(r.e);
+  if constexpr (V == 4 && sizeof(T) == 2) {
+    uint2 w;
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      w.x = pack_bf16x2(x.e[0], x.e[1]);
+      w.y = pack_bf16x2(x.e[2], x.e[3]);
+    } else {
+      const __half2 p = __floats2half2_rn(x.e[0], x.e[1]), q = __floats2half2_rn(x.e[2], x.e[3]);
+      w.x = *reinterpret_cast<const uint32_t*>(&p);
+      w.y = *reinterpret_cast<const uint32_t*>(&q);
+    }
+    *reinterpret_cast<uint2*>(a) = w;
+  } else {
+    Raw<T, V> r;
+#pragma unroll
+    for (int k = 0; k < V; ++k) put(r.e[k], x.e[k]);
+    if constexpr (V == 1)
+      *a = r.e[0];
+    else
+      *reinterpret_cast<uint4*>(a) = *reinterpret_cast<const uint4*>(r.e);
+  }
 }
 
 // 1 / (1 + e^-z) by the special function unit's 2^x and 1 / x (each within two
@@ -351,17 +376,17 @@ __device__ __forceinline__ void apply(const Args& p, int64_t r0, int64_t r1, int
   const T* x = static_cast<const T*>(p.X) + first * p.ldx + c;
   T* o = static_cast<T*>(p.Y) + first * p.ldy + c;
   const int64_t sx = (int64_t)p.ry * p.ldx, so = (int64_t)p.ry * p.ldy;
-  for (int i = 0; i < rows; i += U) {
+  int i = 0;
+  for (; i + U <= rows; i += U) {
     Raw<T, V> w[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i + u < rows) w[u] = load<T, V>(x, u * sx);
+    for (int u = 0; u < U; ++u) w[u] = load<T, V>(x, u * sx);
     x += U * sx;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i + u < rows) store<T, V>(o, u * so, activate<ACT>(fma(add(value(w[u]), mu), sc, be)));
+    for (int u = 0; u < U; ++u) store<T, V>(o, u * so, activate<ACT>(fma(add(value(w[u]), mu), sc, be)));
     o += U * so;
   }
+  for (; i < rows; ++i, x += sx, o += so) store<T, V>(o, 0, activate<ACT>(fma(add(value(load<T, V>(x, 0)), mu), sc, be)));
 }
 
 template <typename T, int V, int ACT>
@@ -374,25 +399,26 @@ __device__ __forceinline__ void apply_bwd(const Args& p, int64_t r0, int64_t r1,
   const T* y = static_cast<const T*>(p.dY) + first * p.lddy + c;
   T* o = static_cast<T*>(p.Y) + first * p.ldy + c;
   const int64_t sx = (int64_t)p.ry * p.ldx, sy = (int64_t)p.ry * p.lddy, so = (int64_t)p.ry * p.ldy;
-  for (int i = 0; i < rows; i += U) {
+  auto use = [&](const Raw<T, V>& wx, const Raw<T, V>& wy) {
+    const Pk<V> xh = mul(add(value(wx), h.mu), h.rs);
+    const Pk<V> dz = ACT == GQ_ACT_NONE ? value(wy) : slope<ACT>(value(wy), fma(xh, h.ga, h.be));
+    return mul(h.rs, fma(xh, h2, fma(dz, h.ga, h1)));
+  };
+  int i = 0;
+  for (; i + U <= rows; i += U) {
     Raw<T, V> wx[U], wy[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i + u < rows) {
-        wx[u] = load<T, V>(x, u * sx);
-        wy[u] = load<T, V>(y, u * sy);
-      }
+    for (int u = 0; u < U; ++u) {
+      wx[u] = load<T, V>(x, u * sx);
+      wy[u] = load<T, V>(y, u * sy);
+    }
     x += U * sx;
     y += U * sy;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i + u < rows) {
-        const Pk<V> xh = mul(add(value(wx[u]), h.mu), h.rs);
-        const Pk<V> dz = ACT == GQ_ACT_NONE ? value(wy[u]) : slope<ACT>(value(wy[u]), fma(xh, h.ga, h.be));
-        store<T, V>(o, u * so, mul(h.rs, fma(xh, h2, fma(dz, h.ga, h1))));
-      }
+    for (int u = 0; u < U; ++u) store<T, V>(o, u * so, use(wx[u], wy[u]));
     o += U * so;
   }
+  for (; i < rows; ++i, x += sx, y += sy, o += so) store<T, V>(o, 0, use(load<T, V>(x, 0), load<T, V>(y, 0)));
 }
 
 // Rows of thread `ry` among `rows`.
@@ -716,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 4) apply_kernel(const Args p) {
 }
 
 template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kThreads, 3) slopes_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, 4) slopes_kernel(const Args p) {
   extern __shared__ float2 red[];
   grid_wait();
   const int t = threadIdx.x, tx = t % p.tx, ry = t / p.tx;
@@ -756,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 3) slopes_kernel(const Args p) {
 }
 
 template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kThreads, 3) apply_bwd_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, 4) apply_bwd_kernel(const Args p) {
   grid_wait();
   const int t = threadIdx.x, tx = t % p.tx, ry = t / p.tx;
   const int v0 = blockIdx.y * p.tx, c = (v0 + tx) * V;

@@ -586,7 +586,7 @@ __device__ __forceinline__ void put(const TileArgs& p, int64_t row0, int64_t col
         out += 8 * p.ldc;
       }
     }
-  } else if (col0 + lane < p.N) {
+  } else if (rows > 0 && col0 + lane < p.N) {
     const float sf = cv[lane], b = cv[128 + lane];
     for (int rr = 0; rr < rows; ++rr)
       store_as(p.C, (row0 + rr) * p.ldc + col0 + lane, activate(fmaf(stg[rr * kStgPitch + lane], sf, b), p.relu), p.type);
@@ -834,6 +834,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<CONV>::threads
           for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
           put<CONV>(p, row0, col0 + c, v, sr, br, cv + c, stg, lane);
         }
+        if (ce <= cb) {  // a tile of 32 columns has none for half of the warps
+          __syncwarp();
+          if (lane == 0) arrive_cluster(tempty0 + a * 8);
+        }
       } else {
         int acc[4][32];
         for (int g = 0; g < gens; ++g, ++gen) {
@@ -887,6 +891,241 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<CONV>::threads
   // after a wait that gave up: copies and products under way (they take
   // microseconds) land before the pair's shared and tensor memory is given up
   if (*abort) {
+    const long long t0 = clock64();
+    while (clock64() - t0 < kDrainCycles) {
+    }
+  }
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc2(tmem, 512);
+  }
+  cluster_sync();
+}
+
+// ---------------------------------------------------- rows quantized on the way
+// The product of full-precision rows with at most 256 rows of F, up to 256
+// values long: a row's scale is known once it is read, so the widening warps
+// quantize it between its copy in shared memory and the tensor cores, and DRAM
+// sees the rows once and no codes.  A pair of CTAs takes 256 rows; F's half stays
+// in shared memory; a CTA's 128 rows arrive in pieces of 16 KB (TMA, three in
+// flight) and are whole in fp16 (64 KB) before their products start.
+constexpr int kRowPiece = 16384, kRowSlots = 3, kRowK = 256;
+constexpr int kRowSteps = kRowK / kStep;
+constexpr int kRowThreads = 640;
+constexpr int kRowSmem = 1024 + 2 * kRowSteps * kSBytes + kRowSlots * kRowPiece + kEpiWarps * (kStg + kColVec) + 2 * 128 * 4 +
+                         512;
+
+// four values of a staged row
+template <typename T>
+__device__ __forceinline__ float4 staged4(const uint8_t* row, int c) {
+  return load4<T>(reinterpret_cast<const T*>(row) + c);
+}
+
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowThreads, 1)
+    i8_rows_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mF, const TileArgs p) {
+  constexpr int piece_rows = kRowPiece / (kRowK * (int)sizeof(T)), pieces = 128 / piece_rows;
+  constexpr int per_warp = piece_rows / kConvWarps;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* sS = smem;                                   // [step][128 rows][128 bytes]
+  uint8_t* sF = sS + kRowSteps * kSBytes;               // [step][NT / 2 rows][128 bytes]
+  uint8_t* sX = sF + kRowSteps * kSBytes;               // pieces of rows as they are
+  float* stg_all = reinterpret_cast<float*>(sX + kRowSlots * kRowPiece);
+  float* scales = stg_all + kEpiWarps * (kStg + kColVec) / 4;  // [2][128]
+  uint64_t* xfull = reinterpret_cast<uint64_t*>(scales + 256);
+  uint64_t* xempty = xfull + kRowSlots;
+  uint64_t* ffull = xempty + kRowSlots;  // F is there (both halves, in the even CTA)
+  uint64_t* sfull = ffull + 1;           // both CTAs' rows are quantized (in the even CTA)
+  uint64_t* sempty = sfull + 1;          // their products are done
+  uint64_t* tfull = sempty + 1;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* cfull = tempty + 2;          // this CTA's scales of a tile are there
+  uint64_t* cempty = cfull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cempty + 2);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t cr = cluster_rank();
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < kRowSlots; ++k) {
+      mbar_init(&xfull[k], 1);
+      mbar_init(&xempty[k], kConvWarps);
+    }
+    mbar_init(ffull, 1);
+    mbar_init(sfull, 2 * kConvWarps);
+    mbar_init(sempty, 1);
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 2 * kEpiWarps);
+      mbar_init(&cfull[a], kConvWarps);
+      mbar_init(&cempty[a], kEpiWarps);
+    }
+    *abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc2(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_wait();
+  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int hn = p.NT / 2;
+
+  // 3 warpgroups at 64 registers and 2 at 144: the 61,440 (96 a thread) that the
+  // block is launched with
+  if (warp < 4) {
+    regs_down<64>();
+    if (warp == 0 && lane == 0) {
+      prefetch_tmap(&mX);
+      prefetch_tmap(&mF);
+      const uint32_t bar = mapa(smem_u32(ffull), 0);
+      if (cr == 0) mbar_expect_tx(ffull, 2u * (uint32_t)(p.steps * hn * 128));
+      for (int s = 0; s < p.steps; ++s) tma_load_pair(smem_u32(sF + s * kSBytes), &mF, s * kStep, (int)cr * hn, bar);
+      int slot = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int64_t i = pair; ok && i < p.tm; i += pairs) {
+        const int y = (int)(i * kTile + cr * 128);
+        for (int k = 0; k < pieces; ++k) {
+          if (!(ok = wait(&xempty[slot], ph ^ 1, abort, p.err, 41))) break;
+          mbar_expect_tx(&xfull[slot], kRowPiece);
+          tma_load_2d(sX + slot * kRowPiece, &mX, 0, y + k * piece_rows, &xfull[slot]);
+          if (++slot == kRowSlots) {
+            slot = 0;
+            ph ^= 1;
+          }
+        }
+      }
+    } else if (warp == 1 && lane == 0 && cr == 0) {
+      const uint32_t idesc = (1u << 4) | ((uint32_t)(p.NT >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+      bool ok = wait(ffull, 0, abort, p.err, 42);
+      int n = 0;
+      for (int64_t i = pair; ok && i < p.tm; i += pairs, ++n) {
+        const int a = n & 1;
+        if (!(ok = wait(&tempty[a], ((n >> 1) & 1) ^ 1, abort, p.err, 43))) break;
+        if (!(ok = wait(sfull, n & 1, abort, p.err, 44))) break;
+        tc_fence_after();
+        const uint32_t d = tmem + a * 256;
+        for (int s = 0; s < p.steps; ++s) {
+          const uint32_t ab = smem_u32(sS + s * kSBytes), bb = smem_u32(sF + s * kSBytes);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_pair(d, smem_desc_sw128(ab + 32 * kk, 16, 1024), smem_desc_sw128(bb + 32 * kk, 16, 1024), idesc,
+                      s > 0 || kk > 0);
+        }
+        commit_pair(sempty);
+        commit_pair(&tfull[a]);
+      }
+    }
+  } else if (warp < 4 + kConvWarps) {
+    regs_down<64>();
+    const int cw = warp - 4;
+    const uint32_t sfull0 = mapa(smem_u32(sfull), 0);
+    int slot = 0, n = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int64_t i = pair; ok && i < p.tm; i += pairs, ++n) {
+      // the tile before the last's scales have been read, the last tile's products are done
+      ok = wait(&cempty[n & 1], ((n >> 1) & 1) ^ 1, abort, p.err, 45) && wait(sempty, (n & 1) ^ 1, abort, p.err, 45);
+      if (!(ok = __all_sync(FULL, ok))) break;
+      float* sc = scales + (n & 1) * 128;
+      for (int k = 0; k < pieces; ++k) {
+        ok = wait(&xfull[slot], ph, abort, p.err, 46);
+        if (!(ok = __all_sync(FULL, ok))) break;
+        const uint8_t* x = sX + slot * kRowPiece + cw * per_warp * kRowK * sizeof(T);
+        float4 v[per_warp][2];
+#pragma unroll
+        for (int r = 0; r < per_warp; ++r) {
+          v[r][0] = staged4<T>(x + r * kRowK * sizeof(T), 4 * lane);
+          v[r][1] = staged4<T>(x + r * kRowK * sizeof(T), 128 + 4 * lane);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&xempty[slot]);
+#pragma unroll
+        for (int r = 0; r < per_warp; ++r) {
+          const float4 &u = v[r][0], &w = v[r][1];
+          const uint32_t top = max(max(max(mag(u.x), mag(u.y)), max(mag(u.z), mag(u.w))),
+                                   max(max(mag(w.x), mag(w.y)), max(mag(w.z), mag(w.w))));
+          const Scale c = make_scale(__reduce_max_sync(FULL, top));
+          const int row = k * piece_rows + cw * per_warp + r;
+          if (lane == 0) sc[row] = c.s;
+          // columns 4 l .. of a 64-column step: 8 bytes of the 16-byte piece l / 2 of the row
+          uint8_t* dst = sS + (lane >> 4) * kSBytes + row * 128 + ((((lane & 15) >> 1) ^ (row & 7)) << 4) + (lane & 1) * 8;
+          uint2 h;
+          widen(pack4(quantize(u.x, c), quantize(u.y, c), quantize(u.z, c), quantize(u.w, c), c), h.x, h.y);
+          *reinterpret_cast<uint2*>(dst) = h;
+          widen(pack4(quantize(w.x, c), quantize(w.y, c), quantize(w.z, c), quantize(w.w, c), c), h.x, h.y);
+          *reinterpret_cast<uint2*>(dst + 2 * kSBytes) = h;
+        }
+        if (++slot == kRowSlots) {
+          slot = 0;
+          ph ^= 1;
+        }
+      }
+      if (!ok) break;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&cfull[n & 1]);
+        arrive_cluster(sfull0);
+      }
+    }
+  } else {
+    regs_up<144>();
+    const int quarter = warp & 3, part = (warp - 12) >> 2;
+    float* stg = stg_all + (warp - 12) * ((kStg + kColVec) / 4);
+    float* cv = stg + kStg / 4;
+    const uint32_t tempty0 = mapa(smem_u32(tempty), 0);
+    const int cb = part ? p.half : 0, ce = part ? p.NT : p.half;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = cb + 32 * k + lane;
+      cv[32 * k + lane] = c < p.N ? p.sF[c] : 0.0f;
+      cv[128 + 32 * k + lane] = c < p.N && p.bias != nullptr ? p.bias[c] : 0.0f;
+    }
+    __syncwarp();
+    int n = 0;
+    bool ok = true;
+    for (int64_t i = pair; ok && i < p.tm; i += pairs, ++n) {
+      const int a = n & 1;
+      const int64_t row0 = i * kTile + cr * 128 + quarter * 32;
+      ok = wait(&cfull[a], (n >> 1) & 1, abort, p.err, 47);
+      if (!(ok = __all_sync(FULL, ok))) break;
+      const float sr = scales[a * 128 + quarter * 32 + lane];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&cempty[a]);
+      ok = wait(&tfull[a], (n >> 1) & 1, abort, p.err, 48);
+      if (!(ok = __all_sync(FULL, ok))) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + a * 256 + cb;
+#pragma unroll 1
+      for (int c = 0; c < ce - cb; c += 32) {
+        uint32_t r[32];
+        tmem_ld32(taddr + c, r);
+        tmem_ld_wait();
+        if (c + 32 >= ce - cb) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(tempty0 + a * 8);
+        }
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+        put<false>(p, row0, cb + c, v, sr, 0.0f, cv + c, stg, lane);
+      }
+      if (ce <= cb) {  // a tile of 32 columns has none for half of the warps
+        __syncwarp();
+        if (lane == 0) arrive_cluster(tempty0 + a * 8);
+      }
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  if (*abort) {  // as in the kernel above
     const long long t0 = clock64();
     while (clock64() - t0 < kDrainCycles) {
     }
@@ -1015,6 +1254,21 @@ int make_tmap(CUtensorMap* m, const void* base, bool wide, int64_t cols, int64_t
                         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? GQ_OK : GQ_ERR_INVALID_ARG;
+}
+
+int make_tmap_rows(CUtensorMap* m, const void* X, int type, int64_t cols, int64_t rows, int64_t ld) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return GQ_ERR_CUDA;
+  const int e = type == GQ_F32 ? 4 : 2;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * e};
+  const cuuint32_t box[2] = {kRowK, (cuuint32_t)(kRowPiece / (kRowK * e))};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(m, type == GQ_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type == GQ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                                                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                        2, const_cast<void*>(X), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? GQ_OK : GQ_ERR_INVALID_ARG;
 }
 
@@ -1166,6 +1420,49 @@ int tile_gemm(const Plan& z, const Operand& A, const Operand& B, int64_t k, cons
   return launch_after(join_kernel, dim3((unsigned)blocks), dim3(256), 0, s, a);
 }
 
+// Whether rows of X can be quantized on their way to the product with n rows of F.
+bool rows_fit(int64_t m, int64_t n, int64_t k) { return m > kFew && n <= kTile && k <= kRowK; }
+bool rows_fit(int64_t m, int64_t n, int64_t k, const void* X, int type, int64_t ldx) {
+  return rows_fit(m, n, k) && aligned(X, 16) && ldx * type_bytes(type) % 16 == 0;
+}
+
+template <typename T>
+int launch_rows(const CUtensorMap& mX, const CUtensorMap& mF, const TileArgs& a, cudaStream_t s) {
+  GQ_TRY_CUDA(cudaFuncSetAttribute(i8_rows_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowSmem));
+  const int64_t pairs = sm_count() / 2 > 0 ? sm_count() / 2 : 1;
+  const int64_t use = a.tm < pairs ? a.tm : pairs;
+  return launch_after(i8_rows_kernel<T>, dim3((unsigned)(2 * use)), dim3(kRowThreads), kRowSmem, s, mX, mF, a);
+}
+
+// act(X F^T + bias) with X's rows quantized on the way; F as fp16.
+int rows_gemm(const void* X, int x_type, int64_t m, int64_t k, int64_t ldx, const Operand& F, int64_t n, const float* bias,
+              int relu, void* C, int type, int64_t ldc, int* err, cudaStream_t s) {
+  TileArgs a{};
+  a.M = m;
+  a.N = n;
+  a.steps = (int)((k + kStep - 1) / kStep);
+  a.NT = (int)((n + 31) / 32 * 32);
+  a.half = (a.NT / 2 + 31) / 32 * 32;
+  a.tm = (m + kTile - 1) / kTile;
+  a.tn = 1;
+  a.C = C;
+  a.ldc = ldc;
+  a.type = type;
+  a.relu = relu;
+  a.vec = aligned(C, 16) && ldc * type_bytes(type) % 16 == 0;
+  a.sF = F.scale;
+  a.bias = bias;
+  a.err = err;
+  CUtensorMap mX, mF;
+  GQ_TRY(make_tmap_rows(&mX, X, x_type, k, m, ldx));
+  GQ_TRY(make_tmap(&mF, F.q, true, k, n, F.ld, a.NT / 2));
+  switch (x_type) {
+    case GQ_F32: return launch_rows<float>(mX, mF, a, s);
+    case GQ_BF16: return launch_rows<__nv_bfloat16>(mX, mF, a, s);
+    default: return launch_rows<__half>(mX, mF, a, s);
+  }
+}
+
 // Workspace of a product whose operands are given as bytes (a, b) or made in it.
 size_t gemm_ws(int64_t m, int64_t n, int64_t k, bool a_bytes, bool b_bytes) {
   if (few(m, k)) return 0;
@@ -1306,7 +1603,9 @@ extern "C" size_t gq_linear_i8_workspace_bytes(int64_t n, int k, int out) {
   using namespace gq;
   if (!valid_shape(n, out, k) || n == 0) return 0;
   const bool wide = !few(n, k) && wants_wide(make_plan(n, out, k), true);
-  return code_bytes(n, k, wide) + round256((size_t)n * 4) + gemm_ws(n, out, k, false, true);
+  const size_t split = code_bytes(n, k, wide) + round256((size_t)n * 4) + gemm_ws(n, out, k, false, true);
+  const size_t fused = rows_fit(n, out, k) ? code_bytes(out, k, true) : 0;
+  return split > fused ? split : fused;
 }
 
 extern "C" int gq_linear_i8(const void* X, int type, int64_t n, int k, int64_t ldx, const int8_t* W, int out,
@@ -1327,6 +1626,11 @@ extern "C" int gq_linear_i8(const void* X, int type, int64_t n, int k, int64_t l
   const int relu = act == GQ_ACT_RELU;
   const int64_t ld = round16(k);
   Carve w(ws, ws_bytes);
+  if (rows_fit(n, out, k, X, type, ldx)) {
+    void* qw = w.take(code_bytes(out, k, true));
+    GQ_TRY(widen(W, out, k, ldw, qw, s));
+    return rows_gemm(X, type, n, k, ldx, Operand{qw, ld, scale_w}, out, bias, relu, Y, y_type, ldy, dev_err, s);
+  }
   float* sc = static_cast<float*>(w.take((size_t)n * 4));
   if (few(n, k)) {
     void* q = w.take(code_bytes(n, k, false));
@@ -1361,7 +1665,8 @@ struct Side {
 size_t product_ws(int64_t m, int64_t n, int64_t k, bool ta, bool tb, bool sums) {
   const bool tiny = few(m, k);
   const Plan z = make_plan(m, n, k);
-  return code_bytes(m, k, !tiny && wants_wide(z, true)) + code_bytes(n, k, !tiny && wants_wide(z, false)) +
+  const bool fused = !ta && rows_fit(m, n, k);  // then B is fp16
+  return code_bytes(m, k, !tiny && wants_wide(z, true)) + code_bytes(n, k, fused || (!tiny && wants_wide(z, false))) +
          round256((size_t)m * 4) + round256((size_t)n * 4) + (ta ? round256(cols_ws(k, (int)m, sums)) : 0) +
          (tb ? round256(cols_ws(k, (int)n, 0)) : 0) + (tiny ? 0 : round256(z.sums));
 }
@@ -1372,6 +1677,13 @@ int product(const Side& a, const Side& b, int64_t m, int64_t n, int64_t k, float
   const bool wa = !tiny && wants_wide(z, true), wb = !tiny && wants_wide(z, false);
   const int64_t ld = round16(k);
   Carve w(ws, ws_bytes);
+  if (!a.transpose && rows_fit(m, n, k, a.X, a.type, a.ldx)) {
+    void* q = w.take(code_bytes(n, k, true));
+    float* sc = static_cast<float*>(w.take((size_t)n * 4));
+    void* c = b.transpose ? w.take(cols_ws(b.n, b.d, 0)) : nullptr;
+    GQ_TRY(quant(b.X, b.type, b.n, b.d, b.ldx, b.transpose, true, q, ld, sc, nullptr, c, s));
+    return rows_gemm(a.X, a.type, m, k, a.ldx, Operand{q, ld, sc}, n, nullptr, 0, C, type, ldc, err, s);
+  }
   void* qa = w.take(code_bytes(m, k, wa));
   void* qb = w.take(code_bytes(n, k, wb));
   float* sa = static_cast<float*>(w.take((size_t)m * 4));

@@ -130,7 +130,7 @@ def _sum64(a, b):
 SHAPES = [(1, 1, 1), (1, 10007, 1024), (1, 33, 17), (2, 100, 64), (3, 50, 1000), (5, 5, 5), (8, 333, 4096), (7, 64, 20000),
           (9, 33, 100), (17, 500, 777), (40, 40, 40), (64, 1024, 1024), (256, 256, 64), (257, 255, 65), (300, 1000, 1024),
           (1000, 300, 1025), (128, 64, 5000), (513, 2000, 2048), (2000, 47, 256), (70, 70, 70000), (32, 20, 140000),
-          (5000, 5000, 128), (20000, 256, 256), (255, 20001, 1056), (9, 9, 16), (1, 3, 70001)]
+          (5000, 5000, 128), (20000, 256, 256), (255, 20001, 1056), (9, 9, 16), (1, 3, 70001), (60000, 20, 256), (50001, 1, 100), (80000, 32, 64), (40000, 33, 1024)]
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES)
@@ -252,6 +252,30 @@ def test_linear(n, k, out, pad, t):
     assert none is None and nb is None and torch.equal(only_x, dx)
     none, only_w, _ = q.linear_i8_bwd(dy, x, w, need_dX=False)
     assert none is None and torch.equal(only_w, dw)
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("n,k,out", [(9, 8, 1), (40, 16, 32), (128, 64, 33), (257, 100, 47), (30000, 256, 256),
+                                     (100001, 200, 20), (60000, 72, 160), (50000, 4, 256)])
+def test_rows_quantized_on_the_way_equal_codes(n, k, out, t):
+    """Aligned rows of up to 256 values are quantized inside the product, others
+    before it: the same result, bit for bit, and the rows behind the last untouched."""
+    q = gq()
+    T = TYPES[t]
+    a = torch.zeros(n, (k + 7) // 8 * 8, dtype=T, device="cuda")[:, :k]
+    a.copy_(_matrix(n, k, 0, T, 5))
+    a[n // 2] = 0
+    a[n // 3, k // 2] = float("inf")
+    w, s = q.quantize_i8(_matrix(out, k, 0, torch.float32, 6))
+    bias = torch.randn(out, device="cuda", generator=_gen(7))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    buf = torch.full((n + 1, (out + 7) // 8 * 8), 3.0, dtype=T, device="cuda")
+    y = q.linear_i8(a, w, s, bias, out=buf[:n, :out], dev_err=err)
+    x, sx = q.quantize_i8(a)
+    want = q.gemm_i8(x, sx, w, s, bias, dtype=T)
+    assert err.item() == 0 and torch.equal(torch.isnan(y), torch.isnan(want)) and torch.isnan(y[n // 3]).all()
+    assert torch.equal(y.nan_to_num(7.0), want.nan_to_num(7.0))
+    assert (buf[n] == 3.0).all() and (buf[:, out:] == 3.0).all()
 
 
 def test_linear_is_the_product_it_approximates():
