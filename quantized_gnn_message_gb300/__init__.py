@@ -779,7 +779,7 @@ def _scales(t, count, ref, name):
 def _out(out, shape, dtype, dev, name):
     """`out`, or a new matrix of that shape and type whose rows start 16-byte aligned."""
     if out is None:
-        a = 16 // torch.empty((), dtype=dtype).element_size()
+        a = 4 if dtype == torch.float32 else 8
         return torch.empty_strided(shape, ((shape[1] + a - 1) // a * a, 1), dtype=dtype, device=dev)
     _typed(out, name)
     if tuple(out.shape) != tuple(shape) or out.device != dev:

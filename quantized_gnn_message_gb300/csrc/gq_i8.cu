@@ -13,27 +13,30 @@
 // contraction are added as 64-bit integers.
 //
 // Tile product: a pair of CTAs (cta_group::2) takes 256 rows of one operand, S,
-// and up to 256 of the other, F.  Per step of 64 products each CTA
-//   warp 0      copies its 128 rows of S and its half of F's as bytes (TMA, a
-//               ring of kRing8 stages),
-//   warps 4-11  turn bytes into fp16 (below) in the swizzled layout that the
-//               tensor cores read (a ring of kRing16 stages),
-//   warp 1      issues tcgen05.mma (even CTA),
-//   warps 12-19 epilogue: TMEM -> registers -> scales, bias, activation ->
-//               shared memory -> rows of C, while the next tile's products run.
-// Four bytes become four fp16 in five instructions: x ^ 0x80 is x + 128; put
-// under the byte 0x64 it is the fp16 number 1024 + 128 + x, and one packed
-// subtraction of 1152 leaves x.
-// Bytes cross DRAM and L2, fp16 only shared memory; its ports are what
-// bounds long contractions: per step of 512 tensor cycles a CTA moves 16 KB in,
-// 16 KB to registers, 32 KB back and 32 KB to the tensor cores at 128 bytes a
-// cycle, 768 cycles.
+// and up to 256 of the other, F.  Per step of 64 products in each CTA
+//   warp 0   copies its 128 rows of S and its half of F's as fp16 (TMA, a ring
+//            of 5 stages of 32 KB),
+//   warp 1   issues tcgen05.mma (even CTA),
+//   the last eight warps are the epilogue: TMEM -> registers -> scales, bias,
+//            activation -> shared memory -> rows of C, while the next tile's
+//            products run.
+// A step takes 632 cycles, of which the products are 512: 16,384 x 65,536 x
+// 1,024 in 1.26 ms, 1.75 PFLOP/s, where the chip holds about 1.72 for long;
+// 8,192 cubed, codes widened before and sums drained eight times, 0.66 ms.
+// Where S comes as bytes and meets few rows of F, eight more warps widen
+// it: bytes cross DRAM and L2, fp16 shared memory only (2,449,029 x 256 codes by
+// 256 x 256: 0.61 ms, 5.1 TB/s).  Four bytes become four fp16 in five
+// instructions: x ^ 0x80 is x + 128; put under the byte 0x64 it is the fp16 number
+// 1024 + 128 + x, and one packed subtraction of 1152 leaves x.
+// Rows in full precision of up to 256 values are quantized by such warps on the
+// way (2,449,029 x 256 fp32 -> 256: 1.10 ms instead of 0.54 + 0.61).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "gq_common.cuh"
 #include "gq_internal.cuh"
@@ -832,7 +835,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<CONV>::threads
           float v[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-          put<CONV>(p, row0, col0 + c, v, sr, br, cv + c, stg, lane);
+          put<true>(p, row0, col0 + c, v, sr, br, cv + c, stg, lane);
         }
         if (ce <= cb) {  // a tile of 32 columns has none for half of the warps
           __syncwarp();
@@ -880,7 +883,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<CONV>::threads
             float v[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = (float)x[j];
-            put<CONV>(p, row0, col0 + c, v, sr, br, cv + c, stg, lane);
+            put<true>(p, row0, col0 + c, v, sr, br, cv + c, stg, lane);
           }
         }
       }
@@ -1178,15 +1181,34 @@ __global__ void __launch_bounds__(256) join_kernel(const TileArgs p) {
 
 // ---------------------------------------------------------------- few rows --
 // Up to kFew rows of A: a warp takes rows of B, its lanes 16 bytes each of a
-// row, products by dp4a; A's rows are read through L1 again and again.  Bound
-// by reading B.
-constexpr int kFew = 8;
-template <int M, int ROWS>
+// row, products by dp4a; A's rows are read through L1 again and again, or, where
+// they come in full precision (T) and are short, quantized by every block into
+// its shared memory (one launch instead of two: 10,007 x 1,024 codes against a
+// row of fp32: 7.7 us instead of 5.1 + 5.2 behind each other).  Bound by reading B.
+constexpr int kFew = 8, kFewCodes = 16384;  // codes that a block quantizes
+template <int M, int ROWS, typename T>
 __global__ void __launch_bounds__(256)
-    few_rows_kernel(const int8_t* A, int64_t lda, const float* sA, const int8_t* B, int64_t N, int64_t ldb,
+    few_rows_kernel(const T* A, int64_t lda, const float* sA, const int8_t* B, int64_t N, int64_t ldb,
                     const float* sB, int K, const float* bias, void* C, int64_t ldc, int type, int relu) {
+  constexpr bool QUANT = !std::is_same<T, int8_t>::value;
+  extern __shared__ __align__(16) uint8_t codes[];
+  __shared__ float scale[M];
   grid_wait();
   const int lane = threadIdx.x & 31;
+  if constexpr (QUANT) {
+    const int pitch = (K + 15) / 16 * 16;
+    for (int m = threadIdx.x >> 5; m < M; m += 8) {
+      const T* x = A + m * lda;
+      uint32_t top = 0;
+#pragma unroll 8
+      for (int k = lane; k < K; k += 32) top = max(top, mag((float)x[k]));
+      const Scale c = make_scale(__reduce_max_sync(FULL, top));
+      if (lane == 0) scale[m] = c.s;
+#pragma unroll 8
+      for (int k = lane; k < K; k += 32) codes[m * pitch + k] = (uint8_t)pack4(quantize((float)x[k], c), 0, 0, 0, c);
+    }
+    __syncthreads();
+  }
   const int64_t j0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * ROWS;
   if (j0 >= N) return;
   int acc[M][ROWS];
@@ -1202,7 +1224,11 @@ __global__ void __launch_bounds__(256)
     const int left = K - k;  // bytes past K may hold anything: A's are taken as 0 there
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      uint4 a = *reinterpret_cast<const uint4*>(A + m * lda + k);
+      uint4 a;
+      if constexpr (QUANT)
+        a = *reinterpret_cast<const uint4*>(codes + m * ((K + 15) / 16 * 16) + k);
+      else
+        a = *reinterpret_cast<const uint4*>(A + m * lda + k);
       if (left < 16) {
         uint32_t* w = &a.x;
 #pragma unroll
@@ -1225,7 +1251,8 @@ __global__ void __launch_bounds__(256)
       const int64_t j = j0 + r;
       if (lane == (m * ROWS + r) % 32 && j < N)
         store_as(C, m * ldc + j,
-                 activate(fmaf(__fmul_rn((float)s, sA[m]), sB[j], bias != nullptr ? bias[j] : 0.0f), relu), type);
+                 activate(fmaf(__fmul_rn((float)s, QUANT ? scale[m] : sA[m]), sB[j], bias != nullptr ? bias[j] : 0.0f), relu),
+                 type);
     }
 }
 
@@ -1282,21 +1309,23 @@ struct Plan {
   size_t sums;           // bytes of the splits' sums
 };
 
-constexpr int64_t kConvColumns = 2048;
+constexpr int64_t kConvColumns = 2048, kConvBytes = (int64_t)48 << 20;
 
 // S is A, unless A has fewer rows than a tile and than B: then B's rows fill
 // the tiles, and C is written transposed.  F's tiles are as equal as multiples
 // of 32 allow.  S is widened in the kernel where it meets few rows of F: one
-// pass over DRAM as bytes instead of bytes, fp16 out and fp16 in; otherwise
-// before it, and the tile loop has TMA feed the tensor cores alone.
+// pass over DRAM as bytes instead of bytes, fp16 out and fp16 in.  Otherwise
+// it is fp16 before it, and the tile loop has TMA feed the tensor cores alone (630
+// cycles a step of 256 x 256, against 1,000 to 1,400): so also for codes that
+// are made in the call (`made`: that of A, of B) and as fp16 stay in L2.
 // The contraction is split where the tiles alone leave more than half of the
 // pairs without work, and beyond 65,536 products.
-Plan make_plan(int64_t m, int64_t n, int64_t k) {
+Plan make_plan(int64_t m, int64_t n, int64_t k, bool a_made = false, bool b_made = false) {
   Plan z{};
   z.swap = m < kTile && n > m;
   z.M = z.swap ? n : m;
   z.N = z.swap ? m : n;
-  z.conv = z.N < kConvColumns;
+  z.conv = z.N < kConvColumns && !((z.swap ? b_made : a_made) && z.M * k <= kConvBytes);
   z.tm = (z.M + kTile - 1) / kTile;
   z.tn = (z.N + kTile - 1) / kTile;
   const int64_t per = (z.N + z.tn - 1) / z.tn;
@@ -1338,26 +1367,30 @@ struct Operand {
 bool wants_wide(const Plan& z, bool is_a) { return !z.conv || is_a == (z.swap != 0); }
 size_t code_bytes(int64_t rows, int64_t k, bool wide) { return round256((size_t)rows * round16(k) * (wide ? 2 : 1)); }
 
-template <int M>
-int few_rows(const int8_t* A, int64_t lda, const float* sA, const int8_t* B, int64_t N, int64_t ldb, const float* sB,
-             int K, const float* bias, void* C, int64_t ldc, int type, int relu, cudaStream_t s) {
+template <int M, typename T>
+int few_rows(const T* A, int64_t lda, const float* sA, const Operand& B, int64_t N, int K, const float* bias, void* C,
+             int64_t ldc, int type, int relu, cudaStream_t s) {
   constexpr int ROWS = M <= 2 ? 4 : 2;
   const int64_t blocks = (N + 8 * ROWS - 1) / (8 * ROWS);
-  return launch_after(few_rows_kernel<M, ROWS>, dim3((unsigned)blocks), dim3(256), 0, s, A, lda, sA, B, N, ldb, sB, K,
-                      bias, C, ldc, type, relu);
+  const size_t smem = std::is_same<T, int8_t>::value ? 0 : (size_t)M * round16(K);
+  return launch_after(few_rows_kernel<M, ROWS, T>, dim3((unsigned)blocks), dim3(256), smem, s, A, lda, sA,
+                      static_cast<const int8_t*>(B.q), N, B.ld, B.scale, K, bias, C, ldc, type, relu);
 }
 
-int few_gemm(const Operand& A, int64_t m, const Operand& B, int64_t n, int64_t k, const float* bias, int relu, void* C,
-             int type, int64_t ldc, cudaStream_t s) {
-  const int8_t* a = static_cast<const int8_t*>(A.q);
-  const int8_t* b = static_cast<const int8_t*>(B.q);
+template <typename T>
+int few_gemm(const T* a, int64_t lda, const float* sA, int64_t m, const Operand& B, int64_t n, int64_t k, const float* bias,
+             int relu, void* C, int type, int64_t ldc, cudaStream_t s) {
 #define GQ_FEW(I) \
-  case I: return few_rows<I>(a, A.ld, A.scale, b, n, B.ld, B.scale, (int)k, bias, C, ldc, type, relu, s);
+  case I: return few_rows<I, T>(a, lda, sA, B, n, (int)k, bias, C, ldc, type, relu, s);
   switch (m) {
     GQ_FEW(1) GQ_FEW(2) GQ_FEW(3) GQ_FEW(4) GQ_FEW(5) GQ_FEW(6) GQ_FEW(7) GQ_FEW(8)
   }
 #undef GQ_FEW
   return GQ_ERR_UNSUPPORTED;
+}
+int few_gemm(const Operand& A, int64_t m, const Operand& B, int64_t n, int64_t k, const float* bias, int relu, void* C,
+             int type, int64_t ldc, cudaStream_t s) {
+  return few_gemm(static_cast<const int8_t*>(A.q), A.ld, A.scale, m, B, n, k, bias, relu, C, type, ldc, s);
 }
 
 int widen(const int8_t* q, int64_t rows, int64_t k, int64_t ld, void* out, cudaStream_t s) {
@@ -1466,7 +1499,7 @@ int rows_gemm(const void* X, int x_type, int64_t m, int64_t k, int64_t ldx, cons
 // Workspace of a product whose operands are given as bytes (a, b) or made in it.
 size_t gemm_ws(int64_t m, int64_t n, int64_t k, bool a_bytes, bool b_bytes) {
   if (few(m, k)) return 0;
-  const Plan z = make_plan(m, n, k);
+  const Plan z = make_plan(m, n, k, !a_bytes, !b_bytes);
   return round256(z.sums) + (a_bytes && wants_wide(z, true) ? code_bytes(m, k, true) : 0) +
          (b_bytes && wants_wide(z, false) ? code_bytes(n, k, true) : 0);
 }
@@ -1602,7 +1635,7 @@ extern "C" int gq_gemm_i8(const int8_t* A, int64_t m, int64_t lda, const float* 
 extern "C" size_t gq_linear_i8_workspace_bytes(int64_t n, int k, int out) {
   using namespace gq;
   if (!valid_shape(n, out, k) || n == 0) return 0;
-  const bool wide = !few(n, k) && wants_wide(make_plan(n, out, k), true);
+  const bool wide = !few(n, k) && wants_wide(make_plan(n, out, k, true, false), true);
   const size_t split = code_bytes(n, k, wide) + round256((size_t)n * 4) + gemm_ws(n, out, k, false, true);
   const size_t fused = rows_fit(n, out, k) ? code_bytes(out, k, true) : 0;
   return split > fused ? split : fused;
@@ -1632,12 +1665,22 @@ extern "C" int gq_linear_i8(const void* X, int type, int64_t n, int k, int64_t l
     return rows_gemm(X, type, n, k, ldx, Operand{qw, ld, scale_w}, out, bias, relu, Y, y_type, ldy, dev_err, s);
   }
   float* sc = static_cast<float*>(w.take((size_t)n * 4));
+  if (few(n, k) && n * round16(k) <= kFewCodes) {
+    const Operand b{W, ldw, scale_w};
+    switch (type) {
+      case GQ_F32:
+        return few_gemm(static_cast<const float*>(X), ldx, nullptr, n, b, out, k, bias, relu, Y, y_type, ldy, s);
+      case GQ_BF16:
+        return few_gemm(static_cast<const __nv_bfloat16*>(X), ldx, nullptr, n, b, out, k, bias, relu, Y, y_type, ldy, s);
+      default: return few_gemm(static_cast<const __half*>(X), ldx, nullptr, n, b, out, k, bias, relu, Y, y_type, ldy, s);
+    }
+  }
   if (few(n, k)) {
     void* q = w.take(code_bytes(n, k, false));
     GQ_TRY(quant(X, type, n, k, ldx, 0, false, q, ld, sc, nullptr, nullptr, s));
     return few_gemm(Operand{q, ld, sc}, n, Operand{W, ldw, scale_w}, out, k, bias, relu, Y, y_type, ldy, s);
   }
-  const Plan z = make_plan(n, out, k);
+  const Plan z = make_plan(n, out, k, true, false);
   const bool wide = wants_wide(z, true);
   void* q = w.take(code_bytes(n, k, wide));
   GQ_TRY(quant(X, type, n, k, ldx, 0, wide, q, ld, sc, nullptr, nullptr, s));
@@ -1664,7 +1707,7 @@ struct Side {
 };
 size_t product_ws(int64_t m, int64_t n, int64_t k, bool ta, bool tb, bool sums) {
   const bool tiny = few(m, k);
-  const Plan z = make_plan(m, n, k);
+  const Plan z = make_plan(m, n, k, true, true);
   const bool fused = !ta && rows_fit(m, n, k);  // then B is fp16
   return code_bytes(m, k, !tiny && wants_wide(z, true)) + code_bytes(n, k, fused || (!tiny && wants_wide(z, false))) +
          round256((size_t)m * 4) + round256((size_t)n * 4) + (ta ? round256(cols_ws(k, (int)m, sums)) : 0) +
@@ -1673,7 +1716,7 @@ size_t product_ws(int64_t m, int64_t n, int64_t k, bool ta, bool tb, bool sums) 
 int product(const Side& a, const Side& b, int64_t m, int64_t n, int64_t k, float* colsum, void* C, int type, int64_t ldc,
             void* ws, size_t ws_bytes, int* err, cudaStream_t s) {
   const bool tiny = few(m, k);
-  const Plan z = make_plan(m, n, k);
+  const Plan z = make_plan(m, n, k, true, true);
   const bool wa = !tiny && wants_wide(z, true), wb = !tiny && wants_wide(z, false);
   const int64_t ld = round16(k);
   Carve w(ws, ws_bytes);
