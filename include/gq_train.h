@@ -153,7 +153,7 @@ GQ_API int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, cons
  *   bias, is rounded at each step and once more to the type.  act = RELU gives 0 for
  *   a NaN.  ws: gq_gemm_i8_workspace_bytes(m, n, k), 256-byte aligned (operands
  *   as fp16, the sums of a split contraction; 0 for few rows; depends on the
- *   device's SM count).  dev_err as for the GEMMs (codes 31 .. 38).
+ *   device's SM count).  dev_err as for the GEMMs (codes 31 .. 48).
  * gq_linear_i8: Y = act(X W^T + bias) with X's rows (n x k) quantized in the call
  *   and W (out x k) as gq_quantize_i8 left it.
  * gq_linear_i8_bwd, W (out x k) and X in full precision, each product of
@@ -214,7 +214,7 @@ GQ_API int gq_linear_i8_bwd(const void* dY, int64_t lddy, const void* X, int64_t
  *   backward), 256-byte aligned; it depends on the device's SM count.
  * Errors: GQ_ERR_INVALID_ARG (bad type, act, sizes, eps; d not a multiple of
  * groups; short leading dimensions; null or misaligned pointers; ptr NULL with
- * segments != 1); GQ_ERR_UNSUPPORTED for d > 16384, n > 2^31, segments > 2^30
+ * segments != 1); GQ_ERR_UNSUPPORTED for d > 16384, n >= 2^31, segments > 2^30
  * or segments * groups >= 2^31; GQ_ERR_WORKSPACE.
  * ---------------------------------------------------------------------- */
 #define GQ_ACT_SILU 2 /* group normalization only */

@@ -178,6 +178,15 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _at(t):
+    """The address alone: ctypes takes it where it takes a pointer, without an object for each."""
+    return None if t is None else t.data_ptr()
+
+
+def _on_stream():
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
 def _cuda(t, dtype, name):
     if t is None:
         return None
@@ -661,9 +670,9 @@ def group_norm_fwd(X: torch.Tensor, groups: int, ptr: torch.Tensor | None = None
     with _on(X.device):
         wb = int(L.gq_group_norm_workspace_bytes(max(n, 1), d, groups, ty, s, max_rows, 0))
         buf = None if wb == 0 else ws.get(wb) if ws is not None else torch.empty(wb, dtype=torch.uint8, device=X.device)
-        _check(L.gq_group_norm_fwd(_ptr(X), ty, n, d, _ld_any(X, d), groups, _ptr(ptr), s, max_rows, _ptr(gamma),
-                                   _ptr(beta), eps, act, _ptr(out), _ld_any(out, d), _ptr(mean), _ptr(rstd), _ptr(buf),
-                                   wb, _stream()), "gq_group_norm_fwd")
+        _check(L.gq_group_norm_fwd(_at(X), ty, n, d, _ld_any(X, d), groups, _at(ptr), s, max_rows, _at(gamma),
+                                   _at(beta), eps, act, _at(out), _ld_any(out, d), _at(mean), _at(rstd), _at(buf),
+                                   wb, _on_stream()), "gq_group_norm_fwd")
     return out, mean, rstd
 
 
@@ -691,9 +700,9 @@ def group_norm_bwd(dY: torch.Tensor, X: torch.Tensor, groups: int, mean: torch.T
     with _on(X.device):
         wb = int(L.gq_group_norm_workspace_bytes(max(n, 1), d, groups, ty, s, max_rows, 1))
         buf = None if wb == 0 else ws.get(wb) if ws is not None else torch.empty(wb, dtype=torch.uint8, device=X.device)
-        _check(L.gq_group_norm_bwd(_ptr(dY), _ld_any(dY, d), _ptr(X), _ld_any(X, d), ty, n, d, groups, _ptr(ptr), s,
-                                   max_rows, _ptr(mean), _ptr(rstd), _ptr(gamma), _ptr(beta), act, _ptr(dX),
-                                   _ld_any(dX, d), _ptr(dgamma), _ptr(dbeta), _ptr(buf), wb, _stream()),
+        _check(L.gq_group_norm_bwd(_at(dY), _ld_any(dY, d), _at(X), _ld_any(X, d), ty, n, d, groups, _at(ptr), s,
+                                   max_rows, _at(mean), _at(rstd), _at(gamma), _at(beta), act, _at(dX),
+                                   _ld_any(dX, d), _at(dgamma), _at(dbeta), _at(buf), wb, _on_stream()),
                "gq_group_norm_bwd")
     return dX, dgamma, dbeta
 
@@ -813,8 +822,8 @@ def quantize_i8(X: torch.Tensor, transpose: bool = False, out: torch.Tensor | No
     with _on(X.device):
         wb = int(L.gq_quantize_i8_workspace_bytes(n, d, int(transpose)))
         buf = None if wb == 0 else ws.get(wb) if ws is not None else torch.empty(wb, dtype=torch.uint8, device=X.device)
-        _check(L.gq_quantize_i8(_ptr(X), ty, n, d, ldx, int(transpose), _ptr(out), _ld_i8(out, "out"), _ptr(scale),
-                                _ptr(buf), wb, _stream()), "gq_quantize_i8")
+        _check(L.gq_quantize_i8(_at(X), ty, n, d, ldx, int(transpose), _at(out), _ld_i8(out, "out"), _at(scale),
+                                _at(buf), wb, _on_stream()), "gq_quantize_i8")
     return out, scale
 
 
@@ -839,8 +848,8 @@ def gemm_i8(A: torch.Tensor, scale_a: torch.Tensor, B: torch.Tensor, scale_b: to
     with _on(A.device):
         wb = int(L.gq_gemm_i8_workspace_bytes(m, n, k))
         buf = None if wb == 0 else ws.get(wb) if ws is not None else torch.empty(wb, dtype=torch.uint8, device=A.device)
-        _check(L.gq_gemm_i8(_ptr(A), m, lda, _ptr(scale_a), _ptr(B), n, ldb, _ptr(scale_b), k, _ptr(bias), act,
-                            _ptr(out), _TYPES[out.dtype], _ld_any(out, n), _ptr(buf), wb, _ptr(dev_err), _stream()),
+        _check(L.gq_gemm_i8(_at(A), m, lda, _at(scale_a), _at(B), n, ldb, _at(scale_b), k, _at(bias), act,
+                            _at(out), _TYPES[out.dtype], _ld_any(out, n), _at(buf), wb, _at(dev_err), _on_stream()),
                "gq_gemm_i8")
     return out
 
@@ -862,11 +871,11 @@ def linear_i8(X: torch.Tensor, W: torch.Tensor, scale_w: torch.Tensor, bias: tor
     out = _out(out, (n, m), X.dtype, X.device, "out")
     L = lib()
     with _on(X.device):
-        wb = int(L.gq_linear_i8_workspace_bytes(n, k, m))
-        buf = ws.get(wb) if ws is not None else torch.empty(wb, dtype=torch.uint8, device=X.device)
-        _check(L.gq_linear_i8(_ptr(X), ty, n, k, _ld_any(X, k), _ptr(W), m, ldw, _ptr(scale_w), _ptr(bias), act,
-                              _ptr(out), _TYPES[out.dtype], _ld_any(out, m), _ptr(buf), buf.numel(), _ptr(dev_err),
-                              _stream()), "gq_linear_i8")
+        wb = L.gq_linear_i8_workspace_bytes(n, k, m)
+        buf = None if wb == 0 else ws.get(wb) if ws is not None else torch.empty(wb, dtype=torch.uint8, device=X.device)
+        _check(L.gq_linear_i8(_at(X), ty, n, k, _ld_any(X, k), _at(W), m, ldw, _at(scale_w), _at(bias), act,
+                              _at(out), _TYPES[out.dtype], _ld_any(out, m), _at(buf), wb, _at(dev_err),
+                              _on_stream()), "gq_linear_i8")
     return out
 
 
@@ -893,11 +902,11 @@ def linear_i8_bwd(dY: torch.Tensor, X: torch.Tensor, W: torch.Tensor, need_dX: b
     with _on(X.device):
         wb = int(L.gq_linear_i8_bwd_workspace_bytes(n, k, m, int(need_dX), int(need_dW)))
         buf = ws.get(wb) if ws is not None else torch.empty(wb, dtype=torch.uint8, device=X.device)
-        _check(L.gq_linear_i8_bwd(_ptr(dY), _ld_any(dY, m), _ptr(X), _ld_any(X, k), ty, n, k, m, _ptr(W), tw,
-                                  _ld_any(W, k), _ptr(dX), _TYPES[dX.dtype] if need_dX else 0,
-                                  _ld_any(dX, k) if need_dX else 0, _ptr(dW), _TYPES[dW.dtype] if need_dW else 0,
-                                  _ld_any(dW, k) if need_dW else 0, _ptr(dbias), _ptr(buf), buf.numel(),
-                                  _ptr(dev_err), _stream()), "gq_linear_i8_bwd")
+        _check(L.gq_linear_i8_bwd(_at(dY), _ld_any(dY, m), _at(X), _ld_any(X, k), ty, n, k, m, _at(W), tw,
+                                  _ld_any(W, k), _at(dX), _TYPES[dX.dtype] if need_dX else 0,
+                                  _ld_any(dX, k) if need_dX else 0, _at(dW), _TYPES[dW.dtype] if need_dW else 0,
+                                  _ld_any(dW, k) if need_dW else 0, _at(dbias), _at(buf), buf.numel(),
+                                  _at(dev_err), _on_stream()), "gq_linear_i8_bwd")
     return dX, dW, dbias
 
 
@@ -924,8 +933,8 @@ def adam_moment(codes: torch.Tensor, exponents: torch.Tensor, second: bool, dtyp
     elif out.shape != codes.shape or out.device != codes.device or not out.is_contiguous():
         raise GQError("out must be contiguous, of the codes' shape and device")
     with _on(codes.device):
-        _check(lib().gq_adam_moment(_ptr(codes), _ptr(exponents), n, int(second), _ptr(out), _typed(out, "out"),
-                                    _stream()), "gq_adam_moment")
+        _check(lib().gq_adam_moment(_at(codes), _at(exponents), n, int(second), _at(out), _typed(out, "out"),
+                                    _on_stream()), "gq_adam_moment")
     return out
 
 
@@ -1073,7 +1082,7 @@ class AdamW:
         a.step = self.steps
         L = lib()
         with _on(self.device):
-            s = _stream()
+            s = _on_stream()
             a.advance = 1
             for arr, count, pt, gt in calls:
                 _check(L.gq_adamw_step(arr, count, pt, gt, self.state_bits, ctypes.byref(a), s), "gq_adamw_step")

@@ -245,12 +245,15 @@ __device__ __forceinline__ float rcp_fast(float x) {
   return y;
 }
 
+// a + b rounded by itself: a packed sum of packed products may be fused with them
+__device__ __forceinline__ float2 sum2(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
+
 // Two values.  The moments' update is products and a sum, each rounded: the codes
 // can be reproduced from elementary operations.  The root and the reciprocal are
 // the special function unit's (a step off each): their quotient is lr times smaller than p.
 __device__ __forceinline__ void update(float2& p, float2 g, float2& m, float2& v, const Coef& c) {
-  m = add2(mul2(m, both(c.b1)), mul2(g, both(c.o1)));
-  v = add2(mul2(v, both(c.b2)), mul2(mul2(g, g), both(c.o2)));
+  m = sum2(mul2(m, both(c.b1)), mul2(g, both(c.o1)));
+  v = sum2(mul2(v, both(c.b2)), mul2(mul2(g, g), both(c.o2)));
   const float2 den = fma2(make_float2(sqrt_fast(v.x), sqrt_fast(v.y)), both(c.rs2), both(c.eps));
   const float2 step = mul2(mul2(m, both(-c.lr1)), make_float2(rcp_fast(den.x), rcp_fast(den.y)));
   p = fma2(p, both(c.keep), step);

@@ -20,9 +20,12 @@
 //                   distinct and every kernel finds them without a table.
 //
 // A thread owns four channels (one where rows are not aligned for that) and walks
-// rows, so groups of any width are met only when channels' sums are put together.  Variances are sums of squares
-// around the first value that a thread meets, then around the mean of the parts:
-// no difference of large squares.  All sums run in fp32 in a fixed order.
+// rows, so groups of any width are met only when channels' sums are put together.
+// Variances are sums of squares around the mean of the first eight values that
+// a thread meets, then around the mean of the parts: no difference of large
+// squares.  Eight values are added up by themselves before the running sum takes
+// them.  All sums run in fp32 in a fixed order, those that join the pieces of
+// long segments in 64 bits.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -286,31 +289,38 @@ __device__ __forceinline__ void spread(const Args& p, int64_t r0, int64_t r1, in
   Pk<V> k = all<V>(0.0f), s = k, q = k;
   const int64_t first = r0 + ry;
   const int rows = first < r1 ? (int)((r1 - first + p.ry - 1) / p.ry) : 0;
-  if (rows > 0) k = neg(value(load<T, V>(p.X, first * p.ldx + c)));
   const T* x = static_cast<const T*>(p.X) + first * p.ldx + c;
   const int64_t step = (int64_t)p.ry * p.ldx;
+  auto total = [](const Pk<V>(&y)[U]) {
+    return add(add(add(y[0], y[1]), add(y[2], y[3])), add(add(y[4], y[5]), add(y[6], y[7])));
+  };
+  static_assert(U == 8, "total");
   int i = 0;
   for (; i + U <= rows; i += U) {
     Raw<T, V> w[U];
+    Pk<V> y[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) w[u] = load<T, V>(x, u * step);
     x += U * step;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const Pk<V> y = add(value(w[u]), k);
-      s = add(s, y);
-      q = fma(y, y, q);
-    }
+    for (int u = 0; u < U; ++u) y[u] = value(w[u]);
+    if (i == 0) k = mul(total(y), all<V>(-1.0f / U));
+#pragma unroll
+    for (int u = 0; u < U; ++u) y[u] = add(y[u], k);
+    s = add(s, total(y));
+#pragma unroll
+    for (int u = 0; u < U; ++u) y[u] = mul(y[u], y[u]);
+    q = add(q, total(y));
   }
+  if (i == 0 && rows > 0) k = neg(value(load<T, V>(x, 0)));
   for (; i < rows; ++i, x += step) {
     const Pk<V> y = add(value(load<T, V>(x, 0)), k);
     s = add(s, y);
     q = fma(y, y, q);
   }
-  const float inv = rows > 0 ? 1.0f / (float)rows : 0.0f;
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    const float m = s.e[e] * inv;
+    const float m = rows > 0 ? __fdiv_rn(s.e[e], (float)rows) : 0.0f;  // the reciprocal would err the same way everywhere
     mean.e[e] = m - k.e[e];
     m2.e[e] = fmaxf(fmaf(-s.e[e], m, q.e[e]), 0.0f);
     if (!(q.e[e] == q.e[e])) m2.e[e] = q.e[e];  // fmaxf would drop a NaN
@@ -844,17 +854,27 @@ struct Plan {
   int64_t rows_per, chunks, blocks, parts;
 };
 
-// A segment of up to kShortBytes stays in a block's share of L2 between its two
-// readings, and one block reads it in the time of the two launches saved.  A
-// warp takes it where it has at most kWarpVectors for each lane.
-constexpr int64_t kShortBytes = 512 << 10;
-constexpr int kShortMaxD = 8192, kWarpMaxD = 512, kWarpVectors = 16;
+// Short segments have one launch and read DRAM once, but a block reads alone: 10
+// us and 10 more for every 100 KB (forward; backward 17).  Long ones have three
+// launches and every SM.  Measured, 256 bf16 channels, short | long, forward and
+// backward: 1 segment of 64 KB 15, 21 | as a long one of 1 MB 22, 22; 4 of 256 KB 35, 56
+// | 26, 26; 32 of 256 KB 35, 57 | 39, 43; 128 of 512 KB 87, 136 | 94, 133; 512 of
+// 512 KB 150, 265 | 215, 338 us.
+int64_t short_bytes(int64_t s) {
+  const int64_t sms = sm_count();
+  return s < sms / 8 ? 128 << 10 : s < sms / 2 ? 256 << 10 : 512 << 10;
+}
+// A warp instead of a block takes a segment where it has at most kWarpVectors for
+// each lane and there are enough of them: 20,000 segments of 512 vectors forward 72 us
+// with warps, 412 with blocks, of 1,024 vectors 156 and 316, of 1,600 279 and 285,
+// of 3,840 596 and 453.
+constexpr int kShortMaxD = 8192, kWarpMaxD = 512, kWarpVectors = 48;
 
 Plan make_plan(int64_t n, int d, int64_t s, int64_t max_rows, int bytes, int v, bool bwd) {
   Plan z{};
   z.vpr = d / v;
   const int64_t longest = max_rows > 0 && max_rows < n ? max_rows : s <= 1 || max_rows > 0 ? n : 4 * (n / s + 1);
-  z.brief = longest * d * bytes <= kShortBytes && d <= kShortMaxD;
+  z.brief = longest * d * bytes <= short_bytes(s) && d <= kShortMaxD;
   const int64_t mean = n / (s > 0 ? s : 1) + 1;
   z.group = z.brief && d <= kWarpMaxD && mean * z.vpr <= 32 * kWarpVectors && s > 4 * (int64_t)sm_count() ? 32 : kThreads;
   z.tx = z.vpr < z.group ? z.vpr : z.group;
@@ -975,7 +995,7 @@ int check(int type, int64_t n, int d, int groups, int64_t s, int64_t max_rows, i
   if (!valid_type(type) || n < 0 || d < 1 || groups < 1 || d % groups || s < 0 || max_rows < 0 ||
       (act != GQ_ACT_NONE && act != GQ_ACT_RELU && act != GQ_ACT_SILU) || !aligned(ptr, 8) || (ptr == nullptr && s != 1))
     return GQ_ERR_INVALID_ARG;
-  if (d > 16384 || n > (int64_t)1 << 31 || s > (int64_t)1 << 30 || s * groups > 0x7fffffff) return GQ_ERR_UNSUPPORTED;
+  if (d > 16384 || n >= (int64_t)1 << 31 || s > (int64_t)1 << 30 || s * groups > 0x7fffffff) return GQ_ERR_UNSUPPORTED;
   return GQ_OK;
 }
 

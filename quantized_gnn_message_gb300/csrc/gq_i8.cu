@@ -1184,8 +1184,10 @@ __global__ void __launch_bounds__(256) join_kernel(const TileArgs p) {
 // row, products by dp4a; A's rows are read through L1 again and again, or, where
 // they come in full precision (T) and are short, quantized by every block into
 // its shared memory (one launch instead of two: 10,007 x 1,024 codes against a
-// row of fp32: 7.7 us instead of 5.1 + 5.2 behind each other).  Bound by reading B.
-constexpr int kFew = 8, kFewCodes = 16384;  // codes that a block quantizes
+// row of fp32: 7.7 us instead of 5.1 + 5.2 behind each other).  Bound by reading B,
+// from four rows on by dp4a: 4,096 x 4,096 by 1, 2, 4, 8 rows 13, 15, 19, 33 us,
+// where the tiles take 22.
+constexpr int kFew = 4, kFewCodes = 16384;  // codes that a block quantizes
 template <int M, int ROWS, typename T>
 __global__ void __launch_bounds__(256)
     few_rows_kernel(const T* A, int64_t lda, const float* sA, const int8_t* B, int64_t N, int64_t ldb,
@@ -1309,15 +1311,16 @@ struct Plan {
   size_t sums;           // bytes of the splits' sums
 };
 
-constexpr int64_t kConvColumns = 2048, kConvBytes = (int64_t)48 << 20;
+constexpr int64_t kConvColumns = 2048;
 
 // S is A, unless A has fewer rows than a tile and than B: then B's rows fill
 // the tiles, and C is written transposed.  F's tiles are as equal as multiples
-// of 32 allow.  S is widened in the kernel where it meets few rows of F: one
-// pass over DRAM as bytes instead of bytes, fp16 out and fp16 in.  Otherwise
-// it is fp16 before it, and the tile loop has TMA feed the tensor cores alone (630
-// cycles a step of 256 x 256, against 1,000 to 1,400): so also for codes that
-// are made in the call (`made`: that of A, of B) and as fp16 stay in L2.
+// of 32 allow.  S that is given as bytes is widened in the kernel where it meets
+// few rows of F, one pass over DRAM as bytes instead of bytes, fp16 out and
+// fp16 in; else before it.  65,536 x 1,024 bytes by 256, 512, 1,024, 2,048 rows
+// in the kernel 48, 70, 126, 231 us, before it 81, 95, 129, 197; 16,384 x 4,096
+// by 64 rows 42 and 82.  Codes that are made in the call (`made`: of A, of B) are
+// made as fp16: 131,072 x 1,024 by 512 rows 199 us, as bytes 222.
 // The contraction is split where the tiles alone leave more than half of the
 // pairs without work, and beyond 65,536 products.
 Plan make_plan(int64_t m, int64_t n, int64_t k, bool a_made = false, bool b_made = false) {
@@ -1325,7 +1328,7 @@ Plan make_plan(int64_t m, int64_t n, int64_t k, bool a_made = false, bool b_made
   z.swap = m < kTile && n > m;
   z.M = z.swap ? n : m;
   z.N = z.swap ? m : n;
-  z.conv = z.N < kConvColumns && !((z.swap ? b_made : a_made) && z.M * k <= kConvBytes);
+  z.conv = z.N < kConvColumns && !(z.swap ? b_made : a_made);
   z.tm = (z.M + kTile - 1) / kTile;
   z.tn = (z.N + kTile - 1) / kTile;
   const int64_t per = (z.N + z.tn - 1) / z.tn;
@@ -1355,6 +1358,8 @@ bool valid_shape(int64_t m, int64_t n, int64_t k) {
 bool few(int64_t m, int64_t k) { return m <= kFew && k <= 65536; }  // a 32-bit sum holds twice that
 
 int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
+// rows that every block of the product quantizes for itself
+bool few_codes(int64_t m, int64_t k) { return few(m, k) && m * round16(k) <= kFewCodes; }
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 // One operand of a product: codes as bytes or fp16, rows of a multiple of 16.
@@ -1383,7 +1388,7 @@ int few_gemm(const T* a, int64_t lda, const float* sA, int64_t m, const Operand&
 #define GQ_FEW(I) \
   case I: return few_rows<I, T>(a, lda, sA, B, n, (int)k, bias, C, ldc, type, relu, s);
   switch (m) {
-    GQ_FEW(1) GQ_FEW(2) GQ_FEW(3) GQ_FEW(4) GQ_FEW(5) GQ_FEW(6) GQ_FEW(7) GQ_FEW(8)
+    GQ_FEW(1) GQ_FEW(2) GQ_FEW(3) GQ_FEW(4)
   }
 #undef GQ_FEW
   return GQ_ERR_UNSUPPORTED;
@@ -1635,6 +1640,7 @@ extern "C" int gq_gemm_i8(const int8_t* A, int64_t m, int64_t lda, const float* 
 extern "C" size_t gq_linear_i8_workspace_bytes(int64_t n, int k, int out) {
   using namespace gq;
   if (!valid_shape(n, out, k) || n == 0) return 0;
+  if (few_codes(n, k)) return 0;
   const bool wide = !few(n, k) && wants_wide(make_plan(n, out, k, true, false), true);
   const size_t split = code_bytes(n, k, wide) + round256((size_t)n * 4) + gemm_ws(n, out, k, false, true);
   const size_t fused = rows_fit(n, out, k) ? code_bytes(out, k, true) : 0;
@@ -1654,7 +1660,8 @@ extern "C" int gq_linear_i8(const void* X, int type, int64_t n, int k, int64_t l
       !aligned(W, 16) || !aligned(Y, type_bytes(y_type)) || !aligned(scale_w, 4) || !aligned(bias, 4) ||
       !aligned(dev_err, 4))
     return GQ_ERR_INVALID_ARG;
-  if (ws == nullptr || !aligned(ws, 256) || ws_bytes < gq_linear_i8_workspace_bytes(n, k, out)) return GQ_ERR_WORKSPACE;
+  const size_t need = gq_linear_i8_workspace_bytes(n, k, out);
+  if (need > 0 && (ws == nullptr || !aligned(ws, 256) || ws_bytes < need)) return GQ_ERR_WORKSPACE;
   cudaStream_t s = (cudaStream_t)stream;
   const int relu = act == GQ_ACT_RELU;
   const int64_t ld = round16(k);
@@ -1665,7 +1672,7 @@ extern "C" int gq_linear_i8(const void* X, int type, int64_t n, int k, int64_t l
     return rows_gemm(X, type, n, k, ldx, Operand{qw, ld, scale_w}, out, bias, relu, Y, y_type, ldy, dev_err, s);
   }
   float* sc = static_cast<float*>(w.take((size_t)n * 4));
-  if (few(n, k) && n * round16(k) <= kFewCodes) {
+  if (few_codes(n, k)) {
     const Operand b{W, ldw, scale_w};
     switch (type) {
       case GQ_F32:

@@ -158,6 +158,21 @@ def test_steps_8bit(pt, gt):
             block0 += (n + 255) // 256
 
 
+def test_moments_are_separate_roundings():
+    """Products and their sum are rounded one by one: where b1 m and (1 - b1) g
+    cancel, what is left is exactly 0, and no rounding error of a product."""
+    q = gq()
+    n = 1 << 16
+    gen = _gen(31)
+    g = torch.randn(n, device="cuda", generator=gen)
+    o = np.float32(1.0 - B1)
+    m0 = (-(g.cpu().numpy() * o) / np.float32(B1)).astype(np.float32)
+    left = m0 * np.float32(B1) + g.cpu().numpy() * o
+    m, v, p = torch.from_numpy(m0).cuda(), torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    q.AdamW([p], LR, (B1, B2), EPS, WD, state=([m], [v]), step=7).step([g])
+    assert (left == 0).sum() > n // 4 and np.array_equal(m.cpu().numpy(), left)
+
+
 def test_values_of_every_code():
     q = gq()
     codes = torch.arange(256, dtype=torch.int32).to(torch.uint8).repeat(7).cuda()

@@ -6,8 +6,8 @@ u = 2^-24.  For a segment and group with mean m, D = max |x - m|:
       at most rows + K2 for a segment that one block takes; for one cut into
       chunks rows / 2,368 (16 chunks for each of 148 SMs) + 5 of a thread,
       5 channels-of-a-group + 21 where they are combined
-  K2  threads of a channel (512 threads, at most 8 channels each: 4096 / d + 1)
-      and a warp's sum over channels: + cg / 32 + 48
+  K2  threads of a channel (256 threads of at least one channel each; 4096 / d + 1
+      is more) and the lanes' sum over a group's channels: + cg / 32 + 48
   mean:  e_m = u (2 K D + (2 K2 + 8) (|m| + D))    (shifted values, then parts' means)
   var:   e_v = 4 u (K + K2 + 20) D^2 + 2 D e_m + e_m^2
   rstd:  e_r = e_v / (2 (var + eps)) + 3u, relative
