@@ -29,7 +29,7 @@
 // instructions: x ^ 0x80 is x + 128; put under the byte 0x64 it is the fp16 number
 // 1024 + 128 + x, and one packed subtraction of 1152 leaves x.
 // Rows in full precision of up to 256 values are quantized by such warps on the
-// way (2,449,029 x 256 fp32 -> 256: 1.10 ms instead of 0.54 + 0.61).
+// way (2,449,029 x 256 fp32 -> 256: 0.97 ms instead of 0.45 + 0.61).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -180,37 +180,48 @@ struct Scale {
 };
 __device__ __forceinline__ Scale make_scale(uint32_t bits) {
   const float top = __uint_as_float(bits);
+  const bool use = top < INFINITY && top >= kTiny;  // not for a NaN
+  const float s = __fdiv_rn(use ? top : 127.0f, 127.0f), inv = __fdiv_rn(1.0f, s);
   Scale r;
-  if (!(top < INFINITY)) {  // infinite or NaN
-    r.s = __int_as_float(0x7fc00000);
-    r.inv = r.half = 0.0f;
-    return r;
-  }
-  r.s = top < kTiny ? 0.0f : __fdiv_rn(top, 127.0f);
-  r.inv = top < kTiny ? 0.0f : __fdiv_rn(1.0f, r.s);
-  r.half = 0.5f * r.s;
+  r.s = use ? s : top < kTiny ? 0.0f : __int_as_float(0x7fc00000);
+  r.inv = use ? inv : 0.0f;
+  r.half = use ? 0.5f * s : 0.0f;
   return r;
 }
 // round(x / s), ties to even, exactly: q within one of it from the reciprocal,
 // then by the remainder x - q s, which a fused multiply-add gives exactly
-// (it is a multiple of half a step of s and no larger than s).  q is the last bits
-// of 1.5 2^23 + x / s, whose low byte is the code: conversions and roundings go
-// through the special function unit at an eighth of the speed.
+// (it is a multiple of half a step of s and no larger than s).  q comes by adding
+// 1.5 2^23: conversions and roundings go through the special function unit at
+// an eighth of the speed.  Four values have one branch for the rare remainder.
 constexpr float kMagic = 12582912.0f;
-__device__ __forceinline__ uint32_t quantize(float x, const Scale& c) {
-  const float t = fmaf(x, c.inv, kMagic);
-  const float q = t - kMagic;
-  const float r = fmaf(-q, c.s, x);
-  uint32_t k = __float_as_uint(t);
-  if (fabsf(r) >= c.half) {  // rare
-    if (c.inv > 0.0f && (fabsf(r) > c.half || (k & 1))) k += r > 0.0f ? 1 : -1;
+__device__ __forceinline__ float4 quantize4(const float4& x, const Scale& c) {
+  const float2 inv = make_float2(c.inv, c.inv), s = make_float2(-c.s, -c.s);
+  const float2 up = make_float2(kMagic, kMagic), down = make_float2(-kMagic, -kMagic);
+  const float2 xa = make_float2(x.x, x.y), xb = make_float2(x.z, x.w);
+  float2 a = add2(fma2(xa, inv, up), down), b = add2(fma2(xb, inv, up), down);
+  const float2 ra = fma2(a, s, xa), rb = fma2(b, s, xb);
+  const float far = fmaxf(fmaxf(fabsf(ra.x), fabsf(ra.y)), fmaxf(fabsf(rb.x), fabsf(rb.y)));
+  if (far >= c.half && c.inv > 0.0f) {  // rare
+    auto fix = [&](float q, float r) {
+      const bool odd = __float_as_uint(q + kMagic) & 1;
+      return fabsf(r) > c.half || (fabsf(r) == c.half && odd) ? q + (r > 0.0f ? 1.0f : -1.0f) : q;
+    };
+    a = make_float2(fix(a.x, ra.x), fix(a.y, ra.y));
+    b = make_float2(fix(b.x, rb.x), fix(b.y, rb.y));
   }
-  return k;
+  if (!(c.inv > 0.0f)) a = b = make_float2(0.0f, 0.0f);
+  return make_float4(a.x, a.y, b.x, b.y);
 }
-// four codes of them, as bytes or as fp16
-__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, const Scale& s) {
-  const uint32_t w = __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
-  return s.inv > 0.0f ? w : 0u;
+__device__ __forceinline__ uint32_t code(float q) { return __float_as_uint(q + kMagic); }  // in the low byte
+__device__ __forceinline__ uint32_t bytes4(const float4& q) {
+  return __byte_perm(__byte_perm(code(q.x), code(q.y), 0x0040), __byte_perm(code(q.z), code(q.w), 0x0040), 0x5410);
+}
+__device__ __forceinline__ uint2 halves4(const float4& q) {
+  const __half2 a = __floats2half2_rn(q.x, q.y), b = __floats2half2_rn(q.z, q.w);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+__device__ __forceinline__ float quantize1(float x, const Scale& c) {
+  return quantize4(make_float4(x, 0.0f, 0.0f, 0.0f), c).x;
 }
 // 4 bytes -> 4 fp16
 __device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -222,14 +233,17 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
   lo = *reinterpret_cast<const uint32_t*>(&x);
   hi = *reinterpret_cast<const uint32_t*>(&y);
 }
-__device__ __forceinline__ void put4(int8_t* q, uint32_t w) { *reinterpret_cast<uint32_t*>(q) = w; }
-__device__ __forceinline__ void put4(__half* q, uint32_t w) {
+// four codes (from floats, or from a word of bytes) and one
+__device__ __forceinline__ void put4(int8_t* o, const float4& q) { *reinterpret_cast<uint32_t*>(o) = bytes4(q); }
+__device__ __forceinline__ void put4(__half* o, const float4& q) { *reinterpret_cast<uint2*>(o) = halves4(q); }
+__device__ __forceinline__ void put4(int8_t* o, uint32_t w) { *reinterpret_cast<uint32_t*>(o) = w; }
+__device__ __forceinline__ void put4(__half* o, uint32_t w) {
   uint2 h;
   widen(w, h.x, h.y);
-  *reinterpret_cast<uint2*>(q) = h;
+  *reinterpret_cast<uint2*>(o) = h;
 }
-__device__ __forceinline__ void put1(int8_t* q, uint32_t w) { *q = (int8_t)w; }
-__device__ __forceinline__ void put1(__half* q, uint32_t w) { *q = __int2half_rn((int)(int8_t)w); }
+__device__ __forceinline__ void put1(int8_t* o, float q) { *o = (int8_t)code(q); }
+__device__ __forceinline__ void put1(__half* o, float q) { *o = __float2half_rn(q); }
 __device__ __forceinline__ uint32_t mag(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
 // 4 consecutive values of a row
@@ -283,7 +297,7 @@ __global__ void __launch_bounds__(kQThreads)
   for (int i = 0; i < NV; ++i) {
     const int at = i * 128 + lane * 4;  // ldq is a multiple of 16: the last four may reach behind d
     if (at < d)
-      put4(q + at, pack4(quantize(v[i].x, c), quantize(v[i].y, c), quantize(v[i].z, c), quantize(v[i].w, c), c));
+      put4(q + at, quantize4(v[i], c));
   }
 }
 
@@ -328,12 +342,12 @@ __global__ void __launch_bounds__(kQThreads)
 #pragma unroll 4
     for (int k = lane * 4; k < d4; k += LANES * 4) {
       const float4 v = load4<T>(x + k);
-      put4(q + k, pack4(quantize(v.x, c), quantize(v.y, c), quantize(v.z, c), quantize(v.w, c), c));
+      put4(q + k, quantize4(v, c));
     }
-    if (d4 + lane < d) put1(q + d4 + lane, pack4(quantize((float)x[d4 + lane], c), 0, 0, 0, c));
+    if (d4 + lane < d) put1(q + d4 + lane, quantize1((float)x[d4 + lane], c));
   } else {
 #pragma unroll 8
-    for (int k = lane; k < d; k += LANES) put1(q + k, pack4(quantize((float)x[k], c), 0, 0, 0, c));
+    for (int k = lane; k < d; k += LANES) put1(q + k, quantize1((float)x[k], c));
   }
 }
 
@@ -448,10 +462,10 @@ __global__ void __launch_bounds__(kQThreads)
     for (int h = 0; h < 2; ++h) {
       uint32_t* o = &tile[4 * cv][rg + 16 * h];
       const Scale a = sc[4 * cv], b = sc[4 * cv + 1], c = sc[4 * cv + 2], e = sc[4 * cv + 3];
-      o[0] = pack4(quantize(v[h][0].x, a), quantize(v[h][1].x, a), quantize(v[h][2].x, a), quantize(v[h][3].x, a), a);
-      o[kTrPitch] = pack4(quantize(v[h][0].y, b), quantize(v[h][1].y, b), quantize(v[h][2].y, b), quantize(v[h][3].y, b), b);
-      o[2 * kTrPitch] = pack4(quantize(v[h][0].z, c), quantize(v[h][1].z, c), quantize(v[h][2].z, c), quantize(v[h][3].z, c), c);
-      o[3 * kTrPitch] = pack4(quantize(v[h][0].w, e), quantize(v[h][1].w, e), quantize(v[h][2].w, e), quantize(v[h][3].w, e), e);
+      o[0] = bytes4(quantize4(make_float4(v[h][0].x, v[h][1].x, v[h][2].x, v[h][3].x), a));
+      o[kTrPitch] = bytes4(quantize4(make_float4(v[h][0].y, v[h][1].y, v[h][2].y, v[h][3].y), b));
+      o[2 * kTrPitch] = bytes4(quantize4(make_float4(v[h][0].z, v[h][1].z, v[h][2].z, v[h][3].z), c));
+      o[3 * kTrPitch] = bytes4(quantize4(make_float4(v[h][0].w, v[h][1].w, v[h][2].w, v[h][3].w), e));
     }
     __syncthreads();
     // rows of Q are a multiple of 16 codes: those past n are written as 0
@@ -1048,21 +1062,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&xempty[slot]);
+        Scale c[per_warp];  // the rows' chains of steps lie side by side
 #pragma unroll
         for (int r = 0; r < per_warp; ++r) {
           const float4 &u = v[r][0], &w = v[r][1];
           const uint32_t top = max(max(max(mag(u.x), mag(u.y)), max(mag(u.z), mag(u.w))),
                                    max(max(mag(w.x), mag(w.y)), max(mag(w.z), mag(w.w))));
-          const Scale c = make_scale(__reduce_max_sync(FULL, top));
+          c[r] = make_scale(__reduce_max_sync(FULL, top));
+        }
+#pragma unroll
+        for (int r = 0; r < per_warp; ++r) {
           const int row = k * piece_rows + cw * per_warp + r;
-          if (lane == 0) sc[row] = c.s;
+          if (lane == 0) sc[row] = c[r].s;
           // columns 4 l .. of a 64-column step: 8 bytes of the 16-byte piece l / 2 of the row
           uint8_t* dst = sS + (lane >> 4) * kSBytes + row * 128 + ((((lane & 15) >> 1) ^ (row & 7)) << 4) + (lane & 1) * 8;
-          uint2 h;
-          widen(pack4(quantize(u.x, c), quantize(u.y, c), quantize(u.z, c), quantize(u.w, c), c), h.x, h.y);
-          *reinterpret_cast<uint2*>(dst) = h;
-          widen(pack4(quantize(w.x, c), quantize(w.y, c), quantize(w.z, c), quantize(w.w, c), c), h.x, h.y);
-          *reinterpret_cast<uint2*>(dst + 2 * kSBytes) = h;
+          *reinterpret_cast<uint2*>(dst) = halves4(quantize4(v[r][0], c[r]));
+          *reinterpret_cast<uint2*>(dst + 2 * kSBytes) = halves4(quantize4(v[r][1], c[r]));
         }
         if (++slot == kRowSlots) {
           slot = 0;
@@ -1207,7 +1222,7 @@ __global__ void __launch_bounds__(256)
       const Scale c = make_scale(__reduce_max_sync(FULL, top));
       if (lane == 0) scale[m] = c.s;
 #pragma unroll 8
-      for (int k = lane; k < K; k += 32) codes[m * pitch + k] = (uint8_t)pack4(quantize((float)x[k], c), 0, 0, 0, c);
+      for (int k = lane; k < K; k += 32) codes[m * pitch + k] = (uint8_t)code(quantize1((float)x[k], c));
     }
     __syncthreads();
   }
