@@ -492,7 +492,7 @@ int launch_p(int pt, int gt, int bits, const Batch<CAP>& b, int64_t tiles, const
 
 // The tensors travel as kernel parameters (no table in device memory that a
 // captured graph and an eager call would share): 16 of them for the usual
-// small model, so that its launch carries 2 KB, up to 256 otherwise (29 KB of
+// small model, so that its launch carries 2 KB, up to 256 otherwise (25 KB of
 // the 32,764 bytes that a kernel may take).
 template <int CAP>
 int run(const gq_adamw_tensor* ts, int count, int pt, int gt, int bits, const Coef& c, const DevRecord* rec,
