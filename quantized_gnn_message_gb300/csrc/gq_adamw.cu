@@ -46,6 +46,7 @@ struct Coef {
   float lr1;              // lr / (1 - b1^t)
   float rs2;              // 1 / sqrt(1 - b2^t)
   float eps;
+  float one;              // 1, which the compiler does not know
   uint32_t key;           // of the rounding noise
 };
 
@@ -85,6 +86,7 @@ Coef make_coef(const gq_adamw_args& a, int64_t step) {
   c.lr1 = (float)(a.lr / (1.0 - std::pow(a.beta1, (double)step)));
   c.rs2 = (float)(1.0 / std::sqrt(1.0 - std::pow(a.beta2, (double)step)));
   c.eps = (float)a.eps;
+  c.one = 1.0f;
   c.key = seed_key_host(a.seed + (uint64_t)step * 0x9E3779B97F4A7C15ULL);
   return c;
 }
@@ -103,6 +105,7 @@ __global__ void begin_kernel(DevRecord* rec, const gq_adamw_args a, const float*
   c.lr1 = (float)(lr / (1.0 - pow(a.beta1, (double)step)));
   c.rs2 = (float)(1.0 / sqrt(1.0 - pow(a.beta2, (double)step)));
   c.eps = (float)a.eps;
+  c.one = 1.0f;
   c.key = fmix32(seed_fold(a.seed + (uint64_t)step * 0x9E3779B97F4A7C15ULL));
   rec->coef = c;
 }
@@ -245,15 +248,16 @@ __device__ __forceinline__ float rcp_fast(float x) {
   return y;
 }
 
-// a + b rounded by itself: a packed sum of packed products may be fused with them
-__device__ __forceinline__ float2 sum2(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
+// a + b rounded by itself, as a one + b: a packed sum of packed products is
+// fused with them, also where the 1 is a constant
+__device__ __forceinline__ float2 sum2(float2 a, float2 b, float one) { return fma2(a, both(one), b); }
 
 // Two values.  The moments' update is products and a sum, each rounded: the codes
 // can be reproduced from elementary operations.  The root and the reciprocal are
 // the special function unit's (a step off each): their quotient is lr times smaller than p.
 __device__ __forceinline__ void update(float2& p, float2 g, float2& m, float2& v, const Coef& c) {
-  m = sum2(mul2(m, both(c.b1)), mul2(g, both(c.o1)));
-  v = sum2(mul2(v, both(c.b2)), mul2(mul2(g, g), both(c.o2)));
+  m = sum2(mul2(m, both(c.b1)), mul2(g, both(c.o1)), c.one);
+  v = sum2(mul2(v, both(c.b2)), mul2(mul2(g, g), both(c.o2)), c.one);
   const float2 den = fma2(make_float2(sqrt_fast(v.x), sqrt_fast(v.y)), both(c.rs2), both(c.eps));
   const float2 step = mul2(mul2(m, both(-c.lr1)), make_float2(rcp_fast(den.x), rcp_fast(den.y)));
   p = fma2(p, both(c.keep), step);

@@ -355,15 +355,41 @@ __global__ void __launch_bounds__(kQThreads)
 // for, their sums: a block takes kColW columns (a thread four of them) and one
 // piece of the rows.
 constexpr int kColW = 64, kColRows = kQThreads / (kColW / 4), kMaxParts = 128;
-template <typename T, bool VEC>
-__device__ __forceinline__ float4 load_cols(const T* x, int left) {  // `left` columns are there
-  if (VEC && left >= 4) return load4<T>(x);
+template <typename T>
+__device__ __forceinline__ float4 load_cols(const T* x, int left, int vec) {  // `left` columns are there
+  if (vec && left >= 4) return load4<T>(x);
   return make_float4(left > 0 ? (float)x[0] : 0.0f, left > 1 ? (float)x[1] : 0.0f, left > 2 ? (float)x[2] : 0.0f,
                      left > 3 ? (float)x[3] : 0.0f);
 }
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kQThreads)
-    col_max_kernel(const T* X, int64_t n, int d, int64_t ldx, int64_t rows_per, uint32_t* top, float* sums) {
+// One matrix; two of them share the launches of the backward pass.
+template <typename T, typename O>
+struct ColJob {
+  const T* X;
+  int64_t n;
+  int d;
+  int64_t ldx;
+  int vec;               // rows start aligned for four values
+  int parts;
+  int64_t rows_per;
+  uint32_t* top;         // [parts][d]
+  float* sums;           // [parts][d], or null
+  O* Q;
+  int64_t ldq;
+  float* S;
+  float* colsum;
+};
+template <typename T, typename O>
+struct ColJobs {
+  ColJob<T, O> of[2];
+};
+
+template <typename T, typename O>
+__global__ void __launch_bounds__(kQThreads) col_max_kernel(const __grid_constant__ ColJobs<T, O> jobs) {
+  const ColJob<T, O>& p = jobs.of[blockIdx.z];
+  const T* X = p.X;
+  const int64_t n = p.n, ldx = p.ldx, rows_per = p.rows_per;
+  const int d = p.d, vec = p.vec;
+  if ((int)blockIdx.x * kColW >= d || (int)blockIdx.y >= p.parts) return;
   __shared__ uint32_t st[kColRows][kColW];
   __shared__ float ss[kColRows][kColW];
   grid_wait();
@@ -377,7 +403,7 @@ __global__ void __launch_bounds__(kQThreads)
     float4 v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      v[u] = load_cols<T, VEC>(X + (r + u * kColRows) * ldx + c, r + u * kColRows < r1 ? d - c : 0);
+      v[u] = load_cols<T>(X + (r + u * kColRows) * ldx + c, r + u * kColRows < r1 ? d - c : 0, vec);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       m[0] = max(m[0], mag(v[u].x));
@@ -405,18 +431,24 @@ __global__ void __launch_bounds__(kQThreads)
       a = max(a, st[k][x]);
       b += ss[k][x];
     }
-    top[(int64_t)blockIdx.y * d + col] = a;
-    if (sums != nullptr) sums[(int64_t)blockIdx.y * d + col] = b;
+    p.top[(int64_t)blockIdx.y * d + col] = a;
+    if (p.sums != nullptr) p.sums[(int64_t)blockIdx.y * d + col] = b;
   }
 }
 
 // Then the pieces' largest and the sums together, by every block for its 64
 // columns, and tiles of 128 rows turned into 64 rows of 128 codes.
 constexpr int kTrRows = 128, kTrPitch = kTrRows / 4 + 1;  // words
-template <typename T, typename O, bool VEC>
-__global__ void __launch_bounds__(kQThreads)
-    quant_cols_kernel(const T* X, int64_t n, int d, int64_t ldx, const uint32_t* top, const float* sums, int parts, O* Q,
-                      int64_t ldq, float* S, float* colsum) {
+template <typename T, typename O>
+__global__ void __launch_bounds__(kQThreads) quant_cols_kernel(const __grid_constant__ ColJobs<T, O> jobs) {
+  const ColJob<T, O>& p = jobs.of[blockIdx.z];
+  const T* X = p.X;
+  const int64_t n = p.n, ldx = p.ldx, ldq = p.ldq;
+  const int d = p.d, vec = p.vec, parts = p.parts;
+  const float* sums = p.sums;
+  O* Q = p.Q;
+  const int64_t tiles = (n + kTrRows - 1) / kTrRows;
+  if ((int)blockIdx.y * kColW >= d || (int64_t)blockIdx.x >= tiles) return;
   __shared__ uint32_t tile[kColW][kTrPitch];
   __shared__ uint32_t smax[4][kColW];
   __shared__ float ssum[4][kColW];
@@ -429,9 +461,9 @@ __global__ void __launch_bounds__(kQThreads)
     float s = 0.0f;
     if (c0 + x < d)
 #pragma unroll 8
-      for (int p = y; p < parts; p += 4) {
-        m = max(m, top[(int64_t)p * d + c0 + x]);
-        if (sums != nullptr && blockIdx.x == 0) s += sums[(int64_t)p * d + c0 + x];
+      for (int k = y; k < parts; k += 4) {
+        m = max(m, p.top[(int64_t)k * d + c0 + x]);
+        if (sums != nullptr && blockIdx.x == 0) s += sums[(int64_t)k * d + c0 + x];
       }
     smax[y][x] = m;
     ssum[y][x] = s;
@@ -439,15 +471,14 @@ __global__ void __launch_bounds__(kQThreads)
     if (t < kColW) {
       sc[t] = make_scale(max(max(smax[0][t], smax[1][t]), max(smax[2][t], smax[3][t])));
       if (blockIdx.x == 0 && c0 + t < d) {
-        S[c0 + t] = sc[t].s;
-        if (sums != nullptr) colsum[c0 + t] = (ssum[0][t] + ssum[1][t]) + (ssum[2][t] + ssum[3][t]);
+        p.S[c0 + t] = sc[t].s;
+        if (sums != nullptr) p.colsum[c0 + t] = (ssum[0][t] + ssum[1][t]) + (ssum[2][t] + ssum[3][t]);
       }
     }
     __syncthreads();
   }
   const int cv = t % 16, rg = t / 16;  // four columns, four rows
   const int left = d - c0 - 4 * cv;
-  const int64_t tiles = (n + kTrRows - 1) / kTrRows;
   for (int64_t k = blockIdx.x; k < tiles; k += gridDim.x) {
     const int64_t r0 = k * kTrRows;
     float4 v[2][4];
@@ -456,7 +487,7 @@ __global__ void __launch_bounds__(kQThreads)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int64_t r = r0 + (rg + 16 * h) * 4 + j;
-        v[h][j] = load_cols<T, VEC>(X + r * ldx + c0 + 4 * cv, r < n ? left : 0);
+        v[h][j] = load_cols<T>(X + r * ldx + c0 + 4 * cv, r < n ? left : 0, vec);
       }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -1552,19 +1583,42 @@ int64_t col_parts(int64_t n, int d) {
 }
 size_t cols_ws(int64_t n, int d, int sums) { return (size_t)col_parts(n, d) * d * 4 * (sums ? 2 : 1); }
 
-template <typename T, typename O, bool VEC>
-int quant_cols(const T* X, int64_t n, int d, int64_t ldx, O* Q, int64_t ldq, float* S, float* colsum, void* ws,
-               cudaStream_t s) {
-  const int64_t parts = col_parts(n, d), rows_per = (n + parts - 1) / parts;
-  uint32_t* top = static_cast<uint32_t*>(ws);
-  float* sums = colsum != nullptr ? reinterpret_cast<float*>(top + parts * d) : nullptr;
-  const unsigned gx = (unsigned)((d + kColW - 1) / kColW);
-  GQ_TRY(launch_after(col_max_kernel<T, VEC>, dim3(gx, (unsigned)parts), dim3(kQThreads), 0, s, X, n, d, ldx, rows_per, top,
-                      sums));
-  int64_t tiles = (n + kTrRows - 1) / kTrRows, most = (8 * (int64_t)sm_count() + gx - 1) / gx;
+template <typename T, typename O>
+ColJob<T, O> col_job(const T* X, int64_t n, int d, int64_t ldx, O* Q, int64_t ldq, float* S, float* colsum, void* ws) {
+  ColJob<T, O> j{};
+  j.X = X;
+  j.n = n;
+  j.d = d;
+  j.ldx = ldx;
+  j.vec = aligned(X, 4 * sizeof(T)) && ldx % 4 == 0;
+  j.parts = (int)col_parts(n, d);
+  j.rows_per = (n + j.parts - 1) / j.parts;
+  j.top = static_cast<uint32_t*>(ws);
+  j.sums = colsum != nullptr ? reinterpret_cast<float*>(j.top + (int64_t)j.parts * d) : nullptr;
+  j.Q = Q;
+  j.ldq = ldq;
+  j.S = S;
+  j.colsum = colsum;
+  return j;
+}
+
+template <typename T, typename O>
+int quant_cols(const ColJobs<T, O>& jobs, int count, cudaStream_t s) {
+  unsigned gx = 1, gy = 1;
+  int64_t tiles = 1;
+  for (int k = 0; k < count; ++k) {
+    const ColJob<T, O>& j = jobs.of[k];
+    const unsigned w = (unsigned)((j.d + kColW - 1) / kColW);
+    const int64_t t = (j.n + kTrRows - 1) / kTrRows;
+    if (w > gx) gx = w;
+    if ((unsigned)j.parts > gy) gy = (unsigned)j.parts;
+    if (t > tiles) tiles = t;
+  }
+  GQ_TRY(launch_after(col_max_kernel<T, O>, dim3(gx, gy, (unsigned)count), dim3(kQThreads), 0, s, jobs));
+  int64_t most = (8 * (int64_t)sm_count() + gx - 1) / gx;
   if (most < 1) most = 1;
-  return launch_after(quant_cols_kernel<T, O, VEC>, dim3((unsigned)(tiles < most ? tiles : most), gx), dim3(kQThreads), 0, s,
-                      X, n, d, ldx, top, sums, (int)parts, Q, ldq, S, colsum);
+  return launch_after(quant_cols_kernel<T, O>, dim3((unsigned)(tiles < most ? tiles : most), gx, (unsigned)count),
+                      dim3(kQThreads), 0, s, jobs);
 }
 
 template <typename T, typename O>
@@ -1573,8 +1627,9 @@ int quant_to(const void* X, int64_t n, int d, int64_t ldx, int transpose, void* 
   const T* x = static_cast<const T*>(X);
   O* q = static_cast<O*>(Q);
   if (!transpose) return quant_rows(x, n, d, ldx, q, ldq, S, s);
-  if (aligned(x, 4 * sizeof(T)) && ldx % 4 == 0) return quant_cols<T, O, true>(x, n, d, ldx, q, ldq, S, colsum, ws, s);
-  return quant_cols<T, O, false>(x, n, d, ldx, q, ldq, S, colsum, ws, s);
+  ColJobs<T, O> jobs;
+  jobs.of[0] = jobs.of[1] = col_job(x, n, d, ldx, q, ldq, S, colsum, ws);
+  return quant_cols(jobs, 1, s);
 }
 
 int quant(const void* X, int type, int64_t n, int d, int64_t ldx, int transpose, bool wide, void* Q, int64_t ldq, float* S,
@@ -1727,6 +1782,24 @@ struct Side {
   int64_t ldx;
   int transpose;
 };
+// two matrices of one type by columns, to the same kind of codes
+template <typename T, typename O>
+int quant_pair_to(const Side& a, void* qa, float* sa, float* colsum, void* ca, const Side& b, void* qb, float* sb, void* cb,
+                  int64_t ld, cudaStream_t s) {
+  ColJobs<T, O> jobs;
+  jobs.of[0] = col_job(static_cast<const T*>(a.X), a.n, a.d, a.ldx, static_cast<O*>(qa), ld, sa, colsum, ca);
+  jobs.of[1] = col_job(static_cast<const T*>(b.X), b.n, b.d, b.ldx, static_cast<O*>(qb), ld, sb, (float*)nullptr, cb);
+  return quant_cols(jobs, 2, s);
+}
+template <typename O>
+int quant_pair(const Side& a, void* qa, float* sa, float* colsum, void* ca, const Side& b, void* qb, float* sb, void* cb,
+               int64_t ld, cudaStream_t s) {
+  switch (a.type) {
+    case GQ_F32: return quant_pair_to<float, O>(a, qa, sa, colsum, ca, b, qb, sb, cb, ld, s);
+    case GQ_BF16: return quant_pair_to<__nv_bfloat16, O>(a, qa, sa, colsum, ca, b, qb, sb, cb, ld, s);
+    default: return quant_pair_to<__half, O>(a, qa, sa, colsum, ca, b, qb, sb, cb, ld, s);
+  }
+}
 size_t product_ws(int64_t m, int64_t n, int64_t k, bool ta, bool tb, bool sums) {
   const bool tiny = few(m, k);
   const Plan z = make_plan(m, n, k, true, true);
@@ -1755,8 +1828,13 @@ int product(const Side& a, const Side& b, int64_t m, int64_t n, int64_t k, float
   float* sb = static_cast<float*>(w.take((size_t)n * 4));
   void* ca = a.transpose ? w.take(cols_ws(a.n, a.d, colsum != nullptr)) : nullptr;
   void* cb = b.transpose ? w.take(cols_ws(b.n, b.d, 0)) : nullptr;
-  GQ_TRY(quant(a.X, a.type, a.n, a.d, a.ldx, a.transpose, wa, qa, ld, sa, colsum, ca, s));
-  GQ_TRY(quant(b.X, b.type, b.n, b.d, b.ldx, b.transpose, wb, qb, ld, sb, nullptr, cb, s));
+  if (a.transpose && b.transpose && a.type == b.type && wa == wb) {
+    GQ_TRY(wa ? quant_pair<__half>(a, qa, sa, colsum, ca, b, qb, sb, cb, ld, s)
+              : quant_pair<int8_t>(a, qa, sa, colsum, ca, b, qb, sb, cb, ld, s));
+  } else {
+    GQ_TRY(quant(a.X, a.type, a.n, a.d, a.ldx, a.transpose, wa, qa, ld, sa, colsum, ca, s));
+    GQ_TRY(quant(b.X, b.type, b.n, b.d, b.ldx, b.transpose, wb, qb, ld, sb, nullptr, cb, s));
+  }
   const Operand A{qa, ld, sa}, B{qb, ld, sb};
   if (tiny) return few_gemm(A, m, B, n, k, nullptr, 0, C, type, ldc, s);
   return tile_gemm(z, A, B, k, nullptr, 0, C, type, ldc, z.sums > 0 ? w.take(z.sums) : nullptr, err, s);
