@@ -142,15 +142,6 @@ __device__ __forceinline__ void regs_up() {
 }
 
 // ------------------------------------------------------------------- types --
-template <typename T>
-__device__ __forceinline__ T from_f(float x);
-template <>
-__device__ __forceinline__ float from_f<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-template <>
-__device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
-
 // Stores one value of the output type chosen at run time.
 __device__ __forceinline__ void store_as(void* base, int64_t i, float x, int type) {
   if (type == GQ_F32)
