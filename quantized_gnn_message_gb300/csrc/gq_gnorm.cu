@@ -330,7 +330,7 @@ __device__ __forceinline__ void spread(const Args& p, int64_t r0, int64_t r1, in
 // What the backward pass needs of a thread's channels (mean negated).
 template <int V>
 struct Chan {
-  Pk<V> mu, rs, ga, be;
+  Pk<V> mu, rs, ga, sc, be;
 };
 template <int V>
 __device__ __forceinline__ void channels(const Args& p, int64_t j, int c, Chan<V>& h) {
@@ -340,8 +340,17 @@ __device__ __forceinline__ void channels(const Args& p, int64_t j, int c, Chan<V
     h.mu.e[e] = -p.mean[g];
     h.rs.e[e] = p.rstd[g];
     h.ga.e[e] = p.gamma != nullptr ? p.gamma[c + e] : 1.0f;
+    h.sc.e[e] = __fmul_rn(h.rs.e[e], h.ga.e[e]);
     h.be.e[e] = p.beta != nullptr ? p.beta[c + e] : 0.0f;
   }
+}
+
+// z once more.  ReLU's from sc = rstd gamma, by forward's own operations: next to 0
+// another order of them has another sign, and ReLU would stop gradients of
+// values that it let through.  SiLU's slope is smooth, and xhat is there.
+template <int ACT, int V>
+__device__ __forceinline__ Pk<V> again(const Pk<V>& xc, const Pk<V>& xh, const Chan<V>& h) {
+  return ACT == GQ_ACT_RELU ? fma(xc, h.sc, h.be) : fma(xh, h.ga, h.be);
 }
 
 // sums of dz xhat and of dz
@@ -356,8 +365,8 @@ __device__ __forceinline__ void slopes(const Args& p, int64_t r0, int64_t r1, in
   const T* y = static_cast<const T*>(p.dY) + first * p.lddy + c;
   const int64_t sx = (int64_t)p.ry * p.ldx, sy = (int64_t)p.ry * p.lddy;
   auto use = [&](const Raw<T, V>& wx, const Raw<T, V>& wy) {
-    const Pk<V> xh = mul(add(value(wx), h.mu), h.rs);
-    const Pk<V> dz = ACT == GQ_ACT_NONE ? value(wy) : slope<ACT>(value(wy), fma(xh, h.ga, h.be));
+    const Pk<V> xc = add(value(wx), h.mu), xh = mul(xc, h.rs);
+    const Pk<V> dz = ACT == GQ_ACT_NONE ? value(wy) : slope<ACT>(value(wy), again<ACT>(xc, xh, h));
     a = fma(dz, xh, a);
     b = add(b, dz);
   };
@@ -403,6 +412,8 @@ template <typename T, int V, int ACT>
 __device__ __forceinline__ void apply_bwd(const Args& p, int64_t r0, int64_t r1, int ry, int c, const Chan<V>& h,
                                           const Pk<V>& h1, const Pk<V>& h2) {  // the means of h and h xhat, negated
   constexpr int U = Ahead<V>::bwd;
+  // sc is there for ReLU: with rstd in the means too, no gamma is held beside it
+  const Pk<V> k1 = mul(h.rs, h1), k2 = mul(h.rs, h2);
   const int64_t first = r0 + ry;
   const int rows = first < r1 ? (int)((r1 - first + p.ry - 1) / p.ry) : 0;
   const T* x = static_cast<const T*>(p.X) + first * p.ldx + c;
@@ -410,8 +421,9 @@ __device__ __forceinline__ void apply_bwd(const Args& p, int64_t r0, int64_t r1,
   T* o = static_cast<T*>(p.Y) + first * p.ldy + c;
   const int64_t sx = (int64_t)p.ry * p.ldx, sy = (int64_t)p.ry * p.lddy, so = (int64_t)p.ry * p.ldy;
   auto use = [&](const Raw<T, V>& wx, const Raw<T, V>& wy) {
-    const Pk<V> xh = mul(add(value(wx), h.mu), h.rs);
-    const Pk<V> dz = ACT == GQ_ACT_NONE ? value(wy) : slope<ACT>(value(wy), fma(xh, h.ga, h.be));
+    const Pk<V> xc = add(value(wx), h.mu), xh = mul(xc, h.rs);
+    const Pk<V> dz = ACT == GQ_ACT_NONE ? value(wy) : slope<ACT>(value(wy), again<ACT>(xc, xh, h));
+    if constexpr (ACT == GQ_ACT_RELU) return fma(dz, h.sc, fma(xh, k2, k1));
     return mul(h.rs, fma(xh, h2, fma(dz, h.ga, h1)));
   };
   int i = 0;
@@ -537,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 4) short_fwd_kernel(const Args p) {
         for (int e = 0; e < V; ++e) {
           const float2 w = ch[c + e];
           mu.e[e] = -w.x;
-          sc.e[e] = w.y * (p.gamma != nullptr ? p.gamma[c + e] : 1.0f);
+          sc.e[e] = __fmul_rn(w.y, p.gamma != nullptr ? p.gamma[c + e] : 1.0f);
           be.e[e] = p.beta != nullptr ? p.beta[c + e] : 0.0f;
         }
         apply<T, V, ACT>(p, r0, r1, ry, c, mu, sc, be);
@@ -744,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 4) apply_kernel(const Args p) {
     for (int e = 0; e < V; ++e) {
       const int64_t g = j * p.groups + (c + e) / p.cg;
       mu.e[e] = -p.mean[g];
-      sc.e[e] = p.rstd[g] * (p.gamma != nullptr ? p.gamma[c + e] : 1.0f);
+      sc.e[e] = __fmul_rn(p.rstd[g], p.gamma != nullptr ? p.gamma[c + e] : 1.0f);
       be.e[e] = p.beta != nullptr ? p.beta[c + e] : 0.0f;
     }
     apply<T, V, ACT>(p, r0, r1, ry, c, mu, sc, be);
