@@ -49,8 +49,9 @@ class GCNStack:
     normalization behind every hidden layer (its weights are the `norms` of
     forward and backward, a (gamma, beta) pair per hidden layer; gradients in
     dgamma, dbeta).  "group" takes groups, and, where the graph is a batch of
-    graphs, ptr, the int64 offsets of their nodes, and max_rows, the largest one's
-    number of nodes.  p: dropout rate of the hidden
+    graphs, ptr, the int64 offsets of their nodes (on the stack's device, rising from 0 to
+    the number of nodes: a node outside every graph would have no features; read
+    once, here), and max_rows, the largest one's number of nodes.  p: dropout rate of the hidden
     layers' outputs (training passes only).  classes: width of the class
     head behind the last layer (loss_and_grad, loss; gradient in dWc).  With
     norm or p the hand-off of dZ between layers is theirs, and fuse_dz does
@@ -68,8 +69,12 @@ class GCNStack:
             raise GQError('groups, ptr and max_rows go with norm="group"')
         if grouped and any(w % groups for w in widths[1:-1]):
             raise GQError(f"every hidden width must be a multiple of the {groups} groups")
-        if grouped and ptr is not None and (ptr.dtype != torch.int64 or ptr.dim() != 1 or ptr.numel() < 1):
-            raise GQError("ptr must be an int64 vector of node offsets")
+        if grouped and ptr is not None:
+            if ptr.dtype != torch.int64 or ptr.dim() != 1 or ptr.numel() < 1 or ptr.device.type != torch.device(device).type:
+                raise GQError("ptr must be an int64 vector of node offsets on the stack's device")
+            offsets = ptr.cpu()
+            if offsets[0] != 0 or offsets[-1] != g.n or (offsets[1:] < offsets[:-1]).any():
+                raise GQError(f"ptr must rise from 0 to the graph's {g.n} nodes")
         norm = bool(norm)
         self.groups, self.ptr, self.max_rows = groups, ptr, max_rows
         self.norm, self.p, self.classes = norm, float(p), classes
