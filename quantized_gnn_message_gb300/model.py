@@ -62,13 +62,13 @@ class GCNStack:
                  classes: int = 0, groups: int = 1, ptr: torch.Tensor | None = None, max_rows: int = 0):
         if not 0.0 <= p <= 1.0 or classes < 0:
             raise GQError("p must lie in [0, 1] and classes must not be negative")
-        if norm not in (True, False, "layer", "group"):
+        if norm not in (True, False, None, "layer", "group"):
             raise GQError(f'norm must be "layer", "group", True (layer) or False, got {norm!r}')
         self.grouped = grouped = norm == "group"
         if not grouped and (groups != 1 or ptr is not None or max_rows):
             raise GQError('groups, ptr and max_rows go with norm="group"')
-        if grouped and any(w % groups for w in widths[1:-1]):
-            raise GQError(f"every hidden width must be a multiple of the {groups} groups")
+        if grouped and (groups < 1 or max_rows < 0 or any(w % groups for w in widths[1:-1])):
+            raise GQError(f"every hidden width must be a multiple of the {groups} groups, max_rows not negative")
         if grouped and ptr is not None:
             if ptr.dtype != torch.int64 or ptr.dim() != 1 or ptr.numel() < 1 or ptr.device.type != torch.device(device).type:
                 raise GQError("ptr must be an int64 vector of node offsets on the stack's device")

@@ -38,3 +38,16 @@ def test_offsets_elsewhere_are_refused(make):
     err, stack = make
     with pytest.raises(err):
         stack(norm="group", ptr=torch.zeros(2, dtype=torch.int64, device="meta"))
+
+
+@pytest.mark.parametrize("kw", [dict(groups=0), dict(groups=-4), dict(groups=3), dict(max_rows=-1)])
+def test_group_arguments(make, kw):
+    err, stack = make
+    with pytest.raises(err):
+        stack(norm="group", **kw)
+
+
+def test_no_normalization_may_be_none(make):
+    """As it could be before there were two kinds of it."""
+    _, stack = make
+    assert stack(norm=None).norm is False
