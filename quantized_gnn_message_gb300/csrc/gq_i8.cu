@@ -574,16 +574,19 @@ __device__ __forceinline__ void widen_chunk(uint4 w, uint8_t* dst, int i) {
 
 // 32 rows x 32 columns of sums, lane = row, the tile's columns col0..  cv: the
 // columns' scales, and 128 floats on their biases.  SWAP: C may be transposed.
+// The warp leaves together: its next access to TMEM is one for all lanes.
 template <bool SWAP>
 __device__ __forceinline__ void put(const TileArgs& p, int64_t row0, int64_t col0, const float (&v)[32], float sr, float br,
                                     const float* cv, float* stg, int lane) {
   if (SWAP && p.swap) {  // a lane's row is a column of C: lanes write side by side
     const int64_t row = row0 + lane;
-    if (row >= p.M) return;
+    if (row < p.M) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (col0 + j < p.N)
-        store_as(p.C, (col0 + j) * p.ldc + row, activate(fmaf(__fmul_rn(v[j], cv[j]), sr, br), p.relu), p.type);
+      for (int j = 0; j < 32; ++j)
+        if (col0 + j < p.N)
+          store_as(p.C, (col0 + j) * p.ldc + row, activate(fmaf(__fmul_rn(v[j], cv[j]), sr, br), p.relu), p.type);
+    }
+    __syncwarp();
     return;
   }
 #pragma unroll
