@@ -937,6 +937,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<CONV>::threads
     while (clock64() - t0 < kDrainCycles) {
     }
   }
+  __syncwarp();  // the lanes' clocks let them go one by one, and what follows is for whole warps
   cluster_sync();
   if (warp == 1) {
     tc_fence_after();
@@ -1173,6 +1174,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowThreads, 1)
     while (clock64() - t0 < kDrainCycles) {
     }
   }
+  __syncwarp();  // the lanes' clocks let them go one by one, and what follows is for whole warps
   cluster_sync();
   if (warp == 1) {
     tc_fence_after();

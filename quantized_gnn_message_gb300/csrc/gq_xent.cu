@@ -811,6 +811,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     while (clock64() - t0 < kDrainCycles) {
     }
   }
+  __syncwarp();  // the lanes' clocks let them go one by one, and what follows is for whole warps
   cluster_sync();
   if (warp == 1) {
     tc_fence_after();

@@ -30,3 +30,12 @@ def test_the_epilogue_leaves_a_warp_together(function):
     ways = [body] + [body[:m.start()] for m in re.finditer(r"\breturn;", body)]
     for way in ways:
         assert way.rstrip().endswith("__syncwarp();"), way[-300:]
+
+
+@pytest.mark.parametrize("name,kernels", [("gq_i8.cu", 2), ("gq_xent.cu", 1)])
+def test_warps_that_gave_up_meet_before_the_clusters_barrier(name, kernels):
+    """After a wait that gave up each lane reads the clock until the time is
+    over: the lanes leave that loop one by one."""
+    code = _code(name)
+    loops = re.findall(r"while \(clock64\(\) - t0 < kDrainCycles\) \{\s*\}\s*\}\s*(\w+)\(\);\s*(\w+)\(\);", code)
+    assert loops == [("__syncwarp", "cluster_sync")] * kernels
