@@ -412,8 +412,11 @@ template <typename T, int V, int ACT>
 __device__ __forceinline__ void apply_bwd(const Args& p, int64_t r0, int64_t r1, int ry, int c, const Chan<V>& h,
                                           const Pk<V>& h1, const Pk<V>& h2) {  // the means of h and h xhat, negated
   constexpr int U = Ahead<V>::bwd;
-  // sc is there for ReLU: with rstd in the means too, no gamma is held beside it
-  const Pk<V> k1 = mul(h.rs, h1), k2 = mul(h.rs, h2);
+  Pk<V> k1, k2;  // ReLU has sc: with rstd in the means too, it holds no gamma beside it
+  if constexpr (ACT == GQ_ACT_RELU) {
+    k1 = mul(h.rs, h1);
+    k2 = mul(h.rs, h2);
+  }
   const int64_t first = r0 + ry;
   const int rows = first < r1 ? (int)((r1 - first + p.ry - 1) / p.ry) : 0;
   const T* x = static_cast<const T*>(p.X) + first * p.ldx + c;
