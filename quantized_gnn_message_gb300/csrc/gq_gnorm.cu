@@ -949,10 +949,13 @@ int combine(const Args& a, cudaStream_t s) {
 
 template <typename T, int V, int ACT, int GROUP>
 int run_short(bool bwd, const Args& a, const Plan& z, cudaStream_t s) {
-  const size_t sm = (size_t)(kThreads / GROUP) * ((bwd ? 2 : 1) * a.d + GROUP * V) * 8;
+  auto bytes = [bwd](int d) { return (kThreads / GROUP) * ((bwd ? 2 : 1) * d + GROUP * V) * 8; };
   auto* kernel = bwd ? short_bwd_kernel<T, V, ACT, GROUP> : short_fwd_kernel<T, V, ACT, GROUP>;
-  GQ_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
-  return launch_after(kernel, dim3((unsigned)z.blocks), dim3(kThreads), sm, s, a);
+  // the most that any call asks for: the limit is the kernel's, and another host
+  // thread may set it between this call's setting and its launch
+  GQ_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   bytes(GROUP == 32 ? kWarpMaxD : kShortMaxD)));
+  return launch_after(kernel, dim3((unsigned)z.blocks), dim3(kThreads), bytes(a.d), s, a);
 }
 
 template <typename T, int V, int ACT>
