@@ -599,7 +599,7 @@ int row_gemm(const void* A, int64_t M, int K, int64_t lda, const void* B, int N,
   memset(&tmC, 0, sizeof(tmC));
   if (p.tma) GQ_TRY(make_tmap_f32_out(&tmC, C, (uint64_t)N, (uint64_t)M, (uint64_t)ldc));
   const size_t smem = 1024 + (size_t)b_bytes + (size_t)p.stages * kATileBytes + kStgBytes + kVecBytes + 256;
-  GQ_TRY_CUDA(cudaFuncSetAttribute(row_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  GQ_TRY_CUDA(cudaFuncSetAttribute(row_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget));
   const int64_t ntiles = (M + kTileM - 1) / kTileM;
   const int grid = (int)(ntiles < sm_count() ? ntiles : sm_count());
   row_gemm_kernel<<<grid, kRgThreads, smem, s>>>(tmA, tmB, tmC, p);
@@ -655,7 +655,7 @@ int wgrad_gemm(const void* X, int64_t R, int K1, int64_t ldx, const void* Y, int
   GQ_TRY(make_tmap(&tmX, X, (uint64_t)K1, rows, (uint64_t)ldx, 64, kWgRows));
   GQ_TRY(make_tmap(&tmY, Y, (uint64_t)N1, rows, (uint64_t)ldy, 64, kWgRows));
   const size_t smem = 1024 + (size_t)p.stages * stage_bytes + 256;
-  GQ_TRY_CUDA(cudaFuncSetAttribute(wgrad_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  GQ_TRY_CUDA(cudaFuncSetAttribute(wgrad_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget));
   dim3 grid(p.mtiles, splits);
   wgrad_gemm_kernel<<<grid, kWgThreads, smem, s>>>(tmX, tmY, p);
   GQ_TRY(launch_status());

@@ -11,7 +11,7 @@ import pytest
 CONSTANT = re.compile(r"(k[A-Z]\w*|[A-Z0-9_]+|sizeof|int|float|size_t|bytes|smem_of|Shape)$")
 
 
-@pytest.mark.parametrize("name,settings", [("gq_gnorm.cu", 1), ("gq_i8.cu", 2), ("gq_xent.cu", 1)])
+@pytest.mark.parametrize("name,settings", [("gq_gnorm.cu", 1), ("gq_i8.cu", 2), ("gq_xent.cu", 1), ("gq_gemm.cu", 2)])
 def test_limits_are_constants(name, settings):
     from quantized_gnn_message_gb300 import build
     with open(os.path.join(build.CSRC, name), encoding="utf-8") as f:
