@@ -251,8 +251,13 @@ GQ_API int gq_group_norm_bwd(const void* dY, int64_t lddy, const void* X, int64_
  *            New codes are rounded down or up at random by the counter hash
  *            of (seed + t 0x9E3779B97F4A7C15, block0 + block, place in the block):
  *            its upper 20 bits for m, its lower 19 for v; a v > 0 is never
- *            rounded to 0.  e lies in [16, 254], which keeps 2^-111 to 2^127.
- *            Non-finite moments leave codes without meaning (and p is NaN)
+ *            rounded to 0.  e lies in [16, 254], which keeps 2^-111 to 2^127, and
+ *            is that of the block's largest finite value: of values 2^17 times
+ *            smaller a first moment is rounded to 0 but for one draw in many, a
+ *            second (2^19) to its least code.  A moment that is not finite takes
+ *            the greatest code and leaves its block's others alone; p is NaN where
+ *            m is not finite, and only decays where the square of |g| > 1.8e19
+ *            makes v infinite (32-bit moments stay so)
  *     block0 the number of the tensor's first block in the noise; tensors with
  *            ranges of their own draw different noise
  *   args->grad_scale  device fp32 or NULL (1).  Where it is not finite the

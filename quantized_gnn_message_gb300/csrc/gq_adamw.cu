@@ -211,8 +211,9 @@ __device__ __forceinline__ void decode4(uint32_t w, float scale, float2& lo, flo
   lo = mul2(mul2(lo, far), s);
   hi = mul2(mul2(hi, far), s);
 }
-// values -> codes, byte k from noise word h[k].  Codes end at 126 (E4M3's 127 is
-// its NaN) and 255; a second moment that is not 0 gets at least 1.
+// values -> codes, byte k from noise word h[k].  Codes end at 120, the 2^8 that a
+// block's largest value may be rounded up to, and 255, the 2^9 less a step; what is
+// not finite gets these.  A second moment that is not 0 gets at least 1.
 template <bool SECOND>
 __device__ __forceinline__ uint32_t encode4(float2 lo, float2 hi, float scale, const uint32_t (&h)[4]) {
   using F = Code<SECOND>;
@@ -226,7 +227,7 @@ __device__ __forceinline__ uint32_t encode4(float2 lo, float2 hi, float scale, c
     if (SECOND)
       c[k] = min(max((x[k] + (h[k] & 0x7FFFFu)) >> F::shift, min(v[k], 1u)), 255u);
     else
-      c[k] = min(((x[k] & 0x7FFFFFFFu) + (h[k] >> 12)) >> F::shift, 126u);
+      c[k] = min(((x[k] & 0x7FFFFFFFu) + (h[k] >> 12)) >> F::shift, 120u);
   }
   const uint32_t w = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
   if (SECOND) return w;
@@ -234,8 +235,13 @@ __device__ __forceinline__ uint32_t encode4(float2 lo, float2 hi, float scale, c
   return w | (sign & 0x80808080u);
 }
 
-__device__ __forceinline__ int block_exp(uint32_t largest_bits) {
-  return min(max((int)(__reduce_max_sync(FULL, largest_bits) >> 23), kMinExp), kMaxExp);
+// A magnitude's rank: twice its bits, which drops the sign, and one exponent more,
+// which takes infinities and NaN past the end, below all finite values.  The
+// block's exponent is that of its largest finite value, so that one that is not
+// finite takes the greatest code and the other 255 keep theirs.
+__device__ __forceinline__ uint32_t rank_of(float x) { return __float_as_uint(x) * 2u + (1u << 24); }
+__device__ __forceinline__ int block_exp(uint32_t largest_rank) {
+  return min(max((int)(__reduce_max_sync(FULL, largest_rank) >> 24) - 1, kMinExp), kMaxExp);
 }
 __device__ __forceinline__ float sqrt_fast(float x) {
   float y;
@@ -295,8 +301,8 @@ __device__ __forceinline__ void step8(float (&p)[8], float (&g)[8], float (&m)[8
     uint32_t bm = 0, bv = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      bm = max(bm, __float_as_uint(m[j]) & 0x7FFFFFFFu);
-      bv = max(bv, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+      bm = max(bm, rank_of(m[j]));
+      bv = max(bv, rank_of(v[j]));
     }
     em = block_exp(bm);
     ev = block_exp(bv);
