@@ -1068,7 +1068,8 @@ class AdamW:
         """One step.  grads: one for each parameter (None: that one is left as it
         is); without them those given at the start.  grad_scale: device float32
         value that the gradients are multiplied by; where it is not finite the step
-        changes nothing (without capturable it still counts)."""
+        changes nothing (without capturable it still counts).  A step that is refused,
+        or without any gradient, does not count."""
         if grads is None and self._bound is None:
             raise GQError("step needs gradients: none were given at the start")
         calls, held = self._bound if grads is None else self._calls(grads)
@@ -1078,14 +1079,14 @@ class AdamW:
             if grad_scale.numel() != 1 or grad_scale.dtype != torch.float32 or grad_scale.device != self.device:
                 raise GQError(f"grad_scale must be one float32 value on {self.device}")
             a.grad_scale = grad_scale.data_ptr()
-        self.steps += 1
-        a.step = self.steps
+        a.step = self.steps + 1
         L = lib()
         with _on(self.device):
             s = _on_stream()
             a.advance = 1
             for arr, count, pt, gt in calls:
                 _check(L.gq_adamw_step(arr, count, pt, gt, self.state_bits, ctypes.byref(a), s), "gq_adamw_step")
+                self.steps = a.step  # a step counts once something of it was launched
                 a.advance = 0
 
     def device_steps(self) -> torch.Tensor | None:
