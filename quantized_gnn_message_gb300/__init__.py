@@ -941,7 +941,8 @@ def adam_moment(codes: torch.Tensor, exponents: torch.Tensor, second: bool, dtyp
 class AdamW:
     """AdamW over a list of parameters, every step one launch for all of them
     (gq_adamw_step).  Parameters: CUDA tensors of float32, bfloat16 or float16,
-    contiguous or 2-D with unit column stride; those of one type share a launch.
+    contiguous or 2-D with unit column stride (blocks of columns of one buffer
+    among them); those of one type share a launch.
     state_bits: 32, or 8 for block-wise 8-bit moments with stochastic rounding
     drawn from seed and the step's number.
 
@@ -965,9 +966,13 @@ class AdamW:
             if t.device != dev:
                 raise GQError("the parameters must be on one device")
             self._pitch(t, f"parameter {i}")
-        spans = sorted((t.data_ptr(), t.data_ptr() + self._span(t)) for t in params if t.numel())
-        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
-            raise GQError("no parameter may appear twice or overlap another")
+        spans = sorted(self._rows_at(t) for t in params if t.numel())
+        for i, a in enumerate(spans):
+            for b in spans[i + 1:]:
+                if b[0] >= a[1]:
+                    break
+                if not self._apart(a, b):
+                    raise GQError("no parameter may appear twice or overlap another")
         self.params, self.state_bits, self.device = params, state_bits, dev
         self.steps = int(step)
         blocks = [(t.numel() + ADAM_BLOCK - 1) // ADAM_BLOCK for t in params]
@@ -1023,8 +1028,21 @@ class AdamW:
         raise GQError(f"{name} must be contiguous, or 2-D with unit column stride")
 
     @staticmethod
-    def _span(t):
-        return ((t.numel() if t.is_contiguous() else (t.shape[0] - 1) * t.stride(0) + t.shape[1]) * t.element_size())
+    def _rows_at(t):
+        """(first byte, end, bytes of a row, pitch): rows at a pitch, or one row (pitch 0)."""
+        e, at = t.element_size(), t.data_ptr()
+        if t.is_contiguous():
+            return at, at + t.numel() * e, t.numel() * e, 0
+        return at, at + ((t.shape[0] - 1) * t.stride(0) + t.shape[1]) * e, t.shape[1] * e, t.stride(0) * e
+
+    @staticmethod
+    def _apart(a, b):
+        """Whether b, which begins inside a, lies between its rows: columns of one buffer."""
+        pitch = a[3] or b[3]
+        if not pitch or (a[3] and b[3] and a[3] != b[3]):
+            return False
+        place = (b[0] - a[0]) % pitch
+        return a[2] <= place and place + b[2] <= pitch
 
     def _calls(self, grads):
         """[(C array, count, parameter type, gradient type)], and the tensors they point to."""
