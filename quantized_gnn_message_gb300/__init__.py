@@ -1195,15 +1195,23 @@ def selftest_bounded_wait(helper: int, complete: bool, limit_cycles: int, status
 
 
 class Workspace:
-    """A reusable device scratch buffer that grows on demand."""
+    """A reusable device scratch buffer that grows on demand.  A buffer that a
+    captured graph uses stays where it is for as long as the Workspace lives,
+    also after it has grown: the graph replays into it."""
 
     def __init__(self, device="cuda"):
         self.device = device
         self.buf = torch.empty(0, dtype=torch.uint8, device=device)
+        self._captured, self._kept = False, []
 
     def get(self, nbytes: int) -> torch.Tensor:
         if self.buf.numel() < nbytes:
+            if self._captured:
+                self._kept.append(self.buf)
             self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            self._captured = False
+        if not self._captured and not self.buf.is_cpu and torch.cuda.is_current_stream_capturing():
+            self._captured = True
         return self.buf
 
 
