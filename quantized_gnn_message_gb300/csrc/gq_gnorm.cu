@@ -467,6 +467,12 @@ __device__ __forceinline__ float2 merge(const float2* red, const Args& p, int k,
   return make_float2(mean, q);
 }
 
+// (mean, squares around it) of na rows and of nb more.
+__device__ __forceinline__ float2 join(const float2& a, int na, const float2& b, int nb) {
+  const float f = (float)nb / (float)(na + nb), dev = b.x - a.x;
+  return make_float2(fmaf(dev, f, a.x), a.y + fmaf((float)na * f * dev, dev, b.y));
+}
+
 template <int V>
 __device__ __forceinline__ float2 add_up(const float2* red, const Args& p, int k) {
   const int tv = k / V, e = k - tv * V;
@@ -480,7 +486,11 @@ __device__ __forceinline__ float2 add_up(const float2* red, const Args& p, int k
 }
 
 // ---------------------------------------------------------- short segments --
-// GROUP threads, a warp or the whole block, take a segment.  Shared memory of each
+// GROUP threads, a warp or the whole block, take a segment, kPieceRows rows of a
+// thread at a time: none has more where the longest segment is what the caller
+// said, and where it is far longer the sums stay as short as long segments'.
+constexpr int kPieceRows = 1024;
+// Shared memory of each
 // of them: [d] channel values, the backward kernel's [d] sums over its segments,
 // [GROUP x V] of the threads'.
 template <int GROUP>
@@ -500,6 +510,7 @@ __global__ void __launch_bounds__(kThreads, 4) short_fwd_kernel(const Args p) {
   float2* red = ch + p.d;
   grid_wait();
   const int tx = t % p.tx, ry = t / p.tx;
+  const int piece = kPieceRows * p.ry;
   const int warp = t >> 5, lane = t & 31;
   for (int64_t j = (int64_t)blockIdx.x * per_block + unit; j < p.s; j += (int64_t)gridDim.x * per_block) {
     int64_t r0, r1;
@@ -514,15 +525,24 @@ __global__ void __launch_bounds__(kThreads, 4) short_fwd_kernel(const Args p) {
     }
     for (int v0 = 0; v0 < p.vpr; v0 += p.tx) {
       const int c = (v0 + tx) * V;
-      if (ry < p.ry && v0 + tx < p.vpr) {
-        Pk<V> mean, m2;
-        spread<T, V>(p, r0, r1, ry, c, mean, m2);
+      int done = 0;
+      do {
+        const int more = min((int)rows - done, piece);
+        if (ry < p.ry && v0 + tx < p.vpr) {
+          Pk<V> mean, m2;
+          spread<T, V>(p, r0 + done, r0 + done + more, ry, c, mean, m2);
 #pragma unroll
-        for (int e = 0; e < V; ++e) red[(ry * p.tx + tx) * V + e] = make_float2(mean.e[e], m2.e[e]);
-      }
-      group_sync<GROUP>();
-      for (int k = t; k < min(p.tx, p.vpr - v0) * V; k += GROUP) ch[v0 * V + k] = merge<V>(red, p, k, rows);
-      group_sync<GROUP>();
+          for (int e = 0; e < V; ++e) red[(ry * p.tx + tx) * V + e] = make_float2(mean.e[e], m2.e[e]);
+        }
+        group_sync<GROUP>();
+        for (int k = t; k < min(p.tx, p.vpr - v0) * V; k += GROUP) {
+          float2 w = merge<V>(red, p, k, more);
+          if (done > 0) w = join(ch[v0 * V + k], done, w, more);
+          ch[v0 * V + k] = w;
+        }
+        group_sync<GROUP>();
+        done += more;
+      } while (done < (int)rows);
     }
     const int at_once = 32 / p.lpg, sub = lane % p.lpg;
     for (int g0 = warp * at_once; g0 < p.groups; g0 += warps * at_once) {
@@ -572,6 +592,7 @@ __global__ void __launch_bounds__(kThreads, 3) short_bwd_kernel(const Args p) {
   float2* red = tot + p.d;
   grid_wait();
   const int tx = t % p.tx, ry = t / p.tx;
+  const int piece = kPieceRows * p.ry;
   const int warp = t >> 5, lane = t & 31;
   for (int k = t; k < p.d; k += GROUP) tot[k] = make_float2(0.0f, 0.0f);
   group_sync<GROUP>();
@@ -582,22 +603,24 @@ __global__ void __launch_bounds__(kThreads, 3) short_bwd_kernel(const Args p) {
     if (rows == 0) continue;
     for (int v0 = 0; v0 < p.vpr; v0 += p.tx) {
       const int c = (v0 + tx) * V;
-      if (ry < p.ry && v0 + tx < p.vpr) {
-        Chan<V> h;
-        Pk<V> a, b;
-        channels<V>(p, j, c, h);
-        slopes<T, V, ACT>(p, r0, r1, ry, c, h, a, b);
+      for (int64_t r = r0; r < r1; r += piece) {
+        if (ry < p.ry && v0 + tx < p.vpr) {
+          Chan<V> h;
+          Pk<V> a, b;
+          channels<V>(p, j, c, h);
+          slopes<T, V, ACT>(p, r, min(r1, r + piece), ry, c, h, a, b);
 #pragma unroll
-        for (int e = 0; e < V; ++e) red[(ry * p.tx + tx) * V + e] = make_float2(a.e[e], b.e[e]);
+          for (int e = 0; e < V; ++e) red[(ry * p.tx + tx) * V + e] = make_float2(a.e[e], b.e[e]);
+        }
+        group_sync<GROUP>();
+        for (int k = t; k < min(p.tx, p.vpr - v0) * V; k += GROUP) {
+          const float2 w = add_up<V>(red, p, k), o = r == r0 ? make_float2(0.0f, 0.0f) : ch[v0 * V + k];
+          ch[v0 * V + k] = make_float2(o.x + w.x, o.y + w.y);
+          tot[v0 * V + k].x += w.x;
+          tot[v0 * V + k].y += w.y;
+        }
+        group_sync<GROUP>();
       }
-      group_sync<GROUP>();
-      for (int k = t; k < min(p.tx, p.vpr - v0) * V; k += GROUP) {
-        const float2 w = add_up<V>(red, p, k);
-        ch[v0 * V + k] = w;
-        tot[v0 * V + k].x += w.x;
-        tot[v0 * V + k].y += w.y;
-      }
-      group_sync<GROUP>();
     }
     const int at_once = 32 / p.lpg, sub = lane % p.lpg;
     for (int g0 = warp * at_once; g0 < p.groups; g0 += warps * at_once) {
