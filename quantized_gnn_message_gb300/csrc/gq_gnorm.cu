@@ -24,8 +24,9 @@
 // Variances are sums of squares around the mean of the first eight values that
 // a thread meets, then around the mean of the parts: no difference of large
 // squares.  Eight values are added up by themselves before the running sum takes
-// them.  All sums run in fp32 in a fixed order, those that join the pieces of
-// long segments in 64 bits.
+// them.  All sums run in fp32 in a fixed order; those that join the pieces of
+// long segments in 64 bits, and the parts of dgamma and dbeta with what each
+// addition loses.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -856,28 +857,43 @@ __global__ void __launch_bounds__(kThreads, 4) apply_bwd_kernel(const Args p) {
   }
 }
 
-// dgamma, dbeta from the parts' sums: 32 channels x 32 parts at a time
-__global__ void __launch_bounds__(1024) columns_kernel(const Args p) {
-  __shared__ float2 sh[32][33];
+// dgamma, dbeta from the parts' sums: a block takes kSumC channels, 128 parts at a time.
+constexpr int kSumC = 8, kSumThreads = 1024;
+__global__ void __launch_bounds__(kSumThreads) columns_kernel(const Args p) {
+  __shared__ Sum2 sh[kSumThreads / 32][2][kSumC];
   grid_wait();
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + x;
-  float2 s = make_float2(0.0f, 0.0f);
+  const int x = threadIdx.x % kSumC, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * kSumC + x;
+  Sum2 ga{}, be{};
   if (c < p.d)
-    for (int64_t k = y; k < p.parts; k += 32) {
+    for (int64_t k = threadIdx.x / kSumC; k < p.parts; k += kSumThreads / kSumC) {
       const float2 w = p.tot[k * p.d + c];
-      s.x += w.x;
-      s.y += w.y;
+      ga.add(w.x);
+      be.add(w.y);
     }
-  sh[y][x] = s;
+  auto lanes = [&] {
+    for (int o = kSumC; o < 32; o *= 2) {
+      ga.add(ga.from_lane(o));
+      be.add(be.from_lane(o));
+    }
+  };
+  lanes();
+  if (lane < kSumC) {
+    sh[warp][0][x] = ga;
+    sh[warp][1][x] = be;
+  }
   __syncthreads();
-  if (y == 0 && c < p.d) {
-    for (int k = 1; k < 32; ++k) {
-      s.x += sh[k][x].x;
-      s.y += sh[k][x].y;
-    }
-    if (p.dgamma != nullptr) p.dgamma[c] = s.x;
-    if (p.dbeta != nullptr) p.dbeta[c] = s.y;
+  if (warp > 0) return;
+  ga = sh[lane / kSumC][0][x];
+  be = sh[lane / kSumC][1][x];
+  for (int w = lane / kSumC + 32 / kSumC; w < kSumThreads / 32; w += 32 / kSumC) {
+    ga.add(sh[w][0][x]);
+    be.add(sh[w][1][x]);
+  }
+  lanes();
+  if (lane < kSumC && c < p.d) {
+    if (p.dgamma != nullptr) p.dgamma[c] = ga.value();
+    if (p.dbeta != nullptr) p.dbeta[c] = be.value();
   }
 }
 
@@ -1001,7 +1017,7 @@ int run_bwd(const Args& a, const Plan& z, cudaStream_t s) {
     GQ_TRY(launch_after(apply_bwd_kernel<T, V, ACT>, g, dim3(kThreads), 0, s, a));
   }
   if (a.dgamma == nullptr && a.dbeta == nullptr) return GQ_OK;
-  return launch_after(columns_kernel, dim3((a.d + 31) / 32), dim3(1024), 0, s, a);
+  return launch_after(columns_kernel, dim3((a.d + kSumC - 1) / kSumC), dim3(kSumThreads), 0, s, a);
 }
 
 template <typename T, int V>
