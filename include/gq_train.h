@@ -159,8 +159,8 @@ GQ_API int gq_linear_xent(const uint16_t* X, int64_t n, int k, int64_t ldx, cons
  * gq_linear_i8_bwd, W (out x k) and X in full precision, each product of
  *   quantized operands with a scale for each row or column that is not summed over:
  *   dX = dY W (dY by rows, W by columns);  dW = dY^T X (both by columns);
- *   dbias[j] = sum_r dY[r,j] (fp32, fixed order).  dX, dW, dbias: nullable,
- *   dbias only with dW; W is not read without dX, X not without dW.
+ *   dbias[j] = sum_r dY[r,j] (fp32 in a fixed order, its parts joined without loss).
+ *   dX, dW, dbias: nullable, dbias only with dW; W is not read without dX, X not without dW.
  *   n == 0 gives dW = 0, dbias = 0.
  * ws of both: the ..._workspace_bytes bytes, 256-byte aligned.  Calls sharing a
  * workspace must not overlap.  Outputs must not overlap inputs.  Results are

@@ -427,8 +427,8 @@ __global__ void __launch_bounds__(kQThreads) col_max_kernel(const __grid_constan
   }
 }
 
-// Then the pieces' largest and the sums together, by every block for its 64
-// columns, and tiles of 128 rows turned into 64 rows of 128 codes.
+// Then the pieces' largest (by every block for its 64 columns) and the sums (by one,
+// with what the additions lose) together, and tiles of 128 rows turned into 64 rows of 128 codes.
 constexpr int kTrRows = 128, kTrPitch = kTrRows / 4 + 1;  // words
 template <typename T, typename O>
 __global__ void __launch_bounds__(kQThreads) quant_cols_kernel(const __grid_constant__ ColJobs<T, O> jobs) {
@@ -442,19 +442,19 @@ __global__ void __launch_bounds__(kQThreads) quant_cols_kernel(const __grid_cons
   if ((int)blockIdx.y * kColW >= d || (int64_t)blockIdx.x >= tiles) return;
   __shared__ uint32_t tile[kColW][kTrPitch];
   __shared__ uint32_t smax[4][kColW];
-  __shared__ float ssum[4][kColW];
+  __shared__ Sum2 ssum[4][kColW];
   __shared__ Scale sc[kColW];
   grid_wait();
   const int t = threadIdx.x, c0 = blockIdx.y * kColW;
   {
     const int x = t % kColW, y = t / kColW;
     uint32_t m = 0;
-    float s = 0.0f;
+    Sum2 s{};
     if (c0 + x < d)
 #pragma unroll 8
       for (int k = y; k < parts; k += 4) {
         m = max(m, p.top[(int64_t)k * d + c0 + x]);
-        if (sums != nullptr && blockIdx.x == 0) s += sums[(int64_t)k * d + c0 + x];
+        if (sums != nullptr && blockIdx.x == 0) s.add(sums[(int64_t)k * d + c0 + x]);
       }
     smax[y][x] = m;
     ssum[y][x] = s;
@@ -463,7 +463,11 @@ __global__ void __launch_bounds__(kQThreads) quant_cols_kernel(const __grid_cons
       sc[t] = make_scale(max(max(smax[0][t], smax[1][t]), max(smax[2][t], smax[3][t])));
       if (blockIdx.x == 0 && c0 + t < d) {
         p.S[c0 + t] = sc[t].s;
-        if (sums != nullptr) p.colsum[c0 + t] = (ssum[0][t] + ssum[1][t]) + (ssum[2][t] + ssum[3][t]);
+        if (sums != nullptr) {
+          Sum2 all = ssum[0][t];
+          for (int k = 1; k < 4; ++k) all.add(ssum[k][t]);
+          p.colsum[c0 + t] = all.value();
+        }
       }
     }
     __syncthreads();

@@ -1,7 +1,7 @@
-"""Sums over very many rows: dbeta of group normalization.  The parts that threads
-and blocks add up are joined with what each addition loses, so with whole
-values, whose parts stay below 2^24 and are exact, the result is the exact sum,
-rounded once."""
+"""Sums over very many rows: dbeta of group normalization, dbias of the 8-bit linear
+layer.  The parts that threads and blocks add up are joined with what each
+addition loses, so with whole values, whose parts stay below 2^24 and are
+exact, the result is the exact sum, rounded once."""
 import pytest
 import torch
 
@@ -14,6 +14,17 @@ def _whole(n, d, t, seed, lo, hi):
     gen = torch.Generator(device="cuda")
     gen.manual_seed(seed)
     return torch.randint(lo, hi, (n, d), device="cuda", generator=gen).to(t)
+
+
+@pytest.mark.parametrize("t", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("n,d,lo,hi", [(300001, 47, 100, 256), (600000, 64, 200, 256), (4097, 300, -255, 256),
+                                       (1, 5, -255, 256), (2449029, 8, 0, 33)])
+def test_dbias_is_the_sum(n, d, lo, hi, t):
+    q = gq()
+    dy, x = _whole(n, d, t, 1, lo, hi), _whole(n, 16, t, 2, -9, 9)
+    w = torch.ones(d, 16, device="cuda")
+    _, _, db = q.linear_i8_bwd(dy, x, w, need_dX=False)
+    assert torch.equal(db, dy.double().sum(0).float())
 
 
 @pytest.mark.parametrize("t", [torch.float32, torch.bfloat16, torch.float16])
