@@ -254,7 +254,11 @@ GQ_API int gq_group_norm_bwd(const void* dY, int64_t lddy, const void* X, int64_
  *            rounded to 0.  e lies in [16, 254], which keeps 2^-111 to 2^127, and
  *            is that of the block's largest finite value: of values 2^17 times
  *            smaller a first moment is rounded to 0 but for one draw in many, a
- *            second (2^19) to its least code.  A moment that is not finite takes
+ *            second (2^19) to its least code.  No code is above 31/16 of the power of
+ *            two below a block's largest second moment, which is therefore not rounded
+ *            up beyond it: it grows into the next octave only in a step that adds a
+ *            32nd of it, and with beta2 = 0.999 stays behind its 32-bit value (half of
+ *            it on average, a quarter at worst).  A moment that is not finite takes
  *            the greatest code and leaves its block's others alone; p is NaN where
  *            m is not finite, and only decays where the square of |g| > 1.8e19
  *            makes v infinite (32-bit moments stay so)
