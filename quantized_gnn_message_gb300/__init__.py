@@ -944,7 +944,8 @@ class AdamW:
     contiguous or 2-D with unit column stride (blocks of columns of one buffer
     among them); those of one type share a launch.
     state_bits: 32, or 8 for block-wise 8-bit moments with stochastic rounding
-    drawn from seed and the step's number.
+    drawn from seed and the step's number (the largest second moments of a block
+    of 256 stay behind those of 32 bits, by half at beta2 = 0.999: gq_train.h).
 
     grads: the gradients' buffers where they stay the same from step to step;
     otherwise step takes them.  state: moments to go on with, the optimizer's own
