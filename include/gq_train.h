@@ -210,6 +210,9 @@ GQ_API int gq_linear_i8_bwd(const void* dY, int64_t lddy, const void* X, int64_t
  *   dY or X (same leading dimension).  Matrices: n x d of `type`, any alignment of
  *   the type; rows of a multiple of 4 values that start aligned for 4 take the
  *   vector path.  Sums run in fp32 in a fixed order; results are rounded once.
+ *   Sums of a segment's rows, and squares of x - mean, that leave fp32's range
+ *   (|x| rows > 3.4e38, |x - mean| > 1.8e19) make the statistics infinite or NaN.
+ *   ReLU's derivative is 1 exactly where forward's z, rounded as there, is above 0.
  *   ws: gq_group_norm_workspace_bytes(n, d, groups, type, segments, max_rows,
  *   backward), 256-byte aligned; it depends on the device's SM count.
  * Errors: GQ_ERR_INVALID_ARG (bad type, act, sizes, eps; d not a multiple of

@@ -806,7 +806,8 @@ def quantize_i8(X: torch.Tensor, transpose: bool = False, out: torch.Tensor | No
                 scale: torch.Tensor | None = None, ws: "Workspace | None" = None):
     """(codes, scale) of X's rows, or, with transpose, of its columns (the
     codes of column i are then row i): 8-bit integers and the fp32 value that
-    one stands for (gq_quantize_i8)."""
+    one stands for (gq_quantize_i8).  Behind a row of out that ends inside a word
+    of 4 bytes, the rest of that word may be written."""
     ty = _typed(X, "X")
     n, d = X.shape
     ldx = _ld_any(X, d)

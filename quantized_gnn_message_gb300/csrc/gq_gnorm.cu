@@ -974,7 +974,11 @@ size_t workspace(int64_t n, int d, int groups, int type, int64_t s, int64_t max_
 }
 
 // A block for each segment and group where that has more than 1,024 values to
-// put together on average, else a warp.
+// put together on average, else a warp.  The whole pass forward, SiLU, fp32 x 256,
+// block | warp, us: one segment of 2,449,029 in 1, 16, 256 groups 2,379 | 18,257, 1,204 |
+// 2,431, 1,135 | 1,208; 16 in one group 1,204 | 2,379; 200 of 3,000 in one 330 | 426, in 8
+// 374 | 323; 2,000 in one 1,218 | 1,153, in 16 2,280 | 1,194.  With one segment and few
+// groups a single SM puts everything together: half of the time at one group.
 template <bool BWD>
 int combine(const Args& a, cudaStream_t s) {
   const int64_t units = a.s * a.groups;

@@ -1362,8 +1362,8 @@ constexpr int64_t kConvColumns = 2048;
 // S is A, unless A has fewer rows than a tile and than B: then B's rows fill
 // the tiles, and C is written transposed.  F's tiles are as equal as multiples
 // of 32 allow, and up to four more of them where a few tiles would be a wave of
-// their own (5,003 x 1,000 by 777: 100 tiles of 160 columns instead of 80 of 224,
-// on 76 pairs of CTAs: 24.5 us instead of 31.6 with the quantizer).  S that is given as bytes is widened in the kernel where it meets
+// their own, by the cycles that the plan counts (5,003 x 1,000 by 777 on 76 pairs of
+// CTAs: 140 tiles of 128 columns 29.3 us, 100 of 160 32.4, 80 of 224 35.5, cold). S that is given as bytes is widened in the kernel where it meets
 // few rows of F, one pass over DRAM as bytes instead of bytes, fp16 out and
 // fp16 in; else before it.  65,536 x 1,024 bytes by 256, 512, 1,024, 2,048 rows
 // in the kernel 48, 70, 126, 231 us, before it 81, 95, 129, 197; 16,384 x 4,096
@@ -1416,7 +1416,11 @@ bool valid_shape(int64_t m, int64_t n, int64_t k) {
 bool few(int64_t m, int64_t k) { return m <= kFew && k <= 65536; }  // a 32-bit sum holds twice that
 
 int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
-// rows that every block of the product quantizes for itself
+// rows that every block of the product quantizes for itself.  In the product | before
+// it, against 10,007 rows, us: 4 x 256 values 8.9 | 10.9, 1 x 1,024 12.9 | 10.9, 4 x 1,024
+// 13.0 | 12.9, 1 x 4,096 27.3 | 27.3, 4 x 4,096 29.3 | 28.3, 1 x 8,192 45.7 | 29.3, 1 x 16,384
+// 84.6 | 51.9 (with the launches' gaps, cold; one launch instead of two, which counts
+// where calls follow one another).
 bool few_codes(int64_t m, int64_t k) { return few(m, k) && m * round16(k) <= kFewCodes; }
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -1517,6 +1521,12 @@ int tile_gemm(const Plan& z, const Operand& A, const Operand& B, int64_t k, cons
 }
 
 // Whether rows of X can be quantized on their way to the product with n rows of F.
+// On the way | codes before, 2,449,029 rows, us: fp32 256 -> 256 979 | 1,111, 256 -> 64
+// 790 | 813, 256 -> 16 774 | 882, 64 -> 256 843 | 874, 100 -> 47 764 | 762, 128 -> 128
+// 786 | 682, 64 -> 64 737 | 575; bf16 256 -> 256 1,172 | 1,059, 128 -> 128 916 | 653,
+// 64 -> 64 818 | 597; 20,000 rows of fp32 256 -> 256 28 | 25, 100 of them 19 | 15.  It
+// pays for many fp32 rows near its 256 values, what it is built for; narrower ones do
+// 256 values' work, and 16-bit ones have less to save.
 bool rows_fit(int64_t m, int64_t n, int64_t k) { return m > kFew && n <= kTile && k <= kRowK; }
 bool rows_fit(int64_t m, int64_t n, int64_t k, const void* X, int type, int64_t ldx) {
   return rows_fit(m, n, k) && aligned(X, 16) && ldx * type_bytes(type) % 16 == 0;
