@@ -409,8 +409,8 @@ __device__ __forceinline__ void ragged(const Tensor& t, int64_t b, int lane, con
 
 // A block a warp, and as many warps as 48 registers a thread allow: what hides the
 // reads is other warps.  With 8-bit moments 152 M fp32 values take 424 us, 5.7 TB/s,
-// and 67 M bf16 ones 165 (their arithmetic, 67 instructions a value, is half
-// of the issue slots) with 40 warps an SM; 411 and 175 with 32; 655 and 300 with 24
+// and 67 M bf16 ones 165 (their arithmetic, 74 instructions a value, is three
+// quarters of the issue slots) with 40 warps an SM; 411 and 175 with 32; 655 and 300 with 24
 // that each read their next block while they work on one.  With fp32 moments
 // 67 M values take 247 us, 7.0 TB/s.
 template <typename TP, typename TG, bool SMALL, int CAP>
